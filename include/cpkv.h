@@ -74,6 +74,7 @@ typedef void *cpkv_stream_t;
 #define CPKV_STATUS_CHUNK_OOB 64          /* cp_index not ascending or out of range      */
 #define CPKV_STATUS_OUT_CAPACITY 128      /* a device-sized output exceeded its capacity */
 #define CPKV_STATUS_TIMEOUT 256           /* a bounded wait gave up (should never occur) */
+#define CPKV_STATUS_POS_OOB 512           /* a position outside the rotation table       */
 
 /* Sizes of a batch, derived from host lengths. */
 typedef struct {
@@ -544,6 +545,145 @@ int cpkv_ragged_plan_build(int B, int chunk, int k_align, int topk, const int32_
                            int32_t *d_kv_lens, int32_t *d_q_starts, int32_t *d_q_lens,
                            int32_t *d_k_bases, int32_t *d_q_bases, int32_t *d_current_bases,
                            int64_t seg_cap, int64_t *d_counts, int32_t *d_status, cpkv_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * Serving on the paged rows: new keys and values into the pools, attention
+ * over the pools (or over a composed dense buffer).
+ *
+ * A token's row of row_bytes bytes holds kv_heads key vectors of 16-bit
+ * elements at key_offset and kv_heads value vectors at value_offset (bytes,
+ * multiples of 16); other bytes of the row are left alone.  Pools are those of
+ * the compose: logical page lp is page lp / cp of h_pools[lp % cp], each pool
+ * [h_pool_cap_pages[r]][page_size][row_bytes] and 16-byte aligned.  Strides are
+ * elements between tokens, multiples of 8, heads side by side within a token.
+ * Pointers to rows are 16-byte aligned.
+ * ------------------------------------------------------------------------- */
+
+/* Element types of keys, values, queries and outputs. */
+#define CPKV_BF16 0
+#define CPKV_FP16 1
+
+/* Flags of the serving calls. */
+#define CPKV_ROTARY_INTERLEAVED 8 /* pairs (2i, 2i + 1) instead of (i, i + rot_dim / 2)                */
+#define CPKV_DENSE_PAGES 16       /* page 0 is an ordinary page: the "pool" is a composed dense buffer */
+
+/*
+ * cpkv_append_rotary — new keys and values into the paged pools, the keys
+ * rotated by their positions on the way, queries rotated beside them.
+ *
+ * For token n: its key vectors, rotated, and its value vectors go to row
+ * d_slots[n] (page slot / page_size, row slot % page_size).  The rotation of
+ * the first rot_dim elements of each key head pairs elements (i, i + rot_dim/2),
+ * or (2i, 2i + 1) with CPKV_ROTARY_INTERLEAVED, for i < rot_dim / 2:
+ *   x1' = x1 c - x2 s,  x2' = x2 c + x1 s,
+ *   c = d_cos_sin[a][i], s = d_cos_sin[a][rot_dim / 2 + i],
+ *   a = d_positions[axis(i)][n],
+ * in 32 bits, rounded once; further elements are copied.  With several position
+ * axes (time, height, width) axis(i) = h_axis_of_freq[i]; with one it is 0.
+ * Query heads (q_heads > 0) are rotated alike from d_q to d_q_out, which may
+ * be d_q itself.
+ *   n_tokens       >= 0
+ *   key_dim        multiple of 8; rot_dim a multiple of 16, 0..min(key_dim, 256)
+ *   value_dim      multiple of 8
+ *   d_k, d_v       [n][kv_heads][key_dim], [n][kv_heads][value_dim]
+ *   d_slots        device int64 [n]: cache row of each token; a negative slot
+ *                  is a padding token, whose row is not written (its query is
+ *                  still rotated).  Two tokens must not share a slot.
+ *   d_positions    device int32, axis a at a * position_stride (n_axes 1..4)
+ *   d_cos_sin      device float [max_position][rot_dim], 16-byte aligned
+ *   flags          CPKV_ROTARY_INTERLEAVED, CPKV_DENSE_PAGES
+ * Status bits: PAGE_OOB (a slot's page is outside the pools: the row is not
+ * written), POS_OOB (a position outside [0, max_position): the row is not
+ * written and the token's rotated queries are zeros).
+ * Errors: ARG, LIMIT, CUDA.  The latent rows of this library's batches (512
+ * latent elements, then 64 rotated ones) are kv_heads 1, value_dim 512 at
+ * offset 0, key_dim = rot_dim = 64 at offset 1024.
+ */
+int cpkv_append_rotary(int64_t n_tokens, int page_size, int cp_size, int dtype, int q_heads, int kv_heads,
+                       int key_dim, int value_dim, int64_t row_bytes, int64_t key_offset, int64_t value_offset,
+                       void *const *h_pools, const int64_t *h_pool_cap_pages, const void *d_k, int64_t k_stride,
+                       const void *d_v, int64_t v_stride, const void *d_q, int64_t q_stride, void *d_q_out,
+                       int64_t q_out_stride, const int64_t *d_slots, const int32_t *d_positions,
+                       int64_t position_stride, int n_axes, const uint8_t *h_axis_of_freq, const float *d_cos_sin,
+                       int64_t max_position, int rot_dim, int flags, int32_t *d_status, cpkv_stream_t stream);
+
+/*
+ * cpkv_attend_window — causal attention of each request's newest tokens over
+ * its paged rows, with a sliding window and a few first tokens that stay
+ * visible.  Request b has h_q_lens[b] query tokens (NULL: one each, a decode
+ * step), the last of its d_kv_lens[b] cached tokens, whose rows are already in
+ * the pools.  Query token i stands at position p = kv_len - q_len + i and sees
+ * key j when j <= p and (p - j < window or j < sinks); window 0 is no window.
+ *   out = sum_j w_j v_j,  w = softmax_j(scale q.k_j),  lse = ln sum_j exp(scale q.k_j)
+ * Query head h uses key/value head h / (q_heads / kv_heads).  Products and the
+ * softmax are held in 32 bits; the weights are rounded to the element type for
+ * the product with the values, and the output once more.  A query that sees no
+ * key (kv_len 0, or a position below 0) gives zeros and lse = -infinity.
+ * Rows that no query of the request sees (behind the window, past kv_len) are
+ * not read, nor are their page ids.  A value row that some query of the
+ * request sees should be finite: a neighbouring query that does not see it
+ * multiplies it by a weight of zero.
+ *   B              requests, at most CPKV_MAX_BATCH
+ *   head_dim       64 or 128; q_heads a multiple of kv_heads
+ *   h_q_lens       host int32 [B] or NULL
+ *   max_kv_len     host bound of d_kv_lens; at most table_stride * page_size
+ *   d_page_table   device int32 [B][table_stride]: page k of request b holds its
+ *                  tokens k * page_size ...
+ *   d_kv_lens      device int32 [B], read by the kernels: a captured graph can
+ *                  be replayed as the requests grow.  A length outside
+ *                  [0, max_kv_len] is clamped and raises OUT_CAPACITY.
+ *   d_q            [sum q_lens][q_heads][head_dim], requests one after the other
+ *   d_out          like d_q; d_lse: float [sum q_lens][q_heads], or NULL
+ *   d_workspace    device, 16-byte aligned, at least
+ *                  cpkv_attend_window_workspace_bytes; contents between calls are
+ *                  irrelevant, calls that overlap on the GPU must not share one
+ *   flags          CPKV_DENSE_PAGES or 0
+ * Status bits: PAGE_OOB (a visible token's page id is outside the pools: its row
+ * reads as zeros), OUT_CAPACITY.  Errors: ARG, CAPACITY (workspace, table),
+ * LIMIT (B, head_dim, sizes), CUDA.
+ */
+int cpkv_attend_window(int B, int page_size, int cp_size, int dtype, int q_heads, int kv_heads, int head_dim,
+                       int64_t row_bytes, int64_t key_offset, int64_t value_offset, const int32_t *h_q_lens,
+                       int64_t max_kv_len, const void *const *h_pools, const int64_t *h_pool_cap_pages,
+                       const int32_t *d_page_table, int64_t table_stride, const int32_t *d_kv_lens, const void *d_q,
+                       int64_t q_stride, float scale, int window, int sinks, void *d_out, int64_t out_stride,
+                       float *d_lse, void *d_workspace, int64_t workspace_bytes, int flags, int32_t *d_status,
+                       cpkv_stream_t stream);
+
+/* Device workspace of cpkv_attend_window (host only); lengths as passed to it. */
+int cpkv_attend_window_workspace_bytes(int B, int q_heads, int kv_heads, int head_dim, const int32_t *h_q_lens,
+                                       int64_t max_kv_len, int window, int sinks, int64_t *h_bytes);
+
+/*
+ * cpkv_attend_shared — a decode step of a batch whose requests share long
+ * prefixes: requests come in n_groups consecutive groups, every request of
+ * group g attends to the group's h_prefix_lens[g] prefix tokens (read and
+ * multiplied once for the whole group) and to its own d_suffix_lens[b] tokens
+ * (its newest included).  One query token per request; output, lse, types and
+ * rounding as cpkv_attend_window without a window.
+ *   h_group_sizes  host int32 [n_groups], adding up to B
+ *   h_prefix_lens  host int32 [n_groups], multiples of page_size
+ *                  (UNALIGNED_PREFIX otherwise), 0 allowed
+ *   d_prefix_pages device int32, CSR by group: h_prefix_lens[g] / page_size ids each
+ *   d_page_table   device int32 [B][table_stride]: pages of the suffixes, whose
+ *                  first token stands at the first row of its first page
+ *   d_suffix_lens  device int32 [B], clamped to [0, max_suffix_len] (OUT_CAPACITY)
+ *   d_q, d_out     [B][q_heads][head_dim]
+ *   other arguments, status bits and errors as cpkv_attend_window.
+ */
+int cpkv_attend_shared(int B, int n_groups, int page_size, int cp_size, int dtype, int q_heads, int kv_heads,
+                       int head_dim, int64_t row_bytes, int64_t key_offset, int64_t value_offset,
+                       const int32_t *h_group_sizes, const int32_t *h_prefix_lens, int64_t max_suffix_len,
+                       const void *const *h_pools, const int64_t *h_pool_cap_pages, const int32_t *d_prefix_pages,
+                       const int32_t *d_page_table, int64_t table_stride, const int32_t *d_suffix_lens,
+                       const void *d_q, int64_t q_stride, float scale, void *d_out, int64_t out_stride, float *d_lse,
+                       void *d_workspace, int64_t workspace_bytes, int flags, int32_t *d_status,
+                       cpkv_stream_t stream);
+
+/* Device workspace of cpkv_attend_shared (host only); lengths as passed to it. */
+int cpkv_attend_shared_workspace_bytes(int B, int n_groups, int q_heads, int kv_heads, int head_dim,
+                                       const int32_t *h_group_sizes, const int32_t *h_prefix_lens,
+                                       int64_t max_suffix_len, int64_t *h_bytes);
 
 /* Human-readable name of a return code. */
 const char *cpkv_error_string(int code);

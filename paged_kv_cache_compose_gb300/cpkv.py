@@ -33,6 +33,7 @@ STATUS_ROW_OOB = 32
 STATUS_CHUNK_OOB = 64
 STATUS_OUT_CAPACITY = 128
 STATUS_TIMEOUT = 256
+STATUS_POS_OOB = 512
 
 GATHER_POOL = 1
 GATHER_STAGING = 2
@@ -43,6 +44,11 @@ GATHER_EARLY_INPUTS = 16  # flag: launched early behind the fill (its contract i
 FLAG_CONSUME_STAGING = 1    # layer compose: the stagings are consumed
 FLAG_EARLY_INPUTS = 2       # layer / fused compose: inputs complete before the previous kernel started
 FILL_PAGE_RUNS = 4          # fill: the index arrays are a plan of cpkv_plan_build (pages move as runs)
+ROTARY_INTERLEAVED = 8      # append: pairs (2i, 2i + 1)
+DENSE_PAGES = 16            # serving calls: page 0 is an ordinary page (a composed dense buffer)
+
+BF16 = 0
+FP16 = 1
 
 
 def compose_flags(consume_staging=False, early_inputs=False) -> int:
@@ -58,7 +64,9 @@ EXPORTED = (
     "cpkv_fill_current_planes",
     "cpkv_compose_gather", "cpkv_compose_gather_kinds", "cpkv_compose_layer", "cpkv_compose_layer_planes",
     "cpkv_compose_fused", "cpkv_compose_fused_planes", "cpkv_selftest_ring_timeout", "cpkv_ragged_plan_sizes",
-    "cpkv_ragged_plan_build", "cpkv_error_string", "cpkv_version",
+    "cpkv_ragged_plan_build", "cpkv_append_rotary", "cpkv_attend_window",
+    "cpkv_attend_window_workspace_bytes", "cpkv_attend_shared", "cpkv_attend_shared_workspace_bytes",
+    "cpkv_error_string", "cpkv_version",
 )
 
 
@@ -75,6 +83,7 @@ class _Sizes(ctypes.Structure):
 _P = ctypes.c_void_p
 _I = ctypes.c_int
 _L = ctypes.c_int64
+_F = ctypes.c_float
 _lib = None
 
 
@@ -97,6 +106,14 @@ def _declare(lib):
                                               _P]
     lib.cpkv_ragged_plan_sizes.argtypes = [_I, _I, _P, _P, _L, _P, _P]
     lib.cpkv_ragged_plan_build.argtypes = [_I, _I, _I, _I, _P, _P, _P, _L, _P, _L] + [_P] * 7 + [_L, _P, _P, _P]
+    lib.cpkv_append_rotary.argtypes = [_L] + [_I] * 7 + [_L] * 3 + [_P] * 2 + [_P, _L] * 4 + [
+        _P, _P, _L, _I, _P, _P, _L, _I, _I, _P, _P]
+    lib.cpkv_attend_window.argtypes = [_I] * 7 + [_L] * 3 + [_P, _L, _P, _P, _P, _L, _P, _P, _L, _F, _I, _I, _P, _L, _P,
+                                                             _P, _L, _I, _P, _P]
+    lib.cpkv_attend_window_workspace_bytes.argtypes = [_I] * 4 + [_P, _L, _I, _I, _P]
+    lib.cpkv_attend_shared.argtypes = [_I] * 8 + [_L] * 3 + [_P, _P, _L, _P, _P, _P, _P, _L, _P, _P, _L, _F, _P, _L, _P,
+                                                             _P, _L, _I, _P, _P]
+    lib.cpkv_attend_shared_workspace_bytes.argtypes = [_I] * 5 + [_P, _P, _L, _P]
     for name in EXPORTED:
         getattr(lib, name).restype = _I
     lib.cpkv_error_string.argtypes = [_I]
@@ -429,3 +446,198 @@ def ragged_buffers(seg_cap: int, topk_cap: int, device="cuda") -> dict:
            for k in ("seg_req", "kv_lens", "q_starts", "q_lens", "k_bases", "q_bases", "current_bases")}
     out["topk_offsets"] = torch.empty(topk_cap, dtype=torch.int32, device=device)
     return out
+
+
+# ---------------------------------------------------------------------------
+# serving on the paged rows
+# ---------------------------------------------------------------------------
+
+class PoolTable:
+    """The owner pools of a paged cache as the serving calls take them: the
+    host arrays of addresses and capacities, the page geometry, the element
+    type, and where a row keeps its keys and values (bytes).  The pools are
+    contiguous CUDA tensors [pages, page_size, width] of bf16 or fp16; the
+    table keeps them alive."""
+
+    def __init__(self, pools: Sequence, page_size: int, key_offset: int, value_offset: int, dense: bool = False):
+        import torch
+
+        self.pools = list(pools)
+        if not self.pools:
+            raise CpkvError("PoolTable", CPKV_ERR_ARG, "no pools")
+        self.dtype, self.device = self.pools[0].dtype, self.pools[0].device
+        self.code = {torch.bfloat16: BF16, torch.float16: FP16}.get(self.dtype)
+        if self.code is None:
+            raise CpkvError("PoolTable", CPKV_ERR_ARG, f"pools of {self.dtype}: bfloat16 or float16 is wanted")
+        for t in self.pools:
+            if t.dim() != 3 or t.shape[1] != page_size or t.shape[2] != self.pools[0].shape[2]:
+                raise CpkvError("PoolTable", CPKV_ERR_ARG, "a pool is [pages, page_size, width], widths alike")
+            if t.dtype != self.dtype or t.device != self.device:
+                raise CpkvError("PoolTable", CPKV_ERR_ARG, "pools of one type on one device are wanted")
+        addresses = np.array([(_dp(t) or _P(0)).value or 0 for t in self.pools], np.uint64)
+        self.page_size, self.cp_size = int(page_size), len(self.pools)
+        self.row_bytes = self.pools[0].shape[2] * 2
+        self.key_offset, self.value_offset = int(key_offset), int(value_offset)
+        self.flags = DENSE_PAGES if dense else 0
+        self._addresses, self._caps = addresses, _host_i64([t.shape[0] for t in self.pools])
+        self.addresses, self.caps = self._addresses.ctypes.data, self._caps.ctypes.data
+
+
+def _rows(t, name: str, table: PoolTable, heads: int | None, dim: int):
+    """(address, elements between tokens) of a [tokens, heads, dim] tensor
+    whose heads are contiguous within a token."""
+    shape, stride = t.shape, t.stride()
+    if t.dtype != table.dtype or t.device != table.device:
+        raise CpkvError("marshal", CPKV_ERR_ARG, f"{name}: {table.dtype} on {table.device} is wanted")
+    if len(shape) != 3 or shape[2] != dim or (heads is not None and shape[1] != heads):
+        raise CpkvError("marshal", CPKV_ERR_ARG, f"{name}: [tokens, {heads or 'heads'}, {dim}] is wanted")
+    if stride[2] != 1 or (shape[1] > 1 and stride[1] != dim):
+        raise CpkvError("marshal", CPKV_ERR_ARG, f"{name}: a token's heads have to be contiguous")
+    return t.data_ptr(), (stride[0] if shape[0] > 1 else max(stride[0], shape[1] * dim))
+
+
+def _ints(t, name: str, table: PoolTable, bits: int, dims: int):
+    """Address of a device tensor of whole numbers with a contiguous last axis."""
+    if t.device != table.device or t.element_size() * 8 != bits or t.is_floating_point() or t.dim() != dims:
+        raise CpkvError("marshal", CPKV_ERR_ARG, f"{name}: int{bits} of {dims} axes on {table.device} is wanted")
+    if t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise CpkvError("marshal", CPKV_ERR_ARG, f"{name}: contiguous entries are wanted")
+    return t.data_ptr()
+
+
+def _out(out, lse, q, table: PoolTable):
+    """Addresses of an attention's results."""
+    o, stride = _rows(out, "out", table, q.shape[1], q.shape[2])
+    if out.shape[0] != q.shape[0]:
+        raise CpkvError("marshal", CPKV_ERR_ARG, "out: as many tokens as q are wanted")
+    if lse is None:
+        return o, stride, None
+    import torch
+
+    if lse.dtype != torch.float32 or lse.device != table.device or lse.shape != q.shape[:2] or not lse.is_contiguous():
+        raise CpkvError("marshal", CPKV_ERR_ARG, "lse: contiguous float32 [tokens, heads] is wanted")
+    return o, stride, lse.data_ptr()
+
+
+def _table(t, name: str, table: PoolTable, rows: int):
+    """(address, ids between requests) of a [requests, pages] table."""
+    at = _ints(t, name, table, 32, 2)
+    if t.shape[0] != rows:
+        raise CpkvError("marshal", CPKV_ERR_ARG, f"{name}: a row per request is wanted")
+    if rows <= 1:
+        return at, t.shape[1]
+    if t.stride(0) < t.shape[1]:
+        raise CpkvError("marshal", CPKV_ERR_ARG, f"{name}: rows that overlap")
+    return at, t.stride(0)
+
+
+def cpkv_append_rotary(k, v, d_slots, d_positions, d_cos_sin, *, table: PoolTable, d_status, q=None, q_out=None,
+                       axis_of_freq=None, interleaved=False, stream=None):
+    """Keys (rotated) and values of new tokens into the pools, queries rotated
+    into ``q_out``.  ``d_positions``: [tokens], or [axes, tokens] with
+    ``axis_of_freq`` naming each frequency's axis; ``d_cos_sin``: float32
+    [positions, rot_dim], cosines then sines."""
+    import torch
+
+    n, kv_heads, key_dim = k.shape
+    kp, ks = _rows(k, "k", table, kv_heads, key_dim)
+    vp, vs = _rows(v, "v", table, kv_heads, v.shape[2])
+    qp = qs = qop = qos = 0
+    q_heads = 0
+    if q is not None:
+        q_heads = q.shape[1]
+        qp, qs = _rows(q, "q", table, q_heads, key_dim)
+        qop, qos = _rows(q_out, "q_out", table, q_heads, key_dim)
+        if q.shape[0] != n or q_out.shape[0] != n:
+            raise CpkvError("marshal", CPKV_ERR_ARG, "q and q_out: as many tokens as k are wanted")
+    sp = _ints(d_slots, "slots", table, 64, 1)
+    pp = _ints(d_positions, "positions", table, 32, d_positions.dim())
+    axes, pos_stride = (1, n) if d_positions.dim() == 1 else (d_positions.shape[0], d_positions.stride(0))
+    if v.shape[0] != n or d_slots.shape[0] != n or d_positions.dim() > 2 or d_positions.shape[-1] != n:
+        raise CpkvError("marshal", CPKV_ERR_ARG, "v, slots and positions: one entry per token of k is wanted")
+    if (d_cos_sin.dtype != torch.float32 or d_cos_sin.dim() != 2 or d_cos_sin.device != table.device
+            or not d_cos_sin.is_contiguous()):
+        raise CpkvError("marshal", CPKV_ERR_ARG, "cos_sin: contiguous float32 [positions, rot_dim] is wanted")
+    axis = None
+    if axis_of_freq is not None:
+        axis = bytes(axis_of_freq)
+        if len(axis) != d_cos_sin.shape[1] // 2:
+            raise CpkvError("marshal", CPKV_ERR_ARG, "axis_of_freq: an axis per frequency is wanted")
+    rc = load().cpkv_append_rotary(
+        n, table.page_size, table.cp_size, table.code, q_heads, kv_heads, key_dim, v.shape[2], table.row_bytes,
+        table.key_offset, table.value_offset, table.addresses, table.caps, kp, ks, vp, vs, qp, qs, qop, qos, sp, pp,
+        pos_stride, axes, axis, d_cos_sin.data_ptr(), d_cos_sin.shape[0], d_cos_sin.shape[1],
+        table.flags | (ROTARY_INTERLEAVED if interleaved else 0), d_status.data_ptr(), _stream(stream))
+    _check("cpkv_append_rotary", rc)
+
+
+def cpkv_attend_window_workspace_bytes(B, q_heads, kv_heads, head_dim, q_lens, max_kv_len, window=0, sinks=0) -> int:
+    """Device workspace of ``cpkv_attend_window`` (``q_lens`` None: one query each)."""
+    ql = None if q_lens is None else _host_i32(q_lens)
+    out = ctypes.c_int64(0)
+    _check("cpkv_attend_window_workspace_bytes", load().cpkv_attend_window_workspace_bytes(
+        B, q_heads, kv_heads, head_dim, None if ql is None else ql.ctypes.data, max_kv_len, window, sinks,
+        ctypes.byref(out)))
+    return int(out.value)
+
+
+def cpkv_attend_window(q, q_lens, page_table, d_kv_lens, *, table: PoolTable, kv_heads, max_kv_len, window, sinks,
+                       scale, out, lse, workspace, d_status, stream=None):
+    """Causal attention of ``q`` [tokens, heads, dim] over paged rows, with a
+    window and first tokens that stay visible (see include/cpkv.h)."""
+    qp, qs = _rows(q, "q", table, None, q.shape[2])
+    op, os_, lp = _out(out, lse, q, table)
+    lens = _ints(d_kv_lens, "kv_lens", table, 32, 1)
+    B = d_kv_lens.shape[0]
+    tp, ts = _table(page_table, "page_table", table, B)
+    if q_lens is None:
+        ql, tokens = None, B
+    else:
+        ql = _host_i32(q_lens)
+        tokens = int(ql.sum()) if len(ql) == B else -1
+    if tokens != q.shape[0]:
+        raise CpkvError("marshal", CPKV_ERR_ARG, "q_lens: one length per request, adding up to q's tokens, is wanted")
+    if max_kv_len > page_table.shape[1] * table.page_size:
+        raise CpkvError("cpkv_attend_window", CPKV_ERR_CAPACITY, "max_kv_len beyond the page table")
+    rc = load().cpkv_attend_window(
+        B, table.page_size, table.cp_size, table.code, q.shape[1], kv_heads, q.shape[2], table.row_bytes,
+        table.key_offset, table.value_offset, None if ql is None else ql.ctypes.data, max_kv_len, table.addresses,
+        table.caps, tp, ts, lens, qp, qs, scale, window, sinks, op, os_, lp,
+        None if workspace is None else workspace.data_ptr(), 0 if workspace is None else workspace.numel(),
+        table.flags, d_status.data_ptr(), _stream(stream))
+    _check("cpkv_attend_window", rc)
+
+
+def cpkv_attend_shared_workspace_bytes(B, q_heads, kv_heads, head_dim, group_sizes, prefix_lens, max_suffix_len) -> int:
+    """Device workspace of ``cpkv_attend_shared``."""
+    gs, pl = _host_i32(group_sizes), _host_i32(prefix_lens)
+    out = ctypes.c_int64(0)
+    _check("cpkv_attend_shared_workspace_bytes", load().cpkv_attend_shared_workspace_bytes(
+        B, len(gs), q_heads, kv_heads, head_dim, _hp(gs), _hp(pl), max_suffix_len, ctypes.byref(out)))
+    return int(out.value)
+
+
+def cpkv_attend_shared(q, group_sizes, prefix_lens, prefix_pages, page_table, d_suffix_lens, *, table: PoolTable,
+                       kv_heads, max_suffix_len, scale, out, lse, workspace, d_status, stream=None):
+    """One query token per request over its group's shared prefix and its own
+    suffix (see include/cpkv.h)."""
+    qp, qs = _rows(q, "q", table, None, q.shape[2])
+    op, os_, lp = _out(out, lse, q, table)
+    lens = _ints(d_suffix_lens, "suffix_lens", table, 32, 1)
+    B = d_suffix_lens.shape[0]
+    tp, ts = _table(page_table, "page_table", table, B)
+    gs, pl = _host_i32(group_sizes), _host_i32(prefix_lens)
+    pp = _ints(prefix_pages, "prefix_pages", table, 32, 1)
+    if q.shape[0] != B or len(gs) != len(pl):
+        raise CpkvError("marshal", CPKV_ERR_ARG, "a query per request and a prefix length per group are wanted")
+    if int(pl.sum()) // table.page_size > prefix_pages.shape[0]:
+        raise CpkvError("cpkv_attend_shared", CPKV_ERR_CAPACITY, "prefix_pages shorter than the prefixes")
+    if max_suffix_len > page_table.shape[1] * table.page_size:
+        raise CpkvError("cpkv_attend_shared", CPKV_ERR_CAPACITY, "max_suffix_len beyond the page table")
+    rc = load().cpkv_attend_shared(
+        B, len(gs), table.page_size, table.cp_size, table.code, q.shape[1], kv_heads, q.shape[2], table.row_bytes,
+        table.key_offset, table.value_offset, gs.ctypes.data, pl.ctypes.data, max_suffix_len, table.addresses,
+        table.caps, pp, tp, ts, lens, qp, qs, scale, op, os_, lp,
+        None if workspace is None else workspace.data_ptr(), 0 if workspace is None else workspace.numel(),
+        table.flags, d_status.data_ptr(), _stream(stream))
+    _check("cpkv_attend_shared", rc)

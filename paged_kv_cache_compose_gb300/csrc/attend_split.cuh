@@ -1,0 +1,475 @@
+// Attention of few query rows over long paged keys: the keys are cut into
+// stretches, each block reduces its stretch to (m, l, o), and a second kernel
+// joins the parts of each row.
+//
+// Bytes bound it: 16 packed rows do 4 D * 16 operations on the 4 D bytes of a
+// key and its value, far below what the matrix instructions give, so what
+// counts is bytes in flight.  Work is counted in units of 64 keys of one tile
+// (sequence, key/value head, 16 rows); all units of the call form one line that
+// is cut evenly over the blocks, whatever the lengths are, and a block's warps
+// each own 16 keys of every unit with a cp.async ring of their own, so that no
+// block-wide barrier stands inside a stretch.
+#pragma once
+
+#include "attend.cuh"
+
+namespace cpkv {
+
+constexpr int kSplitWarps = 4;
+constexpr int kWarpKeys = kSplitTile / kSplitWarps;  // 16
+
+template <int D>
+struct SplitShape {
+  static constexpr int kRow = D * 2;                       // bytes of a key (or value) vector
+  static constexpr int kStage = kWarpKeys * kRow * 2;      // keys, then values
+  static constexpr int kStages = D == 128 ? 3 : 4;
+  static constexpr int kRing = kSplitWarps * kStages * kStage;
+  static constexpr int kJoin = 2 * kSplitRows * D * 4;     // values of two warps while a tile's parts are joined
+  static constexpr int kSmem = kRing + kJoin + kSplitWarps * kSplitRows * 8;
+};
+
+// A position on the line of units.
+template <int N>
+struct Cursor {
+  int s, h, rt, j, row_tiles;
+  int nq, kv;
+  KeyRange keys;
+
+  CPKV_DEV void enter(const SplitParams<N> &p, int seq) {
+    s = seq;
+    nq = p.seqs.q_count(s);
+    kv = p.seqs.kv_len(s);
+    keys = key_range<kSplitTile>(kv, nq, 0, nq, p.seqs.causal, p.seqs.window, p.seqs.sinks);
+    row_tiles = (nq * (int)p.io.group.d + kSplitRows - 1) / kSplitRows;
+  }
+  CPKV_DEV void seek(const SplitParams<N> &p, const int *cum, int u) {
+    enter(p, upper_index(cum, p.seqs.count, u));
+    const int local = u - cum[s];
+    const int tile = local / keys.n_tiles;
+    j = local - tile * keys.n_tiles;
+    h = tile / row_tiles;
+    rt = tile - h * row_tiles;
+  }
+  // To the next unit of the line; there must be one.
+  CPKV_DEV void advance(const SplitParams<N> &p) {
+    if (++j < keys.n_tiles) return;
+    j = 0;
+    if (++rt < row_tiles) return;
+    rt = 0;
+    if (++h < p.io.kv_heads) return;
+    h = 0;
+    do {
+      enter(p, s + 1);
+    } while (keys.n_tiles == 0 || row_tiles == 0);
+  }
+};
+
+template <typename T, int D, int N>
+__global__ void __launch_bounds__(kSplitWarps * 32) attend_split_kernel(const __grid_constant__ SplitParams<N> p) {
+  using Shape = SplitShape<D>;
+  extern __shared__ __align__(128) char smem[];
+  __shared__ int scan_scratch[33];
+  int *cum = reinterpret_cast<int *>(smem + Shape::kSmem);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int count = p.seqs.count;
+
+  // units before each sequence
+  int total = 0;
+  for (int s0 = 0; s0 < count; s0 += kSplitWarps * 32) {
+    const int s = s0 + (int)threadIdx.x;
+    int mine = 0;
+    if (s < count) {
+      Cursor<N> c;
+      c.enter(p, s);
+      mine = c.keys.n_tiles * c.row_tiles * p.io.kv_heads;
+      if (blockIdx.x == 0 && p.seqs.kv_len_bad(s)) raise_status(p.seqs.status, CPKV_STATUS_OUT_CAPACITY);
+    }
+    int part;
+    const int before = block_exclusive_scan(mine, scan_scratch, &part);
+    if (s < count) {
+      cum[s] = total + before;
+      if (blockIdx.x == 0) p.space.cum[s] = total + before;
+    }
+    total += part;
+  }
+  if (blockIdx.x == 0 && threadIdx.x == 0) p.space.cum[count] = total;
+  __syncthreads();
+
+  const int chunk = split_chunk(total, (int)gridDim.x);
+  const int64_t first = (int64_t)blockIdx.x * chunk;
+  if (first >= total) return;
+  const int u0 = (int)first, u1 = (int)min64(first + chunk, total);
+
+  char *ring = smem + warp * Shape::kStages * Shape::kStage;
+  const uint32_t ring_addr = smem_addr(ring);
+  float *join = reinterpret_cast<float *>(smem + Shape::kRing);
+  float2 *ml = reinterpret_cast<float2 *>(smem + Shape::kRing + Shape::kJoin);
+
+  // loads: lanes 0..15 own one key each
+  Cursor<N> ld;
+  ld.seek(p, cum, u0);
+  int ld_u = u0, ld_key = 0, ld_page = -1;
+  bool ld_sees = false;
+  auto look_up = [&] {  // the page of this lane's key, one unit ahead of its copy
+    ld_key = ld.keys.tile_start(ld.j, kSplitTile) + warp * kWarpKeys + (lane & 15);
+    ld_sees = ld.keys.any_sees(ld_key);
+    ld_page = ld_sees ? p.seqs.pages(ld.s)[div_by(ld_key, p.pools.page_size)] : -1;
+  };
+  look_up();
+  auto load_next = [&](int stage) {
+    if (ld_u < u1) {
+      const char *row = nullptr;
+      if (ld_sees) {
+        row = page_address(p.pools, ld_page);
+        if (row == nullptr) {
+          raise_status(p.seqs.status, CPKV_STATUS_PAGE_OOB);
+        } else {
+          row += (int64_t)(ld_key - div_by(ld_key, p.pools.page_size) * (int)p.pools.page_size.d) * p.pools.row_bytes;
+        }
+      }
+      constexpr int kLanes = D / 8, kRows = 32 / kLanes;  // lanes of a vector, keys of one warp-wide copy
+      const int c = lane % kLanes;
+      const uint32_t dst = ring_addr + stage * Shape::kStage;
+      const int64_t k_at = p.io.k_off + (int64_t)ld.h * Shape::kRow + c * 16;
+      const int64_t v_at = p.io.v_off + (int64_t)ld.h * Shape::kRow + c * 16;
+#pragma unroll
+      for (int i = 0; i < kWarpKeys / kRows; ++i) {
+        const int key = i * kRows + lane / kLanes;
+        const char *src = reinterpret_cast<const char *>(__shfl_sync(0xffffffffu, (unsigned long long)row, key));
+        const int bytes = src == nullptr ? 0 : 16;
+        if (src == nullptr) src = reinterpret_cast<const char *>(p.io.q);  // a valid address that is not read
+        const uint32_t to = dst + key * Shape::kRow + ((c ^ (key & 7)) << 4);
+        cp_async16(to, bytes ? src + k_at : src, bytes);
+        cp_async16(to + kWarpKeys * Shape::kRow, bytes ? src + v_at : src, bytes);
+      }
+      if (++ld_u < u1) {
+        ld.advance(p);
+        look_up();
+      }
+    }
+    cp_async_commit();
+  };
+#pragma unroll
+  for (int i = 0; i < Shape::kStages - 1; ++i) load_next(i);
+
+  Cursor<N> at;
+  at.seek(p, cum, u0);
+  int stage = 0, seg_j0 = 0;
+  bool fresh = true, first_segment = true;
+  uint32_t qf[D / 16][4];
+  float o[D / 8][4], m[2], l[2];
+  RowMask mask[2];
+  int full_lo = 0, full_hi = 0;  // keys in [full_lo, full_hi) are seen by every row of the tile
+
+  for (int u = u0; u < u1; ++u) {
+    if (fresh) {
+      fresh = false;
+      seg_j0 = at.j;
+      const int group = p.io.group.d, rows = at.nq * group;
+      full_lo = 0;
+      full_hi = INT32_MAX;
+      const int q0 = p.seqs.q_begin(at.s);
+      int last = at.rt * kSplitRows + kSplitRows - 1;
+      if (last >= rows) last = rows - 1;
+      const RowMask ma = row_mask(at.kv, at.nq, div_by(at.rt * kSplitRows, p.io.group), p.seqs.causal, p.seqs.window, p.seqs.sinks);
+      const RowMask mb = row_mask(at.kv, at.nq, div_by(last, p.io.group), p.seqs.causal, p.seqs.window, p.seqs.sinks);
+      full_hi = ma.hi;
+      full_lo = mb.lo;
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const int row = at.rt * kSplitRows + (lane >> 2) + 8 * r;
+        const bool in = row < rows;
+        const int i = div_by(row, p.io.group), g = row - i * group;
+        mask[r] = row_mask(at.kv, at.nq, i, p.seqs.causal, p.seqs.window, p.seqs.sinks);
+        const char *src = p.io.q + (q0 + i) * p.io.q_stride + ((int64_t)at.h * group + g) * Shape::kRow + (lane & 3) * 4;
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+          qf[k][r] = in ? *reinterpret_cast<const uint32_t *>(src + k * 32) : 0u;
+          qf[k][r + 2] = in ? *reinterpret_cast<const uint32_t *>(src + k * 32 + 16) : 0u;
+        }
+        m[r] = -INFINITY;
+        l[r] = 0.f;
+      }
+#pragma unroll
+      for (int n = 0; n < D / 8; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[n][i] = 0.f;
+    }
+    cp_async_wait<Shape::kStages - 2>();
+    __syncwarp();
+    load_next(stage == 0 ? Shape::kStages - 1 : stage - 1);
+
+    // x = scale log2(e) q.k of 16 rows and this warp's 16 keys
+    const uint32_t kb = ring_addr + stage * Shape::kStage;
+    float x[2][4] = {};
+    {
+      const int key = (lane & 7) + ((lane >> 4) << 3);
+      const uint32_t row = kb + key * Shape::kRow;
+#pragma unroll
+      for (int k = 0; k < D / 16; ++k) {
+        uint32_t b[4];
+        ldmatrix_x4(b, row + (((2 * k + ((lane >> 3) & 1)) ^ (key & 7)) << 4));
+        mma_16816<T>(x[0], qf[k], b[0], b[1]);
+        mma_16816<T>(x[1], qf[k], b[2], b[3]);
+      }
+    }
+    const int key0 = at.keys.tile_start(at.j, kSplitTile) + warp * kWarpKeys;
+    const bool whole = key0 + kWarpKeys <= full_hi && (key0 >= full_lo || key0 + kWarpKeys <= p.seqs.sinks);
+#pragma unroll
+    for (int n = 0; n < 2; ++n)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        x[n][i] *= p.io.scale_log2;
+        if (!whole && !mask[i >> 1].sees(key0 + n * 8 + (lane & 3) * 2 + (i & 1))) x[n][i] = -INFINITY;
+      }
+    float shift[2];
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      float best = fmaxf(fmaxf(x[0][2 * r], x[0][2 * r + 1]), fmaxf(x[1][2 * r], x[1][2 * r + 1]));
+      best = fmaxf(best, __shfl_xor_sync(0xffffffffu, best, 1));
+      best = fmaxf(best, __shfl_xor_sync(0xffffffffu, best, 2));
+      const float next = fmaxf(m[r], best);
+      shift[r] = next == -INFINITY ? 0.f : next;
+      const float fall = exp2_approx(m[r] - shift[r]);
+      if (__any_sync(0xffffffffu, next != m[r])) {
+        l[r] *= fall;
+#pragma unroll
+        for (int n = 0; n < D / 8; ++n) {
+          o[n][2 * r] *= fall;
+          o[n][2 * r + 1] *= fall;
+        }
+      }
+      m[r] = next;
+    }
+    uint32_t pf[4];  // weights as the first operand; rounded to T for the product, summed before it
+#pragma unroll
+    for (int n = 0; n < 2; ++n)
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const float a = exp2_approx(x[n][2 * r] - shift[r]), b = exp2_approx(x[n][2 * r + 1] - shift[r]);
+        l[r] += a + b;
+        pf[2 * n + r] = pack2<T>(a, b);
+      }
+    {
+      const int key = lane & 15;
+      const uint32_t row = kb + kWarpKeys * Shape::kRow + key * Shape::kRow;
+#pragma unroll
+      for (int n = 0; n < D / 16; ++n) {
+        uint32_t b[4];
+        ldmatrix_x4_trans(b, row + (((2 * n + (lane >> 4)) ^ (key & 7)) << 4));
+        mma_16816<T>(o[2 * n], pf, b[0], b[1]);
+        mma_16816<T>(o[2 * n + 1], pf, b[2], b[3]);
+      }
+    }
+    __syncwarp();
+    stage = stage + 1 == Shape::kStages ? 0 : stage + 1;
+
+    const bool tile_ends = at.j + 1 == at.keys.n_tiles;
+    if (!tile_ends && u + 1 < u1) {
+      ++at.j;
+      continue;
+    }
+
+    // join the four warps' parts: common maximum, then values pairwise
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
+      l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
+      if ((lane & 3) == 0) ml[warp * kSplitRows + (lane >> 2) + 8 * r] = make_float2(m[r], l[r]);
+    }
+    __syncthreads();
+    float big[2], sum[2];
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      const int row = (lane >> 2) + 8 * r;
+      float2 v[kSplitWarps];
+      big[r] = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < kSplitWarps; ++w) {
+        v[w] = ml[w * kSplitRows + row];
+        big[r] = fmaxf(big[r], v[w].x);
+      }
+      const float base = big[r] == -INFINITY ? 0.f : big[r];
+      sum[r] = 0.f;
+#pragma unroll
+      for (int w = 0; w < kSplitWarps; ++w) sum[r] += exp2_approx(v[w].x - base) * v[w].y;
+      const float mine = exp2_approx(m[r] - base);
+#pragma unroll
+      for (int n = 0; n < D / 8; ++n) {
+        o[n][2 * r] *= mine;
+        o[n][2 * r + 1] *= mine;
+      }
+    }
+    auto each = [&](float *buf, bool put) {
+#pragma unroll
+      for (int n = 0; n < D / 8; ++n)
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          float2 *q = reinterpret_cast<float2 *>(buf + (n * 32 + lane) * 4 + 2 * r);
+          if (put) {
+            *q = make_float2(o[n][2 * r], o[n][2 * r + 1]);
+          } else {
+            o[n][2 * r] += q->x;
+            o[n][2 * r + 1] += q->y;
+          }
+        }
+    };
+    if (warp >= 2) each(join + (warp - 2) * kSplitRows * D, true);
+    __syncthreads();
+    if (warp < 2) each(join + warp * kSplitRows * D, false);
+    if (warp == 1) each(join + kSplitRows * D, true);
+    __syncthreads();
+    if (warp == 0) {
+      each(join + kSplitRows * D, false);
+      const bool complete = tile_ends && seg_j0 == 0;
+      const int group = p.io.group.d, rows = at.nq * group;
+      const int64_t slot = complete ? 2 * (int64_t)gridDim.x + whole_tile(p.seqs, at.s, at.rt, at.h, group, p.tiles_cap)
+                                    : 2 * (int64_t)blockIdx.x + (first_segment ? 0 : 1);
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const int in_tile = (lane >> 2) + 8 * r, row = at.rt * kSplitRows + in_tile;
+        if (row >= rows) continue;
+        if (complete && p.direct) {
+          const int i = div_by(row, p.io.group), g = row - i * group;
+          const int64_t token = p.seqs.q_begin(at.s) + i;
+          const int head = at.h * group + g;
+          const float inv = sum[r] > 0.f ? 1.f / sum[r] : 0.f;
+          char *dst = p.io.out + token * p.io.out_stride + (int64_t)head * Shape::kRow + (lane & 3) * 4;
+#pragma unroll
+          for (int n = 0; n < D / 8; ++n)
+            *reinterpret_cast<uint32_t *>(dst + n * 16) = pack2<T>(o[n][2 * r] * inv, o[n][2 * r + 1] * inv);
+          if (p.io.lse != nullptr && (lane & 3) == 0)
+            p.io.lse[token * p.io.q_heads + head] = sum[r] > 0.f ? (big[r] + log2_approx(sum[r])) * kLn2 : -INFINITY;
+        } else {
+          float *dst = p.space.o + (slot * kSplitRows + in_tile) * D + (lane & 3) * 2;
+#pragma unroll
+          for (int n = 0; n < D / 8; ++n) *reinterpret_cast<float2 *>(dst + n * 8) = make_float2(o[n][2 * r], o[n][2 * r + 1]);
+          if ((lane & 3) == 0)
+            *reinterpret_cast<float2 *>(p.space.ml + (slot * kSplitRows + in_tile) * 2) = make_float2(big[r], sum[r]);
+        }
+      }
+    }
+    __syncthreads();
+    first_segment = false;
+    fresh = true;
+    if (u + 1 < u1) at.advance(p);
+  }
+  cp_async_wait<0>();
+}
+
+// ---------------------------------------------------------------------------
+// joining
+// ---------------------------------------------------------------------------
+
+// The parts of one row: `count` of them at slots first_slot, then next_slot, next_slot + 2, ...
+struct RowParts {
+  int64_t first_slot, next_slot;
+  int count, in_tile;
+  bool done;  // the split pass wrote the output itself
+  CPKV_DEV int64_t slot(int k) const { return k == 0 ? first_slot : next_slot + 2 * (int64_t)(k - 1); }
+};
+
+template <int N>
+CPKV_DEV RowParts row_parts(const SplitSource<N> &src, const AttendIo &io, int s, int i, int head) {
+  const int group = io.group.d, h = div_by(head, io.group), g = head - h * group;
+  const int nq = src.seqs.q_count(s), kv = src.seqs.kv_len(s);
+  const KeyRange keys = key_range<kSplitTile>(kv, nq, 0, nq, src.seqs.causal, src.seqs.window, src.seqs.sinks);
+  RowParts r;
+  r.done = false;
+  const int row = i * group + g, rt = row / kSplitRows, row_tiles = (nq * group + kSplitRows - 1) / kSplitRows;
+  r.in_tile = row - rt * kSplitRows;
+  r.count = 0;
+  r.first_slot = r.next_slot = 0;
+  if (keys.n_tiles == 0) return r;
+  const int chunk = split_chunk(src.space.cum[src.seqs.count], src.space.grid);
+  const int begin = src.space.cum[s] + (h * row_tiles + rt) * keys.n_tiles, end = begin + keys.n_tiles;
+  const int c0 = begin / chunk, c1 = (end - 1) / chunk;
+  r.count = c1 - c0 + 1;
+  if (c0 == c1) {
+    r.done = src.direct;
+    r.first_slot = 2 * (int64_t)src.space.grid + whole_tile(src.seqs, s, rt, h, group, src.tiles_cap);
+  } else {
+    r.first_slot = 2 * (int64_t)c0 + (begin == c0 * chunk ? 0 : 1);
+    r.next_slot = 2 * (int64_t)(c0 + 1);
+  }
+  return r;
+}
+
+template <int D>
+struct RowSum {
+  static constexpr int kEach = D / 32;
+  float m = -INFINITY, l = 0.f, o[kEach] = {};
+
+  CPKV_DEV void add(const SplitSpace &space, const RowParts &parts, int lane) {
+    for (int k0 = 0; k0 < parts.count; k0 += 32) {
+      const int k = k0 + lane;
+      float2 v = make_float2(-INFINITY, 0.f);
+      if (k < parts.count)
+        v = *reinterpret_cast<const float2 *>(space.ml + (parts.slot(k) * kSplitRows + parts.in_tile) * 2);
+      float best = v.x;
+#pragma unroll
+      for (int w = 16; w > 0; w >>= 1) best = fmaxf(best, __shfl_xor_sync(0xffffffffu, best, w));
+      const float next = fmaxf(m, best), base = next == -INFINITY ? 0.f : next;
+      const float fall = exp2_approx(m - base), weight = exp2_approx(v.x - base);
+      float sum = weight * v.y;
+#pragma unroll
+      for (int w = 16; w > 0; w >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, w);
+      l = l * fall + sum;
+      m = next;
+#pragma unroll
+      for (int e = 0; e < kEach; ++e) o[e] *= fall;
+      const int n = parts.count - k0 < 32 ? parts.count - k0 : 32;
+      for (int i = 0; i < n; ++i) {
+        const float w = __shfl_sync(0xffffffffu, weight, i);
+        const float *src = space.o + (parts.slot(k0 + i) * kSplitRows + parts.in_tile) * D + lane * kEach;
+        if constexpr (kEach == 4) {
+          const float4 x = *reinterpret_cast<const float4 *>(src);
+          o[0] += w * x.x, o[1] += w * x.y, o[2] += w * x.z, o[3] += w * x.w;
+        } else {
+          const float2 x = *reinterpret_cast<const float2 *>(src);
+          o[0] += w * x.x, o[1] += w * x.y;
+        }
+      }
+    }
+  }
+};
+
+template <int N, int M>
+struct JoinParams {
+  SplitSource<N> a;  // the sequences that own the query tokens
+  SplitSource<M> b;  // a second pass over the same tokens (two_passes), else unused
+  AttendIo io;
+  int two_passes;
+  int64_t rows;  // tokens * q_heads
+};
+
+// A warp per row (token, query head).
+template <typename T, int D, int N, int M>
+__global__ void __launch_bounds__(128) attend_join_kernel(const __grid_constant__ JoinParams<N, M> p) {
+  const int lane = threadIdx.x & 31;
+  const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
+  if (row >= p.rows) return;
+  const int token = (int)(row / p.io.q_heads), head = (int)(row - (int64_t)token * p.io.q_heads);
+  RowSum<D> sum;
+  {
+    const int s = p.a.seqs.uniform_q ? token / p.a.seqs.uniform_q : upper_index(p.a.seqs.cu_q, p.a.seqs.count, token);
+    const RowParts parts = row_parts(p.a, p.io, s, token - p.a.seqs.q_begin(s), head);
+    if (parts.done) return;
+    sum.add(p.a.space, parts, lane);
+  }
+  if (p.two_passes) {
+    const int s = p.b.seqs.uniform_q ? token / p.b.seqs.uniform_q : upper_index(p.b.seqs.cu_q, p.b.seqs.count, token);
+    sum.add(p.b.space, row_parts(p.b, p.io, s, token - p.b.seqs.q_begin(s), head), lane);
+  }
+  const float inv = sum.l > 0.f ? 1.f / sum.l : 0.f;
+  char *dst = p.io.out + token * p.io.out_stride + (int64_t)head * D * 2 + lane * (D / 16);
+  if constexpr (D == 128) {
+    *reinterpret_cast<uint2 *>(dst) =
+        make_uint2(pack2<T>(sum.o[0] * inv, sum.o[1] * inv), pack2<T>(sum.o[2] * inv, sum.o[3] * inv));
+  } else {
+    *reinterpret_cast<uint32_t *>(dst) = pack2<T>(sum.o[0] * inv, sum.o[1] * inv);
+  }
+  if (p.io.lse != nullptr && lane == 0) p.io.lse[row] = sum.l > 0.f ? (sum.m + log2_approx(sum.l)) * kLn2 : -INFINITY;
+}
+
+}  // namespace cpkv

@@ -4,7 +4,8 @@
 arrays, and builds the plan once per batch (``cpkv_plan_build``).
 ``ComposeLayers`` owns the writers' staging regions and the dense buffers
 (two, alternated by layer parity: a dense buffer is reused two layers later)
-and runs the per-layer fill + gather.  Allocation uses torch device memory;
+and runs the per-layer fill + gather.  ``PagedCache`` serves from the pools:
+rotated rows of new tokens into them, attention over them.  Allocation uses torch device memory;
 every computation is a library kernel.
 """
 from __future__ import annotations
@@ -178,3 +179,113 @@ class ComposeLayers:
         self.fill(cur_rows_per_writer, stream, early_inputs=early_inputs, page_runs=page_runs)
         self.gather(pools, dense, stream, consume_staging=consume_staging, early_inputs=early_inputs)
         return dense
+
+
+class PagedCache:
+    """Token rows in owner pools, written and attended to by a serving step.
+
+    ``pools``: the cp owner slabs [pages, page_size, width] of bf16 or fp16; a
+    row keeps ``kv_heads`` key vectors of ``key_dim`` elements at
+    ``key_offset`` and as many value vectors of ``value_dim`` at
+    ``value_offset`` (elements; by default keys, then values).  ``dense``: the
+    one "pool" is a composed dense buffer, whose page 0 is an ordinary page.
+    The handle keeps the pools' addresses, a status word (``d_status``) and,
+    per stream, a workspace that grows as calls need it.  Calls are
+    asynchronous; a first call of a size outside a CUDA graph's capture makes
+    the workspace that captured calls then use."""
+
+    def __init__(self, pools, *, page_size: int, kv_heads: int, key_dim: int, value_dim: int | None = None,
+                 key_offset: int = 0, value_offset: int | None = None, dense: bool = False):
+        self.kv_heads, self.key_dim = int(kv_heads), int(key_dim)
+        self.value_dim = self.key_dim if value_dim is None else int(value_dim)
+        if value_offset is None:
+            value_offset = key_offset + self.kv_heads * self.key_dim
+        self.table = cpkv.PoolTable(pools, page_size, 2 * key_offset, 2 * value_offset, dense)
+        self.device = self.table.device
+        self.d_status = torch.zeros(1, dtype=torch.int32, device=self.device)
+        self._workspaces = {}  # by stream
+        self._outgrown = []  # a captured graph may still use them
+
+    def _stream(self, stream):
+        return torch.cuda.current_stream(self.device) if stream is None else stream
+
+    def _with_workspace(self, stream, call, size):
+        """``call(workspace)``, with a larger workspace where the call asks for one."""
+        key = stream.cuda_stream
+        workspace = self._workspaces.get(key)
+        try:
+            return call(workspace)
+        except cpkv.CpkvError as e:
+            need = size() if e.code in (cpkv.CPKV_ERR_CAPACITY, cpkv.CPKV_ERR_ARG) else 0
+            if need <= (0 if workspace is None else workspace.numel()):
+                raise
+        with torch.cuda.stream(stream):
+            grown = torch.empty(need + need // 4, dtype=torch.uint8, device=self.device)
+        if workspace is not None:
+            self._outgrown.append(workspace)
+        self._workspaces[key] = grown
+        return call(grown)
+
+    def append_rotary(self, k, v, slots, positions, cos_sin, *, q=None, q_out=None, axis_of_freq=None,
+                      interleaved=False, stream=None):
+        """Rows of new tokens: ``k`` [tokens, kv_heads, key_dim] rotated by
+        ``positions`` and ``v`` into cache rows ``slots`` (page * page_size +
+        offset; negative: padding), ``q`` rotated into ``q_out`` (allocated
+        when None), which is returned."""
+        if k.dim() != 3 or k.shape[1] != self.kv_heads or k.shape[2] != self.key_dim or v.dim() != 3 \
+                or v.shape[1] != self.kv_heads or v.shape[2] != self.value_dim:
+            raise cpkv.CpkvError("append_rotary", cpkv.CPKV_ERR_ARG, "k and v: [tokens, kv_heads, dim] of this cache")
+        if q is not None and q_out is None:
+            with torch.cuda.stream(self._stream(stream)):
+                q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        cpkv.cpkv_append_rotary(k, v, slots, positions, cos_sin, table=self.table, d_status=self.d_status, q=q,
+                                q_out=q_out, axis_of_freq=axis_of_freq, interleaved=interleaved, stream=stream)
+        return q_out
+
+    def _results(self, q, out, stream):
+        if q.dim() != 3 or q.shape[2] != self.key_dim or self.value_dim != self.key_dim:
+            raise cpkv.CpkvError("attend", cpkv.CPKV_ERR_ARG,
+                                 "q: [tokens, heads, key_dim] over a cache of equal key and value widths")
+        if out is None:
+            with torch.cuda.stream(stream):
+                out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        return out
+
+    def attend_window(self, q, q_lens, page_table, kv_lens, *, max_kv_len: int, window: int = 0, sinks: int = 0,
+                      scale: float | None = None, out=None, lse=None, stream=None):
+        """Causal attention of the newest ``q_lens[b]`` tokens of each request
+        (None: one each) over its ``kv_lens[b]`` rows, those within ``window``
+        and the first ``sinks``.  Returns ``out``; ``lse`` (float32 [tokens,
+        heads]) is written when given."""
+        stream = self._stream(stream)
+        out = self._results(q, out, stream)
+        scale = self.key_dim ** -0.5 if scale is None else scale
+
+        def call(workspace):
+            cpkv.cpkv_attend_window(q, q_lens, page_table, kv_lens, table=self.table, kv_heads=self.kv_heads,
+                                    max_kv_len=max_kv_len, window=window, sinks=sinks, scale=scale, out=out, lse=lse,
+                                    workspace=workspace, d_status=self.d_status, stream=stream)
+
+        self._with_workspace(stream, call, lambda: cpkv.cpkv_attend_window_workspace_bytes(
+            kv_lens.shape[0], q.shape[1], self.kv_heads, self.key_dim, q_lens, max_kv_len, window, sinks))
+        return out
+
+    def attend_shared(self, q, group_sizes, prefix_lens, prefix_pages, page_table, suffix_lens, *,
+                      max_suffix_len: int, scale: float | None = None, out=None, lse=None, stream=None):
+        """A decode step of requests in consecutive groups: ``q`` [requests,
+        heads, dim] over each group's shared prefix (``prefix_pages``, CSR by
+        group) and each request's own ``suffix_lens[b]`` rows.  Returns
+        ``out``; ``lse`` as in ``attend_window``."""
+        stream = self._stream(stream)
+        out = self._results(q, out, stream)
+        scale = self.key_dim ** -0.5 if scale is None else scale
+
+        def call(workspace):
+            cpkv.cpkv_attend_shared(q, group_sizes, prefix_lens, prefix_pages, page_table, suffix_lens,
+                                    table=self.table, kv_heads=self.kv_heads, max_suffix_len=max_suffix_len,
+                                    scale=scale, out=out, lse=lse, workspace=workspace, d_status=self.d_status,
+                                    stream=stream)
+
+        self._with_workspace(stream, call, lambda: cpkv.cpkv_attend_shared_workspace_bytes(
+            suffix_lens.shape[0], q.shape[1], self.kv_heads, self.key_dim, group_sizes, prefix_lens, max_suffix_len))
+        return out
