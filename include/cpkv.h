@@ -624,7 +624,7 @@ int cpkv_append_rotary(int64_t n_tokens, int page_size, int cp_size, int dtype, 
  * request sees should be finite: a neighbouring query that does not see it
  * multiplies it by a weight of zero.
  *   B              requests, at most CPKV_MAX_BATCH
- *   head_dim       64 or 128; q_heads a multiple of kv_heads
+ *   head_dim       64 or 128; q_heads a multiple of kv_heads; scale > 0
  *   h_q_lens       host int32 [B] or NULL
  *   max_kv_len     host bound of d_kv_lens; at most table_stride * page_size
  *   d_page_table   device int32 [B][table_stride]: page k of request b holds its

@@ -2,7 +2,7 @@
 // layout and the choice of passes.
 #include <type_traits>
 
-#include "attend_split.cuh"
+#include "attend_join.cuh"
 
 namespace cpkv {
 namespace {
@@ -34,7 +34,7 @@ int fill_io(AttendIo *io, const HeadArgs &a, const void *q, int64_t q_stride, vo
   const int64_t width = (int64_t)a.q_heads * a.head_dim;
   if (q == nullptr || out == nullptr || !aligned16(q) || !aligned16(out)) return CPKV_ERR_ARG;
   if (q_stride < width || out_stride < width || q_stride % 8 != 0 || out_stride % 8 != 0) return CPKV_ERR_ARG;
-  if (!(scale > -INFINITY && scale < INFINITY)) return CPKV_ERR_ARG;
+  if (!(scale > 0.f && scale < INFINITY)) return CPKV_ERR_ARG;
   io->q = static_cast<const char *>(q);
   io->out = static_cast<char *>(out);
   io->lse = lse;
@@ -85,14 +85,98 @@ struct SplitBounds {
   }
 };
 
-int window_bounds(SplitBounds *b, const HeadArgs &a, int B, const int32_t *h_q_lens, int64_t max_kv, int window,
-                  int sinks) {
+// Bounds and split of a tile pass.
+struct TileBounds {
+  int64_t tokens = 0, tiles = 0, max_rows = 0, max_keys = 0;
+  int splits = 1;
+
+  void add(int64_t nq, int64_t max_kv, int group, int window, int sinks) {
+    int64_t seen = max_kv;
+    if (window > 0) seen = std::min<int64_t>(seen, (int64_t)window + kTileRows / group + sinks);
+    tiles += ceil_div(nq * group, kTileRows);
+    tokens += nq;
+    max_rows = std::max<int64_t>(max_rows, nq * group);
+    max_keys = std::max<int64_t>(max_keys, seen);
+  }
+  // Row tiles that are fewer than the SMs are split along their keys, down to
+  // two key tiles a part, as far as one wave of blocks takes them.
+  int finish(int kv_heads) {
+    const int64_t items = tiles * kv_heads;
+    if (items > INT32_MAX / 2 || tokens > INT32_MAX) return CPKV_ERR_LIMIT;
+    const int64_t parts = std::min<int64_t>(device_sm_count() / std::max<int64_t>(items, 1), ceil_div(max_keys, 2 * kTileKeys));
+    splits = (int)std::max<int64_t>(parts, 1);
+    return CPKV_OK;
+  }
+  int64_t slots(int kv_heads) const { return tiles * kv_heads * splits * kTileRows; }
+  int64_t bytes(int kv_heads, int head_dim, bool direct) const {
+    if (direct && splits == 1) return 0;
+    return round_up(slots(kv_heads) * 8, 256) + round_up(slots(kv_heads) * head_dim * 4, 256);
+  }
+  TileSpace space(char *at, int kv_heads) const {
+    TileSpace s;
+    s.ml = reinterpret_cast<float *>(at);
+    s.o = reinterpret_cast<float *>(at + round_up(slots(kv_heads) * 8, 256));
+    s.splits = splits;
+    return s;
+  }
+};
+
+// Which kernel reads the keys: the split kernel takes 16 packed rows at a time
+// and reads the keys again for each 16, the tile kernel takes 256.
+bool few_rows(int64_t max_rows) { return max_rows <= 2 * kSplitRows; }
+
+// How a call is done, from host lengths alone.
+struct WindowPlan {
+  SplitBounds split;
+  TileBounds tile;
+  bool few = true;
+  int64_t tokens = 0, bytes = 0;
+};
+
+int window_plan(WindowPlan *w, const HeadArgs &a, int B, const int32_t *h_q_lens, int64_t max_kv, int window, int sinks) {
+  const int group = a.q_heads / a.kv_heads;
   for (int s = 0; s < B; ++s) {
     const int64_t nq = h_q_lens == nullptr ? 1 : h_q_lens[s];
     if (nq < 0) return CPKV_ERR_ARG;
-    b->add(nq, max_kv, a.q_heads / a.kv_heads, a.kv_heads, window, sinks);
+    w->split.add(nq, max_kv, group, a.kv_heads, window, sinks);
+    w->tile.add(nq, max_kv, group, window, sinks);
   }
-  return b->finish(B, a.q_heads / a.kv_heads);
+  w->few = few_rows(w->tile.max_rows);
+  w->tokens = w->tile.tokens;
+  const int rc = w->few ? w->split.finish(B, group) : w->tile.finish(a.kv_heads);
+  w->bytes = w->few ? w->split.bytes(B, a.kv_heads, a.head_dim, true) : w->tile.bytes(a.kv_heads, a.head_dim, true);
+  return rc;
+}
+
+struct SharedPlan {
+  SplitBounds split, suffix;  // split: the prefixes, when rows are few
+  TileBounds tile;
+  bool few = true;
+  int64_t prefix_bytes = 0, bytes = 0;
+};
+
+int shared_plan(SharedPlan *w, const HeadArgs &a, int B, int n_groups, const int32_t *h_group_sizes,
+                const int32_t *h_prefix_lens, int page_size, int64_t max_suffix) {
+  const int group = a.q_heads / a.kv_heads;
+  int64_t sum = 0, pages = 0;
+  for (int g = 0; g < n_groups; ++g) {
+    if (h_group_sizes[g] < 0 || h_prefix_lens[g] < 0) return CPKV_ERR_ARG;
+    if (page_size > 0 && h_prefix_lens[g] % page_size != 0) return CPKV_ERR_UNALIGNED_PREFIX;
+    w->split.add(h_group_sizes[g], h_prefix_lens[g], group, a.kv_heads, 0, 0);
+    w->tile.add(h_group_sizes[g], h_prefix_lens[g], group, 0, 0);
+    sum += h_group_sizes[g];
+    if (page_size > 0) pages += h_prefix_lens[g] / page_size;
+  }
+  if (sum != B) return CPKV_ERR_ARG;
+  if (pages > INT32_MAX) return CPKV_ERR_LIMIT;
+  for (int b = 0; b < B; ++b) w->suffix.add(1, max_suffix, group, a.kv_heads, 0, 0);
+  w->few = few_rows(w->tile.max_rows);
+  int rc = w->few ? w->split.finish(n_groups, group) : w->tile.finish(a.kv_heads);
+  if (rc == CPKV_OK) rc = w->suffix.finish(B, group);
+  w->prefix_bytes = w->few ? w->split.bytes(n_groups, a.kv_heads, a.head_dim, false)
+                           : w->tile.bytes(a.kv_heads, a.head_dim, false);
+  w->bytes = w->prefix_bytes + w->suffix.bytes(B, a.kv_heads, a.head_dim, false);
+  return rc;
 }
 
 template <typename F>
@@ -125,86 +209,116 @@ SplitSource<N> source_of(const SplitParams<N> &p) {
   return s;
 }
 
-template <typename T, int D, int N, int M>
-int join_pass(const JoinParams<N, M> &p, cudaStream_t stream) {
-  const int64_t blocks = ceil_div(p.rows, 4);
+template <int N>
+void fill_tiles(TileParams<N> *p, const Seqs<N> &seqs, const PagedPools &pools, const AttendIo &io, const TileBounds &b,
+                char *workspace, bool direct) {
+  p->seqs = seqs;
+  p->pools = pools;
+  p->io = io;
+  p->space = b.space(workspace, io.kv_heads);
+  p->direct = direct && b.splits == 1;
+  const int group = io.group.d;
+  for (int s = 0; s < seqs.count; ++s) {
+    if (seqs.uniform_q == 0) {
+      p->cu_tiles[s + 1] = p->cu_tiles[s] + (int)ceil_div((int64_t)(seqs.cu_q[s + 1] - seqs.cu_q[s]) * group, kTileRows);
+    }
+  }
+}
+
+template <typename T, int D, int N>
+int tile_pass(const TileParams<N> &p, const TileBounds &b, cudaStream_t stream) {
+  auto kernel = attend_tile_kernel<T, D, N>;
+  const int rc = ensure_dynamic_smem((const void *)kernel, TileShape<D>::kSmem);
+  if (rc != CPKV_OK) return rc;
+  const int64_t grid = b.tiles * p.io.kv_heads * b.splits;
+  if (grid == 0) return CPKV_OK;
+  return launch_kernel(kernel, dim3((unsigned)grid), dim3(kTileThreads), TileShape<D>::kSmem, false, stream, p);
+}
+
+template <int N>
+TileSource<N> source_of(const TileParams<N> &p) {
+  TileSource<N> s;
+  s.seqs = p.seqs;
+  s.space = p.space;
+  std::copy(p.cu_tiles, p.cu_tiles + N + 1, s.cu_tiles);
+  return s;
+}
+
+template <typename T, int D, typename A, typename B>
+int join_pass(const A &a, const B &b, const AttendIo &io, int64_t rows, cudaStream_t stream) {
+  const int64_t blocks = ceil_div(rows, 4);
   if (blocks > INT32_MAX) return CPKV_ERR_LIMIT;
-  return launch_kernel(attend_join_kernel<T, D, N, M>, dim3((unsigned)blocks), dim3(128), 0, false, stream, p);
+  JoinParams<A, B> p = {};
+  p.a = a;
+  p.b = b;
+  p.io = io;
+  p.rows = rows;
+  return launch_kernel(attend_join_kernel<T, D, A, B>, dim3((unsigned)blocks), dim3(128), 0, false, stream, p);
 }
 
 template <int N>
 int attend_window(const HeadArgs &heads, const Seqs<N> &seqs, const PagedPools &pools, const AttendIo &io,
-                  const SplitBounds &bounds, char *workspace, cudaStream_t stream) {
-  SplitParams<N> p = {};
-  p.seqs = seqs;
-  p.pools = pools;
-  p.io = io;
-  p.space = bounds.space(workspace, seqs.count, heads.kv_heads, true);
-  p.tiles_cap = bounds.tiles_cap;
-  p.direct = 1;
+                  const WindowPlan &plan, char *workspace, cudaStream_t stream) {
+  const int64_t rows = plan.tokens * heads.q_heads;
+  if (plan.few) {
+    SplitParams<N> p = {};
+    p.seqs = seqs;
+    p.pools = pools;
+    p.io = io;
+    p.space = plan.split.space(workspace, seqs.count, heads.kv_heads, true);
+    p.tiles_cap = plan.split.tiles_cap;
+    p.direct = 1;
+    return for_type_and_dim(heads, [&](auto t, auto d) {
+      using T = decltype(t);
+      constexpr int D = decltype(d)::value;
+      const int rc = split_pass<T, D, N>(&p, plan.split, stream);
+      return rc != CPKV_OK ? rc : join_pass<T, D>(source_of(p), NoSource(), io, rows, stream);
+    });
+  }
+  TileParams<N> p = {};
+  fill_tiles(&p, seqs, pools, io, plan.tile, workspace, true);
   return for_type_and_dim(heads, [&](auto t, auto d) {
     using T = decltype(t);
     constexpr int D = decltype(d)::value;
-    const int rc = split_pass<T, D, N>(&p, bounds, stream);
-    if (rc != CPKV_OK) return rc;
-    JoinParams<N, kFewSeqs> j = {};
-    j.a = source_of(p);
-    j.io = io;
-    j.rows = bounds.tokens * heads.q_heads;
-    return join_pass<T, D, N, kFewSeqs>(j, stream);
+    const int rc = tile_pass<T, D, N>(p, plan.tile, stream);
+    return rc != CPKV_OK || p.direct ? rc : join_pass<T, D>(source_of(p), NoSource(), io, rows, stream);
   });
 }
 
 template <int N>
 int attend_shared(const HeadArgs &heads, const Seqs<N> &prefix, const Seqs<kFewSeqs> &suffix, const PagedPools &pools,
-                  const AttendIo &io, const SplitBounds &pb, const SplitBounds &sb, char *workspace,
-                  cudaStream_t stream) {
-  SplitParams<N> pp = {};
-  pp.seqs = prefix;
-  pp.pools = pools;
-  pp.io = io;
-  pp.space = pb.space(workspace, prefix.count, heads.kv_heads, false);
-  pp.tiles_cap = pb.tiles_cap;
+                  const AttendIo &io, const SharedPlan &plan, char *workspace, cudaStream_t stream) {
+  const int64_t rows = (int64_t)suffix.count * heads.q_heads;
   SplitParams<kFewSeqs> sp = {};
   sp.seqs = suffix;
   sp.pools = pools;
   sp.io = io;
-  sp.space = sb.space(workspace + pb.bytes(prefix.count, heads.kv_heads, heads.head_dim, false), suffix.count,
-                      heads.kv_heads, false);
-  sp.tiles_cap = sb.tiles_cap;
+  sp.space = plan.suffix.space(workspace + plan.prefix_bytes, suffix.count, heads.kv_heads, false);
+  sp.tiles_cap = plan.suffix.tiles_cap;
+  if (plan.few) {
+    SplitParams<N> pp = {};
+    pp.seqs = prefix;
+    pp.pools = pools;
+    pp.io = io;
+    pp.space = plan.split.space(workspace, prefix.count, heads.kv_heads, false);
+    pp.tiles_cap = plan.split.tiles_cap;
+    return for_type_and_dim(heads, [&](auto t, auto d) {
+      using T = decltype(t);
+      constexpr int D = decltype(d)::value;
+      int rc = split_pass<T, D, N>(&pp, plan.split, stream);
+      if (rc == CPKV_OK) rc = split_pass<T, D, kFewSeqs>(&sp, plan.suffix, stream);
+      return rc != CPKV_OK ? rc : join_pass<T, D>(source_of(sp), source_of(pp), io, rows, stream);
+    });
+  }
+  TileParams<N> pp = {};
+  fill_tiles(&pp, prefix, pools, io, plan.tile, workspace, false);
   return for_type_and_dim(heads, [&](auto t, auto d) {
     using T = decltype(t);
     constexpr int D = decltype(d)::value;
-    int rc = split_pass<T, D, N>(&pp, pb, stream);
-    if (rc != CPKV_OK) return rc;
-    rc = split_pass<T, D, kFewSeqs>(&sp, sb, stream);
-    if (rc != CPKV_OK) return rc;
-    JoinParams<kFewSeqs, N> j = {};
-    j.a = source_of(sp);
-    j.b = source_of(pp);
-    j.two_passes = 1;
-    j.io = io;
-    j.rows = sb.tokens * heads.q_heads;
-    return join_pass<T, D, kFewSeqs, N>(j, stream);
+    int rc = tile_pass<T, D, N>(pp, plan.tile, stream);
+    if (rc == CPKV_OK) rc = split_pass<T, D, kFewSeqs>(&sp, plan.suffix, stream);
+    return rc != CPKV_OK ? rc : join_pass<T, D>(source_of(sp), source_of(pp), io, rows, stream);
   });
-}
-
-int shared_bounds(SplitBounds *prefix, SplitBounds *suffix, const HeadArgs &a, int B, int n_groups,
-                  const int32_t *h_group_sizes, const int32_t *h_prefix_lens, int page_size, int64_t max_suffix) {
-  const int group = a.q_heads / a.kv_heads;
-  int64_t sum = 0, pages = 0;
-  for (int g = 0; g < n_groups; ++g) {
-    if (h_group_sizes[g] < 0 || h_prefix_lens[g] < 0) return CPKV_ERR_ARG;
-    if (page_size > 0 && h_prefix_lens[g] % page_size != 0) return CPKV_ERR_UNALIGNED_PREFIX;
-    prefix->add(h_group_sizes[g], h_prefix_lens[g], group, a.kv_heads, 0, 0);
-    sum += h_group_sizes[g];
-    if (page_size > 0) pages += h_prefix_lens[g] / page_size;
-  }
-  if (sum != B) return CPKV_ERR_ARG;
-  if (pages > INT32_MAX) return CPKV_ERR_LIMIT;
-  for (int b = 0; b < B; ++b) suffix->add(1, max_suffix, group, a.kv_heads, 0, 0);
-  const int rc = prefix->finish(n_groups, group);
-  return rc != CPKV_OK ? rc : suffix->finish(B, group);
 }
 
 }  // namespace
@@ -220,10 +334,10 @@ extern "C" int cpkv_attend_window_workspace_bytes(int B, int q_heads, int kv_hea
   int rc = check_heads(heads);
   if (rc != CPKV_OK) return rc;
   if (B > CPKV_MAX_BATCH || max_kv_len > INT32_MAX / 2) return CPKV_ERR_LIMIT;
-  SplitBounds b;
-  rc = window_bounds(&b, heads, B, h_q_lens, max_kv_len, window, sinks);
+  WindowPlan plan;
+  rc = window_plan(&plan, heads, B, h_q_lens, max_kv_len, window, sinks);
   if (rc != CPKV_OK) return rc;
-  *h_bytes = b.bytes(B, kv_heads, head_dim, true);
+  *h_bytes = plan.bytes;
   return CPKV_OK;
 }
 
@@ -245,17 +359,18 @@ extern "C" int cpkv_attend_window(int B, int page_size, int cp_size, int dtype, 
   rc = check_rows(heads, row_bytes, key_offset, value_offset);
   if (rc != CPKV_OK) return rc;
   if (table_stride < 0 || max_kv_len > table_stride * page_size) return CPKV_ERR_CAPACITY;
-  SplitBounds bounds;
-  rc = window_bounds(&bounds, heads, B, h_q_lens, max_kv_len, window, sinks);
+  WindowPlan plan;
+  rc = window_plan(&plan, heads, B, h_q_lens, max_kv_len, window, sinks);
   if (rc != CPKV_OK) return rc;
-  if (bounds.tokens == 0) return CPKV_OK;
+  if (plan.tokens == 0) return CPKV_OK;
   if (d_kv_lens == nullptr || d_status == nullptr || (max_kv_len > 0 && d_page_table == nullptr)) return CPKV_ERR_ARG;
   AttendIo io = {};
   rc = fill_io(&io, heads, d_q, q_stride, d_out, out_stride, d_lse, scale, key_offset, value_offset);
   if (rc != CPKV_OK) return rc;
-  if (d_workspace == nullptr || !aligned16(d_workspace)) return CPKV_ERR_ARG;
-  if (workspace_bytes < bounds.bytes(B, kv_heads, head_dim, true)) return CPKV_ERR_CAPACITY;
-  bool uniform = true;
+  if (plan.bytes > 0 && (d_workspace == nullptr || !aligned16(d_workspace))) return CPKV_ERR_ARG;
+  if (workspace_bytes < plan.bytes) return CPKV_ERR_CAPACITY;
+  // one query length for all needs no lengths in the kernel's block (the tile kernel goes by them)
+  bool uniform = plan.few;
   for (int b = 1; b < B && h_q_lens != nullptr; ++b) uniform &= h_q_lens[b] == h_q_lens[0];
   auto go = [&](auto n) {
     constexpr int N = decltype(n)::value;
@@ -272,9 +387,9 @@ extern "C" int cpkv_attend_window(int B, int page_size, int cp_size, int dtype, 
     if (uniform) {
       s.uniform_q = h_q_lens == nullptr ? 1 : h_q_lens[0];
     } else {
-      for (int b = 0; b < B; ++b) s.cu_q[b + 1] = s.cu_q[b] + h_q_lens[b];
+      for (int b = 0; b < B; ++b) s.cu_q[b + 1] = s.cu_q[b] + (h_q_lens == nullptr ? 1 : h_q_lens[b]);
     }
-    return attend_window<N>(heads, s, pools, io, bounds, static_cast<char *>(d_workspace), (cudaStream_t)stream);
+    return attend_window<N>(heads, s, pools, io, plan, static_cast<char *>(d_workspace), (cudaStream_t)stream);
   };
   if (uniform || B <= kFewSeqs) return go(std::integral_constant<int, kFewSeqs>());
   return go(std::integral_constant<int, CPKV_MAX_BATCH>());
@@ -289,10 +404,10 @@ extern "C" int cpkv_attend_shared_workspace_bytes(int B, int n_groups, int q_hea
   if (rc != CPKV_OK) return rc;
   if (B > CPKV_MAX_BATCH || n_groups > CPKV_MAX_BATCH || max_suffix_len > INT32_MAX / 2) return CPKV_ERR_LIMIT;
   if (n_groups > 0 && (h_group_sizes == nullptr || h_prefix_lens == nullptr)) return CPKV_ERR_ARG;
-  SplitBounds pb, sb;
-  rc = shared_bounds(&pb, &sb, heads, B, n_groups, h_group_sizes, h_prefix_lens, 0, max_suffix_len);
+  SharedPlan plan;
+  rc = shared_plan(&plan, heads, B, n_groups, h_group_sizes, h_prefix_lens, 0, max_suffix_len);
   if (rc != CPKV_OK) return rc;
-  *h_bytes = pb.bytes(n_groups, kv_heads, head_dim, false) + sb.bytes(B, kv_heads, head_dim, false);
+  *h_bytes = plan.bytes;
   return CPKV_OK;
 }
 
@@ -316,19 +431,18 @@ extern "C" int cpkv_attend_shared(int B, int n_groups, int page_size, int cp_siz
   if (rc != CPKV_OK) return rc;
   if (n_groups > 0 && (h_group_sizes == nullptr || h_prefix_lens == nullptr)) return CPKV_ERR_ARG;
   if (table_stride < 0 || max_suffix_len > table_stride * page_size) return CPKV_ERR_CAPACITY;
-  SplitBounds pb, sb;
-  rc = shared_bounds(&pb, &sb, heads, B, n_groups, h_group_sizes, h_prefix_lens, page_size, max_suffix_len);
+  SharedPlan plan;
+  rc = shared_plan(&plan, heads, B, n_groups, h_group_sizes, h_prefix_lens, page_size, max_suffix_len);
   if (rc != CPKV_OK) return rc;
   if (B == 0) return CPKV_OK;
   if (d_suffix_lens == nullptr || d_status == nullptr || (max_suffix_len > 0 && d_page_table == nullptr) ||
-      (pb.units > 0 && d_prefix_pages == nullptr))
+      (plan.split.units > 0 && d_prefix_pages == nullptr))
     return CPKV_ERR_ARG;
   AttendIo io = {};
   rc = fill_io(&io, heads, d_q, q_stride, d_out, out_stride, d_lse, scale, key_offset, value_offset);
   if (rc != CPKV_OK) return rc;
   if (d_workspace == nullptr || !aligned16(d_workspace)) return CPKV_ERR_ARG;
-  if (workspace_bytes < pb.bytes(n_groups, kv_heads, head_dim, false) + sb.bytes(B, kv_heads, head_dim, false))
-    return CPKV_ERR_CAPACITY;
+  if (workspace_bytes < plan.bytes) return CPKV_ERR_CAPACITY;
   Seqs<kFewSeqs> suffix = {};
   suffix.kv_lens = d_suffix_lens;
   suffix.table = d_page_table;
@@ -351,7 +465,7 @@ extern "C" int cpkv_attend_shared(int B, int n_groups, int page_size, int cp_siz
       s.page0[g] = pages;
       pages += h_prefix_lens[g] / page_size;
     }
-    return attend_shared<N>(heads, s, suffix, pools, io, pb, sb, static_cast<char *>(d_workspace), (cudaStream_t)stream);
+    return attend_shared<N>(heads, s, suffix, pools, io, plan, static_cast<char *>(d_workspace), (cudaStream_t)stream);
   };
   if (n_groups <= kFewSeqs) return go(std::integral_constant<int, kFewSeqs>());
   return go(std::integral_constant<int, CPKV_MAX_BATCH>());

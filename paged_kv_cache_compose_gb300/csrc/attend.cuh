@@ -15,6 +15,8 @@
 // A part without keys is m = -inf, l = 0, o = 0.
 #pragma once
 
+#include <type_traits>
+
 #include "paged.cuh"
 
 namespace cpkv {
@@ -108,6 +110,11 @@ CPKV_DEV float log2_approx(float x) {
   asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+
+// A finished row's factor of its output and its log-sum-exp (zeros and -infinity
+// where no key had a weight; a NaN stays one).
+CPKV_DEV float row_scale(float l) { return l == 0.f ? 0.f : 1.f / l; }
+CPKV_DEV float row_lse(float m, float l) { return l == 0.f ? -INFINITY : (m + log2_approx(l)) * kLn2; }
 
 // Where queries come from and results go.
 struct AttendIo {

@@ -1,0 +1,135 @@
+// Joins the parts of each row: m = max m_i, l = sum 2^(m_i - m) l_i,
+// o = sum 2^(m_i - m) o_i, out = o / l.
+#pragma once
+
+#include "attend_split.cuh"
+#include "attend_tile.cuh"
+
+namespace cpkv {
+
+// One row on its way: m, l and this lane's D / 32 elements of o.
+template <int D>
+struct RowSum {
+  static constexpr int kEach = D / 32;
+  float m = -INFINITY, l = 0.f, o[kEach] = {};
+
+  // `count` parts; `at(k)` is part k's row in (m, l) pairs `ml` and values `ov`.
+  template <typename F>
+  CPKV_DEV void add(const float *ml, const float *ov, int count, int lane, F at) {
+    for (int k0 = 0; k0 < count; k0 += 32) {
+      float2 v = make_float2(-INFINITY, 0.f);
+      if (k0 + lane < count) v = *reinterpret_cast<const float2 *>(ml + at(k0 + lane) * 2);
+      float best = v.x;
+#pragma unroll
+      for (int w = 16; w > 0; w >>= 1) best = fmaxf(best, __shfl_xor_sync(0xffffffffu, best, w));
+      const float next = fmaxf(m, best), base = next == -INFINITY ? 0.f : next;
+      const float fall = exp2_approx(m - base), weight = exp2_approx(v.x - base);
+      float sum = weight * v.y;
+#pragma unroll
+      for (int w = 16; w > 0; w >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, w);
+      l = l * fall + sum;
+      m = next;
+#pragma unroll
+      for (int e = 0; e < kEach; ++e) o[e] *= fall;
+      const int n = count - k0 < 32 ? count - k0 : 32;
+#pragma unroll 4
+      for (int i = 0; i < n; ++i) {
+        const float w = __shfl_sync(0xffffffffu, weight, i);
+        if (w == 0.f) continue;  // a part without keys has no values written
+        const float *src = ov + at(k0 + i) * D + lane * kEach;
+        if constexpr (kEach == 4) {
+          const float4 x = *reinterpret_cast<const float4 *>(src);
+          o[0] += w * x.x, o[1] += w * x.y, o[2] += w * x.z, o[3] += w * x.w;
+        } else {
+          const float2 x = *reinterpret_cast<const float2 *>(src);
+          o[0] += w * x.x, o[1] += w * x.y;
+        }
+      }
+    }
+  }
+};
+
+// Adds the parts of query head `head` of token i of sequence s; false when the
+// pass has written that row's output itself.
+template <int D, int N>
+CPKV_DEV bool add_parts(RowSum<D> *sum, const SplitSource<N> &src, const AttendIo &io, int s, int i, int head, int lane) {
+  const int group = io.group.d, h = div_by(head, io.group), g = head - h * group;
+  const int nq = src.seqs.q_count(s), kv = src.seqs.kv_len(s);
+  const KeyRange keys = key_range<kSplitTile>(kv, nq, 0, nq, src.seqs.causal, src.seqs.window, src.seqs.sinks);
+  if (keys.n_tiles == 0) return true;
+  const int row = i * group + g, rt = row / kSplitRows, row_tiles = (nq * group + kSplitRows - 1) / kSplitRows;
+  const int in_tile = row - rt * kSplitRows;
+  const int chunk = split_chunk(src.space.cum[src.seqs.count], src.space.grid);
+  const int begin = src.space.cum[s] + (h * row_tiles + rt) * keys.n_tiles, end = begin + keys.n_tiles;
+  const int c0 = begin / chunk, c1 = (end - 1) / chunk;
+  if (c0 == c1) {
+    if (src.direct) return false;
+    const int64_t slot = 2 * (int64_t)src.space.grid + whole_tile(src.seqs, s, rt, h, group, src.tiles_cap);
+    sum->add(src.space.ml, src.space.o, 1, lane, [&](int) { return slot * kSplitRows + in_tile; });
+    return true;
+  }
+  // the tile's stretch is the last of block c0 unless it begins there, and the first of the others
+  const int64_t first = 2 * (int64_t)c0 + (begin == c0 * chunk ? 0 : 1);
+  sum->add(src.space.ml, src.space.o, c1 - c0 + 1, lane,
+           [&](int k) { return (k == 0 ? first : 2 * (int64_t)(c0 + k)) * kSplitRows + in_tile; });
+  return true;
+}
+
+template <int D, int N>
+CPKV_DEV bool add_parts(RowSum<D> *sum, const TileSource<N> &src, const AttendIo &io, int s, int i, int head, int lane) {
+  const int group = io.group.d, h = div_by(head, io.group), row = i * group + head - h * group, rt = row / kTileRows;
+  const int64_t item = (int64_t)(src.cu_tiles[s] + rt) * io.kv_heads + h;
+  const int64_t at = item * src.space.splits * kTileRows + row - rt * kTileRows;
+  sum->add(src.space.ml, src.space.o, src.space.splits, lane, [&](int k) { return at + (int64_t)k * kTileRows; });
+  return true;
+}
+
+struct NoSource {};
+template <int D>
+CPKV_DEV bool add_parts(RowSum<D> *, const NoSource &, const AttendIo &, int, int, int, int) {
+  return true;
+}
+
+template <int N>
+CPKV_DEV int seq_of(const Seqs<N> &q, int token) {
+  return q.uniform_q ? token / q.uniform_q : upper_index(q.cu_q, q.count, token);
+}
+
+// `a`: the pass whose sequences own the query tokens; `b`: a second pass over
+// the same tokens, or none.
+template <typename A, typename B>
+struct JoinParams {
+  A a;
+  B b;
+  AttendIo io;
+  int64_t rows;  // tokens * q_heads
+};
+
+// A warp per row (token, query head).
+template <typename T, int D, typename A, typename B>
+__global__ void __launch_bounds__(128) attend_join_kernel(const __grid_constant__ JoinParams<A, B> p) {
+  const int lane = threadIdx.x & 31;
+  const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
+  if (row >= p.rows) return;
+  const int token = (int)(row / p.io.q_heads), head = (int)(row - (int64_t)token * p.io.q_heads);
+  RowSum<D> sum;
+  {
+    const int s = seq_of(p.a.seqs, token);
+    if (!add_parts(&sum, p.a, p.io, s, token - p.a.seqs.q_begin(s), head, lane)) return;
+  }
+  if constexpr (!std::is_same<B, NoSource>::value) {
+    const int s = seq_of(p.b.seqs, token);
+    add_parts(&sum, p.b, p.io, s, token - p.b.seqs.q_begin(s), head, lane);
+  }
+  const float inv = row_scale(sum.l);
+  char *dst = p.io.out + token * p.io.out_stride + (int64_t)head * D * 2 + lane * (D / 16);
+  if constexpr (D == 128) {
+    *reinterpret_cast<uint2 *>(dst) =
+        make_uint2(pack2<T>(sum.o[0] * inv, sum.o[1] * inv), pack2<T>(sum.o[2] * inv, sum.o[3] * inv));
+  } else {
+    *reinterpret_cast<uint32_t *>(dst) = pack2<T>(sum.o[0] * inv, sum.o[1] * inv);
+  }
+  if (p.io.lse != nullptr && lane == 0) p.io.lse[row] = row_lse(sum.m, sum.l);
+}
+
+}  // namespace cpkv

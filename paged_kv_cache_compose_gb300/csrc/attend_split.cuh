@@ -333,13 +333,13 @@ __global__ void __launch_bounds__(kSplitWarps * 32) attend_split_kernel(const __
           const int i = div_by(row, p.io.group), g = row - i * group;
           const int64_t token = p.seqs.q_begin(at.s) + i;
           const int head = at.h * group + g;
-          const float inv = sum[r] > 0.f ? 1.f / sum[r] : 0.f;
+          const float inv = row_scale(sum[r]);
           char *dst = p.io.out + token * p.io.out_stride + (int64_t)head * Shape::kRow + (lane & 3) * 4;
 #pragma unroll
           for (int n = 0; n < D / 8; ++n)
             *reinterpret_cast<uint32_t *>(dst + n * 16) = pack2<T>(o[n][2 * r] * inv, o[n][2 * r + 1] * inv);
           if (p.io.lse != nullptr && (lane & 3) == 0)
-            p.io.lse[token * p.io.q_heads + head] = sum[r] > 0.f ? (big[r] + log2_approx(sum[r])) * kLn2 : -INFINITY;
+            p.io.lse[token * p.io.q_heads + head] = row_lse(big[r], sum[r]);
         } else {
           float *dst = p.space.o + (slot * kSplitRows + in_tile) * D + (lane & 3) * 2;
 #pragma unroll
@@ -355,121 +355,6 @@ __global__ void __launch_bounds__(kSplitWarps * 32) attend_split_kernel(const __
     if (u + 1 < u1) at.advance(p);
   }
   cp_async_wait<0>();
-}
-
-// ---------------------------------------------------------------------------
-// joining
-// ---------------------------------------------------------------------------
-
-// The parts of one row: `count` of them at slots first_slot, then next_slot, next_slot + 2, ...
-struct RowParts {
-  int64_t first_slot, next_slot;
-  int count, in_tile;
-  bool done;  // the split pass wrote the output itself
-  CPKV_DEV int64_t slot(int k) const { return k == 0 ? first_slot : next_slot + 2 * (int64_t)(k - 1); }
-};
-
-template <int N>
-CPKV_DEV RowParts row_parts(const SplitSource<N> &src, const AttendIo &io, int s, int i, int head) {
-  const int group = io.group.d, h = div_by(head, io.group), g = head - h * group;
-  const int nq = src.seqs.q_count(s), kv = src.seqs.kv_len(s);
-  const KeyRange keys = key_range<kSplitTile>(kv, nq, 0, nq, src.seqs.causal, src.seqs.window, src.seqs.sinks);
-  RowParts r;
-  r.done = false;
-  const int row = i * group + g, rt = row / kSplitRows, row_tiles = (nq * group + kSplitRows - 1) / kSplitRows;
-  r.in_tile = row - rt * kSplitRows;
-  r.count = 0;
-  r.first_slot = r.next_slot = 0;
-  if (keys.n_tiles == 0) return r;
-  const int chunk = split_chunk(src.space.cum[src.seqs.count], src.space.grid);
-  const int begin = src.space.cum[s] + (h * row_tiles + rt) * keys.n_tiles, end = begin + keys.n_tiles;
-  const int c0 = begin / chunk, c1 = (end - 1) / chunk;
-  r.count = c1 - c0 + 1;
-  if (c0 == c1) {
-    r.done = src.direct;
-    r.first_slot = 2 * (int64_t)src.space.grid + whole_tile(src.seqs, s, rt, h, group, src.tiles_cap);
-  } else {
-    r.first_slot = 2 * (int64_t)c0 + (begin == c0 * chunk ? 0 : 1);
-    r.next_slot = 2 * (int64_t)(c0 + 1);
-  }
-  return r;
-}
-
-template <int D>
-struct RowSum {
-  static constexpr int kEach = D / 32;
-  float m = -INFINITY, l = 0.f, o[kEach] = {};
-
-  CPKV_DEV void add(const SplitSpace &space, const RowParts &parts, int lane) {
-    for (int k0 = 0; k0 < parts.count; k0 += 32) {
-      const int k = k0 + lane;
-      float2 v = make_float2(-INFINITY, 0.f);
-      if (k < parts.count)
-        v = *reinterpret_cast<const float2 *>(space.ml + (parts.slot(k) * kSplitRows + parts.in_tile) * 2);
-      float best = v.x;
-#pragma unroll
-      for (int w = 16; w > 0; w >>= 1) best = fmaxf(best, __shfl_xor_sync(0xffffffffu, best, w));
-      const float next = fmaxf(m, best), base = next == -INFINITY ? 0.f : next;
-      const float fall = exp2_approx(m - base), weight = exp2_approx(v.x - base);
-      float sum = weight * v.y;
-#pragma unroll
-      for (int w = 16; w > 0; w >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, w);
-      l = l * fall + sum;
-      m = next;
-#pragma unroll
-      for (int e = 0; e < kEach; ++e) o[e] *= fall;
-      const int n = parts.count - k0 < 32 ? parts.count - k0 : 32;
-      for (int i = 0; i < n; ++i) {
-        const float w = __shfl_sync(0xffffffffu, weight, i);
-        const float *src = space.o + (parts.slot(k0 + i) * kSplitRows + parts.in_tile) * D + lane * kEach;
-        if constexpr (kEach == 4) {
-          const float4 x = *reinterpret_cast<const float4 *>(src);
-          o[0] += w * x.x, o[1] += w * x.y, o[2] += w * x.z, o[3] += w * x.w;
-        } else {
-          const float2 x = *reinterpret_cast<const float2 *>(src);
-          o[0] += w * x.x, o[1] += w * x.y;
-        }
-      }
-    }
-  }
-};
-
-template <int N, int M>
-struct JoinParams {
-  SplitSource<N> a;  // the sequences that own the query tokens
-  SplitSource<M> b;  // a second pass over the same tokens (two_passes), else unused
-  AttendIo io;
-  int two_passes;
-  int64_t rows;  // tokens * q_heads
-};
-
-// A warp per row (token, query head).
-template <typename T, int D, int N, int M>
-__global__ void __launch_bounds__(128) attend_join_kernel(const __grid_constant__ JoinParams<N, M> p) {
-  const int lane = threadIdx.x & 31;
-  const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
-  if (row >= p.rows) return;
-  const int token = (int)(row / p.io.q_heads), head = (int)(row - (int64_t)token * p.io.q_heads);
-  RowSum<D> sum;
-  {
-    const int s = p.a.seqs.uniform_q ? token / p.a.seqs.uniform_q : upper_index(p.a.seqs.cu_q, p.a.seqs.count, token);
-    const RowParts parts = row_parts(p.a, p.io, s, token - p.a.seqs.q_begin(s), head);
-    if (parts.done) return;
-    sum.add(p.a.space, parts, lane);
-  }
-  if (p.two_passes) {
-    const int s = p.b.seqs.uniform_q ? token / p.b.seqs.uniform_q : upper_index(p.b.seqs.cu_q, p.b.seqs.count, token);
-    sum.add(p.b.space, row_parts(p.b, p.io, s, token - p.b.seqs.q_begin(s), head), lane);
-  }
-  const float inv = sum.l > 0.f ? 1.f / sum.l : 0.f;
-  char *dst = p.io.out + token * p.io.out_stride + (int64_t)head * D * 2 + lane * (D / 16);
-  if constexpr (D == 128) {
-    *reinterpret_cast<uint2 *>(dst) =
-        make_uint2(pack2<T>(sum.o[0] * inv, sum.o[1] * inv), pack2<T>(sum.o[2] * inv, sum.o[3] * inv));
-  } else {
-    *reinterpret_cast<uint32_t *>(dst) = pack2<T>(sum.o[0] * inv, sum.o[1] * inv);
-  }
-  if (p.io.lse != nullptr && lane == 0) p.io.lse[row] = sum.l > 0.f ? (sum.m + log2_approx(sum.l)) * kLn2 : -INFINITY;
 }
 
 }  // namespace cpkv
