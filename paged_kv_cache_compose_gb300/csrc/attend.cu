@@ -209,6 +209,47 @@ SplitSource<N> source_of(const SplitParams<N> &p) {
   return s;
 }
 
+// cuTensorMapEncodeTiled, looked up once; null where the driver has none.
+using EncodeTiled = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
+                                 const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
+                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeTiled encode_tiled() {
+  static const EncodeTiled found = [] {
+    void *f = nullptr;
+    cudaDriverEntryPointQueryResult how;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &how) != cudaSuccess) {
+      (void)cudaGetLastError();
+      return (EncodeTiled) nullptr;
+    }
+    return how == cudaDriverEntryPointSuccess ? (EncodeTiled)f : (EncodeTiled) nullptr;
+  }();
+  return found;
+}
+
+// TMA maps of the pools: [rows][elements], boxes of `box` rows by 64 elements in
+// the 128-byte swizzle of the kernel's shared memory.  Pages of 16 rows or a
+// multiple have them; others (and more than kTileMaps pools) leave box_rows 0,
+// and the kernel copies key by key.
+template <int N>
+void fill_maps(TileParams<N> *p) {
+  const uint32_t ps = p->pools.page_size.d;
+  p->box_rows = 0;
+  if (ps % 16 != 0 || p->pools.cp.d > kTileMaps || encode_tiled() == nullptr) return;
+  const cuuint32_t box[2] = {64, ps % 32 == 0 ? 32u : 16u}, steps[2] = {1, 1};
+  for (uint32_t r = 0; r < p->pools.cp.d; ++r) {
+    const int64_t rows = (int64_t)p->pools.cap[r] * ps;
+    if (rows == 0) continue;  // no page of it is valid
+    if (rows > INT32_MAX) return;
+    const cuuint64_t dims[2] = {(cuuint64_t)p->pools.row_bytes / 2, (cuuint64_t)rows};
+    const cuuint64_t strides[1] = {(cuuint64_t)p->pools.row_bytes};
+    if (encode_tiled()(&p->maps[r], CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, p->pools.pool[r], dims, strides, box, steps,
+                       CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                       CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+      return;
+  }
+  p->box_rows = (int)box[1];
+}
+
 template <int N>
 void fill_tiles(TileParams<N> *p, const Seqs<N> &seqs, const PagedPools &pools, const AttendIo &io, const TileBounds &b,
                 char *workspace, bool direct) {
@@ -217,6 +258,7 @@ void fill_tiles(TileParams<N> *p, const Seqs<N> &seqs, const PagedPools &pools, 
   p->io = io;
   p->space = b.space(workspace, io.kv_heads);
   p->direct = direct && b.splits == 1;
+  fill_maps(p);
   const int group = io.group.d;
   for (int s = 0; s < seqs.count; ++s) {
     if (seqs.uniform_q == 0) {

@@ -164,7 +164,11 @@ CPKV_DEV void ldmatrix_x4_trans(uint32_t r[4], uint32_t addr) {
 CPKV_DEV void cp_async16(uint32_t smem, const void *src, int bytes) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem), "l"(src), "r"(bytes) : "memory");
 }
+CPKV_DEV void cp_async16(uint32_t smem, const void *src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem), "l"(src) : "memory");
+}
 CPKV_DEV void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+CPKV_DEV void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 template <int N>
 CPKV_DEV void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");

@@ -21,16 +21,28 @@ CPKV_DEV void tmem_free(uint32_t addr, uint32_t columns) {
 
 CPKV_DEV void tmem_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 CPKV_DEV void tmem_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-CPKV_DEV void tmem_wait_loads() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 CPKV_DEV void tmem_wait_stores() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // Shared-memory operand with 128-byte swizzle: rows of 128 bytes whose 16-byte
 // chunk c of row r stands at chunk c ^ (r & 7); 8 rows are 1024 bytes.  Along
 // the contiguous axis the next 128 bytes' block is `block_bytes` on (used by
-// operands whose rows run along the sum).
-CPKV_DEV uint64_t operand_desc(uint32_t smem, uint32_t block_bytes) {
-  return (uint64_t)((smem & 0x3ffff) >> 4) | ((uint64_t)(block_bytes >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) |
-         (1ull << 46) | (2ull << 61);
+// operands whose rows run along the sum).  The low word holds the address, in
+// units of 16 bytes: a step along the operand is an addition to it.
+constexpr uint32_t kOperandHigh = (1024 >> 4) | (1u << 14) | (2u << 29);
+CPKV_DEV uint32_t operand_low(uint32_t smem, uint32_t block_bytes) {
+  return ((smem & 0x3ffff) >> 4) | ((block_bytes >> 4) << 16);
+}
+
+// One lane of a converged warp.  The operands of the products are uniform values:
+// they have to be worked out by the whole warp, or each product waits for its
+// operands to move to uniform registers (70 cycles each, measured, against 32 to 64
+// for the product itself).
+CPKV_DEV bool elect_one() {
+  uint32_t chosen;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(chosen));
+  return chosen != 0;
 }
 
 // Shape and types of a product of M x N: both operands bf16 or both fp16.
@@ -39,21 +51,23 @@ constexpr uint32_t product_desc(bool bf16, int m, int n, bool b_rows_along_sum) 
          ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
 }
 
-// d (+)= a b over 16 of the sum, a and b in shared memory; one thread calls.
-CPKV_DEV void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t desc, bool add) {
+// d (+)= a b over 16 of the sum, a and b in shared memory (low words); one thread calls.
+CPKV_DEV void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t desc, uint32_t add) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(desc), "r"((uint32_t)add)
+      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "mov.b64 a, {%1, %5};\n\tmov.b64 b, {%2, %5};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b), "r"(desc), "r"(add), "r"(kOperandHigh)
       : "memory");
 }
 
 // The same with a in tensor memory, two 16-bit values to a column.
-CPKV_DEV void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t desc, bool add) {
+CPKV_DEV void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t desc, uint32_t add) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "l"(b), "r"(desc), "r"((uint32_t)add)
+      "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "mov.b64 b, {%2, %5};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b), "r"(desc), "r"(add), "r"(kOperandHigh)
       : "memory");
 }
 
@@ -75,6 +89,18 @@ CPKV_DEV void tmem_load32(uint32_t (&r)[32], uint32_t addr) {
       : "r"(addr));
 }
 
+// Until this thread's loads have arrived; `r` is named so that its uses stay behind.
+CPKV_DEV void tmem_wait_loads(uint32_t (&r)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]),
+                 "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]),
+                 "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]),
+                 "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
+               :
+               : "memory");
+}
+
 CPKV_DEV void tmem_store32(uint32_t addr, const uint32_t (&r)[32]) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
@@ -94,6 +120,71 @@ CPKV_DEV void tmem_store16(uint32_t addr, const uint32_t (&r)[16]) {
       "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
       "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
+}
+
+// Box of a two-dimensional tensor map to shared memory; its bytes arrive on `bar`.
+CPKV_DEV void box_load(void *smem, const void *map, int x, int y, uint64_t *bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
+          smem_addr(smem)),
+      "l"(map), "r"(x), "r"(y), "r"(smem_addr(bar))
+      : "memory");
+}
+
+// Two 32-bit sums or products at once.
+CPKV_DEV uint64_t pair(uint32_t lo, uint32_t hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(lo), "r"(hi));
+  return r;
+}
+CPKV_DEV float2 unpair(uint64_t v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+CPKV_DEV uint64_t fma_pair(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+CPKV_DEV uint64_t add_pair(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+CPKV_DEV float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
+// Register share of a warpgroup (all four warps call).
+template <int N>
+CPKV_DEV void grow_registers() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+CPKV_DEV void shrink_registers() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+// Arrives on `bar` (one of its counted arrivals) once this thread's earlier
+// asynchronous copies have landed.
+CPKV_DEV void mbar_arrive_after_copies(uint64_t *bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(bar)) : "memory");
+}
+
+// mbar_try_wait that may suspend the thread for about `ns` nanoseconds.
+CPKV_DEV bool mbar_try_wait_for(uint64_t *bar, uint32_t parity, uint32_t ns) {
+  uint32_t done;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(done)
+      : "r"(smem_addr(bar)), "r"(parity), "r"(ns)
+      : "memory");
+  return done != 0;
 }
 
 CPKV_DEV void mbar_arrive(uint64_t *bar) {
