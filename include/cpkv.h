@@ -632,7 +632,8 @@ int cpkv_append_rotary(int64_t n_tokens, int page_size, int cp_size, int dtype, 
  *   d_kv_lens      device int32 [B], read by the kernels: a captured graph can
  *                  be replayed as the requests grow.  A length outside
  *                  [0, max_kv_len] is clamped and raises OUT_CAPACITY.
- *   d_q            [sum q_lens][q_heads][head_dim], requests one after the other
+ *   num_tokens     rows of d_q and d_out: the sum of the query lengths (ARG otherwise)
+ *   d_q            [num_tokens][q_heads][head_dim], requests one after the other
  *   d_out          like d_q; d_lse: float [sum q_lens][q_heads], or NULL
  *   d_workspace    device, 16-byte aligned, at least
  *                  cpkv_attend_window_workspace_bytes; contents between calls are
@@ -645,10 +646,10 @@ int cpkv_append_rotary(int64_t n_tokens, int page_size, int cp_size, int dtype, 
 int cpkv_attend_window(int B, int page_size, int cp_size, int dtype, int q_heads, int kv_heads, int head_dim,
                        int64_t row_bytes, int64_t key_offset, int64_t value_offset, const int32_t *h_q_lens,
                        int64_t max_kv_len, const void *const *h_pools, const int64_t *h_pool_cap_pages,
-                       const int32_t *d_page_table, int64_t table_stride, const int32_t *d_kv_lens, const void *d_q,
-                       int64_t q_stride, float scale, int window, int sinks, void *d_out, int64_t out_stride,
-                       float *d_lse, void *d_workspace, int64_t workspace_bytes, int flags, int32_t *d_status,
-                       cpkv_stream_t stream);
+                       const int32_t *d_page_table, int64_t table_stride, const int32_t *d_kv_lens,
+                       int64_t num_tokens, const void *d_q, int64_t q_stride, float scale, int window, int sinks,
+                       void *d_out, int64_t out_stride, float *d_lse, void *d_workspace, int64_t workspace_bytes,
+                       int flags, int32_t *d_status, cpkv_stream_t stream);
 
 /* Device workspace of cpkv_attend_window (host only); lengths as passed to it. */
 int cpkv_attend_window_workspace_bytes(int B, int q_heads, int kv_heads, int head_dim, const int32_t *h_q_lens,
@@ -664,7 +665,8 @@ int cpkv_attend_window_workspace_bytes(int B, int q_heads, int kv_heads, int hea
  *   h_group_sizes  host int32 [n_groups], adding up to B
  *   h_prefix_lens  host int32 [n_groups], multiples of page_size
  *                  (UNALIGNED_PREFIX otherwise), 0 allowed
- *   d_prefix_pages device int32, CSR by group: h_prefix_lens[g] / page_size ids each
+ *   d_prefix_pages device int32 [num_prefix_pages], CSR by group: h_prefix_lens[g] / page_size
+ *                  ids each (CAPACITY when it holds fewer)
  *   d_page_table   device int32 [B][table_stride]: pages of the suffixes, whose
  *                  first token stands at the first row of its first page
  *   d_suffix_lens  device int32 [B], clamped to [0, max_suffix_len] (OUT_CAPACITY)
@@ -675,8 +677,8 @@ int cpkv_attend_shared(int B, int n_groups, int page_size, int cp_size, int dtyp
                        int head_dim, int64_t row_bytes, int64_t key_offset, int64_t value_offset,
                        const int32_t *h_group_sizes, const int32_t *h_prefix_lens, int64_t max_suffix_len,
                        const void *const *h_pools, const int64_t *h_pool_cap_pages, const int32_t *d_prefix_pages,
-                       const int32_t *d_page_table, int64_t table_stride, const int32_t *d_suffix_lens,
-                       const void *d_q, int64_t q_stride, float scale, void *d_out, int64_t out_stride, float *d_lse,
+                       int64_t num_prefix_pages, const int32_t *d_page_table, int64_t table_stride,
+                       const int32_t *d_suffix_lens, const void *d_q, int64_t q_stride, float scale, void *d_out, int64_t out_stride, float *d_lse,
                        void *d_workspace, int64_t workspace_bytes, int flags, int32_t *d_status,
                        cpkv_stream_t stream);
 

@@ -108,11 +108,11 @@ def _declare(lib):
     lib.cpkv_ragged_plan_build.argtypes = [_I, _I, _I, _I, _P, _P, _P, _L, _P, _L] + [_P] * 7 + [_L, _P, _P, _P]
     lib.cpkv_append_rotary.argtypes = [_L] + [_I] * 7 + [_L] * 3 + [_P] * 2 + [_P, _L] * 4 + [
         _P, _P, _L, _I, _P, _P, _L, _I, _I, _P, _P]
-    lib.cpkv_attend_window.argtypes = [_I] * 7 + [_L] * 3 + [_P, _L, _P, _P, _P, _L, _P, _P, _L, _F, _I, _I, _P, _L, _P,
-                                                             _P, _L, _I, _P, _P]
+    lib.cpkv_attend_window.argtypes = [_I] * 7 + [_L] * 3 + [_P, _L, _P, _P, _P, _L, _P, _L, _P, _L, _F, _I, _I, _P, _L,
+                                                             _P, _P, _L, _I, _P, _P]
     lib.cpkv_attend_window_workspace_bytes.argtypes = [_I] * 4 + [_P, _L, _I, _I, _P]
-    lib.cpkv_attend_shared.argtypes = [_I] * 8 + [_L] * 3 + [_P, _P, _L, _P, _P, _P, _P, _L, _P, _P, _L, _F, _P, _L, _P,
-                                                             _P, _L, _I, _P, _P]
+    lib.cpkv_attend_shared.argtypes = [_I] * 8 + [_L] * 3 + [_P, _P, _L, _P, _P, _P, _L, _P, _L, _P, _P, _L, _F, _P, _L,
+                                                             _P, _P, _L, _I, _P, _P]
     lib.cpkv_attend_shared_workspace_bytes.argtypes = [_I] * 5 + [_P, _P, _L, _P]
     for name in EXPORTED:
         getattr(lib, name).restype = _I
@@ -451,6 +451,9 @@ def ragged_buffers(seg_cap: int, topk_cap: int, device="cuda") -> dict:
 # ---------------------------------------------------------------------------
 # serving on the paged rows
 # ---------------------------------------------------------------------------
+# These calls come once per layer and decode step, whose kernels take a few
+# microseconds: the marshalling below looks at each tensor once and makes no
+# objects that it can do without.
 
 class PoolTable:
     """The owner pools of a paged cache as the serving calls take them: the
@@ -474,61 +477,81 @@ class PoolTable:
                 raise CpkvError("PoolTable", CPKV_ERR_ARG, "a pool is [pages, page_size, width], widths alike")
             if t.dtype != self.dtype or t.device != self.device:
                 raise CpkvError("PoolTable", CPKV_ERR_ARG, "pools of one type on one device are wanted")
-        addresses = np.array([(_dp(t) or _P(0)).value or 0 for t in self.pools], np.uint64)
+        self._addresses = np.array([(_dp(t) or _P(0)).value or 0 for t in self.pools], np.uint64)
+        self._caps = _host_i64([t.shape[0] for t in self.pools])
+        self.addresses, self.caps = self._addresses.ctypes.data, self._caps.ctypes.data
         self.page_size, self.cp_size = int(page_size), len(self.pools)
         self.row_bytes = self.pools[0].shape[2] * 2
         self.key_offset, self.value_offset = int(key_offset), int(value_offset)
         self.flags = DENSE_PAGES if dense else 0
-        self._addresses, self._caps = addresses, _host_i64([t.shape[0] for t in self.pools])
-        self.addresses, self.caps = self._addresses.ctypes.data, self._caps.ctypes.data
+        self.int32, self.int64, self.float32 = torch.int32, torch.int64, torch.float32
 
 
-def _rows(t, name: str, table: PoolTable, heads: int | None, dim: int):
-    """(address, elements between tokens) of a [tokens, heads, dim] tensor
-    whose heads are contiguous within a token."""
-    shape, stride = t.shape, t.stride()
+def _wrong(name: str, what: str):
+    return CpkvError("marshal", CPKV_ERR_ARG, f"{name}: {what} is wanted")
+
+
+def _rows(t, name: str, table: PoolTable):
+    """(address, elements between tokens, shape) of a [tokens, heads, dim]
+    tensor whose heads are contiguous within a token."""
     if t.dtype != table.dtype or t.device != table.device:
-        raise CpkvError("marshal", CPKV_ERR_ARG, f"{name}: {table.dtype} on {table.device} is wanted")
-    if len(shape) != 3 or shape[2] != dim or (heads is not None and shape[1] != heads):
-        raise CpkvError("marshal", CPKV_ERR_ARG, f"{name}: [tokens, {heads or 'heads'}, {dim}] is wanted")
-    if stride[2] != 1 or (shape[1] > 1 and stride[1] != dim):
-        raise CpkvError("marshal", CPKV_ERR_ARG, f"{name}: a token's heads have to be contiguous")
-    return t.data_ptr(), (stride[0] if shape[0] > 1 else max(stride[0], shape[1] * dim))
+        raise _wrong(name, f"{table.dtype} on {table.device}")
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 3:
+        raise _wrong(name, "[tokens, heads, dim]")
+    n, heads, dim = shape
+    between, of_heads, of_dim = stride
+    if of_dim != 1 or (of_heads != dim and heads > 1):
+        raise _wrong(name, "a token's heads side by side")
+    return t.data_ptr(), (between if n > 1 else max(between, heads * dim)), shape
 
 
-def _ints(t, name: str, table: PoolTable, bits: int, dims: int):
-    """Address of a device tensor of whole numbers with a contiguous last axis."""
-    if t.device != table.device or t.element_size() * 8 != bits or t.is_floating_point() or t.dim() != dims:
-        raise CpkvError("marshal", CPKV_ERR_ARG, f"{name}: int{bits} of {dims} axes on {table.device} is wanted")
-    if t.shape[-1] > 1 and t.stride(-1) != 1:
-        raise CpkvError("marshal", CPKV_ERR_ARG, f"{name}: contiguous entries are wanted")
-    return t.data_ptr()
+def _list_i32(t, name: str, table: PoolTable):
+    """(address, length) of a device list of int32."""
+    if t.dtype != table.int32 or t.device != table.device or t.dim() != 1 or not t.is_contiguous():
+        raise _wrong(name, f"a contiguous int32 list on {table.device}")
+    return t.data_ptr(), t.shape[0]
 
 
-def _out(out, lse, q, table: PoolTable):
-    """Addresses of an attention's results."""
-    o, stride = _rows(out, "out", table, q.shape[1], q.shape[2])
-    if out.shape[0] != q.shape[0]:
-        raise CpkvError("marshal", CPKV_ERR_ARG, "out: as many tokens as q are wanted")
-    if lse is None:
-        return o, stride, None
-    import torch
-
-    if lse.dtype != torch.float32 or lse.device != table.device or lse.shape != q.shape[:2] or not lse.is_contiguous():
-        raise CpkvError("marshal", CPKV_ERR_ARG, "lse: contiguous float32 [tokens, heads] is wanted")
-    return o, stride, lse.data_ptr()
-
-
-def _table(t, name: str, table: PoolTable, rows: int):
-    """(address, ids between requests) of a [requests, pages] table."""
-    at = _ints(t, name, table, 32, 2)
-    if t.shape[0] != rows:
-        raise CpkvError("marshal", CPKV_ERR_ARG, f"{name}: a row per request is wanted")
+def _page_rows(t, name: str, table: PoolTable, rows: int):
+    """(address, ids between requests, ids of a request) of a [requests, pages] table."""
+    if t.dtype != table.int32 or t.device != table.device:
+        raise _wrong(name, f"int32 on {table.device}")
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 2 or shape[0] != rows or (stride[1] != 1 and shape[1] > 1):
+        raise _wrong(name, "a contiguous row of page ids per request")
     if rows <= 1:
-        return at, t.shape[1]
-    if t.stride(0) < t.shape[1]:
-        raise CpkvError("marshal", CPKV_ERR_ARG, f"{name}: rows that overlap")
-    return at, t.stride(0)
+        return t.data_ptr(), shape[1], shape[1]
+    if stride[0] < shape[1]:
+        raise _wrong(name, "rows that do not overlap")
+    return t.data_ptr(), stride[0], shape[1]
+
+
+def _results(out, lse, shape, table: PoolTable):
+    """(address of out, elements between tokens, address of lse or None)."""
+    at, between, got = _rows(out, "out", table)
+    if got != shape:
+        raise _wrong("out", "q's shape")
+    if lse is None:
+        return at, between, None
+    if lse.dtype != table.float32 or lse.device != table.device or lse.shape != shape[:2] or not lse.is_contiguous():
+        raise _wrong("lse", "contiguous float32 [tokens, heads]")
+    return at, between, lse.data_ptr()
+
+
+def _host_list(x):
+    """A contiguous int32 host array and its address."""
+    a = x if type(x) is np.ndarray and x.dtype == np.int32 and x.flags.c_contiguous else _host_i32(x)
+    return a, a.__array_interface__["data"][0]
+
+
+def _handle(stream, table: PoolTable) -> int:
+    """Stream handle; None is the current stream of the pools' device."""
+    if stream is None:
+        import torch
+
+        return torch.cuda.current_stream(table.device).cuda_stream
+    return stream if type(stream) is int else stream.cuda_stream
 
 
 def cpkv_append_rotary(k, v, d_slots, d_positions, d_cos_sin, *, table: PoolTable, d_status, q=None, q_out=None,
@@ -537,38 +560,42 @@ def cpkv_append_rotary(k, v, d_slots, d_positions, d_cos_sin, *, table: PoolTabl
     into ``q_out``.  ``d_positions``: [tokens], or [axes, tokens] with
     ``axis_of_freq`` naming each frequency's axis; ``d_cos_sin``: float32
     [positions, rot_dim], cosines then sines."""
-    import torch
-
-    n, kv_heads, key_dim = k.shape
-    kp, ks = _rows(k, "k", table, kv_heads, key_dim)
-    vp, vs = _rows(v, "v", table, kv_heads, v.shape[2])
-    qp = qs = qop = qos = 0
-    q_heads = 0
+    kp, ks, (n, kv_heads, key_dim) = _rows(k, "k", table)
+    vp, vs, v_shape = _rows(v, "v", table)
+    if v_shape[0] != n or v_shape[1] != kv_heads:
+        raise _wrong("v", "k's tokens and heads")
+    qp = qop = None
+    qs = qos = q_heads = 0
     if q is not None:
-        q_heads = q.shape[1]
-        qp, qs = _rows(q, "q", table, q_heads, key_dim)
-        qop, qos = _rows(q_out, "q_out", table, q_heads, key_dim)
-        if q.shape[0] != n or q_out.shape[0] != n:
-            raise CpkvError("marshal", CPKV_ERR_ARG, "q and q_out: as many tokens as k are wanted")
-    sp = _ints(d_slots, "slots", table, 64, 1)
-    pp = _ints(d_positions, "positions", table, 32, d_positions.dim())
-    axes, pos_stride = (1, n) if d_positions.dim() == 1 else (d_positions.shape[0], d_positions.stride(0))
-    if v.shape[0] != n or d_slots.shape[0] != n or d_positions.dim() > 2 or d_positions.shape[-1] != n:
-        raise CpkvError("marshal", CPKV_ERR_ARG, "v, slots and positions: one entry per token of k is wanted")
-    if (d_cos_sin.dtype != torch.float32 or d_cos_sin.dim() != 2 or d_cos_sin.device != table.device
+        qp, qs, q_shape = _rows(q, "q", table)
+        qop, qos, out_shape = _rows(q_out, "q_out", table)
+        if q_shape != out_shape or q_shape[0] != n or q_shape[2] != key_dim:
+            raise _wrong("q and q_out", "k's tokens and width, alike")
+        q_heads = q_shape[1]
+    device = table.device
+    if d_slots.dtype != table.int64 or d_slots.device != device or d_slots.shape != (n,) or not d_slots.is_contiguous():
+        raise _wrong("slots", "a contiguous int64 list, a slot per token")
+    shape, stride = d_positions.shape, d_positions.stride()
+    if (d_positions.dtype != table.int32 or d_positions.device != device or len(shape) not in (1, 2) or shape[-1] != n
+            or (stride[-1] != 1 and n > 1)):
+        raise _wrong("positions", "int32 [tokens] or [axes, tokens]")
+    axes, between = (1, n) if len(shape) == 1 else (shape[0], stride[0])
+    table_shape = d_cos_sin.shape
+    if (d_cos_sin.dtype != table.float32 or d_cos_sin.device != device or len(table_shape) != 2
             or not d_cos_sin.is_contiguous()):
-        raise CpkvError("marshal", CPKV_ERR_ARG, "cos_sin: contiguous float32 [positions, rot_dim] is wanted")
-    axis = None
+        raise _wrong("cos_sin", "contiguous float32 [positions, rot_dim]")
     if axis_of_freq is not None:
-        axis = bytes(axis_of_freq)
-        if len(axis) != d_cos_sin.shape[1] // 2:
-            raise CpkvError("marshal", CPKV_ERR_ARG, "axis_of_freq: an axis per frequency is wanted")
+        axis_of_freq = bytes(axis_of_freq)
+        if len(axis_of_freq) != table_shape[1] // 2:
+            raise _wrong("axis_of_freq", "an axis per frequency")
     rc = load().cpkv_append_rotary(
-        n, table.page_size, table.cp_size, table.code, q_heads, kv_heads, key_dim, v.shape[2], table.row_bytes,
-        table.key_offset, table.value_offset, table.addresses, table.caps, kp, ks, vp, vs, qp, qs, qop, qos, sp, pp,
-        pos_stride, axes, axis, d_cos_sin.data_ptr(), d_cos_sin.shape[0], d_cos_sin.shape[1],
-        table.flags | (ROTARY_INTERLEAVED if interleaved else 0), d_status.data_ptr(), _stream(stream))
-    _check("cpkv_append_rotary", rc)
+        n, table.page_size, table.cp_size, table.code, q_heads, kv_heads, key_dim, v_shape[2], table.row_bytes,
+        table.key_offset, table.value_offset, table.addresses, table.caps, kp, ks, vp, vs, qp, qs, qop, qos,
+        d_slots.data_ptr(), d_positions.data_ptr(), between, axes, axis_of_freq, d_cos_sin.data_ptr(), table_shape[0],
+        table_shape[1], table.flags | ROTARY_INTERLEAVED if interleaved else table.flags, d_status.data_ptr(),
+        _handle(stream, table))
+    if rc:
+        _check("cpkv_append_rotary", rc)
 
 
 def cpkv_attend_window_workspace_bytes(B, q_heads, kv_heads, head_dim, q_lens, max_kv_len, window=0, sinks=0) -> int:
@@ -585,27 +612,24 @@ def cpkv_attend_window(q, q_lens, page_table, d_kv_lens, *, table: PoolTable, kv
                        scale, out, lse, workspace, d_status, stream=None):
     """Causal attention of ``q`` [tokens, heads, dim] over paged rows, with a
     window and first tokens that stay visible (see include/cpkv.h)."""
-    qp, qs = _rows(q, "q", table, None, q.shape[2])
-    op, os_, lp = _out(out, lse, q, table)
-    lens = _ints(d_kv_lens, "kv_lens", table, 32, 1)
-    B = d_kv_lens.shape[0]
-    tp, ts = _table(page_table, "page_table", table, B)
-    if q_lens is None:
-        ql, tokens = None, B
-    else:
-        ql = _host_i32(q_lens)
-        tokens = int(ql.sum()) if len(ql) == B else -1
-    if tokens != q.shape[0]:
-        raise CpkvError("marshal", CPKV_ERR_ARG, "q_lens: one length per request, adding up to q's tokens, is wanted")
-    if max_kv_len > page_table.shape[1] * table.page_size:
+    qp, qs, shape = _rows(q, "q", table)
+    op, os_, lp = _results(out, lse, shape, table)
+    lens, B = _list_i32(d_kv_lens, "kv_lens", table)
+    tp, ts, ids = _page_rows(page_table, "page_table", table, B)
+    if max_kv_len > ids * table.page_size:
         raise CpkvError("cpkv_attend_window", CPKV_ERR_CAPACITY, "max_kv_len beyond the page table")
+    at = None
+    if q_lens is not None:
+        q_lens, at = _host_list(q_lens)
+        if q_lens.shape != (B,):
+            raise _wrong("q_lens", "a length per request")
+    wp, wb = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel())
     rc = load().cpkv_attend_window(
-        B, table.page_size, table.cp_size, table.code, q.shape[1], kv_heads, q.shape[2], table.row_bytes,
-        table.key_offset, table.value_offset, None if ql is None else ql.ctypes.data, max_kv_len, table.addresses,
-        table.caps, tp, ts, lens, qp, qs, scale, window, sinks, op, os_, lp,
-        None if workspace is None else workspace.data_ptr(), 0 if workspace is None else workspace.numel(),
-        table.flags, d_status.data_ptr(), _stream(stream))
-    _check("cpkv_attend_window", rc)
+        B, table.page_size, table.cp_size, table.code, shape[1], kv_heads, shape[2], table.row_bytes, table.key_offset,
+        table.value_offset, at, max_kv_len, table.addresses, table.caps, tp, ts, lens, shape[0], qp, qs, scale, window,
+        sinks, op, os_, lp, wp, wb, table.flags, d_status.data_ptr(), _handle(stream, table))
+    if rc:
+        _check("cpkv_attend_window", rc)
 
 
 def cpkv_attend_shared_workspace_bytes(B, q_heads, kv_heads, head_dim, group_sizes, prefix_lens, max_suffix_len) -> int:
@@ -621,23 +645,21 @@ def cpkv_attend_shared(q, group_sizes, prefix_lens, prefix_pages, page_table, d_
                        kv_heads, max_suffix_len, scale, out, lse, workspace, d_status, stream=None):
     """One query token per request over its group's shared prefix and its own
     suffix (see include/cpkv.h)."""
-    qp, qs = _rows(q, "q", table, None, q.shape[2])
-    op, os_, lp = _out(out, lse, q, table)
-    lens = _ints(d_suffix_lens, "suffix_lens", table, 32, 1)
-    B = d_suffix_lens.shape[0]
-    tp, ts = _table(page_table, "page_table", table, B)
-    gs, pl = _host_i32(group_sizes), _host_i32(prefix_lens)
-    pp = _ints(prefix_pages, "prefix_pages", table, 32, 1)
-    if q.shape[0] != B or len(gs) != len(pl):
-        raise CpkvError("marshal", CPKV_ERR_ARG, "a query per request and a prefix length per group are wanted")
-    if int(pl.sum()) // table.page_size > prefix_pages.shape[0]:
-        raise CpkvError("cpkv_attend_shared", CPKV_ERR_CAPACITY, "prefix_pages shorter than the prefixes")
-    if max_suffix_len > page_table.shape[1] * table.page_size:
+    qp, qs, shape = _rows(q, "q", table)
+    op, os_, lp = _results(out, lse, shape, table)
+    lens, B = _list_i32(d_suffix_lens, "suffix_lens", table)
+    tp, ts, ids = _page_rows(page_table, "page_table", table, B)
+    pp, prefix_ids = _list_i32(prefix_pages, "prefix_pages", table)
+    gs, gs_at = _host_list(group_sizes)
+    pl, pl_at = _host_list(prefix_lens)
+    if shape[0] != B or gs.shape != pl.shape or gs.ndim != 1:
+        raise _wrong("q, group_sizes and prefix_lens", "a query per request, a prefix length per group")
+    if max_suffix_len > ids * table.page_size:
         raise CpkvError("cpkv_attend_shared", CPKV_ERR_CAPACITY, "max_suffix_len beyond the page table")
+    wp, wb = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel())
     rc = load().cpkv_attend_shared(
-        B, len(gs), table.page_size, table.cp_size, table.code, q.shape[1], kv_heads, q.shape[2], table.row_bytes,
-        table.key_offset, table.value_offset, gs.ctypes.data, pl.ctypes.data, max_suffix_len, table.addresses,
-        table.caps, pp, tp, ts, lens, qp, qs, scale, op, os_, lp,
-        None if workspace is None else workspace.data_ptr(), 0 if workspace is None else workspace.numel(),
-        table.flags, d_status.data_ptr(), _stream(stream))
-    _check("cpkv_attend_shared", rc)
+        B, gs.shape[0], table.page_size, table.cp_size, table.code, shape[1], kv_heads, shape[2], table.row_bytes,
+        table.key_offset, table.value_offset, gs_at, pl_at, max_suffix_len, table.addresses, table.caps, pp, prefix_ids,
+        tp, ts, lens, qp, qs, scale, op, os_, lp, wp, wb, table.flags, d_status.data_ptr(), _handle(stream, table))
+    if rc:
+        _check("cpkv_attend_shared", rc)

@@ -53,17 +53,18 @@ int64_t round_up(int64_t n, int64_t to) { return ceil_div(n, to) * to; }
 
 // Bounds of a split pass, from host lengths.
 struct SplitBounds {
-  int64_t tokens = 0, tiles_cap = 0, units = 0;
+  int64_t tokens = 0, tiles_cap = 0, units = 0, max_tiles = 0;
   int grid_cap = 1;
 
   void add(int64_t nq, int64_t max_kv, int group, int kv_heads, int window, int sinks) {
     int64_t tiles = ceil_div(max_kv, kSplitTile);
     if (window > 0) tiles = std::min<int64_t>(tiles, ceil_div((int64_t)sinks, kSplitTile) + ((int64_t)window + nq) / kSplitTile + 2);
     units += ceil_div(nq * group, kSplitRows) * kv_heads * tiles;
+    max_tiles = std::max<int64_t>(max_tiles, tiles);
     tokens += nq;
+    tiles_cap += ceil_div(nq * group, kSplitRows) + 1;
   }
-  int finish(int64_t count, int group) {
-    tiles_cap = tokens * group / kSplitRows + count;
+  int finish(int group) {
     if (units > INT32_MAX || tokens * group > INT32_MAX) return CPKV_ERR_LIMIT;
     grid_cap = (int)std::min<int64_t>(kSplitMaxGrid, units > 0 ? units : 1);
     return CPKV_OK;
@@ -129,9 +130,13 @@ bool few_rows(int64_t max_rows) { return max_rows <= 2 * kSplitRows; }
 struct WindowPlan {
   SplitBounds split;
   TileBounds tile;
-  bool few = true;
+  bool few = true, whole = false;
   int64_t tokens = 0, bytes = 0;
 };
+
+// A block takes whole tiles of few rows when no sequence has more units of keys
+// than this: the units one after the other then cost less than joining parts does.
+constexpr int64_t kWholeUnits = 8;
 
 int window_plan(WindowPlan *w, const HeadArgs &a, int B, const int32_t *h_q_lens, int64_t max_kv, int window, int sinks) {
   const int group = a.q_heads / a.kv_heads;
@@ -143,39 +148,44 @@ int window_plan(WindowPlan *w, const HeadArgs &a, int B, const int32_t *h_q_lens
   }
   w->few = few_rows(w->tile.max_rows);
   w->tokens = w->tile.tokens;
-  const int rc = w->few ? w->split.finish(B, group) : w->tile.finish(a.kv_heads);
-  w->bytes = w->few ? w->split.bytes(B, a.kv_heads, a.head_dim, true) : w->tile.bytes(a.kv_heads, a.head_dim, true);
+  bool uniform = B > 0;
+  for (int s = 1; s < B && h_q_lens != nullptr; ++s) uniform &= h_q_lens[s] == h_q_lens[0];
+  w->whole = w->few && uniform && w->split.max_tiles <= kWholeUnits;
+  const int rc = w->few ? w->split.finish(group) : w->tile.finish(a.kv_heads);
+  w->bytes = w->whole ? 0
+             : w->few ? w->split.bytes(B, a.kv_heads, a.head_dim, true)
+                      : w->tile.bytes(a.kv_heads, a.head_dim, true);
   return rc;
 }
 
 struct SharedPlan {
-  SplitBounds split, suffix;  // split: the prefixes, when rows are few
-  TileBounds tile;
+  SplitBounds split;  // the suffixes, and the prefixes when rows are few
+  TileBounds tile;    // the prefixes when rows are many
   bool few = true;
-  int64_t prefix_bytes = 0, bytes = 0;
+  int64_t prefix_pages = 0, prefix_bytes = 0, bytes = 0;
 };
 
 int shared_plan(SharedPlan *w, const HeadArgs &a, int B, int n_groups, const int32_t *h_group_sizes,
                 const int32_t *h_prefix_lens, int page_size, int64_t max_suffix) {
   const int group = a.q_heads / a.kv_heads;
-  int64_t sum = 0, pages = 0;
+  int64_t sum = 0;
   for (int g = 0; g < n_groups; ++g) {
     if (h_group_sizes[g] < 0 || h_prefix_lens[g] < 0) return CPKV_ERR_ARG;
     if (page_size > 0 && h_prefix_lens[g] % page_size != 0) return CPKV_ERR_UNALIGNED_PREFIX;
-    w->split.add(h_group_sizes[g], h_prefix_lens[g], group, a.kv_heads, 0, 0);
     w->tile.add(h_group_sizes[g], h_prefix_lens[g], group, 0, 0);
     sum += h_group_sizes[g];
-    if (page_size > 0) pages += h_prefix_lens[g] / page_size;
+    if (page_size > 0) w->prefix_pages += h_prefix_lens[g] / page_size;
   }
   if (sum != B) return CPKV_ERR_ARG;
-  if (pages > INT32_MAX) return CPKV_ERR_LIMIT;
-  for (int b = 0; b < B; ++b) w->suffix.add(1, max_suffix, group, a.kv_heads, 0, 0);
+  if (w->prefix_pages > INT32_MAX) return CPKV_ERR_LIMIT;
   w->few = few_rows(w->tile.max_rows);
-  int rc = w->few ? w->split.finish(n_groups, group) : w->tile.finish(a.kv_heads);
-  if (rc == CPKV_OK) rc = w->suffix.finish(B, group);
-  w->prefix_bytes = w->few ? w->split.bytes(n_groups, a.kv_heads, a.head_dim, false)
-                           : w->tile.bytes(a.kv_heads, a.head_dim, false);
-  w->bytes = w->prefix_bytes + w->suffix.bytes(B, a.kv_heads, a.head_dim, false);
+  for (int g = 0; g < n_groups && w->few; ++g)
+    w->split.add(h_group_sizes[g], h_prefix_lens[g], group, a.kv_heads, 0, 0);
+  for (int b = 0; b < B; ++b) w->split.add(1, max_suffix, group, a.kv_heads, 0, 0);
+  int rc = w->split.finish(group);
+  if (!w->few && rc == CPKV_OK) rc = w->tile.finish(a.kv_heads);
+  w->prefix_bytes = w->few ? 0 : w->tile.bytes(a.kv_heads, a.head_dim, false);
+  w->bytes = w->prefix_bytes + w->split.bytes(w->few ? n_groups + B : B, a.kv_heads, a.head_dim, false);
   return rc;
 }
 
@@ -189,19 +199,26 @@ int for_type_and_dim(const HeadArgs &a, F f) {
                            : f(__half(), std::integral_constant<int, 64>());
 }
 
-template <typename T, int D, int N>
-int split_pass(SplitParams<N> *p, const SplitBounds &b, cudaStream_t stream) {
-  const int smem = SplitShape<D>::kSmem + (p->seqs.count + 1) * 4;
-  auto kernel = attend_split_kernel<T, D, N>;
-  const int rc = ensure_dynamic_smem((const void *)kernel, SplitShape<D>::kSmem + (CPKV_MAX_BATCH + 1) * 4);
+// Whole tiles (no join) where each sequence has `row_tiles` tiles; `dependent`:
+// another pass of the call goes before, whose results this one does not read.
+template <typename T, int D, typename S, bool kWhole>
+int split_pass(SplitParams<S> *p, const SplitBounds &b, bool dependent, cudaStream_t stream) {
+  const int smem = SplitShape<D>::kSmem + (kWhole ? 0 : (p->seqs.count + 1) * 4);
+  auto kernel = attend_split_kernel<T, D, S, kWhole>;
+  const int rc = ensure_dynamic_smem((const void *)kernel, SplitShape<D>::kSmem + (2 * CPKV_MAX_BATCH + 1) * 4);
   if (rc != CPKV_OK) return rc;
+  if (kWhole) {
+    const int64_t blocks = (int64_t)p->seqs.count * p->io.kv_heads * p->row_tiles;
+    if (blocks > INT32_MAX) return CPKV_ERR_LIMIT;
+    return launch_kernel(kernel, dim3((unsigned)blocks), dim3(kSplitWarps * 32), smem, dependent, stream, *p);
+  }
   p->space.grid = persistent_grid((const void *)kernel, kSplitWarps * 32, smem, 8, b.grid_cap);
-  return launch_kernel(kernel, dim3(p->space.grid), dim3(kSplitWarps * 32), smem, false, stream, *p);
+  return launch_kernel(kernel, dim3(p->space.grid), dim3(kSplitWarps * 32), smem, dependent, stream, *p);
 }
 
-template <int N>
-SplitSource<N> source_of(const SplitParams<N> &p) {
-  SplitSource<N> s;
+template <typename S>
+SplitSource<S> source_of(const SplitParams<S> &p) {
+  SplitSource<S> s;
   s.seqs = p.seqs;
   s.space = p.space;
   s.tiles_cap = p.tiles_cap;
@@ -295,7 +312,7 @@ int join_pass(const A &a, const B &b, const AttendIo &io, int64_t rows, cudaStre
   p.b = b;
   p.io = io;
   p.rows = rows;
-  return launch_kernel(attend_join_kernel<T, D, A, B>, dim3((unsigned)blocks), dim3(128), 0, false, stream, p);
+  return launch_kernel(attend_join_kernel<T, D, A, B>, dim3((unsigned)blocks), dim3(128), 0, true, stream, p);
 }
 
 template <int N>
@@ -303,17 +320,23 @@ int attend_window(const HeadArgs &heads, const Seqs<N> &seqs, const PagedPools &
                   const WindowPlan &plan, char *workspace, cudaStream_t stream) {
   const int64_t rows = plan.tokens * heads.q_heads;
   if (plan.few) {
-    SplitParams<N> p = {};
+    SplitParams<Seqs<N>> p = {};
     p.seqs = seqs;
     p.pools = pools;
     p.io = io;
+    p.direct = 1;
+    if (plan.whole) {
+      p.row_tiles = (int)ceil_div((int64_t)seqs.uniform_q * io.group.d, kSplitRows);
+      return for_type_and_dim(heads, [&](auto t, auto d) {
+        return split_pass<decltype(t), decltype(d)::value, Seqs<N>, true>(&p, plan.split, false, stream);
+      });
+    }
     p.space = plan.split.space(workspace, seqs.count, heads.kv_heads, true);
     p.tiles_cap = plan.split.tiles_cap;
-    p.direct = 1;
     return for_type_and_dim(heads, [&](auto t, auto d) {
       using T = decltype(t);
       constexpr int D = decltype(d)::value;
-      const int rc = split_pass<T, D, N>(&p, plan.split, stream);
+      const int rc = split_pass<T, D, Seqs<N>, false>(&p, plan.split, false, stream);
       return rc != CPKV_OK ? rc : join_pass<T, D>(source_of(p), NoSource(), io, rows, stream);
     });
   }
@@ -327,38 +350,43 @@ int attend_window(const HeadArgs &heads, const Seqs<N> &seqs, const PagedPools &
   });
 }
 
+// Few query rows per prefix: prefixes and suffixes in one split pass.
 template <int N>
-int attend_shared(const HeadArgs &heads, const Seqs<N> &prefix, const Seqs<kFewSeqs> &suffix, const PagedPools &pools,
-                  const AttendIo &io, const SharedPlan &plan, char *workspace, cudaStream_t stream) {
-  const int64_t rows = (int64_t)suffix.count * heads.q_heads;
-  SplitParams<kFewSeqs> sp = {};
+int attend_shared_few(const HeadArgs &heads, const SharedSeqs<N> &seqs, const PagedPools &pools, const AttendIo &io,
+                      const SharedPlan &plan, char *workspace, cudaStream_t stream) {
+  SplitParams<SharedSeqs<N>> p = {};
+  p.seqs = seqs;
+  p.pools = pools;
+  p.io = io;
+  p.space = plan.split.space(workspace, seqs.count, heads.kv_heads, false);
+  p.tiles_cap = plan.split.tiles_cap;
+  return for_type_and_dim(heads, [&](auto t, auto d) {
+    using T = decltype(t);
+    constexpr int D = decltype(d)::value;
+    const int rc = split_pass<T, D, SharedSeqs<N>, false>(&p, plan.split, false, stream);
+    const int64_t rows = (int64_t)(seqs.count - seqs.groups) * heads.q_heads;
+    return rc != CPKV_OK ? rc : join_pass<T, D>(source_of(p), NoSource(), io, rows, stream);
+  });
+}
+
+template <int N>
+int attend_shared_many(const HeadArgs &heads, const Seqs<N> &prefix, const Seqs<kFewSeqs> &suffix,
+                       const PagedPools &pools, const AttendIo &io, const SharedPlan &plan, char *workspace,
+                       cudaStream_t stream) {
+  SplitParams<Seqs<kFewSeqs>> sp = {};
   sp.seqs = suffix;
   sp.pools = pools;
   sp.io = io;
-  sp.space = plan.suffix.space(workspace + plan.prefix_bytes, suffix.count, heads.kv_heads, false);
-  sp.tiles_cap = plan.suffix.tiles_cap;
-  if (plan.few) {
-    SplitParams<N> pp = {};
-    pp.seqs = prefix;
-    pp.pools = pools;
-    pp.io = io;
-    pp.space = plan.split.space(workspace, prefix.count, heads.kv_heads, false);
-    pp.tiles_cap = plan.split.tiles_cap;
-    return for_type_and_dim(heads, [&](auto t, auto d) {
-      using T = decltype(t);
-      constexpr int D = decltype(d)::value;
-      int rc = split_pass<T, D, N>(&pp, plan.split, stream);
-      if (rc == CPKV_OK) rc = split_pass<T, D, kFewSeqs>(&sp, plan.suffix, stream);
-      return rc != CPKV_OK ? rc : join_pass<T, D>(source_of(sp), source_of(pp), io, rows, stream);
-    });
-  }
+  sp.space = plan.split.space(workspace + plan.prefix_bytes, suffix.count, heads.kv_heads, false);
+  sp.tiles_cap = plan.split.tiles_cap;
   TileParams<N> pp = {};
   fill_tiles(&pp, prefix, pools, io, plan.tile, workspace, false);
   return for_type_and_dim(heads, [&](auto t, auto d) {
     using T = decltype(t);
     constexpr int D = decltype(d)::value;
     int rc = tile_pass<T, D, N>(pp, plan.tile, stream);
-    if (rc == CPKV_OK) rc = split_pass<T, D, kFewSeqs>(&sp, plan.suffix, stream);
+    if (rc == CPKV_OK) rc = split_pass<T, D, Seqs<kFewSeqs>, false>(&sp, plan.split, true, stream);
+    const int64_t rows = (int64_t)suffix.count * heads.q_heads;
     return rc != CPKV_OK ? rc : join_pass<T, D>(source_of(sp), source_of(pp), io, rows, stream);
   });
 }
@@ -387,8 +415,8 @@ extern "C" int cpkv_attend_window(int B, int page_size, int cp_size, int dtype, 
                                   int64_t row_bytes, int64_t key_offset, int64_t value_offset,
                                   const int32_t *h_q_lens, int64_t max_kv_len, const void *const *h_pools,
                                   const int64_t *h_pool_cap_pages, const int32_t *d_page_table, int64_t table_stride,
-                                  const int32_t *d_kv_lens, const void *d_q, int64_t q_stride, float scale, int window,
-                                  int sinks, void *d_out, int64_t out_stride, float *d_lse, void *d_workspace,
+                                  const int32_t *d_kv_lens, int64_t num_tokens, const void *d_q, int64_t q_stride,
+                                  float scale, int window, int sinks, void *d_out, int64_t out_stride, float *d_lse, void *d_workspace,
                                   int64_t workspace_bytes, int flags, int32_t *d_status, cpkv_stream_t stream) {
   const HeadArgs heads = {dtype, q_heads, kv_heads, head_dim};
   if (B < 0 || max_kv_len < 0 || window < 0 || sinks < 0 || (flags & ~CPKV_DENSE_PAGES)) return CPKV_ERR_ARG;
@@ -404,13 +432,14 @@ extern "C" int cpkv_attend_window(int B, int page_size, int cp_size, int dtype, 
   WindowPlan plan;
   rc = window_plan(&plan, heads, B, h_q_lens, max_kv_len, window, sinks);
   if (rc != CPKV_OK) return rc;
+  if (plan.tokens != num_tokens) return CPKV_ERR_ARG;
   if (plan.tokens == 0) return CPKV_OK;
   if (d_kv_lens == nullptr || d_status == nullptr || (max_kv_len > 0 && d_page_table == nullptr)) return CPKV_ERR_ARG;
   AttendIo io = {};
   rc = fill_io(&io, heads, d_q, q_stride, d_out, out_stride, d_lse, scale, key_offset, value_offset);
   if (rc != CPKV_OK) return rc;
-  if (plan.bytes > 0 && (d_workspace == nullptr || !aligned16(d_workspace))) return CPKV_ERR_ARG;
   if (workspace_bytes < plan.bytes) return CPKV_ERR_CAPACITY;
+  if (plan.bytes > 0 && (d_workspace == nullptr || !aligned16(d_workspace))) return CPKV_ERR_ARG;
   // one query length for all needs no lengths in the kernel's block (the tile kernel goes by them)
   bool uniform = plan.few;
   for (int b = 1; b < B && h_q_lens != nullptr; ++b) uniform &= h_q_lens[b] == h_q_lens[0];
@@ -457,8 +486,8 @@ extern "C" int cpkv_attend_shared(int B, int n_groups, int page_size, int cp_siz
                                   int head_dim, int64_t row_bytes, int64_t key_offset, int64_t value_offset,
                                   const int32_t *h_group_sizes, const int32_t *h_prefix_lens, int64_t max_suffix_len,
                                   const void *const *h_pools, const int64_t *h_pool_cap_pages,
-                                  const int32_t *d_prefix_pages, const int32_t *d_page_table, int64_t table_stride,
-                                  const int32_t *d_suffix_lens, const void *d_q, int64_t q_stride, float scale,
+                                  const int32_t *d_prefix_pages, int64_t num_prefix_pages, const int32_t *d_page_table,
+                                  int64_t table_stride, const int32_t *d_suffix_lens, const void *d_q, int64_t q_stride, float scale,
                                   void *d_out, int64_t out_stride, float *d_lse, void *d_workspace,
                                   int64_t workspace_bytes, int flags, int32_t *d_status, cpkv_stream_t stream) {
   const HeadArgs heads = {dtype, q_heads, kv_heads, head_dim};
@@ -476,38 +505,55 @@ extern "C" int cpkv_attend_shared(int B, int n_groups, int page_size, int cp_siz
   SharedPlan plan;
   rc = shared_plan(&plan, heads, B, n_groups, h_group_sizes, h_prefix_lens, page_size, max_suffix_len);
   if (rc != CPKV_OK) return rc;
+  if (num_prefix_pages < plan.prefix_pages) return CPKV_ERR_CAPACITY;
   if (B == 0) return CPKV_OK;
   if (d_suffix_lens == nullptr || d_status == nullptr || (max_suffix_len > 0 && d_page_table == nullptr) ||
-      (plan.split.units > 0 && d_prefix_pages == nullptr))
+      (plan.prefix_pages > 0 && d_prefix_pages == nullptr))
     return CPKV_ERR_ARG;
   AttendIo io = {};
   rc = fill_io(&io, heads, d_q, q_stride, d_out, out_stride, d_lse, scale, key_offset, value_offset);
   if (rc != CPKV_OK) return rc;
-  if (d_workspace == nullptr || !aligned16(d_workspace)) return CPKV_ERR_ARG;
   if (workspace_bytes < plan.bytes) return CPKV_ERR_CAPACITY;
-  Seqs<kFewSeqs> suffix = {};
-  suffix.kv_lens = d_suffix_lens;
-  suffix.table = d_page_table;
-  suffix.stride = table_stride;
-  suffix.status = d_status;
-  suffix.count = B;
-  suffix.uniform_q = 1;
-  suffix.kv_cap = (int)max_suffix_len;
-  auto go = [&](auto n) {
-    constexpr int N = decltype(n)::value;
-    Seqs<N> s = {};
-    s.table = d_prefix_pages;
-    s.stride = -1;
-    s.status = d_status;
-    s.count = n_groups;
+  if (d_workspace == nullptr || !aligned16(d_workspace)) return CPKV_ERR_ARG;
+  char *const space = static_cast<char *>(d_workspace);
+  auto groups = [&](auto *s) {
+    s->status = d_status;
     int pages = 0;
     for (int g = 0; g < n_groups; ++g) {
-      s.cu_q[g + 1] = s.cu_q[g] + h_group_sizes[g];
-      s.kv[g] = h_prefix_lens[g];
-      s.page0[g] = pages;
+      s->cu_q[g + 1] = s->cu_q[g] + h_group_sizes[g];
+      s->kv[g] = h_prefix_lens[g];
+      s->page0[g] = pages;
       pages += h_prefix_lens[g] / page_size;
     }
-    return attend_shared<N>(heads, s, suffix, pools, io, plan, static_cast<char *>(d_workspace), (cudaStream_t)stream);
+  };
+  auto go = [&](auto n) {
+    constexpr int N = decltype(n)::value;
+    if (plan.few) {
+      SharedSeqs<N> s = {};
+      groups(&s);
+      s.prefix_pages = d_prefix_pages;
+      s.table = d_page_table;
+      s.suffix_lens = d_suffix_lens;
+      s.stride = table_stride;
+      s.count = n_groups + B;
+      s.groups = n_groups;
+      s.suffix_cap = (int)max_suffix_len;
+      return attend_shared_few<N>(heads, s, pools, io, plan, space, (cudaStream_t)stream);
+    }
+    Seqs<N> prefix = {};
+    groups(&prefix);
+    prefix.table = d_prefix_pages;
+    prefix.stride = -1;
+    prefix.count = n_groups;
+    Seqs<kFewSeqs> suffix = {};
+    suffix.kv_lens = d_suffix_lens;
+    suffix.table = d_page_table;
+    suffix.stride = table_stride;
+    suffix.status = d_status;
+    suffix.count = B;
+    suffix.uniform_q = 1;
+    suffix.kv_cap = (int)max_suffix_len;
+    return attend_shared_many<N>(heads, prefix, suffix, pools, io, plan, space, (cudaStream_t)stream);
   };
   if (n_groups <= kFewSeqs) return go(std::integral_constant<int, kFewSeqs>());
   return go(std::integral_constant<int, CPKV_MAX_BATCH>());

@@ -48,6 +48,54 @@ struct Seqs {
   }
   CPKV_DEV bool kv_len_bad(int s) const { return kv_lens != nullptr && (kv_lens[s] < 0 || kv_lens[s] > kv_cap); }
   CPKV_DEV const int32_t *pages(int s) const { return stride < 0 ? table + page0[s] : table + s * stride; }
+  // Tiles of 16 packed rows before sequence s, at most.
+  CPKV_DEV int64_t tiles_before(int s, int group) const { return (int64_t)q_begin(s) * group / 16 + s; }
+  // The sequences that hold a query token, and where it stands in them.
+  CPKV_DEV int places(int token, int (&s)[2], int (&i)[2]) const {
+    s[0] = uniform_q ? token / uniform_q : upper_index(cu_q, count, token);
+    i[0] = token - q_begin(s[0]);
+    return 1;
+  }
+};
+
+// Shared prefixes and suffixes as the sequences of one pass: first the groups
+// (every request's query over the prefix), then the requests (one query over its
+// own suffix).
+template <int N>
+struct SharedSeqs {
+  const int32_t *prefix_pages, *table, *suffix_lens;
+  int64_t stride;
+  int32_t *status;
+  int count, groups, suffix_cap;
+  static constexpr int causal = 0, window = 0, sinks = 0;
+  int cu_q[N + 1];  // requests before each group
+  int kv[N];
+  int page0[N];
+
+  CPKV_DEV int q_begin(int s) const { return s < groups ? cu_q[s] : s - groups; }
+  CPKV_DEV int q_count(int s) const { return s < groups ? cu_q[s + 1] - cu_q[s] : 1; }
+  CPKV_DEV int kv_len(int s) const {
+    if (s < groups) return kv[s];
+    const int n = suffix_lens[s - groups];
+    return n < 0 ? 0 : (n > suffix_cap ? suffix_cap : n);
+  }
+  CPKV_DEV bool kv_len_bad(int s) const {
+    return s >= groups && (suffix_lens[s - groups] < 0 || suffix_lens[s - groups] > suffix_cap);
+  }
+  CPKV_DEV const int32_t *pages(int s) const {
+    return s < groups ? prefix_pages + page0[s] : table + (s - groups) * stride;
+  }
+  CPKV_DEV int64_t tiles_before(int s, int group) const {
+    if (s < groups) return (int64_t)cu_q[s] * group / 16 + s;
+    return (int64_t)(count - groups) * group / 16 + groups + (int64_t)(s - groups) * ((group + 15) / 16);
+  }
+  CPKV_DEV int places(int token, int (&s)[2], int (&i)[2]) const {
+    s[0] = groups + token;
+    i[0] = 0;
+    s[1] = upper_index(cu_q, groups, token);
+    i[1] = token - cu_q[s[1]];
+    return 2;
+  }
 };
 
 // Keys that some of the query tokens [i0, i1) of a sequence see, as tiles of
@@ -194,27 +242,21 @@ struct SplitSpace {
 
 CPKV_DEV int split_chunk(int total, int grid) { return total <= grid ? 1 : (total + grid - 1) / grid; }
 
-// Slot index of a whole tile: tiles before sequence s number at most
-// (rows before s) / 16 + s.
-template <int N>
-CPKV_DEV int64_t whole_tile(const Seqs<N> &q, int s, int rt, int h, int group, int64_t tiles_cap) {
-  return h * tiles_cap + (int64_t)q.q_begin(s) * group / kSplitRows + s + rt;
-}
-
-template <int N>
+template <typename S>
 struct SplitParams {
-  Seqs<N> seqs;
+  S seqs;
   PagedPools pools;
   AttendIo io;
   SplitSpace space;
   int64_t tiles_cap;  // tiles of all sequences per key/value head, at most
-  int direct;         // whole tiles go straight to the output
+  int row_tiles;      // of each sequence, when a block takes a whole tile
+  int direct;         // tiles that one block holds whole go straight to the output
 };
 
 // Finds the parts of a row of a split pass.
-template <int N>
+template <typename S>
 struct SplitSource {
-  Seqs<N> seqs;
+  S seqs;
   SplitSpace space;
   int64_t tiles_cap;
   int direct;

@@ -51,8 +51,8 @@ struct RowSum {
 
 // Adds the parts of query head `head` of token i of sequence s; false when the
 // pass has written that row's output itself.
-template <int D, int N>
-CPKV_DEV bool add_parts(RowSum<D> *sum, const SplitSource<N> &src, const AttendIo &io, int s, int i, int head, int lane) {
+template <int D, typename S>
+CPKV_DEV bool add_parts(RowSum<D> *sum, const SplitSource<S> &src, const AttendIo &io, int s, int i, int head, int lane) {
   const int group = io.group.d, h = div_by(head, io.group), g = head - h * group;
   const int nq = src.seqs.q_count(s), kv = src.seqs.kv_len(s);
   const KeyRange keys = key_range<kSplitTile>(kv, nq, 0, nq, src.seqs.causal, src.seqs.window, src.seqs.sinks);
@@ -64,7 +64,7 @@ CPKV_DEV bool add_parts(RowSum<D> *sum, const SplitSource<N> &src, const AttendI
   const int c0 = begin / chunk, c1 = (end - 1) / chunk;
   if (c0 == c1) {
     if (src.direct) return false;
-    const int64_t slot = 2 * (int64_t)src.space.grid + whole_tile(src.seqs, s, rt, h, group, src.tiles_cap);
+    const int64_t slot = 2 * (int64_t)src.space.grid + h * src.tiles_cap + src.seqs.tiles_before(s, group) + rt;
     sum->add(src.space.ml, src.space.o, 1, lane, [&](int) { return slot * kSplitRows + in_tile; });
     return true;
   }
@@ -85,18 +85,18 @@ CPKV_DEV bool add_parts(RowSum<D> *sum, const TileSource<N> &src, const AttendIo
 }
 
 struct NoSource {};
-template <int D>
-CPKV_DEV bool add_parts(RowSum<D> *, const NoSource &, const AttendIo &, int, int, int, int) {
+
+// All parts of a row that a pass has; false when the pass wrote the row itself.
+template <int D, typename Source>
+CPKV_DEV bool add_all(RowSum<D> *sum, const Source &src, const AttendIo &io, int token, int head, int lane) {
+  int s[2], i[2];
+  const int n = src.seqs.places(token, s, i);
+  for (int k = 0; k < n; ++k)
+    if (!add_parts(sum, src, io, s[k], i[k], head, lane)) return false;
   return true;
 }
 
-template <int N>
-CPKV_DEV int seq_of(const Seqs<N> &q, int token) {
-  return q.uniform_q ? token / q.uniform_q : upper_index(q.cu_q, q.count, token);
-}
-
-// `a`: the pass whose sequences own the query tokens; `b`: a second pass over
-// the same tokens, or none.
+// `a`: a pass over the query tokens; `b`: a second one over the same, or none.
 template <typename A, typename B>
 struct JoinParams {
   A a;
@@ -113,14 +113,9 @@ __global__ void __launch_bounds__(128) attend_join_kernel(const __grid_constant_
   if (row >= p.rows) return;
   const int token = (int)(row / p.io.q_heads), head = (int)(row - (int64_t)token * p.io.q_heads);
   RowSum<D> sum;
-  {
-    const int s = seq_of(p.a.seqs, token);
-    if (!add_parts(&sum, p.a, p.io, s, token - p.a.seqs.q_begin(s), head, lane)) return;
-  }
-  if constexpr (!std::is_same<B, NoSource>::value) {
-    const int s = seq_of(p.b.seqs, token);
-    add_parts(&sum, p.b, p.io, s, token - p.b.seqs.q_begin(s), head, lane);
-  }
+  wait_prerequisite();
+  if (!add_all(&sum, p.a, p.io, token, head, lane)) return;
+  if constexpr (!std::is_same<B, NoSource>::value) add_all(&sum, p.b, p.io, token, head, lane);
   const float inv = row_scale(sum.l);
   char *dst = p.io.out + token * p.io.out_stride + (int64_t)head * D * 2 + lane * (D / 16);
   if constexpr (D == 128) {

@@ -8,7 +8,8 @@
 // (sequence, key/value head, 16 rows); all units of the call form one line that
 // is cut evenly over the blocks, whatever the lengths are, and a block's warps
 // each own 16 keys of every unit with a cp.async ring of their own, so that no
-// block-wide barrier stands inside a stretch.
+// block-wide barrier stands inside a stretch.  Where every sequence has few keys
+// (kWhole) a block takes one whole tile instead and nothing is left to join.
 #pragma once
 
 #include "attend.cuh"
@@ -24,25 +25,25 @@ struct SplitShape {
   static constexpr int kStage = kWarpKeys * kRow * 2;      // keys, then values
   static constexpr int kStages = D == 128 ? 3 : 4;
   static constexpr int kRing = kSplitWarps * kStages * kStage;
-  static constexpr int kJoin = 2 * kSplitRows * D * 4;     // values of two warps while a tile's parts are joined
+  static constexpr int kJoin = kSplitRows * D * 4;         // half the columns of two warps while a tile's parts are joined
   static constexpr int kSmem = kRing + kJoin + kSplitWarps * kSplitRows * 8;
 };
 
 // A position on the line of units.
-template <int N>
+template <typename S>
 struct Cursor {
   int s, h, rt, j, row_tiles;
   int nq, kv;
   KeyRange keys;
 
-  CPKV_DEV void enter(const SplitParams<N> &p, int seq) {
+  CPKV_DEV void enter(const SplitParams<S> &p, int seq) {
     s = seq;
     nq = p.seqs.q_count(s);
     kv = p.seqs.kv_len(s);
     keys = key_range<kSplitTile>(kv, nq, 0, nq, p.seqs.causal, p.seqs.window, p.seqs.sinks);
     row_tiles = (nq * (int)p.io.group.d + kSplitRows - 1) / kSplitRows;
   }
-  CPKV_DEV void seek(const SplitParams<N> &p, const int *cum, int u) {
+  CPKV_DEV void seek(const SplitParams<S> &p, const int *cum, int u) {
     enter(p, upper_index(cum, p.seqs.count, u));
     const int local = u - cum[s];
     const int tile = local / keys.n_tiles;
@@ -51,7 +52,7 @@ struct Cursor {
     rt = tile - h * row_tiles;
   }
   // To the next unit of the line; there must be one.
-  CPKV_DEV void advance(const SplitParams<N> &p) {
+  CPKV_DEV void advance(const SplitParams<S> &p) {
     if (++j < keys.n_tiles) return;
     j = 0;
     if (++rt < row_tiles) return;
@@ -64,8 +65,8 @@ struct Cursor {
   }
 };
 
-template <typename T, int D, int N>
-__global__ void __launch_bounds__(kSplitWarps * 32) attend_split_kernel(const __grid_constant__ SplitParams<N> p) {
+template <typename T, int D, typename S, bool kWhole>
+__global__ void __launch_bounds__(kSplitWarps * 32) attend_split_kernel(const __grid_constant__ SplitParams<S> p) {
   using Shape = SplitShape<D>;
   extern __shared__ __align__(128) char smem[];
   __shared__ int scan_scratch[33];
@@ -73,32 +74,51 @@ __global__ void __launch_bounds__(kSplitWarps * 32) attend_split_kernel(const __
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int count = p.seqs.count;
 
-  // units before each sequence
-  int total = 0;
-  for (int s0 = 0; s0 < count; s0 += kSplitWarps * 32) {
-    const int s = s0 + (int)threadIdx.x;
-    int mine = 0;
-    if (s < count) {
-      Cursor<N> c;
-      c.enter(p, s);
-      mine = c.keys.n_tiles * c.row_tiles * p.io.kv_heads;
-      if (blockIdx.x == 0 && p.seqs.kv_len_bad(s)) raise_status(p.seqs.status, CPKV_STATUS_OUT_CAPACITY);
+  release_dependents();  // the joining kernel, which waits for this one
+  Cursor<S> ld;
+  int u0, u1;
+  if constexpr (kWhole) {
+    const int tile = (int)blockIdx.x / p.row_tiles;
+    ld.enter(p, tile / p.io.kv_heads);
+    ld.h = tile % p.io.kv_heads;
+    ld.rt = (int)blockIdx.x % p.row_tiles;
+    ld.j = 0;
+    if (ld.h == 0 && ld.rt == 0 && threadIdx.x == 0 && p.seqs.kv_len_bad(ld.s))
+      raise_status(p.seqs.status, CPKV_STATUS_OUT_CAPACITY);
+    u0 = 0;
+    u1 = ld.keys.n_tiles;
+  } else {
+    // units before each sequence
+    int total = 0;
+    for (int s0 = 0; s0 < count; s0 += kSplitWarps * 32) {
+      const int s = s0 + (int)threadIdx.x;
+      int mine = 0;
+      if (s < count) {
+        Cursor<S> c;
+        c.enter(p, s);
+        mine = c.keys.n_tiles * c.row_tiles * p.io.kv_heads;
+        if (blockIdx.x == 0 && p.seqs.kv_len_bad(s)) raise_status(p.seqs.status, CPKV_STATUS_OUT_CAPACITY);
+      }
+      int part;
+      const int before = block_exclusive_scan(mine, scan_scratch, &part);
+      if (s < count) {
+        cum[s] = total + before;
+        if (blockIdx.x == 0) p.space.cum[s] = total + before;
+      }
+      total += part;
     }
-    int part;
-    const int before = block_exclusive_scan(mine, scan_scratch, &part);
-    if (s < count) {
-      cum[s] = total + before;
-      if (blockIdx.x == 0) p.space.cum[s] = total + before;
+    if (blockIdx.x == 0 && threadIdx.x == 0) p.space.cum[count] = total;
+    __syncthreads();
+    const int chunk = split_chunk(total, (int)gridDim.x);
+    const int64_t first = (int64_t)blockIdx.x * chunk;
+    if (first >= total) {
+      wait_prerequisite();
+      return;
     }
-    total += part;
+    u0 = (int)first;
+    u1 = (int)min64(first + chunk, total);
+    ld.seek(p, cum, u0);
   }
-  if (blockIdx.x == 0 && threadIdx.x == 0) p.space.cum[count] = total;
-  __syncthreads();
-
-  const int chunk = split_chunk(total, (int)gridDim.x);
-  const int64_t first = (int64_t)blockIdx.x * chunk;
-  if (first >= total) return;
-  const int u0 = (int)first, u1 = (int)min64(first + chunk, total);
 
   char *ring = smem + warp * Shape::kStages * Shape::kStage;
   const uint32_t ring_addr = smem_addr(ring);
@@ -106,8 +126,7 @@ __global__ void __launch_bounds__(kSplitWarps * 32) attend_split_kernel(const __
   float2 *ml = reinterpret_cast<float2 *>(smem + Shape::kRing + Shape::kJoin);
 
   // loads: lanes 0..15 own one key each
-  Cursor<N> ld;
-  ld.seek(p, cum, u0);
+  Cursor<S> at = ld;
   int ld_u = u0, ld_key = 0, ld_page = -1;
   bool ld_sees = false;
   auto look_up = [&] {  // the page of this lane's key, one unit ahead of its copy
@@ -115,7 +134,7 @@ __global__ void __launch_bounds__(kSplitWarps * 32) attend_split_kernel(const __
     ld_sees = ld.keys.any_sees(ld_key);
     ld_page = ld_sees ? p.seqs.pages(ld.s)[div_by(ld_key, p.pools.page_size)] : -1;
   };
-  look_up();
+  if (u0 < u1) look_up();
   auto load_next = [&](int stage) {
     if (ld_u < u1) {
       const char *row = nullptr;
@@ -152,8 +171,6 @@ __global__ void __launch_bounds__(kSplitWarps * 32) attend_split_kernel(const __
 #pragma unroll
   for (int i = 0; i < Shape::kStages - 1; ++i) load_next(i);
 
-  Cursor<N> at;
-  at.seek(p, cum, u0);
   int stage = 0, seg_j0 = 0;
   bool fresh = true, first_segment = true;
   uint32_t qf[D / 16][4];
@@ -264,7 +281,7 @@ __global__ void __launch_bounds__(kSplitWarps * 32) attend_split_kernel(const __
     __syncwarp();
     stage = stage + 1 == Shape::kStages ? 0 : stage + 1;
 
-    const bool tile_ends = at.j + 1 == at.keys.n_tiles;
+    const bool tile_ends = kWhole ? u + 1 == u1 : at.j + 1 == at.keys.n_tiles;
     if (!tile_ends && u + 1 < u1) {
       ++at.j;
       continue;
@@ -300,30 +317,36 @@ __global__ void __launch_bounds__(kSplitWarps * 32) attend_split_kernel(const __
         o[n][2 * r + 1] *= mine;
       }
     }
-    auto each = [&](float *buf, bool put) {
+    auto each = [&](int columns, float *buf, bool put) {
 #pragma unroll
-      for (int n = 0; n < D / 8; ++n)
+      for (int n = 0; n < D / 16; ++n)
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
           float2 *q = reinterpret_cast<float2 *>(buf + (n * 32 + lane) * 4 + 2 * r);
+          float *mine = o[columns * (D / 16) + n] + 2 * r;
           if (put) {
-            *q = make_float2(o[n][2 * r], o[n][2 * r + 1]);
+            *q = make_float2(mine[0], mine[1]);
           } else {
-            o[n][2 * r] += q->x;
-            o[n][2 * r + 1] += q->y;
+            mine[0] += q->x;
+            mine[1] += q->y;
           }
         }
     };
-    if (warp >= 2) each(join + (warp - 2) * kSplitRows * D, true);
-    __syncthreads();
-    if (warp < 2) each(join + warp * kSplitRows * D, false);
-    if (warp == 1) each(join + kSplitRows * D, true);
-    __syncthreads();
+    float *const upper = join + kSplitRows * D / 2;
+#pragma unroll
+    for (int columns = 0; columns < 2; ++columns) {
+      if (warp >= 2) each(columns, warp == 2 ? join : upper, true);
+      __syncthreads();
+      if (warp < 2) each(columns, warp == 0 ? join : upper, false);
+      if (warp == 1) each(columns, upper, true);
+      __syncthreads();
+      if (warp == 0) each(columns, upper, false);
+      __syncthreads();
+    }
     if (warp == 0) {
-      each(join + kSplitRows * D, false);
-      const bool complete = tile_ends && seg_j0 == 0;
+      const bool complete = kWhole || (tile_ends && seg_j0 == 0);
       const int group = p.io.group.d, rows = at.nq * group;
-      const int64_t slot = complete ? 2 * (int64_t)gridDim.x + whole_tile(p.seqs, at.s, at.rt, at.h, group, p.tiles_cap)
+      const int64_t slot = complete ? 2 * (int64_t)gridDim.x + at.h * p.tiles_cap + p.seqs.tiles_before(at.s, group) + at.rt
                                     : 2 * (int64_t)blockIdx.x + (first_segment ? 0 : 1);
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
@@ -349,12 +372,28 @@ __global__ void __launch_bounds__(kSplitWarps * 32) attend_split_kernel(const __
         }
       }
     }
-    __syncthreads();
     first_segment = false;
     fresh = true;
     if (u + 1 < u1) at.advance(p);
   }
   cp_async_wait<0>();
+  if constexpr (kWhole) {
+    if (u0 == u1 && warp == 0) {  // no key: zeros
+      const int group = p.io.group.d, rows = at.nq * group;
+      for (int r = 0; r < kSplitRows; ++r) {
+        const int row = at.rt * kSplitRows + r;
+        if (row >= rows) break;
+        const int i = div_by(row, p.io.group), head = at.h * group + row - i * group;
+        const int64_t token = p.seqs.q_begin(at.s) + i;
+        if (lane < D / 8)
+          *reinterpret_cast<uint4 *>(p.io.out + token * p.io.out_stride + (int64_t)head * Shape::kRow + lane * 16) =
+              make_uint4(0, 0, 0, 0);
+        if (p.io.lse != nullptr && lane == 0) p.io.lse[token * p.io.q_heads + head] = -INFINITY;
+      }
+    }
+  }
+  // a pass before this one, on which the joining kernel also depends
+  wait_prerequisite();
 }
 
 }  // namespace cpkv

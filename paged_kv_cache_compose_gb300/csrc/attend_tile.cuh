@@ -124,6 +124,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) attend_tile_kernel(const __gr
   char *q_smem = smem, *k_smem = smem + Shape::kQ, *v_smem = k_smem + kStages * Shape::kOperand;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   int32_t *status = p.seqs.status;
+  release_dependents();  // later passes of the call; the joining kernel waits for this one
 
   // this block's item: the last row tiles first, which see the most keys
   const int splits = p.space.splits;

@@ -205,26 +205,31 @@ class PagedCache:
         self.d_status = torch.zeros(1, dtype=torch.int32, device=self.device)
         self._workspaces = {}  # by stream
         self._outgrown = []  # a captured graph may still use them
+        self._scale = self.key_dim ** -0.5
+        # the current stream's handle: torch's own accessor where it has one (a twentieth of current_stream())
+        self._current = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
-    def _stream(self, stream):
-        return torch.cuda.current_stream(self.device) if stream is None else stream
+    def _stream(self, stream) -> int:
+        if stream is not None:
+            return stream if type(stream) is int else stream.cuda_stream
+        if self._current is not None:
+            return self._current(self.device.index)
+        return torch.cuda.current_stream(self.device).cuda_stream
 
-    def _with_workspace(self, stream, call, size):
-        """``call(workspace)``, with a larger workspace where the call asks for one."""
-        key = stream.cuda_stream
-        workspace = self._workspaces.get(key)
-        try:
-            return call(workspace)
-        except cpkv.CpkvError as e:
-            need = size() if e.code in (cpkv.CPKV_ERR_CAPACITY, cpkv.CPKV_ERR_ARG) else 0
-            if need <= (0 if workspace is None else workspace.numel()):
-                raise
-        with torch.cuda.stream(stream):
-            grown = torch.empty(need + need // 4, dtype=torch.uint8, device=self.device)
+    def _grow(self, stream: int, need: int, error):
+        """A larger workspace after ``error``, or the error where that was not its cause."""
+        workspace = self._workspaces.get(stream)
+        if need <= (0 if workspace is None else workspace.numel()):
+            raise error
         if workspace is not None:
             self._outgrown.append(workspace)
-        self._workspaces[key] = grown
-        return call(grown)
+        workspace = self._workspaces[stream] = self._empty((need + need // 4,), torch.uint8, stream)
+        return workspace
+
+    def _empty(self, shape, dtype, stream: int):
+        """Memory of the stream that the call runs on."""
+        with torch.cuda.stream(torch.cuda.ExternalStream(stream, device=self.device)):
+            return torch.empty(shape, dtype=dtype, device=self.device)
 
     def append_rotary(self, k, v, slots, positions, cos_sin, *, q=None, q_out=None, axis_of_freq=None,
                       interleaved=False, stream=None):
@@ -232,24 +237,19 @@ class PagedCache:
         ``positions`` and ``v`` into cache rows ``slots`` (page * page_size +
         offset; negative: padding), ``q`` rotated into ``q_out`` (allocated
         when None), which is returned."""
-        if k.dim() != 3 or k.shape[1] != self.kv_heads or k.shape[2] != self.key_dim or v.dim() != 3 \
-                or v.shape[1] != self.kv_heads or v.shape[2] != self.value_dim:
+        if k.shape[1:] != (self.kv_heads, self.key_dim) or v.shape[1:] != (self.kv_heads, self.value_dim):
             raise cpkv.CpkvError("append_rotary", cpkv.CPKV_ERR_ARG, "k and v: [tokens, kv_heads, dim] of this cache")
+        stream = self._stream(stream)
         if q is not None and q_out is None:
-            with torch.cuda.stream(self._stream(stream)):
-                q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+            q_out = self._empty(q.shape, q.dtype, stream)
         cpkv.cpkv_append_rotary(k, v, slots, positions, cos_sin, table=self.table, d_status=self.d_status, q=q,
                                 q_out=q_out, axis_of_freq=axis_of_freq, interleaved=interleaved, stream=stream)
         return q_out
 
-    def _results(self, q, out, stream):
+    def _check_queries(self, q):
         if q.dim() != 3 or q.shape[2] != self.key_dim or self.value_dim != self.key_dim:
             raise cpkv.CpkvError("attend", cpkv.CPKV_ERR_ARG,
                                  "q: [tokens, heads, key_dim] over a cache of equal key and value widths")
-        if out is None:
-            with torch.cuda.stream(stream):
-                out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        return out
 
     def attend_window(self, q, q_lens, page_table, kv_lens, *, max_kv_len: int, window: int = 0, sinks: int = 0,
                       scale: float | None = None, out=None, lse=None, stream=None):
@@ -257,18 +257,24 @@ class PagedCache:
         (None: one each) over its ``kv_lens[b]`` rows, those within ``window``
         and the first ``sinks``.  Returns ``out``; ``lse`` (float32 [tokens,
         heads]) is written when given."""
+        self._check_queries(q)
         stream = self._stream(stream)
-        out = self._results(q, out, stream)
-        scale = self.key_dim ** -0.5 if scale is None else scale
-
-        def call(workspace):
-            cpkv.cpkv_attend_window(q, q_lens, page_table, kv_lens, table=self.table, kv_heads=self.kv_heads,
-                                    max_kv_len=max_kv_len, window=window, sinks=sinks, scale=scale, out=out, lse=lse,
-                                    workspace=workspace, d_status=self.d_status, stream=stream)
-
-        self._with_workspace(stream, call, lambda: cpkv.cpkv_attend_window_workspace_bytes(
-            kv_lens.shape[0], q.shape[1], self.kv_heads, self.key_dim, q_lens, max_kv_len, window, sinks))
-        return out
+        if out is None:
+            out = self._empty(q.shape, q.dtype, stream)
+        if scale is None:
+            scale = self._scale
+        workspace = self._workspaces.get(stream)
+        while True:
+            try:
+                cpkv.cpkv_attend_window(q, q_lens, page_table, kv_lens, table=self.table, kv_heads=self.kv_heads,
+                                        max_kv_len=max_kv_len, window=window, sinks=sinks, scale=scale, out=out,
+                                        lse=lse, workspace=workspace, d_status=self.d_status, stream=stream)
+                return out
+            except cpkv.CpkvError as e:
+                if e.code != cpkv.CPKV_ERR_CAPACITY:
+                    raise
+                workspace = self._grow(stream, cpkv.cpkv_attend_window_workspace_bytes(
+                    kv_lens.shape[0], q.shape[1], self.kv_heads, self.key_dim, q_lens, max_kv_len, window, sinks), e)
 
     def attend_shared(self, q, group_sizes, prefix_lens, prefix_pages, page_table, suffix_lens, *,
                       max_suffix_len: int, scale: float | None = None, out=None, lse=None, stream=None):
@@ -276,16 +282,23 @@ class PagedCache:
         heads, dim] over each group's shared prefix (``prefix_pages``, CSR by
         group) and each request's own ``suffix_lens[b]`` rows.  Returns
         ``out``; ``lse`` as in ``attend_window``."""
+        self._check_queries(q)
         stream = self._stream(stream)
-        out = self._results(q, out, stream)
-        scale = self.key_dim ** -0.5 if scale is None else scale
-
-        def call(workspace):
-            cpkv.cpkv_attend_shared(q, group_sizes, prefix_lens, prefix_pages, page_table, suffix_lens,
-                                    table=self.table, kv_heads=self.kv_heads, max_suffix_len=max_suffix_len,
-                                    scale=scale, out=out, lse=lse, workspace=workspace, d_status=self.d_status,
-                                    stream=stream)
-
-        self._with_workspace(stream, call, lambda: cpkv.cpkv_attend_shared_workspace_bytes(
-            suffix_lens.shape[0], q.shape[1], self.kv_heads, self.key_dim, group_sizes, prefix_lens, max_suffix_len))
-        return out
+        if out is None:
+            out = self._empty(q.shape, q.dtype, stream)
+        if scale is None:
+            scale = self._scale
+        workspace = self._workspaces.get(stream)
+        while True:
+            try:
+                cpkv.cpkv_attend_shared(q, group_sizes, prefix_lens, prefix_pages, page_table, suffix_lens,
+                                        table=self.table, kv_heads=self.kv_heads, max_suffix_len=max_suffix_len,
+                                        scale=scale, out=out, lse=lse, workspace=workspace, d_status=self.d_status,
+                                        stream=stream)
+                return out
+            except cpkv.CpkvError as e:
+                if e.code != cpkv.CPKV_ERR_CAPACITY:
+                    raise
+                workspace = self._grow(stream, cpkv.cpkv_attend_shared_workspace_bytes(
+                    suffix_lens.shape[0], q.shape[1], self.kv_heads, self.key_dim, group_sizes, prefix_lens,
+                    max_suffix_len), e)

@@ -63,12 +63,13 @@ def test_append_refusals(lib, changed, code):
 
 def window_args():
     return Args(B=2, ps=16, cp=2, dtype=cpkv.BF16, hq=4, hkv=2, d=64, row=512, k_off=0, v_off=256, q_lens=np.array([1, 2], np.int32),
-                max_kv=64, pools=pools(), caps=np.array([4, 4], np.int64), table=FAKE, stride=4, kv_lens=FAKE, q=FAKE, qs=256, scale=0.1,
+                max_kv=64, pools=pools(), caps=np.array([4, 4], np.int64), table=FAKE, stride=4, kv_lens=FAKE, tokens=3, q=FAKE, qs=256, scale=0.1,
                 window=8, sinks=2, out=FAKE, os=256, lse=None, ws=FAKE, ws_bytes=1 << 40, flags=0, status=FAKE, stream=None)
 
 
 @pytest.mark.parametrize("changed, code", [
-    (dict(B=0), cpkv.CPKV_OK), (dict(q_lens=np.zeros(2, np.int32)), cpkv.CPKV_OK),
+    (dict(B=0, tokens=0), cpkv.CPKV_OK), (dict(q_lens=np.zeros(2, np.int32), tokens=0), cpkv.CPKV_OK),
+    (dict(tokens=4), cpkv.CPKV_ERR_ARG), (dict(tokens=0), cpkv.CPKV_ERR_ARG),
     (dict(B=-1), cpkv.CPKV_ERR_ARG), (dict(B=1025, q_lens=None), cpkv.CPKV_ERR_LIMIT), (dict(q_lens=np.array([1, -1], np.int32)), cpkv.CPKV_ERR_ARG),
     (dict(ps=-4), cpkv.CPKV_ERR_ARG), (dict(dtype=5), cpkv.CPKV_ERR_ARG), (dict(hq=3), cpkv.CPKV_ERR_ARG), (dict(hkv=0), cpkv.CPKV_ERR_ARG),
     (dict(d=96), cpkv.CPKV_ERR_LIMIT), (dict(d=128), cpkv.CPKV_ERR_ARG), (dict(max_kv=-1), cpkv.CPKV_ERR_ARG),
@@ -77,7 +78,7 @@ def window_args():
     (dict(q=None), cpkv.CPKV_ERR_ARG), (dict(q=260), cpkv.CPKV_ERR_ARG), (dict(qs=252), cpkv.CPKV_ERR_ARG), (dict(os=128), cpkv.CPKV_ERR_ARG),
     (dict(out=None), cpkv.CPKV_ERR_ARG), (dict(scale=float("nan")), cpkv.CPKV_ERR_ARG), (dict(scale=float("inf")), cpkv.CPKV_ERR_ARG),
     (dict(ws=None), cpkv.CPKV_ERR_ARG), (dict(ws=264), cpkv.CPKV_ERR_ARG), (dict(ws_bytes=16), cpkv.CPKV_ERR_CAPACITY),
-    (dict(flags=1), cpkv.CPKV_ERR_ARG), (dict(status=None), cpkv.CPKV_ERR_ARG), (dict(v_off=264), cpkv.CPKV_ERR_ARG),
+    (dict(ws=None, ws_bytes=0), cpkv.CPKV_ERR_CAPACITY), (dict(flags=1), cpkv.CPKV_ERR_ARG), (dict(status=None), cpkv.CPKV_ERR_ARG), (dict(v_off=264), cpkv.CPKV_ERR_ARG),
     (dict(k_off=272), cpkv.CPKV_ERR_ARG), (dict(pools=None), cpkv.CPKV_ERR_ARG),
 ], ids=str)
 def test_window_refusals(lib, changed, code):
@@ -86,7 +87,7 @@ def test_window_refusals(lib, changed, code):
 
 def shared_args():
     return Args(B=3, groups=2, ps=16, cp=2, dtype=cpkv.FP16, hq=4, hkv=2, d=64, row=512, k_off=0, v_off=256, sizes=np.array([1, 2], np.int32),
-                prefix=np.array([32, 0], np.int32), max_suffix=64, pools=pools(), caps=np.array([4, 4], np.int64), prefix_pages=FAKE,
+                prefix=np.array([32, 0], np.int32), max_suffix=64, pools=pools(), caps=np.array([4, 4], np.int64), prefix_pages=FAKE, n_prefix=2,
                 table=FAKE, stride=4, suffix=FAKE, q=FAKE, qs=256, scale=0.1, out=FAKE, os=256, lse=None, ws=FAKE, ws_bytes=1 << 40, flags=0,
                 status=FAKE, stream=None)
 
@@ -95,7 +96,7 @@ def shared_args():
     (dict(B=0, groups=0), cpkv.CPKV_OK), (dict(B=2), cpkv.CPKV_ERR_ARG), (dict(groups=1), cpkv.CPKV_ERR_ARG), (dict(groups=-1), cpkv.CPKV_ERR_ARG),
     (dict(sizes=None), cpkv.CPKV_ERR_ARG), (dict(sizes=np.array([4, -1], np.int32)), cpkv.CPKV_ERR_ARG),
     (dict(prefix=np.array([31, 0], np.int32)), cpkv.CPKV_ERR_UNALIGNED_PREFIX), (dict(prefix=np.array([-16, 0], np.int32)), cpkv.CPKV_ERR_ARG),
-    (dict(prefix_pages=None), cpkv.CPKV_ERR_ARG), (dict(max_suffix=65), cpkv.CPKV_ERR_CAPACITY), (dict(d=80), cpkv.CPKV_ERR_LIMIT),
+    (dict(prefix_pages=None), cpkv.CPKV_ERR_ARG), (dict(n_prefix=1), cpkv.CPKV_ERR_CAPACITY), (dict(max_suffix=65), cpkv.CPKV_ERR_CAPACITY), (dict(d=80), cpkv.CPKV_ERR_LIMIT),
     (dict(suffix=None), cpkv.CPKV_ERR_ARG), (dict(ws_bytes=64), cpkv.CPKV_ERR_CAPACITY), (dict(ws=None), cpkv.CPKV_ERR_ARG),
     (dict(flags=8), cpkv.CPKV_ERR_ARG), (dict(status=None), cpkv.CPKV_ERR_ARG), (dict(q=None), cpkv.CPKV_ERR_ARG),
     (dict(B=1025, sizes=np.array([1024, 1], np.int32)), cpkv.CPKV_ERR_LIMIT), (dict(hq=5), cpkv.CPKV_ERR_ARG),
@@ -106,7 +107,8 @@ def test_shared_refusals(lib, changed, code):
 
 def test_workspace_sizes(lib):
     small = cpkv.cpkv_attend_window_workspace_bytes(1, 4, 1, 64, None, 100)
-    assert 0 < small < cpkv.cpkv_attend_window_workspace_bytes(64, 32, 8, 128, None, 100_000)
+    assert small == 0  # few keys: whole tiles, nothing to join
+    assert 0 < cpkv.cpkv_attend_window_workspace_bytes(64, 32, 8, 128, None, 100_000)
     # a window bounds the work of long requests, and so the workspace
     assert cpkv.cpkv_attend_window_workspace_bytes(1, 4, 1, 64, None, 100_000, window=256) < \
         cpkv.cpkv_attend_window_workspace_bytes(1, 4, 1, 64, None, 100_000)
