@@ -53,20 +53,20 @@ int64_t round_up(int64_t n, int64_t to) { return ceil_div(n, to) * to; }
 
 // Bounds of a split pass, from host lengths.
 struct SplitBounds {
-  int64_t tokens = 0, tiles_cap = 0, units = 0, max_tiles = 0;
+  int64_t tokens = 0, tiles_cap = 0, units = 0, max_tiles = 0;  // tiles, units: per key/value head
   int grid_cap = 1;
 
-  void add(int64_t nq, int64_t max_kv, int group, int kv_heads, int window, int sinks) {
+  void add(int64_t nq, int64_t max_kv, int group, int window, int sinks) {
     int64_t tiles = ceil_div(max_kv, kSplitTile);
     if (window > 0) tiles = std::min<int64_t>(tiles, ceil_div((int64_t)sinks, kSplitTile) + ((int64_t)window + nq) / kSplitTile + 2);
-    units += ceil_div(nq * group, kSplitRows) * kv_heads * tiles;
+    units += ceil_div(nq * group, kSplitRows) * tiles;
     max_tiles = std::max<int64_t>(max_tiles, tiles);
     tokens += nq;
     tiles_cap += ceil_div(nq * group, kSplitRows) + 1;
   }
-  int finish(int group) {
-    if (units > INT32_MAX || tokens * group > INT32_MAX) return CPKV_ERR_LIMIT;
-    grid_cap = (int)std::min<int64_t>(kSplitMaxGrid, units > 0 ? units : 1);
+  int finish(int group, int kv_heads) {
+    if (units > INT32_MAX || tokens * group > INT32_MAX || kv_heads > kSplitMaxGrid) return CPKV_ERR_LIMIT;
+    grid_cap = kv_heads * (int)std::min<int64_t>(kSplitMaxGrid / kv_heads, units > 0 ? units : 1);
     return CPKV_OK;
   }
   int64_t slots(int kv_heads, bool direct) const { return 2 * (int64_t)grid_cap + (direct ? 0 : tiles_cap * kv_heads); }
@@ -143,7 +143,7 @@ int window_plan(WindowPlan *w, const HeadArgs &a, int B, const int32_t *h_q_lens
   for (int s = 0; s < B; ++s) {
     const int64_t nq = h_q_lens == nullptr ? 1 : h_q_lens[s];
     if (nq < 0) return CPKV_ERR_ARG;
-    w->split.add(nq, max_kv, group, a.kv_heads, window, sinks);
+    w->split.add(nq, max_kv, group, window, sinks);
     w->tile.add(nq, max_kv, group, window, sinks);
   }
   w->few = few_rows(w->tile.max_rows);
@@ -151,7 +151,7 @@ int window_plan(WindowPlan *w, const HeadArgs &a, int B, const int32_t *h_q_lens
   bool uniform = B > 0;
   for (int s = 1; s < B && h_q_lens != nullptr; ++s) uniform &= h_q_lens[s] == h_q_lens[0];
   w->whole = w->few && uniform && w->split.max_tiles <= kWholeUnits;
-  const int rc = w->few ? w->split.finish(group) : w->tile.finish(a.kv_heads);
+  const int rc = w->few ? w->split.finish(group, a.kv_heads) : w->tile.finish(a.kv_heads);
   w->bytes = w->whole ? 0
              : w->few ? w->split.bytes(B, a.kv_heads, a.head_dim, true)
                       : w->tile.bytes(a.kv_heads, a.head_dim, true);
@@ -180,9 +180,9 @@ int shared_plan(SharedPlan *w, const HeadArgs &a, int B, int n_groups, const int
   if (w->prefix_pages > INT32_MAX) return CPKV_ERR_LIMIT;
   w->few = few_rows(w->tile.max_rows);
   for (int g = 0; g < n_groups && w->few; ++g)
-    w->split.add(h_group_sizes[g], h_prefix_lens[g], group, a.kv_heads, 0, 0);
-  for (int b = 0; b < B; ++b) w->split.add(1, max_suffix, group, a.kv_heads, 0, 0);
-  int rc = w->split.finish(group);
+    w->split.add(h_group_sizes[g], h_prefix_lens[g], group, 0, 0);
+  for (int b = 0; b < B; ++b) w->split.add(1, max_suffix, group, 0, 0);
+  int rc = w->split.finish(group, a.kv_heads);
   if (!w->few && rc == CPKV_OK) rc = w->tile.finish(a.kv_heads);
   w->prefix_bytes = w->few ? 0 : w->tile.bytes(a.kv_heads, a.head_dim, false);
   w->bytes = w->prefix_bytes + w->split.bytes(w->few ? n_groups + B : B, a.kv_heads, a.head_dim, false);
@@ -212,7 +212,9 @@ int split_pass(SplitParams<S> *p, const SplitBounds &b, bool dependent, cudaStre
     if (blocks > INT32_MAX) return CPKV_ERR_LIMIT;
     return launch_kernel(kernel, dim3((unsigned)blocks), dim3(kSplitWarps * 32), smem, dependent, stream, *p);
   }
-  p->space.grid = persistent_grid((const void *)kernel, kSplitWarps * 32, smem, 8, b.grid_cap);
+  // as many blocks for every head as stay resident together
+  const int heads = p->io.kv_heads, resident = persistent_grid((const void *)kernel, kSplitWarps * 32, smem, 8, b.grid_cap);
+  p->space.grid = std::max(resident / heads, 1) * heads;
   return launch_kernel(kernel, dim3(p->space.grid), dim3(kSplitWarps * 32), smem, dependent, stream, *p);
 }
 

@@ -229,8 +229,8 @@ constexpr int kSplitRows = 16;
 constexpr int kSplitTile = 64;     // keys of a unit
 constexpr int kSplitMaxGrid = 1024;
 
-// Workspace of a split pass over `count` sequences, in order: cum (units before
-// each sequence and in all), then the slots' (m, l) pairs, then their values.
+// Workspace of a split pass over `count` sequences, in order: cum (units of a
+// head before each sequence and in all), then the slots' (m, l) pairs, then their values.
 // Slots: two per block (its first stretch, and its last when that is another
 // tile's), then one per tile for the tiles that one block holds whole.
 struct SplitSpace {
@@ -240,7 +240,8 @@ struct SplitSpace {
   int grid;
 };
 
-CPKV_DEV int split_chunk(int total, int grid) { return total <= grid ? 1 : (total + grid - 1) / grid; }
+// Units of a cut when a head's `total` are cut into `parts`.
+CPKV_DEV int split_chunk(int total, int parts) { return total <= parts ? 1 : (total + parts - 1) / parts; }
 
 template <typename S>
 struct SplitParams {

@@ -49,50 +49,80 @@ struct RowSum {
   }
 };
 
-// Adds the parts of query head `head` of token i of sequence s; false when the
-// pass has written that row's output itself.
+// Where a pass keeps a query row: found from the call's own inputs, before the
+// pass has ended.
+struct Spot {
+  int s, rt, in_tile, n_tiles;
+};
+
+template <typename S>
+CPKV_DEV Spot find_spot(const SplitSource<S> &src, const AttendIo &io, int s, int i, int g) {
+  const int nq = src.seqs.q_count(s), row = i * (int)io.group.d + g;
+  const KeyRange keys = key_range<kSplitTile>(src.seqs.kv_len(s), nq, 0, nq, src.seqs.causal, src.seqs.window, src.seqs.sinks);
+  return Spot{s, row / kSplitRows, row % kSplitRows, keys.n_tiles};
+}
+
+template <int N>
+CPKV_DEV Spot find_spot(const TileSource<N> &src, const AttendIo &io, int s, int i, int g) {
+  const int row = i * (int)io.group.d + g;
+  return Spot{s, row / kTileRows, row % kTileRows, 0};
+}
+
+// Adds the parts of a row of key/value head h; false when the pass has written
+// that row's output itself.
 template <int D, typename S>
-CPKV_DEV bool add_parts(RowSum<D> *sum, const SplitSource<S> &src, const AttendIo &io, int s, int i, int head, int lane) {
-  const int group = io.group.d, h = div_by(head, io.group), g = head - h * group;
-  const int nq = src.seqs.q_count(s), kv = src.seqs.kv_len(s);
-  const KeyRange keys = key_range<kSplitTile>(kv, nq, 0, nq, src.seqs.causal, src.seqs.window, src.seqs.sinks);
-  if (keys.n_tiles == 0) return true;
-  const int row = i * group + g, rt = row / kSplitRows, row_tiles = (nq * group + kSplitRows - 1) / kSplitRows;
-  const int in_tile = row - rt * kSplitRows;
-  const int chunk = split_chunk(src.space.cum[src.seqs.count], src.space.grid);
-  const int begin = src.space.cum[s] + (h * row_tiles + rt) * keys.n_tiles, end = begin + keys.n_tiles;
+CPKV_DEV bool add_parts(RowSum<D> *sum, const SplitSource<S> &src, const AttendIo &io, const Spot &at, int h, int lane) {
+  if (at.n_tiles == 0) return true;
+  const int chunk = split_chunk(src.space.cum[src.seqs.count], src.space.grid / io.kv_heads);
+  const int begin = src.space.cum[at.s] + at.rt * at.n_tiles, end = begin + at.n_tiles;
   const int c0 = begin / chunk, c1 = (end - 1) / chunk;
   if (c0 == c1) {
     if (src.direct) return false;
-    const int64_t slot = 2 * (int64_t)src.space.grid + h * src.tiles_cap + src.seqs.tiles_before(s, group) + rt;
-    sum->add(src.space.ml, src.space.o, 1, lane, [&](int) { return slot * kSplitRows + in_tile; });
+    const int64_t slot = 2 * (int64_t)src.space.grid + h * src.tiles_cap + src.seqs.tiles_before(at.s, io.group.d) + at.rt;
+    sum->add(src.space.ml, src.space.o, 1, lane, [&](int) { return slot * kSplitRows + at.in_tile; });
     return true;
   }
-  // the tile's stretch is the last of block c0 unless it begins there, and the first of the others
-  const int64_t first = 2 * (int64_t)c0 + (begin == c0 * chunk ? 0 : 1);
-  sum->add(src.space.ml, src.space.o, c1 - c0 + 1, lane,
-           [&](int k) { return (k == 0 ? first : 2 * (int64_t)(c0 + k)) * kSplitRows + in_tile; });
+  // the tile's stretch is the last of cut c0 unless it begins there, and the first of the others
+  const int late = begin == c0 * chunk ? 0 : 1;
+  sum->add(src.space.ml, src.space.o, c1 - c0 + 1, lane, [&](int k) {
+    return (2 * ((int64_t)(c0 + k) * io.kv_heads + h) + (k == 0 ? late : 0)) * kSplitRows + at.in_tile;
+  });
   return true;
 }
 
 template <int D, int N>
-CPKV_DEV bool add_parts(RowSum<D> *sum, const TileSource<N> &src, const AttendIo &io, int s, int i, int head, int lane) {
-  const int group = io.group.d, h = div_by(head, io.group), row = i * group + head - h * group, rt = row / kTileRows;
-  const int64_t item = (int64_t)(src.cu_tiles[s] + rt) * io.kv_heads + h;
-  const int64_t at = item * src.space.splits * kTileRows + row - rt * kTileRows;
-  sum->add(src.space.ml, src.space.o, src.space.splits, lane, [&](int k) { return at + (int64_t)k * kTileRows; });
+CPKV_DEV bool add_parts(RowSum<D> *sum, const TileSource<N> &src, const AttendIo &io, const Spot &at, int h, int lane) {
+  const int64_t item = (int64_t)(src.cu_tiles[at.s] + at.rt) * io.kv_heads + h;
+  const int64_t first = item * src.space.splits * kTileRows + at.in_tile;
+  sum->add(src.space.ml, src.space.o, src.space.splits, lane, [&](int k) { return first + (int64_t)k * kTileRows; });
   return true;
 }
 
 struct NoSource {};
 
+// The places of a query row in a pass.
+struct Spots {
+  Spot at[2];
+  int count;
+};
+
+template <typename Source>
+CPKV_DEV Spots find_spots(const Source &src, const AttendIo &io, int token, int g) {
+  int s[2], i[2];
+  Spots r;
+  r.count = src.seqs.places(token, s, i);
+#pragma unroll
+  for (int k = 0; k < 2; ++k)
+    if (k < r.count) r.at[k] = find_spot(src, io, s[k], i[k], g);
+  return r;
+}
+
 // All parts of a row that a pass has; false when the pass wrote the row itself.
 template <int D, typename Source>
-CPKV_DEV bool add_all(RowSum<D> *sum, const Source &src, const AttendIo &io, int token, int head, int lane) {
-  int s[2], i[2];
-  const int n = src.seqs.places(token, s, i);
-  for (int k = 0; k < n; ++k)
-    if (!add_parts(sum, src, io, s[k], i[k], head, lane)) return false;
+CPKV_DEV bool add_all(RowSum<D> *sum, const Source &src, const AttendIo &io, const Spots &spots, int h, int lane) {
+#pragma unroll
+  for (int k = 0; k < 2; ++k)
+    if (k < spots.count && !add_parts(sum, src, io, spots.at[k], h, lane)) return false;
   return true;
 }
 
@@ -112,10 +142,14 @@ __global__ void __launch_bounds__(128) attend_join_kernel(const __grid_constant_
   const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
   if (row >= p.rows) return;
   const int token = (int)(row / p.io.q_heads), head = (int)(row - (int64_t)token * p.io.q_heads);
-  RowSum<D> sum;
+  const int h = div_by(head, p.io.group), g = head - h * (int)p.io.group.d;
+  const Spots a = find_spots(p.a, p.io, token, g);
+  Spots b;
+  if constexpr (!std::is_same<B, NoSource>::value) b = find_spots(p.b, p.io, token, g);
   wait_prerequisite();
-  if (!add_all(&sum, p.a, p.io, token, head, lane)) return;
-  if constexpr (!std::is_same<B, NoSource>::value) add_all(&sum, p.b, p.io, token, head, lane);
+  RowSum<D> sum;
+  if (!add_all(&sum, p.a, p.io, a, h, lane)) return;
+  if constexpr (!std::is_same<B, NoSource>::value) add_all(&sum, p.b, p.io, b, h, lane);
   const float inv = row_scale(sum.l);
   char *dst = p.io.out + token * p.io.out_stride + (int64_t)head * D * 2 + lane * (D / 16);
   if constexpr (D == 128) {

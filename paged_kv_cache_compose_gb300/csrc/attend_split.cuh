@@ -5,10 +5,16 @@
 // Bytes bound it: 16 packed rows do 4 D * 16 operations on the 4 D bytes of a
 // key and its value, far below what the matrix instructions give, so what
 // counts is bytes in flight.  Work is counted in units of 64 keys of one tile
-// (sequence, key/value head, 16 rows); all units of the call form one line that
-// is cut evenly over the blocks, whatever the lengths are, and a block's warps
-// each own 16 keys of every unit with a cp.async ring of their own, so that no
-// block-wide barrier stands inside a stretch.  Where every sequence has few keys
+// (sequence, 16 rows); all units of a key/value head form one line that is cut
+// evenly over the head's blocks, whatever the lengths are, and a block's warps each
+// own 16 keys of every unit with a cp.async ring of their own, so that no block-wide
+// barrier stands inside a stretch.  The lines of all heads are cut alike and
+// neighbouring blocks hold the same stretch of different heads: a token's heads lie
+// side by side in its row, and read together they cost DRAM one page opening
+// (64 requests of 4100 keys, 8 heads of 64: 120 us when a block's stretch ran from
+// one head into the next, 106 us so).  Warps, not stages, hide the rest: two stages
+// and as many blocks as registers allow take 100 us, four stages and three blocks 106.  Where every
+// sequence has few keys
 // (kWhole) a block takes one whole tile instead and nothing is left to join.
 #pragma once
 
@@ -23,7 +29,8 @@ template <int D>
 struct SplitShape {
   static constexpr int kRow = D * 2;                       // bytes of a key (or value) vector
   static constexpr int kStage = kWarpKeys * kRow * 2;      // keys, then values
-  static constexpr int kStages = D == 128 ? 3 : 4;
+  static constexpr int kStages = 2;
+  static constexpr int kBlocks = D == 128 ? 3 : 5;         // blocks to an SM
   static constexpr int kRing = kSplitWarps * kStages * kStage;
   static constexpr int kJoin = kSplitRows * D * 4;         // half the columns of two warps while a tile's parts are joined
   static constexpr int kSmem = kRing + kJoin + kSplitWarps * kSplitRows * 8;
@@ -32,7 +39,7 @@ struct SplitShape {
 // A position on the line of units.
 template <typename S>
 struct Cursor {
-  int s, h, rt, j, row_tiles;
+  int s, rt, j, row_tiles;
   int nq, kv;
   KeyRange keys;
 
@@ -46,10 +53,8 @@ struct Cursor {
   CPKV_DEV void seek(const SplitParams<S> &p, const int *cum, int u) {
     enter(p, upper_index(cum, p.seqs.count, u));
     const int local = u - cum[s];
-    const int tile = local / keys.n_tiles;
-    j = local - tile * keys.n_tiles;
-    h = tile / row_tiles;
-    rt = tile - h * row_tiles;
+    rt = local / keys.n_tiles;
+    j = local - rt * keys.n_tiles;
   }
   // To the next unit of the line; there must be one.
   CPKV_DEV void advance(const SplitParams<S> &p) {
@@ -57,8 +62,6 @@ struct Cursor {
     j = 0;
     if (++rt < row_tiles) return;
     rt = 0;
-    if (++h < p.io.kv_heads) return;
-    h = 0;
     do {
       enter(p, s + 1);
     } while (keys.n_tiles == 0 || row_tiles == 0);
@@ -66,7 +69,7 @@ struct Cursor {
 };
 
 template <typename T, int D, typename S, bool kWhole>
-__global__ void __launch_bounds__(kSplitWarps * 32) attend_split_kernel(const __grid_constant__ SplitParams<S> p) {
+__global__ void __launch_bounds__(kSplitWarps * 32, SplitShape<D>::kBlocks) attend_split_kernel(const __grid_constant__ SplitParams<S> p) {
   using Shape = SplitShape<D>;
   extern __shared__ __align__(128) char smem[];
   __shared__ int scan_scratch[33];
@@ -75,15 +78,15 @@ __global__ void __launch_bounds__(kSplitWarps * 32) attend_split_kernel(const __
   const int count = p.seqs.count;
 
   release_dependents();  // the joining kernel, which waits for this one
+  const int head = (int)blockIdx.x % p.io.kv_heads;  // key/value head
   Cursor<S> ld;
   int u0, u1;
   if constexpr (kWhole) {
-    const int tile = (int)blockIdx.x / p.row_tiles;
-    ld.enter(p, tile / p.io.kv_heads);
-    ld.h = tile % p.io.kv_heads;
-    ld.rt = (int)blockIdx.x % p.row_tiles;
+    const int tile = (int)blockIdx.x / p.io.kv_heads;
+    ld.enter(p, tile / p.row_tiles);
+    ld.rt = tile % p.row_tiles;
     ld.j = 0;
-    if (ld.h == 0 && ld.rt == 0 && threadIdx.x == 0 && p.seqs.kv_len_bad(ld.s))
+    if (head == 0 && ld.rt == 0 && threadIdx.x == 0 && p.seqs.kv_len_bad(ld.s))
       raise_status(p.seqs.status, CPKV_STATUS_OUT_CAPACITY);
     u0 = 0;
     u1 = ld.keys.n_tiles;
@@ -96,7 +99,7 @@ __global__ void __launch_bounds__(kSplitWarps * 32) attend_split_kernel(const __
       if (s < count) {
         Cursor<S> c;
         c.enter(p, s);
-        mine = c.keys.n_tiles * c.row_tiles * p.io.kv_heads;
+        mine = c.keys.n_tiles * c.row_tiles;
         if (blockIdx.x == 0 && p.seqs.kv_len_bad(s)) raise_status(p.seqs.status, CPKV_STATUS_OUT_CAPACITY);
       }
       int part;
@@ -109,8 +112,8 @@ __global__ void __launch_bounds__(kSplitWarps * 32) attend_split_kernel(const __
     }
     if (blockIdx.x == 0 && threadIdx.x == 0) p.space.cum[count] = total;
     __syncthreads();
-    const int chunk = split_chunk(total, (int)gridDim.x);
-    const int64_t first = (int64_t)blockIdx.x * chunk;
+    const int chunk = split_chunk(total, (int)gridDim.x / p.io.kv_heads);
+    const int64_t first = (int64_t)((int)blockIdx.x / p.io.kv_heads) * chunk;
     if (first >= total) {
       wait_prerequisite();
       return;
@@ -149,8 +152,8 @@ __global__ void __launch_bounds__(kSplitWarps * 32) attend_split_kernel(const __
       constexpr int kLanes = D / 8, kRows = 32 / kLanes;  // lanes of a vector, keys of one warp-wide copy
       const int c = lane % kLanes;
       const uint32_t dst = ring_addr + stage * Shape::kStage;
-      const int64_t k_at = p.io.k_off + (int64_t)ld.h * Shape::kRow + c * 16;
-      const int64_t v_at = p.io.v_off + (int64_t)ld.h * Shape::kRow + c * 16;
+      const int64_t k_at = p.io.k_off + (int64_t)head * Shape::kRow + c * 16;
+      const int64_t v_at = p.io.v_off + (int64_t)head * Shape::kRow + c * 16;
 #pragma unroll
       for (int i = 0; i < kWarpKeys / kRows; ++i) {
         const int key = i * kRows + lane / kLanes;
@@ -198,7 +201,7 @@ __global__ void __launch_bounds__(kSplitWarps * 32) attend_split_kernel(const __
         const bool in = row < rows;
         const int i = div_by(row, p.io.group), g = row - i * group;
         mask[r] = row_mask(at.kv, at.nq, i, p.seqs.causal, p.seqs.window, p.seqs.sinks);
-        const char *src = p.io.q + (q0 + i) * p.io.q_stride + ((int64_t)at.h * group + g) * Shape::kRow + (lane & 3) * 4;
+        const char *src = p.io.q + (q0 + i) * p.io.q_stride + ((int64_t)head * group + g) * Shape::kRow + (lane & 3) * 4;
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
           qf[k][r] = in ? *reinterpret_cast<const uint32_t *>(src + k * 32) : 0u;
@@ -346,7 +349,7 @@ __global__ void __launch_bounds__(kSplitWarps * 32) attend_split_kernel(const __
     if (warp == 0) {
       const bool complete = kWhole || (tile_ends && seg_j0 == 0);
       const int group = p.io.group.d, rows = at.nq * group;
-      const int64_t slot = complete ? 2 * (int64_t)gridDim.x + at.h * p.tiles_cap + p.seqs.tiles_before(at.s, group) + at.rt
+      const int64_t slot = complete ? 2 * (int64_t)gridDim.x + head * p.tiles_cap + p.seqs.tiles_before(at.s, group) + at.rt
                                     : 2 * (int64_t)blockIdx.x + (first_segment ? 0 : 1);
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
@@ -355,14 +358,14 @@ __global__ void __launch_bounds__(kSplitWarps * 32) attend_split_kernel(const __
         if (complete && p.direct) {
           const int i = div_by(row, p.io.group), g = row - i * group;
           const int64_t token = p.seqs.q_begin(at.s) + i;
-          const int head = at.h * group + g;
+          const int q_head = head * group + g;
           const float inv = row_scale(sum[r]);
-          char *dst = p.io.out + token * p.io.out_stride + (int64_t)head * Shape::kRow + (lane & 3) * 4;
+          char *dst = p.io.out + token * p.io.out_stride + (int64_t)q_head * Shape::kRow + (lane & 3) * 4;
 #pragma unroll
           for (int n = 0; n < D / 8; ++n)
             *reinterpret_cast<uint32_t *>(dst + n * 16) = pack2<T>(o[n][2 * r] * inv, o[n][2 * r + 1] * inv);
           if (p.io.lse != nullptr && (lane & 3) == 0)
-            p.io.lse[token * p.io.q_heads + head] = row_lse(big[r], sum[r]);
+            p.io.lse[token * p.io.q_heads + q_head] = row_lse(big[r], sum[r]);
         } else {
           float *dst = p.space.o + (slot * kSplitRows + in_tile) * D + (lane & 3) * 2;
 #pragma unroll
@@ -383,12 +386,12 @@ __global__ void __launch_bounds__(kSplitWarps * 32) attend_split_kernel(const __
       for (int r = 0; r < kSplitRows; ++r) {
         const int row = at.rt * kSplitRows + r;
         if (row >= rows) break;
-        const int i = div_by(row, p.io.group), head = at.h * group + row - i * group;
+        const int i = div_by(row, p.io.group), q_head = head * group + row - i * group;
         const int64_t token = p.seqs.q_begin(at.s) + i;
         if (lane < D / 8)
-          *reinterpret_cast<uint4 *>(p.io.out + token * p.io.out_stride + (int64_t)head * Shape::kRow + lane * 16) =
+          *reinterpret_cast<uint4 *>(p.io.out + token * p.io.out_stride + (int64_t)q_head * Shape::kRow + lane * 16) =
               make_uint4(0, 0, 0, 0);
-        if (p.io.lse != nullptr && lane == 0) p.io.lse[token * p.io.q_heads + head] = -INFINITY;
+        if (p.io.lse != nullptr && lane == 0) p.io.lse[token * p.io.q_heads + q_head] = -INFINITY;
       }
     }
   }
