@@ -305,16 +305,19 @@ TileSource<N> source_of(const TileParams<N> &p) {
   return s;
 }
 
+// Four warps a row while rows are too few to fill the SMs with a warp each.
 template <typename T, int D, typename A, typename B>
 int join_pass(const A &a, const B &b, const AttendIo &io, int64_t rows, cudaStream_t stream) {
-  const int64_t blocks = ceil_div(rows, 4);
-  if (blocks > INT32_MAX) return CPKV_ERR_LIMIT;
   JoinParams<A, B> p = {};
   p.a = a;
   p.b = b;
   p.io = io;
   p.rows = rows;
-  return launch_kernel(attend_join_kernel<T, D, A, B>, dim3((unsigned)blocks), dim3(128), 0, true, stream, p);
+  const bool wide = rows <= (int64_t)device_sm_count() * 16;
+  const int64_t blocks = wide ? rows : ceil_div(rows, 4);
+  if (blocks > INT32_MAX) return CPKV_ERR_LIMIT;
+  auto kernel = wide ? attend_join_kernel<T, D, A, B, 4> : attend_join_kernel<T, D, A, B, 1>;
+  return launch_kernel(kernel, dim3((unsigned)blocks), dim3(128), 0, true, stream, p);
 }
 
 template <int N>
