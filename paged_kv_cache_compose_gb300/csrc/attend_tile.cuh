@@ -1,6 +1,6 @@
-// Attention of many query rows on the tensor core: a block owns 256 packed rows
-// of one sequence and key/value head and goes once over the keys they see, 128
-// at a time, with the running maximum and sum of each row's softmax.
+// Attention of many query rows on the tensor core: an item is 256 packed rows of
+// one sequence and key/value head, which go once over the keys they see (or over one
+// part of them), 128 at a time, with the running maximum and sum of each row's softmax.
 //
 // Two products per 128 keys, 4 * 256 * 128 * D operations on 2 * 128 * D values:
 // the tensor core bounds it at D = 128, the exponentials (one per query and key)
@@ -8,15 +8,20 @@
 // while the tensor core multiplies for the other:
 //   warps 0..3, 4..7   the softmax of tile 0, 1: a thread owns a row.  Scores come
 //                      from tensor memory; weights go back over them, rounded to
-//                      the element type (summed before that).
+//                      the element type (summed after that, beside the products).
 //   warps 8..11        keys and values of the pages to shared memory, 32 keys each:
 //                      as TMA boxes where a page holds 16 rows or more and all 32
 //                      keys are there, else by cp.async with an address per key, so
 //                      pages may have any size and stand in any order.
 //   warp 12            issues the products: scores (queries, keys in shared memory),
 //                      then values (weights in tensor memory), tile by tile.
-// Weights are handed over in two halves of 64 keys: the first half's product runs
-// while the second half's exponentials do.
+//   warp 13            finds the next item while this one runs: the grid has a block
+//                      for every item, and a running block claims blocks that have not
+//                      started (cluster launch control), so long items go first and no
+//                      SM waits for another.
+//   warps 14, 15       the next item's queries, once this one's scores are done.
+// Of an item with at most 128 rows whose results are joined anyway, the two tiles
+// are the same rows over every other 128 keys (two streams), and each leaves a part.
 // Tensor memory (512 columns): scores of the tiles at 0 and 128, outputs at 256
 // and 384.  A row's output is rescaled only when its maximum has risen by more
 // than 2^8 since the last time: weights stay below 2^8, and the sum and the output
@@ -35,12 +40,12 @@ constexpr int kTileKeys = 128;
 constexpr int kLoaders = 128;
 constexpr int kTileThreads = 512;
 // Registers a thread: 512 threads are launched with 128 each, 65536 in all; the
-// softmax holds a row's 128 scores.  256 * 192 + 256 * 64 = 65536.
-constexpr int kSoftmaxRegisters = 192, kOtherRegisters = 64;
+// softmax holds a row's 128 scores.  256 * 216 + 256 * 40 = 65536.
+constexpr int kSoftmaxRegisters = 216, kOtherRegisters = 40;
 constexpr int kTileMaps = 8;  // most pools that TMA maps travel for
 constexpr float kRescaleAt = 8.f;
 constexpr uint64_t kTileWaitNs = 2000000000ull;
-constexpr uint32_t kTileParkNs = 500000;
+constexpr uint32_t kTileParkNs = 20000;
 
 // Slots of a tile pass: [item][split], an item being (row tile of all
 // sequences, key/value head).
@@ -83,33 +88,75 @@ CPKV_DEV int find_tile_seq(const TileParams<N> &p, int tile) {
   return upper_index(p.cu_tiles, p.seqs.count, tile);
 }
 
+// What the warps of a block are told of an item.
+struct TileItem {
+  int more;  // 0: no item, the block ends
+  int h, row0, rows, group_tiles, kv, nq, n, j0, streams;
+  int index, split;  // of the item without its split
+  int64_t q_begin;
+  const int32_t *pages;
+  KeyRange keys;   // what the item's rows see
+  KeyRange there;  // what the sequence's rows see: present in the pools
+};
+
 struct TileBars {
-  uint64_t k_full[4], k_empty[4], v_full[4], v_empty[4], s_full[2], p_full[2][2], o_full[2], q_full;
+  uint64_t k_full[4], k_empty[4], v_full[4], v_empty[4], s_full[2], p_full[2], o_full[2], q_full, q_empty;
+  uint64_t item_full[2], item_empty[2], wanted, claimed, drain;
+  uint4 claim;
   uint32_t tmem;
   int gave_up;
 };
 
+constexpr int kItemReaders = 15;  // warps that read an item: softmax, loads, products, queries
+
 __device__ const uint4 zero_row[16] = {};  // a key or value vector of zeros
 
-// Bounded wait of one thread; false once any warp of the block has given up.
-// The hardware parks the thread until the phase ends or the hint (0.5 ms) has passed.
-CPKV_DEV bool tile_wait(TileBars *b, uint64_t *bar, uint32_t parity, int32_t *status) {
-  if (mbar_try_wait_for(bar, parity, kTileParkNs)) return true;
+// Bounded wait of a thread.  After kTileWaitNs the block gives up: from then on no
+// wait of it takes longer than a parking, its warps run through what they have begun
+// on whatever is there, end, and the status word says that the results are undefined.
+// The usual way through is one instruction and one branch: the products' warp does
+// nine waits per 128 keys, and its own pace is close to the tensor core's.
+CPKV_DEV void tile_wait(TileBars *b, uint64_t *bar, uint32_t parity, int32_t *status) {
+  if (mbar_try_wait_for(bar, parity, kTileParkNs)) return;
   const uint64_t t0 = global_timer_ns();
   while (!mbar_try_wait_for(bar, parity, kTileParkNs)) {
-    if (*(volatile int *)&b->gave_up) return false;
+    if (*(volatile int *)&b->gave_up) return;
     if (global_timer_ns() - t0 > kTileWaitNs) {
       *(volatile int *)&b->gave_up = 1;
       raise_status(status, CPKV_STATUS_TIMEOUT);
-      return false;
+      return;
     }
   }
-  return true;
 }
 
-// The same for a whole warp, which goes on together.
-CPKV_DEV bool tile_wait_warp(TileBars *b, uint64_t *bar, uint32_t parity, int32_t *status) {
-  return __all_sync(0xffffffffu, tile_wait(b, bar, parity, status));
+// The lowest n bits, n clamped to 0..32.
+CPKV_DEV uint32_t low_bits(int n) { return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1; }
+
+// The item of a block index: the last row tiles first, which see the most keys.
+template <int N>
+CPKV_DEV void find_item(const TileParams<N> &p, int block, TileItem *r) {
+  const int splits = p.space.splits;
+  r->index = (int)gridDim.x / splits - 1 - block / splits;
+  r->split = block % splits;
+  const int tile = r->index / p.io.kv_heads, s = find_tile_seq(p, tile), rt = tile - p.cu_tiles[s];
+  const int group = p.io.group.d;
+  r->h = r->index - tile * p.io.kv_heads;
+  r->nq = p.seqs.q_count(s);
+  r->kv = p.seqs.kv_len(s);
+  r->rows = r->nq * group;
+  r->row0 = rt * kTileRows;
+  r->q_begin = p.seqs.q_begin(s);
+  r->pages = p.seqs.pages(s);
+  const int end = r->row0 + kTileRows < r->rows ? r->row0 + kTileRows : r->rows;
+  r->keys = key_range<kTileKeys>(r->kv, r->nq, div_by(r->row0, p.io.group), div_by(end - 1, p.io.group) + 1, p.seqs.causal,
+                                 p.seqs.window, p.seqs.sinks);
+  r->there = key_range<kTileKeys>(r->kv, r->nq, 0, r->nq, p.seqs.causal, p.seqs.window, p.seqs.sinks);
+  r->j0 = (int)((int64_t)r->keys.n_tiles * r->split / splits);
+  r->n = (int)((int64_t)r->keys.n_tiles * (r->split + 1) / splits) - r->j0;
+  r->group_tiles = end - r->row0 > 128 ? 2 : 1;
+  r->streams = r->group_tiles == 1 && !p.direct ? 2 : 1;
+  r->more = 1;
+  if (r->split == 0 && r->h == 0 && rt == 0 && p.seqs.kv_len_bad(s)) raise_status(p.seqs.status, CPKV_STATUS_OUT_CAPACITY);
 }
 
 template <typename T, int D, int N>
@@ -119,6 +166,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) attend_tile_kernel(const __gr
   constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
   extern __shared__ char raw_smem[];
   __shared__ TileBars bars;
+  __shared__ TileItem items[2];
   __shared__ ulonglong2 addresses[kTileKeys];  // of the keys being copied: key, value
   char *smem = reinterpret_cast<char *>((reinterpret_cast<uintptr_t>(raw_smem) + 1023) & ~uintptr_t(1023));
   char *q_smem = smem, *k_smem = smem + Shape::kQ, *v_smem = k_smem + kStages * Shape::kOperand;
@@ -126,24 +174,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) attend_tile_kernel(const __gr
   int32_t *status = p.seqs.status;
   release_dependents();  // later passes of the call; the joining kernel waits for this one
 
-  // this block's item: the last row tiles first, which see the most keys
-  const int splits = p.space.splits;
-  const int item = (int)(gridDim.x / splits) - 1 - (int)(blockIdx.x / splits);
-  const int split = (int)(blockIdx.x % splits);
-  const int tile = item / p.io.kv_heads, h = item - tile * p.io.kv_heads;
-  const int s = find_tile_seq(p, tile);
-  const int rt = tile - p.cu_tiles[s];
-  const int group = p.io.group.d, nq = p.seqs.q_count(s), kv = p.seqs.kv_len(s), rows = nq * group;
-  const int row0 = rt * kTileRows;
-  const int i0 = div_by(row0, p.io.group);
-  const int i1 = div_by((row0 + kTileRows < rows ? row0 + kTileRows : rows) - 1, p.io.group) + 1;
-  const KeyRange keys = key_range<kTileKeys>(kv, nq, i0, i1, p.seqs.causal, p.seqs.window, p.seqs.sinks);
-  const int j0 = (int)((int64_t)keys.n_tiles * split / splits), j1 = (int)((int64_t)keys.n_tiles * (split + 1) / splits);
-  const int n = j1 - j0;
-  const int tiles = rows - row0 > 128 ? 2 : 1;  // of 128 rows, with any row
-
   if (threadIdx.x == 0) {
-    if (split == 0 && h == 0 && rt == 0 && p.seqs.kv_len_bad(s)) raise_status(status, CPKV_STATUS_OUT_CAPACITY);
     for (int i = 0; i < kStages; ++i) {
       mbar_init(&bars.k_full[i], kLoaders);
       mbar_init(&bars.k_empty[i], 1);
@@ -153,10 +184,15 @@ __global__ void __launch_bounds__(kTileThreads, 1) attend_tile_kernel(const __gr
     for (int t = 0; t < 2; ++t) {
       mbar_init(&bars.s_full[t], 1);
       mbar_init(&bars.o_full[t], 1);
-      mbar_init(&bars.p_full[t][0], 128);
-      mbar_init(&bars.p_full[t][1], 128);
+      mbar_init(&bars.p_full[t], 128);
+      mbar_init(&bars.item_full[t], 1);
+      mbar_init(&bars.item_empty[t], kItemReaders);
     }
-    mbar_init(&bars.q_full, 256);
+    mbar_init(&bars.q_full, 64);
+    mbar_init(&bars.q_empty, 1);
+    mbar_init(&bars.wanted, 1);
+    mbar_init(&bars.claimed, 1);
+    mbar_init(&bars.drain, 1);
     bars.gave_up = 0;
     fence_barrier_init();
   }
@@ -165,162 +201,128 @@ __global__ void __launch_bounds__(kTileThreads, 1) attend_tile_kernel(const __gr
   __syncthreads();
   tmem_fence_after();
   const uint32_t tmem = bars.tmem;
+  auto wait = [&](uint64_t *bar, uint32_t parity) { tile_wait(&bars, bar, parity & 1, status); };
+  // Item number k of this block: whether there is one.  The warp reads it and hands
+  // its place back.
+  auto item_there = [&](int k) {
+    wait(&bars.item_full[k & 1], k >> 1);
+    const bool there = items[k & 1].more && !*(volatile int *)&bars.gave_up;
+    return __all_sync(0xffffffffu, there) != 0;
+  };
+  auto item_read = [&](int k) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&bars.item_empty[k & 1]);
+  };
 
   if (warp < 8) {
-    // ---------------------------------------------------------------- queries, softmax
+    // ---------------------------------------------------------------- softmax
     grow_registers<kSoftmaxRegisters>();
-    if (n > 0) {  // a warp's threads copy 32 / (D / 8) rows at a time
-      constexpr int kLanes = D / 8;
-      const int c = threadIdx.x % kLanes;
-      const char *const zeros = reinterpret_cast<const char *>(zero_row);
-      const char *const q = p.io.q + (int64_t)p.seqs.q_begin(s) * p.io.q_stride + (int64_t)h * group * (D * 2);
-#pragma unroll 4
-      for (int r = threadIdx.x / kLanes; r < kTileRows; r += 256 / kLanes) {
-        const int i = div_by(row0 + r, p.io.group), g = row0 + r - i * group;
-        const char *src = row0 + r < rows ? q + i * p.io.q_stride + g * (D * 2) : zeros;
-        cp_async16(smem_addr(q_smem) + (r >> 7) * Shape::kOperand + (c >> 3) * (kTileKeys * 128) + (r & 127) * 128 +
-                       (((c & 7) ^ (r & 7)) << 4),
-                   src + c * 16);
-      }
-      mbar_arrive_after_copies(&bars.q_full);
-    }
     const int t = warp >> 2;
-    const int in_block = (int)threadIdx.x, row = row0 + in_block;
-    const int tile_first = row0 + t * 128;
     const uint32_t lane_base = tmem + ((uint32_t)(warp & 3) * 32 << 16);
     const uint32_t s_at = lane_base + t * 128, o_at = lane_base + 256 + t * 128;
-    const int token = div_by(row, p.io.group);
-    const RowMask mask = row_mask(kv, nq, token, p.seqs.causal, p.seqs.window, p.seqs.sinks);
-    int last = tile_first + 127;
-    if (last >= rows) last = rows - 1;
-    const int full_hi = row_mask(kv, nq, div_by(tile_first, p.io.group), p.seqs.causal, p.seqs.window, p.seqs.sinks).hi;
-    const int full_lo = row_mask(kv, nq, div_by(last < 0 ? 0 : last, p.io.group), p.seqs.causal, p.seqs.window, p.seqs.sinks).lo;
     const float scale = p.io.scale_log2;
-    float base = -INFINITY, l = 0.f;
-    bool ok = true;
-    const int my_n = t < tiles ? n : 0;
-    for (int it = 0; it < my_n; ++it) {
-      ok = tile_wait_warp(&bars, &bars.s_full[t], it & 1, status);
-      if (!ok) break;
-      tmem_fence_after();
-      uint32_t x[4][32], w[2][16];
-      tmem_load32(x[0], s_at);
-      tmem_load32(x[1], s_at + 32);
-      tmem_wait_loads(x[0]);
-      tmem_wait_loads(x[1]);
-      tmem_load32(x[2], s_at + 64);
-      tmem_load32(x[3], s_at + 96);
-      const int start = keys.tile_start(j0 + it, kTileKeys);
-      const bool whole = start + kTileKeys <= full_hi && (start >= full_lo || start + kTileKeys <= p.seqs.sinks);
-      auto largest = [&](int c) {
-        float a = fmaxf(__uint_as_float(x[c][0]), __uint_as_float(x[c][1]));
-        float b = fmaxf(__uint_as_float(x[c][16]), __uint_as_float(x[c][17]));
+    uint32_t seen = 0, done = 0;  // score tiles, outputs
+    for (int k = 0; item_there(k); ++k) {
+      const TileItem &item = items[k & 1];  // kept until its results are written
+      const int step = item.streams;
+      const int my_n = step == 2 ? (item.n + 1 - t) / 2 : t < item.group_tiles ? item.n : 0;
+      const int j0 = step == 2 ? item.j0 + t : item.j0;
+      const int first = item.row0 + (step == 2 ? 0 : t * 128);
+      const int n_sink = item.keys.n_sink, first_tile = item.keys.first_tile - n_sink;
+      int whole_lo, whole_hi;  // keys that every row of the tile sees
+      {
+        const int last = first + 127 < item.rows ? first + 127 : item.rows - 1;
+        whole_hi = row_mask(item.kv, item.nq, div_by(first, p.io.group), p.seqs.causal, p.seqs.window, p.seqs.sinks).hi;
+        whole_lo = row_mask(item.kv, item.nq, div_by(last, p.io.group), p.seqs.causal, p.seqs.window, p.seqs.sinks).lo;
+      }
+      float base = -INFINITY, l = 0.f;
+      for (int it = 0; it < my_n; ++it) {
+        wait(&bars.s_full[t], seen);
+        __syncwarp();
+        tmem_fence_after();
+        uint32_t x[4][32];
+        tmem_load32(x[0], s_at);
+        tmem_load32(x[1], s_at + 32);
+        tmem_load32(x[2], s_at + 64);
+        tmem_load32(x[3], s_at + 96);
 #pragma unroll
-        for (int i = 2; i < 16; i += 2) {
-          a = max3(a, __uint_as_float(x[c][i]), __uint_as_float(x[c][i + 1]));
-          b = max3(b, __uint_as_float(x[c][16 + i]), __uint_as_float(x[c][17 + i]));
+        for (int c = 0; c < 4; ++c) tmem_wait_loads(x[c]);
+        const int j = j0 + it * step, start = (j < n_sink ? j : first_tile + j) * kTileKeys;
+        if (!(start + kTileKeys <= whole_hi && (start >= whole_lo || start + kTileKeys <= p.seqs.sinks))) {
+          const RowMask mask = row_mask(item.kv, item.nq, div_by(first + (int)(threadIdx.x & 127), p.io.group), p.seqs.causal,
+                                        p.seqs.window, p.seqs.sinks);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const int at = start + c * 32;
+            const uint32_t sees = low_bits(mask.hi - at) & (~low_bits(mask.lo - at) | low_bits(mask.sinks - at));
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (!(sees & (1u << i))) x[c][i] = 0xff800000u;
+          }
         }
-        return fmaxf(a, b);
-      };
-      // 2^(x scale - base) in place of the scores, and rounded
-      auto weigh = [&](int c) {
+        float best[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          best[c] = fmaxf(__uint_as_float(x[c][0]), __uint_as_float(x[c][1]));
+#pragma unroll
+          for (int i = 2; i < 32; i += 2) best[c] = max3(best[c], __uint_as_float(x[c][i]), __uint_as_float(x[c][i + 1]));
+        }
+        const float top = fmaxf(fmaxf(best[0], best[1]), fmaxf(best[2], best[3])) * scale;
+        const bool rise = top > base + kRescaleAt || (base == -INFINITY && top != -INFINITY);
+        if (__any_sync(0xffffffffu, rise)) {  // the sum and the output so far shrink by 2^(old - new)
+          const float next = rise ? top : base;
+          const float fall = rise ? exp2_approx(base - next) : 1.f;
+          base = next;
+          l *= fall;
+          if (it > 0) {
+#pragma unroll 1
+            for (int c = 0; c < D / 32; ++c) {
+              uint32_t o[32];
+              tmem_load32(o, o_at + c * 32);
+              tmem_wait_loads(o);
+#pragma unroll
+              for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * fall);
+              tmem_store32(o_at + c * 32, o);
+            }
+          }
+        }
         const float shift = base == -INFINITY ? 0.f : base;
         const uint64_t scale2 = pair(__float_as_uint(scale), __float_as_uint(scale));
         const uint64_t shift2 = pair(__float_as_uint(-shift), __float_as_uint(-shift));
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const float2 y = unpair(fma_pair(pair(x[c][2 * i], x[c][2 * i + 1]), scale2, shift2));
-          const float a = exp2_approx(y.x), b = exp2_approx(y.y);
-          w[c & 1][i] = pack2<T>(a, b);
-          x[c][2 * i] = __float_as_uint(a);
-          x[c][2 * i + 1] = __float_as_uint(b);
-        }
-      };
-      // A new maximum: the sum and the output so far shrink by 2^(old - new).
-      auto raise = [&](bool rise, float top) {
-        const float next = rise ? top : base;
-        const float fall = rise ? exp2_approx(base - next) : 1.f;
-        base = next;
-        l *= fall;
-        if (it == 0) return;
-#pragma unroll 1
-        for (int c = 0; c < D / 32; ++c) {
-          uint32_t o[32];
-          tmem_load32(o, o_at + c * 32);
-          tmem_wait_loads(o);
+        for (int c = 0; c < 4; ++c) {
+          uint32_t w[16];
 #pragma unroll
-          for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * fall);
-          tmem_store32(o_at + c * 32, o);
+          for (int i = 0; i < 16; ++i) {
+            const float2 y = unpair(fma_pair(pair(x[c][2 * i], x[c][2 * i + 1]), scale2, shift2));
+            const float a = exp2_approx(y.x), b = exp2_approx(y.y);
+            w[i] = pack2<T>(a, b);
+            x[c][2 * i] = __float_as_uint(a);
+            x[c][2 * i + 1] = __float_as_uint(b);
+          }
+          tmem_store16(s_at + c * 16, w);
         }
-      };
-      // With a maximum from before and nothing to mask, the first half's weights
-      // are worked out for that maximum while the second half's scores arrive and
-      // this tile's maximum is found: mostly the old one stands, and they do.
-      const bool ahead = whole && __all_sync(0xffffffffu, base != -INFINITY);
-      float top = 0.f;
-      if (ahead) {
-        top = fmaxf(largest(0), largest(1));
-      } else {
-        tmem_wait_loads(x[2]);
-        tmem_wait_loads(x[3]);
-        if (!whole) {
-          const int lo = mask.lo - start, hi = mask.hi - start, sinks = mask.sinks - start;
-#pragma unroll
-          for (int c = 0; c < 4; ++c)
-#pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              const int j = c * 32 + i;
-              if (!(j < hi && (j >= lo || j < sinks))) x[c][i] = 0xff800000u;
-            }
-        }
-        top = fmaxf(fmaxf(largest(0), largest(1)), fmaxf(largest(2), largest(3))) * scale;
-        const bool rise = top > base + kRescaleAt || (base == -INFINITY && top != -INFINITY);
-        if (__any_sync(0xffffffffu, rise)) raise(rise, top);
-      }
-      weigh(0);
-      weigh(1);
-      if (ahead) {
-        tmem_wait_loads(x[2]);
-        tmem_wait_loads(x[3]);
-        top = fmaxf(top, fmaxf(largest(2), largest(3))) * scale;
-        const bool rise = top > base + kRescaleAt;
-        if (__any_sync(0xffffffffu, rise)) {
-          raise(rise, top);
-          tmem_load32(x[0], s_at);
-          tmem_load32(x[1], s_at + 32);
-          tmem_wait_loads(x[0]);
-          tmem_wait_loads(x[1]);
-          weigh(0);
-          weigh(1);
-        }
-      }
-#pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        if (half == 1) {
-          weigh(2);
-          weigh(3);
-        }
-        tmem_store16(s_at + half * 32, w[0]);
-        tmem_store16(s_at + half * 32 + 16, w[1]);
         tmem_wait_stores();
         tmem_fence_before();
-        mbar_arrive(&bars.p_full[t][half]);
+        mbar_arrive(&bars.p_full[t]);
+        // the sum, beside the products
+        uint64_t sum[4] = {0, 0, 0, 0};
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) sum[c] = add_pair(sum[c], pair(x[c][2 * i], x[c][2 * i + 1]));
+        const float2 all = unpair(add_pair(add_pair(sum[0], sum[1]), add_pair(sum[2], sum[3])));
+        l += all.x + all.y;
+        ++seen;
       }
-      // the sum, beside the products
-      uint64_t sum[4] = {0, 0, 0, 0};
-#pragma unroll
-      for (int i = 0; i < 16; ++i)
-#pragma unroll
-        for (int c = 0; c < 4; ++c) sum[c] = add_pair(sum[c], pair(x[c][2 * i], x[c][2 * i + 1]));
-      const float2 all = unpair(add_pair(add_pair(sum[0], sum[1]), add_pair(sum[2], sum[3])));
-      l += all.x + all.y;
-    }
-    if (ok && my_n > 0) ok = tile_wait_warp(&bars, &bars.o_full[t], 0, status);
-    tmem_fence_after();
-    if (ok) {
-      const int64_t slot_row = ((int64_t)item * splits + split) * kTileRows + in_block;
-      const int head = h * group + row - token * group;
-      const int64_t out_token = p.seqs.q_begin(s) + token;
+      if (my_n > 0) wait(&bars.o_full[t], done++);
+      __syncwarp();
+      tmem_fence_after();
+      const int row = first + (int)(threadIdx.x & 127), rows = item.rows, token = div_by(row, p.io.group);
+      const int head = item.h * (int)p.io.group.d + row - token * (int)p.io.group.d;
+      const int64_t out_token = item.q_begin + token;
+      const int64_t slot_row = ((int64_t)item.index * p.space.splits + item.split) * kTileRows + threadIdx.x;
+      item_read(k);
       if (row < rows) {
         if (!p.direct) {
           *reinterpret_cast<float2 *>(p.space.ml + slot_row * 2) = make_float2(base, l);
@@ -328,45 +330,46 @@ __global__ void __launch_bounds__(kTileThreads, 1) attend_tile_kernel(const __gr
           p.io.lse[out_token * p.io.q_heads + head] = row_lse(base, l);
         }
       }
-      const float inv = row_scale(l);
-      char *dst = p.io.out + out_token * p.io.out_stride + (int64_t)head * (D * 2);
+      if (__any_sync(0xffffffffu, row < rows)) {
+        const float inv = row_scale(l);
+        char *dst = p.io.out + out_token * p.io.out_stride + (int64_t)head * (D * 2);
 #pragma unroll 1
-      for (int c = 0; c < D / 32; ++c) {
-        uint32_t o[32];
-        if (my_n > 0) {
-          tmem_load32(o, o_at + c * 32);
-          tmem_wait_loads(o);
-        }
-        if (row >= rows) continue;
-        if (p.direct) {
-#pragma unroll
-          for (int v = 0; v < 4; ++v) {
-            uint32_t y[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              y[e] = l == 0.f ? 0u : pack2<T>(__uint_as_float(o[v * 8 + 2 * e]) * inv, __uint_as_float(o[v * 8 + 2 * e + 1]) * inv);
-            *reinterpret_cast<uint4 *>(dst + c * 64 + v * 16) = make_uint4(y[0], y[1], y[2], y[3]);
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t o[32];
+          __syncwarp();
+          if (my_n > 0) {
+            tmem_load32(o, o_at + c * 32);
+            tmem_wait_loads(o);
           }
-        } else if (my_n > 0) {
-          float *to = p.space.o + slot_row * D + c * 32;
+          if (row >= rows) continue;
+          if (p.direct) {
 #pragma unroll
-          for (int v = 0; v < 8; ++v)
-            *reinterpret_cast<uint4 *>(to + v * 4) = make_uint4(o[v * 4], o[v * 4 + 1], o[v * 4 + 2], o[v * 4 + 3]);
+            for (int v = 0; v < 4; ++v) {
+              uint32_t y[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                y[e] = l == 0.f ? 0u : pack2<T>(__uint_as_float(o[v * 8 + 2 * e]) * inv, __uint_as_float(o[v * 8 + 2 * e + 1]) * inv);
+              *reinterpret_cast<uint4 *>(dst + c * 64 + v * 16) = make_uint4(y[0], y[1], y[2], y[3]);
+            }
+          } else if (my_n > 0) {
+            float *to = p.space.o + slot_row * D + c * 32;
+#pragma unroll
+            for (int v = 0; v < 8; ++v)
+              *reinterpret_cast<uint4 *>(to + v * 4) = make_uint4(o[v * 4], o[v * 4 + 1], o[v * 4 + 2], o[v * 4 + 3]);
+          }
         }
       }
+      tmem_fence_before();
     }
   } else if (warp < 12) {
-    // ---------------------------------------------------------------- loads
+    // ---------------------------------------------------------------- keys and values
     // A lane looks up one key; its warp brings in those 32 keys.  Without a box it
     // leaves the address in shared memory and copies one 16-byte chunk of several
     // keys.  Keys that no query of the sequence sees are copied from zeros.
     shrink_registers<kOtherRegisters>();
-    const KeyRange there = key_range<kTileKeys>(kv, nq, 0, nq, p.seqs.causal, p.seqs.window, p.seqs.sinks);
     const int lw = warp - 8;
     constexpr int kLanes = D / 8, kRowsAtOnce = 32 / kLanes;
     const int c = lane % kLanes;
-    const int64_t k_at = p.io.k_off + (int64_t)h * D * 2, v_at = p.io.v_off + (int64_t)h * D * 2;
-    const int32_t *pages = p.seqs.pages(s);
     const char *const zeros = reinterpret_cast<const char *>(zero_row);
     ulonglong2 *mine = addresses + lw * 32;
     const ulonglong2 *theirs = mine + lane / kLanes;
@@ -376,12 +379,6 @@ __global__ void __launch_bounds__(kTileThreads, 1) attend_tile_kernel(const __gr
       const int r = e * kRowsAtOnce + lane / kLanes;
       to[e] = (c >> 3) * (kTileKeys * 128) + (lw * 32 + r) * 128 + (((c & 7) ^ (r & 7)) << 4);
     }
-    int key = 0, page = -1;
-    auto look_up = [&](int j) {  // one tile ahead of its copies
-      key = keys.tile_start(j, kTileKeys) + lw * 32 + lane;
-      if (!there.any_sees(key)) key = -1;
-      page = key >= 0 ? pages[div_by(key, p.pools.page_size)] : -1;
-    };
     auto copy = [&](const char *operand, bool values) {
       const uint32_t base = smem_addr(operand);
 #pragma unroll
@@ -394,71 +391,89 @@ __global__ void __launch_bounds__(kTileThreads, 1) attend_tile_kernel(const __gr
     // this lane's box of the warp's: block of 64 elements, first key
     const int boxes = p.box_rows ? 32 / p.box_rows * (D / 64) : 0;
     const int box_block = lane % (D / 64), box_key = lane / (D / 64) * p.box_rows;
-    bool ok = true;
-    if (n > 0) look_up(j0);
-    for (int it = 0; it < n && ok; ++it) {
-      int owner = 0, pool_row = 0;
-      const char *at = nullptr;
-      if (key >= 0) {
-        const int in_page = key - div_by(key, p.pools.page_size) * (int)p.pools.page_size.d;
-        at = page_address(p.pools, page);
-        if (at == nullptr) {
-          raise_status(status, CPKV_STATUS_PAGE_OOB);
-        } else {
-          at += (int64_t)in_page * p.pools.row_bytes;
-          const int local = div_by(page, p.pools.cp);
-          owner = page - local * (int)p.pools.cp.d;
-          pool_row = local * (int)p.pools.page_size.d + in_page;
-        }
-      }
-      const bool by_box = boxes > 0 && __all_sync(0xffffffffu, at != nullptr);
-      if (by_box) {
-        owner = __shfl_sync(0xffffffffu, owner, box_key);
-        pool_row = __shfl_sync(0xffffffffu, pool_row, box_key);
-      } else {
-        __syncwarp();
-        mine[lane] = make_ulonglong2((unsigned long long)(at == nullptr ? zeros : at + k_at),
-                                     (unsigned long long)(at == nullptr ? zeros : at + v_at));
-        __syncwarp();
-      }
-      if (it + 1 < n) look_up(j0 + it + 1);
-      const int stage = it % kStages;
-      const uint32_t freed = (it / kStages - 1) & 1;
-#pragma unroll 1
-      for (int which = 0; which < 2; ++which) {  // keys, then values
-        uint64_t *full = which ? &bars.v_full[stage] : &bars.k_full[stage];
-        if (it >= kStages) ok = tile_wait_warp(&bars, which ? &bars.v_empty[stage] : &bars.k_empty[stage], freed, status);
-        if (!ok) break;
-        char *operand = (which ? v_smem : k_smem) + stage * Shape::kOperand;
-        if (by_box) {
-          if (lane < boxes) {
-            mbar_arrive_expect_tx(full, (uint32_t)p.box_rows * 128);
-            box_load(operand + box_block * (kTileKeys * 128) + (lw * 32 + box_key) * 128, &p.maps[owner],
-                     (int)((which ? v_at : k_at) >> 1) + box_block * 64, pool_row, full);
+    uint32_t loaded = 0;  // key tiles
+    for (int k = 0; item_there(k); ++k) {
+      const int n = items[k & 1].n, j0 = items[k & 1].j0, n_sink = items[k & 1].keys.n_sink, first_tile = items[k & 1].keys.first_tile;
+      const int lo = items[k & 1].there.lo, hi = items[k & 1].there.hi, sink_end = items[k & 1].there.sink_end;
+      const int32_t *const pages = items[k & 1].pages;
+      const int64_t k_at = p.io.k_off + (int64_t)items[k & 1].h * D * 2, v_at = k_at + (p.io.v_off - p.io.k_off);
+      item_read(k);
+      int key = 0, page = -1;
+      auto look_up = [&](int j) {  // one tile ahead of its copies
+        key = (j < n_sink ? j : first_tile + j - n_sink) * kTileKeys + lw * 32 + lane;
+        if (!(key < sink_end || (key >= lo && key < hi))) key = -1;
+        page = key >= 0 ? pages[div_by(key, p.pools.page_size)] : -1;
+      };
+      if (n > 0) look_up(j0);
+      for (int it = 0; it < n; ++it) {
+        int owner = 0, pool_row = 0;
+        const char *at = nullptr;
+        if (key >= 0) {
+          const int in_page = key - div_by(key, p.pools.page_size) * (int)p.pools.page_size.d;
+          at = page_address(p.pools, page);
+          if (at == nullptr) {
+            raise_status(status, CPKV_STATUS_PAGE_OOB);
           } else {
-            mbar_arrive(full);
+            at += (int64_t)in_page * p.pools.row_bytes;
+            const int local = div_by(page, p.pools.cp);
+            owner = page - local * (int)p.pools.cp.d;
+            pool_row = local * (int)p.pools.page_size.d + in_page;
           }
-        } else {
-          copy(operand, which);
-          mbar_arrive_after_copies(full);
         }
+        const bool by_box = boxes > 0 && __all_sync(0xffffffffu, at != nullptr);
+        if (by_box) {
+          owner = __shfl_sync(0xffffffffu, owner, box_key);
+          pool_row = __shfl_sync(0xffffffffu, pool_row, box_key);
+        } else {
+          __syncwarp();
+          mine[lane] = make_ulonglong2((unsigned long long)(at == nullptr ? zeros : at + k_at),
+                                       (unsigned long long)(at == nullptr ? zeros : at + v_at));
+          __syncwarp();
+        }
+        if (it + 1 < n) look_up(j0 + it + 1);
+        const int stage = loaded % kStages;
+        const bool reuse = loaded >= kStages;
+        const uint32_t freed = (loaded / kStages - 1) & 1;
+#pragma unroll 1
+        for (int which = 0; which < 2; ++which) {  // keys, then values
+          uint64_t *full = which ? &bars.v_full[stage] : &bars.k_full[stage];
+          if (reuse) wait(which ? &bars.v_empty[stage] : &bars.k_empty[stage], freed);
+          __syncwarp();
+          char *operand = (which ? v_smem : k_smem) + stage * Shape::kOperand;
+          if (by_box) {
+            if (lane < boxes) {
+              mbar_arrive_expect_tx(full, (uint32_t)p.box_rows * 128);
+              box_load(operand + box_block * (kTileKeys * 128) + (lw * 32 + box_key) * 128, &p.maps[owner],
+                       (int)((which ? v_at : k_at) >> 1) + box_block * 64, pool_row, full);
+            } else {
+              mbar_arrive(full);
+            }
+          } else {
+            copy(operand, which);
+            mbar_arrive_after_copies(full);
+          }
+        }
+        ++loaded;
+        if (warp == 8 && lane == 0 && it == (n > 2 ? n - 3 : 0)) mbar_arrive(&bars.wanted);
       }
+      if (warp == 8 && lane == 0 && n == 0) mbar_arrive(&bars.wanted);
     }
     cp_async_wait_all();
   } else {
-    // ---------------------------------------------------------------- products
-    // The copies are ordinary writes to shared memory: the fence of the thread
-    // that issues the products (after the wait that orders them before it) lets
-    // the tensor core see them.
     shrink_registers<kOtherRegisters>();
-    if (__shfl_sync(0xffffffffu, warp, 0) == 12 && n > 0) {
+    const int role = __shfl_sync(0xffffffffu, warp, 0);
+    if (role == 12) {
+      // -------------------------------------------------------------- products
+      // The copies are ordinary writes to shared memory: the fence of the warp that
+      // issues the products (after the wait that orders them before it) lets the
+      // tensor core see them.
       constexpr uint32_t desc_s = product_desc(kBf16, 128, kTileKeys, false), desc_o = product_desc(kBf16, 128, D, true);
       const uint32_t q_low = operand_low(smem_addr(q_smem), 16), k_low = operand_low(smem_addr(k_smem), 16);
       const uint32_t v_low = operand_low(smem_addr(v_smem), kTileKeys * 128);
       const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
-      const int count = __shfl_sync(0xffffffffu, n, 0), row_tiles = __shfl_sync(0xffffffffu, tiles, 0);
-      auto scores = [&](int t, int stage) {
-        const uint32_t a = q_low + t * (Shape::kOperand >> 4), b = k_low + stage * (Shape::kOperand >> 4);
+      // scores of tile t: queries of block q, keys of a stage
+      auto scores = [&](int t, int q, int stage) {
+        const uint32_t a = q_low + q * (Shape::kOperand >> 4), b = k_low + stage * (Shape::kOperand >> 4);
         const uint32_t d = tm + t * 128;
         if (elect_one()) {
 #pragma unroll
@@ -470,12 +485,11 @@ __global__ void __launch_bounds__(kTileThreads, 1) attend_tile_kernel(const __gr
         }
         __syncwarp();
       };
-      auto values = [&](int t, int stage, int half, uint32_t add) {
-        const uint32_t b = v_low + stage * (Shape::kOperand >> 4) + half * (64 * 128 >> 4);
-        const uint32_t d = tm + 256 + t * 128, a = tm + t * 128 + half * 32;
+      auto values = [&](int t, int stage, uint32_t add) {
+        const uint32_t b = v_low + stage * (Shape::kOperand >> 4), d = tm + 256 + t * 128, a = tm + t * 128;
         if (elect_one()) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) mma_ts(d, a + e * 8, b + e * (16 * 128 >> 4), desc_o, e > 0 ? 1 : add);
+          for (int e = 0; e < kTileKeys / 16; ++e) mma_ts(d, a + e * 8, b + e * (16 * 128 >> 4), desc_o, e > 0 ? 1 : add);
         }
         __syncwarp();
       };
@@ -483,43 +497,139 @@ __global__ void __launch_bounds__(kTileThreads, 1) attend_tile_kernel(const __gr
         if (elect_one()) mma_commit(bar);
         __syncwarp();
       };
-      bool ok = tile_wait_warp(&bars, &bars.q_full, 0, status);
-      if (ok) ok = tile_wait_warp(&bars, &bars.k_full[0], 0, status);
-      if (ok) {
+      uint32_t used = 0, queries = 0, weighed[2] = {0, 0};  // key tiles, items, weight tiles
+      auto keys_in = [&](uint32_t at) {
+        wait(&bars.k_full[at % kStages], at / kStages);
         fence_proxy_async_smem();
-        for (int t = 0; t < row_tiles; ++t) scores(t, 0);
-        commit(&bars.k_empty[0]);
-      }
-      int stage = 0, phase = 0;
-      for (int it = 0; it < count && ok; ++it) {
-        const int next = stage + 1 == kStages ? 0 : stage + 1, next_phase = next == 0 ? phase ^ 1 : phase;
-        ok = tile_wait_warp(&bars, &bars.v_full[stage], phase, status);
-        if (it + 1 < count && ok) ok = tile_wait_warp(&bars, &bars.k_full[next], next_phase, status);
+      };
+      auto values_in = [&](uint32_t at) {
+        wait(&bars.v_full[at % kStages], at / kStages);
         fence_proxy_async_smem();
-        for (int t = 0; t < row_tiles && ok; ++t) {
-          for (int half = 0; half < 2 && ok; ++half) {
-            ok = tile_wait_warp(&bars, &bars.p_full[t][half], it & 1, status);
-            if (!ok) break;
-            tmem_fence_after();
-            values(t, stage, half, half > 0 || it > 0);
+      };
+      // weights of tile t times the values of a stage
+      auto weigh = [&](int t, int stage, bool first) {
+        wait(&bars.p_full[t], weighed[t]++);
+        __syncwarp();
+        tmem_fence_after();
+        values(t, stage, !first);
+      };
+      for (int k = 0; item_there(k); ++k) {
+        const int n = __shfl_sync(0xffffffffu, items[k & 1].n, 0);
+        const int row_tiles = __shfl_sync(0xffffffffu, items[k & 1].group_tiles, 0);
+        const int streams = __shfl_sync(0xffffffffu, items[k & 1].streams, 0);
+        item_read(k);
+        if (n == 0) continue;
+        wait(&bars.q_full, queries++);
+        keys_in(used);
+        if (streams == 1) {
+          for (int t = 0; t < row_tiles; ++t) scores(t, t, used % kStages);
+          commit(&bars.k_empty[used % kStages]);
+          if (n == 1) commit(&bars.q_empty);
+          for (int it = 0; it < n; ++it) {
+            const uint32_t at = used + it;
+            const int stage = at % kStages, next = (at + 1) % kStages;
+            values_in(at);
+            if (it + 1 < n) {
+              keys_in(at + 1);
+              for (int t = 0; t < row_tiles; ++t) {
+                weigh(t, stage, it == 0);
+                if (t == row_tiles - 1) commit(&bars.v_empty[stage]);
+                scores(t, t, next);
+              }
+              commit(&bars.k_empty[next]);
+              if (it + 2 == n) commit(&bars.q_empty);
+            } else {
+              for (int t = 0; t < row_tiles; ++t) {
+                weigh(t, stage, it == 0);
+                commit(&bars.o_full[t]);
+              }
+              commit(&bars.v_empty[stage]);
+            }
           }
-          if (!ok) break;
-          if (t == row_tiles - 1) commit(&bars.v_empty[stage]);
-          if (it + 1 < count) scores(t, next);
+        } else {  // the same rows, every other key tile
+          scores(0, 0, used % kStages);
+          commit(&bars.k_empty[used % kStages]);
+          if (n > 1) {
+            keys_in(used + 1);
+            scores(1, 0, (used + 1) % kStages);
+            commit(&bars.k_empty[(used + 1) % kStages]);
+          }
+          if (n <= 2) commit(&bars.q_empty);
+          for (int it = 0; it < n; ++it) {
+            const uint32_t at = used + it;
+            const int t = it & 1, stage = at % kStages;
+            values_in(at);
+            weigh(t, stage, it < 2);
+            commit(&bars.v_empty[stage]);
+            if (it + 2 < n) {
+              keys_in(at + 2);
+              scores(t, 0, (at + 2) % kStages);
+              commit(&bars.k_empty[(at + 2) % kStages]);
+              if (it + 3 == n) commit(&bars.q_empty);
+            } else {
+              commit(&bars.o_full[t]);
+            }
+          }
         }
-        if (ok && it + 1 < count) commit(&bars.k_empty[next]);
-        stage = next;
-        phase = next_phase;
+        used += n;
       }
-      commit(&bars.o_full[0]);
-      commit(&bars.o_full[1]);
-      if (!ok) {  // products in flight end before tensor memory is freed
+      if (*(volatile int *)&bars.gave_up) {  // products in flight end before tensor memory is freed
+        commit(&bars.drain);
         const uint64_t t0 = global_timer_ns();
-        while (!mbar_try_wait(&bars.o_full[0], 0) && global_timer_ns() - t0 < kTileWaitNs) {
+        while (!mbar_try_wait(&bars.drain, 0) && global_timer_ns() - t0 < kTileWaitNs) {
         }
       }
+    } else if (role == 13) {
+      // -------------------------------------------------------------- items
+      if (lane == 0) {
+        int block = (int)blockIdx.x;
+        for (int k = 0;; ++k) {
+          if (k >= 2) wait(&bars.item_empty[k & 1], (k >> 1) - 1);
+          if (block >= 0) {
+            find_item(p, block, &items[k & 1]);
+          } else {
+            items[k & 1].more = 0;
+          }
+          mbar_arrive(&bars.item_full[k & 1]);
+          if (block < 0) break;
+          wait(&bars.wanted, k);  // the loads of this item near their end
+          fence_proxy_async_smem();
+          claim_block(&bars.claim, &bars.claimed);
+          wait(&bars.claimed, k);
+          block = *(volatile int *)&bars.gave_up ? -1 : claimed_block(&bars.claim);
+        }
+      }
+      __syncwarp();
+    } else {
+      // -------------------------------------------------------------- queries
+      constexpr int kLanes = D / 8;
+      const int at = (int)threadIdx.x - 14 * 32, c = at % kLanes;
+      const char *const zeros = reinterpret_cast<const char *>(zero_row);
+      uint32_t filled = 0;
+      for (int k = 0; item_there(k); ++k) {
+        int row0, rows, count;
+        const char *q;
+        {
+          const TileItem &item = items[k & 1];
+          row0 = item.row0, rows = item.rows, count = item.n > 0 ? item.group_tiles * 128 : 0;
+          q = p.io.q + item.q_begin * p.io.q_stride + (int64_t)item.h * (int)p.io.group.d * (D * 2);
+          item_read(k);
+        }
+        if (count == 0) continue;
+        if (filled > 0) wait(&bars.q_empty, filled - 1);
+#pragma unroll 4
+        for (int r = at / kLanes; r < count; r += 64 / kLanes) {
+          const int i = div_by(row0 + r, p.io.group), g = row0 + r - i * (int)p.io.group.d;
+          const char *src = row0 + r < rows ? q + i * p.io.q_stride + g * (D * 2) : zeros;
+          cp_async16(smem_addr(q_smem) + (r >> 7) * Shape::kOperand + (c >> 3) * (kTileKeys * 128) + (r & 127) * 128 +
+                         (((c & 7) ^ (r & 7)) << 4),
+                     src + c * 16);
+        }
+        mbar_arrive_after_copies(&bars.q_full);
+        ++filled;
+      }
+      cp_async_wait_all();
     }
-    __syncwarp();
   }
   tmem_fence_before();
   __syncthreads();

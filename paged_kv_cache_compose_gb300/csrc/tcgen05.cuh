@@ -187,6 +187,31 @@ CPKV_DEV bool mbar_try_wait_for(uint64_t *bar, uint32_t parity, uint32_t ns) {
   return done != 0;
 }
 
+// Asks for a block of this grid that has not started; the answer (16 bytes in
+// shared memory) arrives on `bar`.  claimed_block: its index in x, or -1 where none
+// was left, after which no more is asked for.
+CPKV_DEV void claim_block(uint4 *answer, uint64_t *bar) {
+  mbar_arrive_expect_tx(bar, 16);
+  asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
+                   smem_addr(answer)),
+               "r"(smem_addr(bar))
+               : "memory");
+}
+CPKV_DEV int claimed_block(const uint4 *answer) {
+  uint32_t got, x;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b128 a;\n\t"
+      "ld.shared.b128 a, [%2];\n\t"
+      "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, a;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t"
+      "mov.u32 %1, 0;\n\t"
+      "@p clusterlaunchcontrol.query_cancel.get_first_ctaid.v4.b32.b128 {%1, _, _, _}, a;\n\t}"
+      : "=r"(got), "=r"(x)
+      : "r"(smem_addr(answer))
+      : "memory");
+  return got ? (int)x : -1;
+}
+
 CPKV_DEV void mbar_arrive(uint64_t *bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
 }
