@@ -103,16 +103,19 @@ struct TileBounds {
   // over the SMs come to the fewest key tiles, each round costing kItemTiles more for
   // its beginning and end, and any parts kJoinTiles for joining them (both measured:
   // about 4 us and 6 us against 1.4 us a key tile).
-  int finish(int kv_heads) {
+  int finish(int kv_heads, int head_dim) {
     const int64_t items = tiles * kv_heads;
     if (items > INT32_MAX / 2 || tokens > INT32_MAX) return CPKV_ERR_LIMIT;
     constexpr int64_t kItemTiles = 3, kJoinTiles = 4;
-    const int64_t sms = device_sm_count(), key_tiles = ceil_div(max_keys, kTileKeys);
-    int64_t best = INT64_MAX;
+    // two streams take the key tiles of at most 128 rows two at a time
+    const int64_t sms = device_sm_count(), key_tiles = ceil_div(max_keys, max_rows <= 128 ? 2 * kTileKeys : kTileKeys);
+    int64_t best = INT64_MAX / 16;
     for (int64_t n = 1; n <= std::min<int64_t>(std::max<int64_t>(key_tiles / 2, 1), sms) && items > 0; ++n) {
       if (n > 1 && items * n > 4 * sms) break;
-      const int64_t cost = ceil_div(items * n, sms) * (ceil_div(key_tiles, n) + kItemTiles) + (n > 1 ? kJoinTiles : 0);
-      if (cost < best) {
+      // in 32nds of a key tile; a part of 256 rows of 128 written and read again is about one
+      const int64_t cost = 32 * ceil_div(items * n, sms) * (ceil_div(key_tiles, n) + kItemTiles) +
+                           (n > 1 ? 32 * kJoinTiles + items * n * head_dim / 128 : 0);
+      if (10 * cost < 9 * best) {  // for a tenth or more
         best = cost;
         splits = (int)n;
       }
@@ -162,7 +165,7 @@ int window_plan(WindowPlan *w, const HeadArgs &a, int B, const int32_t *h_q_lens
   bool uniform = B > 0;
   for (int s = 1; s < B && h_q_lens != nullptr; ++s) uniform &= h_q_lens[s] == h_q_lens[0];
   w->whole = w->few && uniform && w->split.max_tiles <= kWholeUnits;
-  const int rc = w->few ? w->split.finish(group, a.kv_heads) : w->tile.finish(a.kv_heads);
+  const int rc = w->few ? w->split.finish(group, a.kv_heads) : w->tile.finish(a.kv_heads, a.head_dim);
   w->bytes = w->whole ? 0
              : w->few ? w->split.bytes(B, a.kv_heads, a.head_dim, true)
                       : w->tile.bytes(a.kv_heads, a.head_dim, true);
@@ -194,7 +197,7 @@ int shared_plan(SharedPlan *w, const HeadArgs &a, int B, int n_groups, const int
     w->split.add(h_group_sizes[g], h_prefix_lens[g], group, 0, 0);
   for (int b = 0; b < B; ++b) w->split.add(1, max_suffix, group, 0, 0);
   int rc = w->split.finish(group, a.kv_heads);
-  if (!w->few && rc == CPKV_OK) rc = w->tile.finish(a.kv_heads);
+  if (!w->few && rc == CPKV_OK) rc = w->tile.finish(a.kv_heads, a.head_dim);
   w->prefix_bytes = w->few ? 0 : w->tile.bytes(a.kv_heads, a.head_dim, false);
   w->bytes = w->prefix_bytes + w->split.bytes(w->few ? n_groups + B : B, a.kv_heads, a.head_dim, false);
   return rc;
@@ -288,6 +291,7 @@ void fill_tiles(TileParams<N> *p, const Seqs<N> &seqs, const PagedPools &pools, 
   p->io = io;
   p->space = b.space(workspace, io.kv_heads);
   p->direct = direct && b.splits == 1;
+  p->wide_out = (reinterpret_cast<uintptr_t>(io.out) & 31) == 0 && io.out_stride % 32 == 0;
   fill_maps(p);
   const int group = io.group.d;
   for (int s = 0; s < seqs.count; ++s) {

@@ -212,6 +212,12 @@ CPKV_DEV void ldmatrix_x4_trans(uint32_t r[4], uint32_t addr) {
 CPKV_DEV void cp_async16(uint32_t smem, const void *src, int bytes) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem), "l"(src), "r"(bytes) : "memory");
 }
+// The same with an L2 policy.
+CPKV_DEV void cp_async16_hint(uint32_t smem, const void *src, int bytes, uint64_t policy) {
+  asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2, %3;" ::"r"(smem), "l"(src), "r"(bytes),
+               "l"(policy)
+               : "memory");
+}
 CPKV_DEV void cp_async16(uint32_t smem, const void *src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem), "l"(src) : "memory");
 }

@@ -19,7 +19,7 @@ struct Parts {
 // Where a pass keeps a query row: found from the call's own inputs, before the
 // pass has ended.
 struct Spot {
-  int s, rt, in_tile, n_tiles;  // n_tiles: key tiles of a split pass, streams of a tile pass
+  int s, rt, in_tile, n_tiles;
 };
 
 template <typename S>
@@ -31,10 +31,8 @@ CPKV_DEV Spot find_spot(const SplitSource<S> &src, const AttendIo &io, int s, in
 
 template <int N>
 CPKV_DEV Spot find_spot(const TileSource<N> &src, const AttendIo &io, int s, int i, int g) {
-  const int group = io.group.d, row = i * group + g, rt = row / kTileRows;
-  // two streams where the tile has at most 128 rows
-  const int streams = src.seqs.q_count(s) * group - rt * kTileRows <= 128 ? 2 : 1;
-  return Spot{s, rt, row % kTileRows, streams};
+  const int row = i * (int)io.group.d + g;
+  return Spot{s, row / kTileRows, row % kTileRows, 0};
 }
 
 // The parts of a row of key/value head h; false when the pass has written that
@@ -69,9 +67,9 @@ CPKV_DEV bool find_parts(Parts *r, const TileSource<N> &src, const AttendIo &io,
   r->ml = src.space.ml;
   r->o = src.space.o;
   r->first = item * src.space.splits * kTileRows + at.in_tile;
-  r->step = kTileRows / at.n_tiles;
-  r->next = r->first + r->step;
-  r->count = src.space.splits * at.n_tiles;
+  r->step = kTileRows;
+  r->next = r->first + kTileRows;
+  r->count = src.space.splits;
   return true;
 }
 

@@ -128,7 +128,9 @@ __global__ void __launch_bounds__(kSplitWarps * 32, SplitShape<D>::kBlocks) atte
   float *join = reinterpret_cast<float *>(smem + Shape::kRing);
   float2 *ml = reinterpret_cast<float2 *>(smem + Shape::kRing + Shape::kJoin);
 
-  // loads: lanes 0..15 own one key each
+  // loads: lanes 0..15 own one key each.  A row is read once by its head's one tile of
+  // rows (or few): it makes room in L2 before the parts do.
+  const uint64_t once = l2_policy_evict_first();
   Cursor<S> at = ld;
   int ld_u = u0, ld_key = 0, ld_page = -1;
   bool ld_sees = false;
@@ -161,8 +163,8 @@ __global__ void __launch_bounds__(kSplitWarps * 32, SplitShape<D>::kBlocks) atte
         const int bytes = src == nullptr ? 0 : 16;
         if (src == nullptr) src = reinterpret_cast<const char *>(p.io.q);  // a valid address that is not read
         const uint32_t to = dst + key * Shape::kRow + ((c ^ (key & 7)) << 4);
-        cp_async16(to, bytes ? src + k_at : src, bytes);
-        cp_async16(to + kWarpKeys * Shape::kRow, bytes ? src + v_at : src, bytes);
+        cp_async16_hint(to, bytes ? src + k_at : src, bytes, once);
+        cp_async16_hint(to + kWarpKeys * Shape::kRow, bytes ? src + v_at : src, bytes, once);
       }
       if (++ld_u < u1) {
         ld.advance(p);

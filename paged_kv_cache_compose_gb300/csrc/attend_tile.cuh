@@ -20,8 +20,8 @@
 //                      started (cluster launch control), so long items go first and no
 //                      SM waits for another.
 //   warps 14, 15       the next item's queries, once this one's scores are done.
-// Of an item with at most 128 rows whose results are joined anyway, the two tiles
-// are the same rows over every other 128 keys (two streams), and each leaves a part.
+// Of an item with at most 128 rows the two tiles are the same rows over every other
+// 128 keys (two streams), joined at the end.
 // Tensor memory (512 columns): scores of the tiles at 0 and 128, outputs at 256
 // and 384.  A row's output is rescaled only when its maximum has risen by more
 // than 2^8 since the last time: weights stay below 2^8, and the sum and the output
@@ -62,6 +62,7 @@ struct TileParams {
   AttendIo io;
   TileSpace space;
   int direct;           // one split, and the rows go straight to the output
+  int wide_out;         // the output's rows start on 32 bytes
   int box_rows;         // rows of a TMA box (32 or 16); 0: no maps
   int cu_tiles[N + 1];  // row tiles before each sequence
   CUtensorMap maps[kTileMaps];  // pool r as [rows][elements], boxes of box_rows x 64
@@ -101,7 +102,7 @@ struct TileItem {
 
 struct TileBars {
   uint64_t k_full[4], k_empty[4], v_full[4], v_empty[4], s_full[2], p_full[2], o_full[2], q_full, q_empty;
-  uint64_t item_full[2], item_empty[2], wanted, claimed, drain;
+  uint64_t item_full[2], item_empty[2], wanted, claimed, drain, stream_done, stream_free;
   uint4 claim;
   uint32_t tmem;
   int gave_up;
@@ -151,10 +152,11 @@ CPKV_DEV void find_item(const TileParams<N> &p, int block, TileItem *r) {
   r->keys = key_range<kTileKeys>(r->kv, r->nq, div_by(r->row0, p.io.group), div_by(end - 1, p.io.group) + 1, p.seqs.causal,
                                  p.seqs.window, p.seqs.sinks);
   r->there = key_range<kTileKeys>(r->kv, r->nq, 0, r->nq, p.seqs.causal, p.seqs.window, p.seqs.sinks);
-  r->j0 = (int)((int64_t)r->keys.n_tiles * r->split / splits);
-  r->n = (int)((int64_t)r->keys.n_tiles * (r->split + 1) / splits) - r->j0;
+  // fewer than 2^24 key tiles, at most some hundred parts
+  r->j0 = (int)((uint32_t)r->keys.n_tiles * (uint32_t)r->split / (uint32_t)splits);
+  r->n = (int)((uint32_t)r->keys.n_tiles * (uint32_t)(r->split + 1) / (uint32_t)splits) - r->j0;
   r->group_tiles = end - r->row0 > 128 ? 2 : 1;
-  r->streams = r->group_tiles == 1 && !p.direct ? 2 : 1;
+  r->streams = r->group_tiles == 1 ? 2 : 1;
   r->more = 1;
   if (r->split == 0 && r->h == 0 && rt == 0 && p.seqs.kv_len_bad(s)) raise_status(p.seqs.status, CPKV_STATUS_OUT_CAPACITY);
 }
@@ -167,6 +169,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) attend_tile_kernel(const __gr
   extern __shared__ char raw_smem[];
   __shared__ TileBars bars;
   __shared__ TileItem items[2];
+  __shared__ float2 stream_ml[128];            // maximum and sum of the second stream's rows
   __shared__ ulonglong2 addresses[kTileKeys];  // of the keys being copied: key, value
   char *smem = reinterpret_cast<char *>((reinterpret_cast<uintptr_t>(raw_smem) + 1023) & ~uintptr_t(1023));
   char *q_smem = smem, *k_smem = smem + Shape::kQ, *v_smem = k_smem + kStages * Shape::kOperand;
@@ -193,6 +196,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) attend_tile_kernel(const __gr
     mbar_init(&bars.wanted, 1);
     mbar_init(&bars.claimed, 1);
     mbar_init(&bars.drain, 1);
+    mbar_init(&bars.stream_done, 128);
+    mbar_init(&bars.stream_free, 128);
     bars.gave_up = 0;
     fence_barrier_init();
   }
@@ -221,7 +226,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) attend_tile_kernel(const __gr
     const uint32_t lane_base = tmem + ((uint32_t)(warp & 3) * 32 << 16);
     const uint32_t s_at = lane_base + t * 128, o_at = lane_base + 256 + t * 128;
     const float scale = p.io.scale_log2;
-    uint32_t seen = 0, done = 0;  // score tiles, outputs
+    uint32_t seen = 0, done0 = 0, done1 = 0, pairs = 0;  // score tiles, outputs of the tiles, items of two streams
     for (int k = 0; item_there(k); ++k) {
       const TileItem &item = items[k & 1];  // kept until its results are written
       const int step = item.streams;
@@ -315,7 +320,31 @@ __global__ void __launch_bounds__(kTileThreads, 1) attend_tile_kernel(const __gr
         l += all.x + all.y;
         ++seen;
       }
-      if (my_n > 0) wait(&bars.o_full[t], done++);
+      // outputs of the item: of both tiles, so that either thread keeps count
+      const bool has0 = item.n > 0, has1 = step == 2 ? item.n > 1 : has0 && item.group_tiles == 2;
+      float mine = 1.f, other = 0.f;  // factors of the first and second stream's outputs
+      if (step == 2) {
+        if (t == 1) {
+          stream_ml[threadIdx.x & 127] = make_float2(base, l);
+          mbar_arrive(&bars.stream_done);
+          done0 += has0;
+          done1 += has1;
+          wait(&bars.stream_free, pairs++);
+          item_read(k);
+          continue;
+        }
+        wait(&bars.stream_done, pairs++);
+        const float2 ml = stream_ml[threadIdx.x & 127];
+        const float top = fmaxf(base, ml.x), shift = top == -INFINITY ? 0.f : top;
+        mine = exp2_approx(base - shift);
+        other = exp2_approx(ml.x - shift);
+        l = l * mine + ml.y * other;
+        base = top;
+        if (has1) wait(&bars.o_full[1], done1);
+      }
+      if (t == 0 ? has0 : has1) wait(&bars.o_full[t], t == 0 ? done0 : done1);
+      done0 += has0;
+      done1 += has1;
       __syncwarp();
       tmem_fence_after();
       const int row = first + (int)(threadIdx.x & 127), rows = item.rows, token = div_by(row, p.io.group);
@@ -341,25 +370,41 @@ __global__ void __launch_bounds__(kTileThreads, 1) attend_tile_kernel(const __gr
             tmem_load32(o, o_at + c * 32);
             tmem_wait_loads(o);
           }
+          if (step == 2 && has1) {  // the second stream's rows are in the same lanes
+            uint32_t o1[32];
+            tmem_load32(o1, o_at + 128 + c * 32);
+            tmem_wait_loads(o1);
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              o[i] = __float_as_uint(fmaf(__uint_as_float(o1[i]), other, __uint_as_float(o[i]) * mine));
+          }
           if (row >= rows) continue;
+          // 32 bytes a store where they are aligned: a warp's rows lie apart, and each
+          // store of it takes as long as it touches lines
           if (p.direct) {
 #pragma unroll
-            for (int v = 0; v < 4; ++v) {
-              uint32_t y[4];
+            for (int v = 0; v < 2; ++v) {
+              uint32_t y[8];
 #pragma unroll
-              for (int e = 0; e < 4; ++e)
-                y[e] = l == 0.f ? 0u : pack2<T>(__uint_as_float(o[v * 8 + 2 * e]) * inv, __uint_as_float(o[v * 8 + 2 * e + 1]) * inv);
-              *reinterpret_cast<uint4 *>(dst + c * 64 + v * 16) = make_uint4(y[0], y[1], y[2], y[3]);
+              for (int e = 0; e < 8; ++e)
+                y[e] = l == 0.f ? 0u
+                                : pack2<T>(__uint_as_float(o[v * 16 + 2 * e]) * inv, __uint_as_float(o[v * 16 + 2 * e + 1]) * inv);
+              if (p.wide_out) {
+                store32(dst + c * 64 + v * 32, y);
+              } else {
+                *reinterpret_cast<uint4 *>(dst + c * 64 + v * 32) = make_uint4(y[0], y[1], y[2], y[3]);
+                *reinterpret_cast<uint4 *>(dst + c * 64 + v * 32 + 16) = make_uint4(y[4], y[5], y[6], y[7]);
+              }
             }
           } else if (my_n > 0) {
             float *to = p.space.o + slot_row * D + c * 32;
 #pragma unroll
-            for (int v = 0; v < 8; ++v)
-              *reinterpret_cast<uint4 *>(to + v * 4) = make_uint4(o[v * 4], o[v * 4 + 1], o[v * 4 + 2], o[v * 4 + 3]);
+            for (int v = 0; v < 4; ++v) store32(to + v * 8, o + v * 8);
           }
         }
       }
       tmem_fence_before();
+      if (step == 2) mbar_arrive(&bars.stream_free);
     }
   } else if (warp < 12) {
     // ---------------------------------------------------------------- keys and values
@@ -617,13 +662,25 @@ __global__ void __launch_bounds__(kTileThreads, 1) attend_tile_kernel(const __gr
         }
         if (count == 0) continue;
         if (filled > 0) wait(&bars.q_empty, filled - 1);
-#pragma unroll 4
-        for (int r = at / kLanes; r < count; r += 64 / kLanes) {
-          const int i = div_by(row0 + r, p.io.group), g = row0 + r - i * (int)p.io.group.d;
-          const char *src = row0 + r < rows ? q + i * p.io.q_stride + g * (D * 2) : zeros;
-          cp_async16(smem_addr(q_smem) + (r >> 7) * Shape::kOperand + (c >> 3) * (kTileKeys * 128) + (r & 127) * 128 +
-                         (((c & 7) ^ (r & 7)) << 4),
-                     src + c * 16);
+        // rows at / kLanes, + kStep, ...: (token, head) and address go along
+        constexpr int kStep = 64 / kLanes;
+        const int group = p.io.group.d, heads_on = kStep % group, tokens_on = kStep / group;
+        const int64_t on = tokens_on * p.io.q_stride + heads_on * (D * 2), wrap = p.io.q_stride - group * (D * 2);
+        int r = at / kLanes;
+        const int i = div_by(row0 + r, p.io.group);
+        int g = row0 + r - i * group;
+        const char *src = q + i * p.io.q_stride + g * (D * 2) + c * 16;
+        const uint32_t to = smem_addr(q_smem) + (c >> 3) * (kTileKeys * 128);
+#pragma unroll 8
+        for (; r < count; r += kStep) {
+          cp_async16(to + (r >> 7) * Shape::kOperand + (r & 127) * 128 + (((c & 7) ^ (r & 7)) << 4),
+                     row0 + r < rows ? src : zeros + c * 16);
+          src += on;
+          g += heads_on;
+          if (g >= group) {
+            g -= group;
+            src += wrap;
+          }
         }
         mbar_arrive_after_copies(&bars.q_full);
         ++filled;

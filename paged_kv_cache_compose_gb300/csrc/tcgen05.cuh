@@ -187,6 +187,13 @@ CPKV_DEV bool mbar_try_wait_for(uint64_t *bar, uint32_t parity, uint32_t ns) {
   return done != 0;
 }
 
+// 32 bytes to an address that is a multiple of 32.
+CPKV_DEV void store32(void *to, const uint32_t *r) {
+  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(to), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]),
+               "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+
 // Asks for a block of this grid that has not started; the answer (16 bytes in
 // shared memory) arrives on `bar`.  claimed_block: its index in x, or -1 where none
 // was left, after which no more is asked for.
