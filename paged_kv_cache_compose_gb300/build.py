@@ -1,4 +1,5 @@
-"""Build ``libcpkv.so`` in-tree with nvcc for sm_103a.
+"""Build ``libcpkv.so`` in-tree with nvcc for sm_103a, and ``_serving.so``, the
+Python marshalling of the serving calls, with the host compiler.
 
 Each translation unit under ``csrc/`` is compiled in parallel, then linked
 into one shared library next to this file.  Usage::
@@ -15,6 +16,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -22,6 +24,8 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(HERE, "_build")
 LIB_PATH = os.path.join(HERE, "libcpkv.so")
+BINDING_SRC = os.path.join(CSRC, "serving_binding.cpp")
+BINDING_PATH = os.path.join(HERE, "_serving.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
@@ -62,11 +66,53 @@ def _built_for_other_machine(path: str) -> bool:
     return int.from_bytes(head[18:20], "little") != want
 
 
-def stale() -> bool:
-    if not os.path.exists(LIB_PATH) or _built_for_other_machine(LIB_PATH):
+def _older(path: str, deps: list[str]) -> bool:
+    if not os.path.exists(path) or _built_for_other_machine(path):
         return True
-    t = os.path.getmtime(LIB_PATH)
-    return any(os.path.getmtime(p) > t for p in _deps())
+    t = os.path.getmtime(path)
+    return any(os.path.getmtime(p) > t for p in deps)
+
+
+def stale() -> bool:
+    return _older(LIB_PATH, _deps())
+
+
+def binding_stale() -> bool:
+    return _older(BINDING_PATH, [BINDING_SRC, os.path.join(INCLUDE, "cpkv.h")])
+
+
+def _torch_dirs() -> tuple[list[str], str]:
+    """torch's include directories and its library directory."""
+    import torch
+
+    root = os.path.dirname(torch.__file__)
+    inc = os.path.join(root, "include")
+    return [inc, os.path.join(inc, "torch", "csrc", "api", "include")], os.path.join(root, "lib")
+
+
+def _compile_binding() -> str:
+    import torch
+
+    obj = os.path.join(BUILD_DIR, "serving_binding.o")
+    inc = [INCLUDE, *_torch_dirs()[0], sysconfig.get_paths()["include"]]
+    cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-w",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           *[a for d in inc for a in ("-isystem" if "torch" in d else "-I", d)], "-c", BINDING_SRC, "-o", obj]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on {os.path.basename(BINDING_SRC)}:\n{r.stdout}\n{r.stderr}")
+    return obj
+
+
+def _link_binding(obj: str) -> None:
+    lib = _torch_dirs()[1]
+    tmp = BINDING_PATH + f".{os.getpid()}.tmp"
+    cmd = [shutil.which("g++") or "g++", "-shared", "-o", tmp, obj, "-L", HERE, "-lcpkv", "-L", lib, "-ltorch_python",
+           "-ltorch_cpu", "-lc10", "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{lib}"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"link of {os.path.basename(BINDING_PATH)} failed:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BINDING_PATH)
 
 
 def _compile(src: str, extra: list[str]) -> str:
@@ -81,20 +127,27 @@ def _compile(src: str, extra: list[str]) -> str:
 
 
 def build(force: bool = False, verbose_ptxas: bool = False) -> str:
-    """Compile every CUDA translation unit and link ``libcpkv.so``."""
-    if not force and not stale():
+    """Compile every CUDA translation unit and link ``libcpkv.so``; compile and
+    link ``_serving.so`` beside it."""
+    library, binding = force or stale(), force or binding_stale()
+    if not library and not binding:
         return LIB_PATH
     os.makedirs(BUILD_DIR, exist_ok=True)
     extra = ["-Xptxas", "-v"] if verbose_ptxas else []
-    srcs = sources()
-    with cf.ThreadPoolExecutor(max_workers=min(8, len(srcs))) as ex:
-        objs = list(ex.map(lambda s: _compile(s, extra), srcs))
-    tmp = LIB_PATH + f".{os.getpid()}.tmp"
-    cmd = [nvcc(), *ARCH, "-shared", "-o", tmp, *objs]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"nvcc link failed:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, LIB_PATH)
+    srcs = sources() if library else []
+    with cf.ThreadPoolExecutor(max_workers=8) as ex:
+        objs = [ex.submit(_compile, s, extra) for s in srcs]
+        binding_obj = ex.submit(_compile_binding) if binding else None
+        objs = [f.result() for f in objs]
+        if library:
+            tmp = LIB_PATH + f".{os.getpid()}.tmp"
+            cmd = [nvcc(), *ARCH, "-shared", "-o", tmp, *objs]
+            r = subprocess.run(cmd, capture_output=True, text=True)
+            if r.returncode != 0:
+                raise RuntimeError(f"nvcc link failed:\n{r.stdout}\n{r.stderr}")
+            os.replace(tmp, LIB_PATH)
+        if binding_obj is not None:
+            _link_binding(binding_obj.result())
     return LIB_PATH
 
 

@@ -451,9 +451,41 @@ def ragged_buffers(seg_cap: int, topk_cap: int, device="cuda") -> dict:
 # ---------------------------------------------------------------------------
 # serving on the paged rows
 # ---------------------------------------------------------------------------
-# These calls come once per layer and decode step, whose kernels take a few
-# microseconds: the marshalling below looks at each tensor once and makes no
-# objects that it can do without.
+# These calls come once per layer and decode step and their kernels take a few
+# microseconds, so their tensors are checked and handed on by compiled code
+# (csrc/serving_binding.cpp, built beside the library).
+
+class _Table(ctypes.Structure):
+    """``Table`` of csrc/serving_binding.cpp."""
+
+    _fields_ = [("addresses", ctypes.c_uint64), ("caps", ctypes.c_uint64), ("row_bytes", _L), ("key_offset", _L),
+                ("value_offset", _L), ("page_size", ctypes.c_int32), ("cp_size", ctypes.c_int32),
+                ("code", ctypes.c_int32), ("flags", ctypes.c_int32), ("device", ctypes.c_int32)]
+
+
+def _wrong(name: str, what: str):
+    return CpkvError("marshal", CPKV_ERR_ARG, f"{name}: {what} is wanted")
+
+
+_native = None
+
+
+def serving():
+    """The compiled marshalling (loads it, and the library, at the first call)."""
+    global _native
+    if _native is None:
+        import torch  # noqa: F401  (its libraries hold the tensors)
+
+        load()
+        try:
+            from . import _serving
+        except ImportError as e:
+            raise CpkvError("load", -100, f"_serving.so: {e}; build the library first "
+                                          "(python -m paged_kv_cache_compose_gb300.build)") from None
+        _serving.set_fail(_wrong)
+        _native = _serving
+    return _native
+
 
 class PoolTable:
     """The owner pools of a paged cache as the serving calls take them: the
@@ -469,8 +501,8 @@ class PoolTable:
         if not self.pools:
             raise CpkvError("PoolTable", CPKV_ERR_ARG, "no pools")
         self.dtype, self.device = self.pools[0].dtype, self.pools[0].device
-        self.code = {torch.bfloat16: BF16, torch.float16: FP16}.get(self.dtype)
-        if self.code is None:
+        code = {torch.bfloat16: BF16, torch.float16: FP16}.get(self.dtype)
+        if code is None:
             raise CpkvError("PoolTable", CPKV_ERR_ARG, f"pools of {self.dtype}: bfloat16 or float16 is wanted")
         for t in self.pools:
             if t.dim() != 3 or t.shape[1] != page_size or t.shape[2] != self.pools[0].shape[2]:
@@ -479,70 +511,11 @@ class PoolTable:
                 raise CpkvError("PoolTable", CPKV_ERR_ARG, "pools of one type on one device are wanted")
         self._addresses = np.array([(_dp(t) or _P(0)).value or 0 for t in self.pools], np.uint64)
         self._caps = _host_i64([t.shape[0] for t in self.pools])
-        self.addresses, self.caps = self._addresses.ctypes.data, self._caps.ctypes.data
         self.page_size, self.cp_size = int(page_size), len(self.pools)
-        self.row_bytes = self.pools[0].shape[2] * 2
-        self.key_offset, self.value_offset = int(key_offset), int(value_offset)
-        self.flags = DENSE_PAGES if dense else 0
-        self.int32, self.int64, self.float32 = torch.int32, torch.int64, torch.float32
-
-
-def _wrong(name: str, what: str):
-    return CpkvError("marshal", CPKV_ERR_ARG, f"{name}: {what} is wanted")
-
-
-def _rows(t, name: str, table: PoolTable):
-    """(address, elements between tokens, shape) of a [tokens, heads, dim]
-    tensor whose heads are contiguous within a token."""
-    if t.dtype != table.dtype or t.device != table.device:
-        raise _wrong(name, f"{table.dtype} on {table.device}")
-    shape, stride = t.shape, t.stride()
-    if len(shape) != 3:
-        raise _wrong(name, "[tokens, heads, dim]")
-    n, heads, dim = shape
-    between, of_heads, of_dim = stride
-    if of_dim != 1 or (of_heads != dim and heads > 1):
-        raise _wrong(name, "a token's heads side by side")
-    return t.data_ptr(), (between if n > 1 else max(between, heads * dim)), shape
-
-
-def _list_i32(t, name: str, table: PoolTable):
-    """(address, length) of a device list of int32."""
-    if t.dtype != table.int32 or t.device != table.device or t.dim() != 1 or not t.is_contiguous():
-        raise _wrong(name, f"a contiguous int32 list on {table.device}")
-    return t.data_ptr(), t.shape[0]
-
-
-def _page_rows(t, name: str, table: PoolTable, rows: int):
-    """(address, ids between requests, ids of a request) of a [requests, pages] table."""
-    if t.dtype != table.int32 or t.device != table.device:
-        raise _wrong(name, f"int32 on {table.device}")
-    shape, stride = t.shape, t.stride()
-    if len(shape) != 2 or shape[0] != rows or (stride[1] != 1 and shape[1] > 1):
-        raise _wrong(name, "a contiguous row of page ids per request")
-    if rows <= 1:
-        return t.data_ptr(), shape[1], shape[1]
-    if stride[0] < shape[1]:
-        raise _wrong(name, "rows that do not overlap")
-    return t.data_ptr(), stride[0], shape[1]
-
-
-def _results(out, lse, shape, table: PoolTable):
-    """(address of out, elements between tokens, address of lse or None)."""
-    at, between, got = _rows(out, "out", table)
-    if got != shape:
-        raise _wrong("out", "q's shape")
-    if lse is None:
-        return at, between, None
-    if lse.dtype != table.float32 or lse.device != table.device or lse.shape != shape[:2] or not lse.is_contiguous():
-        raise _wrong("lse", "contiguous float32 [tokens, heads]")
-    return at, between, lse.data_ptr()
-
-
-def _host_list(x):
-    """A contiguous int32 host array and its address."""
-    a = x if type(x) is np.ndarray and x.dtype == np.int32 and x.flags.c_contiguous else _host_i32(x)
-    return a, a.__array_interface__["data"][0]
+        self._table = _Table(self._addresses.ctypes.data, self._caps.ctypes.data, self.pools[0].shape[2] * 2,
+                             int(key_offset), int(value_offset), self.page_size, self.cp_size, code,
+                             DENSE_PAGES if dense else 0, self.device.index)
+        self.native = ctypes.addressof(self._table)
 
 
 def _handle(stream, table: PoolTable) -> int:
@@ -560,42 +533,9 @@ def cpkv_append_rotary(k, v, d_slots, d_positions, d_cos_sin, *, table: PoolTabl
     into ``q_out``.  ``d_positions``: [tokens], or [axes, tokens] with
     ``axis_of_freq`` naming each frequency's axis; ``d_cos_sin``: float32
     [positions, rot_dim], cosines then sines."""
-    kp, ks, (n, kv_heads, key_dim) = _rows(k, "k", table)
-    vp, vs, v_shape = _rows(v, "v", table)
-    if v_shape[0] != n or v_shape[1] != kv_heads:
-        raise _wrong("v", "k's tokens and heads")
-    qp = qop = None
-    qs = qos = q_heads = 0
-    if q is not None:
-        qp, qs, q_shape = _rows(q, "q", table)
-        qop, qos, out_shape = _rows(q_out, "q_out", table)
-        if q_shape != out_shape or q_shape[0] != n or q_shape[2] != key_dim:
-            raise _wrong("q and q_out", "k's tokens and width, alike")
-        q_heads = q_shape[1]
-    device = table.device
-    if d_slots.dtype != table.int64 or d_slots.device != device or d_slots.shape != (n,) or not d_slots.is_contiguous():
-        raise _wrong("slots", "a contiguous int64 list, a slot per token")
-    shape, stride = d_positions.shape, d_positions.stride()
-    if (d_positions.dtype != table.int32 or d_positions.device != device or len(shape) not in (1, 2) or shape[-1] != n
-            or (stride[-1] != 1 and n > 1)):
-        raise _wrong("positions", "int32 [tokens] or [axes, tokens]")
-    axes, between = (1, n) if len(shape) == 1 else (shape[0], stride[0])
-    table_shape = d_cos_sin.shape
-    if (d_cos_sin.dtype != table.float32 or d_cos_sin.device != device or len(table_shape) != 2
-            or not d_cos_sin.is_contiguous()):
-        raise _wrong("cos_sin", "contiguous float32 [positions, rot_dim]")
-    if axis_of_freq is not None:
-        axis_of_freq = bytes(axis_of_freq)
-        if len(axis_of_freq) != table_shape[1] // 2:
-            raise _wrong("axis_of_freq", "an axis per frequency")
-    rc = load().cpkv_append_rotary(
-        n, table.page_size, table.cp_size, table.code, q_heads, kv_heads, key_dim, v_shape[2], table.row_bytes,
-        table.key_offset, table.value_offset, table.addresses, table.caps, kp, ks, vp, vs, qp, qs, qop, qos,
-        d_slots.data_ptr(), d_positions.data_ptr(), between, axes, axis_of_freq, d_cos_sin.data_ptr(), table_shape[0],
-        table_shape[1], table.flags | ROTARY_INTERLEAVED if interleaved else table.flags, d_status.data_ptr(),
-        _handle(stream, table))
-    if rc:
-        _check("cpkv_append_rotary", rc)
+    _check("cpkv_append_rotary", serving().append_rotary(
+        table.native, k.shape[1], k.shape[2], v.shape[2], k, v, d_slots, d_positions, d_cos_sin, d_status, q, q_out,
+        None if axis_of_freq is None else bytes(axis_of_freq), interleaved, _handle(stream, table)))
 
 
 def cpkv_attend_window_workspace_bytes(B, q_heads, kv_heads, head_dim, q_lens, max_kv_len, window=0, sinks=0) -> int:
@@ -612,24 +552,9 @@ def cpkv_attend_window(q, q_lens, page_table, d_kv_lens, *, table: PoolTable, kv
                        scale, out, lse, workspace, d_status, stream=None):
     """Causal attention of ``q`` [tokens, heads, dim] over paged rows, with a
     window and first tokens that stay visible (see include/cpkv.h)."""
-    qp, qs, shape = _rows(q, "q", table)
-    op, os_, lp = _results(out, lse, shape, table)
-    lens, B = _list_i32(d_kv_lens, "kv_lens", table)
-    tp, ts, ids = _page_rows(page_table, "page_table", table, B)
-    if max_kv_len > ids * table.page_size:
-        raise CpkvError("cpkv_attend_window", CPKV_ERR_CAPACITY, "max_kv_len beyond the page table")
-    at = None
-    if q_lens is not None:
-        q_lens, at = _host_list(q_lens)
-        if q_lens.shape != (B,):
-            raise _wrong("q_lens", "a length per request")
-    wp, wb = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel())
-    rc = load().cpkv_attend_window(
-        B, table.page_size, table.cp_size, table.code, shape[1], kv_heads, shape[2], table.row_bytes, table.key_offset,
-        table.value_offset, at, max_kv_len, table.addresses, table.caps, tp, ts, lens, shape[0], qp, qs, scale, window,
-        sinks, op, os_, lp, wp, wb, table.flags, d_status.data_ptr(), _handle(stream, table))
-    if rc:
-        _check("cpkv_attend_window", rc)
+    _check("cpkv_attend_window", serving().attend_window(
+        table.native, kv_heads, q, q_lens, page_table, d_kv_lens, max_kv_len, window, sinks, scale, out, lse, workspace,
+        d_status, _handle(stream, table)))
 
 
 def cpkv_attend_shared_workspace_bytes(B, q_heads, kv_heads, head_dim, group_sizes, prefix_lens, max_suffix_len) -> int:
@@ -645,21 +570,6 @@ def cpkv_attend_shared(q, group_sizes, prefix_lens, prefix_pages, page_table, d_
                        kv_heads, max_suffix_len, scale, out, lse, workspace, d_status, stream=None):
     """One query token per request over its group's shared prefix and its own
     suffix (see include/cpkv.h)."""
-    qp, qs, shape = _rows(q, "q", table)
-    op, os_, lp = _results(out, lse, shape, table)
-    lens, B = _list_i32(d_suffix_lens, "suffix_lens", table)
-    tp, ts, ids = _page_rows(page_table, "page_table", table, B)
-    pp, prefix_ids = _list_i32(prefix_pages, "prefix_pages", table)
-    gs, gs_at = _host_list(group_sizes)
-    pl, pl_at = _host_list(prefix_lens)
-    if shape[0] != B or gs.shape != pl.shape or gs.ndim != 1:
-        raise _wrong("q, group_sizes and prefix_lens", "a query per request, a prefix length per group")
-    if max_suffix_len > ids * table.page_size:
-        raise CpkvError("cpkv_attend_shared", CPKV_ERR_CAPACITY, "max_suffix_len beyond the page table")
-    wp, wb = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel())
-    rc = load().cpkv_attend_shared(
-        B, gs.shape[0], table.page_size, table.cp_size, table.code, shape[1], kv_heads, shape[2], table.row_bytes,
-        table.key_offset, table.value_offset, gs_at, pl_at, max_suffix_len, table.addresses, table.caps, pp, prefix_ids,
-        tp, ts, lens, qp, qs, scale, op, os_, lp, wp, wb, table.flags, d_status.data_ptr(), _handle(stream, table))
-    if rc:
-        _check("cpkv_attend_shared", rc)
+    _check("cpkv_attend_shared", serving().attend_shared(
+        table.native, kv_heads, q, group_sizes, prefix_lens, prefix_pages, page_table, d_suffix_lens, max_suffix_len,
+        scale, out, lse, workspace, d_status, _handle(stream, table)))

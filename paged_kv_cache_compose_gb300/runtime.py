@@ -206,6 +206,7 @@ class PagedCache:
         self._workspaces = {}  # by stream
         self._outgrown = []  # a captured graph may still use them
         self._scale = self.key_dim ** -0.5
+        self._native = cpkv.serving()
         # the current stream's handle: torch's own accessor where it has one (a twentieth of current_stream())
         self._current = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
@@ -216,15 +217,15 @@ class PagedCache:
             return self._current(self.device.index)
         return torch.cuda.current_stream(self.device).cuda_stream
 
-    def _grow(self, stream: int, need: int, error):
-        """A larger workspace after ``error``, or the error where that was not its cause."""
+    def _grow(self, fn: str, rc: int, stream: int, size):
+        """A larger workspace where the call wants one; its error otherwise."""
         workspace = self._workspaces.get(stream)
+        need = size() if rc == cpkv.CPKV_ERR_CAPACITY else 0
         if need <= (0 if workspace is None else workspace.numel()):
-            raise error
+            cpkv._check(fn, rc)
         if workspace is not None:
             self._outgrown.append(workspace)
-        workspace = self._workspaces[stream] = self._empty((need + need // 4,), torch.uint8, stream)
-        return workspace
+        self._workspaces[stream] = self._empty((need + need // 4,), torch.uint8, stream)
 
     def _empty(self, shape, dtype, stream: int):
         """Memory of the stream that the call runs on."""
@@ -237,19 +238,23 @@ class PagedCache:
         ``positions`` and ``v`` into cache rows ``slots`` (page * page_size +
         offset; negative: padding), ``q`` rotated into ``q_out`` (allocated
         when None), which is returned."""
-        if k.shape[1:] != (self.kv_heads, self.key_dim) or v.shape[1:] != (self.kv_heads, self.value_dim):
-            raise cpkv.CpkvError("append_rotary", cpkv.CPKV_ERR_ARG, "k and v: [tokens, kv_heads, dim] of this cache")
         stream = self._stream(stream)
         if q is not None and q_out is None:
             q_out = self._empty(q.shape, q.dtype, stream)
-        cpkv.cpkv_append_rotary(k, v, slots, positions, cos_sin, table=self.table, d_status=self.d_status, q=q,
-                                q_out=q_out, axis_of_freq=axis_of_freq, interleaved=interleaved, stream=stream)
+        if axis_of_freq is not None:
+            axis_of_freq = bytes(axis_of_freq)
+        rc = self._native.append_rotary(self.table.native, self.kv_heads, self.key_dim, self.value_dim, k, v, slots,
+                                        positions, cos_sin, self.d_status, q, q_out, axis_of_freq, interleaved, stream)
+        if rc:
+            cpkv._check("cpkv_append_rotary", rc)
         return q_out
 
-    def _check_queries(self, q):
-        if q.dim() != 3 or q.shape[2] != self.key_dim or self.value_dim != self.key_dim:
+    def _results(self, q, out, stream: int):
+        """Where an attention's output goes."""
+        if self.value_dim != self.key_dim or q.dim() != 3 or q.shape[2] != self.key_dim:
             raise cpkv.CpkvError("attend", cpkv.CPKV_ERR_ARG,
                                  "q: [tokens, heads, key_dim] over a cache of equal key and value widths")
+        return self._empty(q.shape, q.dtype, stream) if out is None else out
 
     def attend_window(self, q, q_lens, page_table, kv_lens, *, max_kv_len: int, window: int = 0, sinks: int = 0,
                       scale: float | None = None, out=None, lse=None, stream=None):
@@ -257,24 +262,18 @@ class PagedCache:
         (None: one each) over its ``kv_lens[b]`` rows, those within ``window``
         and the first ``sinks``.  Returns ``out``; ``lse`` (float32 [tokens,
         heads]) is written when given."""
-        self._check_queries(q)
         stream = self._stream(stream)
-        if out is None:
-            out = self._empty(q.shape, q.dtype, stream)
+        out = self._results(q, out, stream)
         if scale is None:
             scale = self._scale
-        workspace = self._workspaces.get(stream)
         while True:
-            try:
-                cpkv.cpkv_attend_window(q, q_lens, page_table, kv_lens, table=self.table, kv_heads=self.kv_heads,
-                                        max_kv_len=max_kv_len, window=window, sinks=sinks, scale=scale, out=out,
-                                        lse=lse, workspace=workspace, d_status=self.d_status, stream=stream)
+            rc = self._native.attend_window(self.table.native, self.kv_heads, q, q_lens, page_table, kv_lens, max_kv_len,
+                                            window, sinks, scale, out, lse, self._workspaces.get(stream), self.d_status,
+                                            stream)
+            if not rc:
                 return out
-            except cpkv.CpkvError as e:
-                if e.code != cpkv.CPKV_ERR_CAPACITY:
-                    raise
-                workspace = self._grow(stream, cpkv.cpkv_attend_window_workspace_bytes(
-                    kv_lens.shape[0], q.shape[1], self.kv_heads, self.key_dim, q_lens, max_kv_len, window, sinks), e)
+            self._grow("cpkv_attend_window", rc, stream, lambda: cpkv.cpkv_attend_window_workspace_bytes(
+                kv_lens.shape[0], q.shape[1], self.kv_heads, self.key_dim, q_lens, max_kv_len, window, sinks))
 
     def attend_shared(self, q, group_sizes, prefix_lens, prefix_pages, page_table, suffix_lens, *,
                       max_suffix_len: int, scale: float | None = None, out=None, lse=None, stream=None):
@@ -282,23 +281,15 @@ class PagedCache:
         heads, dim] over each group's shared prefix (``prefix_pages``, CSR by
         group) and each request's own ``suffix_lens[b]`` rows.  Returns
         ``out``; ``lse`` as in ``attend_window``."""
-        self._check_queries(q)
         stream = self._stream(stream)
-        if out is None:
-            out = self._empty(q.shape, q.dtype, stream)
+        out = self._results(q, out, stream)
         if scale is None:
             scale = self._scale
-        workspace = self._workspaces.get(stream)
         while True:
-            try:
-                cpkv.cpkv_attend_shared(q, group_sizes, prefix_lens, prefix_pages, page_table, suffix_lens,
-                                        table=self.table, kv_heads=self.kv_heads, max_suffix_len=max_suffix_len,
-                                        scale=scale, out=out, lse=lse, workspace=workspace, d_status=self.d_status,
-                                        stream=stream)
+            rc = self._native.attend_shared(self.table.native, self.kv_heads, q, group_sizes, prefix_lens, prefix_pages,
+                                            page_table, suffix_lens, max_suffix_len, scale, out, lse,
+                                            self._workspaces.get(stream), self.d_status, stream)
+            if not rc:
                 return out
-            except cpkv.CpkvError as e:
-                if e.code != cpkv.CPKV_ERR_CAPACITY:
-                    raise
-                workspace = self._grow(stream, cpkv.cpkv_attend_shared_workspace_bytes(
-                    suffix_lens.shape[0], q.shape[1], self.kv_heads, self.key_dim, group_sizes, prefix_lens,
-                    max_suffix_len), e)
+            self._grow("cpkv_attend_shared", rc, stream, lambda: cpkv.cpkv_attend_shared_workspace_bytes(
+                suffix_lens.shape[0], q.shape[1], self.kv_heads, self.key_dim, group_sizes, prefix_lens, max_suffix_len))
