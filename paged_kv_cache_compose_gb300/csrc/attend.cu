@@ -86,52 +86,84 @@ struct SplitBounds {
   }
 };
 
-// Bounds and split of a tile pass.
+// Bounds and splits of a tile pass: ragged sequences, and (of a shared call) the
+// suffixes, of one query each.
 struct TileBounds {
   int64_t tokens = 0, tiles = 0, max_rows = 0, max_keys = 0;
-  int splits = 1;
+  int64_t singles = 0, single_keys = 0, single_tiles = 0, group = 1;
+  int splits = 1, single_splits = 1;
 
-  void add(int64_t nq, int64_t max_kv, int group, int window, int sinks) {
+  // Beginning and end of an item, and the joining of parts, in 128-key steps (about
+  // 4 us and 6 us against 1.4 us a step, measured).
+  static constexpr int64_t kItemSteps = 3, kJoinSteps = 4;
+
+  void add(int64_t nq, int64_t max_kv, int of_group, int window, int sinks) {
     int64_t seen = max_kv;
-    if (window > 0) seen = std::min<int64_t>(seen, (int64_t)window + kTileRows / group + sinks);
+    if (window > 0) seen = std::min<int64_t>(seen, (int64_t)window + kTileRows / of_group + sinks);
+    group = of_group;
     tiles += ceil_div(nq * group, kTileRows);
     tokens += nq;
     max_rows = std::max<int64_t>(max_rows, nq * group);
     max_keys = std::max<int64_t>(max_keys, seen);
   }
-  // How many parts an item's keys are cut into: the count whose rounds of blocks
-  // over the SMs come to the fewest key tiles, each round costing kItemTiles more for
-  // its beginning and end, and any parts kJoinTiles for joining them (both measured:
-  // about 4 us and 6 us against 1.4 us a key tile).
+  void add_singles(int64_t count, int64_t max_kv) {
+    singles = count;
+    single_keys = max_kv;
+    single_tiles = ceil_div(group, kTileRows);
+  }
+  // Steps over keys: two streams take the key tiles of at most 128 rows two at a time.
+  static int64_t steps(int64_t keys, int64_t rows) { return ceil_div(keys, rows <= 128 ? 2 * kTileKeys : kTileKeys); }
+  int check(int kv_heads) const {
+    const int64_t items = tiles * kv_heads, single_items = singles * single_tiles * kv_heads;
+    if (items > INT32_MAX / 1024 || single_items > INT32_MAX / 1024 || tokens > INT32_MAX) return CPKV_ERR_LIMIT;
+    return CPKV_OK;
+  }
+  // How many parts an item's keys are cut into: the count whose rounds of blocks over
+  // the SMs come to the fewest steps.
   int finish(int kv_heads, int head_dim) {
-    const int64_t items = tiles * kv_heads;
-    if (items > INT32_MAX / 2 || tokens > INT32_MAX) return CPKV_ERR_LIMIT;
-    constexpr int64_t kItemTiles = 3, kJoinTiles = 4;
-    // two streams take the key tiles of at most 128 rows two at a time
-    const int64_t sms = device_sm_count(), key_tiles = ceil_div(max_keys, max_rows <= 128 ? 2 * kTileKeys : kTileKeys);
+    const int64_t items = tiles * kv_heads, sms = device_sm_count(), all = steps(max_keys, max_rows);
     int64_t best = INT64_MAX / 16;
-    for (int64_t n = 1; n <= std::min<int64_t>(std::max<int64_t>(key_tiles / 2, 1), sms) && items > 0; ++n) {
+    for (int64_t n = 1; n <= std::min<int64_t>(std::max<int64_t>(all / 2, 1), sms) && items > 0; ++n) {
       if (n > 1 && items * n > 4 * sms) break;
-      // in 32nds of a key tile; a part of 256 rows of 128 written and read again is about one
-      const int64_t cost = 32 * ceil_div(items * n, sms) * (ceil_div(key_tiles, n) + kItemTiles) +
-                           (n > 1 ? 32 * kJoinTiles + items * n * head_dim / 128 : 0);
+      // in 32nds of a step; a part of 256 rows of 128 written and read again is about one
+      const int64_t cost = 32 * ceil_div(items * n, sms) * (ceil_div(all, n) + kItemSteps) +
+                           (n > 1 ? 32 * kJoinSteps + items * n * head_dim / 128 : 0);
       if (10 * cost < 9 * best) {  // for a tenth or more
         best = cost;
         splits = (int)n;
       }
     }
-    return CPKV_OK;
+    return check(kv_heads);
   }
-  int64_t slots(int kv_heads) const { return tiles * kv_heads * splits * kTileRows; }
+  // Prefixes and suffixes of a shared call: as few parts as leave no item longer than
+  // the SMs' even share of all work (a suffix counted at half its bound and a step).
+  int finish_shared(int kv_heads) {
+    const int64_t items = tiles * kv_heads, single_items = singles * single_tiles * kv_heads, sms = device_sm_count();
+    const int64_t all = steps(max_keys, max_rows), of_single = steps(single_keys, group);
+    const int64_t share = ceil_div(items * all + single_items * (ceil_div(of_single, 2) + 1), sms);
+    const int64_t most = std::max<int64_t>(share, 4);
+    splits = (int)std::min<int64_t>(std::max<int64_t>(ceil_div(all, most), 1), sms);
+    single_splits = (int)std::min<int64_t>(std::max<int64_t>(ceil_div(of_single, most), 1), sms);
+    return check(kv_heads);
+  }
+  int64_t blocks(int kv_heads) const { return kv_heads * (tiles * splits + singles * single_tiles * single_splits); }
+  int64_t ragged_rows(int kv_heads) const { return tiles * kv_heads * splits * kTileRows; }
+  int64_t rows(int kv_heads) const {
+    return ragged_rows(kv_heads) + singles * single_tiles * kv_heads * single_splits * std::min<int64_t>(group, kTileRows) + kTileRows;
+  }
   int64_t bytes(int kv_heads, int head_dim, bool direct) const {
     if (direct && splits == 1) return 0;
-    return round_up(slots(kv_heads) * 8, 256) + round_up(slots(kv_heads) * head_dim * 4, 256);
+    return round_up(rows(kv_heads) * 8, 256) + round_up(rows(kv_heads) * head_dim * 4, 256);
   }
   TileSpace space(char *at, int kv_heads) const {
     TileSpace s;
     s.ml = reinterpret_cast<float *>(at);
-    s.o = reinterpret_cast<float *>(at + round_up(slots(kv_heads) * 8, 256));
+    s.o = reinterpret_cast<float *>(at + round_up(rows(kv_heads) * 8, 256));
     s.splits = splits;
+    s.single_splits = single_splits;
+    s.items = (int)(tiles * kv_heads);
+    s.single_tiles = (int)single_tiles;
+    s.single_row = ragged_rows(kv_heads);
     return s;
   }
 };
@@ -173,10 +205,10 @@ int window_plan(WindowPlan *w, const HeadArgs &a, int B, const int32_t *h_q_lens
 }
 
 struct SharedPlan {
-  SplitBounds split;  // the suffixes, and the prefixes when rows are few
-  TileBounds tile;    // the prefixes when rows are many
+  SplitBounds split;  // prefixes and suffixes when rows are few
+  TileBounds tile;    // and when they are many
   bool few = true;
-  int64_t prefix_pages = 0, prefix_bytes = 0, bytes = 0;
+  int64_t prefix_pages = 0, bytes = 0;
 };
 
 int shared_plan(SharedPlan *w, const HeadArgs &a, int B, int n_groups, const int32_t *h_group_sizes,
@@ -193,13 +225,17 @@ int shared_plan(SharedPlan *w, const HeadArgs &a, int B, int n_groups, const int
   if (sum != B) return CPKV_ERR_ARG;
   if (w->prefix_pages > INT32_MAX) return CPKV_ERR_LIMIT;
   w->few = few_rows(w->tile.max_rows);
-  for (int g = 0; g < n_groups && w->few; ++g)
-    w->split.add(h_group_sizes[g], h_prefix_lens[g], group, 0, 0);
-  for (int b = 0; b < B; ++b) w->split.add(1, max_suffix, group, 0, 0);
-  int rc = w->split.finish(group, a.kv_heads);
-  if (!w->few && rc == CPKV_OK) rc = w->tile.finish(a.kv_heads, a.head_dim);
-  w->prefix_bytes = w->few ? 0 : w->tile.bytes(a.kv_heads, a.head_dim, false);
-  w->bytes = w->prefix_bytes + w->split.bytes(w->few ? n_groups + B : B, a.kv_heads, a.head_dim, false);
+  int rc;
+  if (w->few) {
+    for (int g = 0; g < n_groups; ++g) w->split.add(h_group_sizes[g], h_prefix_lens[g], group, 0, 0);
+    for (int b = 0; b < B; ++b) w->split.add(1, max_suffix, group, 0, 0);
+    rc = w->split.finish(group, a.kv_heads);
+    w->bytes = w->split.bytes(n_groups + B, a.kv_heads, a.head_dim, false);
+  } else {
+    w->tile.add_singles(B, max_suffix);
+    rc = w->tile.finish_shared(a.kv_heads);
+    w->bytes = w->tile.bytes(a.kv_heads, a.head_dim, false);
+  }
   return rc;
 }
 
@@ -213,23 +249,21 @@ int for_type_and_dim(const HeadArgs &a, F f) {
                            : f(__half(), std::integral_constant<int, 64>());
 }
 
-// Whole tiles (no join) where each sequence has `row_tiles` tiles; `dependent`:
-// another pass of the call goes before, whose results this one does not read.
-template <typename T, int D, typename S, bool kWhole>
-int split_pass(SplitParams<S> *p, const SplitBounds &b, bool dependent, cudaStream_t stream) {
-  const int smem = SplitShape<D>::kSmem + (kWhole ? 0 : (p->seqs.count + 1) * 4);
-  auto kernel = attend_split_kernel<T, D, S, kWhole>;
-  const int rc = ensure_dynamic_smem((const void *)kernel, SplitShape<D>::kSmem + (2 * CPKV_MAX_BATCH + 1) * 4);
+// A block takes a whole tile (row_tiles of each sequence) unless the mode is kLine.
+template <typename T, int D, SplitMode kMode, typename S>
+int split_pass(SplitParams<S> *p, const SplitBounds &b, cudaStream_t stream) {
+  using Shape = SplitShape<D, kMode>;
+  const int smem = Shape::kSmem + (kMode == kLine ? (p->seqs.count + 1) * 4 : 0);
+  auto kernel = attend_split_kernel<T, D, S, kMode>;
+  const int rc = ensure_dynamic_smem((const void *)kernel, Shape::kSmem + (kMode == kLine ? (2 * CPKV_MAX_BATCH + 1) * 4 : 0));
   if (rc != CPKV_OK) return rc;
-  if (kWhole) {
-    const int64_t blocks = (int64_t)p->seqs.count * p->io.kv_heads * p->row_tiles;
-    if (blocks > INT32_MAX) return CPKV_ERR_LIMIT;
-    return launch_kernel(kernel, dim3((unsigned)blocks), dim3(kSplitWarps * 32), smem, dependent, stream, *p);
+  int64_t blocks = (int64_t)p->seqs.count * p->io.kv_heads * p->row_tiles;
+  if (kMode == kLine) {  // as many blocks for every head as stay resident together
+    const int heads = p->io.kv_heads, resident = persistent_grid((const void *)kernel, kSplitWarps * 32, smem, 8, b.grid_cap);
+    blocks = p->space.grid = std::max(resident / heads, 1) * heads;
   }
-  // as many blocks for every head as stay resident together
-  const int heads = p->io.kv_heads, resident = persistent_grid((const void *)kernel, kSplitWarps * 32, smem, 8, b.grid_cap);
-  p->space.grid = std::max(resident / heads, 1) * heads;
-  return launch_kernel(kernel, dim3(p->space.grid), dim3(kSplitWarps * 32), smem, dependent, stream, *p);
+  if (blocks > INT32_MAX) return CPKV_ERR_LIMIT;
+  return launch_kernel(kernel, dim3((unsigned)blocks), dim3(kSplitWarps * 32), smem, false, stream, *p);
 }
 
 template <typename S>
@@ -263,8 +297,8 @@ EncodeTiled encode_tiled() {
 // the 128-byte swizzle of the kernel's shared memory.  Pages of 16 rows or a
 // multiple have them; others (and more than kTileMaps pools) leave box_rows 0,
 // and the kernel copies key by key.
-template <int N>
-void fill_maps(TileParams<N> *p) {
+template <typename S>
+void fill_maps(TileParams<S> *p) {
   const uint32_t ps = p->pools.page_size.d;
   p->box_rows = 0;
   if (ps % 16 != 0 || p->pools.cp.d > kTileMaps || encode_tiled() == nullptr) return;
@@ -283,9 +317,9 @@ void fill_maps(TileParams<N> *p) {
   p->box_rows = (int)box[1];
 }
 
-template <int N>
-void fill_tiles(TileParams<N> *p, const Seqs<N> &seqs, const PagedPools &pools, const AttendIo &io, const TileBounds &b,
-                char *workspace, bool direct) {
+template <typename S>
+void fill_tiles(TileParams<S> *p, const S &seqs, int ragged, const PagedPools &pools, const AttendIo &io,
+                const TileBounds &b, char *workspace, bool direct) {
   p->seqs = seqs;
   p->pools = pools;
   p->io = io;
@@ -294,44 +328,40 @@ void fill_tiles(TileParams<N> *p, const Seqs<N> &seqs, const PagedPools &pools, 
   p->wide_out = (reinterpret_cast<uintptr_t>(io.out) & 31) == 0 && io.out_stride % 32 == 0;
   fill_maps(p);
   const int group = io.group.d;
-  for (int s = 0; s < seqs.count; ++s) {
-    if (seqs.uniform_q == 0) {
-      p->cu_tiles[s + 1] = p->cu_tiles[s] + (int)ceil_div((int64_t)(seqs.cu_q[s + 1] - seqs.cu_q[s]) * group, kTileRows);
-    }
-  }
+  for (int s = 0; s < ragged; ++s)
+    p->cu_tiles[s + 1] = p->cu_tiles[s] + (int)ceil_div((int64_t)(seqs.cu_q[s + 1] - seqs.cu_q[s]) * group, kTileRows);
 }
 
-template <typename T, int D, int N>
-int tile_pass(const TileParams<N> &p, const TileBounds &b, cudaStream_t stream) {
-  auto kernel = attend_tile_kernel<T, D, N>;
+template <typename T, int D, typename S>
+int tile_pass(const TileParams<S> &p, const TileBounds &b, cudaStream_t stream) {
+  auto kernel = attend_tile_kernel<T, D, S>;
   const int rc = ensure_dynamic_smem((const void *)kernel, TileShape<D>::kSmem);
   if (rc != CPKV_OK) return rc;
-  const int64_t grid = b.tiles * p.io.kv_heads * b.splits;
-  if (grid == 0) return CPKV_OK;
+  const int64_t grid = b.blocks(p.io.kv_heads);
+  if (grid > INT32_MAX) return CPKV_ERR_LIMIT;
   return launch_kernel(kernel, dim3((unsigned)grid), dim3(kTileThreads), TileShape<D>::kSmem, false, stream, p);
 }
 
-template <int N>
-TileSource<N> source_of(const TileParams<N> &p) {
-  TileSource<N> s;
+template <typename S>
+TileSource<S> source_of(const TileParams<S> &p) {
+  TileSource<S> s;
   s.seqs = p.seqs;
   s.space = p.space;
-  std::copy(p.cu_tiles, p.cu_tiles + N + 1, s.cu_tiles);
+  std::copy(p.cu_tiles, p.cu_tiles + S::kArray + 1, s.cu_tiles);
   return s;
 }
 
 // Four warps a row while rows are too few to fill the SMs with a warp each.
-template <typename T, int D, typename A, typename B>
-int join_pass(const A &a, const B &b, const AttendIo &io, int64_t rows, cudaStream_t stream) {
-  JoinParams<A, B> p = {};
-  p.a = a;
-  p.b = b;
+template <typename T, int D, typename Source>
+int join_pass(const Source &source, const AttendIo &io, int64_t rows, cudaStream_t stream) {
+  JoinParams<Source> p = {};
+  p.source = source;
   p.io = io;
   p.rows = rows;
   const bool wide = rows <= (int64_t)device_sm_count() * 16;
   const int64_t blocks = wide ? rows : ceil_div(rows, 4);
   if (blocks > INT32_MAX) return CPKV_ERR_LIMIT;
-  auto kernel = wide ? attend_join_kernel<T, D, A, B, 4> : attend_join_kernel<T, D, A, B, 1>;
+  auto kernel = wide ? attend_join_kernel<T, D, Source, 4> : attend_join_kernel<T, D, Source, 1>;
   return launch_kernel(kernel, dim3((unsigned)blocks), dim3(128), 0, true, stream, p);
 }
 
@@ -348,7 +378,7 @@ int attend_window(const HeadArgs &heads, const Seqs<N> &seqs, const PagedPools &
     if (plan.whole) {
       p.row_tiles = (int)ceil_div((int64_t)seqs.uniform_q * io.group.d, kSplitRows);
       return for_type_and_dim(heads, [&](auto t, auto d) {
-        return split_pass<decltype(t), decltype(d)::value, Seqs<N>, true>(&p, plan.split, false, stream);
+        return split_pass<decltype(t), decltype(d)::value, kFewKeys>(&p, plan.split, stream);
       });
     }
     p.space = plan.split.space(workspace, seqs.count, heads.kv_heads, true);
@@ -356,58 +386,46 @@ int attend_window(const HeadArgs &heads, const Seqs<N> &seqs, const PagedPools &
     return for_type_and_dim(heads, [&](auto t, auto d) {
       using T = decltype(t);
       constexpr int D = decltype(d)::value;
-      const int rc = split_pass<T, D, Seqs<N>, false>(&p, plan.split, false, stream);
-      return rc != CPKV_OK ? rc : join_pass<T, D>(source_of(p), NoSource(), io, rows, stream);
+      const int rc = split_pass<T, D, kLine>(&p, plan.split, stream);
+      return rc != CPKV_OK ? rc : join_pass<T, D>(source_of(p), io, rows, stream);
     });
   }
-  TileParams<N> p = {};
-  fill_tiles(&p, seqs, pools, io, plan.tile, workspace, true);
+  TileParams<Seqs<N>> p = {};
+  fill_tiles(&p, seqs, seqs.count, pools, io, plan.tile, workspace, true);
   return for_type_and_dim(heads, [&](auto t, auto d) {
     using T = decltype(t);
     constexpr int D = decltype(d)::value;
-    const int rc = tile_pass<T, D, N>(p, plan.tile, stream);
-    return rc != CPKV_OK || p.direct ? rc : join_pass<T, D>(source_of(p), NoSource(), io, rows, stream);
+    const int rc = tile_pass<T, D>(p, plan.tile, stream);
+    return rc != CPKV_OK || p.direct ? rc : join_pass<T, D>(source_of(p), io, rows, stream);
   });
 }
 
-// Few query rows per prefix: prefixes and suffixes in one split pass.
+// Prefixes and suffixes in one pass, joined.
 template <int N>
-int attend_shared_few(const HeadArgs &heads, const SharedSeqs<N> &seqs, const PagedPools &pools, const AttendIo &io,
-                      const SharedPlan &plan, char *workspace, cudaStream_t stream) {
-  SplitParams<SharedSeqs<N>> p = {};
-  p.seqs = seqs;
-  p.pools = pools;
-  p.io = io;
-  p.space = plan.split.space(workspace, seqs.count, heads.kv_heads, false);
-  p.tiles_cap = plan.split.tiles_cap;
+int attend_shared(const HeadArgs &heads, const SharedSeqs<N> &seqs, const PagedPools &pools, const AttendIo &io,
+                  const SharedPlan &plan, char *workspace, cudaStream_t stream) {
+  const int64_t rows = (int64_t)(seqs.count - seqs.groups) * heads.q_heads;
+  if (plan.few) {
+    SplitParams<SharedSeqs<N>> p = {};
+    p.seqs = seqs;
+    p.pools = pools;
+    p.io = io;
+    p.space = plan.split.space(workspace, seqs.count, heads.kv_heads, false);
+    p.tiles_cap = plan.split.tiles_cap;
+    return for_type_and_dim(heads, [&](auto t, auto d) {
+      using T = decltype(t);
+      constexpr int D = decltype(d)::value;
+      const int rc = split_pass<T, D, kLine>(&p, plan.split, stream);
+      return rc != CPKV_OK ? rc : join_pass<T, D>(source_of(p), io, rows, stream);
+    });
+  }
+  TileParams<SharedSeqs<N>> p = {};
+  fill_tiles(&p, seqs, seqs.groups, pools, io, plan.tile, workspace, false);
   return for_type_and_dim(heads, [&](auto t, auto d) {
     using T = decltype(t);
     constexpr int D = decltype(d)::value;
-    const int rc = split_pass<T, D, SharedSeqs<N>, false>(&p, plan.split, false, stream);
-    const int64_t rows = (int64_t)(seqs.count - seqs.groups) * heads.q_heads;
-    return rc != CPKV_OK ? rc : join_pass<T, D>(source_of(p), NoSource(), io, rows, stream);
-  });
-}
-
-template <int N>
-int attend_shared_many(const HeadArgs &heads, const Seqs<N> &prefix, const Seqs<kFewSeqs> &suffix,
-                       const PagedPools &pools, const AttendIo &io, const SharedPlan &plan, char *workspace,
-                       cudaStream_t stream) {
-  SplitParams<Seqs<kFewSeqs>> sp = {};
-  sp.seqs = suffix;
-  sp.pools = pools;
-  sp.io = io;
-  sp.space = plan.split.space(workspace + plan.prefix_bytes, suffix.count, heads.kv_heads, false);
-  sp.tiles_cap = plan.split.tiles_cap;
-  TileParams<N> pp = {};
-  fill_tiles(&pp, prefix, pools, io, plan.tile, workspace, false);
-  return for_type_and_dim(heads, [&](auto t, auto d) {
-    using T = decltype(t);
-    constexpr int D = decltype(d)::value;
-    int rc = tile_pass<T, D, N>(pp, plan.tile, stream);
-    if (rc == CPKV_OK) rc = split_pass<T, D, Seqs<kFewSeqs>, false>(&sp, plan.split, true, stream);
-    const int64_t rows = (int64_t)suffix.count * heads.q_heads;
-    return rc != CPKV_OK ? rc : join_pass<T, D>(source_of(sp), source_of(pp), io, rows, stream);
+    const int rc = tile_pass<T, D>(p, plan.tile, stream);
+    return rc != CPKV_OK ? rc : join_pass<T, D>(source_of(p), io, rows, stream);
   });
 }
 
@@ -535,45 +553,25 @@ extern "C" int cpkv_attend_shared(int B, int n_groups, int page_size, int cp_siz
   if (rc != CPKV_OK) return rc;
   if (workspace_bytes < plan.bytes) return CPKV_ERR_CAPACITY;
   if (d_workspace == nullptr || !aligned16(d_workspace)) return CPKV_ERR_ARG;
-  char *const space = static_cast<char *>(d_workspace);
-  auto groups = [&](auto *s) {
-    s->status = d_status;
-    int pages = 0;
-    for (int g = 0; g < n_groups; ++g) {
-      s->cu_q[g + 1] = s->cu_q[g] + h_group_sizes[g];
-      s->kv[g] = h_prefix_lens[g];
-      s->page0[g] = pages;
-      pages += h_prefix_lens[g] / page_size;
-    }
-  };
   auto go = [&](auto n) {
     constexpr int N = decltype(n)::value;
-    if (plan.few) {
-      SharedSeqs<N> s = {};
-      groups(&s);
-      s.prefix_pages = d_prefix_pages;
-      s.table = d_page_table;
-      s.suffix_lens = d_suffix_lens;
-      s.stride = table_stride;
-      s.count = n_groups + B;
-      s.groups = n_groups;
-      s.suffix_cap = (int)max_suffix_len;
-      return attend_shared_few<N>(heads, s, pools, io, plan, space, (cudaStream_t)stream);
+    SharedSeqs<N> s = {};
+    s.prefix_pages = d_prefix_pages;
+    s.table = d_page_table;
+    s.suffix_lens = d_suffix_lens;
+    s.stride = table_stride;
+    s.status = d_status;
+    s.count = n_groups + B;
+    s.groups = n_groups;
+    s.suffix_cap = (int)max_suffix_len;
+    int pages = 0;
+    for (int g = 0; g < n_groups; ++g) {
+      s.cu_q[g + 1] = s.cu_q[g] + h_group_sizes[g];
+      s.kv[g] = h_prefix_lens[g];
+      s.page0[g] = pages;
+      pages += h_prefix_lens[g] / page_size;
     }
-    Seqs<N> prefix = {};
-    groups(&prefix);
-    prefix.table = d_prefix_pages;
-    prefix.stride = -1;
-    prefix.count = n_groups;
-    Seqs<kFewSeqs> suffix = {};
-    suffix.kv_lens = d_suffix_lens;
-    suffix.table = d_page_table;
-    suffix.stride = table_stride;
-    suffix.status = d_status;
-    suffix.count = B;
-    suffix.uniform_q = 1;
-    suffix.kv_cap = (int)max_suffix_len;
-    return attend_shared_many<N>(heads, prefix, suffix, pools, io, plan, space, (cudaStream_t)stream);
+    return attend_shared<N>(heads, s, pools, io, plan, static_cast<char *>(d_workspace), (cudaStream_t)stream);
   };
   if (n_groups <= kFewSeqs) return go(std::integral_constant<int, kFewSeqs>());
   return go(std::integral_constant<int, CPKV_MAX_BATCH>());

@@ -28,6 +28,7 @@ constexpr float kLn2 = 0.6931471805599453f;
 // kv_lens (device) wins over kv where given.
 template <int N>
 struct Seqs {
+  static constexpr int kArray = N;
   const int32_t *kv_lens;  // device lengths, clamped to [0, kv_cap]; null: kv[s]
   const int32_t *table;    // page ids: row s at s * stride, or at page0[s] when stride < 0
   int64_t stride;
@@ -48,6 +49,8 @@ struct Seqs {
   }
   CPKV_DEV bool kv_len_bad(int s) const { return kv_lens != nullptr && (kv_lens[s] < 0 || kv_lens[s] > kv_cap); }
   CPKV_DEV const int32_t *pages(int s) const { return stride < 0 ? table + page0[s] : table + s * stride; }
+  // Sequences with lengths of their own queries; the others have one query each.
+  CPKV_DEV int ragged() const { return count; }
   // Tiles of 16 packed rows before sequence s, at most.
   CPKV_DEV int64_t tiles_before(int s, int group) const { return (int64_t)q_begin(s) * group / 16 + s; }
   // The sequences that hold a query token, and where it stands in them.
@@ -63,6 +66,7 @@ struct Seqs {
 // own suffix).
 template <int N>
 struct SharedSeqs {
+  static constexpr int kArray = N;
   const int32_t *prefix_pages, *table, *suffix_lens;
   int64_t stride;
   int32_t *status;
@@ -85,6 +89,7 @@ struct SharedSeqs {
   CPKV_DEV const int32_t *pages(int s) const {
     return s < groups ? prefix_pages + page0[s] : table + (s - groups) * stride;
   }
+  CPKV_DEV int ragged() const { return groups; }
   CPKV_DEV int64_t tiles_before(int s, int group) const {
     if (s < groups) return (int64_t)cu_q[s] * group / 16 + s;
     return (int64_t)(count - groups) * group / 16 + groups + (int64_t)(s - groups) * ((group + 15) / 16);

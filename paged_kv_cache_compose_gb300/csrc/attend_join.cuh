@@ -29,8 +29,8 @@ CPKV_DEV Spot find_spot(const SplitSource<S> &src, const AttendIo &io, int s, in
   return Spot{s, row / kSplitRows, row % kSplitRows, keys.n_tiles};
 }
 
-template <int N>
-CPKV_DEV Spot find_spot(const TileSource<N> &src, const AttendIo &io, int s, int i, int g) {
+template <typename S>
+CPKV_DEV Spot find_spot(const TileSource<S> &src, const AttendIo &io, int s, int i, int g) {
   const int row = i * (int)io.group.d + g;
   return Spot{s, row / kTileRows, row % kTileRows, 0};
 }
@@ -61,19 +61,25 @@ CPKV_DEV bool find_parts(Parts *r, const SplitSource<S> &src, const AttendIo &io
   return true;
 }
 
-template <int N>
-CPKV_DEV bool find_parts(Parts *r, const TileSource<N> &src, const AttendIo &io, const Spot &at, int h) {
-  const int64_t item = (int64_t)(src.cu_tiles[at.s] + at.rt) * io.kv_heads + h;
-  r->ml = src.space.ml;
-  r->o = src.space.o;
-  r->first = item * src.space.splits * kTileRows + at.in_tile;
-  r->step = kTileRows;
-  r->next = r->first + kTileRows;
-  r->count = src.space.splits;
+template <typename S>
+CPKV_DEV bool find_parts(Parts *r, const TileSource<S> &src, const AttendIo &io, const Spot &at, int h) {
+  const TileSpace &space = src.space;
+  r->ml = space.ml;
+  r->o = space.o;
+  if (at.s < src.seqs.ragged()) {
+    const int64_t item = (int64_t)(src.cu_tiles[at.s] + at.rt) * io.kv_heads + h;
+    r->count = space.splits;
+    r->step = kTileRows;
+    r->first = item * space.splits * kTileRows + at.in_tile;
+  } else {
+    const int64_t item = ((int64_t)(at.s - src.seqs.ragged()) * io.kv_heads + h) * space.single_tiles + at.rt;
+    r->count = space.single_splits;
+    r->step = single_rows(io.group.d);
+    r->first = space.single_row + item * space.single_splits * r->step + at.in_tile;
+  }
+  r->next = r->first + r->step;
   return true;
 }
-
-struct NoSource {};
 
 // The places of a query row in a pass.
 struct Spots {
@@ -92,11 +98,9 @@ CPKV_DEV Spots find_spots(const Source &src, const AttendIo &io, int token, int 
   return r;
 }
 
-// `a`: a pass over the query tokens; `b`: a second one over the same, or none.
-template <typename A, typename B>
+template <typename Source>
 struct JoinParams {
-  A a;
-  B b;
+  Source source;
   AttendIo io;
   int64_t rows;  // tokens * q_heads
 };
@@ -105,25 +109,22 @@ struct JoinParams {
 // lane takes one part of a batch of 32: its maximum and sum, then its weight and
 // address, which go round as the warps add the parts' values, every kWarps-th one
 // each.  Latency bounds it (a few hundred to some thousand rows, a chain of three
-// reads from L2), so one batch holds the parts of both passes.
-template <typename T, int D, typename A, typename B, int kWarps>
-__global__ void __launch_bounds__(128) attend_join_kernel(const __grid_constant__ JoinParams<A, B> p) {
+// reads from L2), so one batch holds a row's parts of prefix and suffix.
+template <typename T, int D, typename Source, int kWarps>
+__global__ void __launch_bounds__(128) attend_join_kernel(const __grid_constant__ JoinParams<Source> p) {
   constexpr int kEach = D / 32;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, part_of = kWarps == 1 ? 0 : warp;
   const int64_t row = kWarps == 1 ? (int64_t)blockIdx.x * 4 + warp : (int64_t)blockIdx.x;
   if (row >= p.rows) return;
   const int token = (int)(row / p.io.q_heads), head = (int)(row - (int64_t)token * p.io.q_heads);
   const int h = div_by(head, p.io.group), g = head - h * (int)p.io.group.d;
-  const Spots a = find_spots(p.a, p.io, token, g);
-  Spots b = {};
-  if constexpr (!std::is_same<B, NoSource>::value) b = find_spots(p.b, p.io, token, g);
+  const Spots spots = find_spots(p.source, p.io, token, g);
   wait_prerequisite();
-  Parts parts[3] = {};
+  Parts parts[2] = {};
 #pragma unroll
   for (int k = 0; k < 2; ++k)
-    if (k < a.count && !find_parts(&parts[k], p.a, p.io, a.at[k], h)) return;
-  if constexpr (!std::is_same<B, NoSource>::value) find_parts(&parts[2], p.b, p.io, b.at[0], h);
-  const int c0 = parts[0].count, c1 = c0 + parts[1].count, count = c1 + parts[2].count;
+    if (k < spots.count && !find_parts(&parts[k], p.source, p.io, spots.at[k], h)) return;
+  const int c0 = parts[0].count, count = c0 + parts[1].count;
 
   float m = -INFINITY, l = 0.f, o[kEach] = {};
   for (int k0 = 0; k0 < count; k0 += 32) {
@@ -131,8 +132,8 @@ __global__ void __launch_bounds__(128) attend_join_kernel(const __grid_constant_
     float2 v = make_float2(-INFINITY, 0.f);
     const float *values = nullptr;
     if (k < count) {
-      const Parts &at = k < c0 ? parts[0] : k < c1 ? parts[1] : parts[2];
-      const int64_t r = at.row(k - (k < c0 ? 0 : k < c1 ? c0 : c1));
+      const Parts &at = k < c0 ? parts[0] : parts[1];
+      const int64_t r = at.row(k < c0 ? k : k - c0);
       v = *reinterpret_cast<const float2 *>(at.ml + r * 2);
       values = at.o + r * D;
     }

@@ -13,9 +13,9 @@
 // side by side in its row, and read together they cost DRAM one page opening
 // (64 requests of 4100 keys, 8 heads of 64: 120 us when a block's stretch ran from
 // one head into the next, 106 us so).  Warps, not stages, hide the rest: two stages
-// and as many blocks as registers allow take 100 us, four stages and three blocks 106.  Where every
-// sequence has few keys
-// (kWhole) a block takes one whole tile instead and nothing is left to join.
+// and as many blocks as registers allow take 100 us, four stages and three blocks 106.
+// Where every sequence has few keys
+// a block takes one whole tile instead and nothing is left to join.
 #pragma once
 
 #include "attend.cuh"
@@ -25,39 +25,43 @@ namespace cpkv {
 constexpr int kSplitWarps = 4;
 constexpr int kWarpKeys = kSplitTile / kSplitWarps;  // 16
 
-template <int D>
+// How a block finds its work: a stretch of the line of units, or one tile of few keys
+// (with a deeper ring: its time is that of a few loads).
+enum SplitMode { kLine, kFewKeys };
+
+template <int D, SplitMode kMode>
 struct SplitShape {
   static constexpr int kRow = D * 2;                       // bytes of a key (or value) vector
   static constexpr int kStage = kWarpKeys * kRow * 2;      // keys, then values
-  static constexpr int kStages = 2;
-  static constexpr int kBlocks = D == 128 ? 3 : 5;         // blocks to an SM
+  static constexpr int kStages = kMode == kFewKeys ? 5 : 2;
+  static constexpr int kBlocks = kMode == kFewKeys ? 1 : D == 128 ? 3 : 5;  // blocks to an SM
   static constexpr int kRing = kSplitWarps * kStages * kStage;
   static constexpr int kJoin = kSplitRows * D * 4;         // half the columns of two warps while a tile's parts are joined
   static constexpr int kSmem = kRing + kJoin + kSplitWarps * kSplitRows * 8;
 };
 
 // A position on the line of units.
-template <typename S>
+template <typename P>
 struct Cursor {
   int s, rt, j, row_tiles;
   int nq, kv;
   KeyRange keys;
 
-  CPKV_DEV void enter(const SplitParams<S> &p, int seq) {
+  CPKV_DEV void enter(const P &p, int seq) {
     s = seq;
     nq = p.seqs.q_count(s);
     kv = p.seqs.kv_len(s);
     keys = key_range<kSplitTile>(kv, nq, 0, nq, p.seqs.causal, p.seqs.window, p.seqs.sinks);
     row_tiles = (nq * (int)p.io.group.d + kSplitRows - 1) / kSplitRows;
   }
-  CPKV_DEV void seek(const SplitParams<S> &p, const int *cum, int u) {
+  CPKV_DEV void seek(const P &p, const int *cum, int u) {
     enter(p, upper_index(cum, p.seqs.count, u));
     const int local = u - cum[s];
     rt = local / keys.n_tiles;
     j = local - rt * keys.n_tiles;
   }
   // To the next unit of the line; there must be one.
-  CPKV_DEV void advance(const SplitParams<S> &p) {
+  CPKV_DEV void advance(const P &p) {
     if (++j < keys.n_tiles) return;
     j = 0;
     if (++rt < row_tiles) return;
@@ -68,9 +72,11 @@ struct Cursor {
   }
 };
 
-template <typename T, int D, typename S, bool kWhole>
-__global__ void __launch_bounds__(kSplitWarps * 32, SplitShape<D>::kBlocks) attend_split_kernel(const __grid_constant__ SplitParams<S> p) {
-  using Shape = SplitShape<D>;
+template <typename T, int D, typename S, SplitMode kMode>
+__global__ void __launch_bounds__(kSplitWarps * 32, SplitShape<D, kMode>::kBlocks) attend_split_kernel(const __grid_constant__ SplitParams<S> p) {
+  using Shape = SplitShape<D, kMode>;
+  using P = SplitParams<S>;
+  constexpr bool kWhole = kMode != kLine;
   extern __shared__ __align__(128) char smem[];
   __shared__ int scan_scratch[33];
   int *cum = reinterpret_cast<int *>(smem + Shape::kSmem);
@@ -79,7 +85,7 @@ __global__ void __launch_bounds__(kSplitWarps * 32, SplitShape<D>::kBlocks) atte
 
   release_dependents();  // the joining kernel, which waits for this one
   const int head = (int)blockIdx.x % p.io.kv_heads;  // key/value head
-  Cursor<S> ld;
+  Cursor<P> ld;
   int u0, u1;
   if constexpr (kWhole) {
     const int tile = (int)blockIdx.x / p.io.kv_heads;
@@ -97,7 +103,7 @@ __global__ void __launch_bounds__(kSplitWarps * 32, SplitShape<D>::kBlocks) atte
       const int s = s0 + (int)threadIdx.x;
       int mine = 0;
       if (s < count) {
-        Cursor<S> c;
+        Cursor<P> c;
         c.enter(p, s);
         mine = c.keys.n_tiles * c.row_tiles;
         if (blockIdx.x == 0 && p.seqs.kv_len_bad(s)) raise_status(p.seqs.status, CPKV_STATUS_OUT_CAPACITY);
@@ -131,7 +137,7 @@ __global__ void __launch_bounds__(kSplitWarps * 32, SplitShape<D>::kBlocks) atte
   // loads: lanes 0..15 own one key each.  A row is read once by its head's one tile of
   // rows (or few): it makes room in L2 before the parts do.
   const uint64_t once = l2_policy_evict_first();
-  Cursor<S> at = ld;
+  Cursor<P> at = ld;
   int ld_u = u0, ld_key = 0, ld_page = -1;
   bool ld_sees = false;
   auto look_up = [&] {  // the page of this lane's key, one unit ahead of its copy
@@ -183,39 +189,130 @@ __global__ void __launch_bounds__(kSplitWarps * 32, SplitShape<D>::kBlocks) atte
   RowMask mask[2];
   int full_lo = 0, full_hi = 0;  // keys in [full_lo, full_hi) are seen by every row of the tile
 
-  for (int u = u0; u < u1; ++u) {
-    if (fresh) {
-      fresh = false;
-      seg_j0 = at.j;
+  // A tile's rows from here on.
+  auto begin_tile = [&] {
+    seg_j0 = at.j;
+    const int group = p.io.group.d, rows = at.nq * group;
+    const int q0 = p.seqs.q_begin(at.s);
+    int last = at.rt * kSplitRows + kSplitRows - 1;
+    if (last >= rows) last = rows - 1;
+    const RowMask ma = row_mask(at.kv, at.nq, div_by(at.rt * kSplitRows, p.io.group), p.seqs.causal, p.seqs.window, p.seqs.sinks);
+    const RowMask mb = row_mask(at.kv, at.nq, div_by(last, p.io.group), p.seqs.causal, p.seqs.window, p.seqs.sinks);
+    full_hi = ma.hi;
+    full_lo = mb.lo;
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      const int row = at.rt * kSplitRows + (lane >> 2) + 8 * r;
+      const bool in = row < rows;
+      const int i = div_by(row, p.io.group), g = row - i * group;
+      mask[r] = row_mask(at.kv, at.nq, i, p.seqs.causal, p.seqs.window, p.seqs.sinks);
+      const char *src = p.io.q + (q0 + i) * p.io.q_stride + ((int64_t)head * group + g) * Shape::kRow + (lane & 3) * 4;
+#pragma unroll
+      for (int k = 0; k < D / 16; ++k) {
+        qf[k][r] = in ? *reinterpret_cast<const uint32_t *>(src + k * 32) : 0u;
+        qf[k][r + 2] = in ? *reinterpret_cast<const uint32_t *>(src + k * 32 + 16) : 0u;
+      }
+      m[r] = -INFINITY;
+      l[r] = 0.f;
+    }
+#pragma unroll
+    for (int n = 0; n < D / 8; ++n)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) o[n][i] = 0.f;
+  };
+  // The end of a tile or of this block's stretch of it: `complete` when the block held it whole.
+  auto end_tile = [&](bool complete) {
+    // join the four warps' parts: common maximum, then values pairwise
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
+      l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
+      if ((lane & 3) == 0) ml[warp * kSplitRows + (lane >> 2) + 8 * r] = make_float2(m[r], l[r]);
+    }
+    __syncthreads();
+    float big[2], sum[2];
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      const int row = (lane >> 2) + 8 * r;
+      float2 v[kSplitWarps];
+      big[r] = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < kSplitWarps; ++w) {
+        v[w] = ml[w * kSplitRows + row];
+        big[r] = fmaxf(big[r], v[w].x);
+      }
+      const float base = big[r] == -INFINITY ? 0.f : big[r];
+      sum[r] = 0.f;
+#pragma unroll
+      for (int w = 0; w < kSplitWarps; ++w) sum[r] += exp2_approx(v[w].x - base) * v[w].y;
+      const float mine = exp2_approx(m[r] - base);
+#pragma unroll
+      for (int n = 0; n < D / 8; ++n) {
+        o[n][2 * r] *= mine;
+        o[n][2 * r + 1] *= mine;
+      }
+    }
+    auto each = [&](int columns, float *buf, bool put) {
+#pragma unroll
+      for (int n = 0; n < D / 16; ++n)
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          float2 *q = reinterpret_cast<float2 *>(buf + (n * 32 + lane) * 4 + 2 * r);
+          float *mine = o[columns * (D / 16) + n] + 2 * r;
+          if (put) {
+            *q = make_float2(mine[0], mine[1]);
+          } else {
+            mine[0] += q->x;
+            mine[1] += q->y;
+          }
+        }
+    };
+    float *const upper = join + kSplitRows * D / 2;
+#pragma unroll
+    for (int columns = 0; columns < 2; ++columns) {
+      if (warp >= 2) each(columns, warp == 2 ? join : upper, true);
+      __syncthreads();
+      if (warp < 2) each(columns, warp == 0 ? join : upper, false);
+      if (warp == 1) each(columns, upper, true);
+      __syncthreads();
+      if (warp == 0) each(columns, upper, false);
+      __syncthreads();
+    }
+    if (warp == 0) {
       const int group = p.io.group.d, rows = at.nq * group;
-      full_lo = 0;
-      full_hi = INT32_MAX;
-      const int q0 = p.seqs.q_begin(at.s);
-      int last = at.rt * kSplitRows + kSplitRows - 1;
-      if (last >= rows) last = rows - 1;
-      const RowMask ma = row_mask(at.kv, at.nq, div_by(at.rt * kSplitRows, p.io.group), p.seqs.causal, p.seqs.window, p.seqs.sinks);
-      const RowMask mb = row_mask(at.kv, at.nq, div_by(last, p.io.group), p.seqs.causal, p.seqs.window, p.seqs.sinks);
-      full_hi = ma.hi;
-      full_lo = mb.lo;
+      const int64_t slot = complete ? 2 * (int64_t)gridDim.x + head * p.tiles_cap + p.seqs.tiles_before(at.s, group) + at.rt
+                                    : 2 * (int64_t)blockIdx.x + (first_segment ? 0 : 1);
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
-        const int row = at.rt * kSplitRows + (lane >> 2) + 8 * r;
-        const bool in = row < rows;
-        const int i = div_by(row, p.io.group), g = row - i * group;
-        mask[r] = row_mask(at.kv, at.nq, i, p.seqs.causal, p.seqs.window, p.seqs.sinks);
-        const char *src = p.io.q + (q0 + i) * p.io.q_stride + ((int64_t)head * group + g) * Shape::kRow + (lane & 3) * 4;
+        const int in_tile = (lane >> 2) + 8 * r, row = at.rt * kSplitRows + in_tile;
+        if (row >= rows) continue;
+        if (complete && p.direct) {
+          const int i = div_by(row, p.io.group), g = row - i * group;
+          const int64_t token = p.seqs.q_begin(at.s) + i;
+          const int q_head = head * group + g;
+          const float inv = row_scale(sum[r]);
+          char *dst = p.io.out + token * p.io.out_stride + (int64_t)q_head * Shape::kRow + (lane & 3) * 4;
 #pragma unroll
-        for (int k = 0; k < D / 16; ++k) {
-          qf[k][r] = in ? *reinterpret_cast<const uint32_t *>(src + k * 32) : 0u;
-          qf[k][r + 2] = in ? *reinterpret_cast<const uint32_t *>(src + k * 32 + 16) : 0u;
+          for (int n = 0; n < D / 8; ++n)
+            *reinterpret_cast<uint32_t *>(dst + n * 16) = pack2<T>(o[n][2 * r] * inv, o[n][2 * r + 1] * inv);
+          if (p.io.lse != nullptr && (lane & 3) == 0)
+            p.io.lse[token * p.io.q_heads + q_head] = row_lse(big[r], sum[r]);
+        } else {
+          float *dst = p.space.o + (slot * kSplitRows + in_tile) * D + (lane & 3) * 2;
+#pragma unroll
+          for (int n = 0; n < D / 8; ++n) *reinterpret_cast<float2 *>(dst + n * 8) = make_float2(o[n][2 * r], o[n][2 * r + 1]);
+          if ((lane & 3) == 0)
+            *reinterpret_cast<float2 *>(p.space.ml + (slot * kSplitRows + in_tile) * 2) = make_float2(big[r], sum[r]);
         }
-        m[r] = -INFINITY;
-        l[r] = 0.f;
       }
-#pragma unroll
-      for (int n = 0; n < D / 8; ++n)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) o[n][i] = 0.f;
+    }
+  };
+
+  if constexpr (kWhole) begin_tile();
+  for (int u = u0; u < u1; ++u) {
+    if (!kWhole && fresh) {
+      fresh = false;
+      begin_tile();
     }
     cp_async_wait<Shape::kStages - 2>();
     __syncwarp();
@@ -286,119 +383,19 @@ __global__ void __launch_bounds__(kSplitWarps * 32, SplitShape<D>::kBlocks) atte
     __syncwarp();
     stage = stage + 1 == Shape::kStages ? 0 : stage + 1;
 
-    const bool tile_ends = kWhole ? u + 1 == u1 : at.j + 1 == at.keys.n_tiles;
-    if (!tile_ends && u + 1 < u1) {
+    const bool tile_ends = at.j + 1 == at.keys.n_tiles;
+    if (kWhole || (!tile_ends && u + 1 < u1)) {
       ++at.j;
       continue;
     }
+    end_tile(tile_ends && seg_j0 == 0);
 
-    // join the four warps' parts: common maximum, then values pairwise
-#pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
-      l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
-      if ((lane & 3) == 0) ml[warp * kSplitRows + (lane >> 2) + 8 * r] = make_float2(m[r], l[r]);
-    }
-    __syncthreads();
-    float big[2], sum[2];
-#pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      const int row = (lane >> 2) + 8 * r;
-      float2 v[kSplitWarps];
-      big[r] = -INFINITY;
-#pragma unroll
-      for (int w = 0; w < kSplitWarps; ++w) {
-        v[w] = ml[w * kSplitRows + row];
-        big[r] = fmaxf(big[r], v[w].x);
-      }
-      const float base = big[r] == -INFINITY ? 0.f : big[r];
-      sum[r] = 0.f;
-#pragma unroll
-      for (int w = 0; w < kSplitWarps; ++w) sum[r] += exp2_approx(v[w].x - base) * v[w].y;
-      const float mine = exp2_approx(m[r] - base);
-#pragma unroll
-      for (int n = 0; n < D / 8; ++n) {
-        o[n][2 * r] *= mine;
-        o[n][2 * r + 1] *= mine;
-      }
-    }
-    auto each = [&](int columns, float *buf, bool put) {
-#pragma unroll
-      for (int n = 0; n < D / 16; ++n)
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          float2 *q = reinterpret_cast<float2 *>(buf + (n * 32 + lane) * 4 + 2 * r);
-          float *mine = o[columns * (D / 16) + n] + 2 * r;
-          if (put) {
-            *q = make_float2(mine[0], mine[1]);
-          } else {
-            mine[0] += q->x;
-            mine[1] += q->y;
-          }
-        }
-    };
-    float *const upper = join + kSplitRows * D / 2;
-#pragma unroll
-    for (int columns = 0; columns < 2; ++columns) {
-      if (warp >= 2) each(columns, warp == 2 ? join : upper, true);
-      __syncthreads();
-      if (warp < 2) each(columns, warp == 0 ? join : upper, false);
-      if (warp == 1) each(columns, upper, true);
-      __syncthreads();
-      if (warp == 0) each(columns, upper, false);
-      __syncthreads();
-    }
-    if (warp == 0) {
-      const bool complete = kWhole || (tile_ends && seg_j0 == 0);
-      const int group = p.io.group.d, rows = at.nq * group;
-      const int64_t slot = complete ? 2 * (int64_t)gridDim.x + head * p.tiles_cap + p.seqs.tiles_before(at.s, group) + at.rt
-                                    : 2 * (int64_t)blockIdx.x + (first_segment ? 0 : 1);
-#pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        const int in_tile = (lane >> 2) + 8 * r, row = at.rt * kSplitRows + in_tile;
-        if (row >= rows) continue;
-        if (complete && p.direct) {
-          const int i = div_by(row, p.io.group), g = row - i * group;
-          const int64_t token = p.seqs.q_begin(at.s) + i;
-          const int q_head = head * group + g;
-          const float inv = row_scale(sum[r]);
-          char *dst = p.io.out + token * p.io.out_stride + (int64_t)q_head * Shape::kRow + (lane & 3) * 4;
-#pragma unroll
-          for (int n = 0; n < D / 8; ++n)
-            *reinterpret_cast<uint32_t *>(dst + n * 16) = pack2<T>(o[n][2 * r] * inv, o[n][2 * r + 1] * inv);
-          if (p.io.lse != nullptr && (lane & 3) == 0)
-            p.io.lse[token * p.io.q_heads + q_head] = row_lse(big[r], sum[r]);
-        } else {
-          float *dst = p.space.o + (slot * kSplitRows + in_tile) * D + (lane & 3) * 2;
-#pragma unroll
-          for (int n = 0; n < D / 8; ++n) *reinterpret_cast<float2 *>(dst + n * 8) = make_float2(o[n][2 * r], o[n][2 * r + 1]);
-          if ((lane & 3) == 0)
-            *reinterpret_cast<float2 *>(p.space.ml + (slot * kSplitRows + in_tile) * 2) = make_float2(big[r], sum[r]);
-        }
-      }
-    }
     first_segment = false;
     fresh = true;
     if (u + 1 < u1) at.advance(p);
   }
   cp_async_wait<0>();
-  if constexpr (kWhole) {
-    if (u0 == u1 && warp == 0) {  // no key: zeros
-      const int group = p.io.group.d, rows = at.nq * group;
-      for (int r = 0; r < kSplitRows; ++r) {
-        const int row = at.rt * kSplitRows + r;
-        if (row >= rows) break;
-        const int i = div_by(row, p.io.group), q_head = head * group + row - i * group;
-        const int64_t token = p.seqs.q_begin(at.s) + i;
-        if (lane < D / 8)
-          *reinterpret_cast<uint4 *>(p.io.out + token * p.io.out_stride + (int64_t)q_head * Shape::kRow + lane * 16) =
-              make_uint4(0, 0, 0, 0);
-        if (p.io.lse != nullptr && lane == 0) p.io.lse[token * p.io.q_heads + q_head] = -INFINITY;
-      }
-    }
-  }
-  // a pass before this one, on which the joining kernel also depends
-  wait_prerequisite();
+  if constexpr (kWhole) end_tile(true);
 }
 
 }  // namespace cpkv

@@ -19,7 +19,8 @@
 //                      for every item, and a running block claims blocks that have not
 //                      started (cluster launch control), so long items go first and no
 //                      SM waits for another.
-//   warps 14, 15       the next item's queries, once this one's scores are done.
+//   warps 14, 15       the next item's queries: two blocks of 128 rows, of which an item
+//                      of at most 128 rows takes one, the items in turn.
 // Of an item with at most 128 rows the two tiles are the same rows over every other
 // 128 keys (two streams), joined at the end.
 // Tensor memory (512 columns): scores of the tiles at 0 and 128, outputs at 256
@@ -42,39 +43,47 @@ constexpr int kTileThreads = 512;
 // Registers a thread: 512 threads are launched with 128 each, 65536 in all; the
 // softmax holds a row's 128 scores.  256 * 216 + 256 * 40 = 65536.
 constexpr int kSoftmaxRegisters = 216, kOtherRegisters = 40;
+constexpr int kClaimAhead = 12;  // key tiles before an item's last load at which the next item is claimed
 constexpr int kTileMaps = 8;  // most pools that TMA maps travel for
 constexpr float kRescaleAt = 8.f;
 constexpr uint64_t kTileWaitNs = 2000000000ull;
 constexpr uint32_t kTileParkNs = 20000;
 
-// Slots of a tile pass: [item][split], an item being (row tile of all
-// sequences, key/value head).
+// Rows of a tile pass's parts: 256 for each [item][split], an item being (row tile
+// of the ragged sequences, key/value head), then those of the sequences of one
+// query, [sequence][key/value head][row tile][split] of its rows.
 struct TileSpace {
-  float *ml;  // [slot][256][2]
-  float *o;   // [slot][256][D]
-  int splits;
+  float *ml;  // [row][2]
+  float *o;   // [row][D]
+  int splits, single_splits;
+  int items;           // of the ragged sequences
+  int single_tiles;    // row tiles of a sequence of one query
+  int64_t single_row;  // where their rows begin
 };
 
-template <int N>
+template <typename S>
 struct TileParams {
-  Seqs<N> seqs;
+  S seqs;
   PagedPools pools;
   AttendIo io;
   TileSpace space;
   int direct;           // one split, and the rows go straight to the output
   int wide_out;         // the output's rows start on 32 bytes
   int box_rows;         // rows of a TMA box (32 or 16); 0: no maps
-  int cu_tiles[N + 1];  // row tiles before each sequence
+  int cu_tiles[S::kArray + 1];  // row tiles before each ragged sequence
   CUtensorMap maps[kTileMaps];  // pool r as [rows][elements], boxes of box_rows x 64
 };
 
 // Finds the parts of a row of a tile pass.
-template <int N>
+template <typename S>
 struct TileSource {
-  Seqs<N> seqs;
+  S seqs;
   TileSpace space;
-  int cu_tiles[N + 1];
+  int cu_tiles[S::kArray + 1];
 };
+
+// Rows of a part of a sequence of one query.
+CPKV_DEV int single_rows(int group) { return group < kTileRows ? group : kTileRows; }
 
 template <int D>
 struct TileShape {
@@ -84,24 +93,18 @@ struct TileShape {
   static constexpr int kSmem = 1024 + kQ + 2 * kStages * kOperand;
 };
 
-template <int N>
-CPKV_DEV int find_tile_seq(const TileParams<N> &p, int tile) {
-  return upper_index(p.cu_tiles, p.seqs.count, tile);
-}
-
 // What the warps of a block are told of an item.
 struct TileItem {
   int more;  // 0: no item, the block ends
   int h, row0, rows, group_tiles, kv, nq, n, j0, streams;
-  int index, split;  // of the item without its split
-  int64_t q_begin;
+  int64_t q_begin, slot;  // first query token; first row of its parts
   const int32_t *pages;
   KeyRange keys;   // what the item's rows see
   KeyRange there;  // what the sequence's rows see: present in the pools
 };
 
 struct TileBars {
-  uint64_t k_full[4], k_empty[4], v_full[4], v_empty[4], s_full[2], p_full[2], o_full[2], q_full, q_empty;
+  uint64_t k_full[4], k_empty[4], v_full[4], v_empty[4], s_full[2], p_full[2], o_full[2], q_full[2], q_empty[2];
   uint64_t item_full[2], item_empty[2], wanted, claimed, drain, stream_done, stream_free;
   uint4 claim;
   uint32_t tmem;
@@ -133,15 +136,29 @@ CPKV_DEV void tile_wait(TileBars *b, uint64_t *bar, uint32_t parity, int32_t *st
 // The lowest n bits, n clamped to 0..32.
 CPKV_DEV uint32_t low_bits(int n) { return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1; }
 
-// The item of a block index: the last row tiles first, which see the most keys.
-template <int N>
-CPKV_DEV void find_item(const TileParams<N> &p, int block, TileItem *r) {
-  const int splits = p.space.splits;
-  r->index = (int)gridDim.x / splits - 1 - block / splits;
-  r->split = block % splits;
-  const int tile = r->index / p.io.kv_heads, s = find_tile_seq(p, tile), rt = tile - p.cu_tiles[s];
-  const int group = p.io.group.d;
-  r->h = r->index - tile * p.io.kv_heads;
+// The item of a block index: the ragged sequences' last row tiles first, which see
+// the most keys, then the sequences of one query.
+template <typename S>
+CPKV_DEV void find_item(const TileParams<S> &p, int block, TileItem *r) {
+  const int heads = p.io.kv_heads, group = p.io.group.d, many = p.space.items * p.space.splits;
+  int s, rt, splits, split;
+  if (block < many) {
+    splits = p.space.splits;
+    const int index = p.space.items - 1 - block / splits, tile = index / heads;
+    split = block % splits;
+    s = upper_index(p.cu_tiles, p.seqs.ragged(), tile);
+    rt = tile - p.cu_tiles[s];
+    r->h = index - tile * heads;
+    r->slot = ((int64_t)index * splits + split) * kTileRows;
+  } else {
+    splits = p.space.single_splits;
+    const int index = (block - many) / splits, tiles = p.space.single_tiles, y = index / tiles;
+    split = block - many - index * splits;
+    s = p.seqs.ragged() + y / heads;
+    rt = index - y * tiles;
+    r->h = y % heads;
+    r->slot = p.space.single_row + (int64_t)(block - many) * single_rows(group);
+  }
   r->nq = p.seqs.q_count(s);
   r->kv = p.seqs.kv_len(s);
   r->rows = r->nq * group;
@@ -153,16 +170,16 @@ CPKV_DEV void find_item(const TileParams<N> &p, int block, TileItem *r) {
                                  p.seqs.window, p.seqs.sinks);
   r->there = key_range<kTileKeys>(r->kv, r->nq, 0, r->nq, p.seqs.causal, p.seqs.window, p.seqs.sinks);
   // fewer than 2^24 key tiles, at most some hundred parts
-  r->j0 = (int)((uint32_t)r->keys.n_tiles * (uint32_t)r->split / (uint32_t)splits);
-  r->n = (int)((uint32_t)r->keys.n_tiles * (uint32_t)(r->split + 1) / (uint32_t)splits) - r->j0;
+  r->j0 = (int)((uint32_t)r->keys.n_tiles * (uint32_t)split / (uint32_t)splits);
+  r->n = (int)((uint32_t)r->keys.n_tiles * (uint32_t)(split + 1) / (uint32_t)splits) - r->j0;
   r->group_tiles = end - r->row0 > 128 ? 2 : 1;
   r->streams = r->group_tiles == 1 ? 2 : 1;
   r->more = 1;
-  if (r->split == 0 && r->h == 0 && rt == 0 && p.seqs.kv_len_bad(s)) raise_status(p.seqs.status, CPKV_STATUS_OUT_CAPACITY);
+  if (split == 0 && r->h == 0 && rt == 0 && p.seqs.kv_len_bad(s)) raise_status(p.seqs.status, CPKV_STATUS_OUT_CAPACITY);
 }
 
-template <typename T, int D, int N>
-__global__ void __launch_bounds__(kTileThreads, 1) attend_tile_kernel(const __grid_constant__ TileParams<N> p) {
+template <typename T, int D, typename S>
+__global__ void __launch_bounds__(kTileThreads, 1) attend_tile_kernel(const __grid_constant__ TileParams<S> p) {
   using Shape = TileShape<D>;
   constexpr int kStages = Shape::kStages;
   constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
@@ -188,11 +205,11 @@ __global__ void __launch_bounds__(kTileThreads, 1) attend_tile_kernel(const __gr
       mbar_init(&bars.s_full[t], 1);
       mbar_init(&bars.o_full[t], 1);
       mbar_init(&bars.p_full[t], 128);
+      mbar_init(&bars.q_full[t], 64);
+      mbar_init(&bars.q_empty[t], 1);
       mbar_init(&bars.item_full[t], 1);
       mbar_init(&bars.item_empty[t], kItemReaders);
     }
-    mbar_init(&bars.q_full, 64);
-    mbar_init(&bars.q_empty, 1);
     mbar_init(&bars.wanted, 1);
     mbar_init(&bars.claimed, 1);
     mbar_init(&bars.drain, 1);
@@ -350,7 +367,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) attend_tile_kernel(const __gr
       const int row = first + (int)(threadIdx.x & 127), rows = item.rows, token = div_by(row, p.io.group);
       const int head = item.h * (int)p.io.group.d + row - token * (int)p.io.group.d;
       const int64_t out_token = item.q_begin + token;
-      const int64_t slot_row = ((int64_t)item.index * p.space.splits + item.split) * kTileRows + threadIdx.x;
+      const int64_t slot_row = item.slot + threadIdx.x;
       item_read(k);
       if (row < rows) {
         if (!p.direct) {
@@ -499,7 +516,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) attend_tile_kernel(const __gr
           }
         }
         ++loaded;
-        if (warp == 8 && lane == 0 && it == (n > 2 ? n - 3 : 0)) mbar_arrive(&bars.wanted);
+        if (warp == 8 && lane == 0 && it == (n > kClaimAhead ? n - kClaimAhead : 0)) mbar_arrive(&bars.wanted);
       }
       if (warp == 8 && lane == 0 && n == 0) mbar_arrive(&bars.wanted);
     }
@@ -542,7 +559,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) attend_tile_kernel(const __gr
         if (elect_one()) mma_commit(bar);
         __syncwarp();
       };
-      uint32_t used = 0, queries = 0, weighed[2] = {0, 0};  // key tiles, items, weight tiles
+      uint32_t used = 0, queries[2] = {0, 0}, weighed[2] = {0, 0};  // key tiles, query blocks, weight tiles
+      int turn = 0;  // query block of the next item that takes one
       auto keys_in = [&](uint32_t at) {
         wait(&bars.k_full[at % kStages], at / kStages);
         fence_proxy_async_smem();
@@ -564,12 +582,17 @@ __global__ void __launch_bounds__(kTileThreads, 1) attend_tile_kernel(const __gr
         const int streams = __shfl_sync(0xffffffffu, items[k & 1].streams, 0);
         item_read(k);
         if (n == 0) continue;
-        wait(&bars.q_full, queries++);
-        keys_in(used);
         if (streams == 1) {
+          wait(&bars.q_full[0], queries[0]++);
+          wait(&bars.q_full[1], queries[1]++);
+          auto queries_done = [&] {
+            commit(&bars.q_empty[0]);
+            commit(&bars.q_empty[1]);
+          };
+          keys_in(used);
           for (int t = 0; t < row_tiles; ++t) scores(t, t, used % kStages);
           commit(&bars.k_empty[used % kStages]);
-          if (n == 1) commit(&bars.q_empty);
+          if (n == 1) queries_done();
           for (int it = 0; it < n; ++it) {
             const uint32_t at = used + it;
             const int stage = at % kStages, next = (at + 1) % kStages;
@@ -582,7 +605,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) attend_tile_kernel(const __gr
                 scores(t, t, next);
               }
               commit(&bars.k_empty[next]);
-              if (it + 2 == n) commit(&bars.q_empty);
+              if (it + 2 == n) queries_done();
             } else {
               for (int t = 0; t < row_tiles; ++t) {
                 weigh(t, stage, it == 0);
@@ -592,14 +615,22 @@ __global__ void __launch_bounds__(kTileThreads, 1) attend_tile_kernel(const __gr
             }
           }
         } else {  // the same rows, every other key tile
-          scores(0, 0, used % kStages);
+          const int q = turn;
+          turn ^= 1;
+          if (q == 0) {
+            wait(&bars.q_full[0], queries[0]++);
+          } else {
+            wait(&bars.q_full[1], queries[1]++);
+          }
+          keys_in(used);
+          scores(0, q, used % kStages);
           commit(&bars.k_empty[used % kStages]);
           if (n > 1) {
             keys_in(used + 1);
-            scores(1, 0, (used + 1) % kStages);
+            scores(1, q, (used + 1) % kStages);
             commit(&bars.k_empty[(used + 1) % kStages]);
           }
-          if (n <= 2) commit(&bars.q_empty);
+          if (n <= 2) commit(&bars.q_empty[q]);
           for (int it = 0; it < n; ++it) {
             const uint32_t at = used + it;
             const int t = it & 1, stage = at % kStages;
@@ -608,9 +639,9 @@ __global__ void __launch_bounds__(kTileThreads, 1) attend_tile_kernel(const __gr
             commit(&bars.v_empty[stage]);
             if (it + 2 < n) {
               keys_in(at + 2);
-              scores(t, 0, (at + 2) % kStages);
+              scores(t, q, (at + 2) % kStages);
               commit(&bars.k_empty[(at + 2) % kStages]);
-              if (it + 3 == n) commit(&bars.q_empty);
+              if (it + 3 == n) commit(&bars.q_empty[q]);
             } else {
               commit(&bars.o_full[t]);
             }
@@ -649,19 +680,33 @@ __global__ void __launch_bounds__(kTileThreads, 1) attend_tile_kernel(const __gr
       // -------------------------------------------------------------- queries
       constexpr int kLanes = D / 8;
       const int at = (int)threadIdx.x - 14 * 32, c = at % kLanes;
-      const char *const zeros = reinterpret_cast<const char *>(zero_row);
-      uint32_t filled = 0;
+      uint32_t filled[2] = {0, 0};
+      int turn = 0;
       for (int k = 0; item_there(k); ++k) {
-        int row0, rows, count;
+        int row0, rows;
+        bool one;
         const char *q;
         {
           const TileItem &item = items[k & 1];
-          row0 = item.row0, rows = item.rows, count = item.n > 0 ? item.group_tiles * 128 : 0;
+          row0 = item.row0, rows = item.rows, one = item.streams == 2;
+          const bool none = item.n == 0;
           q = p.io.q + item.q_begin * p.io.q_stride + (int64_t)item.h * (int)p.io.group.d * (D * 2);
           item_read(k);
+          if (none) continue;
         }
-        if (count == 0) continue;
-        if (filled > 0) wait(&bars.q_empty, filled - 1);
+        const int block = one ? turn : 0;
+        turn ^= one;
+        // rows past the last keep what is there: nothing is made of them
+        const int left = rows - row0, count = one ? left : left < kTileRows ? left : kTileRows;
+        if (block == 0) {
+          if (filled[0] > 0) wait(&bars.q_empty[0], filled[0] - 1);
+          ++filled[0];
+        }
+        if (block == 1 || !one) {
+          if (filled[1] > 0) wait(&bars.q_empty[1], filled[1] - 1);
+          ++filled[1];
+        }
+        __syncwarp();
         // rows at / kLanes, + kStep, ...: (token, head) and address go along
         constexpr int kStep = 64 / kLanes;
         const int group = p.io.group.d, heads_on = kStep % group, tokens_on = kStep / group;
@@ -670,11 +715,10 @@ __global__ void __launch_bounds__(kTileThreads, 1) attend_tile_kernel(const __gr
         const int i = div_by(row0 + r, p.io.group);
         int g = row0 + r - i * group;
         const char *src = q + i * p.io.q_stride + g * (D * 2) + c * 16;
-        const uint32_t to = smem_addr(q_smem) + (c >> 3) * (kTileKeys * 128);
+        const uint32_t to = smem_addr(q_smem) + block * Shape::kOperand + (c >> 3) * (kTileKeys * 128);
 #pragma unroll 8
         for (; r < count; r += kStep) {
-          cp_async16(to + (r >> 7) * Shape::kOperand + (r & 127) * 128 + (((c & 7) ^ (r & 7)) << 4),
-                     row0 + r < rows ? src : zeros + c * 16);
+          cp_async16(to + (r >> 7) * Shape::kOperand + (r & 127) * 128 + (((c & 7) ^ (r & 7)) << 4), src);
           src += on;
           g += heads_on;
           if (g >= group) {
@@ -682,8 +726,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) attend_tile_kernel(const __gr
             src += wrap;
           }
         }
-        mbar_arrive_after_copies(&bars.q_full);
-        ++filled;
+        if (block == 0) mbar_arrive_after_copies(&bars.q_full[0]);
+        if (block == 1 || !one) mbar_arrive_after_copies(&bars.q_full[1]);
       }
       cp_async_wait_all();
     }
