@@ -164,6 +164,10 @@ struct TileBounds {
     s.items = (int)(tiles * kv_heads);
     s.single_tiles = (int)single_tiles;
     s.single_row = ragged_rows(kv_heads);
+    s.by_heads = fast_div((uint32_t)kv_heads);
+    s.by_splits = fast_div((uint32_t)splits);
+    s.by_single_splits = fast_div((uint32_t)single_splits);
+    s.by_single_tiles = fast_div((uint32_t)std::max<int64_t>(single_tiles, 1));
     return s;
   }
 };

@@ -43,6 +43,7 @@ constexpr int kTileThreads = 512;
 // Registers a thread: 512 threads are launched with 128 each, 65536 in all; the
 // softmax holds a row's 128 scores.  256 * 216 + 256 * 40 = 65536.
 constexpr int kSoftmaxRegisters = 216, kOtherRegisters = 40;
+constexpr int kItemSlots = 4;   // items known at a time: of small ones, some are loaded while others are finished
 constexpr int kClaimAhead = 12;  // key tiles before an item's last load at which the next item is claimed
 constexpr int kTileMaps = 8;  // most pools that TMA maps travel for
 constexpr float kRescaleAt = 8.f;
@@ -59,6 +60,7 @@ struct TileSpace {
   int items;           // of the ragged sequences
   int single_tiles;    // row tiles of a sequence of one query
   int64_t single_row;  // where their rows begin
+  FastDiv by_heads, by_splits, by_single_splits, by_single_tiles;
 };
 
 template <typename S>
@@ -105,7 +107,7 @@ struct TileItem {
 
 struct TileBars {
   uint64_t k_full[4], k_empty[4], v_full[4], v_empty[4], s_full[2], p_full[2], o_full[2], q_full[2], q_empty[2];
-  uint64_t item_full[2], item_empty[2], wanted, claimed, drain, stream_done, stream_free;
+  uint64_t item_full[kItemSlots], item_empty[kItemSlots], wanted, claimed, drain, stream_done, stream_free;
   uint4 claim;
   uint32_t tmem;
   int gave_up;
@@ -144,20 +146,22 @@ CPKV_DEV void find_item(const TileParams<S> &p, int block, TileItem *r) {
   int s, rt, splits, split;
   if (block < many) {
     splits = p.space.splits;
-    const int index = p.space.items - 1 - block / splits, tile = index / heads;
-    split = block % splits;
+    const int cut = div_by(block, p.space.by_splits), index = p.space.items - 1 - cut;
+    const int tile = div_by(index, p.space.by_heads);
+    split = block - cut * splits;
     s = upper_index(p.cu_tiles, p.seqs.ragged(), tile);
     rt = tile - p.cu_tiles[s];
     r->h = index - tile * heads;
     r->slot = ((int64_t)index * splits + split) * kTileRows;
   } else {
     splits = p.space.single_splits;
-    const int index = (block - many) / splits, tiles = p.space.single_tiles, y = index / tiles;
-    split = block - many - index * splits;
-    s = p.seqs.ragged() + y / heads;
-    rt = index - y * tiles;
-    r->h = y % heads;
-    r->slot = p.space.single_row + (int64_t)(block - many) * single_rows(group);
+    const int rest = block - many, index = div_by(rest, p.space.by_single_splits);
+    const int y = div_by(index, p.space.by_single_tiles), of = div_by(y, p.space.by_heads);
+    split = rest - index * splits;
+    s = p.seqs.ragged() + of;
+    rt = index - y * p.space.single_tiles;
+    r->h = y - of * heads;
+    r->slot = p.space.single_row + (int64_t)rest * single_rows(group);
   }
   r->nq = p.seqs.q_count(s);
   r->kv = p.seqs.kv_len(s);
@@ -169,9 +173,12 @@ CPKV_DEV void find_item(const TileParams<S> &p, int block, TileItem *r) {
   r->keys = key_range<kTileKeys>(r->kv, r->nq, div_by(r->row0, p.io.group), div_by(end - 1, p.io.group) + 1, p.seqs.causal,
                                  p.seqs.window, p.seqs.sinks);
   r->there = key_range<kTileKeys>(r->kv, r->nq, 0, r->nq, p.seqs.causal, p.seqs.window, p.seqs.sinks);
-  // fewer than 2^24 key tiles, at most some hundred parts
-  r->j0 = (int)((uint32_t)r->keys.n_tiles * (uint32_t)split / (uint32_t)splits);
-  r->n = (int)((uint32_t)r->keys.n_tiles * (uint32_t)(split + 1) / (uint32_t)splits) - r->j0;
+  r->j0 = 0;
+  r->n = r->keys.n_tiles;
+  if (splits > 1) {  // fewer than 2^24 key tiles, at most some hundred parts
+    r->j0 = (int)((uint32_t)r->keys.n_tiles * (uint32_t)split / (uint32_t)splits);
+    r->n = (int)((uint32_t)r->keys.n_tiles * (uint32_t)(split + 1) / (uint32_t)splits) - r->j0;
+  }
   r->group_tiles = end - r->row0 > 128 ? 2 : 1;
   r->streams = r->group_tiles == 1 ? 2 : 1;
   r->more = 1;
@@ -185,7 +192,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) attend_tile_kernel(const __gr
   constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
   extern __shared__ char raw_smem[];
   __shared__ TileBars bars;
-  __shared__ TileItem items[2];
+  __shared__ TileItem items[kItemSlots];
   __shared__ float2 stream_ml[128];            // maximum and sum of the second stream's rows
   __shared__ ulonglong2 addresses[kTileKeys];  // of the keys being copied: key, value
   char *smem = reinterpret_cast<char *>((reinterpret_cast<uintptr_t>(raw_smem) + 1023) & ~uintptr_t(1023));
@@ -207,8 +214,10 @@ __global__ void __launch_bounds__(kTileThreads, 1) attend_tile_kernel(const __gr
       mbar_init(&bars.p_full[t], 128);
       mbar_init(&bars.q_full[t], 64);
       mbar_init(&bars.q_empty[t], 1);
-      mbar_init(&bars.item_full[t], 1);
-      mbar_init(&bars.item_empty[t], kItemReaders);
+    }
+    for (int i = 0; i < kItemSlots; ++i) {
+      mbar_init(&bars.item_full[i], 1);
+      mbar_init(&bars.item_empty[i], kItemReaders);
     }
     mbar_init(&bars.wanted, 1);
     mbar_init(&bars.claimed, 1);
@@ -227,13 +236,13 @@ __global__ void __launch_bounds__(kTileThreads, 1) attend_tile_kernel(const __gr
   // Item number k of this block: whether there is one.  The warp reads it and hands
   // its place back.
   auto item_there = [&](int k) {
-    wait(&bars.item_full[k & 1], k >> 1);
-    const bool there = items[k & 1].more && !*(volatile int *)&bars.gave_up;
+    wait(&bars.item_full[k % kItemSlots], k / kItemSlots);
+    const bool there = items[k % kItemSlots].more && !*(volatile int *)&bars.gave_up;
     return __all_sync(0xffffffffu, there) != 0;
   };
   auto item_read = [&](int k) {
     __syncwarp();
-    if (lane == 0) mbar_arrive(&bars.item_empty[k & 1]);
+    if (lane == 0) mbar_arrive(&bars.item_empty[k % kItemSlots]);
   };
 
   if (warp < 8) {
@@ -245,7 +254,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) attend_tile_kernel(const __gr
     const float scale = p.io.scale_log2;
     uint32_t seen = 0, done0 = 0, done1 = 0, pairs = 0;  // score tiles, outputs of the tiles, items of two streams
     for (int k = 0; item_there(k); ++k) {
-      const TileItem &item = items[k & 1];  // kept until its results are written
+      const TileItem &item = items[k % kItemSlots];  // kept until its results are written
       const int step = item.streams;
       const int my_n = step == 2 ? (item.n + 1 - t) / 2 : t < item.group_tiles ? item.n : 0;
       const int j0 = step == 2 ? item.j0 + t : item.j0;
@@ -455,10 +464,10 @@ __global__ void __launch_bounds__(kTileThreads, 1) attend_tile_kernel(const __gr
     const int box_block = lane % (D / 64), box_key = lane / (D / 64) * p.box_rows;
     uint32_t loaded = 0;  // key tiles
     for (int k = 0; item_there(k); ++k) {
-      const int n = items[k & 1].n, j0 = items[k & 1].j0, n_sink = items[k & 1].keys.n_sink, first_tile = items[k & 1].keys.first_tile;
-      const int lo = items[k & 1].there.lo, hi = items[k & 1].there.hi, sink_end = items[k & 1].there.sink_end;
-      const int32_t *const pages = items[k & 1].pages;
-      const int64_t k_at = p.io.k_off + (int64_t)items[k & 1].h * D * 2, v_at = k_at + (p.io.v_off - p.io.k_off);
+      const int n = items[k % kItemSlots].n, j0 = items[k % kItemSlots].j0, n_sink = items[k % kItemSlots].keys.n_sink, first_tile = items[k % kItemSlots].keys.first_tile;
+      const int lo = items[k % kItemSlots].there.lo, hi = items[k % kItemSlots].there.hi, sink_end = items[k % kItemSlots].there.sink_end;
+      const int32_t *const pages = items[k % kItemSlots].pages;
+      const int64_t k_at = p.io.k_off + (int64_t)items[k % kItemSlots].h * D * 2, v_at = k_at + (p.io.v_off - p.io.k_off);
       item_read(k);
       int key = 0, page = -1;
       auto look_up = [&](int j) {  // one tile ahead of its copies
@@ -577,9 +586,9 @@ __global__ void __launch_bounds__(kTileThreads, 1) attend_tile_kernel(const __gr
         values(t, stage, !first);
       };
       for (int k = 0; item_there(k); ++k) {
-        const int n = __shfl_sync(0xffffffffu, items[k & 1].n, 0);
-        const int row_tiles = __shfl_sync(0xffffffffu, items[k & 1].group_tiles, 0);
-        const int streams = __shfl_sync(0xffffffffu, items[k & 1].streams, 0);
+        const int n = __shfl_sync(0xffffffffu, items[k % kItemSlots].n, 0);
+        const int row_tiles = __shfl_sync(0xffffffffu, items[k % kItemSlots].group_tiles, 0);
+        const int streams = __shfl_sync(0xffffffffu, items[k % kItemSlots].streams, 0);
         item_read(k);
         if (n == 0) continue;
         if (streams == 1) {
@@ -660,13 +669,13 @@ __global__ void __launch_bounds__(kTileThreads, 1) attend_tile_kernel(const __gr
       if (lane == 0) {
         int block = (int)blockIdx.x;
         for (int k = 0;; ++k) {
-          if (k >= 2) wait(&bars.item_empty[k & 1], (k >> 1) - 1);
+          if (k >= kItemSlots) wait(&bars.item_empty[k % kItemSlots], k / kItemSlots - 1);
           if (block >= 0) {
-            find_item(p, block, &items[k & 1]);
+            find_item(p, block, &items[k % kItemSlots]);
           } else {
-            items[k & 1].more = 0;
+            items[k % kItemSlots].more = 0;
           }
-          mbar_arrive(&bars.item_full[k & 1]);
+          mbar_arrive(&bars.item_full[k % kItemSlots]);
           if (block < 0) break;
           wait(&bars.wanted, k);  // the loads of this item near their end
           fence_proxy_async_smem();
@@ -687,7 +696,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) attend_tile_kernel(const __gr
         bool one;
         const char *q;
         {
-          const TileItem &item = items[k & 1];
+          const TileItem &item = items[k % kItemSlots];
           row0 = item.row0, rows = item.rows, one = item.streams == 2;
           const bool none = item.n == 0;
           q = p.io.q + item.q_begin * p.io.q_stride + (int64_t)item.h * (int)p.io.group.d * (D * 2);
