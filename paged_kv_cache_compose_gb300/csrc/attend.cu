@@ -1,7 +1,5 @@
 // Entry points of the attention over paged rows: argument checks, workspace
 // layout and the choice of passes.
-#include <type_traits>
-
 #include "attend_join.cuh"
 
 namespace cpkv {
@@ -494,7 +492,6 @@ extern "C" int cpkv_attend_window(int B, int page_size, int cp_size, int dtype, 
     s.status = d_status;
     s.count = B;
     s.kv_cap = (int)max_kv_len;
-    s.causal = 1;
     s.window = window;
     s.sinks = sinks;
     if (uniform) {

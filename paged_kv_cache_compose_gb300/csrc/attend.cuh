@@ -13,9 +13,14 @@
 // bits; parts over disjoint keys join as
 //   m = max m_i, l = sum 2^(m_i - m) l_i, o = sum 2^(m_i - m) o_i.
 // A part without keys is m = -inf, l = 0, o = 0.
+//
+// A product adds weight 0 times the value for a key that a row does not see, which
+// is a NaN where that value is infinite or one.  Keys that no query of a sequence
+// sees are never read; for those that only some see, the split pass takes infinite
+// values out before the product and adds them to the rows that see them (weights are
+// positive, so an infinity or a NaN is what they contribute), and the tile pass
+// works rows that came out as NaN out again.
 #pragma once
-
-#include <type_traits>
 
 #include "paged.cuh"
 
@@ -24,31 +29,28 @@ namespace cpkv {
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
-// The sequences of a call.  Lengths that the host knows travel in the block;
-// kv_lens (device) wins over kv where given.
+// The requests of a windowed call.
 template <int N>
 struct Seqs {
   static constexpr int kArray = N;
-  const int32_t *kv_lens;  // device lengths, clamped to [0, kv_cap]; null: kv[s]
-  const int32_t *table;    // page ids: row s at s * stride, or at page0[s] when stride < 0
+  const int32_t *kv_lens;  // device lengths, clamped to [0, kv_cap]
+  const int32_t *table;    // page ids: row s at s * stride
   int64_t stride;
   int32_t *status;
   int count, uniform_q;  // uniform_q > 0: every sequence has that many query tokens
   int kv_cap;
-  int causal, window, sinks;  // window 0: none
+  int window, sinks;  // window 0: none
+  static constexpr int causal = 1;
   int cu_q[N + 1];
-  int kv[N];
-  int page0[N];
 
   CPKV_DEV int q_begin(int s) const { return uniform_q ? s * uniform_q : cu_q[s]; }
   CPKV_DEV int q_count(int s) const { return uniform_q ? uniform_q : cu_q[s + 1] - cu_q[s]; }
   CPKV_DEV int kv_len(int s) const {
-    if (kv_lens == nullptr) return kv[s];
     const int n = kv_lens[s];
     return n < 0 ? 0 : (n > kv_cap ? kv_cap : n);
   }
-  CPKV_DEV bool kv_len_bad(int s) const { return kv_lens != nullptr && (kv_lens[s] < 0 || kv_lens[s] > kv_cap); }
-  CPKV_DEV const int32_t *pages(int s) const { return stride < 0 ? table + page0[s] : table + s * stride; }
+  CPKV_DEV bool kv_len_bad(int s) const { return kv_lens[s] < 0 || kv_lens[s] > kv_cap; }
+  CPKV_DEV const int32_t *pages(int s) const { return table + s * stride; }
   // Sequences with lengths of their own queries; the others have one query each.
   CPKV_DEV int ragged() const { return count; }
   // Tiles of 16 packed rows before sequence s, at most.
@@ -213,11 +215,7 @@ CPKV_DEV void ldmatrix_x4_trans(uint32_t r[4], uint32_t addr) {
                : "r"(addr));
 }
 
-// 16-byte asynchronous copy; `bytes` 0 writes zeros and reads nothing.
-CPKV_DEV void cp_async16(uint32_t smem, const void *src, int bytes) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem), "l"(src), "r"(bytes) : "memory");
-}
-// The same with an L2 policy.
+// 16-byte asynchronous copy with an L2 policy; `bytes` 0 writes zeros and reads nothing.
 CPKV_DEV void cp_async16_hint(uint32_t smem, const void *src, int bytes, uint64_t policy) {
   asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2, %3;" ::"r"(smem), "l"(src), "r"(bytes),
                "l"(policy)

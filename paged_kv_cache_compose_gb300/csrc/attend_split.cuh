@@ -369,6 +369,31 @@ __global__ void __launch_bounds__(kSplitWarps * 32, SplitShape<D, kMode>::kBlock
         l[r] += a + b;
         pf[2 * n + r] = pack2<T>(a, b);
       }
+    if (S::causal && !whole && at.nq > 1) {  // infinite values of keys that some rows do not see
+      char *const values = ring + stage * Shape::kStage + kWarpKeys * Shape::kRow;
+      uint4 marks = make_uint4(0, 0, 0, 0);
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i) marks = mark_infinite<T>(reinterpret_cast<const uint4 *>(values)[i * 32 + lane], marks);
+      if (__any_sync(0xffffffffu, (marks.x | marks.y | marks.z | marks.w) != 0)) {
+        for (int key = 0; key < kWarpKeys; ++key) {
+          const bool sees[2] = {mask[0].sees(key0 + key), mask[1].sees(key0 + key)};
+#pragma unroll
+          for (int n = 0; n < D / 8; ++n) {
+            const float2 v = unpack2<T>(infinite_of<T>(
+                *reinterpret_cast<const uint32_t *>(values + key * Shape::kRow + ((n ^ (key & 7)) << 4) + (lane & 3) * 4)));
+#pragma unroll
+            for (int r = 0; r < 2; ++r)
+              if (sees[r]) o[n][2 * r] += v.x, o[n][2 * r + 1] += v.y;
+          }
+        }
+        __syncwarp();
+        for (int i = lane; i < kWarpKeys * Shape::kRow / 4; i += 32) {
+          uint32_t *const v = reinterpret_cast<uint32_t *>(values) + i;
+          *v = finite_of<T>(*v);
+        }
+        __syncwarp();
+      }
+    }
     {
       const int key = lane & 15;
       const uint32_t row = kb + kWarpKeys * Shape::kRow + key * Shape::kRow;

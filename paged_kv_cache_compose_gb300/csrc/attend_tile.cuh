@@ -185,6 +185,74 @@ CPKV_DEV void find_item(const TileParams<S> &p, int block, TileItem *r) {
   if (split == 0 && r->h == 0 && rt == 0 && p.seqs.kv_len_bad(s)) raise_status(p.seqs.status, CPKV_STATUS_OUT_CAPACITY);
 }
 
+// A row of an item whose output holds a NaN, by the thread that wrote it.  A product
+// adds weight 0 times the value for keys of a tile that the row does not see, so where
+// one of those values is infinite or a NaN the output is worked out again over the keys
+// that it does see, with the maximum and sum that the row has (which no other key
+// enters): to `out` (16-bit results) or `part` (a part's values).  For NaNs only: to look
+// at the values beforehand costs more (traced prefill 2.27 ms where it is 2.13).
+template <typename T, int D, typename S>
+__device__ __noinline__ void mend_row(const TileParams<S> &p, const TileItem &item, int token, int head, float base, float l,
+                                      char *out, float *part) {
+  const RowMask mask = row_mask(item.kv, item.nq, token, p.seqs.causal, p.seqs.window, p.seqs.sinks);
+  const int64_t k_at = p.io.k_off + (int64_t)item.h * D * 2, v_at = p.io.v_off + (int64_t)item.h * D * 2;
+  auto row_of = [&](int key) -> const char * {
+    const int page = div_by(key, p.pools.page_size);
+    const char *const at = page_address(p.pools, item.pages[page]);
+    return at == nullptr ? nullptr : at + (int64_t)(key - page * (int)p.pools.page_size.d) * p.pools.row_bytes;
+  };
+  uint4 marks = make_uint4(0, 0, 0, 0);
+  for (int j = item.j0; j < item.j0 + item.n; ++j) {
+    const int start = item.keys.tile_start(j, kTileKeys);
+    if (start + kTileKeys <= mask.hi && (start >= mask.lo || start + kTileKeys <= mask.sinks)) continue;
+    for (int key = start; key < start + kTileKeys; ++key) {
+      if (mask.sees(key) || !item.there.any_sees(key)) continue;
+      const char *const at = row_of(key);
+      if (at == nullptr) continue;
+#pragma unroll
+      for (int c = 0; c < D / 8; ++c) marks = mark_infinite<T>(reinterpret_cast<const uint4 *>(at + v_at)[c], marks);
+    }
+  }
+  if ((marks.x | marks.y | marks.z | marks.w) == 0) return;  // its NaNs are its own
+
+  const char *const q = p.io.q + (item.q_begin + token) * p.io.q_stride + (int64_t)head * (D * 2);
+  const float shift = base == -INFINITY ? 0.f : base, inv = row_scale(l);
+#pragma unroll 1
+  for (int half = 0; half < D / 64; ++half) {
+    float o[64] = {};
+    for (int j = item.j0; j < item.j0 + item.n; ++j) {
+      const int start = item.keys.tile_start(j, kTileKeys);
+#pragma unroll 1
+      for (int key = start; key < start + kTileKeys; ++key) {
+        const char *const at = mask.sees(key) ? row_of(key) : nullptr;
+        if (at == nullptr) continue;
+        float dot = 0.f;
+#pragma unroll 4
+        for (int c = 0; c < D / 2; ++c) {
+          const float2 a = unpack2<T>(reinterpret_cast<const uint32_t *>(q)[c]);
+          const float2 b = unpack2<T>(reinterpret_cast<const uint32_t *>(at + k_at)[c]);
+          dot = fmaf(a.x, b.x, fmaf(a.y, b.y, dot));
+        }
+        const float w = exp2_approx(fmaf(dot, p.io.scale_log2, -shift));
+#pragma unroll
+        for (int c = 0; c < 32; ++c) {
+          const float2 v = unpack2<T>(reinterpret_cast<const uint32_t *>(at + v_at + half * 128)[c]);
+          o[2 * c] = fmaf(w, v.x, o[2 * c]);
+          o[2 * c + 1] = fmaf(w, v.y, o[2 * c + 1]);
+        }
+      }
+    }
+#pragma unroll
+    for (int c = 0; c < 32; ++c) {
+      if (part != nullptr) {
+        reinterpret_cast<float2 *>(part + half * 64)[c] = make_float2(o[2 * c], o[2 * c + 1]);
+      } else {
+        reinterpret_cast<uint32_t *>(out + half * 128)[c] = pack2<T>(o[2 * c] * inv, o[2 * c + 1] * inv);
+      }
+    }
+  }
+}
+
 template <typename T, int D, typename S>
 __global__ void __launch_bounds__(kTileThreads, 1) attend_tile_kernel(const __grid_constant__ TileParams<S> p) {
   using Shape = TileShape<D>;
@@ -377,7 +445,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) attend_tile_kernel(const __gr
       const int head = item.h * (int)p.io.group.d + row - token * (int)p.io.group.d;
       const int64_t out_token = item.q_begin + token;
       const int64_t slot_row = item.slot + threadIdx.x;
-      item_read(k);
+      if (!S::causal) item_read(k);
+      uint64_t marks = 0;  // 0 until an output is infinite or a NaN
       if (row < rows) {
         if (!p.direct) {
           *reinterpret_cast<float2 *>(p.space.ml + slot_row * 2) = make_float2(base, l);
@@ -405,6 +474,10 @@ __global__ void __launch_bounds__(kTileThreads, 1) attend_tile_kernel(const __gr
               o[i] = __float_as_uint(fmaf(__uint_as_float(o1[i]), other, __uint_as_float(o[i]) * mine));
           }
           if (row >= rows) continue;
+          if constexpr (S::causal) {
+#pragma unroll
+            for (int i = 0; i < 32; i += 2) marks = fma_pair(pair(o[i], o[i + 1]), 0, marks);
+          }
           // 32 bytes a store where they are aligned: a warp's rows lie apart, and each
           // store of it takes as long as it touches lines
           if (p.direct) {
@@ -431,6 +504,13 @@ __global__ void __launch_bounds__(kTileThreads, 1) attend_tile_kernel(const __gr
       }
       tmem_fence_before();
       if (step == 2) mbar_arrive(&bars.stream_free);
+      if constexpr (S::causal) {
+        const float2 m = unpair(marks);
+        if (row < rows && item.nq > 1 && my_n > 0 && !(m.x == 0.f && m.y == 0.f))
+          mend_row<T, D>(p, item, token, head, base, l, p.io.out + out_token * p.io.out_stride + (int64_t)head * (D * 2),
+                         p.direct ? nullptr : p.space.o + slot_row * D);
+        item_read(k);
+      }
     }
   } else if (warp < 12) {
     // ---------------------------------------------------------------- keys and values
@@ -464,10 +544,11 @@ __global__ void __launch_bounds__(kTileThreads, 1) attend_tile_kernel(const __gr
     const int box_block = lane % (D / 64), box_key = lane / (D / 64) * p.box_rows;
     uint32_t loaded = 0;  // key tiles
     for (int k = 0; item_there(k); ++k) {
-      const int n = items[k % kItemSlots].n, j0 = items[k % kItemSlots].j0, n_sink = items[k % kItemSlots].keys.n_sink, first_tile = items[k % kItemSlots].keys.first_tile;
-      const int lo = items[k % kItemSlots].there.lo, hi = items[k % kItemSlots].there.hi, sink_end = items[k % kItemSlots].there.sink_end;
-      const int32_t *const pages = items[k % kItemSlots].pages;
-      const int64_t k_at = p.io.k_off + (int64_t)items[k % kItemSlots].h * D * 2, v_at = k_at + (p.io.v_off - p.io.k_off);
+      const TileItem &item = items[k % kItemSlots];
+      const int n = item.n, j0 = item.j0, n_sink = item.keys.n_sink, first_tile = item.keys.first_tile;
+      const int lo = item.there.lo, hi = item.there.hi, sink_end = item.there.sink_end;
+      const int32_t *const pages = item.pages;
+      const int64_t k_at = p.io.k_off + (int64_t)item.h * D * 2, v_at = k_at + (p.io.v_off - p.io.k_off);
       item_read(k);
       int key = 0, page = -1;
       auto look_up = [&](int j) {  // one tile ahead of its copies
@@ -530,6 +611,13 @@ __global__ void __launch_bounds__(kTileThreads, 1) attend_tile_kernel(const __gr
       if (warp == 8 && lane == 0 && n == 0) mbar_arrive(&bars.wanted);
     }
     cp_async_wait_all();
+    if (*(volatile int *)&bars.gave_up) {  // boxes on their way land before the block ends
+      const uint64_t t0 = global_timer_ns();
+      for (uint32_t at = loaded > kStages ? loaded - kStages : 0; at < loaded; ++at)
+        while ((!mbar_try_wait(&bars.k_full[at % kStages], at / kStages & 1) ||
+                !mbar_try_wait(&bars.v_full[at % kStages], at / kStages & 1)) && global_timer_ns() - t0 < kTileWaitNs) {
+        }
+    }
   } else {
     shrink_registers<kOtherRegisters>();
     const int role = __shfl_sync(0xffffffffu, warp, 0);

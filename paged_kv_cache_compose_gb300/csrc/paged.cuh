@@ -7,6 +7,7 @@
 #include <cuda_fp16.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "common.cuh"
 
@@ -100,6 +101,38 @@ CPKV_DEV uint32_t pack2<__half>(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
+}
+
+// acc + 0 v in both halves: from an acc of 0, 0 unless v holds an infinity or a NaN.
+template <typename T>
+CPKV_DEV uint32_t mark_infinite(uint32_t v, uint32_t acc);
+template <>
+CPKV_DEV uint32_t mark_infinite<__nv_bfloat16>(uint32_t v, uint32_t acc) {
+  uint32_t r;
+  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(v), "r"(0), "r"(acc));
+  return r;
+}
+template <>
+CPKV_DEV uint32_t mark_infinite<__half>(uint32_t v, uint32_t acc) {
+  uint32_t r;
+  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(v), "r"(0), "r"(acc));
+  return r;
+}
+template <typename T>
+CPKV_DEV uint4 mark_infinite(const uint4 &v, const uint4 &acc) {
+  return make_uint4(mark_infinite<T>(v.x, acc.x), mark_infinite<T>(v.y, acc.y), mark_infinite<T>(v.z, acc.z),
+                    mark_infinite<T>(v.w, acc.w));
+}
+
+// The infinities and NaNs of a pair, zeros for the other numbers; and the reverse.
+template <typename T>
+CPKV_DEV uint32_t infinite_of(uint32_t v) {
+  constexpr uint32_t kExponent = std::is_same<T, __nv_bfloat16>::value ? 0x7f80u : 0x7c00u;
+  return ((v & kExponent) == kExponent ? v & 0xffffu : 0u) | (((v >> 16) & kExponent) == kExponent ? v & 0xffff0000u : 0u);
+}
+template <typename T>
+CPKV_DEV uint32_t finite_of(uint32_t v) {
+  return v ^ infinite_of<T>(v);
 }
 
 }  // namespace cpkv

@@ -1,4 +1,6 @@
 """The serving operators on the GPU against plain 64-bit implementations."""
+import math
+
 import numpy as np
 import pytest
 import torch
@@ -188,6 +190,38 @@ def test_window_reads_nothing_that_no_query_sees(case):
     out, lse = run_window(poisoned, case, q, table)
     assert int(poisoned.d_status) == 0
     assert torch.equal(out, want) and torch.equal(lse, want_lse)
+
+
+MIXED = [c for c in WINDOW if max(c[8]) > 1] + [
+    (1, 1, 128, 16, 2, BF16, 0, 0, [256, 100], [700, 100]),  # 256 tokens an item: several tiles that only some see
+    (1, 1, 64, 7, 2, FP16, 140, 130, [300], [900]),
+    (64, 1, 128, 32, 2, FP16, 6, 0, [9], [300]),  # every row sees a NaN among its keys
+    (64, 1, 128, 32, 2, FP16, 60, 0, [9], [300]),
+    (16, 2, 64, 16, 2, BF16, 0, 0, [5], [2600]),  # two streams, parts
+]
+
+
+@pytest.mark.parametrize("case", MIXED, ids=lambda c: "-".join(str(x).replace(" ", "") for x in c)[:80])
+def test_window_infinite_values_reach_only_the_rows_that_see_them(case):
+    """Keys and values that hold infinities and NaNs where some query tokens of the request see them and others do not."""
+    hq, hkv, d, ps, cp, dtype, w, sinks, q_lens, kv_lens = case
+    rng, pools, table, q = window_case(case)
+    for b, (nq, kv) in enumerate(zip(q_lens, kv_lens)):
+        edge = kv - nq - (w or 10**6) + nq // 2
+        for j, what, key in [(kv - 1, math.inf, False), (kv - nq // 3 - 1, math.nan, False), (kv - nq // 2, math.nan, True),
+                             (edge, -math.inf, False), (edge + 1, math.nan, True)]:
+            if 0 <= j < kv:
+                pools.row(int(table[b, j // ps]), j % ps)[rng.integers(0, d) + (0 if key else hkv * d)] = what
+    want = model.window(q, q_lens, table, kv_lens, pools, kv_heads=hkv, dim=d, window=w, sinks=sinks, scale=d**-0.5)
+    cache = PagedCache(pools.cuda(), page_size=ps, kv_heads=hkv, key_dim=d)
+    out, lse = run_window(cache, case, q, table)
+    assert int(cache.d_status) == 0
+    finite = want[0].isfinite()
+    assert not finite.all()
+    assert torch.equal(out.cpu().isfinite(), finite)
+    seen = [torch.where(finite, x, 0.0) for x in (out.double().cpu(), want[0], want[2])]
+    model.check(seen[0], None, (seen[1], want[1], seen[2]), dtype)
+    assert torch.equal(lse.cpu().isnan(), want[1].isnan())
 
 
 @pytest.mark.parametrize("rows", [1, 40])
