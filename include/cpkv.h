@@ -620,9 +620,8 @@ int cpkv_append_rotary(int64_t n_tokens, int page_size, int cp_size, int dtype, 
  * the product with the values, and the output once more.  A query that sees no
  * key (kv_len 0, or a position below 0) gives zeros and lse = -infinity.
  * Rows that no query of the request sees (behind the window, past kv_len) are
- * not read, nor are their page ids.  A value row that some query of the
- * request sees should be finite: a neighbouring query that does not see it
- * multiplies it by a weight of zero.
+ * not read, nor are their page ids.  An infinity or a NaN in a row reaches the
+ * queries that see that row and no others.
  *   B              requests, at most CPKV_MAX_BATCH
  *   head_dim       64 or 128; q_heads a multiple of kv_heads; scale > 0
  *   h_q_lens       host int32 [B] or NULL
@@ -640,8 +639,10 @@ int cpkv_append_rotary(int64_t n_tokens, int page_size, int cp_size, int dtype, 
  *                  irrelevant, calls that overlap on the GPU must not share one
  *   flags          CPKV_DENSE_PAGES or 0
  * Status bits: PAGE_OOB (a visible token's page id is outside the pools: its row
- * reads as zeros), OUT_CAPACITY.  Errors: ARG, CAPACITY (workspace, table),
- * LIMIT (B, head_dim, sizes), CUDA.
+ * reads as zeros), OUT_CAPACITY, TIMEOUT (a bounded wait inside the kernel gave
+ * up, which should never occur: the results are undefined).  Errors: ARG,
+ * CAPACITY (workspace, table), LIMIT (B, head_dim, q_heads above 4096, kv_heads
+ * above 1024, sizes), CUDA.
  */
 int cpkv_attend_window(int B, int page_size, int cp_size, int dtype, int q_heads, int kv_heads, int head_dim,
                        int64_t row_bytes, int64_t key_offset, int64_t value_offset, const int32_t *h_q_lens,
@@ -678,9 +679,9 @@ int cpkv_attend_shared(int B, int n_groups, int page_size, int cp_size, int dtyp
                        const int32_t *h_group_sizes, const int32_t *h_prefix_lens, int64_t max_suffix_len,
                        const void *const *h_pools, const int64_t *h_pool_cap_pages, const int32_t *d_prefix_pages,
                        int64_t num_prefix_pages, const int32_t *d_page_table, int64_t table_stride,
-                       const int32_t *d_suffix_lens, const void *d_q, int64_t q_stride, float scale, void *d_out, int64_t out_stride, float *d_lse,
-                       void *d_workspace, int64_t workspace_bytes, int flags, int32_t *d_status,
-                       cpkv_stream_t stream);
+                       const int32_t *d_suffix_lens, const void *d_q, int64_t q_stride, float scale, void *d_out,
+                       int64_t out_stride, float *d_lse, void *d_workspace, int64_t workspace_bytes, int flags,
+                       int32_t *d_status, cpkv_stream_t stream);
 
 /* Device workspace of cpkv_attend_shared (host only); lengths as passed to it. */
 int cpkv_attend_shared_workspace_bytes(int B, int n_groups, int q_heads, int kv_heads, int head_dim,

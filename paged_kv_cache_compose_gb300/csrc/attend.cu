@@ -16,7 +16,7 @@ int check_heads(const HeadArgs &a) {
   if (a.dtype != CPKV_BF16 && a.dtype != CPKV_FP16) return CPKV_ERR_ARG;
   if (a.kv_heads < 1 || a.q_heads < 1 || a.q_heads % a.kv_heads != 0) return CPKV_ERR_ARG;
   if (a.head_dim != 64 && a.head_dim != 128) return CPKV_ERR_LIMIT;
-  if (a.q_heads > 4096) return CPKV_ERR_LIMIT;
+  if (a.q_heads > 4096 || a.kv_heads > kSplitMaxGrid) return CPKV_ERR_LIMIT;
   return CPKV_OK;
 }
 
@@ -63,7 +63,7 @@ struct SplitBounds {
     tiles_cap += ceil_div(nq * group, kSplitRows) + 1;
   }
   int finish(int group, int kv_heads) {
-    if (units > INT32_MAX || tokens * group > INT32_MAX || kv_heads > kSplitMaxGrid) return CPKV_ERR_LIMIT;
+    if (units > INT32_MAX || tokens * group > INT32_MAX) return CPKV_ERR_LIMIT;
     grid_cap = kv_heads * (int)std::min<int64_t>(kSplitMaxGrid / kv_heads, units > 0 ? units : 1);
     return CPKV_OK;
   }

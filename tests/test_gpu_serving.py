@@ -1,5 +1,7 @@
 """The serving operators on the GPU against plain 64-bit implementations."""
+import importlib.util
 import math
+import pathlib
 
 import numpy as np
 import pytest
@@ -392,3 +394,118 @@ def test_shared_reports_bad_pages():
         cache.d_status.zero_()
         cache.attend_shared(q, [2], [32], torch.tensor(prefix_pages, dtype=torch.int32).cuda(), table, lens, max_suffix_len=16)
         assert int(cache.d_status) == cpkv.STATUS_PAGE_OOB
+
+
+@pytest.mark.parametrize("case", [
+    (48, 1, 64, 16, 2, FP16, [3, 1], [208, 64], [40, 3, 1, 90]),  # 48 heads to one: suffixes of several row tiles, few rows
+    (160, 1, 64, 16, 2, BF16, [2], [400], [5, 200]),  # two row tiles of a single request's 160 heads
+    (300, 1, 128, 32, 2, BF16, [1, 1], [96, 1024], [70, 1]),  # more heads than an item has rows
+    (8, 1, 128, 1, 3, FP16, [24], [700], [1 + 11 * i for i in range(24)]),  # pages of one token, key by key
+], ids=lambda c: "-".join(str(x).replace(" ", "") for x in c)[:80])
+def test_shared_with_many_heads_to_one(case):
+    test_shared_matches_64_bits(case)
+
+
+@pytest.mark.parametrize("case", [
+    (20, 1, 64, 16, 2, FP16, 0, 0, [1, 1], [700, 64]),  # several row tiles of one token
+    (160, 1, 64, 48, 2, BF16, 0, 0, [1], [1500]),  # pages of 48 tokens: boxes of 16 rows
+    (300, 1, 128, 32, 2, BF16, 90, 7, [1, 2], [1030, 400]),  # more heads than an item has rows
+    (12, 1, 128, 128, 2, BF16, 0, 0, [11], [4000]),  # few rows over long keys: parts of two streams
+    (4, 1, 64, 16, 12, FP16, 0, 0, [40], [600]),  # more pools than maps
+], ids=lambda c: "-".join(str(x).replace(" ", "") for x in c)[:80])
+def test_window_with_many_heads_to_one(case):
+    test_window_matches_64_bits(case)
+
+
+def test_shared_in_a_graph_follows_the_suffixes():
+    """A captured decode step of two groups, replayed as the suffixes grow; a call of another size between."""
+    rng = np.random.default_rng(11)
+    ps, d, hkv, hq = 16, 64, 2, 8
+    sizes, prefix, most = [12, 3], [160, 32], 80
+    lists, n_pages = page_tables(rng, prefix + [most] * 15, ps)
+    pools = model.Pools(rng, n_pages, ps, 2, 2 * hkv * d, BF16)
+    prefix_pages = np.concatenate([lists[g, :n // ps] for g, n in enumerate(prefix)]).astype(np.int32)
+    q = queries(rng, 15, hq, d, BF16)
+    cache = PagedCache(pools.cuda(), page_size=ps, kv_heads=hkv, key_dim=d)
+    d_q, d_table, d_prefix = q.cuda(), torch.from_numpy(lists[2:]).cuda(), torch.from_numpy(prefix_pages).cuda()
+    lens = torch.ones(15, dtype=torch.int32, device="cuda")
+    out, lse = torch.empty_like(d_q), torch.empty(15, hq, device="cuda")
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+
+    def step():
+        cache.attend_shared(d_q, sizes, prefix, d_prefix, d_table, lens, max_suffix_len=most, out=out, lse=lse)
+
+    with torch.cuda.stream(side):
+        step()
+    side.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        step()
+    with torch.cuda.stream(side):  # a larger call on the stream: the captured one keeps its own workspace
+        cache.attend_window(queries(rng, 64, hq, d, BF16).cuda(), [64], d_table[:1], lens[:1] * 64, max_kv_len=most)
+    side.synchronize()
+    for now in ([1 + 5 * i for i in range(15)], [80 - i for i in range(15)]):
+        lens.copy_(torch.tensor(now, dtype=torch.int32))
+        graph.replay()
+        torch.cuda.synchronize()
+        model.check(out, lse, model.shared(q, sizes, prefix, prefix_pages, lists[2:], now, pools, kv_heads=hkv, dim=d, scale=0.125), BF16)
+    assert int(cache.d_status) == 0
+
+
+def test_calls_refuse_what_their_tensors_cannot_be():
+    """Types, widths, strides and counts of tensors that a call would read past or misread."""
+    d, ps = 64, 16
+    cache = PagedCache([torch.zeros(4, ps, 4 * d, dtype=BF16, device="cuda")], page_size=ps, kv_heads=2, key_dim=d)
+    q = torch.zeros(3, 4, d, dtype=BF16, device="cuda")
+    k = torch.zeros(3, 2, d, dtype=BF16, device="cuda")
+    slots, pos = torch.arange(16, 19, device="cuda"), torch.zeros(3, dtype=torch.int32, device="cuda")
+    turns = torch.ones(8, d, device="cuda")
+    table, lens = torch.ones(3, 2, dtype=torch.int32, device="cuda"), torch.ones(3, dtype=torch.int32, device="cuda")
+
+    def append(**changed):
+        a = {**dict(k=k, v=k, slots=slots, positions=pos, cos_sin=turns), **changed}
+        return cache.append_rotary(a.pop("k"), a.pop("v"), a.pop("slots"), a.pop("positions"), a.pop("cos_sin"), **a)
+
+    def window(**changed):
+        a = {**dict(q=q, q_lens=None, table=table, lens=lens, max_kv_len=32), **changed}
+        return cache.attend_window(a.pop("q"), a.pop("q_lens"), a.pop("table"), a.pop("lens"), **a)
+
+    def shared(**changed):
+        a = {**dict(q=q, sizes=[3], prefix=[16], pages=lens[:1], table=table, lens=lens, max_suffix_len=32), **changed}
+        return cache.attend_shared(a.pop("q"), a.pop("sizes"), a.pop("prefix"), a.pop("pages"), a.pop("table"), a.pop("lens"), **a)
+
+    append(), window(), shared()
+    for call, bad in [
+        (append, dict(k=k.float())), (append, dict(k=k.half())), (append, dict(k=k[:, :1])), (append, dict(v=k[:2])), (append, dict(k=k.cpu())),
+        (append, dict(k=k.transpose(0, 1))), (append, dict(slots=slots.int())), (append, dict(slots=slots[:2])), (append, dict(positions=pos.long())),
+        (append, dict(positions=pos[:2])), (append, dict(positions=torch.zeros(5, 3, dtype=torch.int32, device="cuda"))),
+        (append, dict(cos_sin=turns.half())), (append, dict(cos_sin=turns[:, :40].contiguous())), (append, dict(cos_sin=turns[:, :32])),
+        (append, dict(q=q[:2])), (append, dict(q=q, q_out=q[:, :2])), (append, dict(positions=torch.zeros(2, 3, dtype=torch.int32, device="cuda"))),
+        (append, dict(axis_of_freq=[0] * 31)),
+        (window, dict(q=q.half())), (window, dict(q=q[:, :3])), (window, dict(q=q[..., :32])), (window, dict(q=q[:2])), (window, dict(q_lens=[1, 1])),
+        (window, dict(q_lens=[1, 1, 2])), (window, dict(table=table.long())), (window, dict(table=table[:2])), (window, dict(table=table.t())),
+        (window, dict(lens=lens.long())), (window, dict(max_kv_len=33)), (window, dict(out=q.float())), (window, dict(out=q[:2])),
+        (window, dict(lse=torch.zeros(3, 2, device="cuda"))), (window, dict(scale=0.0)), (window, dict(window=-1)),
+        (shared, dict(sizes=[2])), (shared, dict(sizes=[2, 1])), (shared, dict(prefix=[20])), (shared, dict(prefix=[32])), (shared, dict(pages=lens.long())),
+        (shared, dict(table=table[:2])), (shared, dict(lens=lens[:2])), (shared, dict(max_suffix_len=33)), (shared, dict(q=q.cpu())),
+    ]:
+        with pytest.raises(cpkv.CpkvError):
+            call(**bad)
+    torch.cuda.synchronize()
+    assert int(cache.d_status) == 0
+
+
+def test_example_of_a_serving_step():
+    """Compose, append and both attentions together, as examples/serving_step.py runs them."""
+    path = pathlib.Path(__file__).parents[1] / "examples" / "serving_step.py"
+    spec = importlib.util.spec_from_file_location("serving_step", path)
+    example = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(example)
+    got = example.run()
+    assert not any(got["status"])
+    assert torch.equal(got["prefill"], got["paged"])
+    u = model.bound_of(BF16)
+    for a, b in zip(got["decode"], got["window"]):  # the same sums in another order: a step of weights and of the result
+        a, b = a.double(), b.double()
+        assert bool(((a - b).abs() <= 2 * u * b.abs() + 2 * (u + 2.0**-13) * 5).all())  # weighted |values| below 5

@@ -71,8 +71,8 @@ def window_args():
     (dict(B=0, tokens=0), cpkv.CPKV_OK), (dict(q_lens=np.zeros(2, np.int32), tokens=0), cpkv.CPKV_OK),
     (dict(tokens=4), cpkv.CPKV_ERR_ARG), (dict(tokens=0), cpkv.CPKV_ERR_ARG),
     (dict(B=-1), cpkv.CPKV_ERR_ARG), (dict(B=1025, q_lens=None), cpkv.CPKV_ERR_LIMIT), (dict(q_lens=np.array([1, -1], np.int32)), cpkv.CPKV_ERR_ARG),
-    (dict(ps=-4), cpkv.CPKV_ERR_ARG), (dict(dtype=5), cpkv.CPKV_ERR_ARG), (dict(hq=3), cpkv.CPKV_ERR_ARG), (dict(hkv=0), cpkv.CPKV_ERR_ARG),
-    (dict(d=96), cpkv.CPKV_ERR_LIMIT), (dict(d=128), cpkv.CPKV_ERR_ARG), (dict(max_kv=-1), cpkv.CPKV_ERR_ARG),
+    (dict(ps=-4), cpkv.CPKV_ERR_ARG), (dict(dtype=5), cpkv.CPKV_ERR_ARG), (dict(hq=3), cpkv.CPKV_ERR_ARG), (dict(hkv=0), cpkv.CPKV_ERR_ARG), (dict(hq=4100), cpkv.CPKV_ERR_LIMIT),
+    (dict(hq=1025, hkv=1025), cpkv.CPKV_ERR_LIMIT), (dict(d=96), cpkv.CPKV_ERR_LIMIT), (dict(d=128), cpkv.CPKV_ERR_ARG), (dict(max_kv=-1), cpkv.CPKV_ERR_ARG),
     (dict(max_kv=65), cpkv.CPKV_ERR_CAPACITY), (dict(stride=-1), cpkv.CPKV_ERR_CAPACITY), (dict(window=-1), cpkv.CPKV_ERR_ARG),
     (dict(sinks=-1), cpkv.CPKV_ERR_ARG), (dict(table=None), cpkv.CPKV_ERR_ARG), (dict(kv_lens=None), cpkv.CPKV_ERR_ARG),
     (dict(q=None), cpkv.CPKV_ERR_ARG), (dict(q=260), cpkv.CPKV_ERR_ARG), (dict(qs=252), cpkv.CPKV_ERR_ARG), (dict(os=128), cpkv.CPKV_ERR_ARG),
