@@ -34,59 +34,66 @@ struct AppendParams {
   alignas(4) uint8_t axis[kMaxHalf];
 };
 
+// One unit of work: unit u of token n, and what the token says of itself.
+template <bool kAxes>
+struct Work {
+  int64_t id;
+  int n, u;
+  int64_t slot;
+  int pos[kAxes ? kMaxAxes : 1];
+
+  CPKV_DEV int64_t position(uint32_t axis) const {
+    if constexpr (kAxes) return axis == 0 ? pos[0] : axis == 1 ? pos[1] : axis == 2 ? pos[2] : pos[3];
+    return pos[0];
+  }
+  // Whether every position of the token lies in the table: a token that fails is
+  // dropped whole.
+  CPKV_DEV bool positions_ok(const AppendParams &p) const {
+    bool ok = pos[0] >= 0 && pos[0] < p.max_pos;
+    if constexpr (kAxes) {
+#pragma unroll
+      for (int a = 1; a < kMaxAxes; ++a) ok &= pos[a] >= 0 && pos[a] < p.max_pos;
+    }
+    return ok;
+  }
+};
+
+template <bool kAxes>
+CPKV_DEV Work<kAxes> find_work(const AppendParams &p, int64_t id, int64_t total) {
+  Work<kAxes> w;
+  w.id = id;
+  if (id >= total) return w;
+  w.n = id < INT32_MAX ? div_by((int)id, p.threads) : (int)(id / p.threads.d);
+  w.u = (int)(id - (int64_t)w.n * p.threads.d);
+  w.slot = p.slots[w.n];
+  w.pos[0] = p.positions[w.n];
+  if constexpr (kAxes) {
+#pragma unroll
+    for (int a = 1; a < kMaxAxes; ++a) w.pos[a] = a < p.n_axes ? p.positions[a * p.pos_stride + w.n] : 0;
+  }
+  return w;
+}
+
 // Four cosines and sines, of frequencies f .. f + 3.
 template <bool kAxes>
-CPKV_DEV void angles4(const AppendParams &p, int n, int64_t first_pos, int f, float *c, float *s) {
+CPKV_DEV void angles4(const AppendParams &p, const Work<kAxes> &w, int f, float *c, float *s) {
   const int rot = 2 * p.half;
   uint32_t axes = 0;
   if (kAxes) axes = *reinterpret_cast<const uint32_t *>(p.axis + f);
   if (!kAxes || axes == (axes & 0xff) * 0x01010101u) {
-    const int64_t pos = kAxes ? p.positions[(axes & 0xff) * p.pos_stride + n] : first_pos;
-    const float4 cs = __ldg(reinterpret_cast<const float4 *>(p.table + pos * rot + f));
-    const float4 sn = __ldg(reinterpret_cast<const float4 *>(p.table + pos * rot + p.half + f));
+    const float *const row = p.table + w.position(axes & 0xff) * rot + f;
+    const float4 cs = __ldg(reinterpret_cast<const float4 *>(row));
+    const float4 sn = __ldg(reinterpret_cast<const float4 *>(row + p.half));
     c[0] = cs.x, c[1] = cs.y, c[2] = cs.z, c[3] = cs.w;
     s[0] = sn.x, s[1] = sn.y, s[2] = sn.z, s[3] = sn.w;
     return;
   }
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const int64_t pos = p.positions[p.axis[f + i] * p.pos_stride + n];
-    c[i] = __ldg(p.table + pos * rot + f + i);
-    s[i] = __ldg(p.table + pos * rot + p.half + f + i);
+    const float *const row = p.table + w.position(axes >> (8 * i) & 0xff) * rot + f + i;
+    c[i] = __ldg(row);
+    s[i] = __ldg(row + p.half);
   }
-}
-
-// One unit of work: unit u of token n, and what the token says of itself.
-struct Work {
-  int64_t id;
-  int n, u;
-  int64_t slot;
-  int first_pos;
-};
-
-CPKV_DEV Work find_work(const AppendParams &p, int64_t id, int64_t total) {
-  Work w;
-  w.id = id;
-  if (id >= total) return w;
-  w.n = id < INT32_MAX ? div_by((int)id, p.threads) : (int)(id / p.threads.d);
-  w.u = (int)(id - (int64_t)w.n * p.threads.d);
-  w.slot = p.slots[w.n];
-  w.first_pos = p.positions[w.n];
-  return w;
-}
-
-// Whether every position of a token lies in the table: a token that fails is
-// dropped whole.
-template <bool kAxes>
-CPKV_DEV bool positions_ok(const AppendParams &p, const Work &w) {
-  bool ok = w.first_pos >= 0 && w.first_pos < p.max_pos;
-  if (kAxes) {
-    for (int a = 1; a < p.n_axes; ++a) {
-      const int64_t pos = p.positions[a * p.pos_stride + w.n];
-      ok &= pos >= 0 && pos < p.max_pos;
-    }
-  }
-  return ok;
 }
 
 // Row of a slot in the pools; null (with a status bit) where its page is
@@ -109,14 +116,10 @@ CPKV_DEV char *slot_row(const AppendParams &p, int64_t slot, bool reports) {
 // threads hold a head's neighbouring units, so warps read and write whole heads.
 // The threads after those copy kEach 16-byte chunks of the values each.
 template <typename T, bool kPairs, bool kAxes, int kEach>
-CPKV_DEV void do_work(const AppendParams &p, const Work &w) {
+CPKV_DEV void do_work(const AppendParams &p, const Work<kAxes> &w) {
   const int n = w.n, u = w.u;
-  const bool ok = positions_ok<kAxes>(p, w);
-  if (!ok && u == 0) raise_status(p.status, CPKV_STATUS_POS_OOB);
-  char *const row = ok ? slot_row(p, w.slot, u == 0) : nullptr;
-
+  const bool ok = w.positions_ok(p);
   if (u >= p.rotated) {  // values
-    if (row == nullptr) return;
     const char *src = p.v + n * p.v_stride;
     const int first = u - p.rotated;
     uint4 x[kEach];
@@ -125,6 +128,8 @@ CPKV_DEV void do_work(const AppendParams &p, const Work &w) {
       const int c = first + e * p.value_groups;
       if (c < p.value_chunks) x[e] = ld_stream16(src + c * 16);
     }
+    char *const row = ok ? slot_row(p, w.slot, false) : nullptr;
+    if (row == nullptr) return;
 #pragma unroll
     for (int e = 0; e < kEach; ++e) {
       const int c = first + e * p.value_groups;
@@ -152,9 +157,11 @@ CPKV_DEV void do_work(const AppendParams &p, const Work &w) {
   }
   float c[8], s[8];
   if (turns && ok) {
-    angles4<kAxes>(p, n, w.first_pos, unit * 8, c, s);
-    angles4<kAxes>(p, n, w.first_pos, unit * 8 + 4, c + 4, s + 4);
+    angles4<kAxes>(p, w, unit * 8, c, s);
+    angles4<kAxes>(p, w, unit * 8 + 4, c + 4, s + 4);
   }
+  if (!ok && u == 0) raise_status(p.status, CPKV_STATUS_POS_OOB);
+  char *const row = ok ? slot_row(p, w.slot, u == 0) : nullptr;
 #pragma unroll
   for (int e = 0; e < kEach; ++e) {
     const int head = first + e * p.head_groups;
@@ -199,9 +206,9 @@ CPKV_DEV void do_work(const AppendParams &p, const Work &w) {
 template <typename T, bool kPairs, bool kAxes, int kEach>
 __global__ void __launch_bounds__(kThreads) append_rotary_kernel(const __grid_constant__ AppendParams p) {
   const int64_t total = (int64_t)p.n_tokens * p.threads.d, step = (int64_t)gridDim.x * kThreads;
-  Work w = find_work(p, (int64_t)blockIdx.x * kThreads + threadIdx.x, total);
+  Work<kAxes> w = find_work<kAxes>(p, (int64_t)blockIdx.x * kThreads + threadIdx.x, total);
   while (w.id < total) {
-    const Work next = find_work(p, w.id + step, total);
+    const Work<kAxes> next = find_work<kAxes>(p, w.id + step, total);
     do_work<T, kPairs, kAxes, kEach>(p, w);
     w = next;
   }
