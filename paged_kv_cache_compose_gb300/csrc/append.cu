@@ -296,9 +296,9 @@ extern "C" int cpkv_append_rotary(int64_t n_tokens, int page_size, int cp_size, 
   p.value_chunks = kv_heads * value_dim / 8;
   const int head_units = (key_dim + 15) / 16;
   // Two heads a thread once that leaves every SM its 1024 threads, one before.
-  // Traced tokens (44600, 32 + 8 heads of 128): 190 us with two, 210 with one, 206
-  // with four (whose registers halve the threads of an SM); 5.8 TB/s, 86% of the
-  // measured copy rate.
+  // 44600 tokens of 32 + 8 heads of 128, all of a head rotated: 168 us with two (6.5
+  // TB/s, 96% of the measured copy rate), 182 with one; four need registers that halve
+  // the threads of an SM and lost to two.  512 tokens: 6.2 us with either.
   const int64_t units = n_tokens * ((int64_t)p.heads * head_units + p.value_chunks);
   const int each = units >= (int64_t)device_sm_count() * 2 * 1024 ? 2 : 1;
   p.head_groups = (int)ceil_div(p.heads, each);

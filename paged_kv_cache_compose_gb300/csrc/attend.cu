@@ -171,8 +171,10 @@ struct TileBounds {
 };
 
 // Which kernel reads the keys: the split kernel takes 16 packed rows at a time
-// and reads the keys again for each 16, the tile kernel takes 256.
-bool few_rows(int64_t max_rows) { return max_rows <= 2 * kSplitRows; }
+// and reads the keys again for each 16, the tile kernel takes 256.  64 requests of
+// 2048 keys, 8 heads of 128: at 16 rows 88 us with the split kernel and 95 with the
+// tile kernel, at 24 rows 160 and 103 us.
+bool few_rows(int64_t max_rows) { return max_rows <= kSplitRows; }
 
 // How a call is done, from host lengths alone.
 struct WindowPlan {
@@ -183,7 +185,11 @@ struct WindowPlan {
 };
 
 // A block takes whole tiles of few rows when no sequence has more units of keys
-// than this: the units one after the other then cost less than joining parts does.
+// than this and there are no more tiles than SMs: the units one after the other then
+// cost less than joining parts does (4 requests, 8 heads of 128: 384 keys in 10.3 us
+// where parts take 12.3, 512 keys in 12.3 either way, 1024 in 20.5 where parts take
+// 13.4), and no more blocks wait than lines would have (64 requests of 384 keys: 36 us
+// with whole tiles, 26 with parts).
 constexpr int64_t kWholeUnits = 8;
 
 int window_plan(WindowPlan *w, const HeadArgs &a, int B, const int32_t *h_q_lens, int64_t max_kv, int window, int sinks) {
@@ -198,7 +204,8 @@ int window_plan(WindowPlan *w, const HeadArgs &a, int B, const int32_t *h_q_lens
   w->tokens = w->tile.tokens;
   bool uniform = B > 0;
   for (int s = 1; s < B && h_q_lens != nullptr; ++s) uniform &= h_q_lens[s] == h_q_lens[0];
-  w->whole = w->few && uniform && w->split.max_tiles <= kWholeUnits;
+  w->whole = w->few && uniform && w->split.max_tiles <= kWholeUnits &&
+             w->split.tiles_cap * a.kv_heads <= 2 * (int64_t)device_sm_count();
   const int rc = w->few ? w->split.finish(group, a.kv_heads) : w->tile.finish(a.kv_heads, a.head_dim);
   w->bytes = w->whole ? 0
              : w->few ? w->split.bytes(B, a.kv_heads, a.head_dim, true)
@@ -353,7 +360,9 @@ TileSource<S> source_of(const TileParams<S> &p) {
   return s;
 }
 
-// Four warps a row while rows are too few to fill the SMs with a warp each.
+// Four warps a row while rows are too few to fill the SMs with a warp each: 32 rows
+// of 8192 keys take 18.0 us with four and 22.6 with one, 8192 rows of 1024 keys 252 us
+// with four and 158 with one (both with the pass before them).
 template <typename T, int D, typename Source>
 int join_pass(const Source &source, const AttendIo &io, int64_t rows, cudaStream_t stream) {
   JoinParams<Source> p = {};
