@@ -184,14 +184,6 @@ struct WindowPlan {
   int64_t tokens = 0, bytes = 0;
 };
 
-// A block takes whole tiles of few rows when no sequence has more units of keys
-// than this and there are no more tiles than SMs: the units one after the other then
-// cost less than joining parts does (4 requests, 8 heads of 128: 384 keys in 10.3 us
-// where parts take 12.3, 512 keys in 12.3 either way, 1024 in 20.5 where parts take
-// 13.4), and no more blocks wait than lines would have (64 requests of 384 keys: 36 us
-// with whole tiles, 26 with parts).
-constexpr int64_t kWholeUnits = 8;
-
 int window_plan(WindowPlan *w, const HeadArgs &a, int B, const int32_t *h_q_lens, int64_t max_kv, int window, int sinks) {
   const int group = a.q_heads / a.kv_heads;
   for (int s = 0; s < B; ++s) {
@@ -204,6 +196,12 @@ int window_plan(WindowPlan *w, const HeadArgs &a, int B, const int32_t *h_q_lens
   w->tokens = w->tile.tokens;
   bool uniform = B > 0;
   for (int s = 1; s < B && h_q_lens != nullptr; ++s) uniform &= h_q_lens[s] == h_q_lens[0];
+  // A block takes whole tiles of few rows when no sequence has more units of keys
+  // than kWholeUnits and there are no more tiles than SMs: the units one after the other then
+  // cost less than joining parts does (4 requests, 8 heads of 128: 384 keys in 10.3 us
+  // where parts take 12.3, 512 keys in 12.3 either way, 1024 in 20.5 where parts take
+  // 13.4), and no more blocks wait than lines would have (64 requests of 384 keys: 36 us
+  // with whole tiles, 26 with parts).
   w->whole = w->few && uniform && w->split.max_tiles <= kWholeUnits &&
              w->split.tiles_cap * a.kv_heads <= 2 * (int64_t)device_sm_count();
   const int rc = w->few ? w->split.finish(group, a.kv_heads) : w->tile.finish(a.kv_heads, a.head_dim);

@@ -29,6 +29,7 @@ constexpr int kWarpKeys = kSplitTile / kSplitWarps;  // 16
 // How a block finds its work: a stretch of the line of units, or one tile of few keys
 // (with a deeper ring: its time is that of a few loads).
 enum SplitMode { kLine, kFewKeys };
+constexpr int kWholeUnits = 8;  // most units of a tile of few keys
 
 template <int D, SplitMode kMode>
 struct SplitShape {
@@ -80,6 +81,7 @@ __global__ void __launch_bounds__(kSplitWarps * 32, SplitShape<D, kMode>::kBlock
   constexpr bool kWhole = kMode != kLine;
   extern __shared__ __align__(128) char smem[];
   __shared__ int scan_scratch[33];
+  __shared__ int few_pages[kWhole ? kSplitWarps : 1][kWholeUnits][kWarpKeys];
   int *cum = reinterpret_cast<int *>(smem + Shape::kSmem);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int count = p.seqs.count;
@@ -144,8 +146,20 @@ __global__ void __launch_bounds__(kSplitWarps * 32, SplitShape<D, kMode>::kBlock
   auto look_up = [&] {  // the page of this lane's key, one unit ahead of its copy
     ld_key = ld.keys.tile_start(ld.j, kSplitTile) + warp * kWarpKeys + (lane & 15);
     ld_sees = ld.keys.any_sees(ld_key);
-    ld_page = ld_sees ? p.seqs.pages(ld.s)[div_by(ld_key, p.pools.page_size)] : -1;
+    if (kWhole && ld.j < kWholeUnits) {
+      ld_page = few_pages[warp][ld.j][lane & 15];
+    } else {
+      ld_page = ld_sees ? p.seqs.pages(ld.s)[div_by(ld_key, p.pools.page_size)] : -1;
+    }
   };
+  if constexpr (kWhole) {  // all page ids of the tile at once: one latency, not one per unit
+#pragma unroll
+    for (int i = 0; i < kWholeUnits; i += 2) {
+      const int j = i + (lane >> 4), key = ld.keys.tile_start(j, kSplitTile) + warp * kWarpKeys + (lane & 15);
+      if (j < u1 && ld.keys.any_sees(key)) few_pages[warp][j][lane & 15] = p.seqs.pages(ld.s)[div_by(key, p.pools.page_size)];
+    }
+    __syncwarp();
+  }
   if (u0 < u1) look_up();
   auto load_next = [&](int stage) {
     if (ld_u < u1) {
