@@ -135,6 +135,8 @@ struct TileBounds {
   }
   // Prefixes and suffixes of a shared call: as few parts as leave no item longer than
   // the SMs' even share of all work (a suffix counted at half its bound and a step).
+  // 48 requests of three prefixes of about 9000: 41.3 us so, 44.5 with items of half that
+  // length, 49.2 of one and a half; 256 requests on one of 65536: 556, 572 and 555 us.
   int finish_shared(int kv_heads) {
     const int64_t items = tiles * kv_heads, single_items = singles * single_tiles * kv_heads, sms = device_sm_count();
     const int64_t all = steps(max_keys, max_rows), of_single = steps(single_keys, group);
