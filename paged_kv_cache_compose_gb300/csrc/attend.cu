@@ -153,9 +153,13 @@ struct TileBounds {
   }
   int64_t bytes(int kv_heads, int head_dim, bool direct) const {
     if (direct && splits == 1) return 0;
-    return round_up(rows(kv_heads) * 8, 256) + round_up(rows(kv_heads) * head_dim * 4, 256);
+    return kPartAlign + round_up(rows(kv_heads) * 8, 256) + round_up(rows(kv_heads) * head_dim * 4, 256);
   }
+  // The parts' values go out 32 bytes at a time, and a caller's workspace may begin at
+  // any multiple of 16: bytes() counts the room for the step to the next 32.
+  static constexpr int64_t kPartAlign = 32;
   TileSpace space(char *at, int kv_heads) const {
+    at += -reinterpret_cast<uintptr_t>(at) & (kPartAlign - 1);
     TileSpace s;
     s.ml = reinterpret_cast<float *>(at);
     s.o = reinterpret_cast<float *>(at + round_up(rows(kv_heads) * 8, 256));

@@ -1,0 +1,69 @@
+"""Serving calls where their arguments sit at the edges of what the contract allows, against plain 64-bit implementations."""
+import numpy as np
+import pytest
+import torch
+
+import serving_model as model
+from paged_kv_cache_compose_gb300 import cpkv
+from paged_kv_cache_compose_gb300.runtime import PagedCache
+from test_gpu_serving import BF16, FP16, page_tables, queries
+
+pytestmark = pytest.mark.gpu
+
+
+def workspace_at(need, offset):
+    """`need` bytes at `offset` past a 256-byte boundary, and a check that nothing around them was written."""
+    whole = torch.full((offset + need + 64,), 0xA5, dtype=torch.uint8, device="cuda")
+    assert whole.data_ptr() % 256 == 0
+
+    def untouched():
+        return bool((whole[:offset] == 0xA5).all()) and bool((whole[offset + need:] == 0xA5).all())
+
+    return whole[offset:offset + need], untouched
+
+
+@pytest.mark.parametrize("offset", [0, 16, 32, 48])
+@pytest.mark.parametrize("q_lens, kv_lens", [([11], [4000]), ([1, 1], [3000, 900])], ids=["tile", "split"])
+def test_window_workspace_at_any_multiple_of_16(q_lens, kv_lens, offset):
+    """The workspace that the sizing call asks for, wherever it begins, is enough and all that is written."""
+    hq, hkv, d, ps = 12, 1, 128, 64
+    rng = np.random.default_rng(offset)
+    lists, n_pages = page_tables(rng, kv_lens, ps)
+    pools = model.Pools(rng, n_pages, ps, 2, 2 * hkv * d, BF16)
+    q = queries(rng, sum(q_lens), hq, d, BF16)
+    cache = PagedCache(pools.cuda(), page_size=ps, kv_heads=hkv, key_dim=d)
+    need = cpkv.cpkv_attend_window_workspace_bytes(len(q_lens), hq, hkv, d, q_lens, max(kv_lens))
+    assert need > 0
+    workspace, untouched = workspace_at(need, offset)
+    d_q = q.cuda()
+    out, lse = torch.empty_like(d_q), torch.empty(q.shape[:2], device="cuda")
+    cpkv.cpkv_attend_window(d_q, q_lens, torch.from_numpy(lists).cuda(), torch.tensor(kv_lens, dtype=torch.int32).cuda(),
+                            table=cache.table, kv_heads=hkv, max_kv_len=max(kv_lens), window=0, sinks=0, scale=d**-0.5, out=out,
+                            lse=lse, workspace=workspace, d_status=cache.d_status)
+    torch.cuda.synchronize()
+    assert int(cache.d_status) == 0 and untouched()
+    model.check(out, lse, model.window(q, q_lens, lists, kv_lens, pools, kv_heads=hkv, dim=d, window=0, sinks=0, scale=d**-0.5), BF16)
+
+
+@pytest.mark.parametrize("offset", [0, 16, 32, 48])
+@pytest.mark.parametrize("requests", [24, 2], ids=["tile", "split"])
+def test_shared_workspace_at_any_multiple_of_16(requests, offset):
+    hq, hkv, d, ps = 8, 2, 64, 16
+    sizes, prefix, suffix = [requests], [800], [1 + 7 * i for i in range(requests)]
+    rng = np.random.default_rng(offset)
+    lists, n_pages = page_tables(rng, prefix + suffix, ps)
+    pools = model.Pools(rng, n_pages, ps, 2, 2 * hkv * d, FP16)
+    prefix_pages = lists[0, :prefix[0] // ps].astype(np.int32)
+    q = queries(rng, requests, hq, d, FP16)
+    cache = PagedCache(pools.cuda(), page_size=ps, kv_heads=hkv, key_dim=d)
+    need = cpkv.cpkv_attend_shared_workspace_bytes(requests, hq, hkv, d, sizes, prefix, max(suffix))
+    workspace, untouched = workspace_at(need, offset)
+    d_q = q.cuda()
+    out, lse = torch.empty_like(d_q), torch.empty(q.shape[:2], device="cuda")
+    cpkv.cpkv_attend_shared(d_q, sizes, prefix, torch.from_numpy(prefix_pages).cuda(), torch.from_numpy(lists[1:]).cuda(),
+                            torch.tensor(suffix, dtype=torch.int32).cuda(), table=cache.table, kv_heads=hkv,
+                            max_suffix_len=max(suffix), scale=d**-0.5, out=out, lse=lse, workspace=workspace, d_status=cache.d_status)
+    torch.cuda.synchronize()
+    assert int(cache.d_status) == 0 and untouched()
+    want = model.shared(q, sizes, prefix, prefix_pages, lists[1:], suffix, pools, kv_heads=hkv, dim=d, scale=d**-0.5)
+    model.check(out, lse, want, FP16)
