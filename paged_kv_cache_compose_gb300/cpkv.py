@@ -539,7 +539,7 @@ def cpkv_append_rotary(k, v, d_slots, d_positions, d_cos_sin, *, table: PoolTabl
 
 
 def cpkv_attend_window_workspace_bytes(B, q_heads, kv_heads, head_dim, q_lens, max_kv_len, window=0, sinks=0) -> int:
-    """Device workspace of ``cpkv_attend_window`` (``q_lens`` None: one query each)."""
+    """Workspace of ``cpkv_attend_window`` on the current device (``q_lens`` None: one query each)."""
     ql = None if q_lens is None else _host_i32(q_lens)
     out = ctypes.c_int64(0)
     _check("cpkv_attend_window_workspace_bytes", load().cpkv_attend_window_workspace_bytes(
@@ -558,7 +558,7 @@ def cpkv_attend_window(q, q_lens, page_table, d_kv_lens, *, table: PoolTable, kv
 
 
 def cpkv_attend_shared_workspace_bytes(B, q_heads, kv_heads, head_dim, group_sizes, prefix_lens, max_suffix_len) -> int:
-    """Device workspace of ``cpkv_attend_shared``."""
+    """Workspace of ``cpkv_attend_shared`` on the current device."""
     gs, pl = _host_i32(group_sizes), _host_i32(prefix_lens)
     out = ctypes.c_int64(0)
     _check("cpkv_attend_shared_workspace_bytes", load().cpkv_attend_shared_workspace_bytes(

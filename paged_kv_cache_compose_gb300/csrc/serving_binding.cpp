@@ -6,6 +6,7 @@
 // took 8 of a small call's 12.  Each function returns the entry point's code; a
 // tensor that does not fit raises what the `fail` function given to set_fail makes.
 #include <Python.h>
+#include <c10/core/DeviceGuard.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <vector>
@@ -171,15 +172,19 @@ cpkv_stream_t stream_of(PyObject *o) {
   return reinterpret_cast<cpkv_stream_t>(static_cast<uintptr_t>(PyLong_AsUnsignedLongLong(o)));
 }
 
-// Runs a call; Python sees an exception instead of C++.
+// Runs a call, its first argument the table, with the pools' device current: the entry
+// points launch on the current device, and their stream handle is one of the pools'.
+// Python sees an exception instead of C++.
 template <typename F>
-PyObject *guarded(Py_ssize_t got, Py_ssize_t wanted, F f) {
+PyObject *guarded(PyObject *const *a, Py_ssize_t got, Py_ssize_t wanted, F f) {
   if (got != wanted) {
     PyErr_Format(PyExc_TypeError, "%zd arguments: %zd are wanted", got, wanted);
     return nullptr;
   }
   try {
-    const int rc = f();
+    const Table &t = table(a[0]);
+    const c10::DeviceGuard current(c10::Device(c10::kCUDA, static_cast<c10::DeviceIndex>(t.device)));
+    const int rc = f(t);
     if (PyErr_Occurred()) return nullptr;
     return PyLong_FromLong(rc);
   } catch (const Failed &) {
@@ -193,8 +198,7 @@ PyObject *guarded(Py_ssize_t got, Py_ssize_t wanted, F f) {
 
 // (table, kv_heads, key_dim, value_dim, k, v, slots, positions, cos_sin, status, q, q_out, axis_of_freq, interleaved, stream)
 PyObject *append_rotary(PyObject *, PyObject *const *a, Py_ssize_t n) {
-  return guarded(n, 15, [&] {
-    const Table &t = table(a[0]);
+  return guarded(a, n, 15, [&](const Table &t) {
     const Rows k = rows(a[4], "k", t), v = rows(a[5], "v", t);
     if (k.heads != whole(a[1]) || k.dim != whole(a[2])) fail("k", "[tokens, kv_heads, key_dim] of the cache");
     if (v.n != k.n || v.heads != k.heads || v.dim != whole(a[3])) fail("v", "[tokens, kv_heads, value_dim] of the cache, k's tokens");
@@ -232,8 +236,7 @@ PyObject *append_rotary(PyObject *, PyObject *const *a, Py_ssize_t n) {
 
 // (table, kv_heads, q, q_lens, page_table, kv_lens, max_kv_len, window, sinks, scale, out, lse, workspace, status, stream)
 PyObject *attend_window(PyObject *, PyObject *const *a, Py_ssize_t n) {
-  return guarded(n, 15, [&] {
-    const Table &t = table(a[0]);
+  return guarded(a, n, 15, [&](const Table &t) {
     const Rows q = rows(a[2], "q", t), out = rows(a[10], "out", t);
     if (!q.same_shape(out)) fail("out", "q's shape");
     int64_t requests = 0, bytes = 0, word = 0;
@@ -258,8 +261,7 @@ PyObject *attend_window(PyObject *, PyObject *const *a, Py_ssize_t n) {
 
 // (table, kv_heads, q, group_sizes, prefix_lens, prefix_pages, page_table, suffix_lens, max_suffix_len, scale, out, lse, workspace, status, stream)
 PyObject *attend_shared(PyObject *, PyObject *const *a, Py_ssize_t n) {
-  return guarded(n, 15, [&] {
-    const Table &t = table(a[0]);
+  return guarded(a, n, 15, [&](const Table &t) {
     const Rows q = rows(a[2], "q", t), out = rows(a[10], "out", t);
     if (!q.same_shape(out)) fail("out", "q's shape");
     int64_t requests = 0, prefix_pages = 0, bytes = 0, word = 0;

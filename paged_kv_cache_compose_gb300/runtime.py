@@ -220,7 +220,8 @@ class PagedCache:
     def _grow(self, fn: str, rc: int, stream: int, size):
         """A larger workspace where the call wants one; its error otherwise."""
         workspace = self._workspaces.get(stream)
-        need = size() if rc == cpkv.CPKV_ERR_CAPACITY else 0
+        with torch.cuda.device(self.device):  # the size goes by its SMs
+            need = size() if rc == cpkv.CPKV_ERR_CAPACITY else 0
         if need <= (0 if workspace is None else workspace.numel()):
             cpkv._check(fn, rc)
         if workspace is not None:

@@ -67,3 +67,31 @@ def test_shared_workspace_at_any_multiple_of_16(requests, offset):
     assert int(cache.d_status) == 0 and untouched()
     want = model.shared(q, sizes, prefix, prefix_pages, lists[1:], suffix, pools, kv_heads=hkv, dim=d, scale=d**-0.5)
     model.check(out, lse, want, FP16)
+
+
+def test_calls_run_with_the_pools_device_current():
+    """Every call makes the pools' device current before it looks at anything else: of a device that is not there, the switch itself fails."""
+    cache = PagedCache([torch.zeros(4, 16, 256, dtype=BF16, device="cuda")], page_size=16, kv_heads=2, key_dim=64)
+    rows = torch.zeros(0, 2, 64, dtype=BF16, device="cuda")
+    none = torch.zeros(0, dtype=torch.int32, device="cuda")
+    turns, pages = torch.ones(8, 64, device="cuda"), torch.zeros(0, 1, dtype=torch.int32, device="cuda")
+
+    def calls():
+        cache.append_rotary(rows, rows, none.long(), none, turns)
+        cache.attend_window(rows, None, pages, none, max_kv_len=16, out=rows)
+        cache.attend_shared(rows, [], [], none, pages, none, max_suffix_len=16, out=rows)
+
+    calls()
+    missing = torch.cuda.device_count()
+    cache.table._table.device = missing
+    stream = torch.cuda.current_stream().cuda_stream
+    for call in (lambda: cache.append_rotary(rows, rows, none.long(), none, turns, stream=stream),
+                 lambda: cache.attend_window(rows, None, pages, none, max_kv_len=16, out=rows, stream=stream),
+                 lambda: cache.attend_shared(rows, [], [], none, pages, none, max_suffix_len=16, out=rows, stream=stream)):
+        with pytest.raises(RuntimeError) as e:
+            call()
+        assert not isinstance(e.value, cpkv.CpkvError)  # which is a tensor's refusal
+    assert torch.cuda.current_device() == 0
+    cache.table._table.device = 0
+    calls()
+    assert int(cache.d_status) == 0
