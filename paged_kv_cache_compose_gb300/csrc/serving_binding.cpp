@@ -98,15 +98,23 @@ float *lse_of(PyObject *o, const Table &t, const Rows &q) {
   return static_cast<float *>(x.data_ptr());
 }
 
-// Bytes of a workspace or a status word.
-void *memory(PyObject *o, int64_t *bytes) {
+// A workspace and its bytes.
+void *memory(PyObject *o, const Table &t, int64_t *bytes) {
   *bytes = 0;
   if (o == Py_None) return nullptr;
-  if (!THPVariable_Check(o)) fail("workspace", "a tensor");
+  static const char *const what = "a contiguous tensor on the pools' device";
+  if (!THPVariable_Check(o)) fail("workspace", what);
   const at::Tensor &x = THPVariable_Unpack(o);
-  if (!x.is_cuda() || !x.is_contiguous()) fail("workspace", "a contiguous tensor on the pools' device");
+  if (!x.is_cuda() || x.device().index() != t.device || !x.is_contiguous()) fail("workspace", what);
   *bytes = static_cast<int64_t>(x.nbytes());
   return x.data_ptr();
+}
+
+int32_t *status_word(PyObject *o, const Table &t) {
+  static const char *const what = "an int32 on the pools' device";
+  const at::Tensor &x = tensor(o, "status", t, at::kInt, what);
+  if (x.numel() < 1) fail("status", what);
+  return static_cast<int32_t *>(x.data_ptr());
 }
 
 // Host lengths: an int32 array as it is, other sequences copied.
@@ -202,7 +210,7 @@ PyObject *append_rotary(PyObject *, PyObject *const *a, Py_ssize_t n) {
     const Rows k = rows(a[4], "k", t), v = rows(a[5], "v", t);
     if (k.heads != whole(a[1]) || k.dim != whole(a[2])) fail("k", "[tokens, kv_heads, key_dim] of the cache");
     if (v.n != k.n || v.heads != k.heads || v.dim != whole(a[3])) fail("v", "[tokens, kv_heads, value_dim] of the cache, k's tokens");
-    int64_t count = 0, bytes = 0;
+    int64_t count = 0;
     const int64_t *slots = list<int64_t>(a[6], "slots", t, at::kLong, &count);
     if (count != k.n) fail("slots", "a slot per token");
     static const char *const of_positions = "int32 [tokens] or [axes, tokens] on the pools' device";
@@ -212,7 +220,7 @@ PyObject *append_rotary(PyObject *, PyObject *const *a, Py_ssize_t n) {
     static const char *const of_table = "contiguous float32 [positions, rot_dim] on the pools' device";
     const at::Tensor &turns = tensor(a[8], "cos_sin", t, at::kFloat, of_table);
     if (turns.dim() != 2 || !turns.is_contiguous() || axes > INT32_MAX || turns.size(1) > INT32_MAX) fail("cos_sin", of_table);
-    int32_t *status = static_cast<int32_t *>(memory(a[9], &bytes));
+    int32_t *status = status_word(a[9], t);
     Rows q = {nullptr, 0, 0, 0, k.dim}, q_out = q;
     if (a[10] != Py_None) {
       q = rows(a[10], "q", t);
@@ -239,7 +247,7 @@ PyObject *attend_window(PyObject *, PyObject *const *a, Py_ssize_t n) {
   return guarded(a, n, 15, [&](const Table &t) {
     const Rows q = rows(a[2], "q", t), out = rows(a[10], "out", t);
     if (!q.same_shape(out)) fail("out", "q's shape");
-    int64_t requests = 0, bytes = 0, word = 0;
+    int64_t requests = 0, bytes = 0;
     const int32_t *kv_lens = list<int32_t>(a[5], "kv_lens", t, at::kInt, &requests);
     const PageRows pages = page_rows(a[4], "page_table", t, requests);
     const Lengths q_lens(a[3]);
@@ -248,8 +256,8 @@ PyObject *attend_window(PyObject *, PyObject *const *a, Py_ssize_t n) {
     if (max_kv > pages.pages * t.page_size) return CPKV_ERR_CAPACITY;
     const double scale = PyFloat_AsDouble(a[9]);
     float *lse = lse_of(a[11], t, q);
-    void *workspace = memory(a[12], &bytes);
-    int32_t *status = static_cast<int32_t *>(memory(a[13], &word));
+    void *workspace = memory(a[12], t, &bytes);
+    int32_t *status = status_word(a[13], t);
     if (requests > INT32_MAX || q.heads > INT32_MAX || q.dim > INT32_MAX) return CPKV_ERR_LIMIT;
     return cpkv_attend_window(static_cast<int>(requests), t.page_size, t.cp_size, t.code, static_cast<int>(q.heads),
                               small(a[1], "kv_heads"), static_cast<int>(q.dim), t.row_bytes, t.key_offset, t.value_offset,
@@ -264,7 +272,7 @@ PyObject *attend_shared(PyObject *, PyObject *const *a, Py_ssize_t n) {
   return guarded(a, n, 15, [&](const Table &t) {
     const Rows q = rows(a[2], "q", t), out = rows(a[10], "out", t);
     if (!q.same_shape(out)) fail("out", "q's shape");
-    int64_t requests = 0, prefix_pages = 0, bytes = 0, word = 0;
+    int64_t requests = 0, prefix_pages = 0, bytes = 0;
     const int32_t *suffix_lens = list<int32_t>(a[7], "suffix_lens", t, at::kInt, &requests);
     const int32_t *prefix = list<int32_t>(a[5], "prefix_pages", t, at::kInt, &prefix_pages);
     const PageRows pages = page_rows(a[6], "page_table", t, requests);
@@ -274,8 +282,8 @@ PyObject *attend_shared(PyObject *, PyObject *const *a, Py_ssize_t n) {
     if (max_suffix > pages.pages * t.page_size) return CPKV_ERR_CAPACITY;
     const double scale = PyFloat_AsDouble(a[9]);
     float *lse = lse_of(a[11], t, q);
-    void *workspace = memory(a[12], &bytes);
-    int32_t *status = static_cast<int32_t *>(memory(a[13], &word));
+    void *workspace = memory(a[12], t, &bytes);
+    int32_t *status = status_word(a[13], t);
     if (requests > INT32_MAX || q.heads > INT32_MAX || q.dim > INT32_MAX || sizes.count() > INT32_MAX) return CPKV_ERR_LIMIT;
     return cpkv_attend_shared(static_cast<int>(requests), static_cast<int>(sizes.count()), t.page_size, t.cp_size, t.code,
                               static_cast<int>(q.heads), small(a[1], "kv_heads"), static_cast<int>(q.dim), t.row_bytes,

@@ -95,3 +95,35 @@ def test_calls_run_with_the_pools_device_current():
     cache.table._table.device = 0
     calls()
     assert int(cache.d_status) == 0
+
+
+def test_status_words_and_workspaces_that_calls_refuse():
+    """A status word that is no int32 or is empty, and memory of the host: refused before anything is launched."""
+    cache = PagedCache([torch.zeros(4, 16, 256, dtype=BF16, device="cuda")], page_size=16, kv_heads=2, key_dim=64)
+    k = torch.zeros(1, 2, 64, dtype=BF16, device="cuda")
+    one, turns, pages = torch.ones(1, dtype=torch.int32, device="cuda"), torch.ones(8, 64, device="cuda"), torch.ones(1, 1, dtype=torch.int32, device="cuda")
+    out, room = torch.empty_like(k), torch.empty(1 << 20, dtype=torch.uint8, device="cuda")
+
+    def append(d_status, workspace):
+        cpkv.cpkv_append_rotary(k, k, 16 * one.long(), one, turns, table=cache.table, d_status=d_status)
+
+    def window(d_status, workspace):
+        cpkv.cpkv_attend_window(k, None, pages, one, table=cache.table, kv_heads=2, max_kv_len=16, window=0, sinks=0, scale=0.1, out=out,
+                                lse=None, workspace=workspace, d_status=d_status)
+
+    def shared(d_status, workspace):
+        cpkv.cpkv_attend_shared(k, [1], [0], one[:0], pages, one, table=cache.table, kv_heads=2, max_suffix_len=16, scale=0.1, out=out, lse=None,
+                                workspace=workspace, d_status=d_status)
+
+    word = torch.zeros(1, dtype=torch.int32, device="cuda")
+    for call in (append, window, shared):
+        call(word, room)
+        for bad in (word.to(torch.int8), word.float(), word.long(), word[:0], word.cpu(), None):
+            with pytest.raises(cpkv.CpkvError):
+                call(bad, room)
+    for call in (window, shared):
+        for bad in (room.cpu(), room[::2]):
+            with pytest.raises(cpkv.CpkvError):
+                call(word, bad)
+    torch.cuda.synchronize()
+    assert int(word) == 0
