@@ -191,8 +191,13 @@ class PagedCache:
     one "pool" is a composed dense buffer, whose page 0 is an ordinary page.
     The handle keeps the pools' addresses, a status word (``d_status``) and,
     per stream, a workspace that grows as calls need it.  Calls are
-    asynchronous; a first call of a size outside a CUDA graph's capture makes
-    the workspace that captured calls then use."""
+    asynchronous.  A call captured into a CUDA graph takes a workspace from
+    the memory that ``torch.cuda.graph`` gives the capture, which belongs to
+    the graph, so graphs may be replayed beside each other and beside other
+    calls.  A ``workspace`` that the caller gives (a uint8 CUDA tensor of at
+    least ``cpkv_attend_*_workspace_bytes``) is used as it is, for captures
+    made by other means and for memory shared between handles; calls that
+    overlap on the GPU must not share one."""
 
     def __init__(self, pools, *, page_size: int, kv_heads: int, key_dim: int, value_dim: int | None = None,
                  key_offset: int = 0, value_offset: int | None = None, dense: bool = False):
@@ -204,11 +209,12 @@ class PagedCache:
         self.device = self.table.device
         self.d_status = torch.zeros(1, dtype=torch.int32, device=self.device)
         self._workspaces = {}  # by stream
-        self._outgrown = []  # a captured graph may still use them
         self._scale = self.key_dim ** -0.5
         self._native = cpkv.serving()
         # the current stream's handle: torch's own accessor where it has one (a twentieth of current_stream())
         self._current = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        self._current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+        self._current_captures = getattr(torch._C, "_cuda_isCurrentStreamCapturing", torch.cuda.is_current_stream_capturing)
 
     def _stream(self, stream) -> int:
         if stream is not None:
@@ -217,16 +223,32 @@ class PagedCache:
             return self._current(self.device.index)
         return torch.cuda.current_stream(self.device).cuda_stream
 
-    def _grow(self, fn: str, rc: int, stream: int, size):
-        """A larger workspace where the call wants one; its error otherwise."""
-        workspace = self._workspaces.get(stream)
-        with torch.cuda.device(self.device):  # the size goes by its SMs
-            need = size() if rc == cpkv.CPKV_ERR_CAPACITY else 0
-        if need <= (0 if workspace is None else workspace.numel()):
-            cpkv._check(fn, rc)
-        if workspace is not None:
-            self._outgrown.append(workspace)
-        self._workspaces[stream] = self._empty((need + need // 4,), torch.uint8, stream)
+    def _capturing(self, stream: int, is_current: bool) -> bool:
+        """Whether calls on the stream go into a CUDA graph."""
+        if is_current and self._current_device() == self.device.index:
+            return self._current_captures()
+        with torch.cuda.stream(torch.cuda.ExternalStream(stream, device=self.device)):
+            return self._current_captures()
+
+    def _attend(self, fn: str, args: tuple, stream: int, is_current: bool, workspace, size):
+        """Runs a call of the library, with a larger workspace where it wants one: ``size(args)`` bytes."""
+        native = getattr(self._native, fn)
+        mine, captured = workspace is None, False
+        if mine:
+            captured = self._capturing(stream, is_current)
+            if not captured:
+                workspace = self._workspaces.get(stream)
+        rc = native(*args, workspace, self.d_status, stream)
+        if rc == cpkv.CPKV_ERR_CAPACITY and mine:
+            with torch.cuda.device(self.device):  # the size goes by its SMs
+                need = size(*args)
+            if need > (0 if workspace is None else workspace.numel()):
+                workspace = self._empty((need if captured else need + need // 4,), torch.uint8, stream)
+                if not captured:
+                    self._workspaces[stream] = workspace
+                rc = native(*args, workspace, self.d_status, stream)
+        if rc:
+            cpkv._check("cpkv_" + fn, rc)
 
     def _empty(self, shape, dtype, stream: int):
         """Memory of the stream that the call runs on."""
@@ -258,39 +280,38 @@ class PagedCache:
         return self._empty(q.shape, q.dtype, stream) if out is None else out
 
     def attend_window(self, q, q_lens, page_table, kv_lens, *, max_kv_len: int, window: int = 0, sinks: int = 0,
-                      scale: float | None = None, out=None, lse=None, stream=None):
+                      scale: float | None = None, out=None, lse=None, workspace=None, stream=None):
         """Causal attention of the newest ``q_lens[b]`` tokens of each request
         (None: one each) over its ``kv_lens[b]`` rows, those within ``window``
         and the first ``sinks``.  Returns ``out``; ``lse`` (float32 [tokens,
         heads]) is written when given."""
-        stream = self._stream(stream)
+        is_current, stream = stream is None, self._stream(stream)
         out = self._results(q, out, stream)
         if scale is None:
             scale = self._scale
-        while True:
-            rc = self._native.attend_window(self.table.native, self.kv_heads, q, q_lens, page_table, kv_lens, max_kv_len,
-                                            window, sinks, scale, out, lse, self._workspaces.get(stream), self.d_status,
-                                            stream)
-            if not rc:
-                return out
-            self._grow("cpkv_attend_window", rc, stream, lambda: cpkv.cpkv_attend_window_workspace_bytes(
-                kv_lens.shape[0], q.shape[1], self.kv_heads, self.key_dim, q_lens, max_kv_len, window, sinks))
+        self._attend("attend_window", (self.table.native, self.kv_heads, q, q_lens, page_table, kv_lens, max_kv_len, window, sinks,
+                                       scale, out, lse), stream, is_current, workspace, _window_bytes)
+        return out
 
     def attend_shared(self, q, group_sizes, prefix_lens, prefix_pages, page_table, suffix_lens, *,
-                      max_suffix_len: int, scale: float | None = None, out=None, lse=None, stream=None):
+                      max_suffix_len: int, scale: float | None = None, out=None, lse=None, workspace=None, stream=None):
         """A decode step of requests in consecutive groups: ``q`` [requests,
         heads, dim] over each group's shared prefix (``prefix_pages``, CSR by
         group) and each request's own ``suffix_lens[b]`` rows.  Returns
         ``out``; ``lse`` as in ``attend_window``."""
-        stream = self._stream(stream)
+        is_current, stream = stream is None, self._stream(stream)
         out = self._results(q, out, stream)
         if scale is None:
             scale = self._scale
-        while True:
-            rc = self._native.attend_shared(self.table.native, self.kv_heads, q, group_sizes, prefix_lens, prefix_pages,
-                                            page_table, suffix_lens, max_suffix_len, scale, out, lse,
-                                            self._workspaces.get(stream), self.d_status, stream)
-            if not rc:
-                return out
-            self._grow("cpkv_attend_shared", rc, stream, lambda: cpkv.cpkv_attend_shared_workspace_bytes(
-                suffix_lens.shape[0], q.shape[1], self.kv_heads, self.key_dim, group_sizes, prefix_lens, max_suffix_len))
+        self._attend("attend_shared", (self.table.native, self.kv_heads, q, group_sizes, prefix_lens, prefix_pages, page_table,
+                                       suffix_lens, max_suffix_len, scale, out, lse), stream, is_current, workspace, _shared_bytes)
+        return out
+
+
+def _window_bytes(table, kv_heads, q, q_lens, page_table, kv_lens, max_kv_len, window, sinks, *rest) -> int:
+    return cpkv.cpkv_attend_window_workspace_bytes(kv_lens.shape[0], q.shape[1], kv_heads, q.shape[2], q_lens, max_kv_len, window, sinks)
+
+
+def _shared_bytes(table, kv_heads, q, group_sizes, prefix_lens, prefix_pages, page_table, suffix_lens, max_suffix_len, *rest) -> int:
+    return cpkv.cpkv_attend_shared_workspace_bytes(suffix_lens.shape[0], q.shape[1], kv_heads, q.shape[2], group_sizes, prefix_lens,
+                                                   max_suffix_len)

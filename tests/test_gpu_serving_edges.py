@@ -127,3 +127,106 @@ def test_status_words_and_workspaces_that_calls_refuse():
                 call(word, bad)
     torch.cuda.synchronize()
     assert int(word) == 0
+
+
+class Recorder:
+    """The compiled calls of a handle, with the workspaces that they were given."""
+
+    def __init__(self, native):
+        self.native, self.spans = native, []
+
+    def __getattr__(self, name):
+        def call(*args):
+            rc = getattr(self.native, name)(*args)
+            if rc == 0 and args[12] is not None:
+                self.spans.append((args[12].data_ptr(), args[12].data_ptr() + args[12].numel()))
+            return rc
+
+        return call
+
+
+def decode_batch(seed=0):
+    """A decode step whose rows are cut into parts: inputs on the GPU and the wanted result."""
+    hq, hkv, d, ps, kv_lens = 8, 2, 128, 16, [3000, 1700, 2500]
+    rng = np.random.default_rng(seed)
+    lists, n_pages = page_tables(rng, kv_lens, ps)
+    pools = model.Pools(rng, n_pages, ps, 2, 2 * hkv * d, BF16)
+    cache = PagedCache(pools.cuda(), page_size=ps, kv_heads=hkv, key_dim=d)
+    q = [queries(rng, 3, hq, d, BF16) for _ in range(3)]
+    want = [model.window(x, [1] * 3, lists, kv_lens, pools, kv_heads=hkv, dim=d, window=0, sinks=0, scale=d**-0.5) for x in q]
+    table, lens = torch.from_numpy(lists).cuda(), torch.tensor(kv_lens, dtype=torch.int32).cuda()
+
+    def step(k_q, out, lse, **more):
+        return cache.attend_window(k_q, None, table, lens, max_kv_len=3000, out=out, lse=lse, **more)
+
+    d_q = [x.cuda() for x in q]
+    outs = [(torch.zeros_like(x), torch.zeros(3, hq, device="cuda")) for x in d_q]
+    return cache, step, d_q, outs, want
+
+
+def test_captured_calls_have_workspaces_of_their_own():
+    """Two graphs captured on one stream, and an eager call there, take memory apart from each other."""
+    cache, step, q, outs, want = decode_batch()
+    cache._native = recorder = Recorder(cache._native)
+    stream = torch.cuda.Stream()
+    graphs = [torch.cuda.CUDAGraph() for _ in range(2)]
+    with torch.cuda.stream(stream):
+        step(q[2], *outs[2])
+    for graph, x, out in zip(graphs, q, outs):
+        with torch.cuda.graph(graph, stream=stream):
+            step(x, *out)
+    with torch.cuda.stream(stream):
+        step(q[2], *outs[2])
+    torch.cuda.synchronize()
+    eager, first, second, again = recorder.spans
+    assert again == eager
+    for a, b in ((eager, first), (eager, second), (first, second)):
+        assert a[1] <= b[0] or b[1] <= a[0]
+    for graph in graphs:
+        graph.replay()
+    torch.cuda.synchronize()
+    for out, w in zip(outs, want):
+        model.check(*out, w, BF16)
+    assert int(cache.d_status) == 0
+
+
+def test_replays_and_eager_calls_side_by_side():
+    cache, step, q, outs, want = decode_batch(1)
+    capture, one, two = (torch.cuda.Stream() for _ in range(3))
+    graphs = [torch.cuda.CUDAGraph() for _ in range(2)]
+    for graph, x, out in zip(graphs, q, outs):
+        with torch.cuda.graph(graph, stream=capture):
+            for _ in range(20):
+                step(x, *out)
+    torch.cuda.synchronize()
+    for _ in range(30):
+        for side, graph in ((one, graphs[0]), (two, graphs[1])):
+            with torch.cuda.stream(side):
+                graph.replay()
+        with torch.cuda.stream(capture):
+            for _ in range(10):
+                step(q[2], *outs[2])
+    torch.cuda.synchronize()
+    for out, w in zip(outs, want):
+        model.check(*out, w, BF16)
+
+
+def test_a_workspace_of_the_caller():
+    """The caller's memory is used as it is, and refused when it is too small."""
+    cache, step, q, outs, want = decode_batch(2)
+    need = cpkv.cpkv_attend_window_workspace_bytes(3, 8, 2, 128, None, 3000)
+    cache._native = recorder = Recorder(cache._native)
+    mine = torch.empty(need, dtype=torch.uint8, device="cuda")
+    step(q[0], *outs[0], workspace=mine)
+    assert recorder.spans == [(mine.data_ptr(), mine.data_ptr() + need)]
+    model.check(*outs[0], want[0], BF16)
+    with pytest.raises(cpkv.CpkvError):
+        step(q[0], *outs[0], workspace=mine[:-1])
+    stream = torch.cuda.Stream()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=stream):
+        step(q[1], *outs[1], workspace=mine)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert recorder.spans[1] == recorder.spans[0]
+    model.check(*outs[1], want[1], BF16)
