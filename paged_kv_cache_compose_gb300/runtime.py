@@ -189,15 +189,18 @@ class PagedCache:
     ``key_offset`` and as many value vectors of ``value_dim`` at
     ``value_offset`` (elements; by default keys, then values).  ``dense``: the
     one "pool" is a composed dense buffer, whose page 0 is an ordinary page.
-    The handle keeps the pools' addresses, a status word (``d_status``) and,
-    per stream, a workspace that grows as calls need it.  Calls are
-    asynchronous.  A call captured into a CUDA graph takes a workspace from
-    the memory that ``torch.cuda.graph`` gives the capture, which belongs to
-    the graph, so graphs may be replayed beside each other and beside other
-    calls.  A ``workspace`` that the caller gives (a uint8 CUDA tensor of at
-    least ``cpkv_attend_*_workspace_bytes``) is used as it is, for captures
-    made by other means and for memory shared between handles; calls that
-    overlap on the GPU must not share one."""
+    The handle keeps the pools' addresses and a status word (``d_status``).
+    Handles share one workspace per stream, which grows as calls need it: calls
+    on a stream run one after the other, and a model has a handle per layer.
+    Calls are asynchronous.  A call captured into a CUDA graph takes a
+    workspace from the memory that ``torch.cuda.graph`` gives the capture,
+    which belongs to the graph, so graphs may be replayed beside each other and
+    beside other calls.  A ``workspace`` that the caller gives (a uint8 CUDA
+    tensor of at least ``cpkv_attend_*_workspace_bytes``) is used as it is, for
+    captures made by other means; calls that overlap on the GPU must not share
+    one."""
+
+    _workspaces = {}  # of all handles, by device and stream
 
     def __init__(self, pools, *, page_size: int, kv_heads: int, key_dim: int, value_dim: int | None = None,
                  key_offset: int = 0, value_offset: int | None = None, dense: bool = False):
@@ -208,7 +211,6 @@ class PagedCache:
         self.table = cpkv.PoolTable(pools, page_size, 2 * key_offset, 2 * value_offset, dense)
         self.device = self.table.device
         self.d_status = torch.zeros(1, dtype=torch.int32, device=self.device)
-        self._workspaces = {}  # by stream
         self._scale = self.key_dim ** -0.5
         self._native = cpkv.serving()
         # the current stream's handle: torch's own accessor where it has one (a twentieth of current_stream())
@@ -237,7 +239,7 @@ class PagedCache:
         if mine:
             captured = self._capturing(stream, is_current)
             if not captured:
-                workspace = self._workspaces.get(stream)
+                workspace = self._workspaces.get((self.device.index, stream))
         rc = native(*args, workspace, self.d_status, stream)
         if rc == cpkv.CPKV_ERR_CAPACITY and mine:
             with torch.cuda.device(self.device):  # the size goes by its SMs
@@ -245,7 +247,7 @@ class PagedCache:
             if need > (0 if workspace is None else workspace.numel()):
                 workspace = self._empty((need if captured else need + need // 4,), torch.uint8, stream)
                 if not captured:
-                    self._workspaces[stream] = workspace
+                    self._workspaces[self.device.index, stream] = workspace
                 rc = native(*args, workspace, self.d_status, stream)
         if rc:
             cpkv._check("cpkv_" + fn, rc)

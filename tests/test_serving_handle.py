@@ -32,7 +32,7 @@ def handle(monkeypatch):
     cache = object.__new__(PagedCache)
     cache.kv_heads = cache.key_dim = cache.value_dim = 64
     cache.table, cache.device, cache.d_status, cache._scale = types.SimpleNamespace(native=0), torch.device("cuda", 0), None, 1.0
-    cache._workspaces = {}
+    monkeypatch.setattr(PagedCache, "_workspaces", {})
     cache._stream = lambda stream: 7
     cache._capturing = lambda stream, is_current: False
     cache._empty = lambda shape, dtype, stream: torch.empty(shape, dtype=dtype)
@@ -57,7 +57,7 @@ def test_the_workspace_grows_once_and_stays(handle):
 def test_a_workspace_that_another_thread_grew_meanwhile(handle):
     """Another thread replaces the workspace between this call's failure and its look at the size: the call still runs."""
     def other():
-        handle._workspaces[7] = torch.empty(2 * NEED, dtype=torch.uint8)
+        handle._workspaces[0, 7] = torch.empty(2 * NEED, dtype=torch.uint8)
 
     handle._native = Native(other)
     attend(handle)
@@ -86,3 +86,13 @@ def test_a_workspace_of_the_caller_is_not_replaced(handle):
     with pytest.raises(cpkv.CpkvError):
         attend(handle, workspace=torch.empty(NEED - 1, dtype=torch.uint8))
     assert len(handle._native.rooms) == 1 and not handle._workspaces
+
+
+def test_handles_share_the_workspace_of_a_stream(handle):
+    """A model's layers, one handle each, keep one workspace and not one each."""
+    other = object.__new__(PagedCache)
+    other.__dict__.update(handle.__dict__)
+    handle._native, other._native = Native(), Native()
+    attend(handle)
+    attend(other)
+    assert other._native.rooms == [handle._native.rooms[-1]]
