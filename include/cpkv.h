@@ -688,6 +688,23 @@ int cpkv_attend_shared_workspace_bytes(int B, int n_groups, int q_heads, int kv_
                                        const int32_t *h_group_sizes, const int32_t *h_prefix_lens,
                                        int64_t max_suffix_len, int64_t *h_bytes);
 
+/*
+ * cpkv_selftest_attend_timeout — diagnostics: runs the attention's kernel for many query
+ * rows on one request with waits that may take `wait_ns` only, whatever progress is
+ * made, so that blocks give up in the middle of their work: copies and products in
+ * flight are waited for, CPKV_STATUS_TIMEOUT is raised, the results are undefined, and
+ * the context stays usable.  (In use a wait may take two seconds in which its block
+ * does not get on.)
+ *   head_dim       64 or 128; one bf16 query head, one key/value head
+ *   n_tokens       query tokens, more than 16: d_q and d_out are [n_tokens][head_dim]
+ *   d_rows         [n_pages][64][2 * head_dim]: keys, values; d_page_table int32 [n_pages]
+ *                  and the number of keys *d_kv_len on the device
+ * Errors: ARG, LIMIT, CUDA.
+ */
+int cpkv_selftest_attend_timeout(int head_dim, int n_tokens, int n_pages, const void *d_rows,
+                                 const int32_t *d_page_table, const int32_t *d_kv_len, const void *d_q, void *d_out,
+                                 int64_t wait_ns, int32_t *d_status, cpkv_stream_t stream);
+
 /* Human-readable name of a return code. */
 const char *cpkv_error_string(int code);
 

@@ -66,7 +66,7 @@ EXPORTED = (
     "cpkv_compose_fused", "cpkv_compose_fused_planes", "cpkv_selftest_ring_timeout", "cpkv_ragged_plan_sizes",
     "cpkv_ragged_plan_build", "cpkv_append_rotary", "cpkv_attend_window",
     "cpkv_attend_window_workspace_bytes", "cpkv_attend_shared", "cpkv_attend_shared_workspace_bytes",
-    "cpkv_error_string", "cpkv_version",
+    "cpkv_selftest_attend_timeout", "cpkv_error_string", "cpkv_version",
 )
 
 
@@ -114,6 +114,7 @@ def _declare(lib):
     lib.cpkv_attend_shared.argtypes = [_I] * 8 + [_L] * 3 + [_P, _P, _L, _P, _P, _P, _L, _P, _L, _P, _P, _L, _F, _P, _L,
                                                              _P, _P, _L, _I, _P, _P]
     lib.cpkv_attend_shared_workspace_bytes.argtypes = [_I] * 5 + [_P, _P, _L, _P]
+    lib.cpkv_selftest_attend_timeout.argtypes = [_I] * 3 + [_P] * 5 + [_L, _P, _P]
     for name in EXPORTED:
         getattr(lib, name).restype = _I
     lib.cpkv_error_string.argtypes = [_I]
@@ -573,3 +574,11 @@ def cpkv_attend_shared(q, group_sizes, prefix_lens, prefix_pages, page_table, d_
     _check("cpkv_attend_shared", serving().attend_shared(
         table.native, kv_heads, q, group_sizes, prefix_lens, prefix_pages, page_table, d_suffix_lens, max_suffix_len,
         scale, out, lse, workspace, d_status, _handle(stream, table)))
+
+
+def cpkv_selftest_attend_timeout(rows, page_table, d_kv_len, q, out, wait_ns, d_status, stream=None):
+    """Diagnostics: the attention of ``q`` [tokens, head_dim] over ``rows`` [pages, 64, 2 * head_dim] with waits that run
+    out after ``wait_ns`` (see include/cpkv.h)."""
+    _check("cpkv_selftest_attend_timeout", load().cpkv_selftest_attend_timeout(
+        q.shape[1], q.shape[0], rows.shape[0], _dp(rows), _dp(page_table), _dp(d_kv_len), _dp(q), _dp(out), wait_ns, _dp(d_status),
+        _stream(stream)))

@@ -345,9 +345,9 @@ void fill_tiles(TileParams<S> *p, const S &seqs, int ragged, const PagedPools &p
     p->cu_tiles[s + 1] = p->cu_tiles[s] + (int)ceil_div((int64_t)(seqs.cu_q[s + 1] - seqs.cu_q[s]) * group, kTileRows);
 }
 
-template <typename T, int D, typename S>
+template <typename T, int D, bool kTest = false, typename S>
 int tile_pass(const TileParams<S> &p, const TileBounds &b, cudaStream_t stream) {
-  auto kernel = attend_tile_kernel<T, D, S>;
+  auto kernel = attend_tile_kernel<T, D, S, kTest>;
   const int rc = ensure_dynamic_smem((const void *)kernel, TileShape<D>::kSmem);
   if (rc != CPKV_OK) return rc;
   const int64_t grid = b.blocks(p.io.kv_heads);
@@ -589,4 +589,38 @@ extern "C" int cpkv_attend_shared(int B, int n_groups, int page_size, int cp_siz
   };
   if (n_groups <= kFewSeqs) return go(std::integral_constant<int, kFewSeqs>());
   return go(std::integral_constant<int, CPKV_MAX_BATCH>());
+}
+
+// The tile kernel over one request with waits that run out at once or after `wait_ns`.
+extern "C" int cpkv_selftest_attend_timeout(int head_dim, int n_tokens, int n_pages, const void *d_rows,
+                                            const int32_t *d_page_table, const int32_t *d_kv_len, const void *d_q, void *d_out,
+                                            int64_t wait_ns, int32_t *d_status, cpkv_stream_t stream) {
+  constexpr int kPage = 64;
+  const HeadArgs heads = {CPKV_BF16, 1, 1, head_dim};
+  int rc = check_heads(heads);
+  if (rc != CPKV_OK) return rc;
+  if (n_tokens <= kSplitRows || n_pages < 1 || n_pages > (1 << 20) || wait_ns < 0) return CPKV_ERR_ARG;
+  if (d_rows == nullptr || d_page_table == nullptr || d_kv_len == nullptr || d_status == nullptr) return CPKV_ERR_ARG;
+  const int64_t row_bytes = 4 * head_dim, cap = n_pages;
+  PagedPools pools = {};
+  rc = paged_pools(&pools, kPage, 1, row_bytes, &d_rows, &cap, CPKV_DENSE_PAGES);
+  if (rc != CPKV_OK) return rc;
+  AttendIo io = {};
+  rc = fill_io(&io, heads, d_q, head_dim, d_out, head_dim, nullptr, 0.125f, 0, 2 * head_dim);
+  if (rc != CPKV_OK) return rc;
+  Seqs<kFewSeqs> s = {};
+  s.kv_lens = d_kv_len;
+  s.table = d_page_table;
+  s.stride = n_pages;
+  s.status = d_status;
+  s.count = 1;
+  s.kv_cap = n_pages * kPage;
+  s.cu_q[1] = n_tokens;
+  TileBounds bounds;
+  bounds.add(n_tokens, s.kv_cap, 1, 0, 0);  // never finished: one part an item, however long
+  TileParams<Seqs<kFewSeqs>> p = {};
+  fill_tiles(&p, s, 1, pools, io, bounds, nullptr, true);
+  p.test_wait_ns = (uint64_t)wait_ns;
+  return head_dim == 128 ? tile_pass<__nv_bfloat16, 128, true>(p, bounds, (cudaStream_t)stream)
+                         : tile_pass<__nv_bfloat16, 64, true>(p, bounds, (cudaStream_t)stream);
 }

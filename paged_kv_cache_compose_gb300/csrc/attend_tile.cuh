@@ -54,8 +54,10 @@ constexpr int kItemSlots = 4;   // items known at a time: of small ones, some ar
 constexpr int kClaimAhead = 12;  // key tiles before an item's last load at which the next item is claimed
 constexpr int kTileMaps = 8;  // most pools that TMA maps travel for
 constexpr float kRescaleAt = 8.f;
-constexpr uint64_t kTileWaitNs = 2000000000ull;
-constexpr uint32_t kTileParkNs = 20000;
+constexpr uint64_t kTileWaitNs = 2000000000ull;  // and, for each key tile of an item,
+constexpr uint64_t kTileStepNs = 50000;          // of which one takes about 1.4 us
+constexpr uint32_t kTileParkNs = 2000;
+constexpr uint64_t kTileDrainNs = 50000000ull;  // for copies and products in flight after giving up: they take microseconds
 
 // Rows of a tile pass's parts: 256 for each [item][split], an item being (row tile
 // of the ragged sequences, key/value head), then those of the sequences of one
@@ -80,6 +82,7 @@ struct TileParams {
   int wide_out;         // the output's rows start on 32 bytes
   int box_rows;         // rows of a TMA box (32 or 16); 0: no maps
   int cu_tiles[S::kArray + 1];  // row tiles before each ragged sequence
+  uint64_t test_wait_ns;  // limit of the waits in the self-test of giving up
   CUtensorMap maps[kTileMaps];  // pool r as [rows][elements], boxes of box_rows x 64
 };
 
@@ -118,27 +121,47 @@ struct TileBars {
   uint4 claim;
   uint32_t tmem;
   int gave_up;
+  int loaders;        // warps that may issue copies
+  uint64_t deadline;  // of the waits; moves on with the items
+  uint32_t issued[4];  // keys and values of tiles, in turn, that a loading warp has issued
 };
 
 constexpr int kItemReaders = 15;  // warps that read an item: softmax, loads, products, queries
 
 __device__ const uint4 zero_row[16] = {};  // a key or value vector of zeros
 
-// Bounded wait of a thread.  After kTileWaitNs the block gives up: from then on no
-// wait of it takes longer than a parking, its warps run through what they have begun
-// on whatever is there, end, and the status word says that the results are undefined.
+// Bounded wait of a thread: whether the phase came.  When it did not before the
+// deadline, or another wait of the block ran out, the block gives up: loads and claims
+// end at once (kStops), the other roles run through what they have begun on whatever is
+// there once no copy is issued any more (a stage that they hand back unseen is not filled
+// again), what is in flight is waited for, and the status word says that the results are
+// undefined.
 // The usual way through is one instruction and one branch: the products' warp does
-// nine waits per 128 keys, and its own pace is close to the tensor core's.
-CPKV_DEV void tile_wait(TileBars *b, uint64_t *bar, uint32_t parity, int32_t *status) {
-  if (mbar_try_wait_for(bar, parity, kTileParkNs)) return;
-  const uint64_t t0 = global_timer_ns();
-  while (!mbar_try_wait_for(bar, parity, kTileParkNs)) {
-    if (*(volatile int *)&b->gave_up) return;
-    if (global_timer_ns() - t0 > kTileWaitNs) {
+// nine waits per 128 keys, and its own pace is close to the tensor core's.  A branch on
+// the result in its loop cost 1.6% of a prefill, and so did a deadline that a loading
+// warp moves on every 64 tiles: the warp that finds the items keeps it.
+template <bool kTest, bool kStops>
+CPKV_DEV bool tile_wait(TileBars *b, uint64_t *bar, uint32_t parity, int32_t *status) {
+  constexpr uint32_t kPark = kTest ? 0 : kTileParkNs;
+  if (mbar_try_wait_for(bar, parity, kPark)) return true;
+  while (!mbar_try_wait_for(bar, parity, kPark)) {
+    if (!*(volatile int *)&b->gave_up) {
+      if (global_timer_ns() <= *(volatile uint64_t *)&b->deadline) continue;
       *(volatile int *)&b->gave_up = 1;
       raise_status(status, CPKV_STATUS_TIMEOUT);
-      return;
     }
+    if (kStops) return false;
+    const uint64_t t0 = global_timer_ns();
+    while (*(volatile int *)&b->loaders > 0 && global_timer_ns() - t0 < kTileDrainNs) {
+    }
+    return false;
+  }
+  return true;
+}
+
+// Waits for a phase that something in flight completes, no longer than kTileDrainNs from t0.
+CPKV_DEV void tile_drain(uint64_t *bar, uint32_t parity, uint64_t t0) {
+  while (!mbar_try_wait(bar, parity & 1) && global_timer_ns() - t0 < kTileDrainNs) {
   }
 }
 
@@ -260,7 +283,7 @@ __device__ __noinline__ void mend_row(const TileParams<S> &p, const TileItem &it
   }
 }
 
-template <typename T, int D, typename S>
+template <typename T, int D, typename S, bool kTest = false>
 __global__ void __launch_bounds__(kTileThreads, 1) attend_tile_kernel(const __grid_constant__ TileParams<S> p) {
   using Shape = TileShape<D>;
   constexpr int kStages = Shape::kStages;
@@ -300,6 +323,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) attend_tile_kernel(const __gr
     mbar_init(&bars.stream_done, 128);
     mbar_init(&bars.stream_free, 128);
     bars.gave_up = 0;
+    bars.loaders = 4;
+    bars.deadline = ~uint64_t(0);  // until the first item is known
     fence_barrier_init();
   }
   if (warp == 12) tmem_alloc(&bars.tmem, 512);
@@ -307,13 +332,14 @@ __global__ void __launch_bounds__(kTileThreads, 1) attend_tile_kernel(const __gr
   __syncthreads();
   tmem_fence_after();
   const uint32_t tmem = bars.tmem;
-  auto wait = [&](uint64_t *bar, uint32_t parity) { tile_wait(&bars, bar, parity & 1, status); };
+  auto wait = [&](uint64_t *bar, uint32_t parity) { (void)tile_wait<kTest, false>(&bars, bar, parity & 1, status); };
+  auto wait_or_stop = [&](uint64_t *bar, uint32_t parity) { return tile_wait<kTest, true>(&bars, bar, parity & 1, status); };
+  auto all = [](bool ok) { return __all_sync(0xffffffffu, ok) != 0; };
   // Item number k of this block: whether there is one.  The warp reads it and hands
   // its place back.
   auto item_there = [&](int k) {
-    wait(&bars.item_full[k % kItemSlots], k / kItemSlots);
-    const bool there = items[k % kItemSlots].more && !*(volatile int *)&bars.gave_up;
-    return __all_sync(0xffffffffu, there) != 0;
+    wait_or_stop(&bars.item_full[k % kItemSlots], k / kItemSlots);
+    return all(items[k % kItemSlots].more && !*(volatile int *)&bars.gave_up);
   };
   auto item_read = [&](int k) {
     __syncwarp();
@@ -549,8 +575,9 @@ __global__ void __launch_bounds__(kTileThreads, 1) attend_tile_kernel(const __gr
     // this lane's box of the warp's: block of 64 elements, first key
     const int boxes = p.box_rows ? 32 / p.box_rows * (D / 64) : 0;
     const int box_block = lane % (D / 64), box_key = lane / (D / 64) * p.box_rows;
-    uint32_t loaded = 0;  // key tiles
-    for (int k = 0; item_there(k); ++k) {
+    bool ok = true;
+    uint32_t operands = 0;
+    for (int k = 0; ok && item_there(k); ++k) {
       const TileItem &item = items[k % kItemSlots];
       const int n = item.n, j0 = item.j0, n_sink = item.keys.n_sink, first_tile = item.keys.first_tile;
       const int lo = item.there.lo, hi = item.there.hi, sink_end = item.there.sink_end;
@@ -590,14 +617,16 @@ __global__ void __launch_bounds__(kTileThreads, 1) attend_tile_kernel(const __gr
           __syncwarp();
         }
         if (it + 1 < n) look_up(j0 + it + 1);
+        const uint32_t loaded = operands / 2;  // key tiles
         const int stage = loaded % kStages;
         const bool reuse = loaded >= kStages;
         const uint32_t freed = (loaded / kStages - 1) & 1;
 #pragma unroll 1
         for (int which = 0; which < 2; ++which) {  // keys, then values
           uint64_t *full = which ? &bars.v_full[stage] : &bars.k_full[stage];
-          if (reuse) wait(which ? &bars.v_empty[stage] : &bars.k_empty[stage], freed);
-          __syncwarp();
+          ok = all(!reuse || wait_or_stop(which ? &bars.v_empty[stage] : &bars.k_empty[stage], freed));
+          if (!ok) break;
+          ++operands;
           char *operand = (which ? v_smem : k_smem) + stage * Shape::kOperand;
           if (by_box) {
             if (lane < boxes) {
@@ -612,19 +641,16 @@ __global__ void __launch_bounds__(kTileThreads, 1) attend_tile_kernel(const __gr
             mbar_arrive_after_copies(full);
           }
         }
-        ++loaded;
+        if (!ok) break;
         if (warp == 8 && lane == 0 && it == (n > kClaimAhead ? n - kClaimAhead : 0)) mbar_arrive(&bars.wanted);
       }
       if (warp == 8 && lane == 0 && n == 0) mbar_arrive(&bars.wanted);
     }
-    cp_async_wait_all();
-    if (*(volatile int *)&bars.gave_up) {  // boxes on their way land before the block ends
-      const uint64_t t0 = global_timer_ns();
-      for (uint32_t at = loaded > kStages ? loaded - kStages : 0; at < loaded; ++at)
-        while ((!mbar_try_wait(&bars.k_full[at % kStages], at / kStages & 1) ||
-                !mbar_try_wait(&bars.v_full[at % kStages], at / kStages & 1)) && global_timer_ns() - t0 < kTileWaitNs) {
-        }
+    if (lane == 0) {
+      bars.issued[lw] = operands;
+      atomicSub(&bars.loaders, 1);
     }
+    cp_async_wait_all();
   } else {
     shrink_registers<kOtherRegisters>();
     const int role = __shfl_sync(0xffffffffu, warp, 0);
@@ -637,6 +663,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) attend_tile_kernel(const __gr
       const uint32_t q_low = operand_low(smem_addr(q_smem), 16), k_low = operand_low(smem_addr(k_smem), 16);
       const uint32_t v_low = operand_low(smem_addr(v_smem), kTileKeys * 128);
       const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+      uint32_t used = 0, queries[2] = {0, 0}, weighed[2] = {0, 0};  // key tiles, query blocks, weight tiles
       // scores of tile t: queries of block q, keys of a stage
       auto scores = [&](int t, int q, int stage) {
         const uint32_t a = q_low + q * (Shape::kOperand >> 4), b = k_low + stage * (Shape::kOperand >> 4);
@@ -663,7 +690,6 @@ __global__ void __launch_bounds__(kTileThreads, 1) attend_tile_kernel(const __gr
         if (elect_one()) mma_commit(bar);
         __syncwarp();
       };
-      uint32_t used = 0, queries[2] = {0, 0}, weighed[2] = {0, 0};  // key tiles, query blocks, weight tiles
       int turn = 0;  // query block of the next item that takes one
       auto keys_in = [&](uint32_t at) {
         wait(&bars.k_full[at % kStages], at / kStages);
@@ -753,30 +779,30 @@ __global__ void __launch_bounds__(kTileThreads, 1) attend_tile_kernel(const __gr
         }
         used += n;
       }
-      if (*(volatile int *)&bars.gave_up) {  // products in flight end before tensor memory is freed
-        commit(&bars.drain);
-        const uint64_t t0 = global_timer_ns();
-        while (!mbar_try_wait(&bars.drain, 0) && global_timer_ns() - t0 < kTileWaitNs) {
-        }
-      }
     } else if (role == 13) {
       // -------------------------------------------------------------- items
       if (lane == 0) {
         int block = (int)blockIdx.x;
         for (int k = 0;; ++k) {
-          if (k >= kItemSlots) wait(&bars.item_empty[k % kItemSlots], k / kItemSlots - 1);
+          if (k >= kItemSlots && !wait_or_stop(&bars.item_empty[k % kItemSlots], k / kItemSlots - 1)) break;
           if (block >= 0) {
             find_item(p, block, &items[k % kItemSlots]);
           } else {
-            items[k % kItemSlots].more = 0;
+            items[k % kItemSlots].more = items[k % kItemSlots].n = 0;
           }
           mbar_arrive(&bars.item_full[k % kItemSlots]);
+          if (!kTest || k == 0)
+            *(volatile uint64_t *)&bars.deadline =
+                global_timer_ns() + (kTest ? p.test_wait_ns : kTileWaitNs + items[k % kItemSlots].n * kTileStepNs);
           if (block < 0) break;
-          wait(&bars.wanted, k);  // the loads of this item near their end
+          if (!wait_or_stop(&bars.wanted, k)) break;  // the loads of this item near their end
           fence_proxy_async_smem();
           claim_block(&bars.claim, &bars.claimed);
-          wait(&bars.claimed, k);
-          block = *(volatile int *)&bars.gave_up ? -1 : claimed_block(&bars.claim);
+          if (!wait_or_stop(&bars.claimed, k)) {  // the answer is on its way: the block stays until it is there
+            tile_drain(&bars.claimed, k, global_timer_ns());
+            break;
+          }
+          block = claimed_block(&bars.claim);
         }
       }
       __syncwarp();
@@ -839,7 +865,22 @@ __global__ void __launch_bounds__(kTileThreads, 1) attend_tile_kernel(const __gr
   tmem_fence_before();
   __syncthreads();
   tmem_fence_after();
-  if (warp == 12) tmem_free(tmem, 512);
+  if (warp == 12) {
+    if (*(volatile int *)&bars.gave_up) {  // what is in flight ends before the block and its tensor memory do
+      if (elect_one()) mma_commit(&bars.drain);
+      __syncwarp();
+      const uint64_t t0 = global_timer_ns();
+      tile_drain(&bars.drain, 0, t0);
+      for (int w = 0; w < 4; ++w) {  // the last use of every stage
+        const uint32_t values = bars.issued[w] / 2, keys = bars.issued[w] - values;
+        for (uint32_t at = keys > kStages ? keys - kStages : 0; at < keys; ++at) tile_drain(&bars.k_full[at % kStages], at / kStages, t0);
+        for (uint32_t at = values > kStages ? values - kStages : 0; at < values; ++at)
+          tile_drain(&bars.v_full[at % kStages], at / kStages, t0);
+      }
+      __syncwarp();
+    }
+    tmem_free(tmem, 512);
+  }
 }
 
 }  // namespace cpkv

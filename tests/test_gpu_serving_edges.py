@@ -230,3 +230,27 @@ def test_a_workspace_of_the_caller():
     torch.cuda.synchronize()
     assert recorder.spans[1] == recorder.spans[0]
     model.check(*outs[1], want[1], BF16)
+
+
+@pytest.mark.parametrize("d, tokens", [(64, 64), (128, 64), (64, 256), (128, 2048), (64, 60000)])
+def test_blocks_that_give_up_leave_the_gpu_usable(d, tokens):
+    """Waits that run out at the start and in the middle of long items: the status says so, and what runs next is right."""
+    pages = 1024
+    rows = torch.zeros(pages, 64, 2 * d, dtype=BF16, device="cuda")
+    table, lens = torch.arange(pages, dtype=torch.int32, device="cuda"), torch.tensor([64 * pages], dtype=torch.int32, device="cuda")
+    q = torch.zeros(tokens, d, dtype=BF16, device="cuda")
+    out = torch.empty_like(q)
+    for wait_ns in (0, 1000, 10_000, 50_000, 10**9):
+        status = torch.zeros(1, dtype=torch.int32, device="cuda")
+        cpkv.cpkv_selftest_attend_timeout(rows, table, lens, q, out, wait_ns, status)
+        torch.cuda.synchronize()
+        # 65536 keys take hundreds of us: no block gets through without a wait of 50; none of them waits for a second
+        assert int(status) == (0 if wait_ns == 10**9 else cpkv.STATUS_TIMEOUT), wait_ns
+        assert wait_ns < 10**9 or bool((out == 0).all())
+        cache, step, d_q, outs, want = decode_batch(3)
+        step(d_q[0], *outs[0])
+        long = cache.attend_window(d_q[1].expand(3, -1, -1).contiguous(), [3], torch.arange(1, 180, dtype=torch.int32, device="cuda")[None],
+                                   torch.tensor([2500], dtype=torch.int32, device="cuda"), max_kv_len=2500)
+        torch.cuda.synchronize()
+        model.check(*outs[0], want[0], BF16)
+        assert bool(long.isfinite().all()) and int(cache.d_status) == 0
