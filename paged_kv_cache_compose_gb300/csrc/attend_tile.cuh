@@ -215,14 +215,32 @@ CPKV_DEV void find_item(const TileParams<S> &p, int block, TileItem *r) {
   if (split == 0 && r->h == 0 && rt == 0 && p.seqs.kv_len_bad(s)) raise_status(p.seqs.status, CPKV_STATUS_OUT_CAPACITY);
 }
 
+// x.y + sum and o + w v, two elements each.
+template <typename T>
+CPKV_DEV float add_product(uint32_t x, uint32_t y, float sum) {
+  const float2 a = unpack2<T>(x), b = unpack2<T>(y);
+  return fmaf(a.x, b.x, fmaf(a.y, b.y, sum));
+}
+template <typename T>
+CPKV_DEV void add_scaled(float *o, float w, uint32_t v) {
+  const float2 b = unpack2<T>(v);
+  o[0] = fmaf(w, b.x, o[0]);
+  o[1] = fmaf(w, b.y, o[1]);
+}
+
 // A row of an item whose output holds a NaN, by the thread that wrote it.  A product
 // adds weight 0 times the value for keys of a tile that the row does not see, so where
 // one of those values is infinite or a NaN the output is worked out again over the keys
 // that it does see, with the maximum and sum that the row has (which no other key
 // enters): to `out` (16-bit results) or `part` (a part's values).  For NaNs only: to look
 // at the values beforehand costs more (traced prefill 2.27 ms where it is 2.13).
+// Latency bounds it: an item whose 256 rows all need it takes 3.1 us a key (19 a key at a
+// time; four in flight together), so the block's waits are given more time meanwhile.
+// Eight rows at a time over a warp's lanes took 2.1 us a key, but the kernel that called
+// it, without calling it, took 8% longer.
+constexpr int kMendKeys = 4;  // at a time
 template <typename T, int D, typename S>
-__device__ __noinline__ void mend_row(const TileParams<S> &p, const TileItem &item, int token, int head, float base, float l,
+__device__ __noinline__ void mend_row(const TileParams<S> &p, const TileItem &item, uint64_t *deadline, int token, int head, float base, float l,
                                       char *out, float *part) {
   const RowMask mask = row_mask(item.kv, item.nq, token, p.seqs.causal, p.seqs.window, p.seqs.sinks);
   const int64_t k_at = p.io.k_off + (int64_t)item.h * D * 2, v_at = p.io.v_off + (int64_t)item.h * D * 2;
@@ -252,24 +270,40 @@ __device__ __noinline__ void mend_row(const TileParams<S> &p, const TileItem &it
     float o[64] = {};
     for (int j = item.j0; j < item.j0 + item.n; ++j) {
       const int start = item.keys.tile_start(j, kTileKeys);
+      atomicMax(reinterpret_cast<unsigned long long *>(deadline), (unsigned long long)(global_timer_ns() + kTileWaitNs));
 #pragma unroll 1
-      for (int key = start; key < start + kTileKeys; ++key) {
-        const char *const at = mask.sees(key) ? row_of(key) : nullptr;
-        if (at == nullptr) continue;
-        float dot = 0.f;
-#pragma unroll 4
-        for (int c = 0; c < D / 2; ++c) {
-          const float2 a = unpack2<T>(reinterpret_cast<const uint32_t *>(q)[c]);
-          const float2 b = unpack2<T>(reinterpret_cast<const uint32_t *>(at + k_at)[c]);
-          dot = fmaf(a.x, b.x, fmaf(a.y, b.y, dot));
-        }
-        const float w = exp2_approx(fmaf(dot, p.io.scale_log2, -shift));
+      for (int first = start; first < start + kTileKeys; first += kMendKeys) {
+        const char *k[kMendKeys], *v[kMendKeys];  // vectors of zeros for keys that the row does not see
+        float w[kMendKeys] = {};
+        uint32_t seen = 0;
 #pragma unroll
-        for (int c = 0; c < 32; ++c) {
-          const float2 v = unpack2<T>(reinterpret_cast<const uint32_t *>(at + v_at + half * 128)[c]);
-          o[2 * c] = fmaf(w, v.x, o[2 * c]);
-          o[2 * c + 1] = fmaf(w, v.y, o[2 * c + 1]);
+        for (int i = 0; i < kMendKeys; ++i) {
+          const char *const at = mask.sees(first + i) ? row_of(first + i) : nullptr;
+          k[i] = at != nullptr ? at + k_at : reinterpret_cast<const char *>(zero_row);
+          v[i] = at != nullptr ? at + v_at + half * 128 : reinterpret_cast<const char *>(zero_row);
+          seen |= at != nullptr ? 1u << i : 0u;
         }
+#pragma unroll 2
+        for (int c = 0; c < D / 8; ++c) {
+          const uint4 a = reinterpret_cast<const uint4 *>(q)[c];
+#pragma unroll
+          for (int i = 0; i < kMendKeys; ++i) {
+            const uint4 b = reinterpret_cast<const uint4 *>(k[i])[c];
+            w[i] = add_product<T>(a.x, b.x, add_product<T>(a.y, b.y, add_product<T>(a.z, b.z, add_product<T>(a.w, b.w, w[i]))));
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < kMendKeys; ++i) w[i] = seen >> i & 1 ? exp2_approx(fmaf(w[i], p.io.scale_log2, -shift)) : 0.f;
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+#pragma unroll
+          for (int i = 0; i < kMendKeys; ++i) {
+            const uint4 b = reinterpret_cast<const uint4 *>(v[i])[c];
+            add_scaled<T>(o + 8 * c, w[i], b.x);
+            add_scaled<T>(o + 8 * c + 2, w[i], b.y);
+            add_scaled<T>(o + 8 * c + 4, w[i], b.z);
+            add_scaled<T>(o + 8 * c + 6, w[i], b.w);
+          }
       }
     }
 #pragma unroll
@@ -539,9 +573,11 @@ __global__ void __launch_bounds__(kTileThreads, 1) attend_tile_kernel(const __gr
       if (step == 2) mbar_arrive(&bars.stream_free);
       if constexpr (S::causal) {
         const float2 m = unpair(marks);
-        if (row < rows && item.nq > 1 && my_n > 0 && !(m.x == 0.f && m.y == 0.f))
-          mend_row<T, D>(p, item, token, head, base, l, p.io.out + out_token * p.io.out_stride + (int64_t)head * (D * 2),
-                         p.direct ? nullptr : p.space.o + slot_row * D);
+        const bool bad = row < rows && item.nq > 1 && my_n > 0 && !(m.x == 0.f && m.y == 0.f);
+        if (bad)
+          mend_row<T, D>(p, item, &bars.deadline, token, head, base, l,
+                          p.io.out + out_token * p.io.out_stride + (int64_t)head * (D * 2),
+                          p.direct ? nullptr : p.space.o + slot_row * D);
         item_read(k);
       }
     }

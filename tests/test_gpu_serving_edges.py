@@ -254,3 +254,38 @@ def test_blocks_that_give_up_leave_the_gpu_usable(d, tokens):
         torch.cuda.synchronize()
         model.check(*outs[0], want[0], BF16)
         assert bool(long.isfinite().all()) and int(cache.d_status) == 0
+
+
+def test_infinite_values_beside_very_many_keys():
+    """One NaN and one infinity among 300 000 keys, near the end: the rows that do not see them are worked out again in
+    time, whole items long, and stay right."""
+    hq, hkv, d, ps, kv, nq = 32, 8, 128, 64, 300_000, 2560  # 320 items, each over all keys
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    pages = -(-kv // ps)
+    pool = torch.randn(pages, ps, 2 * hkv * d, dtype=BF16, device="cuda", generator=gen)
+    table = torch.randperm(pages, device="cuda", generator=gen).int()[None]
+    q = torch.randn(nq, hq, d, dtype=BF16, device="cuda", generator=gen)
+
+    def spoil(key, head, element, value):
+        pool[int(table[0, key // ps]), key % ps, (hkv + head) * d + element] = value
+
+    # (key, head, element): the last token sees the first; tokens from kv - 1000 on see the second
+    spoil(kv - 1, 2, 5, float("nan"))
+    spoil(kv - 1000, 6, 77, float("inf"))
+    cache = PagedCache([pool], page_size=ps, kv_heads=hkv, key_dim=d, dense=True)
+    lse = torch.empty(nq, hq, device="cuda")
+    out = cache.attend_window(q, [nq], table, torch.tensor([kv], dtype=torch.int32, device="cuda"), max_kv_len=kv, lse=lse)
+    torch.cuda.synchronize()
+    assert int(cache.d_status) == 0
+    want = torch.ones_like(out, dtype=torch.bool)
+    want[nq - 1, 8:12, 5] = False
+    want[nq - 1000:, 24:28, 77] = False
+    assert torch.equal(out.isfinite(), want) and bool(lse.isfinite().all())
+    rows = pool[table[0].long()].view(-1, 2, hkv, d)[:kv]
+    for token, head in [(nq - 2, 9), (nq - 64, 11), (nq - 30, 8), (nq - 1001, 25), (nq - 1024, 24), (nq - 1001, 9), (nq - 1, 0)]:
+        seen, c = kv - nq + token + 1, head // 4
+        k, v = rows[:seen, 0, c].double(), rows[:seen, 1, c].double()
+        s = k @ q[token, head].double() * d**-0.5
+        e = torch.logsumexp(s, 0)
+        w = torch.exp(s - e)
+        model.check(out[token, head], lse[token, head], ((w @ v).cpu(), e.cpu(), (w @ v.abs()).cpu()), BF16)
