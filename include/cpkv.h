@@ -613,7 +613,8 @@ int cpkv_append_rotary(int64_t n_tokens, int page_size, int cp_size, int dtype, 
  * visible.  Request b has h_q_lens[b] query tokens (NULL: one each, a decode
  * step), the last of its d_kv_lens[b] cached tokens, whose rows are already in
  * the pools.  Query token i stands at position p = kv_len - q_len + i and sees
- * key j when j <= p and (p - j < window or j < sinks); window 0 is no window.
+ * key j when j <= p and (p - j < window or j < sinks); window 0 is no window (nor is
+ * one of max_kv_len or more).
  *   out = sum_j w_j v_j,  w = softmax_j(scale q.k_j),  lse = ln sum_j exp(scale q.k_j)
  * Query head h uses key/value head h / (q_heads / kv_heads).  Products and the
  * softmax are held in 32 bits; the weights are rounded to the element type for

@@ -190,6 +190,10 @@ struct WindowPlan {
   int64_t tokens = 0, bytes = 0;
 };
 
+// A window that no request's keys reach past is none: positions less it stay in 32 bits,
+// also below 0 (a request shorter than its queries).
+int clamp_window(int window, int64_t max_kv) { return window >= max_kv ? 0 : window; }
+
 int window_plan(WindowPlan *w, const HeadArgs &a, int B, const int32_t *h_q_lens, int64_t max_kv, int window, int sinks) {
   const int group = a.q_heads / a.kv_heads;
   for (int s = 0; s < B; ++s) {
@@ -231,6 +235,7 @@ int shared_plan(SharedPlan *w, const HeadArgs &a, int B, int n_groups, const int
   for (int g = 0; g < n_groups; ++g) {
     if (h_group_sizes[g] < 0 || h_prefix_lens[g] < 0) return CPKV_ERR_ARG;
     if (page_size > 0 && h_prefix_lens[g] % page_size != 0) return CPKV_ERR_UNALIGNED_PREFIX;
+    if (h_prefix_lens[g] > INT32_MAX / 2) return CPKV_ERR_LIMIT;
     w->tile.add(h_group_sizes[g], h_prefix_lens[g], group, 0, 0);
     sum += h_group_sizes[g];
     if (page_size > 0) w->prefix_pages += h_prefix_lens[g] / page_size;
@@ -457,6 +462,7 @@ extern "C" int cpkv_attend_window_workspace_bytes(int B, int q_heads, int kv_hea
   int rc = check_heads(heads);
   if (rc != CPKV_OK) return rc;
   if (B > CPKV_MAX_BATCH || max_kv_len > INT32_MAX / 2) return CPKV_ERR_LIMIT;
+  window = clamp_window(window, max_kv_len);
   WindowPlan plan;
   rc = window_plan(&plan, heads, B, h_q_lens, max_kv_len, window, sinks);
   if (rc != CPKV_OK) return rc;
@@ -482,6 +488,7 @@ extern "C" int cpkv_attend_window(int B, int page_size, int cp_size, int dtype, 
   rc = check_rows(heads, row_bytes, key_offset, value_offset);
   if (rc != CPKV_OK) return rc;
   if (table_stride < 0 || max_kv_len > table_stride * page_size) return CPKV_ERR_CAPACITY;
+  window = clamp_window(window, max_kv_len);
   WindowPlan plan;
   rc = window_plan(&plan, heads, B, h_q_lens, max_kv_len, window, sinks);
   if (rc != CPKV_OK) return rc;

@@ -289,3 +289,27 @@ def test_infinite_values_beside_very_many_keys():
         e = torch.logsumexp(s, 0)
         w = torch.exp(s - e)
         model.check(out[token, head], lse[token, head], ((w @ v).cpu(), e.cpu(), (w @ v.abs()).cpu()), BF16)
+
+
+@pytest.mark.parametrize("q_lens, kv_lens", [([1, 1, 1], [3, 700, 0]), ([5, 5], [2, 0]), ([40, 3], [20, 300]), ([64], [1])],
+                         ids=lambda x: "-".join(map(str, x)))
+@pytest.mark.parametrize("window", [2**31 - 1, 2**31 - 6, "longest"])
+def test_windows_beyond_every_key_are_none(q_lens, kv_lens, window):
+    """Requests shorter than their queries under windows near 2^31: positions below 0 less the window."""
+    hq, hkv, d, ps = 8, 2, 64, 16
+    rng = np.random.default_rng(sum(kv_lens))
+    lists, n_pages = page_tables(rng, kv_lens, ps)
+    pools = model.Pools(rng, n_pages, ps, 2, 2 * hkv * d, BF16)
+    q = queries(rng, sum(q_lens), hq, d, BF16)
+    cache = PagedCache(pools.cuda(), page_size=ps, kv_heads=hkv, key_dim=d)
+    table, lens = torch.from_numpy(lists).cuda(), torch.tensor(kv_lens, dtype=torch.int32).cuda()
+    results = []
+    for w, sinks in ((0, 0), (max(kv_lens) if window == "longest" else window, 0), (max(kv_lens) if window == "longest" else window, 2**31 - 1)):
+        lse = torch.full((sum(q_lens), hq), 7.0, device="cuda")
+        out = cache.attend_window(q.cuda(), q_lens, table, lens, max_kv_len=max(kv_lens), window=w, sinks=sinks, lse=lse)
+        torch.cuda.synchronize()
+        model.check(out, lse, model.window(q, q_lens, lists, kv_lens, pools, kv_heads=hkv, dim=d, window=0, sinks=0, scale=d**-0.5), BF16)
+        results.append((out, lse))
+    for out, lse in results[1:]:
+        assert torch.equal(out, results[0][0]) and torch.equal(lse, results[0][1])
+    assert int(cache.d_status) == 0
