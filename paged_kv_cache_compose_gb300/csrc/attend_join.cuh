@@ -135,7 +135,7 @@ __global__ void __launch_bounds__(128) attend_join_kernel(const __grid_constant_
       const Parts &at = k < c0 ? parts[0] : parts[1];
       const int64_t r = at.row(k < c0 ? k : k - c0);
       v = *reinterpret_cast<const float2 *>(at.ml + r * 2);
-      values = at.o + r * D;
+      if (v.y != 0.f) values = at.o + r * D;  // a part without keys has no values written
     }
     float best = v.x;
 #pragma unroll
@@ -153,8 +153,9 @@ __global__ void __launch_bounds__(128) attend_join_kernel(const __grid_constant_
 #pragma unroll 8
     for (int i = part_of; i < n; i += kWarps) {
       const float w = __shfl_sync(0xffffffffu, weight, i);
-      const float *src = reinterpret_cast<const float *>(__shfl_sync(0xffffffffu, (unsigned long long)values, i)) + lane * kEach;
-      if (w == 0.f) continue;  // a part without keys has no values written
+      const float *src = reinterpret_cast<const float *>(__shfl_sync(0xffffffffu, (unsigned long long)values, i));
+      if (src == nullptr) continue;  // (a weight of 0 still lets infinite values through, as in one pass)
+      src += lane * kEach;
       if constexpr (kEach == 4) {
         const float4 x = *reinterpret_cast<const float4 *>(src);
         o[0] += w * x.x, o[1] += w * x.y, o[2] += w * x.z, o[3] += w * x.w;

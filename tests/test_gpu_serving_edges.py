@@ -313,3 +313,42 @@ def test_windows_beyond_every_key_are_none(q_lens, kv_lens, window):
     for out, lse in results[1:]:
         assert torch.equal(out, results[0][0]) and torch.equal(lse, results[0][1])
     assert int(cache.d_status) == 0
+
+
+@pytest.mark.parametrize("nq, hq", [(1, 8), (3, 8), (11, 24)], ids=["split", "split-queries", "tile"])
+def test_an_infinite_value_of_tiny_weight_in_another_part(nq, hq):
+    """The first key's score leaves nothing to the others in 32 bits; an infinity among them still reaches the rows that see it."""
+    hkv, d, ps, kv = 2, 128, 16, 3000
+    rng = np.random.default_rng(nq)
+    lists, n_pages = page_tables(rng, [kv], ps)
+    pools = model.Pools(rng, n_pages, ps, 2, 2 * hkv * d, BF16)
+    q = queries(rng, nq, hq, d, BF16)
+    q[..., 0] = 64.0
+    first = pools.row(int(lists[0, 0]), 0)
+    first[0] = first[d] = 64.0  # a score of 64 * 64 / sqrt(128) more than the others'
+    key = 2000
+    pools.row(int(lists[0, key // ps]), key % ps)[hkv * d + d + 7] = float("inf")
+    cache = PagedCache(pools.cuda(), page_size=ps, kv_heads=hkv, key_dim=d)
+    out = cache.attend_window(q.cuda(), [nq], torch.from_numpy(lists).cuda(), torch.tensor([kv], dtype=torch.int32).cuda(), max_kv_len=kv)
+    want = torch.ones(nq, hq, d, dtype=torch.bool)
+    want[:, hq // 2:, 7] = False
+    assert torch.equal(out.cpu().isfinite(), want)
+
+
+@pytest.mark.parametrize("requests", [2, 24], ids=["split", "tile"])
+def test_an_infinite_value_of_tiny_weight_in_a_suffix(requests):
+    hq, hkv, d, ps, prefix = 8, 1, 64, 16, 480
+    suffix = [1 + 3 * i for i in range(requests)]
+    rng = np.random.default_rng(requests)
+    lists, n_pages = page_tables(rng, [prefix] + suffix, ps)
+    pools = model.Pools(rng, n_pages, ps, 2, 2 * hkv * d, FP16)
+    q = queries(rng, requests, hq, d, FP16)
+    q[..., 0] = 64.0
+    pools.row(int(lists[0, 0]), 0)[0] = 64.0
+    pools.row(int(lists[2, 0]), 1)[hkv * d + 3] = -float("inf")  # the second request's
+    cache = PagedCache(pools.cuda(), page_size=ps, kv_heads=hkv, key_dim=d)
+    out = cache.attend_shared(q.cuda(), [requests], [prefix], torch.from_numpy(lists[0, :prefix // ps].astype(np.int32)).cuda(),
+                              torch.from_numpy(lists[1:]).cuda(), torch.tensor(suffix, dtype=torch.int32).cuda(), max_suffix_len=max(suffix))
+    want = torch.ones(requests, hq, d, dtype=torch.bool)
+    want[1, :, 3] = False
+    assert torch.equal(out.cpu().isfinite(), want)
