@@ -27,6 +27,16 @@
 namespace cpkv {
 
 constexpr float kLog2e = 1.4426950408889634f;
+
+// Weights are rounded to the element type for the product with the values, which is the
+// matrix instructions' operand type (their sum is taken before that, in 32 bits): half a
+// step of each weight, about as much again as the result's own rounding (bf16 results are
+// 0.0017 from those in 64 bits with weights in 32 bits, 0.0018 to 0.0023 so).  fp16 would lose
+// weights below 2^-25 whole, so its maximum is held kLift below the scores': weights
+// reach up to 2^15 (32768, with the tile pass's threshold of 2^8) and down to 2^-39 of
+// the largest, or 2^-32 there.
+template <typename T, bool kTile>
+constexpr float kLift = std::is_same<T, __half>::value ? (kTile ? 7.f : 15.f) : 0.f;
 constexpr float kLn2 = 0.6931471805599453f;
 
 // The requests of a windowed call.

@@ -362,7 +362,7 @@ __global__ void __launch_bounds__(kSplitWarps * 32, SplitShape<D, kMode>::kBlock
       float best = fmaxf(fmaxf(x[0][2 * r], x[0][2 * r + 1]), fmaxf(x[1][2 * r], x[1][2 * r + 1]));
       best = fmaxf(best, __shfl_xor_sync(0xffffffffu, best, 1));
       best = fmaxf(best, __shfl_xor_sync(0xffffffffu, best, 2));
-      const float next = fmaxf(m[r], best);
+      const float next = fmaxf(m[r], best - kLift<T, false>);
       shift[r] = next == -INFINITY ? 0.f : next;
       const float fall = exp2_approx(m[r] - shift[r]);
       if (__any_sync(0xffffffffu, next != m[r])) {
@@ -375,7 +375,7 @@ __global__ void __launch_bounds__(kSplitWarps * 32, SplitShape<D, kMode>::kBlock
       }
       m[r] = next;
     }
-    uint32_t pf[4];  // weights as the first operand; rounded to T for the product, summed before it
+    uint32_t pf[4];  // weights as the first operand; rounded to T for the product, summed before it (kLift says why)
 #pragma unroll
     for (int n = 0; n < 2; ++n)
 #pragma unroll

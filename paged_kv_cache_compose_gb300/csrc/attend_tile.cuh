@@ -25,8 +25,8 @@
 // 128 keys (two streams), joined at the end.
 // Tensor memory (512 columns): scores of the tiles at 0 and 128, outputs at 256
 // and 384.  A row's output is rescaled only when its maximum has risen by more
-// than 2^8 since the last time: weights stay below 2^8, and the sum and the output
-// carry the same factor, which cancels at the end.
+// than 2^8 since the last time: weights stay below 2^8 (times kLift's factor), and the
+// sum and the output carry the same factor, which cancels at the end.
 // Measured: 44600 tokens of 12 requests, 32 heads of 128 on 8, a window of 4096 and 64
 // sinks behind prefixes of up to 16384, take 2.13 ms: 1.40 PFLOP/s on the visible keys,
 // 74% of the measured bf16 rate of plain products (the tensor pipe is busy 61% of the
@@ -433,7 +433,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) attend_tile_kernel(const __gr
 #pragma unroll
           for (int i = 2; i < 32; i += 2) best[c] = max3(best[c], __uint_as_float(x[c][i]), __uint_as_float(x[c][i + 1]));
         }
-        const float top = fmaxf(fmaxf(best[0], best[1]), fmaxf(best[2], best[3])) * scale;
+        const float top = fmaf(fmaxf(fmaxf(best[0], best[1]), fmaxf(best[2], best[3])), scale, -kLift<T, true>);
         const bool rise = top > base + kRescaleAt || (base == -INFINITY && top != -INFINITY);
         if (__any_sync(0xffffffffu, rise)) {  // the sum and the output so far shrink by 2^(old - new)
           const float next = rise ? top : base;

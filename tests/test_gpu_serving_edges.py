@@ -352,3 +352,26 @@ def test_an_infinite_value_of_tiny_weight_in_a_suffix(requests):
     want = torch.ones(requests, hq, d, dtype=torch.bool)
     want[1, :, 3] = False
     assert torch.equal(out.cpu().isfinite(), want)
+
+
+@pytest.mark.parametrize("dtype", [FP16, BF16])
+@pytest.mark.parametrize("nq, hq, kv", [(1, 2, 3000), (3, 2, 3000), (64, 1, 3000), (300, 1, 900), (1, 2, 200)],
+                         ids=["split", "split-queries", "parts", "tile", "few-keys"])
+def test_many_small_weights_beside_one_large(nq, hq, kv, dtype):
+    """One key's weight is 2^25 times the others', whose values are all that the result is made of."""
+    d, ps = 64, 16
+    rng = np.random.default_rng(kv)
+    lists, n_pages = page_tables(rng, [kv], ps)
+    pools = model.Pools(rng, n_pages, ps, 2, 2 * d, dtype)
+    for s in pools.slabs:
+        s[..., :d] = 0.0
+        s[..., d:] = 1.0
+    first = pools.row(int(lists[0, 0]), 0)
+    first[0], first[d:] = 8.75, 0.0
+    q = torch.zeros(nq, hq, d, dtype=dtype)
+    q[..., 0] = 16.0
+    want = model.window(q, [nq], lists, [kv], pools, kv_heads=1, dim=d, window=0, sinks=0, scale=d**-0.5)
+    cache = PagedCache(pools.cuda(), page_size=ps, kv_heads=1, key_dim=d)
+    lse = torch.empty(nq, hq, device="cuda")
+    out = cache.attend_window(q.cuda(), [nq], torch.from_numpy(lists).cuda(), torch.tensor([kv], dtype=torch.int32).cuda(), max_kv_len=kv, lse=lse)
+    model.check(out, lse, want, dtype)
