@@ -123,11 +123,12 @@ class Lengths {
   explicit Lengths(PyObject *o) {
     if (o == Py_None) return;
     if (PyObject_CheckBuffer(o)) {
-      if (PyObject_GetBuffer(o, &view_, PyBUF_ND | PyBUF_FORMAT | PyBUF_C_CONTIGUOUS) == 0) {
-        held_ = true;
-        if (view_.ndim == 1 && view_.itemsize == 4 && view_.format != nullptr && (view_.format[0] == 'i' || view_.format[0] == 'l')) {
-          at_ = static_cast<const int32_t *>(view_.buf);
-          count_ = view_.shape[0];
+      if (PyObject_GetBuffer(o, &view_.buffer, PyBUF_ND | PyBUF_FORMAT | PyBUF_C_CONTIGUOUS) == 0) {
+        view_.held = true;
+        const Py_buffer &v = view_.buffer;
+        if (v.ndim == 1 && v.itemsize == 4 && v.format != nullptr && (v.format[0] == 'i' || v.format[0] == 'l')) {
+          at_ = static_cast<const int32_t *>(v.buf);
+          count_ = v.shape[0];
           return;
         }
       } else {
@@ -138,7 +139,7 @@ class Lengths {
     if (seq == nullptr) throw Failed();
     const Py_ssize_t n = PySequence_Fast_GET_SIZE(seq);
     copy_.resize(n);
-    for (Py_ssize_t i = 0; i < n; ++i) {
+    for (Py_ssize_t i = 0; i < n && !PyErr_Occurred(); ++i) {
       const long long v = PyLong_AsLongLong(PySequence_Fast_GET_ITEM(seq, i));
       copy_[i] = v < INT32_MIN || v > INT32_MAX ? -1 : static_cast<int32_t>(v);
     }
@@ -147,16 +148,20 @@ class Lengths {
     at_ = copy_.data();
     count_ = n;
   }
-  ~Lengths() {
-    if (held_) PyBuffer_Release(&view_);
-  }
-  Lengths(const Lengths &) = delete;
   const int32_t *at() const { return at_; }
   int64_t count() const { return count_; }
 
  private:
-  Py_buffer view_;
-  bool held_ = false;
+  struct View {  // released also when the constructor above throws
+    Py_buffer buffer;
+    bool held = false;
+    View() = default;
+    View(const View &) = delete;
+    ~View() {
+      if (held) PyBuffer_Release(&buffer);
+    }
+  };
+  View view_;
   std::vector<int32_t> copy_;
   const int32_t *at_ = nullptr;
   int64_t count_ = 0;
@@ -174,10 +179,26 @@ int small(PyObject *o, const char *name) {
   return static_cast<int>(v);
 }
 
-const Table &table(PyObject *o) { return *reinterpret_cast<const Table *>(static_cast<uintptr_t>(PyLong_AsUnsignedLongLong(o))); }
+// An address that Python holds as a number.
+template <typename T>
+T address(PyObject *o) {
+  const unsigned long long v = PyLong_AsUnsignedLongLong(o);
+  if (v == static_cast<unsigned long long>(-1) && PyErr_Occurred()) throw Failed();
+  return reinterpret_cast<T>(static_cast<uintptr_t>(v));
+}
 
-cpkv_stream_t stream_of(PyObject *o) {
-  return reinterpret_cast<cpkv_stream_t>(static_cast<uintptr_t>(PyLong_AsUnsignedLongLong(o)));
+const Table &table(PyObject *o) {
+  const Table *t = address<const Table *>(o);
+  if (t == nullptr) fail("table", "a PoolTable's address");
+  return *t;
+}
+
+cpkv_stream_t stream_of(PyObject *o) { return address<cpkv_stream_t>(o); }
+
+double real(PyObject *o) {
+  const double v = PyFloat_AsDouble(o);
+  if (v == -1.0 && PyErr_Occurred()) throw Failed();
+  return v;
 }
 
 // Runs a call, its first argument the table, with the pools' device current: the entry
@@ -232,7 +253,9 @@ PyObject *append_rotary(PyObject *, PyObject *const *a, Py_ssize_t n) {
       if (!PyBytes_Check(a[12]) || PyBytes_GET_SIZE(a[12]) != turns.size(1) / 2) fail("axis_of_freq", "an axis per frequency");
       axis = reinterpret_cast<const uint8_t *>(PyBytes_AS_STRING(a[12]));
     }
-    const int flags = t.flags | (PyObject_IsTrue(a[13]) ? CPKV_ROTARY_INTERLEAVED : 0);
+    const int interleaved = PyObject_IsTrue(a[13]);
+    if (interleaved < 0) throw Failed();
+    const int flags = t.flags | (interleaved ? CPKV_ROTARY_INTERLEAVED : 0);
     return cpkv_append_rotary(k.n, t.page_size, t.cp_size, t.code, static_cast<int>(q.heads), static_cast<int>(k.heads),
                               static_cast<int>(k.dim), static_cast<int>(v.dim), t.row_bytes, t.key_offset, t.value_offset,
                               t.pools(), t.cap_pages(), k.at, k.stride, v.at, v.stride, q.at, q.stride, q_out.at, q_out.stride,
@@ -254,7 +277,7 @@ PyObject *attend_window(PyObject *, PyObject *const *a, Py_ssize_t n) {
     if (q_lens.at() != nullptr && q_lens.count() != requests) fail("q_lens", "a length per request");
     const int64_t max_kv = whole(a[6]);
     if (max_kv > pages.pages * t.page_size) return CPKV_ERR_CAPACITY;
-    const double scale = PyFloat_AsDouble(a[9]);
+    const double scale = real(a[9]);
     float *lse = lse_of(a[11], t, q);
     void *workspace = memory(a[12], t, &bytes);
     int32_t *status = status_word(a[13], t);
@@ -280,7 +303,7 @@ PyObject *attend_shared(PyObject *, PyObject *const *a, Py_ssize_t n) {
     if (q.n != requests || sizes.count() != lens.count()) fail("q, group_sizes and prefix_lens", "a query per request, a prefix length per group");
     const int64_t max_suffix = whole(a[8]);
     if (max_suffix > pages.pages * t.page_size) return CPKV_ERR_CAPACITY;
-    const double scale = PyFloat_AsDouble(a[9]);
+    const double scale = real(a[9]);
     float *lse = lse_of(a[11], t, q);
     void *workspace = memory(a[12], t, &bytes);
     int32_t *status = status_word(a[13], t);

@@ -375,3 +375,41 @@ def test_many_small_weights_beside_one_large(nq, hq, kv, dtype):
     lse = torch.empty(nq, hq, device="cuda")
     out = cache.attend_window(q.cuda(), [nq], torch.from_numpy(lists).cuda(), torch.tensor([kv], dtype=torch.int32).cuda(), max_kv_len=kv, lse=lse)
     model.check(out, lse, want, dtype)
+
+
+def small_calls():
+    cache = PagedCache([torch.zeros(4, 16, 256, dtype=BF16, device="cuda")], page_size=16, kv_heads=2, key_dim=64)
+    k = torch.zeros(1, 2, 64, dtype=BF16, device="cuda")
+    one, turns = torch.ones(1, dtype=torch.int32, device="cuda"), torch.ones(8, 64, device="cuda")
+    pages = torch.ones(1, 1, dtype=torch.int32, device="cuda")
+    return cache, dict(
+        append=lambda x=k, **more: cache.append_rotary(x, x, 16 * one.long(), one, turns, **more),
+        window=lambda x=k, lens=None, **more: cache.attend_window(x, lens, pages, one, max_kv_len=16, **more),
+        shared=lambda x=k, lens=(1,), **more: cache.attend_shared(x, lens, [0], one[:0], pages, one, max_suffix_len=16, **more))
+
+
+def test_streams_and_numbers_that_are_none():
+    """A stream that is no handle, a scale that is no number: an exception before anything is launched."""
+    cache, calls = small_calls()
+    for name, call in calls.items():
+        for stream in (-1, 1 << 70):
+            with pytest.raises(Exception):
+                call(stream=stream)
+    for name in ("window", "shared"):
+        with pytest.raises(TypeError):
+            calls[name](scale="1")
+    torch.cuda.synchronize()
+    assert int(cache.d_status) == 0
+
+
+def test_lengths_that_are_refused_let_their_array_go():
+    """An array of lengths of another type is free again after the exception."""
+    _, calls = small_calls()
+    for name in ("window", "shared"):
+        for bad in (np.ones(1, np.float64), np.array([1.5], np.float32)):
+            with pytest.raises(TypeError):
+                calls[name](lens=bad)
+            bad.resize(3, refcheck=False)  # raises while a buffer of it is held
+        held = bytearray(b"\x01")
+        calls[name](lens=held)
+        held.append(1)  # likewise
