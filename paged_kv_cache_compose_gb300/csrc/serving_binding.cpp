@@ -62,8 +62,8 @@ Rows rows(PyObject *o, const char *name, const Table &t) {
   if (x.dim() != 3) fail(name, what);
   const auto size = x.sizes(), stride = x.strides();
   if ((stride[2] != 1 && size[2] > 1) || (stride[1] != size[2] && size[1] > 1)) fail(name, what);
-  const int64_t width = size[1] * size[2];
-  return Rows{x.data_ptr(), size[0] > 1 ? stride[0] : std::max<int64_t>(stride[0], width), size[0], size[1], size[2]};
+  const int64_t width = size[1] * size[2];  // also the stride of a single token, which has none
+  return Rows{x.data_ptr(), size[0] > 1 ? stride[0] : width, size[0], size[1], size[2]};
 }
 
 // A contiguous device list.

@@ -413,3 +413,13 @@ def test_lengths_that_are_refused_let_their_array_go():
         held = bytearray(b"\x01")
         calls[name](lens=held)
         held.append(1)  # likewise
+
+
+def test_a_single_token_has_no_stride():
+    """A token taken out of a tensor whose rows are no multiple of 16 bytes apart."""
+    _, calls = small_calls()
+    rows = torch.zeros(1, 132, dtype=BF16, device="cuda")  # one row of 132 elements, of which the first 128 are the heads
+    odd = rows.as_strided((1, 2, 64), (132, 64, 1))
+    assert odd.stride(0) == 132
+    for call in calls.values():
+        call(odd)
