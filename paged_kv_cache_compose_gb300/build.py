@@ -1,5 +1,7 @@
-"""Build ``libcpkv.so`` in-tree with nvcc for sm_103a, and ``_serving.so``, the
-Python marshalling of the serving calls, with the host compiler.
+"""Build ``libcpkv.so`` in-tree with nvcc for sm_103a, and ``_serving``, the
+Python marshalling of the serving calls, with the host compiler against the
+torch that is installed (left out where there is none: the library and the
+compose need neither).
 
 Each translation unit under ``csrc/`` is compiled in parallel, then linked
 into one shared library next to this file.  Usage::
@@ -12,6 +14,7 @@ from __future__ import annotations
 import argparse
 import concurrent.futures as cf
 import glob
+import importlib.metadata
 import os
 import shutil
 import subprocess
@@ -25,7 +28,8 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(HERE, "_build")
 LIB_PATH = os.path.join(HERE, "libcpkv.so")
 BINDING_SRC = os.path.join(CSRC, "serving_binding.cpp")
-BINDING_PATH = os.path.join(HERE, "_serving.so")
+BINDING_PATH = os.path.join(HERE, "_serving" + sysconfig.get_config_var("EXT_SUFFIX"))
+BINDING_STAMP = os.path.join(BUILD_DIR, "serving_binding.torch")  # version of torch that it was built against
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
@@ -77,8 +81,24 @@ def stale() -> bool:
     return _older(LIB_PATH, _deps())
 
 
+def torch_version() -> str | None:
+    """Of the installed torch, without importing it; None where there is none."""
+    try:
+        return importlib.metadata.version("torch")
+    except importlib.metadata.PackageNotFoundError:
+        return None
+
+
 def binding_stale() -> bool:
-    return _older(BINDING_PATH, [BINDING_SRC, os.path.join(INCLUDE, "cpkv.h")])
+    version = torch_version()
+    if version is None:
+        return False
+    try:
+        with open(BINDING_STAMP) as f:
+            built_for = f.read()
+    except OSError:
+        return True
+    return built_for != version or _older(BINDING_PATH, [BINDING_SRC, os.path.join(INCLUDE, "cpkv.h")])
 
 
 def _torch_dirs() -> tuple[list[str], str]:
@@ -96,7 +116,7 @@ def _compile_binding() -> str:
     obj = os.path.join(BUILD_DIR, "serving_binding.o")
     inc = [INCLUDE, *_torch_dirs()[0], sysconfig.get_paths()["include"]]
     cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-w",
-           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", f'-DBUILT_FOR="{torch_version()}"',
            *[a for d in inc for a in ("-isystem" if "torch" in d else "-I", d)], "-c", BINDING_SRC, "-o", obj]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
@@ -113,6 +133,8 @@ def _link_binding(obj: str) -> None:
     if r.returncode != 0:
         raise RuntimeError(f"link of {os.path.basename(BINDING_PATH)} failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, BINDING_PATH)
+    with open(BINDING_STAMP, "w") as f:
+        f.write(torch_version())
 
 
 def _compile(src: str, extra: list[str]) -> str:
@@ -128,8 +150,8 @@ def _compile(src: str, extra: list[str]) -> str:
 
 def build(force: bool = False, verbose_ptxas: bool = False) -> str:
     """Compile every CUDA translation unit and link ``libcpkv.so``; compile and
-    link ``_serving.so`` beside it."""
-    library, binding = force or stale(), force or binding_stale()
+    link ``_serving`` beside it."""
+    library, binding = force or stale(), binding_stale() or force and torch_version() is not None
     if not library and not binding:
         return LIB_PATH
     os.makedirs(BUILD_DIR, exist_ok=True)

@@ -477,12 +477,16 @@ def serving():
     if _native is None:
         import torch  # noqa: F401  (its libraries hold the tensors)
 
+        from .build import torch_version
+
         load()
+        again = "build the library again (python -m paged_kv_cache_compose_gb300.build)"
         try:
             from . import _serving
         except ImportError as e:
-            raise CpkvError("load", -100, f"_serving.so: {e}; build the library first "
-                                          "(python -m paged_kv_cache_compose_gb300.build)") from None
+            raise CpkvError("load", -100, f"_serving: {e}; {again}") from None
+        if _serving.built_for != torch_version():
+            raise CpkvError("load", -100, f"_serving was built for torch {_serving.built_for}, not {torch_version()}; {again}")
         _serving.set_fail(_wrong)
         _native = _serving
     return _native
