@@ -51,25 +51,23 @@ int64_t round_up(int64_t n, int64_t to) { return ceil_div(n, to) * to; }
 
 // Bounds of a split pass, from host lengths.
 struct SplitBounds {
-  int64_t tokens = 0, tiles_cap = 0, units = 0, max_tiles = 0;  // tiles, units: per key/value head
+  int64_t units = 0, max_tiles = 0;  // of all sequences, of one
   int grid_cap = 1;
 
-  void add(int64_t nq, int64_t max_kv, int group, int window, int sinks) {
+  void add(int64_t nq, int64_t max_kv, int window, int sinks) {
     int64_t tiles = ceil_div(max_kv, kSplitTile);
     if (window > 0) tiles = std::min<int64_t>(tiles, ceil_div((int64_t)sinks, kSplitTile) + ((int64_t)window + nq) / kSplitTile + 2);
-    units += ceil_div(nq * group, kSplitRows) * tiles;
+    units += nq > 0 ? tiles : 0;
     max_tiles = std::max<int64_t>(max_tiles, tiles);
-    tokens += nq;
-    tiles_cap += ceil_div(nq * group, kSplitRows) + 1;
   }
-  int finish(int group, int kv_heads) {
-    if (units > INT32_MAX || tokens * group > INT32_MAX) return CPKV_ERR_LIMIT;
+  int finish(int kv_heads) {
+    if (units > INT32_MAX) return CPKV_ERR_LIMIT;
     grid_cap = kv_heads * (int)std::min<int64_t>(kSplitMaxGrid / kv_heads, units > 0 ? units : 1);
     return CPKV_OK;
   }
-  int64_t slots(int kv_heads, bool direct) const { return 2 * (int64_t)grid_cap + (direct ? 0 : tiles_cap * kv_heads); }
+  int64_t slots(int64_t count, int kv_heads, bool direct) const { return 2 * (int64_t)grid_cap + (direct ? 0 : count * kv_heads); }
   int64_t bytes(int64_t count, int kv_heads, int head_dim, bool direct) const {
-    const int64_t n = slots(kv_heads, direct) * kSplitRows;
+    const int64_t n = slots(count, kv_heads, direct) * kSplitRows;
     return round_up((count + 1) * 4, 256) + round_up(n * 8, 256) + round_up(n * head_dim * 4, 256);
   }
   SplitSpace space(char *at, int64_t count, int kv_heads, bool direct) const {
@@ -77,7 +75,7 @@ struct SplitBounds {
     s.cum = reinterpret_cast<int32_t *>(at);
     at += round_up((count + 1) * 4, 256);
     s.ml = reinterpret_cast<float *>(at);
-    at += round_up(slots(kv_heads, direct) * kSplitRows * 8, 256);
+    at += round_up(slots(count, kv_heads, direct) * kSplitRows * 8, 256);
     s.o = reinterpret_cast<float *>(at);
     s.grid = grid_cap;
     return s;
@@ -199,22 +197,22 @@ int window_plan(WindowPlan *w, const HeadArgs &a, int B, const int32_t *h_q_lens
   for (int s = 0; s < B; ++s) {
     const int64_t nq = h_q_lens == nullptr ? 1 : h_q_lens[s];
     if (nq < 0) return CPKV_ERR_ARG;
-    w->split.add(nq, max_kv, group, window, sinks);
+    w->split.add(nq, max_kv, window, sinks);
     w->tile.add(nq, max_kv, group, window, sinks);
   }
   w->few = few_rows(w->tile.max_rows);
   w->tokens = w->tile.tokens;
   bool uniform = B > 0;
   for (int s = 1; s < B && h_q_lens != nullptr; ++s) uniform &= h_q_lens[s] == h_q_lens[0];
-  // A block takes whole tiles of few rows when no sequence has more units of keys
-  // than kWholeUnits and there are no more tiles than SMs: the units one after the other then
+  // A block takes a whole sequence of few rows when none has more units of keys
+  // than kWholeUnits and there are no more of them than SMs: the units one after the other then
   // cost less than joining parts does (4 requests, 8 heads of 128: 384 keys in 10.3 us
   // where parts take 12.3, 512 keys in 12.3 either way, 1024 in 20.5 where parts take
   // 13.4), and no more blocks wait than lines would have (64 requests of 384 keys: 36 us
-  // with whole tiles, 26 with parts).
+  // with whole sequences, 26 with parts).
   w->whole = w->few && uniform && w->split.max_tiles <= kWholeUnits &&
-             w->split.tiles_cap * a.kv_heads <= 2 * (int64_t)device_sm_count();
-  const int rc = w->few ? w->split.finish(group, a.kv_heads) : w->tile.finish(a.kv_heads, a.head_dim);
+             (int64_t)B * a.kv_heads <= device_sm_count();
+  const int rc = w->few ? w->split.finish(a.kv_heads) : w->tile.finish(a.kv_heads, a.head_dim);
   w->bytes = w->whole ? 0
              : w->few ? w->split.bytes(B, a.kv_heads, a.head_dim, true)
                       : w->tile.bytes(a.kv_heads, a.head_dim, true);
@@ -245,9 +243,9 @@ int shared_plan(SharedPlan *w, const HeadArgs &a, int B, int n_groups, const int
   w->few = few_rows(w->tile.max_rows);
   int rc;
   if (w->few) {
-    for (int g = 0; g < n_groups; ++g) w->split.add(h_group_sizes[g], h_prefix_lens[g], group, 0, 0);
-    for (int b = 0; b < B; ++b) w->split.add(1, max_suffix, group, 0, 0);
-    rc = w->split.finish(group, a.kv_heads);
+    for (int g = 0; g < n_groups; ++g) w->split.add(h_group_sizes[g], h_prefix_lens[g], 0, 0);
+    for (int b = 0; b < B; ++b) w->split.add(1, max_suffix, 0, 0);
+    rc = w->split.finish(a.kv_heads);
     w->bytes = w->split.bytes(n_groups + B, a.kv_heads, a.head_dim, false);
   } else {
     w->tile.add_singles(B, max_suffix);
@@ -267,7 +265,7 @@ int for_type_and_dim(const HeadArgs &a, F f) {
                            : f(__half(), std::integral_constant<int, 64>());
 }
 
-// A block takes a whole tile (row_tiles of each sequence) unless the mode is kLine.
+// A block takes a whole sequence unless the mode is kLine.
 template <typename T, int D, SplitMode kMode, typename S>
 int split_pass(SplitParams<S> *p, const SplitBounds &b, cudaStream_t stream) {
   using Shape = SplitShape<D, kMode>;
@@ -275,7 +273,7 @@ int split_pass(SplitParams<S> *p, const SplitBounds &b, cudaStream_t stream) {
   auto kernel = attend_split_kernel<T, D, S, kMode>;
   const int rc = ensure_dynamic_smem((const void *)kernel, Shape::kSmem + (kMode == kLine ? (2 * CPKV_MAX_BATCH + 1) * 4 : 0));
   if (rc != CPKV_OK) return rc;
-  int64_t blocks = (int64_t)p->seqs.count * p->io.kv_heads * p->row_tiles;
+  int64_t blocks = (int64_t)p->seqs.count * p->io.kv_heads;
   if (kMode == kLine) {  // as many blocks for every head as stay resident together
     const int heads = p->io.kv_heads, resident = persistent_grid((const void *)kernel, kSplitWarps * 32, smem, 8, b.grid_cap);
     blocks = p->space.grid = std::max(resident / heads, 1) * heads;
@@ -289,7 +287,6 @@ SplitSource<S> source_of(const SplitParams<S> &p) {
   SplitSource<S> s;
   s.seqs = p.seqs;
   s.space = p.space;
-  s.tiles_cap = p.tiles_cap;
   s.direct = p.direct;
   return s;
 }
@@ -396,13 +393,11 @@ int attend_window(const HeadArgs &heads, const Seqs<N> &seqs, const PagedPools &
     p.io = io;
     p.direct = 1;
     if (plan.whole) {
-      p.row_tiles = (int)ceil_div((int64_t)seqs.uniform_q * io.group.d, kSplitRows);
       return for_type_and_dim(heads, [&](auto t, auto d) {
         return split_pass<decltype(t), decltype(d)::value, kFewKeys>(&p, plan.split, stream);
       });
     }
     p.space = plan.split.space(workspace, seqs.count, heads.kv_heads, true);
-    p.tiles_cap = plan.split.tiles_cap;
     return for_type_and_dim(heads, [&](auto t, auto d) {
       using T = decltype(t);
       constexpr int D = decltype(d)::value;
@@ -431,7 +426,6 @@ int attend_shared(const HeadArgs &heads, const SharedSeqs<N> &seqs, const PagedP
     p.pools = pools;
     p.io = io;
     p.space = plan.split.space(workspace, seqs.count, heads.kv_heads, false);
-    p.tiles_cap = plan.split.tiles_cap;
     return for_type_and_dim(heads, [&](auto t, auto d) {
       using T = decltype(t);
       constexpr int D = decltype(d)::value;

@@ -63,8 +63,6 @@ struct Seqs {
   CPKV_DEV const int32_t *pages(int s) const { return table + s * stride; }
   // Sequences with lengths of their own queries; the others have one query each.
   CPKV_DEV int ragged() const { return count; }
-  // Tiles of 16 packed rows before sequence s, at most.
-  CPKV_DEV int64_t tiles_before(int s, int group) const { return (int64_t)q_begin(s) * group / 16 + s; }
   // The sequences that hold a query token, and where it stands in them.
   CPKV_DEV int places(int token, int (&s)[2], int (&i)[2]) const {
     s[0] = uniform_q ? token / uniform_q : upper_index(cu_q, count, token);
@@ -102,10 +100,6 @@ struct SharedSeqs {
     return s < groups ? prefix_pages + page0[s] : table + (s - groups) * stride;
   }
   CPKV_DEV int ragged() const { return groups; }
-  CPKV_DEV int64_t tiles_before(int s, int group) const {
-    if (s < groups) return (int64_t)cu_q[s] * group / 16 + s;
-    return (int64_t)(count - groups) * group / 16 + groups + (int64_t)(s - groups) * ((group + 15) / 16);
-  }
   CPKV_DEV int places(int token, int (&s)[2], int (&i)[2]) const {
     s[0] = groups + token;
     i[0] = 0;
@@ -242,7 +236,7 @@ CPKV_DEV void cp_async_wait() {
 }
 
 // ---------------------------------------------------------------------------
-// the split pass: parts of 16 packed rows over stretches of keys
+// the split pass: parts of sequences of at most 16 packed rows over stretches of keys
 // ---------------------------------------------------------------------------
 constexpr int kSplitRows = 16;
 constexpr int kSplitTile = 64;     // keys of a unit
@@ -251,7 +245,7 @@ constexpr int kSplitMaxGrid = 1024;
 // Workspace of a split pass over `count` sequences, in order: cum (units of a
 // head before each sequence and in all), then the slots' (m, l) pairs, then their values.
 // Slots: two per block (its first stretch, and its last when that is another
-// tile's), then one per tile for the tiles that one block holds whole.
+// sequence's), then one per key/value head and sequence for those that one block holds whole.
 struct SplitSpace {
   int32_t *cum;
   float *ml;  // [slot][16][2]
@@ -268,9 +262,7 @@ struct SplitParams {
   PagedPools pools;
   AttendIo io;
   SplitSpace space;
-  int64_t tiles_cap;  // tiles of all sequences per key/value head, at most
-  int row_tiles;      // of each sequence, when a block takes a whole tile
-  int direct;         // tiles that one block holds whole go straight to the output
+  int direct;  // sequences that one block holds whole go straight to the output
 };
 
 // Finds the parts of a row of a split pass.
@@ -278,7 +270,6 @@ template <typename S>
 struct SplitSource {
   S seqs;
   SplitSpace space;
-  int64_t tiles_cap;
   int direct;
 };
 

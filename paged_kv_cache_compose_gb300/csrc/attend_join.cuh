@@ -24,9 +24,9 @@ struct Spot {
 
 template <typename S>
 CPKV_DEV Spot find_spot(const SplitSource<S> &src, const AttendIo &io, int s, int i, int g) {
-  const int nq = src.seqs.q_count(s), row = i * (int)io.group.d + g;
+  const int nq = src.seqs.q_count(s);
   const KeyRange keys = key_range<kSplitTile>(src.seqs.kv_len(s), nq, 0, nq, src.seqs.causal, src.seqs.window, src.seqs.sinks);
-  return Spot{s, row / kSplitRows, row % kSplitRows, keys.n_tiles};
+  return Spot{s, 0, i * (int)io.group.d + g, keys.n_tiles};
 }
 
 template <typename S>
@@ -44,16 +44,16 @@ CPKV_DEV bool find_parts(Parts *r, const SplitSource<S> &src, const AttendIo &io
   r->count = 0;
   if (at.n_tiles == 0) return true;
   const int chunk = split_chunk(src.space.cum[src.seqs.count], src.space.grid / io.kv_heads);
-  const int begin = src.space.cum[at.s] + at.rt * at.n_tiles, end = begin + at.n_tiles;
+  const int begin = src.space.cum[at.s], end = begin + at.n_tiles;
   const int c0 = begin / chunk, c1 = (end - 1) / chunk;
   r->count = c1 - c0 + 1;
   if (c0 == c1) {
     if (src.direct) return false;
-    const int64_t slot = 2 * (int64_t)src.space.grid + h * src.tiles_cap + src.seqs.tiles_before(at.s, io.group.d) + at.rt;
+    const int64_t slot = 2 * (int64_t)src.space.grid + (int64_t)h * src.seqs.count + at.s;
     r->first = slot * kSplitRows + at.in_tile;
     return true;
   }
-  // the tile's stretch is the last of cut c0 unless it begins there, and the first of the others
+  // the sequence's stretch is the last of cut c0 unless it begins there, and the first of the others
   const int64_t slot = 2 * ((int64_t)c0 * io.kv_heads + h);
   r->first = (slot + (begin == c0 * chunk ? 0 : 1)) * kSplitRows + at.in_tile;
   r->step = 2 * (int64_t)io.kv_heads * kSplitRows;

@@ -1,11 +1,11 @@
-// Attention of few query rows over long paged keys: the keys are cut into
+// Attention of few query rows (at most 16 packed ones a sequence) over long paged keys: the keys are cut into
 // stretches, each block reduces its stretch to (m, l, o), and a second kernel
 // joins the parts of each row.
 //
 // Bytes bound it: 16 packed rows do 4 D * 16 operations on the 4 D bytes of a
 // key and its value, far below what the matrix instructions give, so what
-// counts is bytes in flight.  Work is counted in units of 64 keys of one tile
-// (sequence, 16 rows); all units of a key/value head form one line that is cut
+// counts is bytes in flight.  Work is counted in units of 64 keys of one
+// sequence; all units of a key/value head form one line that is cut
 // evenly over the head's blocks, whatever the lengths are, and a block's warps each
 // own 16 keys of every unit with a cp.async ring of their own, so that no block-wide
 // barrier stands inside a stretch.  The lines of all heads are cut alike and
@@ -16,7 +16,7 @@
 // and as many blocks as registers allow take 100 us, four stages and three blocks 106.
 // With rows that make room in L2 first and the join's set-up beside this pass the
 // same step takes 88 us, 5.9 TB/s and 89% of the measured copy rate.  Where every
-// sequence has few keys a block takes one whole tile instead and nothing is left to join.
+// sequence has few keys a block takes one whole sequence instead and nothing is left to join.
 #pragma once
 
 #include "attend.cuh"
@@ -26,10 +26,10 @@ namespace cpkv {
 constexpr int kSplitWarps = 4;
 constexpr int kWarpKeys = kSplitTile / kSplitWarps;  // 16
 
-// How a block finds its work: a stretch of the line of units, or one tile of few keys
+// How a block finds its work: a stretch of the line of units, or one sequence of few keys
 // (with a deeper ring: its time is that of a few loads).
 enum SplitMode { kLine, kFewKeys };
-constexpr int kWholeUnits = 8;  // most units of a tile of few keys
+constexpr int kWholeUnits = 8;  // most units of a sequence of few keys
 
 template <int D, SplitMode kMode>
 struct SplitShape {
@@ -38,14 +38,14 @@ struct SplitShape {
   static constexpr int kStages = kMode == kFewKeys ? 5 : 2;
   static constexpr int kBlocks = kMode == kFewKeys ? 1 : D == 128 ? 3 : 5;  // blocks to an SM
   static constexpr int kRing = kSplitWarps * kStages * kStage;
-  static constexpr int kJoin = kSplitRows * D * 4;         // half the columns of two warps while a tile's parts are joined
+  static constexpr int kJoin = kSplitRows * D * 4;         // half the columns of two warps while a sequence's parts are joined
   static constexpr int kSmem = kRing + kJoin + kSplitWarps * kSplitRows * 8;
 };
 
 // A position on the line of units.
 template <typename P>
 struct Cursor {
-  int s, rt, j, row_tiles;
+  int s, j, units;
   int nq, kv;
   KeyRange keys;
 
@@ -54,23 +54,19 @@ struct Cursor {
     nq = p.seqs.q_count(s);
     kv = p.seqs.kv_len(s);
     keys = key_range<kSplitTile>(kv, nq, 0, nq, p.seqs.causal, p.seqs.window, p.seqs.sinks);
-    row_tiles = (nq * (int)p.io.group.d + kSplitRows - 1) / kSplitRows;
+    units = nq > 0 ? keys.n_tiles : 0;
   }
   CPKV_DEV void seek(const P &p, const int *cum, int u) {
     enter(p, upper_index(cum, p.seqs.count, u));
-    const int local = u - cum[s];
-    rt = local / keys.n_tiles;
-    j = local - rt * keys.n_tiles;
+    j = u - cum[s];
   }
   // To the next unit of the line; there must be one.
   CPKV_DEV void advance(const P &p) {
-    if (++j < keys.n_tiles) return;
+    if (++j < units) return;
     j = 0;
-    if (++rt < row_tiles) return;
-    rt = 0;
     do {
       enter(p, s + 1);
-    } while (keys.n_tiles == 0 || row_tiles == 0);
+    } while (units == 0);
   }
 };
 
@@ -91,11 +87,9 @@ __global__ void __launch_bounds__(kSplitWarps * 32, SplitShape<D, kMode>::kBlock
   Cursor<P> ld;
   int u0, u1;
   if constexpr (kWhole) {
-    const int tile = (int)blockIdx.x / p.io.kv_heads;
-    ld.enter(p, tile / p.row_tiles);
-    ld.rt = tile % p.row_tiles;
+    ld.enter(p, (int)blockIdx.x / p.io.kv_heads);
     ld.j = 0;
-    if (head == 0 && ld.rt == 0 && threadIdx.x == 0 && p.seqs.kv_len_bad(ld.s))
+    if (head == 0 && threadIdx.x == 0 && p.seqs.kv_len_bad(ld.s))
       raise_status(p.seqs.status, CPKV_STATUS_OUT_CAPACITY);
     u0 = 0;
     u1 = ld.keys.n_tiles;
@@ -108,7 +102,7 @@ __global__ void __launch_bounds__(kSplitWarps * 32, SplitShape<D, kMode>::kBlock
       if (s < count) {
         Cursor<P> c;
         c.enter(p, s);
-        mine = c.keys.n_tiles * c.row_tiles;
+        mine = c.units;
         if (blockIdx.x == 0 && p.seqs.kv_len_bad(s)) raise_status(p.seqs.status, CPKV_STATUS_OUT_CAPACITY);
       }
       int part;
@@ -137,8 +131,8 @@ __global__ void __launch_bounds__(kSplitWarps * 32, SplitShape<D, kMode>::kBlock
   float *join = reinterpret_cast<float *>(smem + Shape::kRing);
   float2 *ml = reinterpret_cast<float2 *>(smem + Shape::kRing + Shape::kJoin);
 
-  // loads: lanes 0..15 own one key each.  A row is read once by its head's one tile of
-  // rows (or few): it makes room in L2 before the parts do.
+  // loads: lanes 0..15 own one key each.  A row is read once, by its head's packed
+  // rows: it makes room in L2 before the parts do.
   const uint64_t once = l2_policy_evict_first();
   Cursor<P> at = ld;
   int ld_u = u0, ld_key = 0, ld_page = -1;
@@ -152,7 +146,7 @@ __global__ void __launch_bounds__(kSplitWarps * 32, SplitShape<D, kMode>::kBlock
       ld_page = ld_sees ? p.seqs.pages(ld.s)[div_by(ld_key, p.pools.page_size)] : -1;
     }
   };
-  if constexpr (kWhole) {  // all page ids of the tile at once: one latency, not one per unit
+  if constexpr (kWhole) {  // all page ids of the sequence at once: one latency, not one per unit
 #pragma unroll
     for (int i = 0; i < kWholeUnits; i += 2) {
       const int j = i + (lane >> 4), key = ld.keys.tile_start(j, kSplitTile) + warp * kWarpKeys + (lane & 15);
@@ -202,22 +196,18 @@ __global__ void __launch_bounds__(kSplitWarps * 32, SplitShape<D, kMode>::kBlock
   uint32_t qf[D / 16][4];
   float o[D / 8][4], m[2], l[2];
   RowMask mask[2];
-  int full_lo = 0, full_hi = 0;  // keys in [full_lo, full_hi) are seen by every row of the tile
+  int full_lo = 0, full_hi = 0;  // keys in [full_lo, full_hi) are seen by every row
 
-  // A tile's rows from here on.
-  auto begin_tile = [&] {
+  // A sequence's rows from here on.
+  auto begin_rows = [&] {
     seg_j0 = at.j;
     const int group = p.io.group.d, rows = at.nq * group;
     const int q0 = p.seqs.q_begin(at.s);
-    int last = at.rt * kSplitRows + kSplitRows - 1;
-    if (last >= rows) last = rows - 1;
-    const RowMask ma = row_mask(at.kv, at.nq, div_by(at.rt * kSplitRows, p.io.group), p.seqs.causal, p.seqs.window, p.seqs.sinks);
-    const RowMask mb = row_mask(at.kv, at.nq, div_by(last, p.io.group), p.seqs.causal, p.seqs.window, p.seqs.sinks);
-    full_hi = ma.hi;
-    full_lo = mb.lo;
+    full_hi = row_mask(at.kv, at.nq, 0, p.seqs.causal, p.seqs.window, p.seqs.sinks).hi;
+    full_lo = row_mask(at.kv, at.nq, at.nq - 1, p.seqs.causal, p.seqs.window, p.seqs.sinks).lo;
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
-      const int row = at.rt * kSplitRows + (lane >> 2) + 8 * r;
+      const int row = (lane >> 2) + 8 * r;
       const bool in = row < rows;
       const int i = div_by(row, p.io.group), g = row - i * group;
       mask[r] = row_mask(at.kv, at.nq, i, p.seqs.causal, p.seqs.window, p.seqs.sinks);
@@ -235,8 +225,8 @@ __global__ void __launch_bounds__(kSplitWarps * 32, SplitShape<D, kMode>::kBlock
 #pragma unroll
       for (int i = 0; i < 4; ++i) o[n][i] = 0.f;
   };
-  // The end of a tile or of this block's stretch of it: `complete` when the block held it whole.
-  auto end_tile = [&](bool complete) {
+  // The end of a sequence or of this block's stretch of it: `complete` when the block held it whole.
+  auto end_rows = [&](bool complete) {
     // join the four warps' parts: common maximum, then values pairwise
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
@@ -295,11 +285,11 @@ __global__ void __launch_bounds__(kSplitWarps * 32, SplitShape<D, kMode>::kBlock
     }
     if (warp == 0) {
       const int group = p.io.group.d, rows = at.nq * group;
-      const int64_t slot = complete ? 2 * (int64_t)gridDim.x + head * p.tiles_cap + p.seqs.tiles_before(at.s, group) + at.rt
+      const int64_t slot = complete ? 2 * (int64_t)gridDim.x + (int64_t)head * p.seqs.count + at.s
                                     : 2 * (int64_t)blockIdx.x + (first_segment ? 0 : 1);
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
-        const int in_tile = (lane >> 2) + 8 * r, row = at.rt * kSplitRows + in_tile;
+        const int row = (lane >> 2) + 8 * r;
         if (row >= rows) continue;
         if (complete && p.direct) {
           const int i = div_by(row, p.io.group), g = row - i * group;
@@ -313,21 +303,21 @@ __global__ void __launch_bounds__(kSplitWarps * 32, SplitShape<D, kMode>::kBlock
           if (p.io.lse != nullptr && (lane & 3) == 0)
             p.io.lse[token * p.io.q_heads + q_head] = row_lse(big[r], sum[r]);
         } else {
-          float *dst = p.space.o + (slot * kSplitRows + in_tile) * D + (lane & 3) * 2;
+          float *dst = p.space.o + (slot * kSplitRows + row) * D + (lane & 3) * 2;
 #pragma unroll
           for (int n = 0; n < D / 8; ++n) *reinterpret_cast<float2 *>(dst + n * 8) = make_float2(o[n][2 * r], o[n][2 * r + 1]);
           if ((lane & 3) == 0)
-            *reinterpret_cast<float2 *>(p.space.ml + (slot * kSplitRows + in_tile) * 2) = make_float2(big[r], sum[r]);
+            *reinterpret_cast<float2 *>(p.space.ml + (slot * kSplitRows + row) * 2) = make_float2(big[r], sum[r]);
         }
       }
     }
   };
 
-  if constexpr (kWhole) begin_tile();
+  if constexpr (kWhole) begin_rows();
   for (int u = u0; u < u1; ++u) {
     if (!kWhole && fresh) {
       fresh = false;
-      begin_tile();
+      begin_rows();
     }
     cp_async_wait<Shape::kStages - 2>();
     __syncwarp();
@@ -423,19 +413,19 @@ __global__ void __launch_bounds__(kSplitWarps * 32, SplitShape<D, kMode>::kBlock
     __syncwarp();
     stage = stage + 1 == Shape::kStages ? 0 : stage + 1;
 
-    const bool tile_ends = at.j + 1 == at.keys.n_tiles;
-    if (kWhole || (!tile_ends && u + 1 < u1)) {
+    const bool keys_end = at.j + 1 == at.units;
+    if (kWhole || (!keys_end && u + 1 < u1)) {
       ++at.j;
       continue;
     }
-    end_tile(tile_ends && seg_j0 == 0);
+    end_rows(keys_end && seg_j0 == 0);
 
     first_segment = false;
     fresh = true;
     if (u + 1 < u1) at.advance(p);
   }
   cp_async_wait<0>();
-  if constexpr (kWhole) end_tile(true);
+  if constexpr (kWhole) end_rows(true);
 }
 
 }  // namespace cpkv
