@@ -17,8 +17,9 @@
 //                      then values (weights in tensor memory), tile by tile.
 //   warp 13            finds the next item while this one runs: the grid has a block
 //                      for every item, and a running block claims blocks that have not
-//                      started (cluster launch control), so long items go first and no
-//                      SM waits for another.
+//                      started (cluster launch control), a request's later rows, which
+//                      see more keys, before its earlier ones, so that no SM waits for
+//                      another.  Requests go by number, whatever their lengths.
 //   warps 14, 15       the next item's queries: two blocks of 128 rows, of which an item
 //                      of at most 128 rows takes one, the items in turn.
 // Of an item with at most 128 rows the two tiles are the same rows over every other
@@ -28,7 +29,7 @@
 // than 2^8 since the last time: weights stay below 2^8 (times kLift's factor), and the
 // sum and the output carry the same factor, which cancels at the end.
 // Measured: 44600 tokens of 12 requests, 32 heads of 128 on 8, a window of 4096 and 64
-// sinks behind prefixes of up to 16384, take 2.13 ms: 1.40 PFLOP/s on the visible keys,
+// sinks behind prefixes of up to 16384, take 2.12 ms: 1.41 PFLOP/s on the visible keys,
 // 74% of the measured bf16 rate of plain products (the tensor pipe is busy 61% of the
 // cycles of a causal prefill of 2 x 4096, whose diagonals it multiplies in full).  One
 // decode step of 256 requests on a prefix of 65536: 0.55 ms, 1.02 PFLOP/s.
@@ -138,8 +139,8 @@ __device__ const uint4 zero_row[16] = {};  // a key or value vector of zeros
 // undefined.
 // The usual way through is one instruction and one branch: the products' warp does
 // nine waits per 128 keys, and its own pace is close to the tensor core's.  A branch on
-// the result in its loop cost 1.6% of a prefill, and so did a deadline that a loading
-// warp moves on every 64 tiles: the warp that finds the items keeps it.
+// the result in its loop cost 1.6% of a prefill, a deadline that a loading warp moves on
+// every 64 tiles 2.7%: the warp that finds the items keeps it.
 template <bool kTest, bool kStops>
 CPKV_DEV bool tile_wait(TileBars *b, uint64_t *bar, uint32_t parity, int32_t *status) {
   constexpr uint32_t kPark = kTest ? 0 : kTileParkNs;
