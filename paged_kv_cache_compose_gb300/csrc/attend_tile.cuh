@@ -30,7 +30,7 @@
 // sum and the output carry the same factor, which cancels at the end.
 // Measured: 44600 tokens of 12 requests, 32 heads of 128 on 8, a window of 4096 and 64
 // sinks behind prefixes of up to 16384, take 2.12 ms: 1.41 PFLOP/s on the visible keys,
-// 74% of the measured bf16 rate of plain products (the tensor pipe is busy 61% of the
+// 74% of the measured bf16 rate of plain products (the tensor pipe is busy 60% of the
 // cycles of a causal prefill of 2 x 4096, whose diagonals it multiplies in full).  One
 // decode step of 256 requests on a prefix of 65536: 0.55 ms, 1.02 PFLOP/s.
 // With the products issued by one lane of a diverged warp, or operands worked out by
