@@ -708,6 +708,10 @@ int cpkv_selftest_attend_timeout(int head_dim, int n_tokens, int n_pages, const 
                                  const int32_t *d_page_table, const int32_t *d_kv_len, const void *d_q, void *d_out,
                                  int64_t wait_ns, int32_t *d_status, cpkv_stream_t stream);
 
+/* Whether work put on the stream goes into a CUDA graph that is being captured
+ * (*h_capturing 1 or 0).  Errors: ARG, CUDA. */
+int cpkv_stream_is_capturing(cpkv_stream_t stream, int *h_capturing);
+
 /* Human-readable name of a return code. */
 const char *cpkv_error_string(int code);
 

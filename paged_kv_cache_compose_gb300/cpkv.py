@@ -66,7 +66,7 @@ EXPORTED = (
     "cpkv_compose_fused", "cpkv_compose_fused_planes", "cpkv_selftest_ring_timeout", "cpkv_ragged_plan_sizes",
     "cpkv_ragged_plan_build", "cpkv_append_rotary", "cpkv_attend_window",
     "cpkv_attend_window_workspace_bytes", "cpkv_attend_shared", "cpkv_attend_shared_workspace_bytes",
-    "cpkv_selftest_attend_timeout", "cpkv_error_string", "cpkv_version",
+    "cpkv_selftest_attend_timeout", "cpkv_stream_is_capturing", "cpkv_error_string", "cpkv_version",
 )
 
 
@@ -115,6 +115,7 @@ def _declare(lib):
                                                              _P, _P, _L, _I, _P, _P]
     lib.cpkv_attend_shared_workspace_bytes.argtypes = [_I] * 5 + [_P, _P, _L, _P]
     lib.cpkv_selftest_attend_timeout.argtypes = [_I] * 3 + [_P] * 5 + [_L, _P, _P]
+    lib.cpkv_stream_is_capturing.argtypes = [_P, _P]
     for name in EXPORTED:
         getattr(lib, name).restype = _I
     lib.cpkv_error_string.argtypes = [_I]

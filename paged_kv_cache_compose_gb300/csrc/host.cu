@@ -161,6 +161,17 @@ extern "C" int cpkv_ragged_plan_sizes(int B, int chunk, const int32_t *h_q_lens,
   return CPKV_OK;
 }
 
+extern "C" int cpkv_stream_is_capturing(cpkv_stream_t stream, int *h_capturing) {
+  if (h_capturing == nullptr) return CPKV_ERR_ARG;
+  cudaStreamCaptureStatus status;
+  if (cudaStreamIsCapturing((cudaStream_t)stream, &status) != cudaSuccess) {
+    (void)cudaGetLastError();
+    return CPKV_ERR_CUDA;
+  }
+  *h_capturing = status != cudaStreamCaptureStatusNone;
+  return CPKV_OK;
+}
+
 extern "C" const char *cpkv_error_string(int code) {
   switch (code) {
     case CPKV_OK: return "CPKV_OK";

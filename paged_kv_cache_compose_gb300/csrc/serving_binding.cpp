@@ -317,6 +317,18 @@ PyObject *attend_shared(PyObject *, PyObject *const *a, Py_ssize_t n) {
   });
 }
 
+// (stream) -> whether calls on it go into a CUDA graph; not where that cannot be told (the
+// default stream beside a capture).
+PyObject *captures(PyObject *, PyObject *stream) {
+  int yes = 0;
+  try {
+    if (cpkv_stream_is_capturing(stream_of(stream), &yes) != CPKV_OK) yes = 0;
+  } catch (const Failed &) {
+    return nullptr;
+  }
+  return PyBool_FromLong(yes);
+}
+
 // The function (name, what is wanted) that makes an exception.
 PyObject *set_fail(PyObject *, PyObject *f) {
   Py_INCREF(f);
@@ -332,6 +344,7 @@ PyCFunction as_method(F *f) {
 PyMethodDef methods[] = {{"append_rotary", as_method(append_rotary), METH_FASTCALL, nullptr},
                          {"attend_window", as_method(attend_window), METH_FASTCALL, nullptr},
                          {"attend_shared", as_method(attend_shared), METH_FASTCALL, nullptr},
+                         {"captures", captures, METH_O, nullptr},
                          {"set_fail", set_fail, METH_O, nullptr},
                          {nullptr, nullptr, 0, nullptr}};
 

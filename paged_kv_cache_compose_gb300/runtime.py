@@ -215,8 +215,6 @@ class PagedCache:
         self._native = cpkv.serving()
         # the current stream's handle: torch's own accessor where it has one (a twentieth of current_stream())
         self._current = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-        self._current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
-        self._current_captures = getattr(torch._C, "_cuda_isCurrentStreamCapturing", torch.cuda.is_current_stream_capturing)
 
     def _stream(self, stream) -> int:
         if stream is not None:
@@ -225,19 +223,12 @@ class PagedCache:
             return self._current(self.device.index)
         return torch.cuda.current_stream(self.device).cuda_stream
 
-    def _capturing(self, stream: int, is_current: bool) -> bool:
-        """Whether calls on the stream go into a CUDA graph."""
-        if is_current and self._current_device() == self.device.index:
-            return self._current_captures()
-        with torch.cuda.stream(torch.cuda.ExternalStream(stream, device=self.device)):
-            return self._current_captures()
-
-    def _attend(self, fn: str, args: tuple, stream: int, is_current: bool, workspace, size):
+    def _attend(self, fn: str, args: tuple, stream: int, workspace, size):
         """Runs a call of the library, with a larger workspace where it wants one: ``size(args)`` bytes."""
         native = getattr(self._native, fn)
         mine, captured = workspace is None, False
         if mine:
-            captured = self._capturing(stream, is_current)
+            captured = self._native.captures(stream)
             if not captured:
                 workspace = self._workspaces.get((self.device.index, stream))
         rc = native(*args, workspace, self.d_status, stream)
@@ -287,12 +278,12 @@ class PagedCache:
         (None: one each) over its ``kv_lens[b]`` rows, those within ``window``
         and the first ``sinks``.  Returns ``out``; ``lse`` (float32 [tokens,
         heads]) is written when given."""
-        is_current, stream = stream is None, self._stream(stream)
+        stream = self._stream(stream)
         out = self._results(q, out, stream)
         if scale is None:
             scale = self._scale
         self._attend("attend_window", (self.table.native, self.kv_heads, q, q_lens, page_table, kv_lens, max_kv_len, window, sinks,
-                                       scale, out, lse), stream, is_current, workspace, _window_bytes)
+                                       scale, out, lse), stream, workspace, _window_bytes)
         return out
 
     def attend_shared(self, q, group_sizes, prefix_lens, prefix_pages, page_table, suffix_lens, *,
@@ -301,12 +292,12 @@ class PagedCache:
         heads, dim] over each group's shared prefix (``prefix_pages``, CSR by
         group) and each request's own ``suffix_lens[b]`` rows.  Returns
         ``out``; ``lse`` as in ``attend_window``."""
-        is_current, stream = stream is None, self._stream(stream)
+        stream = self._stream(stream)
         out = self._results(q, out, stream)
         if scale is None:
             scale = self._scale
         self._attend("attend_shared", (self.table.native, self.kv_heads, q, group_sizes, prefix_lens, prefix_pages, page_table,
-                                       suffix_lens, max_suffix_len, scale, out, lse), stream, is_current, workspace, _shared_bytes)
+                                       suffix_lens, max_suffix_len, scale, out, lse), stream, workspace, _shared_bytes)
         return out
 
 

@@ -136,6 +136,9 @@ class Recorder:
         self.native, self.spans = native, []
 
     def __getattr__(self, name):
+        if name == "captures":
+            return self.native.captures
+
         def call(*args):
             rc = getattr(self.native, name)(*args)
             if rc == 0 and args[12] is not None:
@@ -164,17 +167,18 @@ def decode_batch(seed=0):
     return cache, step, d_q, outs, want
 
 
-def test_captured_calls_have_workspaces_of_their_own():
+@pytest.mark.parametrize("explicit", [False, True])
+def test_captured_calls_have_workspaces_of_their_own(explicit):
     """Two graphs captured on one stream, and an eager call there, take memory apart from each other."""
     cache, step, q, outs, want = decode_batch()
     cache._native = recorder = Recorder(cache._native)
     stream = torch.cuda.Stream()
-    graphs = [torch.cuda.CUDAGraph() for _ in range(2)]
+    graphs, more = [torch.cuda.CUDAGraph() for _ in range(2)], dict(stream=stream) if explicit else {}
     with torch.cuda.stream(stream):
         step(q[2], *outs[2])
     for graph, x, out in zip(graphs, q, outs):
         with torch.cuda.graph(graph, stream=stream):
-            step(x, *out)
+            step(x, *out, **more)
     with torch.cuda.stream(stream):
         step(q[2], *outs[2])
     torch.cuda.synchronize()

@@ -20,3 +20,11 @@ def test_tables_that_are_no_addresses(native, call):
         getattr(native, call)(0, *[None] * 14)
     with pytest.raises(TypeError):
         getattr(native, call)(0)
+
+
+def test_capture_status_of_streams(native):
+    """No GPU, or the default stream: no capture; a stream that is no handle: an exception."""
+    assert native.captures(0) is False
+    with pytest.raises((TypeError, OverflowError)):
+        native.captures("stream")
+    assert cpkv.load().cpkv_stream_is_capturing(None, None) == cpkv.CPKV_ERR_ARG

@@ -15,8 +15,11 @@ NEED = 1000
 class Native:
     """A library whose attention wants NEED bytes; `during` runs inside its first call."""
 
-    def __init__(self, during=lambda: None):
-        self.rooms, self.during = [], during
+    def __init__(self, during=lambda: None, captured=False):
+        self.rooms, self.during, self.captured = [], during, captured
+
+    def captures(self, stream):
+        return self.captured
 
     def attend_window(self, *args):
         room = args[12]
@@ -34,7 +37,6 @@ def handle(monkeypatch):
     cache.table, cache.device, cache.d_status, cache._scale = types.SimpleNamespace(native=0), torch.device("cuda", 0), None, 1.0
     monkeypatch.setattr(PagedCache, "_workspaces", {})
     cache._stream = lambda stream: 7
-    cache._capturing = lambda stream, is_current: False
     cache._empty = lambda shape, dtype, stream: torch.empty(shape, dtype=dtype)
     monkeypatch.setattr(torch.cuda, "device", lambda d: contextlib.nullcontext())
     monkeypatch.setattr(runtime, "_window_bytes", lambda *args: NEED)
@@ -74,8 +76,7 @@ def test_a_capacity_that_no_workspace_mends(handle, monkeypatch):
 
 
 def test_captured_calls_keep_nothing(handle):
-    handle._native = Native()
-    handle._capturing = lambda stream, is_current: True
+    handle._native = Native(captured=True)
     attend(handle)
     attend(handle)
     assert not handle._workspaces and [r is None for r in handle._native.rooms] == [True, False, True, False]
