@@ -636,7 +636,7 @@ int cpkv_append_rotary(int64_t n_tokens, int page_size, int cp_size, int dtype, 
  *                  [0, max_kv_len] is clamped and raises OUT_CAPACITY.
  *   num_tokens     rows of d_q and d_out: the sum of the query lengths (ARG otherwise)
  *   d_q            [num_tokens][q_heads][head_dim], requests one after the other
- *   d_out          like d_q; d_lse: float [sum q_lens][q_heads], or NULL
+ *   d_out          like d_q, apart from it; d_lse: float [sum q_lens][q_heads], or NULL
  *   d_workspace    device, 16-byte aligned, at least
  *                  cpkv_attend_window_workspace_bytes; contents between calls are
  *                  irrelevant, calls that overlap on the GPU must not share one

@@ -427,3 +427,17 @@ def test_a_single_token_has_no_stride():
     assert odd.stride(0) == 132
     for call in calls.values():
         call(odd)
+
+
+@pytest.mark.parametrize("q_lens, heads", [([1, 1], 4), ([1] * 60, 4), ([2, 0, 3], 4), ([40, 300], 4)], ids=["few-keys", "line", "queries", "tile"])
+def test_requests_without_any_keys(q_lens, heads):
+    """No request has a key, nor the table a page: zeros and -infinity."""
+    hkv, d = 4, 64
+    cache = PagedCache([torch.ones(4, 16, 2 * hkv * d, dtype=BF16, device="cuda")], page_size=16, kv_heads=hkv, key_dim=d)
+    q = torch.ones(sum(q_lens), heads, d, dtype=BF16, device="cuda")
+    lse = torch.zeros(q.shape[:2], device="cuda")
+    for pages, most in ((0, 0), (1, 16)):
+        out = cache.attend_window(q, q_lens, torch.full((len(q_lens), pages), -7, dtype=torch.int32, device="cuda"),
+                                  torch.zeros(len(q_lens), dtype=torch.int32, device="cuda"), max_kv_len=most, lse=lse.zero_(), window=3, sinks=2)
+        torch.cuda.synchronize()
+        assert int(cache.d_status) == 0 and bool((out == 0).all()) and bool(torch.isneginf(lse).all())
