@@ -691,6 +691,67 @@ int cpkv_attend_shared_workspace_bytes(int B, int n_groups, int q_heads, int kv_
                                        const int32_t *h_group_sizes, const int32_t *h_prefix_lens,
                                        int64_t max_suffix_len, int64_t *h_bytes);
 
+/* ---------------------------------------------------------------------------
+ * The same on quantised rows: e4m3 values with float scales.
+ *
+ * A row keeps kv_heads key vectors and kv_heads value vectors of e4m3 elements (one byte
+ * each) and their scales: a float per key head, and a float for each 128 values (for a
+ * value head of 64, one), heads side by side.  An element stands for e4m3 * scale.  With
+ * keep_keys the key vectors stay in 16 bits, as the rotated part of latent rows does.
+ * The append writes as a group's scale the smallest power of two, at least 2^-126, with
+ * |x| <= 448 scale for all finite elements x of the group, and x / scale rounded once to
+ * e4m3 (to nearest, ties to even; an infinity or a NaN as e4m3's NaN).  The readers
+ * take any positive scale.
+ * ------------------------------------------------------------------------- */
+
+/* Where a quantised row keeps what, in bytes from its start. */
+typedef struct {
+  int64_t row_bytes;          /* a multiple of 16                                              */
+  int64_t key_offset;         /* [kv_heads][key_dim] e4m3, or 16-bit elements with keep_keys; a multiple of 16 */
+  int64_t value_offset;       /* [kv_heads][value_dim] e4m3; a multiple of 16                  */
+  int64_t key_scale_offset;   /* float [kv_heads]; a multiple of 4 (not looked at with keep_keys) */
+  int64_t value_scale_offset; /* float [kv_heads][value_dim / 128], at least one a head; a multiple of 4 */
+  int32_t kv_heads, key_dim, value_dim;
+  int32_t keep_keys;
+} cpkv_quantised_row;
+
+/*
+ * cpkv_append_quantised — cpkv_append_rotary into quantised rows.  The rotated key
+ * element x1 c - x2 s (x2 c + x1 s) is quantised from its exact value: neither the
+ * products nor their sum are rounded before.  Queries are rotated as there.
+ *   h_row          key_dim 64 or 128 (a multiple of 8 with keep_keys), value_dim 64 or a
+ *                  multiple of 128; keys that are kept are rounded to the element type
+ *   other arguments, status bits and errors: as cpkv_append_rotary (LIMIT: widths that
+ *   cannot be quantised; ARG: parts of a row that overlap or lie outside it).
+ * The latent rows of the fp8 batches (512 e4m3, 4 scales, 64 rotated 16-bit elements, 656 bytes) are
+ * kv_heads 1, value_dim 512 at 0, value scales at 512, keep_keys, key_dim = rot_dim = 64 at 528.
+ */
+int cpkv_append_quantised(int64_t n_tokens, int page_size, int cp_size, int dtype, int q_heads,
+                          const cpkv_quantised_row *h_row, void *const *h_pools, const int64_t *h_pool_cap_pages,
+                          const void *d_k, int64_t k_stride, const void *d_v, int64_t v_stride, const void *d_q,
+                          int64_t q_stride, void *d_q_out, int64_t q_out_stride, const int64_t *d_slots,
+                          const int32_t *d_positions, int64_t position_stride, int n_axes,
+                          const uint8_t *h_axis_of_freq, const float *d_cos_sin, int64_t max_position, int rot_dim,
+                          int flags, int32_t *d_status, cpkv_stream_t stream);
+
+/*
+ * cpkv_read_quantised — rows of quantised pools back into 16 bits: row n of d_k and
+ * d_v is cache row d_slots[n] (as in the append), element by element e4m3 * scale in 32
+ * bits, rounded once to the element type (in fp16 a magnitude past 65504 becomes
+ * 65504).  A negative slot gives a row of zeros; a slot may be named more than once.
+ *   n_rows         >= 0
+ *   d_slots        device int64 [n]
+ *   d_k, d_v       [n][kv_heads][key_dim], [n][kv_heads][value_dim] with strides in elements,
+ *                  multiples of 8; either may be NULL.  They must not overlap the pools.
+ *   flags          CPKV_DENSE_PAGES or 0
+ * Status bits: PAGE_OOB (a slot's page is outside the pools: a row of zeros).
+ * Errors: ARG, LIMIT, CUDA.
+ */
+int cpkv_read_quantised(int64_t n_rows, int page_size, int cp_size, int dtype, const cpkv_quantised_row *h_row,
+                        const void *const *h_pools, const int64_t *h_pool_cap_pages, const int64_t *d_slots,
+                        void *d_k, int64_t k_stride, void *d_v, int64_t v_stride, int flags, int32_t *d_status,
+                        cpkv_stream_t stream);
+
 /*
  * cpkv_selftest_attend_timeout — diagnostics: runs the attention's kernel for many query
  * rows on one request with waits that may take `wait_ns` only, whatever progress is

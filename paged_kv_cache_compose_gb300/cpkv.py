@@ -64,7 +64,7 @@ EXPORTED = (
     "cpkv_fill_current_planes",
     "cpkv_compose_gather", "cpkv_compose_gather_kinds", "cpkv_compose_layer", "cpkv_compose_layer_planes",
     "cpkv_compose_fused", "cpkv_compose_fused_planes", "cpkv_selftest_ring_timeout", "cpkv_ragged_plan_sizes",
-    "cpkv_ragged_plan_build", "cpkv_append_rotary", "cpkv_attend_window",
+    "cpkv_ragged_plan_build", "cpkv_append_rotary", "cpkv_append_quantised", "cpkv_read_quantised", "cpkv_attend_window",
     "cpkv_attend_window_workspace_bytes", "cpkv_attend_shared", "cpkv_attend_shared_workspace_bytes",
     "cpkv_selftest_attend_timeout", "cpkv_stream_is_capturing", "cpkv_error_string", "cpkv_version",
 )
@@ -108,6 +108,8 @@ def _declare(lib):
     lib.cpkv_ragged_plan_build.argtypes = [_I, _I, _I, _I, _P, _P, _P, _L, _P, _L] + [_P] * 7 + [_L, _P, _P, _P]
     lib.cpkv_append_rotary.argtypes = [_L] + [_I] * 7 + [_L] * 3 + [_P] * 2 + [_P, _L] * 4 + [
         _P, _P, _L, _I, _P, _P, _L, _I, _I, _P, _P]
+    lib.cpkv_append_quantised.argtypes = [_L] + [_I] * 4 + [_P] * 3 + [_P, _L] * 4 + [_P, _P, _L, _I, _P, _P, _L, _I, _I, _P, _P]
+    lib.cpkv_read_quantised.argtypes = [_L] + [_I] * 3 + [_P] * 4 + [_P, _L] * 2 + [_I, _P, _P]
     lib.cpkv_attend_window.argtypes = [_I] * 7 + [_L] * 3 + [_P, _L, _P, _P, _P, _L, _P, _L, _P, _L, _F, _I, _I, _P, _L,
                                                              _P, _P, _L, _I, _P, _P]
     lib.cpkv_attend_window_workspace_bytes.argtypes = [_I] * 4 + [_P, _L, _I, _I, _P]
@@ -460,7 +462,7 @@ def ragged_buffers(seg_cap: int, topk_cap: int, device="cuda") -> dict:
 class _Table(ctypes.Structure):
     """``Table`` of csrc/serving_binding.cpp."""
 
-    _fields_ = [("addresses", ctypes.c_uint64), ("caps", ctypes.c_uint64), ("row_bytes", _L), ("key_offset", _L),
+    _fields_ = [("addresses", ctypes.c_uint64), ("caps", ctypes.c_uint64), ("quantised", ctypes.c_uint64), ("row_bytes", _L), ("key_offset", _L),
                 ("value_offset", _L), ("page_size", ctypes.c_int32), ("cp_size", ctypes.c_int32),
                 ("code", ctypes.c_int32), ("flags", ctypes.c_int32), ("device", ctypes.c_int32)]
 
@@ -503,25 +505,74 @@ class PoolTable:
     def __init__(self, pools: Sequence, page_size: int, key_offset: int, value_offset: int, dense: bool = False):
         import torch
 
+        self._keep(pools, page_size)
+        self.dtype = self.pools[0].dtype
+        if self.dtype not in (torch.bfloat16, torch.float16):
+            raise CpkvError("PoolTable", CPKV_ERR_ARG, f"pools of {self.dtype}: bfloat16 or float16 is wanted")
+        self._describe(0, self.pools[0].shape[2] * 2, int(key_offset), int(value_offset), dense)
+
+    def _keep(self, pools, page_size) -> None:
         self.pools = list(pools)
         if not self.pools:
             raise CpkvError("PoolTable", CPKV_ERR_ARG, "no pools")
-        self.dtype, self.device = self.pools[0].dtype, self.pools[0].device
-        code = {torch.bfloat16: BF16, torch.float16: FP16}.get(self.dtype)
-        if code is None:
-            raise CpkvError("PoolTable", CPKV_ERR_ARG, f"pools of {self.dtype}: bfloat16 or float16 is wanted")
+        first = self.pools[0]
         for t in self.pools:
-            if t.dim() != 3 or t.shape[1] != page_size or t.shape[2] != self.pools[0].shape[2]:
+            if t.dim() != 3 or t.shape[1] != page_size or t.shape[2] != first.shape[2]:
                 raise CpkvError("PoolTable", CPKV_ERR_ARG, "a pool is [pages, page_size, width], widths alike")
-            if t.dtype != self.dtype or t.device != self.device:
+            if t.dtype != first.dtype or t.device != first.device:
                 raise CpkvError("PoolTable", CPKV_ERR_ARG, "pools of one type on one device are wanted")
+        self.device = first.device
         self._addresses = np.array([(_dp(t) or _P(0)).value or 0 for t in self.pools], np.uint64)
         self._caps = _host_i64([t.shape[0] for t in self.pools])
         self.page_size, self.cp_size = int(page_size), len(self.pools)
-        self._table = _Table(self._addresses.ctypes.data, self._caps.ctypes.data, self.pools[0].shape[2] * 2,
-                             int(key_offset), int(value_offset), self.page_size, self.cp_size, code,
-                             DENSE_PAGES if dense else 0, self.device.index)
+
+    def _describe(self, quantised: int, row_bytes: int, key_offset: int, value_offset: int, dense: bool) -> None:
+        import torch
+
+        code = {torch.bfloat16: BF16, torch.float16: FP16}[self.dtype]
+        self._table = _Table(self._addresses.ctypes.data, self._caps.ctypes.data, quantised, row_bytes, key_offset, value_offset,
+                             self.page_size, self.cp_size, code, DENSE_PAGES if dense else 0, self.device.index)
         self.native = ctypes.addressof(self._table)
+
+
+class QuantisedRow(ctypes.Structure):
+    """``cpkv_quantised_row`` of include/cpkv.h: where a quantised row keeps what (bytes)."""
+
+    _fields_ = [("row_bytes", _L), ("key_offset", _L), ("value_offset", _L), ("key_scale_offset", _L),
+                ("value_scale_offset", _L), ("kv_heads", ctypes.c_int32), ("key_dim", ctypes.c_int32),
+                ("value_dim", ctypes.c_int32), ("keep_keys", ctypes.c_int32)]
+
+    @classmethod
+    def of(cls, kv_heads: int, key_dim: int, value_dim: int | None = None, keep_keys: bool = False) -> "QuantisedRow":
+        """The usual layout: keys, values, key scales, value scales; with
+        ``keep_keys`` values, their scales, then the keys in 16 bits."""
+        value_dim = key_dim if value_dim is None else value_dim
+        keys, values, scales = kv_heads * key_dim, kv_heads * value_dim, 4 * kv_heads * max(1, value_dim // 128)
+        if keep_keys:
+            at = -(-(values + scales) // 16) * 16
+            return cls(-(-(at + 2 * keys) // 16) * 16, at, 0, 0, values, kv_heads, key_dim, value_dim, 1)
+        key_scales = -(-(keys + values) // 4) * 4
+        end = key_scales + 4 * kv_heads
+        return cls(-(-(end + scales) // 16) * 16, 0, -(-keys // 16) * 16, key_scales, end, kv_heads, key_dim, value_dim, 0)
+
+
+class QuantisedTable(PoolTable):
+    """The owner pools of a quantised cache: contiguous uint8 CUDA tensors
+    [pages, page_size, row bytes], rows as ``row`` says, read and written as
+    ``dtype`` (bf16 or fp16).  Rows may be longer than ``row`` needs."""
+
+    def __init__(self, pools: Sequence, page_size: int, row: QuantisedRow, dtype, dense: bool = False):
+        import torch
+
+        self._keep(pools, page_size)
+        if dtype not in (torch.bfloat16, torch.float16):
+            raise CpkvError("QuantisedTable", CPKV_ERR_ARG, f"elements of {dtype}: bfloat16 or float16 is wanted")
+        width = self.pools[0].shape[2]
+        if self.pools[0].dtype != torch.uint8 or width < row.row_bytes:
+            raise CpkvError("QuantisedTable", CPKV_ERR_ARG, f"uint8 pools with rows of at least {row.row_bytes} bytes are wanted")
+        self.dtype = dtype
+        self.row = QuantisedRow(width, *[getattr(row, name) for name, _ in QuantisedRow._fields_[1:]])
+        self._describe(ctypes.addressof(self.row), width, row.key_offset, row.value_offset, dense)
 
 
 def _handle(stream, table: PoolTable) -> int:
@@ -542,6 +593,19 @@ def cpkv_append_rotary(k, v, d_slots, d_positions, d_cos_sin, *, table: PoolTabl
     _check("cpkv_append_rotary", serving().append_rotary(
         table.native, k.shape[1], k.shape[2], v.shape[2], k, v, d_slots, d_positions, d_cos_sin, d_status, q, q_out,
         None if axis_of_freq is None else bytes(axis_of_freq), interleaved, _handle(stream, table)))
+
+
+def cpkv_append_quantised(k, v, d_slots, d_positions, d_cos_sin, *, table: QuantisedTable, d_status, q=None, q_out=None,
+                          axis_of_freq=None, interleaved=False, stream=None):
+    """``cpkv_append_rotary`` into quantised rows."""
+    _check("cpkv_append_quantised", serving().append_rotary(
+        table.native, k.shape[1], k.shape[2], v.shape[2], k, v, d_slots, d_positions, d_cos_sin, d_status, q, q_out,
+        None if axis_of_freq is None else bytes(axis_of_freq), interleaved, _handle(stream, table)))
+
+
+def cpkv_read_quantised(d_slots, k_out, v_out, *, table: QuantisedTable, d_status, stream=None):
+    """Quantised rows named by slot (negative: zeros) into 16-bit ``k_out`` and ``v_out``, either of them None."""
+    _check("cpkv_read_quantised", serving().read_rows(table.native, d_slots, k_out, v_out, d_status, _handle(stream, table)))
 
 
 def cpkv_attend_window_workspace_bytes(B, q_heads, kv_heads, head_dim, q_lens, max_kv_len, window=0, sinks=0) -> int:

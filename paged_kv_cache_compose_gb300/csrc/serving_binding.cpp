@@ -15,13 +15,15 @@
 
 namespace {
 
-// The pools as the binding's PoolTable describes them (the same fields there).
+// The pools as the binding's tables describe them (the same fields there).
 struct Table {
-  uint64_t addresses, caps;
+  uint64_t addresses, caps, quantised;
   int64_t row_bytes, key_offset, value_offset;
   int32_t page_size, cp_size, code, flags, device;
   void *const *pools() const { return reinterpret_cast<void *const *>(addresses); }
   const int64_t *cap_pages() const { return reinterpret_cast<const int64_t *>(caps); }
+  // Where a quantised row keeps what; null: rows of the element type.
+  const cpkv_quantised_row *row() const { return reinterpret_cast<const cpkv_quantised_row *>(quantised); }
 };
 
 PyObject *g_fail = nullptr;
@@ -57,7 +59,7 @@ struct Rows {
 };
 
 Rows rows(PyObject *o, const char *name, const Table &t) {
-  static const char *const what = "[tokens, heads, dim] of the pools' type on their device, a token's heads side by side";
+  static const char *const what = "[tokens, heads, dim] of the cache's type on the pools' device, a token's heads side by side";
   const at::Tensor &x = tensor(o, name, t, element(t), what);
   if (x.dim() != 3) fail(name, what);
   const auto size = x.sizes(), stride = x.strides();
@@ -256,6 +258,12 @@ PyObject *append_rotary(PyObject *, PyObject *const *a, Py_ssize_t n) {
     const int interleaved = PyObject_IsTrue(a[13]);
     if (interleaved < 0) throw Failed();
     const int flags = t.flags | (interleaved ? CPKV_ROTARY_INTERLEAVED : 0);
+    if (t.row() != nullptr)
+      return cpkv_append_quantised(k.n, t.page_size, t.cp_size, t.code, static_cast<int>(q.heads), t.row(), t.pools(), t.cap_pages(),
+                                   k.at, k.stride, v.at, v.stride, q.at, q.stride, q_out.at, q_out.stride, slots,
+                                   static_cast<const int32_t *>(pos.data_ptr()), between, static_cast<int>(axes), axis,
+                                   static_cast<const float *>(turns.data_ptr()), turns.size(0), static_cast<int>(turns.size(1)),
+                                   flags, status, stream_of(a[14]));
     return cpkv_append_rotary(k.n, t.page_size, t.cp_size, t.code, static_cast<int>(q.heads), static_cast<int>(k.heads),
                               static_cast<int>(k.dim), static_cast<int>(v.dim), t.row_bytes, t.key_offset, t.value_offset,
                               t.pools(), t.cap_pages(), k.at, k.stride, v.at, v.stride, q.at, q.stride, q_out.at, q_out.stride,
@@ -265,9 +273,30 @@ PyObject *append_rotary(PyObject *, PyObject *const *a, Py_ssize_t n) {
   });
 }
 
+// (table, slots, k_out, v_out, status, stream); either output may be None
+PyObject *read_rows(PyObject *, PyObject *const *a, Py_ssize_t n) {
+  return guarded(a, n, 6, [&](const Table &t) {
+    if (t.row() == nullptr) fail("table", "quantised rows");
+    int64_t count = 0;
+    const int64_t *slots = list<int64_t>(a[1], "slots", t, at::kLong, &count);
+    Rows k = {nullptr, 0, 0, 0, 0}, v = k;
+    if (a[2] != Py_None) {
+      k = rows(a[2], "k_out", t);
+      if (k.n != count || k.heads != t.row()->kv_heads || k.dim != t.row()->key_dim) fail("k_out", "[slots, kv_heads, key_dim] of the cache");
+    }
+    if (a[3] != Py_None) {
+      v = rows(a[3], "v_out", t);
+      if (v.n != count || v.heads != t.row()->kv_heads || v.dim != t.row()->value_dim) fail("v_out", "[slots, kv_heads, value_dim] of the cache");
+    }
+    return cpkv_read_quantised(count, t.page_size, t.cp_size, t.code, t.row(), t.pools(), t.cap_pages(), slots, k.at, k.stride, v.at,
+                               v.stride, t.flags, status_word(a[4], t), stream_of(a[5]));
+  });
+}
+
 // (table, kv_heads, q, q_lens, page_table, kv_lens, max_kv_len, window, sinks, scale, out, lse, workspace, status, stream)
 PyObject *attend_window(PyObject *, PyObject *const *a, Py_ssize_t n) {
   return guarded(a, n, 15, [&](const Table &t) {
+    if (t.row() != nullptr) fail("table", "rows of the element type");
     const Rows q = rows(a[2], "q", t), out = rows(a[10], "out", t);
     if (!q.same_shape(out)) fail("out", "q's shape");
     int64_t requests = 0, bytes = 0;
@@ -293,6 +322,7 @@ PyObject *attend_window(PyObject *, PyObject *const *a, Py_ssize_t n) {
 // (table, kv_heads, q, group_sizes, prefix_lens, prefix_pages, page_table, suffix_lens, max_suffix_len, scale, out, lse, workspace, status, stream)
 PyObject *attend_shared(PyObject *, PyObject *const *a, Py_ssize_t n) {
   return guarded(a, n, 15, [&](const Table &t) {
+    if (t.row() != nullptr) fail("table", "rows of the element type");
     const Rows q = rows(a[2], "q", t), out = rows(a[10], "out", t);
     if (!q.same_shape(out)) fail("out", "q's shape");
     int64_t requests = 0, prefix_pages = 0, bytes = 0;
@@ -342,6 +372,7 @@ PyCFunction as_method(F *f) {
 }
 
 PyMethodDef methods[] = {{"append_rotary", as_method(append_rotary), METH_FASTCALL, nullptr},
+                         {"read_rows", as_method(read_rows), METH_FASTCALL, nullptr},
                          {"attend_window", as_method(attend_window), METH_FASTCALL, nullptr},
                          {"attend_shared", as_method(attend_shared), METH_FASTCALL, nullptr},
                          {"captures", captures, METH_O, nullptr},

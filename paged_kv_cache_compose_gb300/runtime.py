@@ -5,7 +5,8 @@ arrays, and builds the plan once per batch (``cpkv_plan_build``).
 ``ComposeLayers`` owns the writers' staging regions and the dense buffers
 (two, alternated by layer parity: a dense buffer is reused two layers later)
 and runs the per-layer fill + gather.  ``PagedCache`` serves from the pools:
-rotated rows of new tokens into them, attention over them.  Allocation uses torch device memory;
+rotated rows of new tokens into them, attention over them; ``QuantisedCache``
+does so with rows of e4m3 values.  Allocation uses torch device memory;
 every computation is a library kernel.
 """
 from __future__ import annotations
@@ -208,7 +209,10 @@ class PagedCache:
         self.value_dim = self.key_dim if value_dim is None else int(value_dim)
         if value_offset is None:
             value_offset = key_offset + self.kv_heads * self.key_dim
-        self.table = cpkv.PoolTable(pools, page_size, 2 * key_offset, 2 * value_offset, dense)
+        self._open(cpkv.PoolTable(pools, page_size, 2 * key_offset, 2 * value_offset, dense))
+
+    def _open(self, table) -> None:
+        self.table = table
         self.device = self.table.device
         self.d_status = torch.zeros(1, dtype=torch.int32, device=self.device)
         self._scale = self.key_dim ** -0.5
@@ -299,6 +303,46 @@ class PagedCache:
         self._attend("attend_shared", (self.table.native, self.kv_heads, q, group_sizes, prefix_lens, prefix_pages, page_table,
                                        suffix_lens, max_suffix_len, scale, out, lse), stream, workspace, _shared_bytes)
         return out
+
+
+class QuantisedCache(PagedCache):
+    """Token rows in owner pools as e4m3 values with float scales, half the
+    bytes of a ``PagedCache``, written and attended to through the same calls.
+
+    ``pools``: the cp owner slabs [pages, page_size, row bytes] of uint8, rows
+    of ``QuantisedCache.row_bytes(...)`` bytes or more.  Heads of 64 or 128 have
+    a scale per token and head, wider values one per 128.  ``dtype`` (bf16 or
+    fp16) is the type of what goes in and comes out.  ``keep_keys``: the key
+    vectors stay in ``dtype`` (the rotated part of latent rows); such rows are
+    appended and read back, not attended to.  ``row``: another layout of the
+    row (``cpkv.QuantisedRow``)."""
+
+    def __init__(self, pools, *, page_size: int, kv_heads: int, key_dim: int, value_dim: int | None = None,
+                 dtype=torch.bfloat16, keep_keys: bool = False, row: cpkv.QuantisedRow | None = None, dense: bool = False):
+        if row is None:
+            row = cpkv.QuantisedRow.of(kv_heads, key_dim, value_dim, keep_keys)
+        elif (row.kv_heads, row.key_dim, bool(row.keep_keys)) != (kv_heads, key_dim, keep_keys) or value_dim not in (None, row.value_dim):
+            raise cpkv.CpkvError("QuantisedCache", cpkv.CPKV_ERR_ARG, "row: the heads and widths of the cache are wanted")
+        self.kv_heads, self.key_dim, self.value_dim = row.kv_heads, row.key_dim, row.value_dim
+        self._open(cpkv.QuantisedTable(pools, page_size, row, dtype, dense))
+
+    @staticmethod
+    def row_bytes(kv_heads: int, key_dim: int, value_dim: int | None = None, keep_keys: bool = False) -> int:
+        """Bytes of a row in the usual layout."""
+        return cpkv.QuantisedRow.of(kv_heads, key_dim, value_dim, keep_keys).row_bytes
+
+    def read_rows(self, slots, *, k_out=None, v_out=None, stream=None):
+        """Cache rows ``slots`` (as in ``append_rotary``; negative: zeros) back
+        in 16 bits: ``k_out`` [slots, kv_heads, key_dim] and ``v_out`` [slots,
+        kv_heads, value_dim], both allocated when both are None; one that is
+        None beside the other is not read.  Returns (k_out, v_out)."""
+        stream = self._stream(stream)
+        if k_out is None and v_out is None:
+            k_out, v_out = (self._empty((slots.shape[0], self.kv_heads, n), self.table.dtype, stream) for n in (self.key_dim, self.value_dim))
+        rc = self._native.read_rows(self.table.native, slots, k_out, v_out, self.d_status, stream)
+        if rc:
+            cpkv._check("cpkv_read_quantised", rc)
+        return k_out, v_out
 
 
 def _window_bytes(table, kv_heads, q, q_lens, page_table, kv_lens, max_kv_len, window, sinks, *rest) -> int:
