@@ -753,6 +753,33 @@ int cpkv_read_quantised(int64_t n_rows, int page_size, int cp_size, int dtype, c
                         cpkv_stream_t stream);
 
 /*
+ * cpkv_attend_window_quantised — cpkv_attend_window over quantised rows: k = e4m3 * key
+ * scale, v = e4m3 * value scale.  Beside 16 query rows per key/value head or fewer the
+ * products are of the e4m3 numbers themselves and the scales are applied in 32 bits; beside
+ * more, keys and values are brought to the element type first (e4m3 * scale rounded once: in bf16
+ * exact for the append's scales, in fp16 up to 65504, and in steps of 2^-24 below 2^-14).
+ *   h_row          quantised keys (no keep_keys), key_dim = value_dim (ARG otherwise)
+ *   other arguments, workspace, status bits and errors: as cpkv_attend_window
+ */
+int cpkv_attend_window_quantised(int B, int page_size, int cp_size, int dtype, int q_heads,
+                                 const cpkv_quantised_row *h_row, const int32_t *h_q_lens, int64_t max_kv_len,
+                                 const void *const *h_pools, const int64_t *h_pool_cap_pages,
+                                 const int32_t *d_page_table, int64_t table_stride, const int32_t *d_kv_lens,
+                                 int64_t num_tokens, const void *d_q, int64_t q_stride, float scale, int window,
+                                 int sinks, void *d_out, int64_t out_stride, float *d_lse, void *d_workspace,
+                                 int64_t workspace_bytes, int flags, int32_t *d_status, cpkv_stream_t stream);
+
+/* cpkv_attend_shared over quantised rows; h_row and rounding as cpkv_attend_window_quantised. */
+int cpkv_attend_shared_quantised(int B, int n_groups, int page_size, int cp_size, int dtype, int q_heads,
+                                 const cpkv_quantised_row *h_row, const int32_t *h_group_sizes,
+                                 const int32_t *h_prefix_lens, int64_t max_suffix_len, const void *const *h_pools,
+                                 const int64_t *h_pool_cap_pages, const int32_t *d_prefix_pages,
+                                 int64_t num_prefix_pages, const int32_t *d_page_table, int64_t table_stride,
+                                 const int32_t *d_suffix_lens, const void *d_q, int64_t q_stride, float scale,
+                                 void *d_out, int64_t out_stride, float *d_lse, void *d_workspace,
+                                 int64_t workspace_bytes, int flags, int32_t *d_status, cpkv_stream_t stream);
+
+/*
  * cpkv_selftest_attend_timeout — diagnostics: runs the attention's kernel for many query
  * rows on one request with waits that may take `wait_ns` only, whatever progress is
  * made, so that blocks give up in the middle of their work: copies and products in
@@ -768,6 +795,11 @@ int cpkv_read_quantised(int64_t n_rows, int page_size, int cp_size, int dtype, c
 int cpkv_selftest_attend_timeout(int head_dim, int n_tokens, int n_pages, const void *d_rows,
                                  const int32_t *d_page_table, const int32_t *d_kv_len, const void *d_q, void *d_out,
                                  int64_t wait_ns, int32_t *d_status, cpkv_stream_t stream);
+
+/* The same over quantised rows, d_rows [n_pages][64][2 * head_dim + 16] bytes: keys, values, their two scales. */
+int cpkv_selftest_attend_quantised_timeout(int head_dim, int n_tokens, int n_pages, const void *d_rows,
+                                           const int32_t *d_page_table, const int32_t *d_kv_len, const void *d_q,
+                                           void *d_out, int64_t wait_ns, int32_t *d_status, cpkv_stream_t stream);
 
 /* Whether work put on the stream goes into a CUDA graph that is being captured
  * (*h_capturing 1 or 0).  Errors: ARG, CUDA. */

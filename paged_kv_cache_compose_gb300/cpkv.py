@@ -66,7 +66,8 @@ EXPORTED = (
     "cpkv_compose_fused", "cpkv_compose_fused_planes", "cpkv_selftest_ring_timeout", "cpkv_ragged_plan_sizes",
     "cpkv_ragged_plan_build", "cpkv_append_rotary", "cpkv_append_quantised", "cpkv_read_quantised", "cpkv_attend_window",
     "cpkv_attend_window_workspace_bytes", "cpkv_attend_shared", "cpkv_attend_shared_workspace_bytes",
-    "cpkv_selftest_attend_timeout", "cpkv_stream_is_capturing", "cpkv_error_string", "cpkv_version",
+    "cpkv_attend_window_quantised", "cpkv_attend_shared_quantised",
+    "cpkv_selftest_attend_timeout", "cpkv_selftest_attend_quantised_timeout", "cpkv_stream_is_capturing", "cpkv_error_string", "cpkv_version",
 )
 
 
@@ -112,11 +113,14 @@ def _declare(lib):
     lib.cpkv_read_quantised.argtypes = [_L] + [_I] * 3 + [_P] * 4 + [_P, _L] * 2 + [_I, _P, _P]
     lib.cpkv_attend_window.argtypes = [_I] * 7 + [_L] * 3 + [_P, _L, _P, _P, _P, _L, _P, _L, _P, _L, _F, _I, _I, _P, _L,
                                                              _P, _P, _L, _I, _P, _P]
+    lib.cpkv_attend_window_quantised.argtypes = [_I] * 5 + [_P, _P, _L, _P, _P, _P, _L, _P, _L, _P, _L, _F, _I, _I, _P, _L, _P, _P, _L, _I, _P, _P]
+    lib.cpkv_attend_shared_quantised.argtypes = [_I] * 6 + [_P] * 3 + [_L, _P, _P, _P, _L, _P, _L, _P, _P, _L, _F, _P, _L, _P, _P, _L, _I, _P, _P]
     lib.cpkv_attend_window_workspace_bytes.argtypes = [_I] * 4 + [_P, _L, _I, _I, _P]
     lib.cpkv_attend_shared.argtypes = [_I] * 8 + [_L] * 3 + [_P, _P, _L, _P, _P, _P, _L, _P, _L, _P, _P, _L, _F, _P, _L,
                                                              _P, _P, _L, _I, _P, _P]
     lib.cpkv_attend_shared_workspace_bytes.argtypes = [_I] * 5 + [_P, _P, _L, _P]
     lib.cpkv_selftest_attend_timeout.argtypes = [_I] * 3 + [_P] * 5 + [_L, _P, _P]
+    lib.cpkv_selftest_attend_quantised_timeout.argtypes = [_I] * 3 + [_P] * 5 + [_L, _P, _P]
     lib.cpkv_stream_is_capturing.argtypes = [_P, _P]
     for name in EXPORTED:
         getattr(lib, name).restype = _I
@@ -645,9 +649,32 @@ def cpkv_attend_shared(q, group_sizes, prefix_lens, prefix_pages, page_table, d_
         scale, out, lse, workspace, d_status, _handle(stream, table)))
 
 
+def cpkv_attend_window_quantised(q, q_lens, page_table, d_kv_lens, *, table: QuantisedTable, max_kv_len, window, sinks, scale, out, lse,
+                                 workspace, d_status, stream=None):
+    """``cpkv_attend_window`` over quantised rows; the workspace is that call's."""
+    _check("cpkv_attend_window_quantised", serving().attend_window(
+        table.native, table.row.kv_heads, q, q_lens, page_table, d_kv_lens, max_kv_len, window, sinks, scale, out, lse, workspace,
+        d_status, _handle(stream, table)))
+
+
+def cpkv_attend_shared_quantised(q, group_sizes, prefix_lens, prefix_pages, page_table, d_suffix_lens, *, table: QuantisedTable,
+                                 max_suffix_len, scale, out, lse, workspace, d_status, stream=None):
+    """``cpkv_attend_shared`` over quantised rows; the workspace is that call's."""
+    _check("cpkv_attend_shared_quantised", serving().attend_shared(
+        table.native, table.row.kv_heads, q, group_sizes, prefix_lens, prefix_pages, page_table, d_suffix_lens, max_suffix_len,
+        scale, out, lse, workspace, d_status, _handle(stream, table)))
+
+
 def cpkv_selftest_attend_timeout(rows, page_table, d_kv_len, q, out, wait_ns, d_status, stream=None):
     """Diagnostics: the attention of ``q`` [tokens, head_dim] over ``rows`` [pages, 64, 2 * head_dim] with waits that run
     out after ``wait_ns`` (see include/cpkv.h)."""
     _check("cpkv_selftest_attend_timeout", load().cpkv_selftest_attend_timeout(
+        q.shape[1], q.shape[0], rows.shape[0], _dp(rows), _dp(page_table), _dp(d_kv_len), _dp(q), _dp(out), wait_ns, _dp(d_status),
+        _stream(stream)))
+
+
+def cpkv_selftest_attend_quantised_timeout(rows, page_table, d_kv_len, q, out, wait_ns, d_status, stream=None):
+    """The same over quantised ``rows`` [pages, 64, 2 * head_dim + 16] of uint8."""
+    _check("cpkv_selftest_attend_quantised_timeout", load().cpkv_selftest_attend_quantised_timeout(
         q.shape[1], q.shape[0], rows.shape[0], _dp(rows), _dp(page_table), _dp(d_kv_len), _dp(q), _dp(out), wait_ns, _dp(d_status),
         _stream(stream)))

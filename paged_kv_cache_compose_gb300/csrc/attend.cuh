@@ -184,7 +184,8 @@ struct AttendIo {
   int q_heads, kv_heads;
   FastDiv group;  // query heads per key/value head
   float scale_log2;
-  int64_t k_off, v_off;  // bytes of the keys and values in a row
+  int64_t k_off, v_off;    // bytes of the keys and values in a row
+  int64_t ks_off, vs_off;  // of quantised rows: of the scales
 };
 
 // ---------------------------------------------------------------------------

@@ -70,29 +70,17 @@ struct Cursor {
   }
 };
 
-template <typename T, int D, typename S, SplitMode kMode>
-__global__ void __launch_bounds__(kSplitWarps * 32, SplitShape<D, kMode>::kBlocks) attend_split_kernel(const __grid_constant__ SplitParams<S> p) {
-  using Shape = SplitShape<D, kMode>;
-  using P = SplitParams<S>;
-  constexpr bool kWhole = kMode != kLine;
-  extern __shared__ __align__(128) char smem[];
-  __shared__ int scan_scratch[33];
-  __shared__ int few_pages[kWhole ? kSplitWarps : 1][kWholeUnits][kWarpKeys];
-  int *cum = reinterpret_cast<int *>(smem + Shape::kSmem);
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+// This block's units [u0, u1) and a cursor at the first; false where there is none for it.
+template <SplitMode kMode, typename P>
+CPKV_DEV bool find_stretch(const P &p, int head, int *cum, int *scan_scratch, Cursor<P> *ld, int *u0, int *u1) {
   const int count = p.seqs.count;
-
-  release_dependents();  // the joining kernel, which waits for this one
-  const int head = (int)blockIdx.x % p.io.kv_heads;  // key/value head
-  Cursor<P> ld;
-  int u0, u1;
-  if constexpr (kWhole) {
-    ld.enter(p, (int)blockIdx.x / p.io.kv_heads);
-    ld.j = 0;
-    if (head == 0 && threadIdx.x == 0 && p.seqs.kv_len_bad(ld.s))
+  if constexpr (kMode != kLine) {
+    ld->enter(p, (int)blockIdx.x / p.io.kv_heads);
+    ld->j = 0;
+    if (head == 0 && threadIdx.x == 0 && p.seqs.kv_len_bad(ld->s))
       raise_status(p.seqs.status, CPKV_STATUS_OUT_CAPACITY);
-    u0 = 0;
-    u1 = ld.keys.n_tiles;
+    *u0 = 0;
+    *u1 = ld->keys.n_tiles;
   } else {
     // units before each sequence
     int total = 0;
@@ -119,12 +107,31 @@ __global__ void __launch_bounds__(kSplitWarps * 32, SplitShape<D, kMode>::kBlock
     const int64_t first = (int64_t)((int)blockIdx.x / p.io.kv_heads) * chunk;
     if (first >= total) {
       wait_prerequisite();
-      return;
+      return false;
     }
-    u0 = (int)first;
-    u1 = (int)min64(first + chunk, total);
-    ld.seek(p, cum, u0);
+    *u0 = (int)first;
+    *u1 = (int)min64(first + chunk, total);
+    ld->seek(p, cum, *u0);
   }
+  return true;
+}
+
+template <typename T, int D, typename S, SplitMode kMode>
+__global__ void __launch_bounds__(kSplitWarps * 32, SplitShape<D, kMode>::kBlocks) attend_split_kernel(const __grid_constant__ SplitParams<S> p) {
+  using Shape = SplitShape<D, kMode>;
+  using P = SplitParams<S>;
+  constexpr bool kWhole = kMode != kLine;
+  extern __shared__ __align__(128) char smem[];
+  __shared__ int scan_scratch[33];
+  __shared__ int few_pages[kWhole ? kSplitWarps : 1][kWholeUnits][kWarpKeys];
+  int *cum = reinterpret_cast<int *>(smem + Shape::kSmem);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+
+  release_dependents();  // the joining kernel, which waits for this one
+  const int head = (int)blockIdx.x % p.io.kv_heads;  // key/value head
+  Cursor<P> ld;
+  int u0, u1;
+  if (!find_stretch<kMode>(p, head, cum, scan_scratch, &ld, &u0, &u1)) return;
 
   char *ring = smem + warp * Shape::kStages * Shape::kStage;
   const uint32_t ring_addr = smem_addr(ring);

@@ -40,6 +40,7 @@
 #include <cuda.h>
 
 #include "attend.cuh"
+#include "quantised.cuh"
 #include "tcgen05.cuh"
 
 namespace cpkv {
@@ -51,6 +52,9 @@ constexpr int kTileThreads = 512;
 // Registers a thread: 512 threads are launched with 128 each, 65536 in all; the
 // softmax holds a row's 128 scores.  256 * 216 + 256 * 40 = 65536.
 constexpr int kSoftmaxRegisters = 216, kOtherRegisters = 40;
+// Over quantised rows the loading warps hold 8 vectors in flight and more: 256 * 200 +
+// 128 * 72 + 128 * 40 = 65536.
+constexpr int kSoftmaxRegistersQ = 200, kLoadRegistersQ = 72;
 constexpr int kItemSlots = 4;   // items known at a time: of small ones, some are loaded while others are finished
 constexpr int kClaimAhead = 12;  // key tiles before an item's last load at which the next item is claimed
 constexpr int kTileMaps = 8;  // most pools that TMA maps travel for
@@ -240,15 +244,33 @@ CPKV_DEV void add_scaled(float *o, float w, uint32_t v) {
 // Eight rows at a time over a warp's lanes took 2.1 us a key, but the kernel that called
 // it, without calling it, took 8% longer.
 constexpr int kMendKeys = 4;  // at a time
-template <typename T, int D, typename S>
+
+// A key's vectors in memory, 8 elements at a time.
+template <typename T, bool kQuantised>
+struct RowVector {
+  const char *at;  // zero_row for none
+  float scale;
+  CPKV_DEV uint4 operator[](int c) const {
+    if constexpr (kQuantised) return read_back8<T>(reinterpret_cast<const uint2 *>(at)[c], scale);
+    return reinterpret_cast<const uint4 *>(at)[c];
+  }
+};
+
+template <typename T, int D, typename S, bool kQuantised>
 __device__ __noinline__ void mend_row(const TileParams<S> &p, const TileItem &item, uint64_t *deadline, int token, int head, float base, float l,
                                       char *out, float *part) {
   const RowMask mask = row_mask(item.kv, item.nq, token, p.seqs.causal, p.seqs.window, p.seqs.sinks);
-  const int64_t k_at = p.io.k_off + (int64_t)item.h * D * 2, v_at = p.io.v_off + (int64_t)item.h * D * 2;
+  using Vector = RowVector<T, kQuantised>;
+  constexpr int kBytes = D * (kQuantised ? 1 : 2);  // of a vector
+  const int64_t k_at = p.io.k_off + (int64_t)item.h * kBytes, v_at = p.io.v_off + (int64_t)item.h * kBytes;
   auto row_of = [&](int key) -> const char * {
     const int page = div_by(key, p.pools.page_size);
     const char *const at = page_address(p.pools, item.pages[page]);
     return at == nullptr ? nullptr : at + (int64_t)(key - page * (int)p.pools.page_size.d) * p.pools.row_bytes;
+  };
+  auto scale_of = [&](const char *row, int64_t off) {
+    if constexpr (kQuantised) return *reinterpret_cast<const float *>(row + off + (int64_t)item.h * 4);
+    return 1.f;
   };
   uint4 marks = make_uint4(0, 0, 0, 0);
   for (int j = item.j0; j < item.j0 + item.n; ++j) {
@@ -258,8 +280,9 @@ __device__ __noinline__ void mend_row(const TileParams<S> &p, const TileItem &it
       if (mask.sees(key) || !item.there.any_sees(key)) continue;
       const char *const at = row_of(key);
       if (at == nullptr) continue;
+      const Vector v = {at + v_at, scale_of(at, p.io.vs_off)};
 #pragma unroll
-      for (int c = 0; c < D / 8; ++c) marks = mark_infinite<T>(reinterpret_cast<const uint4 *>(at + v_at)[c], marks);
+      for (int c = 0; c < D / 8; ++c) marks = mark_infinite<T>(v[c], marks);
     }
   }
   if ((marks.x | marks.y | marks.z | marks.w) == 0) return;  // its NaNs are its own
@@ -274,14 +297,15 @@ __device__ __noinline__ void mend_row(const TileParams<S> &p, const TileItem &it
       atomicMax(reinterpret_cast<unsigned long long *>(deadline), (unsigned long long)(global_timer_ns() + kTileWaitNs));
 #pragma unroll 1
       for (int first = start; first < start + kTileKeys; first += kMendKeys) {
-        const char *k[kMendKeys], *v[kMendKeys];  // vectors of zeros for keys that the row does not see
+        Vector k[kMendKeys], v[kMendKeys];  // vectors of zeros for keys that the row does not see
         float w[kMendKeys] = {};
         uint32_t seen = 0;
 #pragma unroll
         for (int i = 0; i < kMendKeys; ++i) {
           const char *const at = mask.sees(first + i) ? row_of(first + i) : nullptr;
-          k[i] = at != nullptr ? at + k_at : reinterpret_cast<const char *>(zero_row);
-          v[i] = at != nullptr ? at + v_at + half * 128 : reinterpret_cast<const char *>(zero_row);
+          const char *const none = reinterpret_cast<const char *>(zero_row);
+          k[i] = at != nullptr ? Vector{at + k_at, scale_of(at, p.io.ks_off)} : Vector{none, 0.f};
+          v[i] = at != nullptr ? Vector{at + v_at + half * (kBytes / (D / 64)), scale_of(at, p.io.vs_off)} : Vector{none, 0.f};
           seen |= at != nullptr ? 1u << i : 0u;
         }
 #pragma unroll 2
@@ -289,7 +313,7 @@ __device__ __noinline__ void mend_row(const TileParams<S> &p, const TileItem &it
           const uint4 a = reinterpret_cast<const uint4 *>(q)[c];
 #pragma unroll
           for (int i = 0; i < kMendKeys; ++i) {
-            const uint4 b = reinterpret_cast<const uint4 *>(k[i])[c];
+            const uint4 b = k[i][c];
             w[i] = add_product<T>(a.x, b.x, add_product<T>(a.y, b.y, add_product<T>(a.z, b.z, add_product<T>(a.w, b.w, w[i]))));
           }
         }
@@ -299,7 +323,7 @@ __device__ __noinline__ void mend_row(const TileParams<S> &p, const TileItem &it
         for (int c = 0; c < 8; ++c)
 #pragma unroll
           for (int i = 0; i < kMendKeys; ++i) {
-            const uint4 b = reinterpret_cast<const uint4 *>(v[i])[c];
+            const uint4 b = v[i][c];
             add_scaled<T>(o + 8 * c, w[i], b.x);
             add_scaled<T>(o + 8 * c + 2, w[i], b.y);
             add_scaled<T>(o + 8 * c + 4, w[i], b.z);
@@ -318,7 +342,7 @@ __device__ __noinline__ void mend_row(const TileParams<S> &p, const TileItem &it
   }
 }
 
-template <typename T, int D, typename S, bool kTest = false>
+template <typename T, int D, typename S, bool kTest, bool kQuantised>
 __global__ void __launch_bounds__(kTileThreads, 1) attend_tile_kernel(const __grid_constant__ TileParams<S> p) {
   using Shape = TileShape<D>;
   constexpr int kStages = Shape::kStages;
@@ -383,7 +407,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) attend_tile_kernel(const __gr
 
   if (warp < 8) {
     // ---------------------------------------------------------------- softmax
-    grow_registers<kSoftmaxRegisters>();
+    grow_registers<kQuantised ? kSoftmaxRegistersQ : kSoftmaxRegisters>();
     const int t = warp >> 2;
     const uint32_t lane_base = tmem + ((uint32_t)(warp & 3) * 32 << 16);
     const uint32_t s_at = lane_base + t * 128, o_at = lane_base + 256 + t * 128;
@@ -576,7 +600,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) attend_tile_kernel(const __gr
         const float2 m = unpair(marks);
         const bool bad = row < rows && item.nq > 1 && my_n > 0 && !(m.x == 0.f && m.y == 0.f);
         if (bad)
-          mend_row<T, D>(p, item, &bars.deadline, token, head, base, l,
+          mend_row<T, D, S, kQuantised>(p, item, &bars.deadline, token, head, base, l,
                           p.io.out + out_token * p.io.out_stride + (int64_t)head * (D * 2),
                           p.direct ? nullptr : p.space.o + slot_row * D);
         item_read(k);
@@ -584,6 +608,115 @@ __global__ void __launch_bounds__(kTileThreads, 1) attend_tile_kernel(const __gr
     }
   } else if (warp < 12) {
     // ---------------------------------------------------------------- keys and values
+    if constexpr (kQuantised) {
+    // A lane looks up one key; its warp brings in those 32 keys, 16 e4m3 elements a lane
+    // and pass, and stores them times their scale in the element type.  While one
+    // operand is converted the next one's elements are on their way to registers: through
+    // shared memory they would cost it half as many bytes again as it moves already
+    // (operands read by the tensor core and written once take four fifths of what it can).
+    shrink_registers<kLoadRegistersQ>();
+    const int lw = warp - 8;
+    constexpr int kLanes = D / 16, kAtOnce = 32 / kLanes, kPasses = 32 / kAtOnce;
+    const int cc = lane % kLanes, odd = cc >> 2;  // lanes of the upper 64 elements begin with their second chunk: no bank twice
+    ulonglong2 *mine = addresses + lw * 32;
+    const ulonglong2 *theirs = mine + lane / kLanes;
+    // this lane's two chunks of 8 elements; of D = 128 every other pass lies 4 keys on
+    uint32_t to[2][128 / D == 1 ? 2 : 1];
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int e = 0; e < (D == 128 ? 2 : 1); ++e) {
+        const int r = e * kAtOnce + lane / kLanes, c = 2 * cc + (h ^ odd);
+        to[h][e] = (c >> 3) * (kTileKeys * 128) + (lw * 32 + r) * 128 + (((c & 7) ^ (r & 7)) << 4);
+      }
+    bool ok = true;
+    uint32_t loaded = 0;  // key tiles
+    for (int k = 0; ok && item_there(k); ++k) {
+      const TileItem &item = items[k % kItemSlots];
+      const int n = item.n, j0 = item.j0, n_sink = item.keys.n_sink, first_tile = item.keys.first_tile;
+      const int lo = item.there.lo, hi = item.there.hi, sink_end = item.there.sink_end;
+      const int32_t *const pages = item.pages;
+      const int h = item.h;
+      item_read(k);
+      int key = 0, page = -1;
+      float k_scale = 0.f, v_scale = 0.f;
+      auto look_up = [&](int j) {
+        key = (j < n_sink ? j : first_tile + j - n_sink) * kTileKeys + lw * 32 + lane;
+        if (!(key < sink_end || (key >= lo && key < hi))) key = -1;
+        page = key >= 0 ? pages[div_by(key, p.pools.page_size)] : -1;
+      };
+      auto resolve = [&] {  // addresses and scales of the keys looked up last
+        const char *at = nullptr;
+        if (key >= 0) {
+          at = page_address(p.pools, page);
+          if (at == nullptr) {
+            raise_status(status, CPKV_STATUS_PAGE_OOB);
+          } else {
+            at += (int64_t)(key - div_by(key, p.pools.page_size) * (int)p.pools.page_size.d) * p.pools.row_bytes;
+          }
+        }
+        k_scale = at == nullptr ? 0.f : __ldg(reinterpret_cast<const float *>(at + p.io.ks_off) + h);
+        v_scale = at == nullptr ? 0.f : __ldg(reinterpret_cast<const float *>(at + p.io.vs_off) + h);
+        const char *const zeros = reinterpret_cast<const char *>(zero_row);
+        __syncwarp();
+        mine[lane] = make_ulonglong2((unsigned long long)(at == nullptr ? zeros : at + p.io.k_off + h * D),
+                                     (unsigned long long)(at == nullptr ? zeros : at + p.io.v_off + h * D));
+        __syncwarp();
+      };
+      uint4 raw[kPasses];
+      auto load = [&](int i, bool values) {
+        const ulonglong2 src = theirs[i * kAtOnce];
+        raw[i] = ld_stream16(reinterpret_cast<const char *>(values ? src.y : src.x) + cc * 16);
+      };
+      auto store = [&](int i, uint32_t base, float scale, const uint4 &x) {
+        const float s = __shfl_sync(0xffffffffu, scale, i * kAtOnce + lane / kLanes);
+        const uint32_t on = base + (D == 128 ? i / 2 * 1024 : i * 1024);
+        st_shared16(on + to[0][D == 128 ? i & 1 : 0], read_back8<T>(odd ? make_uint2(x.z, x.w) : make_uint2(x.x, x.y), s));
+        st_shared16(on + to[1][D == 128 ? i & 1 : 0], read_back8<T>(odd ? make_uint2(x.x, x.y) : make_uint2(x.z, x.w), s));
+      };
+      if (n > 0) {
+        look_up(j0);
+        resolve();
+#pragma unroll
+        for (int i = 0; i < kPasses; ++i) load(i, false);
+      }
+      for (int it = 0; it < n; ++it) {
+        const bool more = it + 1 < n;
+        const int stage = loaded % kStages;
+        const bool reuse = loaded >= kStages;
+        const uint32_t freed = (loaded / kStages - 1) & 1;
+        ++loaded;
+        const float ks = k_scale, vs = v_scale;
+        if (more) look_up(j0 + it + 1);
+        ok = all(!reuse || wait_or_stop(&bars.k_empty[stage], freed));
+        if (!ok) break;
+        const uint32_t k_base = smem_addr(k_smem + stage * Shape::kOperand), v_base = smem_addr(v_smem + stage * Shape::kOperand);
+#pragma unroll
+        for (int i = 0; i < kPasses; ++i) {
+          const uint4 x = raw[i];
+          load(i, true);
+          store(i, k_base, ks, x);
+        }
+        mbar_arrive(&bars.k_full[stage]);
+        if (more) resolve();
+        ok = all(!reuse || wait_or_stop(&bars.v_empty[stage], freed));
+        if (!ok) break;
+#pragma unroll
+        for (int i = 0; i < kPasses; ++i) {
+          const uint4 x = raw[i];
+          if (more) load(i, false);
+          store(i, v_base, vs, x);
+        }
+        mbar_arrive(&bars.v_full[stage]);
+        if (warp == 8 && lane == 0 && it == (n > kClaimAhead ? n - kClaimAhead : 0)) mbar_arrive(&bars.wanted);
+      }
+      if (warp == 8 && lane == 0 && n == 0) mbar_arrive(&bars.wanted);
+    }
+    if (lane == 0) {
+      bars.issued[lw] = 0;  // nothing is in flight: every element went through registers
+      atomicSub(&bars.loaders, 1);
+    }
+    } else {
     // A lane looks up one key; its warp brings in those 32 keys.  Without a box it
     // leaves the address in shared memory and copies one 16-byte chunk of several
     // keys.  Keys that no query of the sequence sees are copied from zeros.
@@ -688,6 +821,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) attend_tile_kernel(const __gr
       atomicSub(&bars.loaders, 1);
     }
     cp_async_wait_all();
+    }
   } else {
     shrink_registers<kOtherRegisters>();
     const int role = __shfl_sync(0xffffffffu, warp, 0);

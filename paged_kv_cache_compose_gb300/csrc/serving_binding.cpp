@@ -296,7 +296,6 @@ PyObject *read_rows(PyObject *, PyObject *const *a, Py_ssize_t n) {
 // (table, kv_heads, q, q_lens, page_table, kv_lens, max_kv_len, window, sinks, scale, out, lse, workspace, status, stream)
 PyObject *attend_window(PyObject *, PyObject *const *a, Py_ssize_t n) {
   return guarded(a, n, 15, [&](const Table &t) {
-    if (t.row() != nullptr) fail("table", "rows of the element type");
     const Rows q = rows(a[2], "q", t), out = rows(a[10], "out", t);
     if (!q.same_shape(out)) fail("out", "q's shape");
     int64_t requests = 0, bytes = 0;
@@ -311,6 +310,13 @@ PyObject *attend_window(PyObject *, PyObject *const *a, Py_ssize_t n) {
     void *workspace = memory(a[12], t, &bytes);
     int32_t *status = status_word(a[13], t);
     if (requests > INT32_MAX || q.heads > INT32_MAX || q.dim > INT32_MAX) return CPKV_ERR_LIMIT;
+    if (t.row() != nullptr) {
+      if (small(a[1], "kv_heads") != t.row()->kv_heads || q.dim != t.row()->key_dim) fail("q", "[tokens, heads, key_dim] of the cache");
+      return cpkv_attend_window_quantised(static_cast<int>(requests), t.page_size, t.cp_size, t.code, static_cast<int>(q.heads), t.row(),
+                                          q_lens.at(), max_kv, t.pools(), t.cap_pages(), pages.at, pages.stride, kv_lens, q.n, q.at,
+                                          q.stride, static_cast<float>(scale), small(a[7], "window"), small(a[8], "sinks"), out.at,
+                                          out.stride, lse, workspace, bytes, t.flags, status, stream_of(a[14]));
+    }
     return cpkv_attend_window(static_cast<int>(requests), t.page_size, t.cp_size, t.code, static_cast<int>(q.heads),
                               small(a[1], "kv_heads"), static_cast<int>(q.dim), t.row_bytes, t.key_offset, t.value_offset,
                               q_lens.at(), max_kv, t.pools(), t.cap_pages(), pages.at, pages.stride, kv_lens, q.n, q.at,
@@ -322,7 +328,6 @@ PyObject *attend_window(PyObject *, PyObject *const *a, Py_ssize_t n) {
 // (table, kv_heads, q, group_sizes, prefix_lens, prefix_pages, page_table, suffix_lens, max_suffix_len, scale, out, lse, workspace, status, stream)
 PyObject *attend_shared(PyObject *, PyObject *const *a, Py_ssize_t n) {
   return guarded(a, n, 15, [&](const Table &t) {
-    if (t.row() != nullptr) fail("table", "rows of the element type");
     const Rows q = rows(a[2], "q", t), out = rows(a[10], "out", t);
     if (!q.same_shape(out)) fail("out", "q's shape");
     int64_t requests = 0, prefix_pages = 0, bytes = 0;
@@ -338,6 +343,14 @@ PyObject *attend_shared(PyObject *, PyObject *const *a, Py_ssize_t n) {
     void *workspace = memory(a[12], t, &bytes);
     int32_t *status = status_word(a[13], t);
     if (requests > INT32_MAX || q.heads > INT32_MAX || q.dim > INT32_MAX || sizes.count() > INT32_MAX) return CPKV_ERR_LIMIT;
+    if (t.row() != nullptr) {
+      if (small(a[1], "kv_heads") != t.row()->kv_heads || q.dim != t.row()->key_dim) fail("q", "[tokens, heads, key_dim] of the cache");
+      return cpkv_attend_shared_quantised(static_cast<int>(requests), static_cast<int>(sizes.count()), t.page_size, t.cp_size, t.code,
+                                          static_cast<int>(q.heads), t.row(), sizes.at(), lens.at(), max_suffix, t.pools(),
+                                          t.cap_pages(), prefix, prefix_pages, pages.at, pages.stride, suffix_lens, q.at, q.stride,
+                                          static_cast<float>(scale), out.at, out.stride, lse, workspace, bytes, t.flags, status,
+                                          stream_of(a[14]));
+    }
     return cpkv_attend_shared(static_cast<int>(requests), static_cast<int>(sizes.count()), t.page_size, t.cp_size, t.code,
                               static_cast<int>(q.heads), small(a[1], "kv_heads"), static_cast<int>(q.dim), t.row_bytes,
                               t.key_offset, t.value_offset, sizes.at(), lens.at(), max_suffix, t.pools(), t.cap_pages(),

@@ -120,3 +120,38 @@ def test_tables_want_byte_pools_of_whole_rows():
             cpkv.QuantisedTable(bad, ps, row, dtype)
     with pytest.raises(cpkv.CpkvError):  # a row of other heads
         QuantisedCache([good], page_size=16, kv_heads=1, key_dim=64, row=row)
+
+
+def window_args():
+    return Args(B=2, ps=16, cp=2, dtype=cpkv.BF16, hq=4, row=Row(row_of()), q_lens=np.array([1, 2], np.int32), max_kv=64, pools=pools(),
+                caps=np.array([4, 4], np.int64), table=FAKE, stride=4, kv_lens=FAKE, tokens=3, q=FAKE, qs=256, scale=0.1, window=8, sinks=2, out=FAKE,
+                os=256, lse=None, ws=FAKE, ws_bytes=1 << 40, flags=0, status=FAKE, stream=None)
+
+
+def shared_args():
+    return Args(B=3, groups=2, ps=16, cp=2, dtype=cpkv.FP16, hq=4, row=Row(row_of()), sizes=np.array([1, 2], np.int32),
+                prefix=np.array([32, 0], np.int32), max_suffix=64, pools=pools(), caps=np.array([4, 4], np.int64), prefix_pages=FAKE, n_prefix=2,
+                table=FAKE, stride=4, suffix=FAKE, q=FAKE, qs=256, scale=0.1, out=FAKE, os=256, lse=None, ws=FAKE, ws_bytes=1 << 40, flags=0,
+                status=FAKE, stream=None)
+
+
+UNFIT = [(dict(row=Row(QuantisedRow.of(1, 64, 512, True))), cpkv.CPKV_ERR_ARG), (dict(row=Row(QuantisedRow.of(1, 64, 128))), cpkv.CPKV_ERR_ARG),
+         (dict(row=None), cpkv.CPKV_ERR_ARG), (dict(hq=3), cpkv.CPKV_ERR_ARG), (dict(hq=4100), cpkv.CPKV_ERR_LIMIT), (dict(dtype=5), cpkv.CPKV_ERR_ARG),
+         (dict(q=None), cpkv.CPKV_ERR_ARG), (dict(q=260), cpkv.CPKV_ERR_ARG), (dict(out=None), cpkv.CPKV_ERR_ARG), (dict(os=128), cpkv.CPKV_ERR_ARG),
+         (dict(scale=float("nan")), cpkv.CPKV_ERR_ARG), (dict(ws_bytes=16), cpkv.CPKV_ERR_CAPACITY), (dict(ws=264), cpkv.CPKV_ERR_ARG),
+         (dict(flags=1), cpkv.CPKV_ERR_ARG), (dict(status=None), cpkv.CPKV_ERR_ARG), (dict(table=None), cpkv.CPKV_ERR_ARG),
+         (dict(pools=None), cpkv.CPKV_ERR_ARG), (dict(stride=-1), cpkv.CPKV_ERR_CAPACITY)] + [(dict(row=Row(row_of(**bad))), code) for bad, code in BAD_ROWS]
+
+
+@pytest.mark.parametrize("changed, code", UNFIT + [
+    (dict(B=0, tokens=0), cpkv.CPKV_OK), (dict(tokens=4), cpkv.CPKV_ERR_ARG), (dict(max_kv=65), cpkv.CPKV_ERR_CAPACITY),
+    (dict(window=-1), cpkv.CPKV_ERR_ARG), (dict(sinks=-1), cpkv.CPKV_ERR_ARG), (dict(kv_lens=None), cpkv.CPKV_ERR_ARG)], ids=str)
+def test_window_refusals(lib, changed, code):
+    assert call(window_args(), lib.cpkv_attend_window_quantised, **changed) == code
+
+
+@pytest.mark.parametrize("changed, code", UNFIT + [
+    (dict(B=0, groups=0), cpkv.CPKV_OK), (dict(B=2), cpkv.CPKV_ERR_ARG), (dict(prefix=np.array([31, 0], np.int32)), cpkv.CPKV_ERR_UNALIGNED_PREFIX),
+    (dict(n_prefix=1), cpkv.CPKV_ERR_CAPACITY), (dict(max_suffix=65), cpkv.CPKV_ERR_CAPACITY), (dict(suffix=None), cpkv.CPKV_ERR_ARG)], ids=str)
+def test_shared_refusals(lib, changed, code):
+    assert call(shared_args(), lib.cpkv_attend_shared_quantised, **changed) == code
