@@ -759,7 +759,9 @@ int cpkv_read_quantised(int64_t n_rows, int page_size, int cp_size, int dtype, c
  * more, keys and values are brought to the element type first (e4m3 * scale rounded once: in bf16
  * exact for the append's scales, in fp16 up to 65504, and in steps of 2^-24 below 2^-14).
  *   h_row          quantised keys (no keep_keys), key_dim = value_dim (ARG otherwise)
- *   other arguments, workspace, status bits and errors: as cpkv_attend_window
+ *   d_workspace    at least cpkv_attend_window_quantised_workspace_bytes: beside many query
+ *                  rows, the rows that they see are read back into it first
+ *   other arguments, status bits and errors: as cpkv_attend_window
  */
 int cpkv_attend_window_quantised(int B, int page_size, int cp_size, int dtype, int q_heads,
                                  const cpkv_quantised_row *h_row, const int32_t *h_q_lens, int64_t max_kv_len,
@@ -769,7 +771,13 @@ int cpkv_attend_window_quantised(int B, int page_size, int cp_size, int dtype, i
                                  int sinks, void *d_out, int64_t out_stride, float *d_lse, void *d_workspace,
                                  int64_t workspace_bytes, int flags, int32_t *d_status, cpkv_stream_t stream);
 
-/* cpkv_attend_shared over quantised rows; h_row and rounding as cpkv_attend_window_quantised. */
+/* Device workspace of cpkv_attend_window_quantised (host only); lengths as passed to it. */
+int cpkv_attend_window_quantised_workspace_bytes(int B, int q_heads, int kv_heads, int head_dim,
+                                                 const int32_t *h_q_lens, int64_t max_kv_len, int window, int sinks,
+                                                 int64_t *h_bytes);
+
+/* cpkv_attend_shared over quantised rows; h_row and rounding as cpkv_attend_window_quantised,
+ * the workspace that of cpkv_attend_shared. */
 int cpkv_attend_shared_quantised(int B, int n_groups, int page_size, int cp_size, int dtype, int q_heads,
                                  const cpkv_quantised_row *h_row, const int32_t *h_group_sizes,
                                  const int32_t *h_prefix_lens, int64_t max_suffix_len, const void *const *h_pools,

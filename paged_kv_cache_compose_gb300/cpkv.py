@@ -66,7 +66,7 @@ EXPORTED = (
     "cpkv_compose_fused", "cpkv_compose_fused_planes", "cpkv_selftest_ring_timeout", "cpkv_ragged_plan_sizes",
     "cpkv_ragged_plan_build", "cpkv_append_rotary", "cpkv_append_quantised", "cpkv_read_quantised", "cpkv_attend_window",
     "cpkv_attend_window_workspace_bytes", "cpkv_attend_shared", "cpkv_attend_shared_workspace_bytes",
-    "cpkv_attend_window_quantised", "cpkv_attend_shared_quantised",
+    "cpkv_attend_window_quantised", "cpkv_attend_window_quantised_workspace_bytes", "cpkv_attend_shared_quantised",
     "cpkv_selftest_attend_timeout", "cpkv_selftest_attend_quantised_timeout", "cpkv_stream_is_capturing", "cpkv_error_string", "cpkv_version",
 )
 
@@ -116,6 +116,7 @@ def _declare(lib):
     lib.cpkv_attend_window_quantised.argtypes = [_I] * 5 + [_P, _P, _L, _P, _P, _P, _L, _P, _L, _P, _L, _F, _I, _I, _P, _L, _P, _P, _L, _I, _P, _P]
     lib.cpkv_attend_shared_quantised.argtypes = [_I] * 6 + [_P] * 3 + [_L, _P, _P, _P, _L, _P, _L, _P, _P, _L, _F, _P, _L, _P, _P, _L, _I, _P, _P]
     lib.cpkv_attend_window_workspace_bytes.argtypes = [_I] * 4 + [_P, _L, _I, _I, _P]
+    lib.cpkv_attend_window_quantised_workspace_bytes.argtypes = [_I] * 4 + [_P, _L, _I, _I, _P]
     lib.cpkv_attend_shared.argtypes = [_I] * 8 + [_L] * 3 + [_P, _P, _L, _P, _P, _P, _L, _P, _L, _P, _P, _L, _F, _P, _L,
                                                              _P, _P, _L, _I, _P, _P]
     lib.cpkv_attend_shared_workspace_bytes.argtypes = [_I] * 5 + [_P, _P, _L, _P]
@@ -612,14 +613,23 @@ def cpkv_read_quantised(d_slots, k_out, v_out, *, table: QuantisedTable, d_statu
     _check("cpkv_read_quantised", serving().read_rows(table.native, d_slots, k_out, v_out, d_status, _handle(stream, table)))
 
 
-def cpkv_attend_window_workspace_bytes(B, q_heads, kv_heads, head_dim, q_lens, max_kv_len, window=0, sinks=0) -> int:
-    """Workspace of ``cpkv_attend_window`` on the current device (``q_lens`` None: one query each)."""
+def _window_workspace_bytes(name, B, q_heads, kv_heads, head_dim, q_lens, max_kv_len, window, sinks) -> int:
     ql = None if q_lens is None else _host_i32(q_lens)
     out = ctypes.c_int64(0)
-    _check("cpkv_attend_window_workspace_bytes", load().cpkv_attend_window_workspace_bytes(
-        B, q_heads, kv_heads, head_dim, None if ql is None else ql.ctypes.data, max_kv_len, window, sinks,
-        ctypes.byref(out)))
+    _check(name, getattr(load(), name)(B, q_heads, kv_heads, head_dim, None if ql is None else ql.ctypes.data, max_kv_len, window, sinks,
+                                       ctypes.byref(out)))
     return int(out.value)
+
+
+def cpkv_attend_window_workspace_bytes(B, q_heads, kv_heads, head_dim, q_lens, max_kv_len, window=0, sinks=0) -> int:
+    """Workspace of ``cpkv_attend_window`` on the current device (``q_lens`` None: one query each)."""
+    return _window_workspace_bytes("cpkv_attend_window_workspace_bytes", B, q_heads, kv_heads, head_dim, q_lens, max_kv_len, window, sinks)
+
+
+def cpkv_attend_window_quantised_workspace_bytes(B, q_heads, kv_heads, head_dim, q_lens, max_kv_len, window=0, sinks=0) -> int:
+    """Workspace of ``cpkv_attend_window_quantised``, likewise."""
+    return _window_workspace_bytes("cpkv_attend_window_quantised_workspace_bytes", B, q_heads, kv_heads, head_dim, q_lens, max_kv_len,
+                                   window, sinks)
 
 
 def cpkv_attend_window(q, q_lens, page_table, d_kv_lens, *, table: PoolTable, kv_heads, max_kv_len, window, sinks,
@@ -651,7 +661,7 @@ def cpkv_attend_shared(q, group_sizes, prefix_lens, prefix_pages, page_table, d_
 
 def cpkv_attend_window_quantised(q, q_lens, page_table, d_kv_lens, *, table: QuantisedTable, max_kv_len, window, sinks, scale, out, lse,
                                  workspace, d_status, stream=None):
-    """``cpkv_attend_window`` over quantised rows; the workspace is that call's."""
+    """``cpkv_attend_window`` over quantised rows."""
     _check("cpkv_attend_window_quantised", serving().attend_window(
         table.native, table.row.kv_heads, q, q_lens, page_table, d_kv_lens, max_kv_len, window, sinks, scale, out, lse, workspace,
         d_status, _handle(stream, table)))

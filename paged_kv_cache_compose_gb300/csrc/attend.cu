@@ -6,17 +6,7 @@ using namespace cpkv;
 extern "C" int cpkv_attend_window_workspace_bytes(int B, int q_heads, int kv_heads, int head_dim,
                                                   const int32_t *h_q_lens, int64_t max_kv_len, int window, int sinks,
                                                   int64_t *h_bytes) {
-  const HeadArgs heads = {CPKV_BF16, q_heads, kv_heads, head_dim};
-  if (B < 0 || max_kv_len < 0 || window < 0 || sinks < 0 || h_bytes == nullptr) return CPKV_ERR_ARG;
-  int rc = check_heads(heads);
-  if (rc != CPKV_OK) return rc;
-  if (B > CPKV_MAX_BATCH || max_kv_len > INT32_MAX / 2) return CPKV_ERR_LIMIT;
-  window = clamp_window(window, max_kv_len);
-  WindowPlan plan;
-  rc = window_plan(&plan, heads, B, h_q_lens, max_kv_len, window, sinks);
-  if (rc != CPKV_OK) return rc;
-  *h_bytes = plan.bytes;
-  return CPKV_OK;
+  return window_bytes(false, HeadArgs{CPKV_BF16, q_heads, kv_heads, head_dim}, B, h_q_lens, max_kv_len, window, sinks, h_bytes);
 }
 
 extern "C" int cpkv_attend_window(int B, int page_size, int cp_size, int dtype, int q_heads, int kv_heads, int head_dim,

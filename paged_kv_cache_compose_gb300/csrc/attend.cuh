@@ -229,6 +229,13 @@ CPKV_DEV void cp_async16_hint(uint32_t smem, const void *src, int bytes, uint64_
 CPKV_DEV void cp_async16(uint32_t smem, const void *src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem), "l"(src) : "memory");
 }
+// Four bytes alike; `bytes` 0 writes zeros and reads nothing.
+CPKV_DEV void cp_async4(uint32_t smem, const void *src, int bytes) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem), "l"(src), "r"(bytes) : "memory");
+}
+CPKV_DEV void cp_async16_or_zeros(uint32_t smem, const void *src, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem), "l"(src), "r"(bytes) : "memory");
+}
 CPKV_DEV void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 CPKV_DEV void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 template <int N>

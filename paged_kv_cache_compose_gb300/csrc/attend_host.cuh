@@ -4,6 +4,7 @@
 
 #include "attend_join.cuh"
 #include "attend_split_quantised.cuh"
+#include "attend_unpack.cuh"
 
 namespace cpkv {
 namespace {
@@ -184,25 +185,54 @@ struct TileBounds {
 // tile kernel, at 24 rows 160 and 103 us.
 inline bool few_rows(int64_t max_rows) { return max_rows <= kSplitRows; }
 
+// Quantised rows that a tile pass brings to the element type beforehand (attend_unpack.cuh):
+// where the sequences have kUnpackTiles row tiles each or more, and the dense rows fit kUnpackMost.
+// PLACEHOLDER
+struct UnpackBounds {
+  int64_t pages = 0, stride = 0;
+  int sequences = 0;
+
+  static int64_t pages_of(int64_t nq, int64_t max_kv, int window, int sinks) {
+    const int64_t all = ceil_div(max_kv, kDensePage);
+    if (nq == 0) return 0;
+    if (window == 0) return all;
+    return std::min<int64_t>(all, ceil_div((int64_t)sinks, kDensePage) + ((int64_t)window + nq) / kDensePage + 2);
+  }
+  void add(int64_t nq, int64_t max_kv, int window, int sinks) {
+    pages += pages_of(nq, max_kv, window, sinks);
+    sequences += nq > 0;
+    stride = ceil_div(max_kv, kDensePage);
+  }
+  static int64_t row_bytes(int kv_heads, int head_dim) { return (int64_t)kv_heads * head_dim * 4; }
+  int64_t table_bytes(int64_t count) const { return round_up(count * stride * 4, 256); }
+  int64_t bytes(int64_t count, int kv_heads, int head_dim) const {
+    return table_bytes(count) + pages * kDensePage * row_bytes(kv_heads, head_dim) + 256;
+  }
+};
+
+constexpr int64_t kUnpackTiles = 4, kUnpackMost = (int64_t)1 << 32;
+
 // How a call is done, from host lengths alone.
 struct WindowPlan {
   SplitBounds split;
   TileBounds tile;
-  bool few = true, whole = false;
-  int64_t tokens = 0, bytes = 0;
+  UnpackBounds unpack;
+  bool few = true, whole = false, unpacks = false;
+  int64_t tokens = 0, bytes = 0, pass_bytes = 0;  // of the workspace: in all, of the passes alone
 };
 
 // A window that no request's keys reach past is none: positions less it stay in 32 bits,
 // also below 0 (a request shorter than its queries).
 inline int clamp_window(int window, int64_t max_kv) { return window >= max_kv ? 0 : window; }
 
-inline int window_plan(WindowPlan *w, const HeadArgs &a, int B, const int32_t *h_q_lens, int64_t max_kv, int window, int sinks) {
+inline int window_plan(WindowPlan *w, const HeadArgs &a, bool quantised, int B, const int32_t *h_q_lens, int64_t max_kv, int window, int sinks) {
   const int group = a.q_heads / a.kv_heads;
   for (int s = 0; s < B; ++s) {
     const int64_t nq = h_q_lens == nullptr ? 1 : h_q_lens[s];
     if (nq < 0) return CPKV_ERR_ARG;
     w->split.add(nq, max_kv, window, sinks);
     w->tile.add(nq, max_kv, group, window, sinks);
+    w->unpack.add(nq, max_kv, window, sinks);
   }
   w->few = few_rows(w->tile.max_rows);
   w->tokens = w->tile.tokens;
@@ -220,6 +250,10 @@ inline int window_plan(WindowPlan *w, const HeadArgs &a, int B, const int32_t *h
   w->bytes = w->whole ? 0
              : w->few ? w->split.bytes(B, a.kv_heads, a.head_dim, true)
                       : w->tile.bytes(a.kv_heads, a.head_dim, true);
+  w->pass_bytes = round_up(w->bytes, 256);
+  w->unpacks = quantised && !w->few && w->tile.tiles >= kUnpackTiles * w->unpack.sequences &&
+               w->unpack.bytes(B, a.kv_heads, a.head_dim) <= kUnpackMost;
+  if (w->unpacks) w->bytes = w->pass_bytes + w->unpack.bytes(B, a.kv_heads, a.head_dim);
   return rc;
 }
 
@@ -367,11 +401,11 @@ void fill_tiles(TileParams<S> *p, const S &seqs, int ragged, const PagedPools &p
 template <typename T, int D, bool kQuantised, bool kTest = false, typename S>
 int tile_pass(const TileParams<S> &p, const TileBounds &b, cudaStream_t stream) {
   auto kernel = attend_tile_kernel<T, D, S, kTest, kQuantised>;
-  const int rc = ensure_dynamic_smem((const void *)kernel, TileShape<D>::kSmem);
+  const int rc = ensure_dynamic_smem((const void *)kernel, TileShape<D, kQuantised>::kSmem);
   if (rc != CPKV_OK) return rc;
   const int64_t grid = b.blocks(p.io.kv_heads);
   if (grid > INT32_MAX) return CPKV_ERR_LIMIT;
-  return launch_kernel(kernel, dim3((unsigned)grid), dim3(kTileThreads), TileShape<D>::kSmem, false, stream, p);
+  return launch_kernel(kernel, dim3((unsigned)grid), dim3(tile_threads(kQuantised)), TileShape<D, kQuantised>::kSmem, false, stream, p);
 }
 
 template <typename S>
@@ -522,6 +556,35 @@ struct WindowCall {
   int window, sinks;
 };
 
+// The rows that the queries see into dense pages, then the call over those.
+template <int N>
+int unpacked_call(const HeadArgs &heads, const Seqs<N> &s, const PagedPools &pools, const AttendIo &io, const WindowPlan &plan,
+                  const WindowCall &c, const ResultArgs &r) {
+  char *at = static_cast<char *>(r.d_workspace) + plan.pass_bytes;
+  at += -reinterpret_cast<uintptr_t>(at) & 255;
+  UnpackParams<Seqs<N>> p = {};
+  p.seqs = s;
+  p.pools = pools;
+  p.io = io;
+  p.table = reinterpret_cast<int32_t *>(at);
+  p.table_stride = plan.unpack.stride;
+  p.rows = at + plan.unpack.table_bytes(c.B);
+  for (int b = 0; b < c.B; ++b)
+    p.cu_pages[b + 1] = p.cu_pages[b] + (int)UnpackBounds::pages_of(c.h_q_lens == nullptr ? 1 : c.h_q_lens[b], c.max_kv_len, s.window, s.sinks);
+  const int64_t blocks = plan.unpack.pages * (kDensePage / kUnpackRows), row_bytes = UnpackBounds::row_bytes(heads.kv_heads, heads.head_dim);
+  if (blocks > INT32_MAX) return CPKV_ERR_LIMIT;
+  int rc = for_type_and_dim(heads, [&](auto t, auto d) {
+    return launch_kernel(unpack_kernel<decltype(t), decltype(d)::value, Seqs<N>>, dim3((unsigned)blocks), dim3(kUnpackRows * 32), 0, false, r.stream, p);
+  });
+  if (rc != CPKV_OK) return rc;
+  const void *const rows = p.rows;
+  const int64_t cap = plan.unpack.pages;
+  return cpkv_attend_window(c.B, kDensePage, 1, heads.dtype, heads.q_heads, heads.kv_heads, heads.head_dim, row_bytes, 0, row_bytes / 2,
+                            c.h_q_lens, c.max_kv_len, &rows, &cap, p.table, p.table_stride, c.d_kv_lens, c.num_tokens, r.d_q, r.q_stride,
+                            r.scale, c.window, c.sinks, r.d_out, r.out_stride, r.d_lse, r.d_workspace, plan.pass_bytes,
+                            CPKV_DENSE_PAGES, r.d_status, (cpkv_stream_t)r.stream);
+}
+
 template <bool kQuantised>
 int window_call(const HeadArgs &heads, const RowArgs &rows, const WindowCall &c, const ResultArgs &r) {
   const int B = c.B;
@@ -535,7 +598,7 @@ int window_call(const HeadArgs &heads, const RowArgs &rows, const WindowCall &c,
   if (c.table_stride < 0 || c.max_kv_len > c.table_stride * rows.page_size) return CPKV_ERR_CAPACITY;
   const int window = clamp_window(c.window, c.max_kv_len);
   WindowPlan plan;
-  rc = window_plan(&plan, heads, B, c.h_q_lens, c.max_kv_len, window, c.sinks);
+  rc = window_plan(&plan, heads, kQuantised, B, c.h_q_lens, c.max_kv_len, window, c.sinks);
   if (rc != CPKV_OK) return rc;
   if (plan.tokens != c.num_tokens) return CPKV_ERR_ARG;
   if (plan.tokens == 0) return CPKV_OK;
@@ -564,10 +627,27 @@ int window_call(const HeadArgs &heads, const RowArgs &rows, const WindowCall &c,
     } else {
       for (int b = 0; b < B; ++b) s.cu_q[b + 1] = s.cu_q[b] + (c.h_q_lens == nullptr ? 1 : c.h_q_lens[b]);
     }
+    if constexpr (kQuantised) {
+      if (plan.unpacks) return unpacked_call<N>(heads, s, pools, io, plan, c, r);
+    }
     return attend_window<kQuantised, N>(heads, s, pools, io, plan, static_cast<char *>(r.d_workspace), r.stream);
   };
   if (uniform || B <= kFewSeqs) return go(std::integral_constant<int, kFewSeqs>());
   return go(std::integral_constant<int, CPKV_MAX_BATCH>());
+}
+
+// Bytes of the workspace of a windowed call.
+inline int window_bytes(bool quantised, const HeadArgs &heads, int B, const int32_t *h_q_lens, int64_t max_kv_len, int window, int sinks,
+                        int64_t *h_bytes) {
+  if (B < 0 || max_kv_len < 0 || window < 0 || sinks < 0 || h_bytes == nullptr) return CPKV_ERR_ARG;
+  int rc = check_heads(heads);
+  if (rc != CPKV_OK) return rc;
+  if (B > CPKV_MAX_BATCH || max_kv_len > INT32_MAX / 2) return CPKV_ERR_LIMIT;
+  WindowPlan plan;
+  rc = window_plan(&plan, heads, quantised, B, h_q_lens, max_kv_len, clamp_window(window, max_kv_len), sinks);
+  if (rc != CPKV_OK) return rc;
+  *h_bytes = plan.bytes;
+  return CPKV_OK;
 }
 
 struct SharedCall {

@@ -3,6 +3,12 @@
 
 using namespace cpkv;
 
+extern "C" int cpkv_attend_window_quantised_workspace_bytes(int B, int q_heads, int kv_heads, int head_dim,
+                                                            const int32_t *h_q_lens, int64_t max_kv_len, int window,
+                                                            int sinks, int64_t *h_bytes) {
+  return window_bytes(true, HeadArgs{CPKV_BF16, q_heads, kv_heads, head_dim}, B, h_q_lens, max_kv_len, window, sinks, h_bytes);
+}
+
 extern "C" int cpkv_attend_window_quantised(int B, int page_size, int cp_size, int dtype, int q_heads,
                                             const cpkv_quantised_row *h_row, const int32_t *h_q_lens, int64_t max_kv_len,
                                             const void *const *h_pools, const int64_t *h_pool_cap_pages,

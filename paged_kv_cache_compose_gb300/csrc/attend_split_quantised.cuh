@@ -36,10 +36,6 @@ struct SplitShapeQ {
   static constexpr int kSmem = kRing + kJoin + kSplitWarps * kSplitRows * 8;
 };
 
-CPKV_DEV void cp_async4(uint32_t smem, const void *src, int bytes) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem), "l"(src), "r"(bytes) : "memory");
-}
-
 // Bytes 0, 2, 1, 3.
 CPKV_DEV uint32_t sort_pairs(uint32_t v) { return __byte_perm(v, 0, 0x3120); }
 

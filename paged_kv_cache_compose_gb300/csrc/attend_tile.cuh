@@ -47,14 +47,17 @@ namespace cpkv {
 
 constexpr int kTileRows = 256;  // packed rows of a block
 constexpr int kTileKeys = 128;
-constexpr int kLoaders = 128;
-constexpr int kTileThreads = 512;
+// Warps: 8 of the softmax, then those that load, then four that issue products, find items
+// and load queries.  Quantised rows are converted on the way and take eight warps.
+constexpr int load_warps(bool quantised) { return quantised ? 8 : 4; }
+constexpr int tile_threads(bool quantised) { return 32 * (12 + load_warps(quantised)); }
 // Registers a thread: 512 threads are launched with 128 each, 65536 in all; the
 // softmax holds a row's 128 scores.  256 * 216 + 256 * 40 = 65536.
 constexpr int kSoftmaxRegisters = 216, kOtherRegisters = 40;
-// Over quantised rows the loading warps hold 8 vectors in flight and more: 256 * 200 +
-// 128 * 72 + 128 * 40 = 65536.
-constexpr int kSoftmaxRegistersQ = 200, kLoadRegistersQ = 72;
+// Over quantised rows 640 threads are launched with 96 each, 61440 in all, and the softmax
+// holds half a row's scores: 256 * 152 + 256 * 64 + 128 * 48 = 61440.
+constexpr int kSoftmaxRegistersQ = 152, kLoadRegistersQ = 64, kOtherRegistersQ = 48;
+constexpr int kTurn = 2;  // passes (16 elements a lane) that a loading warp converts together
 constexpr int kItemSlots = 4;   // items known at a time: of small ones, some are loaded while others are finished
 constexpr int kClaimAhead = 12;  // key tiles before an item's last load at which the next item is claimed
 constexpr int kTileMaps = 8;  // most pools that TMA maps travel for
@@ -102,12 +105,14 @@ struct TileSource {
 // Rows of a part of a sequence of one query.
 CPKV_DEV int single_rows(int group) { return group < kTileRows ? group : kTileRows; }
 
-template <int D>
+template <int D, bool kQuantised>
 struct TileShape {
   static constexpr int kOperand = kTileKeys * D * 2;  // keys (or values, or 128 queries) in shared memory
   static constexpr int kStages = D == 128 ? 2 : 4;
   static constexpr int kQ = 2 * kOperand;
-  static constexpr int kSmem = 1024 + kQ + 2 * kStages * kOperand;
+  static constexpr int kRawTurns = 3;  // turns of quantised rows in a loading warp's ring
+  static constexpr int kRaw = kQuantised ? load_warps(true) * kRawTurns * kTurn * 512 : 0;
+  static constexpr int kSmem = 1024 + kQ + 2 * kStages * kOperand + kRaw;
 };
 
 // What the warps of a block are told of an item.
@@ -131,7 +136,7 @@ struct TileBars {
   uint32_t issued[4];  // keys and values of tiles, in turn, that a loading warp has issued
 };
 
-constexpr int kItemReaders = 15;  // warps that read an item: softmax, loads, products, queries
+constexpr int item_readers(bool quantised) { return 11 + load_warps(quantised); }  // warps that read an item: softmax, loads, products, queries
 
 __device__ const uint4 zero_row[16] = {};  // a key or value vector of zeros
 
@@ -343,26 +348,29 @@ __device__ __noinline__ void mend_row(const TileParams<S> &p, const TileItem &it
 }
 
 template <typename T, int D, typename S, bool kTest, bool kQuantised>
-__global__ void __launch_bounds__(kTileThreads, 1) attend_tile_kernel(const __grid_constant__ TileParams<S> p) {
-  using Shape = TileShape<D>;
+__global__ void __launch_bounds__(tile_threads(kQuantised), 1) attend_tile_kernel(const __grid_constant__ TileParams<S> p) {
+  using Shape = TileShape<D, kQuantised>;
   constexpr int kStages = Shape::kStages;
+  constexpr int kLoadWarps = load_warps(kQuantised), kProducts = 8 + kLoadWarps;  // the warp that issues products
+  constexpr int kOthers = kQuantised ? kOtherRegistersQ : kOtherRegisters;
   constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
   extern __shared__ char raw_smem[];
   __shared__ TileBars bars;
   __shared__ TileItem items[kItemSlots];
   __shared__ float2 stream_ml[128];            // maximum and sum of the second stream's rows
-  __shared__ ulonglong2 addresses[kTileKeys];  // of the keys being copied: key, value
+  __shared__ ulonglong2 addresses[kQuantised ? 1 : kTileKeys];  // of the keys being copied: key, value
   char *smem = reinterpret_cast<char *>((reinterpret_cast<uintptr_t>(raw_smem) + 1023) & ~uintptr_t(1023));
   char *q_smem = smem, *k_smem = smem + Shape::kQ, *v_smem = k_smem + kStages * Shape::kOperand;
+  [[maybe_unused]] char *const pieces = v_smem + kStages * Shape::kOperand;  // the loading warps' rings of quantised rows
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   int32_t *status = p.seqs.status;
   release_dependents();  // later passes of the call; the joining kernel waits for this one
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) {
-      mbar_init(&bars.k_full[i], kLoaders);
+      mbar_init(&bars.k_full[i], 32 * kLoadWarps);
       mbar_init(&bars.k_empty[i], 1);
-      mbar_init(&bars.v_full[i], kLoaders);
+      mbar_init(&bars.v_full[i], 32 * kLoadWarps);
       mbar_init(&bars.v_empty[i], 1);
     }
     for (int t = 0; t < 2; ++t) {
@@ -374,7 +382,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) attend_tile_kernel(const __gr
     }
     for (int i = 0; i < kItemSlots; ++i) {
       mbar_init(&bars.item_full[i], 1);
-      mbar_init(&bars.item_empty[i], kItemReaders);
+      mbar_init(&bars.item_empty[i], item_readers(kQuantised));
     }
     mbar_init(&bars.wanted, 1);
     mbar_init(&bars.claimed, 1);
@@ -382,11 +390,11 @@ __global__ void __launch_bounds__(kTileThreads, 1) attend_tile_kernel(const __gr
     mbar_init(&bars.stream_done, 128);
     mbar_init(&bars.stream_free, 128);
     bars.gave_up = 0;
-    bars.loaders = 4;
+    bars.loaders = kLoadWarps;
     bars.deadline = ~uint64_t(0);  // until the first item is known
     fence_barrier_init();
   }
-  if (warp == 12) tmem_alloc(&bars.tmem, 512);
+  if (warp == kProducts) tmem_alloc(&bars.tmem, 512);
   tmem_fence_before();
   __syncthreads();
   tmem_fence_after();
@@ -431,32 +439,42 @@ __global__ void __launch_bounds__(kTileThreads, 1) attend_tile_kernel(const __gr
         wait(&bars.s_full[t], seen);
         __syncwarp();
         tmem_fence_after();
-        uint32_t x[4][32];
-        tmem_load32(x[0], s_at);
-        tmem_load32(x[1], s_at + 32);
-        tmem_load32(x[2], s_at + 64);
-        tmem_load32(x[3], s_at + 96);
-#pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_wait_loads(x[c]);
+        constexpr int kChunks = kQuantised ? 2 : 4;  // 32 columns each that are held at a time
+        uint32_t x[kChunks][32];
         const int j = j0 + it * step, start = (j < n_sink ? j : first_tile + j) * kTileKeys;
-        if (!(start + kTileKeys <= whole_hi && (start >= whole_lo || start + kTileKeys <= p.seqs.sinks))) {
-          const RowMask mask = row_mask(item.kv, item.nq, div_by(first + (int)(threadIdx.x & 127), p.io.group), p.seqs.causal,
-                                        p.seqs.window, p.seqs.sinks);
+        const bool partly = !(start + kTileKeys <= whole_hi && (start >= whole_lo || start + kTileKeys <= p.seqs.sinks));
+        auto scores_of = [&](int from) {  // of columns from 32 * from on; -infinity where the row does not see the key
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const int at = start + c * 32;
-            const uint32_t sees = low_bits(mask.hi - at) & (~low_bits(mask.lo - at) | low_bits(mask.sinks - at));
+          for (int c = 0; c < kChunks; ++c) tmem_load32(x[c], s_at + (from + c) * 32);
 #pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if (!(sees & (1u << i))) x[c][i] = 0xff800000u;
+          for (int c = 0; c < kChunks; ++c) tmem_wait_loads(x[c]);
+          if (partly) {
+            const RowMask mask = row_mask(item.kv, item.nq, div_by(first + (int)(threadIdx.x & 127), p.io.group), p.seqs.causal,
+                                          p.seqs.window, p.seqs.sinks);
+#pragma unroll
+            for (int c = 0; c < kChunks; ++c) {
+              const int at = start + (from + c) * 32;
+              const uint32_t sees = low_bits(mask.hi - at) & (~low_bits(mask.lo - at) | low_bits(mask.sinks - at));
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                if (!(sees & (1u << i))) x[c][i] = 0xff800000u;
+            }
           }
-        }
+        };
         float best[4];
+        auto best_of = [&](int from) {
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          best[c] = fmaxf(__uint_as_float(x[c][0]), __uint_as_float(x[c][1]));
+          for (int c = 0; c < kChunks; ++c) {
+            best[from + c] = fmaxf(__uint_as_float(x[c][0]), __uint_as_float(x[c][1]));
 #pragma unroll
-          for (int i = 2; i < 32; i += 2) best[c] = max3(best[c], __uint_as_float(x[c][i]), __uint_as_float(x[c][i + 1]));
+            for (int i = 2; i < 32; i += 2) best[from + c] = max3(best[from + c], __uint_as_float(x[c][i]), __uint_as_float(x[c][i + 1]));
+          }
+        };
+        scores_of(0);
+        best_of(0);
+        if constexpr (kQuantised) {  // the first half is looked at once more: its registers are the loading warps'
+          scores_of(2);
+          best_of(2);
         }
         const float top = fmaf(fmaxf(fmaxf(best[0], best[1]), fmaxf(best[2], best[3])), scale, -kLift<T, true>);
         const bool rise = top > base + kRescaleAt || (base == -INFINITY && top != -INFINITY);
@@ -480,30 +498,45 @@ __global__ void __launch_bounds__(kTileThreads, 1) attend_tile_kernel(const __gr
         const float shift = base == -INFINITY ? 0.f : base;
         const uint64_t scale2 = pair(__float_as_uint(scale), __float_as_uint(scale));
         const uint64_t shift2 = pair(__float_as_uint(-shift), __float_as_uint(-shift));
+        auto weights = [&](int at) {  // over the scores, 32 columns of them in 16
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          uint32_t w[16];
+          for (int c = 0; c < kChunks; ++c) {
+            uint32_t w[16];
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const float2 y = unpair(fma_pair(pair(x[c][2 * i], x[c][2 * i + 1]), scale2, shift2));
-            const float a = exp2_approx(y.x), b = exp2_approx(y.y);
-            w[i] = pack2<T>(a, b);
-            x[c][2 * i] = __float_as_uint(a);
-            x[c][2 * i + 1] = __float_as_uint(b);
+            for (int i = 0; i < 16; ++i) {
+              const float2 y = unpair(fma_pair(pair(x[c][2 * i], x[c][2 * i + 1]), scale2, shift2));
+              const float a = exp2_approx(y.x), b = exp2_approx(y.y);
+              w[i] = pack2<T>(a, b);
+              x[c][2 * i] = __float_as_uint(a);
+              x[c][2 * i + 1] = __float_as_uint(b);
+            }
+            tmem_store16(s_at + at + c * 16, w);
           }
-          tmem_store16(s_at + c * 16, w);
+        };
+        auto add_up = [&] {
+          uint64_t sum[kChunks] = {};
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+#pragma unroll
+            for (int c = 0; c < kChunks; ++c) sum[c] = add_pair(sum[c], pair(x[c][2 * i], x[c][2 * i + 1]));
+          if constexpr (kChunks == 4) {
+            const float2 all = unpair(add_pair(add_pair(sum[0], sum[1]), add_pair(sum[2], sum[3])));
+            l += all.x + all.y;
+          } else {
+            const float2 all = unpair(add_pair(sum[0], sum[1]));
+            l += all.x + all.y;
+          }
+        };
+        if constexpr (kQuantised) {
+          weights(64);
+          add_up();
+          scores_of(0);
         }
+        weights(0);
         tmem_wait_stores();
         tmem_fence_before();
         mbar_arrive(&bars.p_full[t]);
-        // the sum, beside the products
-        uint64_t sum[4] = {0, 0, 0, 0};
-#pragma unroll
-        for (int i = 0; i < 16; ++i)
-#pragma unroll
-          for (int c = 0; c < 4; ++c) sum[c] = add_pair(sum[c], pair(x[c][2 * i], x[c][2 * i + 1]));
-        const float2 all = unpair(add_pair(add_pair(sum[0], sum[1]), add_pair(sum[2], sum[3])));
-        l += all.x + all.y;
+        add_up();  // beside the products
         ++seen;
       }
       // outputs of the item: of both tiles, so that either thread keeps count
@@ -606,47 +639,49 @@ __global__ void __launch_bounds__(kTileThreads, 1) attend_tile_kernel(const __gr
         item_read(k);
       }
     }
-  } else if (warp < 12) {
+  } else if (warp < kProducts) {
     // ---------------------------------------------------------------- keys and values
     if constexpr (kQuantised) {
-    // A lane looks up one key; its warp brings in those 32 keys, 16 e4m3 elements a lane
-    // and pass, and stores them times their scale in the element type.  While one
-    // operand is converted the next one's elements are on their way to registers: through
-    // shared memory they would cost it half as many bytes again as it moves already
-    // (operands read by the tensor core and written once take four fifths of what it can).
+    // A lane looks up one key; its warp brings in those 16 keys, 16 e4m3 elements a lane
+    // and pass: by cp.async to a place of the lane's own, from there, times their scale and in
+    // the element type, into the operand.  Through registers alone the same loads took
+    // half as long again: with this much shared memory in use, the first-level cache that
+    // they pass through holds too few of them (prefill 3.6 ms, 2.4 without the loads).
     shrink_registers<kLoadRegistersQ>();
     const int lw = warp - 8;
-    constexpr int kLanes = D / 16, kAtOnce = 32 / kLanes, kPasses = 32 / kAtOnce;
+    constexpr int kKeys = kTileKeys / kLoadWarps, kLanes = D / 16, kAtOnce = 32 / kLanes, kPasses = kKeys / kAtOnce;  // of an operand
+    constexpr int kTurns = 2 * kPasses / kTurn, kAhead = Shape::kRawTurns - 1;      // of a tile; on their way
     const int cc = lane % kLanes, odd = cc >> 2;  // lanes of the upper 64 elements begin with their second chunk: no bank twice
-    ulonglong2 *mine = addresses + lw * 32;
-    const ulonglong2 *theirs = mine + lane / kLanes;
-    // this lane's two chunks of 8 elements; of D = 128 every other pass lies 4 keys on
-    uint32_t to[2][128 / D == 1 ? 2 : 1];
+    char *const ring = pieces + lw * (Shape::kRawTurns * kTurn * 512) + lane * 16;
+    int to[2][D == 128 ? 2 : 1];  // this lane's two chunks of 8 elements; of D = 128 every other pass lies 4 keys on
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll
       for (int e = 0; e < (D == 128 ? 2 : 1); ++e) {
         const int r = e * kAtOnce + lane / kLanes, c = 2 * cc + (h ^ odd);
-        to[h][e] = (c >> 3) * (kTileKeys * 128) + (lw * 32 + r) * 128 + (((c & 7) ^ (r & 7)) << 4);
+        to[h][e] = (c >> 3) * (kTileKeys * 128) + (lw * kKeys + r) * 128 + (((c & 7) ^ (r & 7)) << 4);
       }
     bool ok = true;
-    uint32_t loaded = 0;  // key tiles
+    uint32_t loaded = 0;         // key tiles
+    int fill = 0, empty = 0;     // places in the ring of the next turn to issue and to convert
     for (int k = 0; ok && item_there(k); ++k) {
       const TileItem &item = items[k % kItemSlots];
       const int n = item.n, j0 = item.j0, n_sink = item.keys.n_sink, first_tile = item.keys.first_tile;
       const int lo = item.there.lo, hi = item.there.hi, sink_end = item.there.sink_end;
       const int32_t *const pages = item.pages;
-      const int h = item.h;
+      const int64_t k_at = p.io.k_off + (int64_t)item.h * D + cc * 16, v_at = p.io.v_off + (int64_t)item.h * D + cc * 16;
+      const int64_t ks_at = p.io.ks_off + (int64_t)item.h * 4, vs_at = p.io.vs_off + (int64_t)item.h * 4;
       item_read(k);
       int key = 0, page = -1;
-      float k_scale = 0.f, v_scale = 0.f;
-      auto look_up = [&](int j) {
-        key = (j < n_sink ? j : first_tile + j - n_sink) * kTileKeys + lw * 32 + lane;
+      auto look_up = [&](int j) {  // this lane's key of a tile, and its page
+        key = (j < n_sink ? j : first_tile + j - n_sink) * kTileKeys + lw * kKeys + lane % kKeys;
         if (!(key < sink_end || (key >= lo && key < hi))) key = -1;
         page = key >= 0 ? pages[div_by(key, p.pools.page_size)] : -1;
       };
-      auto resolve = [&] {  // addresses and scales of the keys looked up last
-        const char *at = nullptr;
+      const char *at = nullptr;             // row of this lane's key, in the tile that is issued; null: none
+      float k_scale = 0.f, v_scale = 0.f;   // its scales
+      auto resolve = [&] {
+        at = nullptr;
         if (key >= 0) {
           at = page_address(p.pools, page);
           if (at == nullptr) {
@@ -655,65 +690,70 @@ __global__ void __launch_bounds__(kTileThreads, 1) attend_tile_kernel(const __gr
             at += (int64_t)(key - div_by(key, p.pools.page_size) * (int)p.pools.page_size.d) * p.pools.row_bytes;
           }
         }
-        k_scale = at == nullptr ? 0.f : __ldg(reinterpret_cast<const float *>(at + p.io.ks_off) + h);
-        v_scale = at == nullptr ? 0.f : __ldg(reinterpret_cast<const float *>(at + p.io.vs_off) + h);
-        const char *const zeros = reinterpret_cast<const char *>(zero_row);
-        __syncwarp();
-        mine[lane] = make_ulonglong2((unsigned long long)(at == nullptr ? zeros : at + p.io.k_off + h * D),
-                                     (unsigned long long)(at == nullptr ? zeros : at + p.io.v_off + h * D));
-        __syncwarp();
+        k_scale = at == nullptr ? 0.f : __ldg(reinterpret_cast<const float *>(at + ks_at));
+        v_scale = at == nullptr ? 0.f : __ldg(reinterpret_cast<const float *>(at + vs_at));
       };
-      uint4 raw[kPasses];
-      auto load = [&](int i, bool values) {
-        const ulonglong2 src = theirs[i * kAtOnce];
-        raw[i] = ld_stream16(reinterpret_cast<const char *>(values ? src.y : src.x) + cc * 16);
-      };
-      auto store = [&](int i, uint32_t base, float scale, const uint4 &x) {
-        const float s = __shfl_sync(0xffffffffu, scale, i * kAtOnce + lane / kLanes);
-        const uint32_t on = base + (D == 128 ? i / 2 * 1024 : i * 1024);
-        st_shared16(on + to[0][D == 128 ? i & 1 : 0], read_back8<T>(odd ? make_uint2(x.z, x.w) : make_uint2(x.x, x.y), s));
-        st_shared16(on + to[1][D == 128 ? i & 1 : 0], read_back8<T>(odd ? make_uint2(x.x, x.y) : make_uint2(x.z, x.w), s));
+      auto issue = [&](int turn, bool there) {  // turn of the tile in hand
+        if (there) {
+          const uint32_t dst = smem_addr(ring + fill * (kTurn * 512));
+#pragma unroll
+          for (int e = 0; e < kTurn; ++e) {
+            const int pass = turn * kTurn + e, which = pass / kPasses, i = pass % kPasses;
+            const char *const row = reinterpret_cast<const char *>(__shfl_sync(0xffffffffu, (unsigned long long)at, i * kAtOnce + lane / kLanes));
+            cp_async16_or_zeros(dst + e * 512, row == nullptr ? (const char *)zero_row : row + (which ? v_at : k_at), row == nullptr ? 0 : 16);
+          }
+          fill = fill + 1 == Shape::kRawTurns ? 0 : fill + 1;
+        }
+        cp_async_commit();
       };
       if (n > 0) {
         look_up(j0);
         resolve();
 #pragma unroll
-        for (int i = 0; i < kPasses; ++i) load(i, false);
+        for (int turn = 0; turn < kAhead; ++turn) issue(turn, true);
+        if (n > 1) look_up(j0 + 1);
       }
       for (int it = 0; it < n; ++it) {
-        const bool more = it + 1 < n;
         const int stage = loaded % kStages;
-        const bool reuse = loaded >= kStages;
+        const bool reuse = loaded >= kStages, more = it + 1 < n;
         const uint32_t freed = (loaded / kStages - 1) & 1;
         ++loaded;
         const float ks = k_scale, vs = v_scale;
-        if (more) look_up(j0 + it + 1);
-        ok = all(!reuse || wait_or_stop(&bars.k_empty[stage], freed));
-        if (!ok) break;
-        const uint32_t k_base = smem_addr(k_smem + stage * Shape::kOperand), v_base = smem_addr(v_smem + stage * Shape::kOperand);
 #pragma unroll
-        for (int i = 0; i < kPasses; ++i) {
-          const uint4 x = raw[i];
-          load(i, true);
-          store(i, k_base, ks, x);
-        }
-        mbar_arrive(&bars.k_full[stage]);
-        if (more) resolve();
-        ok = all(!reuse || wait_or_stop(&bars.v_empty[stage], freed));
-        if (!ok) break;
+        for (int turn = 0; turn < kTurns; ++turn) {
+          if (turn + kAhead == kTurns && more) {  // what is issued from here on is the next tile's
+            resolve();
+            if (it + 2 < n) look_up(j0 + it + 2);
+          }
+          const int which = turn * kTurn / kPasses;  // keys, then values
+          if (turn * kTurn % kPasses == 0) {
+            ok = all(!reuse || wait_or_stop(which ? &bars.v_empty[stage] : &bars.k_empty[stage], freed));
+            if (!ok) break;
+          }
+          issue((turn + kAhead) % kTurns, turn + kAhead < kTurns || more);
+          cp_async_wait<kAhead>();
+          uint4 x[kTurn];
 #pragma unroll
-        for (int i = 0; i < kPasses; ++i) {
-          const uint4 x = raw[i];
-          if (more) load(i, false);
-          store(i, v_base, vs, x);
+          for (int e = 0; e < kTurn; ++e) x[e] = *reinterpret_cast<const uint4 *>(ring + empty * (kTurn * 512) + e * 512);
+          empty = empty + 1 == Shape::kRawTurns ? 0 : empty + 1;
+          char *const operand = (which ? v_smem : k_smem) + stage * Shape::kOperand;
+#pragma unroll
+          for (int e = 0; e < kTurn; ++e) {
+            const int i = (turn * kTurn + e) % kPasses;
+            const float s = __shfl_sync(0xffffffffu, which ? vs : ks, i * kAtOnce + lane / kLanes);
+            char *const on = operand + (D == 128 ? i / 2 * 1024 : i * 1024);
+            *reinterpret_cast<uint4 *>(on + to[0][D == 128 ? i & 1 : 0]) = read_back8<T>(odd ? make_uint2(x[e].z, x[e].w) : make_uint2(x[e].x, x[e].y), s);
+            *reinterpret_cast<uint4 *>(on + to[1][D == 128 ? i & 1 : 0]) = read_back8<T>(odd ? make_uint2(x[e].x, x[e].y) : make_uint2(x[e].z, x[e].w), s);
+          }
+          if ((turn + 1) * kTurn % kPasses == 0) mbar_arrive(which ? &bars.v_full[stage] : &bars.k_full[stage]);
         }
-        mbar_arrive(&bars.v_full[stage]);
+        if (!ok) break;
         if (warp == 8 && lane == 0 && it == (n > kClaimAhead ? n - kClaimAhead : 0)) mbar_arrive(&bars.wanted);
       }
       if (warp == 8 && lane == 0 && n == 0) mbar_arrive(&bars.wanted);
     }
+    cp_async_wait_all();
     if (lane == 0) {
-      bars.issued[lw] = 0;  // nothing is in flight: every element went through registers
       atomicSub(&bars.loaders, 1);
     }
     } else {
@@ -823,9 +863,9 @@ __global__ void __launch_bounds__(kTileThreads, 1) attend_tile_kernel(const __gr
     cp_async_wait_all();
     }
   } else {
-    shrink_registers<kOtherRegisters>();
+    shrink_registers<kOthers>();
     const int role = __shfl_sync(0xffffffffu, warp, 0);
-    if (role == 12) {
+    if (role == kProducts) {
       // -------------------------------------------------------------- products
       // The copies are ordinary writes to shared memory: the fence of the warp that
       // issues the products (after the wait that orders them before it) lets the
@@ -853,7 +893,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) attend_tile_kernel(const __gr
         const uint32_t b = v_low + stage * (Shape::kOperand >> 4), d = tm + 256 + t * 128, a = tm + t * 128;
         if (elect_one()) {
 #pragma unroll
-          for (int e = 0; e < kTileKeys / 16; ++e) mma_ts(d, a + e * 8, b + e * (16 * 128 >> 4), desc_o, e > 0 ? 1 : add);
+          for (int e = 0; e < kTileKeys / 16; ++e) mma_ts(d, a + (kQuantised ? e / 4 * 64 + e % 4 * 8 : e * 8), b + e * (16 * 128 >> 4), desc_o, e > 0 ? 1 : add);
         }
         __syncwarp();
       };
@@ -950,7 +990,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) attend_tile_kernel(const __gr
         }
         used += n;
       }
-    } else if (role == 13) {
+    } else if (role == kProducts + 1) {
       // -------------------------------------------------------------- items
       if (lane == 0) {
         int block = (int)blockIdx.x;
@@ -980,7 +1020,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) attend_tile_kernel(const __gr
     } else {
       // -------------------------------------------------------------- queries
       constexpr int kLanes = D / 8;
-      const int at = (int)threadIdx.x - 14 * 32, c = at % kLanes;
+      const int at = (int)threadIdx.x - (kProducts + 2) * 32, c = at % kLanes;
       uint32_t filled[2] = {0, 0};
       int turn = 0;
       for (int k = 0; item_there(k); ++k) {
@@ -1036,13 +1076,13 @@ __global__ void __launch_bounds__(kTileThreads, 1) attend_tile_kernel(const __gr
   tmem_fence_before();
   __syncthreads();
   tmem_fence_after();
-  if (warp == 12) {
+  if (warp == kProducts) {
     if (*(volatile int *)&bars.gave_up) {  // what is in flight ends before the block and its tensor memory do
       if (elect_one()) mma_commit(&bars.drain);
       __syncwarp();
       const uint64_t t0 = global_timer_ns();
       tile_drain(&bars.drain, 0, t0);
-      for (int w = 0; w < 4; ++w) {  // the last use of every stage
+      for (int w = 0; w < (kQuantised ? 0 : kLoadWarps); ++w) {  // the last use of every stage (quantised rows are written by the warps themselves)
         const uint32_t values = bars.issued[w] / 2, keys = bars.issued[w] - values;
         for (uint32_t at = keys > kStages ? keys - kStages : 0; at < keys; ++at) tile_drain(&bars.k_full[at % kStages], at / kStages, t0);
         for (uint32_t at = values > kStages ? values - kStages : 0; at < values; ++at)

@@ -86,7 +86,10 @@ CPKV_DEV uint32_t halves_high(uint32_t v) {
 template <typename T>
 CPKV_DEV uint32_t read_back2(uint32_t halves, float scale) {
   const float2 x = unpack2<__half>(halves);
-  const float a = x.x * scale, b = x.y * scale;
+  float a, b;
+  asm("{\n.reg .b64 x, s;\nmov.b64 x, {%2, %3};\nmov.b64 s, {%4, %4};\nmul.rn.f32x2 x, x, s;\nmov.b64 {%0, %1}, x;\n}"
+      : "=f"(a), "=f"(b)
+      : "f"(x.x), "f"(x.y), "f"(scale));
   if constexpr (std::is_same<T, __half>::value) {
     uint32_t r;
     asm("cvt.rn.satfinite.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));

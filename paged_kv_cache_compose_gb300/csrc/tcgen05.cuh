@@ -188,10 +188,6 @@ CPKV_DEV bool mbar_try_wait_for(uint64_t *bar, uint32_t parity, uint32_t ns) {
 }
 
 // 32 bytes to an address that is a multiple of 32.
-CPKV_DEV void st_shared16(uint32_t to, const uint4 &v) {
-  asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(to), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
-}
-
 CPKV_DEV void store32(void *to, const uint32_t *r) {
   asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(to), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]),
                "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])

@@ -287,8 +287,11 @@ class PagedCache:
         if scale is None:
             scale = self._scale
         self._attend("attend_window", (self.table.native, self.kv_heads, q, q_lens, page_table, kv_lens, max_kv_len, window, sinks,
-                                       scale, out, lse), stream, workspace, _window_bytes)
+                                       scale, out, lse), stream, workspace, self._window_size())
         return out
+
+    def _window_size(self):
+        return _window_bytes
 
     def attend_shared(self, q, group_sizes, prefix_lens, prefix_pages, page_table, suffix_lens, *,
                       max_suffix_len: int, scale: float | None = None, out=None, lse=None, workspace=None, stream=None):
@@ -331,6 +334,9 @@ class QuantisedCache(PagedCache):
         """Bytes of a row in the usual layout."""
         return cpkv.QuantisedRow.of(kv_heads, key_dim, value_dim, keep_keys).row_bytes
 
+    def _window_size(self):
+        return _window_quantised_bytes
+
     def read_rows(self, slots, *, k_out=None, v_out=None, stream=None):
         """Cache rows ``slots`` (as in ``append_rotary``; negative: zeros) back
         in 16 bits: ``k_out`` [slots, kv_heads, key_dim] and ``v_out`` [slots,
@@ -347,6 +353,10 @@ class QuantisedCache(PagedCache):
 
 def _window_bytes(table, kv_heads, q, q_lens, page_table, kv_lens, max_kv_len, window, sinks, *rest) -> int:
     return cpkv.cpkv_attend_window_workspace_bytes(kv_lens.shape[0], q.shape[1], kv_heads, q.shape[2], q_lens, max_kv_len, window, sinks)
+
+
+def _window_quantised_bytes(table, kv_heads, q, q_lens, page_table, kv_lens, max_kv_len, window, sinks, *rest) -> int:
+    return cpkv.cpkv_attend_window_quantised_workspace_bytes(kv_lens.shape[0], q.shape[1], kv_heads, q.shape[2], q_lens, max_kv_len, window, sinks)
 
 
 def _shared_bytes(table, kv_heads, q, group_sizes, prefix_lens, prefix_pages, page_table, suffix_lens, max_suffix_len, *rest) -> int:
