@@ -294,15 +294,18 @@ inline int shared_plan(SharedPlan *w, const HeadArgs &a, int B, int n_groups, co
 }
 
 // Which split kernel and shape.
-template <typename T, int D, SplitMode kMode, typename S, bool kQuantised>
+struct Plain {};
+template <int kBlocks8>
+struct Quantised {};
+template <typename T, int D, SplitMode kMode, typename S, typename Rows>
 struct SplitPass {
   using Shape = SplitShape<D, kMode>;
   static constexpr auto kernel = attend_split_kernel<T, D, S, kMode>;
 };
-template <typename T, int D, SplitMode kMode, typename S>
-struct SplitPass<T, D, kMode, S, true> {
-  using Shape = SplitShapeQ<D, kMode>;
-  static constexpr auto kernel = attend_split_quantised_kernel<T, D, S, kMode>;
+template <typename T, int D, SplitMode kMode, typename S, int kBlocks8>
+struct SplitPass<T, D, kMode, S, Quantised<kBlocks8>> {
+  using Shape = SplitShapeQ<D, kMode, kBlocks8>;
+  static constexpr auto kernel = attend_split_quantised_kernel<T, D, S, kMode, kBlocks8>;
 };
 
 template <typename F>
@@ -316,9 +319,9 @@ int for_type_and_dim(const HeadArgs &a, F f) {
 }
 
 // A block takes a whole sequence unless the mode is kLine.
-template <typename T, int D, SplitMode kMode, bool kQuantised, typename S>
-int split_pass(SplitParams<S> *p, const SplitBounds &b, cudaStream_t stream) {
-  using Pass = SplitPass<T, D, kMode, S, kQuantised>;
+template <typename T, int D, SplitMode kMode, typename Rows, typename S>
+int split_pass_of(SplitParams<S> *p, const SplitBounds &b, cudaStream_t stream) {
+  using Pass = SplitPass<T, D, kMode, S, Rows>;
   using Shape = typename Pass::Shape;
   const int smem = Shape::kSmem + (kMode == kLine ? (p->seqs.count + 1) * 4 : 0);
   auto kernel = Pass::kernel;
@@ -331,6 +334,16 @@ int split_pass(SplitParams<S> *p, const SplitBounds &b, cudaStream_t stream) {
   }
   if (blocks > INT32_MAX) return CPKV_ERR_LIMIT;
   return launch_kernel(kernel, dim3((unsigned)blocks), dim3(kSplitWarps * 32), smem, false, stream, *p);
+}
+
+// max_rows: of a sequence.
+template <typename T, int D, SplitMode kMode, bool kQuantised, typename S>
+int split_pass(SplitParams<S> *p, const SplitBounds &b, int64_t max_rows, cudaStream_t stream) {
+  if constexpr (!kQuantised) {
+    return split_pass_of<T, D, kMode, Plain>(p, b, stream);
+  } else {
+    return max_rows <= 8 ? split_pass_of<T, D, kMode, Quantised<1>>(p, b, stream) : split_pass_of<T, D, kMode, Quantised<2>>(p, b, stream);
+  }
 }
 
 template <typename S>
@@ -445,14 +458,14 @@ int attend_window(const HeadArgs &heads, const Seqs<N> &seqs, const PagedPools &
     p.direct = 1;
     if (plan.whole) {
       return for_type_and_dim(heads, [&](auto t, auto d) {
-        return split_pass<decltype(t), decltype(d)::value, kFewKeys, kQuantised>(&p, plan.split, stream);
+        return split_pass<decltype(t), decltype(d)::value, kFewKeys, kQuantised>(&p, plan.split, plan.tile.max_rows, stream);
       });
     }
     p.space = plan.split.space(workspace, seqs.count, heads.kv_heads, true);
     return for_type_and_dim(heads, [&](auto t, auto d) {
       using T = decltype(t);
       constexpr int D = decltype(d)::value;
-      const int rc = split_pass<T, D, kLine, kQuantised>(&p, plan.split, stream);
+      const int rc = split_pass<T, D, kLine, kQuantised>(&p, plan.split, plan.tile.max_rows, stream);
       return rc != CPKV_OK ? rc : join_pass<T, D>(source_of(p), io, rows, stream);
     });
   }
@@ -480,7 +493,7 @@ int attend_shared(const HeadArgs &heads, const SharedSeqs<N> &seqs, const PagedP
     return for_type_and_dim(heads, [&](auto t, auto d) {
       using T = decltype(t);
       constexpr int D = decltype(d)::value;
-      const int rc = split_pass<T, D, kLine, kQuantised>(&p, plan.split, stream);
+      const int rc = split_pass<T, D, kLine, kQuantised>(&p, plan.split, plan.tile.max_rows, stream);
       return rc != CPKV_OK ? rc : join_pass<T, D>(source_of(p), io, rows, stream);
     });
   }

@@ -14,10 +14,13 @@
 // second exponential a score: with e4m3 * scale in the element type it were five
 // instructions a pair.
 //
-// Fragments: a lane's four bytes of a 16-byte chunk c of a key are elements
-// 16 c + 4 t .. + 3 (t = lane % 4), so the queries' fragments hold those; values come
-// by transposed pairs of bytes, sorted into two columns of keys by one permutation, so
-// a lane's outputs are elements 16 c + 4 t .. + 3 of its rows too.
+// Keys and values are the first operand, of 16 keys (or 16 elements) by 16, and the queries
+// (the weights) the second, 8 rows at a time: a key converted once serves 8 rows, or 16 with
+// a second product, and what a lane holds of outputs, queries and scores halves for the 8
+// rows or fewer that a decode step of most models has.  A lane's four bytes of a 16-byte
+// chunk c of a key are elements 16 c + 4 t .. + 3 (t = lane % 4), so the queries' fragments hold
+// those; values come by transposed pairs of bytes, sorted into two columns of keys by one
+// permutation, so a lane's outputs are elements 16 c + 2 g and + 1 (g = lane / 4) of rows 2 t and + 1.
 #pragma once
 
 #include "attend_split.cuh"
@@ -25,19 +28,34 @@
 
 namespace cpkv {
 
-template <int D, SplitMode kMode>
+// kBlocks8 8 rows at a time: 1 or 2.
+template <int D, SplitMode kMode, int kBlocks8>
 struct SplitShapeQ {
-  static constexpr int kVectors = 2 * kWarpKeys * D;               // keys, then values
-  static constexpr int kStage = kVectors + 2 * kWarpKeys * 4;      // then their scales
-  static constexpr int kStages = kMode == kFewKeys ? 5 : 4;
-  static constexpr int kBlocks = kMode == kFewKeys ? 1 : D == 128 ? 3 : 5;  // blocks to an SM
+  static constexpr int kUnits = 2;                    // units that a warp takes at once
+  static constexpr int kKeys = kUnits * kWarpKeys;         // its keys of them
+  static constexpr int kVectors = 2 * kKeys * D;           // keys, then values
+  static constexpr int kStage = kVectors + 2 * kKeys * 4;  // then their scales
+  static constexpr int kStages = kMode == kFewKeys ? 3 : 2;
+  static constexpr int kBlocks = kMode == kFewKeys ? 1 : kBlocks8 == 1 ? (D == 128 ? 3 : 5) : (D == 128 ? 2 : 3);  // blocks to an SM
   static constexpr int kRing = kSplitWarps * kStages * kStage;
-  static constexpr int kJoin = kSplitRows * D * 4;  // half the columns of two warps while a sequence's parts are joined
+  static constexpr int kJoin = 8 * kBlocks8 * D * 4;  // half the columns of two warps while a sequence's parts are joined
   static constexpr int kSmem = kRing + kJoin + kSplitWarps * kSplitRows * 8;
 };
 
+// The weights' maximum is held kLiftQ below the scores', and let go kSlackQ above itself before
+// anything is rescaled (most units end there, after one vote): weights reach 2^15 in fp16 and
+// are held to half a step of 2^-24, 2^-37 of the largest.
+constexpr float kLiftQ = 12.f, kSlackQ = 3.f;
+
 // Bytes 0, 2, 1, 3.
 CPKV_DEV uint32_t sort_pairs(uint32_t v) { return __byte_perm(v, 0, 0x3120); }
+
+// The 8 x 8 matrix of fp16 whose rows the warp's lanes hold four to one, the other way round.
+CPKV_DEV uint32_t transposed(uint32_t v) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  return r;
+}
 
 // The factor that brings a query of this largest magnitude (the bits of a bf16 number) to
 // [2^14, 2^15), and its inverse.
@@ -46,13 +64,14 @@ CPKV_DEV float2 query_factors(uint32_t largest) {
   return make_float2(__uint_as_float((uint32_t)min(268 - e, 254) << 23), __uint_as_float((uint32_t)max(e - 14, 1) << 23));
 }
 
-template <typename T, int D, typename S, SplitMode kMode>
-__global__ void __launch_bounds__(kSplitWarps * 32, SplitShapeQ<D, kMode>::kBlocks) attend_split_quantised_kernel(const __grid_constant__ SplitParams<S> p) {
-  using Shape = SplitShapeQ<D, kMode>;
+template <typename T, int D, typename S, SplitMode kMode, int kBlocks8>
+__global__ void __launch_bounds__(kSplitWarps * 32, SplitShapeQ<D, kMode, kBlocks8>::kBlocks) attend_split_quantised_kernel(const __grid_constant__ SplitParams<S> p) {
+  using Shape = SplitShapeQ<D, kMode, kBlocks8>;
   using P = SplitParams<S>;
   constexpr bool kWhole = kMode != kLine;
   constexpr bool kHalf = std::is_same<T, __half>::value;
   constexpr int kChunks = D / 16;  // 16-byte chunks of a vector
+  constexpr int kUnits = Shape::kUnits, kKeys = Shape::kKeys;
   extern __shared__ __align__(128) char smem[];
   __shared__ int scan_scratch[33];
   __shared__ int few_pages[kWhole ? kSplitWarps : 1][kWholeUnits][kWarpKeys];
@@ -72,16 +91,19 @@ __global__ void __launch_bounds__(kSplitWarps * 32, SplitShapeQ<D, kMode>::kBloc
   // where chunk c of a key lies: eight neighbouring keys' in different banks
   auto place = [](int key, int c) { return key * D + ((c ^ (D == 128 ? key & 7 : key >> 1 & 3)) << 4); };
 
-  // loads: lanes 0..15 own one key each, as in the other split pass
+  // Loads: lanes 0..15 own a key each of one unit, the others of the next, which is taken with it
+  // where it is of the same sequence.
   const uint64_t once = l2_policy_evict_first();
   Cursor<P> at = ld;
+  auto together = [&](const Cursor<P> &c, int u) { return min(min(kUnits, c.units - c.j), u1 - u); };
+  const int sub = lane >> 4;
   int ld_u = u0, ld_key = 0, ld_page = -1;
   bool ld_sees = false;
-  auto look_up = [&] {  // the page of this lane's key, one unit ahead of its copy
-    ld_key = ld.keys.tile_start(ld.j, kSplitTile) + warp * kWarpKeys + (lane & 15);
-    ld_sees = ld.keys.any_sees(ld_key);
-    if (kWhole && ld.j < kWholeUnits) {
-      ld_page = few_pages[warp][ld.j][lane & 15];
+  auto look_up = [&] {  // the page of this lane's key, one turn ahead of its copy
+    ld_key = ld.keys.tile_start(ld.j + sub, kSplitTile) + warp * kWarpKeys + (lane & 15);
+    ld_sees = sub < together(ld, ld_u) && ld.keys.any_sees(ld_key);
+    if (kWhole && ld.j + sub < kWholeUnits) {
+      ld_page = few_pages[warp][ld.j + sub][lane & 15];
     } else {
       ld_page = ld_sees ? p.seqs.pages(ld.s)[div_by(ld_key, p.pools.page_size)] : -1;
     }
@@ -112,18 +134,22 @@ __global__ void __launch_bounds__(kSplitWarps * 32, SplitShapeQ<D, kMode>::kBloc
       const char *const none = reinterpret_cast<const char *>(p.io.q);  // a valid address that is not read
       const int64_t k_at = p.io.k_off + (int64_t)head * D + c * 16;
       const int64_t v_at = p.io.v_off + (int64_t)head * D + c * 16;
-      const int64_t s_at = (lane < 16 ? p.io.ks_off : p.io.vs_off) + (int64_t)head * 4;
-      cp_async4(dst + Shape::kVectors + lane * 4, row == nullptr ? none : row + s_at, row == nullptr ? 0 : 4);
+      const char *const scales_at = row == nullptr ? none : row + (int64_t)head * 4;
+      cp_async4(dst + Shape::kVectors + lane * 4, row == nullptr ? none : scales_at + p.io.ks_off, row == nullptr ? 0 : 4);
+      cp_async4(dst + Shape::kVectors + (kKeys + lane) * 4, row == nullptr ? none : scales_at + p.io.vs_off, row == nullptr ? 0 : 4);
 #pragma unroll
-      for (int i = 0; i < kWarpKeys / kRows; ++i) {
+      for (int i = 0; i < kKeys / kRows; ++i) {
         const int key = i * kRows + lane / kChunks;
         const char *src = reinterpret_cast<const char *>(__shfl_sync(0xffffffffu, (unsigned long long)row, key));
         const int bytes = src == nullptr ? 0 : 16;
         const uint32_t to = dst + place(key, c);
         cp_async16_hint(to, bytes ? src + k_at : none, bytes, once);
-        cp_async16_hint(to + kWarpKeys * D, bytes ? src + v_at : none, bytes, once);
+        cp_async16_hint(to + kKeys * D, bytes ? src + v_at : none, bytes, once);
       }
-      if (++ld_u < u1) {
+      const int taken = together(ld, ld_u);
+      ld_u += taken;
+      if (ld_u < u1) {
+        ld.j += taken - 1;
         ld.advance(p);
         look_up();
       }
@@ -135,11 +161,12 @@ __global__ void __launch_bounds__(kSplitWarps * 32, SplitShapeQ<D, kMode>::kBloc
 
   int stage = 0, seg_j0 = 0;
   bool fresh = true, first_segment = true;
-  uint32_t qf[kChunks][4];
-  float o[kChunks][2][4];  // of chunk c: elements 4 t, 4 t + 2 and 4 t + 1, 4 t + 3 of both rows
-  float m[2], l[2], n[2];  // maximum and sum of the weights; maximum of the weights times the values' scales
-  float factor[2];         // of the products of a row
-  RowMask mask[2];
+  const int t = lane & 3, g = lane >> 2;  // this lane's rows are 2 t and 2 t + 1 of each 8, its keys g and g + 8
+  uint32_t qf[kBlocks8][kChunks][2];
+  float o[kBlocks8][kChunks][4];  // of chunk c: element 2 g of both rows, then 2 g + 1
+  float m[kBlocks8][2], l[kBlocks8][2], n[kBlocks8][2];  // references of the weights' exponents and their sum; of the weights times the values' scales
+  float factor[kBlocks8][2];                             // of the products of a row
+  RowMask mask[kBlocks8][2];
   int full_lo = 0, full_hi = 0;  // keys in [full_lo, full_hi) are seen by every row
 
   // A sequence's rows from here on.
@@ -150,21 +177,20 @@ __global__ void __launch_bounds__(kSplitWarps * 32, SplitShapeQ<D, kMode>::kBloc
     full_hi = row_mask(at.kv, at.nq, 0, p.seqs.causal, p.seqs.window, p.seqs.sinks).hi;
     full_lo = row_mask(at.kv, at.nq, at.nq - 1, p.seqs.causal, p.seqs.window, p.seqs.sinks).lo;
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      const int row = (lane >> 2) + 8 * r;
+    for (int b = 0; b < kBlocks8; ++b) {
+      const int row = 8 * b + g;
       const bool in = row < rows;
-      const int i = div_by(row, p.io.group), g = row - i * group;
-      mask[r] = row_mask(at.kv, at.nq, i, p.seqs.causal, p.seqs.window, p.seqs.sinks);
-      const char *src = p.io.q + (q0 + i) * p.io.q_stride + ((int64_t)head * group + g) * (D * 2) + (lane & 3) * 8;
+      const int i = div_by(row, p.io.group), h = row - i * group;
+      const char *src = p.io.q + (q0 + i) * p.io.q_stride + ((int64_t)head * group + h) * (D * 2) + t * 8;
       uint32_t largest = 0;
 #pragma unroll
       for (int c = 0; c < kChunks; ++c) {
         const uint2 v = in ? *reinterpret_cast<const uint2 *>(src + c * 32) : make_uint2(0u, 0u);
-        qf[c][r] = v.x;
-        qf[c][r + 2] = v.y;
+        qf[b][c][0] = v.x;
+        qf[b][c][1] = v.y;
         if constexpr (!kHalf) largest = __vmaxu2(largest, __vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu));
       }
-      factor[r] = p.io.scale_log2;
+      float mine = p.io.scale_log2;
       if constexpr (!kHalf) {
         largest = max(largest & 0xffffu, largest >> 16);
         largest = max(largest, __shfl_xor_sync(0xffffffffu, largest, 1));
@@ -173,61 +199,68 @@ __global__ void __launch_bounds__(kSplitWarps * 32, SplitShapeQ<D, kMode>::kBloc
 #pragma unroll
         for (int c = 0; c < kChunks; ++c)
 #pragma unroll
-          for (int h = 0; h < 4; h += 2) {
-            const float2 v = unpack2<__nv_bfloat16>(qf[c][r + h]);
-            qf[c][r + h] = pack2<__half>(v.x * f.x, v.y * f.x);
+          for (int e = 0; e < 2; ++e) {
+            const float2 v = unpack2<__nv_bfloat16>(qf[b][c][e]);
+            qf[b][c][e] = pack2<__half>(v.x * f.x, v.y * f.x);
           }
-        factor[r] *= f.y;
+        mine *= f.y;
       }
-      m[r] = n[r] = -INFINITY;
-      l[r] = 0.f;
-    }
 #pragma unroll
-    for (int c = 0; c < kChunks; ++c)
-#pragma unroll
-      for (int i = 0; i < 8; ++i) o[c][i >> 2][i & 3] = 0.f;
-  };
-  // The end of a sequence or of this block's stretch of it: `complete` when the block held it whole.
-  auto end_rows = [&](bool complete) {
-    // join the four warps' parts: common maximum, then values pairwise
-#pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
-      l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
-      if ((lane & 3) == 0) ml[warp * kSplitRows + (lane >> 2) + 8 * r] = make_float2(m[r], l[r]);
-    }
-    __syncthreads();
-    float big[2], sum[2];
-#pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      const int row = (lane >> 2) + 8 * r;
-      float2 v[kSplitWarps];
-      big[r] = -INFINITY;
-#pragma unroll
-      for (int w = 0; w < kSplitWarps; ++w) {
-        v[w] = ml[w * kSplitRows + row];
-        big[r] = fmaxf(big[r], v[w].x);
+      for (int r = 0; r < 2; ++r) {
+        factor[b][r] = __shfl_sync(0xffffffffu, mine, (2 * t + r) * 4);
+        mask[b][r] = row_mask(at.kv, at.nq, div_by(8 * b + 2 * t + r, p.io.group), p.seqs.causal, p.seqs.window, p.seqs.sinks);
+        m[b][r] = n[b][r] = -INFINITY;
+        l[b][r] = 0.f;
       }
-      const float base = big[r] == -INFINITY ? 0.f : big[r];
-      sum[r] = 0.f;
-#pragma unroll
-      for (int w = 0; w < kSplitWarps; ++w) sum[r] += exp2_approx(v[w].x - base) * v[w].y;
-      const float mine = exp2_approx(n[r] - base);  // the values' scales come back here
 #pragma unroll
       for (int c = 0; c < kChunks; ++c)
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          o[c][h][2 * r] *= mine;
-          o[c][h][2 * r + 1] *= mine;
-        }
+        for (int e = 0; e < 4; ++e) o[b][c][e] = 0.f;
     }
+  };
+  // The end of a sequence or of this block's stretch of it: `complete` when the block held it whole.
+  auto end_rows = [&](bool complete) {
+    // join the four warps' parts: common reference, then values pairwise
+#pragma unroll
+    for (int b = 0; b < kBlocks8; ++b)
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+#pragma unroll
+        for (int w = 4; w < 32; w <<= 1) l[b][r] += __shfl_xor_sync(0xffffffffu, l[b][r], w);
+        if (g == 0) ml[warp * kSplitRows + 8 * b + 2 * t + r] = make_float2(m[b][r], l[b][r]);
+      }
+    __syncthreads();
+    float big[kBlocks8][2], sum[kBlocks8][2];
+#pragma unroll
+    for (int b = 0; b < kBlocks8; ++b)
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        float2 v[kSplitWarps];
+        float top = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < kSplitWarps; ++w) {
+          v[w] = ml[w * kSplitRows + 8 * b + 2 * t + r];
+          top = fmaxf(top, v[w].x);
+        }
+        const float base = top == -INFINITY ? 0.f : top;
+        big[b][r] = top;
+        sum[b][r] = 0.f;
+#pragma unroll
+        for (int w = 0; w < kSplitWarps; ++w) sum[b][r] += exp2_approx(v[w].x - base) * v[w].y;
+        const float mine = exp2_approx(n[b][r] - base);  // the values' scales come back here
+#pragma unroll
+        for (int c = 0; c < kChunks; ++c) {
+          o[b][c][r] *= mine;
+          o[b][c][2 + r] *= mine;
+        }
+      }
     auto each = [&](int columns, float *buf, bool put) {
 #pragma unroll
-      for (int c = 0; c < kChunks / 2; ++c)
+      for (int b = 0; b < kBlocks8; ++b)
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          float4 *q = reinterpret_cast<float4 *>(buf) + (2 * c + h) * 32 + lane;
-          float *mine = o[columns * (kChunks / 2) + c][h];
+        for (int c = 0; c < kChunks / 2; ++c) {
+          float4 *q = reinterpret_cast<float4 *>(buf) + (b * (kChunks / 2) + c) * 32 + lane;
+          float *mine = o[b][columns * (kChunks / 2) + c];
           if (put) {
             *q = make_float4(mine[0], mine[1], mine[2], mine[3]);
           } else {
@@ -236,7 +269,7 @@ __global__ void __launch_bounds__(kSplitWarps * 32, SplitShapeQ<D, kMode>::kBloc
           }
         }
     };
-    float *const upper = join + kSplitRows * D / 2;
+    float *const upper = join + 8 * kBlocks8 * D / 2;
 #pragma unroll
     for (int columns = 0; columns < 2; ++columns) {
       if (warp >= 2) each(columns, warp == 2 ? join : upper, true);
@@ -252,163 +285,195 @@ __global__ void __launch_bounds__(kSplitWarps * 32, SplitShapeQ<D, kMode>::kBloc
       const int64_t slot = complete ? 2 * (int64_t)gridDim.x + (int64_t)head * p.seqs.count + at.s
                                     : 2 * (int64_t)blockIdx.x + (first_segment ? 0 : 1);
 #pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        const int row = (lane >> 2) + 8 * r;
-        if (row >= rows) continue;
-        if (complete && p.direct) {
-          const int i = div_by(row, p.io.group), g = row - i * group;
-          const int64_t token = p.seqs.q_begin(at.s) + i;
-          const int q_head = head * group + g;
-          const float inv = row_scale(sum[r]);
-          char *dst = p.io.out + token * p.io.out_stride + (int64_t)q_head * (D * 2) + (lane & 3) * 8;
+      for (int b = 0; b < kBlocks8; ++b)
 #pragma unroll
-          for (int c = 0; c < kChunks; ++c)
-            *reinterpret_cast<uint2 *>(dst + c * 32) = make_uint2(pack2<T>(o[c][0][2 * r] * inv, o[c][1][2 * r] * inv),
-                                                                 pack2<T>(o[c][0][2 * r + 1] * inv, o[c][1][2 * r + 1] * inv));
-          if (p.io.lse != nullptr && (lane & 3) == 0)
-            p.io.lse[token * p.io.q_heads + q_head] = row_lse(big[r], sum[r]);
-        } else {
-          float *dst = p.space.o + (slot * kSplitRows + row) * D + (lane & 3) * 4;
+        for (int r = 0; r < 2; ++r) {
+          const int row = 8 * b + 2 * t + r;
+          if (row >= rows) continue;
+          if (complete && p.direct) {
+            const int i = div_by(row, p.io.group);
+            const int64_t token = p.seqs.q_begin(at.s) + i;
+            const int q_head = head * group + row - i * group;
+            const float inv = row_scale(sum[b][r]);
+            char *dst = p.io.out + token * p.io.out_stride + (int64_t)q_head * (D * 2) + g * 4;
 #pragma unroll
-          for (int c = 0; c < kChunks; ++c)
-            *reinterpret_cast<float4 *>(dst + c * 16) = make_float4(o[c][0][2 * r], o[c][1][2 * r], o[c][0][2 * r + 1], o[c][1][2 * r + 1]);
-          if ((lane & 3) == 0)
-            *reinterpret_cast<float2 *>(p.space.ml + (slot * kSplitRows + row) * 2) = make_float2(big[r], sum[r]);
+            for (int c = 0; c < kChunks; ++c)
+              *reinterpret_cast<uint32_t *>(dst + c * 32) = pack2<T>(o[b][c][r] * inv, o[b][c][2 + r] * inv);
+            if (p.io.lse != nullptr && g == 0) p.io.lse[token * p.io.q_heads + q_head] = row_lse(big[b][r], sum[b][r]);
+          } else {
+            float *dst = p.space.o + (slot * kSplitRows + row) * D + g * 2;
+#pragma unroll
+            for (int c = 0; c < kChunks; ++c) *reinterpret_cast<float2 *>(dst + c * 16) = make_float2(o[b][c][r], o[b][c][2 + r]);
+            if (g == 0) *reinterpret_cast<float2 *>(p.space.ml + (slot * kSplitRows + row) * 2) = make_float2(big[b][r], sum[b][r]);
+          }
         }
-      }
     }
   };
 
   if constexpr (kWhole) begin_rows();
-  for (int u = u0; u < u1; ++u) {
+  for (int u = u0, taken; u < u1; u += taken) {
     if (!kWhole && fresh) {
       fresh = false;
       begin_rows();
     }
+    taken = together(at, u);
     cp_async_wait<Shape::kStages - 2>();
     __syncwarp();
     load_next(stage == 0 ? Shape::kStages - 1 : stage - 1);
 
-    // products of 16 rows and this warp's 16 keys
+    // products of this warp's 16 keys of each unit and the rows
     const uint32_t kb = ring_addr + stage * Shape::kStage;
     const float *const scales = reinterpret_cast<const float *>(ring + stage * Shape::kStage + Shape::kVectors);
-    float x[2][4] = {};
-    {
-      const int key = (lane & 7) + ((lane >> 4) << 3);
+    float x[kBlocks8][kUnits][4] = {};  // rows 2 t, 2 t + 1 of key g, then of key g + 8
+#pragma unroll
+    for (int i = 0; i < kUnits; ++i) {
+      const int key = 16 * i + (lane & 15);
 #pragma unroll
       for (int c = 0; c < kChunks; c += 2) {
-        uint32_t b[4];
-        ldmatrix_x4(b, kb + place(key, c + ((lane >> 3) & 1)));
-        mma_16816<__half>(x[0], qf[c], halves_low(b[0]), halves_high(b[0]));
-        mma_16816<__half>(x[1], qf[c], halves_low(b[2]), halves_high(b[2]));
-        mma_16816<__half>(x[0], qf[c + 1], halves_low(b[1]), halves_high(b[1]));
-        mma_16816<__half>(x[1], qf[c + 1], halves_low(b[3]), halves_high(b[3]));
+        uint32_t v[4];
+        ldmatrix_x4(v, kb + place(key, c + (lane >> 4)));
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const uint32_t a[4] = {halves_low(v[2 * e]), halves_low(v[2 * e + 1]), halves_high(v[2 * e]), halves_high(v[2 * e + 1])};
+#pragma unroll
+          for (int b = 0; b < kBlocks8; ++b) mma_16816<__half>(x[b][i], a, qf[b][c + e][0], qf[b][c + e][1]);
+        }
       }
     }
-    const int key0 = at.keys.tile_start(at.j, kSplitTile) + warp * kWarpKeys;
-    const bool whole = key0 + kWarpKeys <= full_hi && (key0 >= full_lo || key0 + kWarpKeys <= p.seqs.sinks);
-    float y[2][4];  // with the values' scales
+    float y[kBlocks8][kUnits][4];  // with the values' scales
+    bool whole = true;             // every row sees all keys
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const float2 ks = *reinterpret_cast<const float2 *>(scales + e * 8 + (lane & 3) * 2);
-      const float2 vs = *reinterpret_cast<const float2 *>(scales + kWarpKeys + e * 8 + (lane & 3) * 2);
-      const float lift[2] = {log2_approx(vs.x), log2_approx(vs.y)};
+    for (int i = 0; i < kUnits; ++i) {
+      const int key0 = at.keys.tile_start(at.j + i, kSplitTile) + warp * kWarpKeys;
+      const bool all = i < taken && key0 + kWarpKeys <= full_hi && (key0 >= full_lo || key0 + kWarpKeys <= p.seqs.sinks);
+      const float ks[2] = {scales[16 * i + g], scales[16 * i + g + 8]};
+      const float lift[2] = {log2_approx(scales[kKeys + 16 * i + g]), log2_approx(scales[kKeys + 16 * i + g + 8])};
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        x[e][i] *= factor[i >> 1] * (i & 1 ? ks.y : ks.x);
-        y[e][i] = x[e][i] + lift[i & 1];
-        if (!whole && !mask[i >> 1].sees(key0 + e * 8 + (lane & 3) * 2 + (i & 1))) x[e][i] = y[e][i] = -INFINITY;
-      }
+      for (int b = 0; b < kBlocks8; ++b)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int r = e & 1, k = e >> 1;
+          x[b][i][e] *= factor[b][r] * ks[k];
+          y[b][i][e] = x[b][i][e] + lift[k];
+          if (!all && !(i < taken && mask[b][r].sees(key0 + g + 8 * k))) x[b][i][e] = y[b][i][e] = -INFINITY;
+        }
+      whole &= all;
     }
-    uint32_t pf[4];  // weights as the first operand; rounded to fp16 for the product, summed before it
+    bool rise = false;
+    float best[kBlocks8][2], top[kBlocks8][2];
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      float best = fmaxf(fmaxf(x[0][2 * r], x[0][2 * r + 1]), fmaxf(x[1][2 * r], x[1][2 * r + 1]));
-      float top = fmaxf(fmaxf(y[0][2 * r], y[0][2 * r + 1]), fmaxf(y[1][2 * r], y[1][2 * r + 1]));
-      best = fmaxf(best, __shfl_xor_sync(0xffffffffu, best, 1));
-      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-      best = fmaxf(best, __shfl_xor_sync(0xffffffffu, best, 2));
-      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-      const float next = fmaxf(m[r], best), up = fmaxf(n[r], top - kLift<__half, false>);
-      const float shift = next == -INFINITY ? 0.f : next, over = up == -INFINITY ? 0.f : up;
-      l[r] *= exp2_approx(m[r] - shift);
-      const float fall = exp2_approx(n[r] - over);
-      if (__any_sync(0xffffffffu, up != n[r])) {
+    for (int b = 0; b < kBlocks8; ++b)
 #pragma unroll
-        for (int c = 0; c < kChunks; ++c)
+      for (int r = 0; r < 2; ++r) {
+        best[b][r] = fmaxf(fmaxf(x[b][0][r], x[b][0][2 + r]), fmaxf(x[b][1][r], x[b][1][2 + r]));
+        top[b][r] = fmaxf(fmaxf(y[b][0][r], y[b][0][2 + r]), fmaxf(y[b][1][r], y[b][1][2 + r]));
+        rise |= best[b][r] - m[b][r] > kSlackQ || top[b][r] - n[b][r] > kLiftQ + kSlackQ;
+      }
+    if (__any_sync(0xffffffffu, rise)) {
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            o[c][h][2 * r] *= fall;
-            o[c][h][2 * r + 1] *= fall;
+      for (int b = 0; b < kBlocks8; ++b)
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+#pragma unroll
+          for (int w = 4; w < 32; w <<= 1) {
+            best[b][r] = fmaxf(best[b][r], __shfl_xor_sync(0xffffffffu, best[b][r], w));
+            top[b][r] = fmaxf(top[b][r], __shfl_xor_sync(0xffffffffu, top[b][r], w));
           }
-      }
-      m[r] = next;
-      n[r] = up;
+          const float next = fmaxf(m[b][r], best[b][r]), up = fmaxf(n[b][r], top[b][r] - kLiftQ);
+          l[b][r] *= exp2_approx(m[b][r] - (next == -INFINITY ? 0.f : next));
+          const float fall = exp2_approx(n[b][r] - (up == -INFINITY ? 0.f : up));
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        l[r] += exp2_approx(x[e][2 * r] - shift) + exp2_approx(x[e][2 * r + 1] - shift);
-        pf[2 * e + r] = pack2<__half>(exp2_approx(y[e][2 * r] - over), exp2_approx(y[e][2 * r + 1] - over));
+          for (int c = 0; c < kChunks; ++c) {
+            o[b][c][r] *= fall;
+            o[b][c][2 + r] *= fall;
+          }
+          m[b][r] = next;
+          n[b][r] = up;
+        }
+    }
+    uint32_t pf[kBlocks8][kUnits][2];  // weights as the second operand; rounded to fp16 for the product, summed before it
+#pragma unroll
+    for (int b = 0; b < kBlocks8; ++b) {
+      const float shift[2] = {m[b][0] == -INFINITY ? 0.f : m[b][0], m[b][1] == -INFINITY ? 0.f : m[b][1]};
+      const float over[2] = {n[b][0] == -INFINITY ? 0.f : n[b][0], n[b][1] == -INFINITY ? 0.f : n[b][1]};
+#pragma unroll
+      for (int i = 0; i < kUnits; ++i) {
+        float w[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          l[b][e & 1] += exp2_approx(x[b][i][e] - shift[e & 1]);
+          w[e] = exp2_approx(y[b][i][e] - over[e & 1]);
+        }
+        pf[b][i][0] = transposed(pack2<__half>(w[0], w[1]));
+        pf[b][i][1] = transposed(pack2<__half>(w[2], w[3]));
       }
     }
     if (S::causal && !whole && at.nq > 1) {  // values that are no numbers, of keys that some rows do not see
-      char *const values = ring + stage * Shape::kStage + kWarpKeys * D;
+      char *const values = ring + stage * Shape::kStage + kKeys * D;
       uint32_t marks = 0;
 #pragma unroll
-      for (int i = 0; i < D / 32; ++i) {
+      for (int i = 0; i < kKeys * D / 512; ++i) {
         const uint4 v = reinterpret_cast<const uint4 *>(values)[i * 32 + lane];
         marks |= ((v.x & 0x7f7f7f7fu) + 0x01010101u) | ((v.y & 0x7f7f7f7fu) + 0x01010101u) | ((v.z & 0x7f7f7f7fu) + 0x01010101u) |
                  ((v.w & 0x7f7f7f7fu) + 0x01010101u);
       }
       if (__any_sync(0xffffffffu, (marks & 0x80808080u) != 0)) {
-        for (int key = 0; key < kWarpKeys; ++key) {
-          const bool sees[2] = {mask[0].sees(key0 + key), mask[1].sees(key0 + key)};
+        for (int key = 0; key < 16 * taken; ++key) {
+          const int number = at.keys.tile_start(at.j + key / 16, kSplitTile) + warp * kWarpKeys + key % 16;
 #pragma unroll
           for (int c = 0; c < kChunks; ++c) {
-            const uint32_t v = *reinterpret_cast<const uint32_t *>(values + place(key, c) + (lane & 3) * 4);
+            const uint32_t v = *reinterpret_cast<const uint16_t *>(values + place(key, c) + g * 2);
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-              if ((v >> (8 * i) & 0x7f) == 0x7f) {
+            for (int e = 0; e < 2; ++e)
+              if ((v >> (8 * e) & 0x7f) == 0x7f) {
 #pragma unroll
-                for (int r = 0; r < 2; ++r)
-                  if (sees[r]) o[c][i & 1][2 * r + (i >> 1)] = NAN;
+                for (int b = 0; b < kBlocks8; ++b)
+#pragma unroll
+                  for (int r = 0; r < 2; ++r)
+                    if (mask[b][r].sees(number)) o[b][c][2 * e + r] = NAN;
               }
           }
         }
         __syncwarp();
-        for (int i = lane; i < kWarpKeys * D / 4; i += 32) {
+        for (int i = lane; i < kKeys * D / 4; i += 32) {
           uint32_t *const v = reinterpret_cast<uint32_t *>(values) + i;
           *v &= ~((((*v & 0x7f7f7f7fu) + 0x01010101u & 0x80808080u) >> 7) * 0xffu);
         }
         __syncwarp();
       }
     }
-    {
-      const int key = lane & 15;
+#pragma unroll
+    for (int i = 0; i < kUnits; ++i) {
+      const int key = 16 * i + (lane & 15);
 #pragma unroll
       for (int c = 0; c < kChunks; c += 2) {
-        uint32_t b[4];
-        ldmatrix_x4_trans(b, kb + kWarpKeys * D + place(key, c + (lane >> 4)));
+        uint32_t v[4];  // keys 0..7 and 8..15 of chunk c, then of the next
+        ldmatrix_x4_trans(v, kb + kKeys * D + place(key, c + (lane >> 4)));
 #pragma unroll
-        for (int i = 0; i < 4; ++i) b[i] = sort_pairs(b[i]);
-        mma_16816<__half>(o[c][0], pf, halves_low(b[0]), halves_low(b[1]));
-        mma_16816<__half>(o[c][1], pf, halves_high(b[0]), halves_high(b[1]));
-        mma_16816<__half>(o[c + 1][0], pf, halves_low(b[2]), halves_low(b[3]));
-        mma_16816<__half>(o[c + 1][1], pf, halves_high(b[2]), halves_high(b[3]));
+        for (int e = 0; e < 2; ++e) {
+          const uint32_t lo = sort_pairs(v[2 * e]), hi = sort_pairs(v[2 * e + 1]);
+          const uint32_t a[4] = {halves_low(lo), halves_high(lo), halves_low(hi), halves_high(hi)};
+#pragma unroll
+          for (int b = 0; b < kBlocks8; ++b) mma_16816<__half>(o[b][c + e], a, pf[b][i][0], pf[b][i][1]);
+        }
       }
     }
     __syncwarp();
     stage = stage + 1 == Shape::kStages ? 0 : stage + 1;
 
-    const bool keys_end = at.j + 1 == at.units;
-    if (kWhole || (!keys_end && u + 1 < u1)) {
-      ++at.j;
+    const bool keys_end = at.j + taken == at.units;
+    if (kWhole || (!keys_end && u + taken < u1)) {
+      at.j += taken;
       continue;
     }
     end_rows(keys_end && seg_j0 == 0);
 
     first_segment = false;
     fresh = true;
-    if (u + 1 < u1) at.advance(p);
+    if (u + taken < u1) {
+      at.j += taken - 1;
+      at.advance(p);
+    }
   }
   cp_async_wait<0>();
   if constexpr (kWhole) end_rows(true);
