@@ -719,7 +719,7 @@ typedef struct {
  * cpkv_append_quantised — cpkv_append_rotary into quantised rows.  The rotated key
  * element x1 c - x2 s (x2 c + x1 s) is quantised from its exact value: neither the
  * products nor their sum are rounded before.  Queries are rotated as there.
- *   h_row          key_dim 64 or 128 (a multiple of 8 with keep_keys), value_dim 64 or a
+ *   h_row          key_dim 64 or 128 (a multiple of 8 up to 512 with keep_keys), value_dim 64 or a
  *                  multiple of 128; keys that are kept are rounded to the element type
  *   other arguments, status bits and errors: as cpkv_append_rotary (LIMIT: widths that
  *   cannot be quantised; ARG: parts of a row that overlap or lie outside it).

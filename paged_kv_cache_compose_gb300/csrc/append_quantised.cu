@@ -1,15 +1,15 @@
 // cpkv_append_quantised: new keys and values into quantised rows, keys (and
 // queries beside them) rotated by their positions on the way.
 //
-// A rotated key element is y = a c - b s (or b c + a s).  It is rounded to 16 bits
-// nowhere on its way to e4m3, and not to 32 either in a way that shows: next to the
-// border between two e4m3 numbers a product rounded to 32 bits can fall on the other
-// side (one element in about 2^19), and the row would depend on the order of three
-// instructions.  So products are held as pairs (a rounded product and its exact rest),
-// and their sum is rounded "to odd": a 32-bit number whose last bit says that
-// something follows rounds to e4m3 as the exact sum does.  Some twenty instructions
-// more an element of the keys; bytes bound the call all the same (44600 tokens of 32 + 8
-// heads of 128 in fp16, half of a head rotated).
+// A rotated key element is y = a c - b s (or b c + a s), and what is kept is e4m3 of y over the
+// group's scale.  In 32 bits y is off by less than 2^-23 of |a c| + |b s|, which falls on the
+// wrong side of a border between two e4m3 numbers for one element in about 2^18: the row
+// would depend on the order of three instructions.  So each element is rounded from below and
+// from above its error, and where the two differ (or the group's scale does) the head is
+// worked out again exactly: products as pairs (a rounded product and its exact rest),
+// their sum rounded "to odd", a 32-bit number whose last bit says that something follows,
+// which rounds to e4m3 as the exact sum does.  Bytes bound the call (5.6 TB/s
+// on 44600 tokens of 32 + 8 heads of 128, in 181 us) nearly as much as instructions do.
 #include "append.cuh"
 #include "quantised.cuh"
 
@@ -19,12 +19,14 @@ namespace {
 struct QuantisedParams {
   AppendParams a;
   int64_t ks_off, vs_off;  // bytes of the scales in a row
-  int value_first;         // first thread of a token that works on values
+  int keys_kept;           // keys stay in 16 bits
+  int lane_shift;          // 2^lane_shift lanes take a head, 16 elements each
+  int group_threads;       // of a group of values: 8, or 4
   int value_units;         // 16 elements each
-  int key_heads_kept;      // keys stay in 16 bits
-  int group_threads;       // threads of a group of values: 8, or 4
-  int key_threads;         // of a key head
-  FastDiv by_group;
+  // A token's work in turns of a warp: query heads, key heads, values; turn i is that of
+  // warp i % parts of the token.
+  int q_turns, k_turns, v_turns, k_first, v_first;  // k_first: q_turns % parts; v_first: (q_turns + k_turns) % parts
+  FastDiv parts;
 };
 
 // x y exactly, as a rounded product and the rest.
@@ -58,19 +60,81 @@ CPKV_DEV float largest_of(float x, int threads) {
   return x;
 }
 
-// The largest magnitude of 16 finite elements; infinite ones become NaNs.
-CPKV_DEV float largest_of16(float (&y)[16]) {
-  float top = 0.f;
+// The largest magnitude of a group's finite elements, 16 of them this thread's.  Infinities
+// and NaNs (acc + 0 y is one then) are rare: infinite ones become NaNs, and are no largest.
+CPKV_DEV float largest_of16(float (&y)[16], int threads) {
+  float top = fabsf(y[0]), marks = 0.f;
 #pragma unroll
   for (int i = 0; i < 16; ++i) {
-    y[i] = finite_or_nan(y[i]);
-    top = fmaxf(top, fabsf(y[i]));  // a NaN is no largest
+    top = fmaxf(top, fabsf(y[i]));
+    marks = __fmaf_rn(y[i], 0.f, marks);
   }
-  return top;
+  if (marks != 0.f) {
+    top = 0.f;
+    for (int i = 0; i < 16; ++i) {
+      y[i] = finite_or_nan(y[i]);
+      top = fmaxf(top, fabsf(y[i]));
+    }
+  }
+  return largest_of(top, threads);
+}
+
+// The same of 16-bit elements as they are, two at a time: their bits order like their
+// magnitudes, infinities and NaNs last.
+template <typename T>
+CPKV_DEV bool largest_of16(const uint4 &a, const uint4 &b, int threads, float *top) {
+  constexpr uint32_t kInfinite = std::is_same<T, __half>::value ? 0x7c00u : 0x7f80u, kAll = 0x7fff7fffu;
+  const uint32_t w = __vmaxu2(__vmaxu2(__vmaxu2(a.x & kAll, a.y & kAll), __vmaxu2(a.z & kAll, a.w & kAll)),
+                              __vmaxu2(__vmaxu2(b.x & kAll, b.y & kAll), __vmaxu2(b.z & kAll, b.w & kAll)));
+  const uint32_t most = max(w & 0xffffu, w >> 16);
+  *top = largest_of(unpack2<T>(most).x, threads);  // of NaNs none
+  const uint32_t first = (threadIdx.x & 31) & ~(uint32_t)(threads - 1), mask = ((1u << threads) - 1) << first;
+  return __any_sync(mask, most >= kInfinite) == 0;
 }
 
 CPKV_DEV uint2 pack8(const float *y, float f) {
   return make_uint2(pack_e4m3(y[0] * f, y[1] * f, y[2] * f, y[3] * f), pack_e4m3(y[4] * f, y[5] * f, y[6] * f, y[7] * f));
+}
+
+// Whether a condition holds for all threads of a group.
+CPKV_DEV bool all_of(bool ok, int threads) {
+  const uint32_t first = (threadIdx.x & 31) & ~(uint32_t)(threads - 1), mask = ((1u << threads) - 1) << first;
+  return __all_sync(mask, ok) != 0;
+}
+
+// Quantises a thread's 16 elements, each known to the error d of its pair; false where what
+// comes out may depend on the errors, or an element is infinite or a NaN.
+template <bool kPairs>
+CPKV_DEV bool quantise_surely(const float *y, const float *d, int threads, GroupScale *g, uint2 *lo, uint2 *hi) {
+  float top = 0.f, off = 0.f, marks = 0.f;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    top = fmaxf(top, fabsf(y[i]));
+    marks = __fmaf_rn(y[i], 0.f, marks);
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) off = fmaxf(off, d[i]);
+  const float most = largest_of(top + off, threads), least = largest_of(top - off, threads);
+  *g = group_scale(most);
+  const float f = g->inverse;
+  uint32_t below[4], above[4];
+#pragma unroll
+  for (int w = 0; w < 4; ++w) {
+    float a[4], b[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int i = 4 * w + k;
+      const float z = y[i] * f, e = d[kPairs ? i / 2 : i % 8] * f;
+      a[k] = z - e;
+      b[k] = z + e;
+    }
+    below[w] = pack_e4m3(a[0], a[1], a[2], a[3]);
+    above[w] = pack_e4m3(b[0], b[1], b[2], b[3]);
+  }
+  *lo = make_uint2(below[0], below[1]);
+  *hi = make_uint2(below[2], below[3]);
+  return marks == 0.f && group_scale(least).scale == g->scale && below[0] == above[0] && below[1] == above[1] && below[2] == above[2] &&
+         below[3] == above[3];
 }
 
 template <typename T>
@@ -79,130 +143,195 @@ CPKV_DEV void unpack8(const uint4 &v, float *y) {
   y[0] = a.x, y[1] = a.y, y[2] = b.x, y[3] = b.y, y[4] = c.x, y[5] = c.y, y[6] = d.x, y[7] = d.y;
 }
 
-// A thread's unit is 16 elements: of a head, 8 frequencies' elements (two 16-byte
-// vectors) or 16 plain ones; of the values, 16 in a row.  A group's threads lie side by
-// side in a warp, a token's threads come in eights, so that the largest magnitude is
-// found by shuffles and each row is written once.
-template <typename T, bool kPairs, bool kAxes, int kEach>
-CPKV_DEV void quantise_work(const QuantisedParams &p, const Work<kAxes> &w) {
-  const AppendParams &a = p.a;
-  const int n = w.n, u = w.u;
-  const bool ok = w.positions_ok(a);
-  if (u >= a.rotated) {  // values
-    const int first = u - p.value_first;
-    if (first < 0) return;  // between the heads and the values
-    const char *src = a.v + n * a.v_stride;
-    uint4 x[kEach][2];
-#pragma unroll
-    for (int e = 0; e < kEach; ++e) {
-      const int c = first + e * a.value_groups;
-      if (c < p.value_units) x[e][0] = ld_stream16(src + c * 32), x[e][1] = ld_stream16(src + c * 32 + 16);
-    }
-    char *const row = ok ? slot_row(a, w.slot, false) : nullptr;
-    if (row == nullptr) return;
-#pragma unroll
-    for (int e = 0; e < kEach; ++e) {
-      const int c = first + e * a.value_groups;
-      if (c >= p.value_units) continue;
-      float y[16];
-      unpack8<T>(x[e][0], y);
-      unpack8<T>(x[e][1], y + 8);
-      const GroupScale g = group_scale(largest_of(largest_of16(y), p.group_threads));
-      const uint2 lo = pack8(y, g.inverse), hi = pack8(y + 8, g.inverse);
-      *reinterpret_cast<uint4 *>(row + a.v_off + c * 16) = make_uint4(lo.x, lo.y, hi.x, hi.y);
-      if ((c & (p.group_threads - 1)) == 0)
-        *reinterpret_cast<float *>(row + p.vs_off + div_by(c, p.by_group) * 4) = g.scale;
-    }
-    return;
-  }
+struct ExactUnit {
+  uint2 lo, hi;
+  float scale;
+};
 
-  const int first = div_by(u, a.head_units), unit = u - first * (int)a.head_units.d;
+// A unit of a key head, exactly; all threads of the head call.  Read again and apart, so that
+// the usual way needs no registers for it.
+template <typename T, bool kPairs, bool kAxes>
+__device__ __noinline__ ExactUnit exact_unit(const QuantisedParams &p, const Work<kAxes> &w, int head, int unit) {
+  const AppendParams &a = p.a;
   const bool turns = unit * 8 < a.half;
+  const int a0 = turns && !kPairs ? unit * 16 : unit * 32, a1 = turns && !kPairs ? a0 + a.half * 2 : a0 + 16;
+  const char *const src = a.k + w.n * a.k_stride + head * (a.key_dim * 2);
+  float v[16], y[16];
+  unpack8<T>(ld_stream16(src + a0), v);
+  unpack8<T>(ld_stream16(src + a1), v + 8);
+  float c[8], s[8];
+  if (turns) {
+    angles4<kAxes>(a, w, unit * 8, c, s);
+    angles4<kAxes>(a, w, unit * 8 + 4, c + 4, s + 4);
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int one = kPairs ? 2 * i : i, two = kPairs ? 2 * i + 1 : i + 8;
+    y[one] = v[one];
+    y[two] = v[two];
+    if (turns) {
+      const Exact ac = product(v[one], c[i]), bc = product(v[two], c[i]), as = product(v[one], s[i]), bs = product(v[two], s[i]);
+      y[one] = sum_to_odd(ac, Exact{-bs.hi, -bs.lo});
+      y[two] = sum_to_odd(bc, as);
+    }
+  }
+  const GroupScale g = group_scale(largest_of16(y, 1 << p.lane_shift));
+  return ExactUnit{pack8(y, g.inverse), pack8(y + 8, g.inverse), g.scale};
+}
+
+// A warp takes a token, or one of `parts` shares of it where tokens are few: its row and
+// angles are looked up once for all its heads.  A unit is 16 elements: of a head, 8
+// frequencies' elements (two 16-byte vectors) or 16 plain ones; of the values, 16 in a
+// row.  A group's threads lie side by side in a warp, so that its largest magnitude is found
+// by shuffles and each row is written once.
+template <typename T, bool kPairs, bool kAxes, int kAtOnce>
+CPKV_DEV void quantise_token(const QuantisedParams &p, const Work<kAxes> &w, int part) {
+  const AppendParams &a = p.a;
+  const int n = w.n, lane = threadIdx.x & 31, parts = p.parts.d;
+  const bool ok = w.positions_ok(a), reports = part == 0 && lane == 0;
+  if (!ok && reports) raise_status(a.status, CPKV_STATUS_POS_OOB);
+  char *const row = ok ? slot_row(a, w.slot, reports) : nullptr;
+  const int unit = lane & ((1 << p.lane_shift) - 1), sub = lane >> p.lane_shift, heads = 32 >> p.lane_shift;  // of a turn
   const int head_bytes = a.key_dim * 2;
+  const bool turns = unit * 8 < a.half;
   const int a0 = turns && !kPairs ? unit * 16 : unit * 32;  // plain units follow the rotated 2 half elements
   const int a1 = turns && !kPairs ? a0 + a.half * 2 : a0 + 16;
-  const bool two = a1 < head_bytes;
-  const char *const q = a.q + n * a.q_stride, *const k = a.k + n * a.k_stride;
-  char *const q_out = a.q_out + n * a.q_out_stride;
-  uint4 x0[kEach], x1[kEach];
-#pragma unroll
-  for (int e = 0; e < kEach; ++e) {
-    const int head = first + e * a.head_groups;
-    if (head >= a.heads) continue;
-    const char *src = head < a.q_heads ? q + head * head_bytes : k + (head - a.q_heads) * head_bytes;
-    x0[e] = ld_stream16(src + a0);
-    if (two) x1[e] = ld_stream16(src + a1);
-  }
+  const bool one = a0 < head_bytes, two = a1 < head_bytes;
   float c[8], s[8];
   if (turns && ok) {
     angles4<kAxes>(a, w, unit * 8, c, s);
     angles4<kAxes>(a, w, unit * 8 + 4, c + 4, s + 4);
   }
-  if (!ok && u == 0) raise_status(a.status, CPKV_STATUS_POS_OOB);
-  char *const row = ok ? slot_row(a, w.slot, u == 0) : nullptr;
+  {
+    const char *const src = a.q + n * a.q_stride;
+    char *const dst = a.q_out + n * a.q_out_stride;
+    for (int i = part; i < p.q_turns; i += kAtOnce * parts) {
+      uint4 x0[kAtOnce], x1[kAtOnce];
 #pragma unroll
-  for (int e = 0; e < kEach; ++e) {
-    const int head = first + e * a.head_groups;
-    if (head >= a.heads) continue;
-    if (head >= a.q_heads && !p.key_heads_kept) {  // a quantised key head
-      if (row == nullptr) continue;
-      float v[16], y[16];  // a thread's first, then its second vector
-      unpack8<T>(x0[e], v);
-      unpack8<T>(x1[e], v + 8);
-      if (turns) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int one = kPairs ? 2 * i : i, two_ = kPairs ? 2 * i + 1 : i + 8;
-          const Exact ac = product(v[one], c[i]), bc = product(v[two_], c[i]);
-          const Exact as = product(v[one], s[i]), bs = product(v[two_], s[i]);
-          y[one] = sum_to_odd(ac, Exact{-bs.hi, -bs.lo});
-          y[two_] = sum_to_odd(bc, as);
-        }
-      } else {
-#pragma unroll
-        for (int i = 0; i < 16; ++i) y[i] = v[i];
+      for (int e = 0; e < kAtOnce; ++e) {
+        const int head = (i + e * parts) * heads + sub;
+        x0[e] = x1[e] = make_uint4(0, 0, 0, 0);
+        if (head >= a.q_heads || !ok) continue;  // (a token that is dropped has queries of zeros)
+        if (one) x0[e] = ld_stream16(src + head * head_bytes + a0);
+        if (two) x1[e] = ld_stream16(src + head * head_bytes + a1);
       }
-      const GroupScale g = group_scale(largest_of(largest_of16(y), p.key_threads));
-      char *const dst = row + a.k_off + (head - a.q_heads) * a.key_dim;
-      *reinterpret_cast<uint2 *>(dst + (a0 >> 1)) = pack8(y, g.inverse);
-      *reinterpret_cast<uint2 *>(dst + (a1 >> 1)) = pack8(y + 8, g.inverse);
-      if (unit == 0) *reinterpret_cast<float *>(row + p.ks_off + (head - a.q_heads) * 4) = g.scale;
+#pragma unroll
+      for (int e = 0; e < kAtOnce; ++e) {
+        const int head = (i + e * parts) * heads + sub;
+        if (head >= a.q_heads) continue;
+        if (turns && ok) rotate_unit<T, kPairs>(x0[e], x1[e], c, s);
+        if (one) *reinterpret_cast<uint4 *>(dst + head * head_bytes + a0) = x0[e];
+        if (two) *reinterpret_cast<uint4 *>(dst + head * head_bytes + a1) = x1[e];
+      }
+    }
+  }
+  if (row == nullptr) return;
+  for (int i = part - p.k_first + (part < p.k_first ? parts : 0); i < p.k_turns; i += parts) {
+    const int head = i * heads + sub;
+    if (head >= a.heads - a.q_heads) continue;
+    const char *const src = a.k + n * a.k_stride + head * head_bytes;
+    uint4 x0 = make_uint4(0, 0, 0, 0), x1 = x0;
+    if (one) x0 = ld_stream16(src + a0);
+    if (two) x1 = ld_stream16(src + a1);
+    if (p.keys_kept) {
+      if (turns) rotate_unit<T, kPairs>(x0, x1, c, s);
+      char *const dst = row + a.k_off + head * head_bytes;
+      if (one) *reinterpret_cast<uint4 *>(dst + a0) = x0;
+      if (two) *reinterpret_cast<uint4 *>(dst + a1) = x1;
       continue;
     }
-    char *dst;
-    if (head < a.q_heads) {
-      dst = q_out + head * head_bytes;
-      if (!ok) x0[e] = x1[e] = make_uint4(0, 0, 0, 0);
-    } else {
-      if (row == nullptr) continue;
-      dst = row + a.k_off + (head - a.q_heads) * head_bytes;
+    float y[16], d[8];  // a thread's first, then its second vector; bounds of the errors of y
+    unpack8<T>(x0, y);
+    unpack8<T>(x1, y + 8);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const int i1 = kPairs ? 2 * k : k, i2 = kPairs ? 2 * k + 1 : k + 8;
+      d[k] = 0.f;
+      if (turns) {
+        const float v1 = y[i1], v2 = y[i2];
+        y[i1] = __fmaf_rn(v1, c[k], -__fmul_rn(v2, s[k]));
+        y[i2] = __fmaf_rn(v2, c[k], __fmul_rn(v1, s[k]));
+        d[k] = (fabsf(v1) + fabsf(v2)) * (fmaxf(fabsf(c[k]), fabsf(s[k])) * 0x1p-22f);
+      }
     }
-    if (turns && ok) rotate_unit<T, kPairs>(x0[e], x1[e], c, s);
-    *reinterpret_cast<uint4 *>(dst + a0) = x0[e];
-    if (two) *reinterpret_cast<uint4 *>(dst + a1) = x1[e];
+    GroupScale g;
+    uint2 lo, hi;
+    const bool sure = quantise_surely<kPairs>(y, d, 1 << p.lane_shift, &g, &lo, &hi);
+    if (!all_of(sure, 1 << p.lane_shift)) {
+      const ExactUnit exact = exact_unit<T, kPairs, kAxes>(p, w, head, unit);
+      lo = exact.lo;
+      hi = exact.hi;
+      g.scale = exact.scale;
+    }
+    char *const dst = row + a.k_off + head * a.key_dim;
+    *reinterpret_cast<uint2 *>(dst + (a0 >> 1)) = lo;
+    *reinterpret_cast<uint2 *>(dst + (a1 >> 1)) = hi;
+    if (unit == 0) *reinterpret_cast<float *>(row + p.ks_off + head * 4) = g.scale;
+  }
+  for (int i = part - p.v_first + (part < p.v_first ? parts : 0); i < p.v_turns; i += parts) {
+    const int at = i * 32 + lane;
+    if (at >= p.value_units) continue;
+    const char *const src = a.v + n * a.v_stride + at * 32;
+    const uint4 x0 = ld_stream16(src), x1 = ld_stream16(src + 16);
+    float y[16], top;
+    const bool finite = largest_of16<T>(x0, x1, p.group_threads, &top);
+    unpack8<T>(x0, y);
+    unpack8<T>(x1, y + 8);
+    if (!finite) top = largest_of16(y, p.group_threads);
+    const GroupScale g = group_scale(top);
+    const uint2 lo = pack8(y, g.inverse), hi = pack8(y + 8, g.inverse);
+    *reinterpret_cast<uint4 *>(row + a.v_off + at * 16) = make_uint4(lo.x, lo.y, hi.x, hi.y);
+    if ((at & (p.group_threads - 1)) == 0)
+      *reinterpret_cast<float *>(row + p.vs_off + (at >> (p.group_threads == 8 ? 3 : 2)) * 4) = g.scale;
   }
 }
 
-template <typename T, bool kPairs, bool kAxes, int kEach>
-__global__ void __launch_bounds__(kAppendThreads) append_quantised_kernel(const __grid_constant__ QuantisedParams p) {
-  const int64_t total = (int64_t)p.a.n_tokens * p.a.threads.d, step = (int64_t)gridDim.x * kAppendThreads;
-  Work<kAxes> w = find_work<kAxes>(p.a, (int64_t)blockIdx.x * kAppendThreads + threadIdx.x, total);
-  while (w.id < total) {  // a token's threads come in eights: a group's go on together
-    const Work<kAxes> next = find_work<kAxes>(p.a, w.id + step, total);
-    quantise_work<T, kPairs, kAxes, kEach>(p, w);
-    w = next;
+// What token n says of itself.
+template <bool kAxes>
+CPKV_DEV Work<kAxes> token_work(const AppendParams &p, int n) {
+  Work<kAxes> w;
+  w.n = n;
+  w.slot = p.slots[n];
+  w.pos[0] = p.positions[n];
+  if constexpr (kAxes) {
+#pragma unroll
+    for (int a = 1; a < kMaxAxes; ++a) w.pos[a] = a < p.n_axes ? p.positions[a * p.pos_stride + n] : 0;
+  }
+  return w;
+}
+
+// kAtOnce turns of a token's queries have their loads in flight together: four where it has so
+// many, and then five blocks to an SM instead of six.  32 heads of 128 (eight turns): 197 us
+// with two and 181 with four for 44600 tokens; 16 heads of 64 (two turns): 171 and 191 us for 131072.
+constexpr int append_blocks(int at_once) { return at_once == 4 ? 5 : 6; }
+
+template <typename T, bool kPairs, bool kAxes, int kAtOnce>
+__global__ void __launch_bounds__(kAppendThreads, append_blocks(kAtOnce)) append_quantised_kernel(const __grid_constant__ QuantisedParams p) {
+  const int64_t jobs = (int64_t)p.a.n_tokens * p.parts.d, step = (int64_t)gridDim.x * (kAppendThreads / 32);
+  int64_t job = (int64_t)blockIdx.x * (kAppendThreads / 32) + (threadIdx.x >> 5);
+  auto token_of = [&](int64_t id) { return id < INT32_MAX ? div_by((int)id, p.parts) : (int)(id / p.parts.d); };
+  if (job >= jobs) return;
+  Work<kAxes> w = token_work<kAxes>(p.a, token_of(job));
+  while (true) {
+    const int64_t next = job + step;
+    Work<kAxes> then;
+    if (next < jobs) then = token_work<kAxes>(p.a, token_of(next));
+    quantise_token<T, kPairs, kAxes, kAtOnce>(p, w, (int)(job - (int64_t)w.n * p.parts.d));
+    if (next >= jobs) return;
+    job = next;
+    w = then;
   }
 }
 
-template <typename T, int kEach>
+template <typename T, int kAtOnce>
 auto quantised_kernel(bool pairs, bool axes) {
-  if (pairs) return axes ? append_quantised_kernel<T, true, true, kEach> : append_quantised_kernel<T, true, false, kEach>;
-  return axes ? append_quantised_kernel<T, false, true, kEach> : append_quantised_kernel<T, false, false, kEach>;
+  if (pairs) return axes ? append_quantised_kernel<T, true, true, kAtOnce> : append_quantised_kernel<T, true, false, kAtOnce>;
+  return axes ? append_quantised_kernel<T, false, true, kAtOnce> : append_quantised_kernel<T, false, false, kAtOnce>;
 }
 
 template <typename T>
-auto quantised_kernel(bool pairs, bool axes, int each) {
-  return each == 1 ? quantised_kernel<T, 1>(pairs, axes) : quantised_kernel<T, 2>(pairs, axes);
+auto quantised_kernel(bool pairs, bool axes, bool many) {
+  return many ? quantised_kernel<T, 4>(pairs, axes) : quantised_kernel<T, 2>(pairs, axes);
 }
 
 }  // namespace
@@ -258,24 +387,22 @@ extern "C" int cpkv_append_quantised(int64_t n_tokens, int page_size, int cp_siz
   p.a.v_off = row.value_offset;
   p.ks_off = row.key_scale_offset;
   p.vs_off = row.value_scale_offset;
-  p.key_heads_kept = row.keep_keys != 0;
+  p.keys_kept = row.keep_keys != 0;
   p.group_threads = value_group(row) / 16;
-  p.by_group = fast_div((uint32_t)p.group_threads);
-  p.key_threads = row.key_dim / 16;
   p.value_units = row.kv_heads * row.value_dim / 16;
-  const int head_units = (row.key_dim + 15) / 16;
-  // Two heads (16 values twice) a thread once that leaves every SM its 1024 threads,
-  // one before, as in the append without quantisation.
-  const int64_t units = n_tokens * ((int64_t)p.a.heads * head_units + p.value_units);
-  const int each = units >= (int64_t)device_sm_count() * 2 * 1024 ? 2 : 1;
-  p.a.head_groups = (int)ceil_div(p.a.heads, each);
-  p.a.value_groups = (int)ceil_div(ceil_div(p.value_units, each), 8) * 8;
-  p.a.rotated = p.a.head_groups * head_units;
-  p.value_first = (int)ceil_div(p.a.rotated, 8) * 8;
-  p.a.head_units = fast_div((uint32_t)head_units);
-  p.a.threads = fast_div((uint32_t)(p.value_first + p.a.value_groups));
-  const bool pairs = flags & CPKV_ROTARY_INTERLEAVED, axes = n_axes > 1;
-  auto kernel = dtype == CPKV_BF16 ? quantised_kernel<__nv_bfloat16>(pairs, axes, each) : quantised_kernel<__half>(pairs, axes, each);
-  const int grid = persistent_grid((const void *)kernel, kAppendThreads, 0, 16, ceil_div(n_tokens * (int64_t)p.a.threads.d, kAppendThreads));
+  while (16 << p.lane_shift < row.key_dim) ++p.lane_shift;
+  const int heads = 32 >> p.lane_shift;
+  p.q_turns = (int)ceil_div(q_heads, heads);
+  p.k_turns = (int)ceil_div(row.kv_heads, heads);
+  p.v_turns = (int)ceil_div(p.value_units, 32);
+  // A warp a token once that gives every SM its warps, shares of tokens before.
+  const int64_t turns = p.q_turns + p.k_turns + p.v_turns, warps = (int64_t)device_sm_count() * append_blocks(4) * (kAppendThreads / 32);
+  const int parts = (int)std::min<int64_t>(std::max<int64_t>(warps / n_tokens, 1), turns);
+  p.parts = fast_div((uint32_t)parts);
+  p.k_first = p.q_turns % parts;
+  p.v_first = (p.q_turns + p.k_turns) % parts;
+  const bool pairs = flags & CPKV_ROTARY_INTERLEAVED, axes = n_axes > 1, many = p.q_turns >= 4;
+  auto kernel = dtype == CPKV_BF16 ? quantised_kernel<__nv_bfloat16>(pairs, axes, many) : quantised_kernel<__half>(pairs, axes, many);
+  const int grid = persistent_grid((const void *)kernel, kAppendThreads, 0, 16, ceil_div(n_tokens * parts, kAppendThreads / 32));
   return launch_kernel(kernel, dim3(grid), dim3(kAppendThreads), 0, false, (cudaStream_t)stream, p);
 }

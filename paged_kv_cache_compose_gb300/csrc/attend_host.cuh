@@ -186,8 +186,11 @@ struct TileBounds {
 inline bool few_rows(int64_t max_rows) { return max_rows <= kSplitRows; }
 
 // Quantised rows that a tile pass brings to the element type beforehand (attend_unpack.cuh):
-// where the sequences have kUnpackTiles row tiles each or more, and the dense rows fit kUnpackMost.
-// PLACEHOLDER
+// where the sequences have kUnpackTiles row tiles each or more, and the dense rows fit
+// kUnpackMost (the passes over the rows themselves need next to no memory).  5 requests of
+// 16384 keys, 32 heads of 128 on 8, beforehand and on the way: one row tile 186 and 118 us, two
+// 261 and 224, three 300 and 287, four 432 and 462, six 494 and 560, eight 679 and 824; 32
+// requests with four 1956 and 1965.
 struct UnpackBounds {
   int64_t pages = 0, stride = 0;
   int sequences = 0;

@@ -33,7 +33,7 @@ inline RowParts row_parts(const cpkv_quantised_row &r) {
 inline int check_quantised_row(const cpkv_quantised_row *r) {
   if (r == nullptr || r->kv_heads < 1 || r->key_dim <= 0 || r->value_dim <= 0) return CPKV_ERR_ARG;
   if (r->kv_heads > 1024 || r->key_dim > 4096 || r->value_dim > 4096) return CPKV_ERR_LIMIT;
-  if (r->keep_keys ? r->key_dim % 8 != 0 : r->key_dim != 64 && r->key_dim != 128) return CPKV_ERR_LIMIT;
+  if (r->keep_keys ? r->key_dim % 8 != 0 || r->key_dim > 512 : r->key_dim != 64 && r->key_dim != 128) return CPKV_ERR_LIMIT;
   if (r->value_dim != 64 && r->value_dim % kValueGroup != 0) return CPKV_ERR_LIMIT;
   const RowParts parts = row_parts(*r);
   for (int i = 0; i < 4; ++i) {
