@@ -642,25 +642,24 @@ __global__ void __launch_bounds__(tile_threads(kQuantised), 1) attend_tile_kerne
   } else if (warp < kProducts) {
     // ---------------------------------------------------------------- keys and values
     if constexpr (kQuantised) {
-    // A lane looks up one key; its warp brings in those 16 keys, 16 e4m3 elements a lane
-    // and pass: by cp.async to a place of the lane's own, from there, times their scale and in
-    // the element type, into the operand.  Through registers alone the same loads took
-    // half as long again: with this much shared memory in use, the first-level cache that
-    // they pass through holds too few of them (prefill 3.6 ms, 2.4 without the loads).
+    // A lane has one key of the warp's 16 and half its vector (lanes 0..15 the first half):
+    // it looks the key up and brings 16 e4m3 elements at a time by cp.async to a place of its own,
+    // from there, times their scale and in the element type, into the operand, and shares
+    // nothing with the other lanes.  Through registers alone the same loads took half as long
+    // again: with this much shared memory in use, the first-level cache that they pass through
+    // holds too few of them.  The instructions of the conversion (about 45 for 16 elements)
+    // set the pace, beside the softmax's: a prefill of 3.02 ms took 3.06 with addresses and
+    // scales shuffled between lanes, and 3.67 with four warps of them (2.13 over plain rows).
     shrink_registers<kLoadRegistersQ>();
     const int lw = warp - 8;
-    constexpr int kKeys = kTileKeys / kLoadWarps, kLanes = D / 16, kAtOnce = 32 / kLanes, kPasses = kKeys / kAtOnce;  // of an operand
+    constexpr int kKeys = kTileKeys / kLoadWarps, kPasses = D / 32;                 // of an operand
     constexpr int kTurns = 2 * kPasses / kTurn, kAhead = Shape::kRawTurns - 1;      // of a tile; on their way
-    const int cc = lane % kLanes, odd = cc >> 2;  // lanes of the upper 64 elements begin with their second chunk: no bank twice
+    static_assert(kKeys == 16 && kPasses % kTurn == 0 && kAhead <= kTurns, "lanes, passes and turns");
+    const int half = lane >> 4;
     char *const ring = pieces + lw * (Shape::kRawTurns * kTurn * 512) + lane * 16;
-    int to[2][D == 128 ? 2 : 1];  // this lane's two chunks of 8 elements; of D = 128 every other pass lies 4 keys on
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-      for (int e = 0; e < (D == 128 ? 2 : 1); ++e) {
-        const int r = e * kAtOnce + lane / kLanes, c = 2 * cc + (h ^ odd);
-        to[h][e] = (c >> 3) * (kTileKeys * 128) + (lw * kKeys + r) * 128 + (((c & 7) ^ (r & 7)) << 4);
-      }
+    // this lane's row of an operand; 16-byte chunk c of it lies at c ^ (row % 8)
+    const int row = lw * kKeys + lane % kKeys;
+    const int to = half * (D == 128 ? kTileKeys * 128 : 0) + row * 128 + ((row & 7) << 4), flip = D == 128 ? 0 : half * 64;
     bool ok = true;
     uint32_t loaded = 0;         // key tiles
     int fill = 0, empty = 0;     // places in the ring of the next turn to issue and to convert
@@ -669,19 +668,20 @@ __global__ void __launch_bounds__(tile_threads(kQuantised), 1) attend_tile_kerne
       const int n = item.n, j0 = item.j0, n_sink = item.keys.n_sink, first_tile = item.keys.first_tile;
       const int lo = item.there.lo, hi = item.there.hi, sink_end = item.there.sink_end;
       const int32_t *const pages = item.pages;
-      const int64_t k_at = p.io.k_off + (int64_t)item.h * D + cc * 16, v_at = p.io.v_off + (int64_t)item.h * D + cc * 16;
-      const int64_t ks_at = p.io.ks_off + (int64_t)item.h * 4, vs_at = p.io.vs_off + (int64_t)item.h * 4;
+      const int h = item.h;
       item_read(k);
       int key = 0, page = -1;
       auto look_up = [&](int j) {  // this lane's key of a tile, and its page
-        key = (j < n_sink ? j : first_tile + j - n_sink) * kTileKeys + lw * kKeys + lane % kKeys;
+        key = (j < n_sink ? j : first_tile + j - n_sink) * kTileKeys + row;
         if (!(key < sink_end || (key >= lo && key < hi))) key = -1;
         page = key >= 0 ? pages[div_by(key, p.pools.page_size)] : -1;
       };
-      const char *at = nullptr;             // row of this lane's key, in the tile that is issued; null: none
-      float k_scale = 0.f, v_scale = 0.f;   // its scales
+      // of this lane's key in the tile that is issued: its half vectors (zeros where there is none) and scales
+      const char *from[2] = {nullptr, nullptr};
+      int bytes = 0;
+      float k_scale = 0.f, v_scale = 0.f;
       auto resolve = [&] {
-        at = nullptr;
+        const char *at = nullptr;
         if (key >= 0) {
           at = page_address(p.pools, page);
           if (at == nullptr) {
@@ -690,17 +690,20 @@ __global__ void __launch_bounds__(tile_threads(kQuantised), 1) attend_tile_kerne
             at += (int64_t)(key - div_by(key, p.pools.page_size) * (int)p.pools.page_size.d) * p.pools.row_bytes;
           }
         }
-        k_scale = at == nullptr ? 0.f : __ldg(reinterpret_cast<const float *>(at + ks_at));
-        v_scale = at == nullptr ? 0.f : __ldg(reinterpret_cast<const float *>(at + vs_at));
+        const char *const zeros = reinterpret_cast<const char *>(zero_row);
+        bytes = at == nullptr ? 0 : 16;
+        from[0] = at == nullptr ? zeros : at + p.io.k_off + (h * D + half * (D / 2));
+        from[1] = at == nullptr ? zeros : at + p.io.v_off + (h * D + half * (D / 2));
+        k_scale = at == nullptr ? 0.f : __ldg(reinterpret_cast<const float *>(at + p.io.ks_off) + h);
+        v_scale = at == nullptr ? 0.f : __ldg(reinterpret_cast<const float *>(at + p.io.vs_off) + h);
       };
       auto issue = [&](int turn, bool there) {  // turn of the tile in hand
         if (there) {
           const uint32_t dst = smem_addr(ring + fill * (kTurn * 512));
 #pragma unroll
           for (int e = 0; e < kTurn; ++e) {
-            const int pass = turn * kTurn + e, which = pass / kPasses, i = pass % kPasses;
-            const char *const row = reinterpret_cast<const char *>(__shfl_sync(0xffffffffu, (unsigned long long)at, i * kAtOnce + lane / kLanes));
-            cp_async16_or_zeros(dst + e * 512, row == nullptr ? (const char *)zero_row : row + (which ? v_at : k_at), row == nullptr ? 0 : 16);
+            const int pass = turn * kTurn + e;
+            cp_async16_or_zeros(dst + e * 512, from[pass / kPasses] + pass % kPasses * 16, bytes);
           }
           fill = fill + 1 == Shape::kRawTurns ? 0 : fill + 1;
         }
@@ -737,13 +740,12 @@ __global__ void __launch_bounds__(tile_threads(kQuantised), 1) attend_tile_kerne
           for (int e = 0; e < kTurn; ++e) x[e] = *reinterpret_cast<const uint4 *>(ring + empty * (kTurn * 512) + e * 512);
           empty = empty + 1 == Shape::kRawTurns ? 0 : empty + 1;
           char *const operand = (which ? v_smem : k_smem) + stage * Shape::kOperand;
+          const float s = which ? vs : ks;
 #pragma unroll
           for (int e = 0; e < kTurn; ++e) {
-            const int i = (turn * kTurn + e) % kPasses;
-            const float s = __shfl_sync(0xffffffffu, which ? vs : ks, i * kAtOnce + lane / kLanes);
-            char *const on = operand + (D == 128 ? i / 2 * 1024 : i * 1024);
-            *reinterpret_cast<uint4 *>(on + to[0][D == 128 ? i & 1 : 0]) = read_back8<T>(odd ? make_uint2(x[e].z, x[e].w) : make_uint2(x[e].x, x[e].y), s);
-            *reinterpret_cast<uint4 *>(on + to[1][D == 128 ? i & 1 : 0]) = read_back8<T>(odd ? make_uint2(x[e].x, x[e].y) : make_uint2(x[e].z, x[e].w), s);
+            const int c = (turn * kTurn + e) % kPasses * 2;  // the first of this half's two chunks of 8 elements
+            *reinterpret_cast<uint4 *>(operand + (to ^ (flip + c * 16))) = read_back8<T>(make_uint2(x[e].x, x[e].y), s);
+            *reinterpret_cast<uint4 *>(operand + (to ^ (flip + c * 16 + 16))) = read_back8<T>(make_uint2(x[e].z, x[e].w), s);
           }
           if ((turn + 1) * kTurn % kPasses == 0) mbar_arrive(which ? &bars.v_full[stage] : &bars.k_full[stage]);
         }
@@ -753,9 +755,7 @@ __global__ void __launch_bounds__(tile_threads(kQuantised), 1) attend_tile_kerne
       if (warp == 8 && lane == 0 && n == 0) mbar_arrive(&bars.wanted);
     }
     cp_async_wait_all();
-    if (lane == 0) {
-      atomicSub(&bars.loaders, 1);
-    }
+    if (lane == 0) atomicSub(&bars.loaders, 1);
     } else {
     // A lane looks up one key; its warp brings in those 32 keys.  Without a box it
     // leaves the address in shared memory and copies one 16-byte chunk of several
