@@ -4,9 +4,10 @@ Requests share a prompt's pages.  Their own first tokens are rotated into rows
 (append_rotary), composed behind the prefix (compose_fused) and attended to in
 the dense buffer (attend_window); the same rows go to the pools, where each
 decode step appends a token per request and attends to the shared prompt once
-(attend_shared) and to each request's own rows.
+(attend_shared) and to each request's own rows.  With quantised rows (QuantisedCache) the same calls
+work on half the bytes.
 
-    python examples/serving_step.py
+    python examples/serving_step.py [--quantised]
 """
 import os
 import sys
@@ -16,7 +17,7 @@ import torch
 
 sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
 
-from paged_kv_cache_compose_gb300.runtime import ComposeLayers, ComposePlan, PagedCache  # noqa: E402
+from paged_kv_cache_compose_gb300.runtime import ComposeLayers, ComposePlan, PagedCache, QuantisedCache  # noqa: E402
 
 PAGE, OWNERS, HEADS, KV_HEADS, DIM = 16, 2, 8, 2, 64
 PREFIX, OWN, STEPS = 64, [20, 5, 33], 3  # prompt tokens, each request's own tokens, decode steps
@@ -32,10 +33,14 @@ def random_heads(gen, tokens: int, heads: int, device) -> torch.Tensor:
     return torch.randn(tokens, heads, DIM, generator=gen).to(torch.bfloat16).to(device)
 
 
-def run(seed: int = 0, device: str = "cuda") -> dict:
+def run(seed: int = 0, device: str = "cuda", quantised: bool = False) -> dict:
     """The loop's inputs and results, for a check from outside."""
     gen = torch.Generator().manual_seed(seed)
-    requests, width = len(OWN), 2 * KV_HEADS * DIM
+    requests = len(OWN)
+    if quantised:
+        Cache, dtype, width = QuantisedCache, torch.uint8, QuantisedCache.row_bytes(KV_HEADS, DIM)
+    else:
+        Cache, dtype, width = PagedCache, torch.bfloat16, 2 * KV_HEADS * DIM
     turns = rope_table(PREFIX + max(OWN) + STEPS, DIM, device)
     # pages: the prompt's, then each request's own with room for the decode steps
     prompt_pages = PREFIX // PAGE
@@ -43,8 +48,8 @@ def run(seed: int = 0, device: str = "cuda") -> dict:
     order = 1 + torch.randperm(prompt_pages + sum(own_pages), generator=gen)
     prompt, rest = order[:prompt_pages], order[prompt_pages:].split(own_pages)
     cap = int(order.max()) // OWNERS + 1
-    pools = [torch.zeros(cap, PAGE, width, dtype=torch.bfloat16, device=device) for _ in range(OWNERS)]
-    cache = PagedCache(pools, page_size=PAGE, kv_heads=KV_HEADS, key_dim=DIM)
+    pools = [torch.zeros(cap, PAGE, width, dtype=dtype, device=device) for _ in range(OWNERS)]
+    cache = Cache(pools, page_size=PAGE, kv_heads=KV_HEADS, key_dim=DIM)
     table = torch.zeros(requests, max(own_pages), dtype=torch.int32)
     for b, pages in enumerate(rest):
         table[b, :len(pages)] = pages
@@ -63,16 +68,16 @@ def run(seed: int = 0, device: str = "cuda") -> dict:
     total = sum(OWN)
     q, k, v = (random_heads(gen, total, h, device) for h in (HEADS, KV_HEADS, KV_HEADS))
     positions = torch.cat([PREFIX + torch.arange(n, dtype=torch.int32) for n in OWN]).to(device)
-    rows = torch.empty(total, 1, width, dtype=torch.bfloat16, device=device)
-    writer = PagedCache([rows], page_size=1, kv_heads=KV_HEADS, key_dim=DIM, dense=True)
+    rows = torch.empty(total, 1, width, dtype=dtype, device=device)
+    writer = Cache([rows], page_size=1, kv_heads=KV_HEADS, key_dim=DIM, dense=True)
     q = writer.append_rotary(k, v, torch.arange(total, device=device), positions, turns, q=q)
     cur_pages = torch.cat([table[b, :-(-n // PAGE)] for b, n in enumerate(OWN)])
     plan = ComposePlan([PREFIX] * requests, OWN, prompt.repeat(requests).numpy(), cur_pages.numpy(), np.zeros(len(cur_pages), np.int32),
                        page_size=PAGE, cp_size=OWNERS, num_pool_pages=cap * OWNERS, device=device).build()
-    layers = ComposeLayers(plan, 2 * width, num_dense=1)
+    layers = ComposeLayers(plan, rows[0].nbytes, num_dense=1)
     dense = layers.dense[0]
     layers.compose_fused([p.view(torch.uint8) for p in pools], [rows.view(torch.uint8).view(total, -1), dense[:0]], dense)
-    composed = PagedCache([dense.view(torch.bfloat16).view(-1, PAGE, width)], page_size=PAGE, kv_heads=KV_HEADS, key_dim=DIM, dense=True)
+    composed = Cache([dense.view(dtype).view(-1, PAGE, width)], page_size=PAGE, kv_heads=KV_HEADS, key_dim=DIM, dense=True)
     pages = [prompt_pages + -(-n // PAGE) for n in OWN]
     dense_table = torch.zeros(requests, max(pages), dtype=torch.int32)
     for b, n in enumerate(pages):
@@ -102,7 +107,7 @@ def run(seed: int = 0, device: str = "cuda") -> dict:
 
 
 if __name__ == "__main__":
-    got = run()
+    got = run(quantised="--quantised" in sys.argv[1:])
     assert not any(got["status"]), got["status"]
     assert torch.equal(got["prefill"], got["paged"])
     off = max(float((a.float() - b.float()).abs().max()) for a, b in zip(got["decode"], got["window"]))

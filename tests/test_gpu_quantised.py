@@ -251,3 +251,37 @@ def test_read_wants_its_shapes():
     for bad in (slots.int(), slots.cpu(), slots[::2], slots[None]):
         with pytest.raises(cpkv.CpkvError):
             cache.read_rows(bad)
+
+
+@pytest.mark.parametrize("n, hq", [(3, 4), (700, 32)])
+def test_append_takes_slices_and_rotates_in_place(n, hq):
+    """Queries, keys and values as slices of one projection's output; the queries rotated where they stand."""
+    rng = np.random.default_rng(n)
+    hkv, d, ps = 2, 128, 16
+    qkv = tensor(rng.standard_normal((n, hq + 2 * hkv, d)), BF16).cuda()
+    pools = model.Pools(-(-n // ps) + 1, ps, 2, QuantisedRow.of(hkv, d), BF16)
+    slots = torch.from_numpy(ps + rng.permutation(n)).cuda()
+    table, pos = torch.from_numpy(turns(rng, 100, d)).cuda(), torch.from_numpy(rng.integers(0, 100, n).astype(np.int32)).cuda()
+    one, two = cache_of(pools, BF16), cache_of(pools, BF16)
+    q, k, v = qkv[:, :hq], qkv[:, hq:hq + hkv], qkv[:, hq + hkv:]
+    want = one.append_rotary(k.contiguous(), v.contiguous(), slots, pos, table, q=q.contiguous())
+    two.append_rotary(k, v, slots, pos, table, q=q, q_out=q)
+    assert torch.equal(q, want) and all(torch.equal(a, b) for a, b in zip(one.table.pools, two.table.pools))
+    assert int(one.d_status) == 0 and int(two.d_status) == 0
+
+
+def test_calls_run_with_the_pools_device_current():
+    """Of a device that is not there, the switch to it fails before anything else."""
+    pools = model.Pools(3, 16, 1, QuantisedRow.of(2, 64), BF16)
+    cache = cache_of(pools, BF16)
+    none = torch.zeros(0, dtype=torch.int64, device="cuda")
+    stream = torch.cuda.current_stream().cuda_stream
+    cache.read_rows(none)
+    cache.table._table.device = torch.cuda.device_count()
+    rows = torch.zeros(0, 2, 64, dtype=BF16, device="cuda")
+    for call in (lambda: cache.read_rows(none, k_out=rows, stream=stream),
+                 lambda: cache.append_rotary(rows, rows, none, none.int(), torch.ones(8, 64, device="cuda"), stream=stream)):
+        with pytest.raises(RuntimeError) as e:
+            call()
+        assert not isinstance(e.value, cpkv.CpkvError)
+    assert torch.cuda.current_device() == 0

@@ -1,4 +1,7 @@
 """Attention over quantised rows on the GPU against plain 64-bit implementations on the numbers that the rows hold."""
+import importlib.util
+import pathlib
+
 import numpy as np
 import pytest
 import torch
@@ -81,7 +84,7 @@ def test_window_reads_nothing_that_no_query_sees(case):
 
 
 @pytest.mark.parametrize("what", ["element", "scale"])
-@pytest.mark.parametrize("case", MIXED, ids=name)
+@pytest.mark.parametrize("case", MIXED + [(8, 1, 64, 16, 2, BF16, 0, 0, [200], [333]), (16, 2, 128, 24, 2, FP16, 50, 3, [150, 90], [400, 90])], ids=name)
 def test_window_no_numbers_reach_only_the_rows_that_see_them(case, what):
     """Keys and values that are no numbers (an element of them, or their scale) where some query tokens see them and others do not."""
     hq, hkv, d, ps, cp, dtype, w, sinks, q_lens, kv_lens = case
@@ -289,9 +292,9 @@ def test_shared_reports_bad_pages():
 
 # --------------------------------------------------------------------------- graphs, workspaces, waits, refusals
 
-@pytest.mark.parametrize("tokens", [1, 24], ids=["split", "tile"])
+@pytest.mark.parametrize("tokens", [1, 24, 260], ids=["split", "tile", "unpacked"])
 def test_in_a_graph_on_another_stream_follows_the_lengths(tokens):
-    case = (8, 2, 128, 16, 2, BF16, 100, 4, [tokens] * 3, [300, 90, 200])
+    case = (8, 2, 128, 16, 2, BF16, 100, 4, [tokens] * 3, [300, 290, 280])
     rng, pools, table, q = window_case(case)
     cache = cache_of(pools, BF16)
     lens = torch.full((3,), tokens, dtype=torch.int32).cuda()
@@ -461,3 +464,18 @@ def test_a_serving_run_on_quantised_rows():
         model.check(one, None, want, BF16)
         model.check(two, None, want, BF16)
     assert int(cache.d_status) == 0 and int(plain.d_status) == 0
+
+
+def test_example_of_a_serving_step_on_quantised_rows():
+    """Compose, append and both attentions together on quantised rows, as examples/serving_step.py runs them."""
+    path = pathlib.Path(__file__).parents[1] / "examples" / "serving_step.py"
+    spec = importlib.util.spec_from_file_location("serving_step", path)
+    example = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(example)
+    got = example.run(quantised=True)
+    assert not any(got["status"])
+    assert torch.equal(got["prefill"], got["paged"])
+    u = model.bound_of(BF16)
+    for a, b in zip(got["decode"], got["window"]):  # each within its own bound: a step of weights and of the result
+        a, b = a.double(), b.double()
+        assert bool(((a - b).abs() <= 2 * u * b.abs() + 2 * (u + 2.0**-13) * 5).all())  # weighted |values| below 5

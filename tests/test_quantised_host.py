@@ -155,3 +155,25 @@ def test_window_refusals(lib, changed, code):
     (dict(n_prefix=1), cpkv.CPKV_ERR_CAPACITY), (dict(max_suffix=65), cpkv.CPKV_ERR_CAPACITY), (dict(suffix=None), cpkv.CPKV_ERR_ARG)], ids=str)
 def test_shared_refusals(lib, changed, code):
     assert call(shared_args(), lib.cpkv_attend_shared_quantised, **changed) == code
+
+
+def test_workspace_sizes(lib):
+    """Many query rows: room for the rows that they see, in 16 bits, as far as a window lets them see; never more than 4 GiB of it."""
+    def size(*args, **more):
+        return cpkv.cpkv_attend_window_quantised_workspace_bytes(*args, **more)
+
+    def plain(*args, **more):
+        return cpkv.cpkv_attend_window_workspace_bytes(*args, **more)
+
+    for few in ((1, 4, 1, 64, None, 100), (64, 32, 8, 128, None, 100_000), (3, 32, 8, 128, [100, 100, 100], 5000)):
+        assert size(*few) == plain(*few)
+    many = (2, 32, 8, 128, [400, 300], 20_000)
+    rows = 2 * -(-20_000 // 32) * 32 * 8 * 128 * 4
+    assert rows <= size(*many) - plain(*many) <= rows + (1 << 20)
+    assert size(*many, window=512) - plain(*many, window=512) <= (2 * (512 + 400 + 64 + 96)) * 8 * 128 * 4
+    huge = (64, 32, 8, 128, [400] * 64, 1_000_000)
+    assert size(*huge) == plain(*huge)
+    for bad in (dict(head_dim=96), dict(B=1025), dict(q_heads=3), dict(window=-1), dict(max_kv_len=-1)):
+        args = dict(B=1, q_heads=4, kv_heads=2, head_dim=64, q_lens=None, max_kv_len=10)
+        with pytest.raises(cpkv.CpkvError):
+            size(**{**args, **bad})
