@@ -9,10 +9,10 @@
 // elements only the parts below 2^-39 of that one round.  The values' scales t_j go into
 // the weights,
 //   o_i = sum_j 2^(x_ij + log2 t_j - n_i) v_j,   l_i = sum_j 2^(x_ij - m_i),
-// with a maximum n_i of their own, so that neither a row of zeros (t_j = 2^-126) nor a
-// large one costs the other weights their bits.  One conversion a pair of elements and a
-// second exponential a score: with e4m3 * scale in the element type it were five
-// instructions a pair.
+// with a reference n_i of their own, so that neither a row of zeros (t_j = 2^-126) nor a
+// large one costs the other weights their bits.  m_i and n_i follow the largest exponents with a
+// little slack (kSlackQ).  One conversion a pair of elements and a second exponential a score:
+// with e4m3 * scale in the element type it were five instructions a pair.
 //
 // Keys and values are the first operand, of 16 keys (or 16 elements) by 16, and the queries
 // (the weights) the second, 8 rows at a time: a key converted once serves 8 rows, or 16 with
@@ -21,6 +21,12 @@
 // chunk c of a key are elements 16 c + 4 t .. + 3 (t = lane % 4), so the queries' fragments hold
 // those; values come by transposed pairs of bytes, sorted into two columns of keys by one
 // permutation, so a lane's outputs are elements 16 c + 2 g and + 1 (g = lane / 4) of rows 2 t and + 1.
+//
+// Measured with the joining pass: 64 requests of 8 query rows, 8 heads of 64, the last 4096 of up
+// to 65536 keys, 65.9 us (4.3 TB/s; instructions issue in 60% of the cycles), 96.7 with queries and
+// weights as the first operand and 16 rows always; 12 requests of 12 query rows on 8 heads of 128,
+// up to 16384 keys in one-token pages, 67.9 us (3.8 TB/s).  A unit at a time, with half the
+// loads in flight and a vote for each: 77 and 73 us.
 #pragma once
 
 #include "attend_split.cuh"
@@ -31,12 +37,13 @@ namespace cpkv {
 // kBlocks8 8 rows at a time: 1 or 2.
 template <int D, SplitMode kMode, int kBlocks8>
 struct SplitShapeQ {
-  static constexpr int kUnits = 2;                    // units that a warp takes at once
+  static constexpr int kUnits = 2;                         // units that a warp takes at once
   static constexpr int kKeys = kUnits * kWarpKeys;         // its keys of them
   static constexpr int kVectors = 2 * kKeys * D;           // keys, then values
   static constexpr int kStage = kVectors + 2 * kKeys * 4;  // then their scales
   static constexpr int kStages = kMode == kFewKeys ? 3 : 2;
-  static constexpr int kBlocks = kMode == kFewKeys ? 1 : kBlocks8 == 1 ? (D == 128 ? 3 : 5) : (D == 128 ? 2 : 3);  // blocks to an SM
+  // Blocks to an SM: as many as registers and two stages in shared memory allow.
+  static constexpr int kBlocks = kMode == kFewKeys ? 1 : kBlocks8 == 1 ? (D == 128 ? 3 : 5) : (D == 128 ? 2 : 3);
   static constexpr int kRing = kSplitWarps * kStages * kStage;
   static constexpr int kJoin = 8 * kBlocks8 * D * 4;  // half the columns of two warps while a sequence's parts are joined
   static constexpr int kSmem = kRing + kJoin + kSplitWarps * kSplitRows * 8;

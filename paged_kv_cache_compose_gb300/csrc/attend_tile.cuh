@@ -22,6 +22,10 @@
 //                      another.  Requests go by number, whatever their lengths.
 //   warps 14, 15       the next item's queries: two blocks of 128 rows, of which an item
 //                      of at most 128 rows takes one, the items in turn.
+// Over quantised rows (of few row tiles: many are read back first, attend_unpack.cuh) eight
+// warps load, from the ninth on, and the others follow; they bring a key's e4m3 elements, times
+// its scale, into shared memory in the element type, and the softmax holds half a row of scores
+// at a time, for the registers that they take.
 // Of an item with at most 128 rows the two tiles are the same rows over every other
 // 128 keys (two streams), joined at the end.
 // Tensor memory (512 columns): scores of the tiles at 0 and 128, outputs at 256
@@ -35,6 +39,9 @@
 // decode step of 256 requests on a prefix of 65536: 0.55 ms, 1.02 PFLOP/s.
 // With the products issued by one lane of a diverged warp, or operands worked out by
 // it, the same prefill took 2.65 ms, with copies by cp.async alone 4.0 ms.
+// Quantised rows: 48 requests of three prefixes of about 9000 keys in 50.3 us (42.6 over plain
+// rows, twice their bytes), 5 requests of 64 tokens on 8192 keys in 68 us (the tensor pipe is
+// busy 37% of them): the conversion's instructions and the softmax's bound it together.
 #pragma once
 
 #include <cuda.h>
@@ -634,233 +641,233 @@ __global__ void __launch_bounds__(tile_threads(kQuantised), 1) attend_tile_kerne
         const bool bad = row < rows && item.nq > 1 && my_n > 0 && !(m.x == 0.f && m.y == 0.f);
         if (bad)
           mend_row<T, D, S, kQuantised>(p, item, &bars.deadline, token, head, base, l,
-                          p.io.out + out_token * p.io.out_stride + (int64_t)head * (D * 2),
-                          p.direct ? nullptr : p.space.o + slot_row * D);
+                                        p.io.out + out_token * p.io.out_stride + (int64_t)head * (D * 2),
+                                        p.direct ? nullptr : p.space.o + slot_row * D);
         item_read(k);
       }
     }
   } else if (warp < kProducts) {
     // ---------------------------------------------------------------- keys and values
     if constexpr (kQuantised) {
-    // A lane has one key of the warp's 16 and half its vector (lanes 0..15 the first half):
-    // it looks the key up and brings 16 e4m3 elements at a time by cp.async to a place of its own,
-    // from there, times their scale and in the element type, into the operand, and shares
-    // nothing with the other lanes.  Through registers alone the same loads took half as long
-    // again: with this much shared memory in use, the first-level cache that they pass through
-    // holds too few of them.  The instructions of the conversion (about 45 for 16 elements)
-    // set the pace, beside the softmax's: a prefill of 3.02 ms took 3.06 with addresses and
-    // scales shuffled between lanes, and 3.67 with four warps of them (2.13 over plain rows).
-    shrink_registers<kLoadRegistersQ>();
-    const int lw = warp - 8;
-    constexpr int kKeys = kTileKeys / kLoadWarps, kPasses = D / 32;                 // of an operand
-    constexpr int kTurns = 2 * kPasses / kTurn, kAhead = Shape::kRawTurns - 1;      // of a tile; on their way
-    static_assert(kKeys == 16 && kPasses % kTurn == 0 && kAhead <= kTurns, "lanes, passes and turns");
-    const int half = lane >> 4;
-    char *const ring = pieces + lw * (Shape::kRawTurns * kTurn * 512) + lane * 16;
-    // this lane's row of an operand; 16-byte chunk c of it lies at c ^ (row % 8)
-    const int row = lw * kKeys + lane % kKeys;
-    const int to = half * (D == 128 ? kTileKeys * 128 : 0) + row * 128 + ((row & 7) << 4), flip = D == 128 ? 0 : half * 64;
-    bool ok = true;
-    uint32_t loaded = 0;         // key tiles
-    int fill = 0, empty = 0;     // places in the ring of the next turn to issue and to convert
-    for (int k = 0; ok && item_there(k); ++k) {
-      const TileItem &item = items[k % kItemSlots];
-      const int n = item.n, j0 = item.j0, n_sink = item.keys.n_sink, first_tile = item.keys.first_tile;
-      const int lo = item.there.lo, hi = item.there.hi, sink_end = item.there.sink_end;
-      const int32_t *const pages = item.pages;
-      const int h = item.h;
-      item_read(k);
-      int key = 0, page = -1;
-      auto look_up = [&](int j) {  // this lane's key of a tile, and its page
-        key = (j < n_sink ? j : first_tile + j - n_sink) * kTileKeys + row;
-        if (!(key < sink_end || (key >= lo && key < hi))) key = -1;
-        page = key >= 0 ? pages[div_by(key, p.pools.page_size)] : -1;
-      };
-      // of this lane's key in the tile that is issued: its half vectors (zeros where there is none) and scales
-      const char *from[2] = {nullptr, nullptr};
-      int bytes = 0;
-      float k_scale = 0.f, v_scale = 0.f;
-      auto resolve = [&] {
-        const char *at = nullptr;
-        if (key >= 0) {
-          at = page_address(p.pools, page);
-          if (at == nullptr) {
-            raise_status(status, CPKV_STATUS_PAGE_OOB);
-          } else {
-            at += (int64_t)(key - div_by(key, p.pools.page_size) * (int)p.pools.page_size.d) * p.pools.row_bytes;
+      // A lane has one key of the warp's 16 and half its vector (lanes 0..15 the first half):
+      // it looks the key up and brings 16 e4m3 elements at a time by cp.async to a place of its own,
+      // from there, times their scale and in the element type, into the operand, and shares
+      // nothing with the other lanes.  Through registers alone the same loads took half as long
+      // again: with this much shared memory in use, the first-level cache that they pass through
+      // holds too few of them.  The instructions of the conversion (about 45 for 16 elements)
+      // set the pace, beside the softmax's: a prefill of 3.02 ms took 3.06 with addresses and
+      // scales shuffled between lanes, and 3.67 with four warps of them (2.13 over plain rows).
+      shrink_registers<kLoadRegistersQ>();
+      const int lw = warp - 8;
+      constexpr int kKeys = kTileKeys / kLoadWarps, kPasses = D / 32;                 // of an operand
+      constexpr int kTurns = 2 * kPasses / kTurn, kAhead = Shape::kRawTurns - 1;      // of a tile; on their way
+      static_assert(kKeys == 16 && kPasses % kTurn == 0 && kAhead <= kTurns, "lanes, passes and turns");
+      const int half = lane >> 4;
+      char *const ring = pieces + lw * (Shape::kRawTurns * kTurn * 512) + lane * 16;
+      // this lane's row of an operand; 16-byte chunk c of it lies at c ^ (row % 8)
+      const int row = lw * kKeys + lane % kKeys;
+      const int to = half * (D == 128 ? kTileKeys * 128 : 0) + row * 128 + ((row & 7) << 4), flip = D == 128 ? 0 : half * 64;
+      bool ok = true;
+      uint32_t loaded = 0;         // key tiles
+      int fill = 0, empty = 0;     // places in the ring of the next turn to issue and to convert
+      for (int k = 0; ok && item_there(k); ++k) {
+        const TileItem &item = items[k % kItemSlots];
+        const int n = item.n, j0 = item.j0, n_sink = item.keys.n_sink, first_tile = item.keys.first_tile;
+        const int lo = item.there.lo, hi = item.there.hi, sink_end = item.there.sink_end;
+        const int32_t *const pages = item.pages;
+        const int h = item.h;
+        item_read(k);
+        int key = 0, page = -1;
+        auto look_up = [&](int j) {  // this lane's key of a tile, and its page
+          key = (j < n_sink ? j : first_tile + j - n_sink) * kTileKeys + row;
+          if (!(key < sink_end || (key >= lo && key < hi))) key = -1;
+          page = key >= 0 ? pages[div_by(key, p.pools.page_size)] : -1;
+        };
+        // of this lane's key in the tile that is issued: its half vectors (zeros where there is none) and scales
+        const char *from[2] = {nullptr, nullptr};
+        int bytes = 0;
+        float k_scale = 0.f, v_scale = 0.f;
+        auto resolve = [&] {
+          const char *at = nullptr;
+          if (key >= 0) {
+            at = page_address(p.pools, page);
+            if (at == nullptr) {
+              raise_status(status, CPKV_STATUS_PAGE_OOB);
+            } else {
+              at += (int64_t)(key - div_by(key, p.pools.page_size) * (int)p.pools.page_size.d) * p.pools.row_bytes;
+            }
           }
-        }
-        const char *const zeros = reinterpret_cast<const char *>(zero_row);
-        bytes = at == nullptr ? 0 : 16;
-        from[0] = at == nullptr ? zeros : at + p.io.k_off + (h * D + half * (D / 2));
-        from[1] = at == nullptr ? zeros : at + p.io.v_off + (h * D + half * (D / 2));
-        k_scale = at == nullptr ? 0.f : __ldg(reinterpret_cast<const float *>(at + p.io.ks_off) + h);
-        v_scale = at == nullptr ? 0.f : __ldg(reinterpret_cast<const float *>(at + p.io.vs_off) + h);
-      };
-      auto issue = [&](int turn, bool there) {  // turn of the tile in hand
-        if (there) {
-          const uint32_t dst = smem_addr(ring + fill * (kTurn * 512));
+          const char *const zeros = reinterpret_cast<const char *>(zero_row);
+          bytes = at == nullptr ? 0 : 16;
+          from[0] = at == nullptr ? zeros : at + p.io.k_off + (h * D + half * (D / 2));
+          from[1] = at == nullptr ? zeros : at + p.io.v_off + (h * D + half * (D / 2));
+          k_scale = at == nullptr ? 0.f : __ldg(reinterpret_cast<const float *>(at + p.io.ks_off) + h);
+          v_scale = at == nullptr ? 0.f : __ldg(reinterpret_cast<const float *>(at + p.io.vs_off) + h);
+        };
+        auto issue = [&](int turn, bool there) {  // turn of the tile in hand
+          if (there) {
+            const uint32_t dst = smem_addr(ring + fill * (kTurn * 512));
 #pragma unroll
-          for (int e = 0; e < kTurn; ++e) {
-            const int pass = turn * kTurn + e;
-            cp_async16_or_zeros(dst + e * 512, from[pass / kPasses] + pass % kPasses * 16, bytes);
+            for (int e = 0; e < kTurn; ++e) {
+              const int pass = turn * kTurn + e;
+              cp_async16_or_zeros(dst + e * 512, from[pass / kPasses] + pass % kPasses * 16, bytes);
+            }
+            fill = fill + 1 == Shape::kRawTurns ? 0 : fill + 1;
           }
-          fill = fill + 1 == Shape::kRawTurns ? 0 : fill + 1;
-        }
-        cp_async_commit();
-      };
-      if (n > 0) {
-        look_up(j0);
-        resolve();
+          cp_async_commit();
+        };
+        if (n > 0) {
+          look_up(j0);
+          resolve();
 #pragma unroll
-        for (int turn = 0; turn < kAhead; ++turn) issue(turn, true);
-        if (n > 1) look_up(j0 + 1);
+          for (int turn = 0; turn < kAhead; ++turn) issue(turn, true);
+          if (n > 1) look_up(j0 + 1);
+        }
+        for (int it = 0; it < n; ++it) {
+          const int stage = loaded % kStages;
+          const bool reuse = loaded >= kStages, more = it + 1 < n;
+          const uint32_t freed = (loaded / kStages - 1) & 1;
+          ++loaded;
+          const float ks = k_scale, vs = v_scale;
+#pragma unroll
+          for (int turn = 0; turn < kTurns; ++turn) {
+            if (turn + kAhead == kTurns && more) {  // what is issued from here on is the next tile's
+              resolve();
+              if (it + 2 < n) look_up(j0 + it + 2);
+            }
+            const int which = turn * kTurn / kPasses;  // keys, then values
+            if (turn * kTurn % kPasses == 0) {
+              ok = all(!reuse || wait_or_stop(which ? &bars.v_empty[stage] : &bars.k_empty[stage], freed));
+              if (!ok) break;
+            }
+            issue((turn + kAhead) % kTurns, turn + kAhead < kTurns || more);
+            cp_async_wait<kAhead>();
+            uint4 x[kTurn];
+#pragma unroll
+            for (int e = 0; e < kTurn; ++e) x[e] = *reinterpret_cast<const uint4 *>(ring + empty * (kTurn * 512) + e * 512);
+            empty = empty + 1 == Shape::kRawTurns ? 0 : empty + 1;
+            char *const operand = (which ? v_smem : k_smem) + stage * Shape::kOperand;
+            const float s = which ? vs : ks;
+#pragma unroll
+            for (int e = 0; e < kTurn; ++e) {
+              const int c = (turn * kTurn + e) % kPasses * 2;  // the first of this half's two chunks of 8 elements
+              *reinterpret_cast<uint4 *>(operand + (to ^ (flip + c * 16))) = read_back8<T>(make_uint2(x[e].x, x[e].y), s);
+              *reinterpret_cast<uint4 *>(operand + (to ^ (flip + c * 16 + 16))) = read_back8<T>(make_uint2(x[e].z, x[e].w), s);
+            }
+            if ((turn + 1) * kTurn % kPasses == 0) mbar_arrive(which ? &bars.v_full[stage] : &bars.k_full[stage]);
+          }
+          if (!ok) break;
+          if (warp == 8 && lane == 0 && it == (n > kClaimAhead ? n - kClaimAhead : 0)) mbar_arrive(&bars.wanted);
+        }
+        if (warp == 8 && lane == 0 && n == 0) mbar_arrive(&bars.wanted);
       }
-      for (int it = 0; it < n; ++it) {
-        const int stage = loaded % kStages;
-        const bool reuse = loaded >= kStages, more = it + 1 < n;
-        const uint32_t freed = (loaded / kStages - 1) & 1;
-        ++loaded;
-        const float ks = k_scale, vs = v_scale;
+      cp_async_wait_all();
+      if (lane == 0) atomicSub(&bars.loaders, 1);
+    } else {
+      // A lane looks up one key; its warp brings in those 32 keys.  Without a box it
+      // leaves the address in shared memory and copies one 16-byte chunk of several
+      // keys.  Keys that no query of the sequence sees are copied from zeros.
+      shrink_registers<kOtherRegisters>();
+      const int lw = warp - 8;
+      constexpr int kLanes = D / 8, kRowsAtOnce = 32 / kLanes;
+      const int c = lane % kLanes;
+      const char *const zeros = reinterpret_cast<const char *>(zero_row);
+      ulonglong2 *mine = addresses + lw * 32;
+      const ulonglong2 *theirs = mine + lane / kLanes;
+      uint32_t to[8 / kRowsAtOnce];  // this lane's places repeat every 8 keys
 #pragma unroll
-        for (int turn = 0; turn < kTurns; ++turn) {
-          if (turn + kAhead == kTurns && more) {  // what is issued from here on is the next tile's
-            resolve();
-            if (it + 2 < n) look_up(j0 + it + 2);
+      for (int e = 0; e < 8 / kRowsAtOnce; ++e) {
+        const int r = e * kRowsAtOnce + lane / kLanes;
+        to[e] = (c >> 3) * (kTileKeys * 128) + (lw * 32 + r) * 128 + (((c & 7) ^ (r & 7)) << 4);
+      }
+      auto copy = [&](const char *operand, bool values) {
+        const uint32_t base = smem_addr(operand);
+#pragma unroll
+        for (int g = 0; g < 32 / kRowsAtOnce; ++g) {
+          const unsigned long long src = values ? theirs[g * kRowsAtOnce].y : theirs[g * kRowsAtOnce].x;
+          cp_async16(base + to[g % (8 / kRowsAtOnce)] + g / (8 / kRowsAtOnce) * 1024,
+                     reinterpret_cast<const char *>(src) + c * 16);
+        }
+      };
+      // this lane's box of the warp's: block of 64 elements, first key
+      const int boxes = p.box_rows ? 32 / p.box_rows * (D / 64) : 0;
+      const int box_block = lane % (D / 64), box_key = lane / (D / 64) * p.box_rows;
+      bool ok = true;
+      uint32_t operands = 0;
+      for (int k = 0; ok && item_there(k); ++k) {
+        const TileItem &item = items[k % kItemSlots];
+        const int n = item.n, j0 = item.j0, n_sink = item.keys.n_sink, first_tile = item.keys.first_tile;
+        const int lo = item.there.lo, hi = item.there.hi, sink_end = item.there.sink_end;
+        const int32_t *const pages = item.pages;
+        const int64_t k_at = p.io.k_off + (int64_t)item.h * D * 2, v_at = k_at + (p.io.v_off - p.io.k_off);
+        item_read(k);
+        int key = 0, page = -1;
+        auto look_up = [&](int j) {  // one tile ahead of its copies
+          key = (j < n_sink ? j : first_tile + j - n_sink) * kTileKeys + lw * 32 + lane;
+          if (!(key < sink_end || (key >= lo && key < hi))) key = -1;
+          page = key >= 0 ? pages[div_by(key, p.pools.page_size)] : -1;
+        };
+        if (n > 0) look_up(j0);
+        for (int it = 0; it < n; ++it) {
+          int owner = 0, pool_row = 0;
+          const char *at = nullptr;
+          if (key >= 0) {
+            const int in_page = key - div_by(key, p.pools.page_size) * (int)p.pools.page_size.d;
+            at = page_address(p.pools, page);
+            if (at == nullptr) {
+              raise_status(status, CPKV_STATUS_PAGE_OOB);
+            } else {
+              at += (int64_t)in_page * p.pools.row_bytes;
+              const int local = div_by(page, p.pools.cp);
+              owner = page - local * (int)p.pools.cp.d;
+              pool_row = local * (int)p.pools.page_size.d + in_page;
+            }
           }
-          const int which = turn * kTurn / kPasses;  // keys, then values
-          if (turn * kTurn % kPasses == 0) {
+          const bool by_box = boxes > 0 && __all_sync(0xffffffffu, at != nullptr);
+          if (by_box) {
+            owner = __shfl_sync(0xffffffffu, owner, box_key);
+            pool_row = __shfl_sync(0xffffffffu, pool_row, box_key);
+          } else {
+            __syncwarp();
+            mine[lane] = make_ulonglong2((unsigned long long)(at == nullptr ? zeros : at + k_at),
+                                         (unsigned long long)(at == nullptr ? zeros : at + v_at));
+            __syncwarp();
+          }
+          if (it + 1 < n) look_up(j0 + it + 1);
+          const uint32_t loaded = operands / 2;  // key tiles
+          const int stage = loaded % kStages;
+          const bool reuse = loaded >= kStages;
+          const uint32_t freed = (loaded / kStages - 1) & 1;
+#pragma unroll 1
+          for (int which = 0; which < 2; ++which) {  // keys, then values
+            uint64_t *full = which ? &bars.v_full[stage] : &bars.k_full[stage];
             ok = all(!reuse || wait_or_stop(which ? &bars.v_empty[stage] : &bars.k_empty[stage], freed));
             if (!ok) break;
-          }
-          issue((turn + kAhead) % kTurns, turn + kAhead < kTurns || more);
-          cp_async_wait<kAhead>();
-          uint4 x[kTurn];
-#pragma unroll
-          for (int e = 0; e < kTurn; ++e) x[e] = *reinterpret_cast<const uint4 *>(ring + empty * (kTurn * 512) + e * 512);
-          empty = empty + 1 == Shape::kRawTurns ? 0 : empty + 1;
-          char *const operand = (which ? v_smem : k_smem) + stage * Shape::kOperand;
-          const float s = which ? vs : ks;
-#pragma unroll
-          for (int e = 0; e < kTurn; ++e) {
-            const int c = (turn * kTurn + e) % kPasses * 2;  // the first of this half's two chunks of 8 elements
-            *reinterpret_cast<uint4 *>(operand + (to ^ (flip + c * 16))) = read_back8<T>(make_uint2(x[e].x, x[e].y), s);
-            *reinterpret_cast<uint4 *>(operand + (to ^ (flip + c * 16 + 16))) = read_back8<T>(make_uint2(x[e].z, x[e].w), s);
-          }
-          if ((turn + 1) * kTurn % kPasses == 0) mbar_arrive(which ? &bars.v_full[stage] : &bars.k_full[stage]);
-        }
-        if (!ok) break;
-        if (warp == 8 && lane == 0 && it == (n > kClaimAhead ? n - kClaimAhead : 0)) mbar_arrive(&bars.wanted);
-      }
-      if (warp == 8 && lane == 0 && n == 0) mbar_arrive(&bars.wanted);
-    }
-    cp_async_wait_all();
-    if (lane == 0) atomicSub(&bars.loaders, 1);
-    } else {
-    // A lane looks up one key; its warp brings in those 32 keys.  Without a box it
-    // leaves the address in shared memory and copies one 16-byte chunk of several
-    // keys.  Keys that no query of the sequence sees are copied from zeros.
-    shrink_registers<kOtherRegisters>();
-    const int lw = warp - 8;
-    constexpr int kLanes = D / 8, kRowsAtOnce = 32 / kLanes;
-    const int c = lane % kLanes;
-    const char *const zeros = reinterpret_cast<const char *>(zero_row);
-    ulonglong2 *mine = addresses + lw * 32;
-    const ulonglong2 *theirs = mine + lane / kLanes;
-    uint32_t to[8 / kRowsAtOnce];  // this lane's places repeat every 8 keys
-#pragma unroll
-    for (int e = 0; e < 8 / kRowsAtOnce; ++e) {
-      const int r = e * kRowsAtOnce + lane / kLanes;
-      to[e] = (c >> 3) * (kTileKeys * 128) + (lw * 32 + r) * 128 + (((c & 7) ^ (r & 7)) << 4);
-    }
-    auto copy = [&](const char *operand, bool values) {
-      const uint32_t base = smem_addr(operand);
-#pragma unroll
-      for (int g = 0; g < 32 / kRowsAtOnce; ++g) {
-        const unsigned long long src = values ? theirs[g * kRowsAtOnce].y : theirs[g * kRowsAtOnce].x;
-        cp_async16(base + to[g % (8 / kRowsAtOnce)] + g / (8 / kRowsAtOnce) * 1024,
-                   reinterpret_cast<const char *>(src) + c * 16);
-      }
-    };
-    // this lane's box of the warp's: block of 64 elements, first key
-    const int boxes = p.box_rows ? 32 / p.box_rows * (D / 64) : 0;
-    const int box_block = lane % (D / 64), box_key = lane / (D / 64) * p.box_rows;
-    bool ok = true;
-    uint32_t operands = 0;
-    for (int k = 0; ok && item_there(k); ++k) {
-      const TileItem &item = items[k % kItemSlots];
-      const int n = item.n, j0 = item.j0, n_sink = item.keys.n_sink, first_tile = item.keys.first_tile;
-      const int lo = item.there.lo, hi = item.there.hi, sink_end = item.there.sink_end;
-      const int32_t *const pages = item.pages;
-      const int64_t k_at = p.io.k_off + (int64_t)item.h * D * 2, v_at = k_at + (p.io.v_off - p.io.k_off);
-      item_read(k);
-      int key = 0, page = -1;
-      auto look_up = [&](int j) {  // one tile ahead of its copies
-        key = (j < n_sink ? j : first_tile + j - n_sink) * kTileKeys + lw * 32 + lane;
-        if (!(key < sink_end || (key >= lo && key < hi))) key = -1;
-        page = key >= 0 ? pages[div_by(key, p.pools.page_size)] : -1;
-      };
-      if (n > 0) look_up(j0);
-      for (int it = 0; it < n; ++it) {
-        int owner = 0, pool_row = 0;
-        const char *at = nullptr;
-        if (key >= 0) {
-          const int in_page = key - div_by(key, p.pools.page_size) * (int)p.pools.page_size.d;
-          at = page_address(p.pools, page);
-          if (at == nullptr) {
-            raise_status(status, CPKV_STATUS_PAGE_OOB);
-          } else {
-            at += (int64_t)in_page * p.pools.row_bytes;
-            const int local = div_by(page, p.pools.cp);
-            owner = page - local * (int)p.pools.cp.d;
-            pool_row = local * (int)p.pools.page_size.d + in_page;
-          }
-        }
-        const bool by_box = boxes > 0 && __all_sync(0xffffffffu, at != nullptr);
-        if (by_box) {
-          owner = __shfl_sync(0xffffffffu, owner, box_key);
-          pool_row = __shfl_sync(0xffffffffu, pool_row, box_key);
-        } else {
-          __syncwarp();
-          mine[lane] = make_ulonglong2((unsigned long long)(at == nullptr ? zeros : at + k_at),
-                                       (unsigned long long)(at == nullptr ? zeros : at + v_at));
-          __syncwarp();
-        }
-        if (it + 1 < n) look_up(j0 + it + 1);
-        const uint32_t loaded = operands / 2;  // key tiles
-        const int stage = loaded % kStages;
-        const bool reuse = loaded >= kStages;
-        const uint32_t freed = (loaded / kStages - 1) & 1;
-#pragma unroll 1
-        for (int which = 0; which < 2; ++which) {  // keys, then values
-          uint64_t *full = which ? &bars.v_full[stage] : &bars.k_full[stage];
-          ok = all(!reuse || wait_or_stop(which ? &bars.v_empty[stage] : &bars.k_empty[stage], freed));
-          if (!ok) break;
-          ++operands;
-          char *operand = (which ? v_smem : k_smem) + stage * Shape::kOperand;
-          if (by_box) {
-            if (lane < boxes) {
-              mbar_arrive_expect_tx(full, (uint32_t)p.box_rows * 128);
-              box_load(operand + box_block * (kTileKeys * 128) + (lw * 32 + box_key) * 128, &p.maps[owner],
-                       (int)((which ? v_at : k_at) >> 1) + box_block * 64, pool_row, full);
+            ++operands;
+            char *operand = (which ? v_smem : k_smem) + stage * Shape::kOperand;
+            if (by_box) {
+              if (lane < boxes) {
+                mbar_arrive_expect_tx(full, (uint32_t)p.box_rows * 128);
+                box_load(operand + box_block * (kTileKeys * 128) + (lw * 32 + box_key) * 128, &p.maps[owner],
+                         (int)((which ? v_at : k_at) >> 1) + box_block * 64, pool_row, full);
+              } else {
+                mbar_arrive(full);
+              }
             } else {
-              mbar_arrive(full);
+              copy(operand, which);
+              mbar_arrive_after_copies(full);
             }
-          } else {
-            copy(operand, which);
-            mbar_arrive_after_copies(full);
           }
+          if (!ok) break;
+          if (warp == 8 && lane == 0 && it == (n > kClaimAhead ? n - kClaimAhead : 0)) mbar_arrive(&bars.wanted);
         }
-        if (!ok) break;
-        if (warp == 8 && lane == 0 && it == (n > kClaimAhead ? n - kClaimAhead : 0)) mbar_arrive(&bars.wanted);
+        if (warp == 8 && lane == 0 && n == 0) mbar_arrive(&bars.wanted);
       }
-      if (warp == 8 && lane == 0 && n == 0) mbar_arrive(&bars.wanted);
-    }
-    if (lane == 0) {
-      bars.issued[lw] = operands;
-      atomicSub(&bars.loaders, 1);
-    }
-    cp_async_wait_all();
+      if (lane == 0) {
+        bars.issued[lw] = operands;
+        atomicSub(&bars.loaders, 1);
+      }
+      cp_async_wait_all();
     }
   } else {
     shrink_registers<kOthers>();
@@ -893,7 +900,8 @@ __global__ void __launch_bounds__(tile_threads(kQuantised), 1) attend_tile_kerne
         const uint32_t b = v_low + stage * (Shape::kOperand >> 4), d = tm + 256 + t * 128, a = tm + t * 128;
         if (elect_one()) {
 #pragma unroll
-          for (int e = 0; e < kTileKeys / 16; ++e) mma_ts(d, a + (kQuantised ? e / 4 * 64 + e % 4 * 8 : e * 8), b + e * (16 * 128 >> 4), desc_o, e > 0 ? 1 : add);
+          for (int e = 0; e < kTileKeys / 16; ++e)  // weights lie over the scores that were held at a time
+            mma_ts(d, a + (kQuantised ? e / 4 * 64 + e % 4 * 8 : e * 8), b + e * (16 * 128 >> 4), desc_o, e > 0 ? 1 : add);
         }
         __syncwarp();
       };
@@ -1082,7 +1090,8 @@ __global__ void __launch_bounds__(tile_threads(kQuantised), 1) attend_tile_kerne
       __syncwarp();
       const uint64_t t0 = global_timer_ns();
       tile_drain(&bars.drain, 0, t0);
-      for (int w = 0; w < (kQuantised ? 0 : kLoadWarps); ++w) {  // the last use of every stage (quantised rows are written by the warps themselves)
+      // the last use of every stage (of quantised rows the warps write the stages themselves)
+      for (int w = 0; w < (kQuantised ? 0 : kLoadWarps); ++w) {
         const uint32_t values = bars.issued[w] / 2, keys = bars.issued[w] - values;
         for (uint32_t at = keys > kStages ? keys - kStages : 0; at < keys; ++at) tile_drain(&bars.k_full[at % kStages], at / kStages, t0);
         for (uint32_t at = values > kStages ? values - kStages : 0; at < values; ++at)
