@@ -776,8 +776,9 @@ int cpkv_attend_window_quantised_workspace_bytes(int B, int q_heads, int kv_head
                                                  const int32_t *h_q_lens, int64_t max_kv_len, int window, int sinks,
                                                  int64_t *h_bytes);
 
-/* cpkv_attend_shared over quantised rows; h_row and rounding as cpkv_attend_window_quantised,
- * the workspace that of cpkv_attend_shared. */
+/* cpkv_attend_shared over quantised rows; h_row and rounding as cpkv_attend_window_quantised (a suffix by the
+ * query heads of a key/value head, a prefix by those of all its requests), the workspace at least
+ * cpkv_attend_shared_quantised_workspace_bytes. */
 int cpkv_attend_shared_quantised(int B, int n_groups, int page_size, int cp_size, int dtype, int q_heads,
                                  const cpkv_quantised_row *h_row, const int32_t *h_group_sizes,
                                  const int32_t *h_prefix_lens, int64_t max_suffix_len, const void *const *h_pools,
@@ -786,6 +787,11 @@ int cpkv_attend_shared_quantised(int B, int n_groups, int page_size, int cp_size
                                  const int32_t *d_suffix_lens, const void *d_q, int64_t q_stride, float scale,
                                  void *d_out, int64_t out_stride, float *d_lse, void *d_workspace,
                                  int64_t workspace_bytes, int flags, int32_t *d_status, cpkv_stream_t stream);
+
+/* Device workspace of cpkv_attend_shared_quantised (host only); lengths as passed to it. */
+int cpkv_attend_shared_quantised_workspace_bytes(int B, int n_groups, int q_heads, int kv_heads, int head_dim,
+                                                 const int32_t *h_group_sizes, const int32_t *h_prefix_lens,
+                                                 int64_t max_suffix_len, int64_t *h_bytes);
 
 /*
  * cpkv_selftest_attend_timeout — diagnostics: runs the attention's kernel for many query

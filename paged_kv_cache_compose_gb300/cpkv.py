@@ -67,6 +67,7 @@ EXPORTED = (
     "cpkv_ragged_plan_build", "cpkv_append_rotary", "cpkv_append_quantised", "cpkv_read_quantised", "cpkv_attend_window",
     "cpkv_attend_window_workspace_bytes", "cpkv_attend_shared", "cpkv_attend_shared_workspace_bytes",
     "cpkv_attend_window_quantised", "cpkv_attend_window_quantised_workspace_bytes", "cpkv_attend_shared_quantised",
+    "cpkv_attend_shared_quantised_workspace_bytes",
     "cpkv_selftest_attend_timeout", "cpkv_selftest_attend_quantised_timeout", "cpkv_stream_is_capturing", "cpkv_error_string", "cpkv_version",
 )
 
@@ -120,6 +121,7 @@ def _declare(lib):
     lib.cpkv_attend_shared.argtypes = [_I] * 8 + [_L] * 3 + [_P, _P, _L, _P, _P, _P, _L, _P, _L, _P, _P, _L, _F, _P, _L,
                                                              _P, _P, _L, _I, _P, _P]
     lib.cpkv_attend_shared_workspace_bytes.argtypes = [_I] * 5 + [_P, _P, _L, _P]
+    lib.cpkv_attend_shared_quantised_workspace_bytes.argtypes = [_I] * 5 + [_P, _P, _L, _P]
     lib.cpkv_selftest_attend_timeout.argtypes = [_I] * 3 + [_P] * 5 + [_L, _P, _P]
     lib.cpkv_selftest_attend_quantised_timeout.argtypes = [_I] * 3 + [_P] * 5 + [_L, _P, _P]
     lib.cpkv_stream_is_capturing.argtypes = [_P, _P]
@@ -641,13 +643,23 @@ def cpkv_attend_window(q, q_lens, page_table, d_kv_lens, *, table: PoolTable, kv
         d_status, _handle(stream, table)))
 
 
-def cpkv_attend_shared_workspace_bytes(B, q_heads, kv_heads, head_dim, group_sizes, prefix_lens, max_suffix_len) -> int:
-    """Workspace of ``cpkv_attend_shared`` on the current device."""
+def _shared_workspace_bytes(name, B, q_heads, kv_heads, head_dim, group_sizes, prefix_lens, max_suffix_len) -> int:
     gs, pl = _host_i32(group_sizes), _host_i32(prefix_lens)
     out = ctypes.c_int64(0)
-    _check("cpkv_attend_shared_workspace_bytes", load().cpkv_attend_shared_workspace_bytes(
-        B, len(gs), q_heads, kv_heads, head_dim, _hp(gs), _hp(pl), max_suffix_len, ctypes.byref(out)))
+    _check(name, getattr(load(), name)(B, len(gs), q_heads, kv_heads, head_dim, _hp(gs), _hp(pl), max_suffix_len, ctypes.byref(out)))
     return int(out.value)
+
+
+def cpkv_attend_shared_workspace_bytes(B, q_heads, kv_heads, head_dim, group_sizes, prefix_lens, max_suffix_len) -> int:
+    """Workspace of ``cpkv_attend_shared`` on the current device."""
+    return _shared_workspace_bytes("cpkv_attend_shared_workspace_bytes", B, q_heads, kv_heads, head_dim, group_sizes, prefix_lens,
+                                   max_suffix_len)
+
+
+def cpkv_attend_shared_quantised_workspace_bytes(B, q_heads, kv_heads, head_dim, group_sizes, prefix_lens, max_suffix_len) -> int:
+    """Workspace of ``cpkv_attend_shared_quantised``, likewise."""
+    return _shared_workspace_bytes("cpkv_attend_shared_quantised_workspace_bytes", B, q_heads, kv_heads, head_dim, group_sizes,
+                                   prefix_lens, max_suffix_len)
 
 
 def cpkv_attend_shared(q, group_sizes, prefix_lens, prefix_pages, page_table, d_suffix_lens, *, table: PoolTable,

@@ -82,11 +82,13 @@ CPKV_DEV void angles4(const AppendParams &p, const Work<kAxes> &w, int f, float 
     s[0] = sn.x, s[1] = sn.y, s[2] = sn.z, s[3] = sn.w;
     return;
   }
+  if constexpr (kAxes) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float *const row = p.table + w.position(axes >> (8 * i) & 0xff) * rot + f + i;
-    c[i] = __ldg(row);
-    s[i] = __ldg(row + p.half);
+    for (int i = 0; i < 4; ++i) {
+      const float *const row = p.table + w.position(axes >> (8 * i) & 0xff) * rot + f + i;
+      c[i] = __ldg(row);
+      s[i] = __ldg(row + p.half);
+    }
   }
 }
 

@@ -26,17 +26,8 @@ extern "C" int cpkv_attend_window(int B, int page_size, int cp_size, int dtype, 
 extern "C" int cpkv_attend_shared_workspace_bytes(int B, int n_groups, int q_heads, int kv_heads, int head_dim,
                                                   const int32_t *h_group_sizes, const int32_t *h_prefix_lens,
                                                   int64_t max_suffix_len, int64_t *h_bytes) {
-  const HeadArgs heads = {CPKV_BF16, q_heads, kv_heads, head_dim};
-  if (B < 0 || n_groups < 0 || max_suffix_len < 0 || h_bytes == nullptr) return CPKV_ERR_ARG;
-  int rc = check_heads(heads);
-  if (rc != CPKV_OK) return rc;
-  if (B > CPKV_MAX_BATCH || n_groups > CPKV_MAX_BATCH || max_suffix_len > INT32_MAX / 2) return CPKV_ERR_LIMIT;
-  if (n_groups > 0 && (h_group_sizes == nullptr || h_prefix_lens == nullptr)) return CPKV_ERR_ARG;
-  SharedPlan plan;
-  rc = shared_plan(&plan, heads, B, n_groups, h_group_sizes, h_prefix_lens, 0, max_suffix_len);
-  if (rc != CPKV_OK) return rc;
-  *h_bytes = plan.bytes;
-  return CPKV_OK;
+  return shared_bytes(false, HeadArgs{CPKV_BF16, q_heads, kv_heads, head_dim}, B, n_groups, h_group_sizes, h_prefix_lens, max_suffix_len,
+                      h_bytes);
 }
 
 extern "C" int cpkv_attend_shared(int B, int n_groups, int page_size, int cp_size, int dtype, int q_heads, int kv_heads,

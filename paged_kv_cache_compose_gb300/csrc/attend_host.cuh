@@ -120,16 +120,19 @@ struct TileBounds {
     return CPKV_OK;
   }
   // How many parts an item's keys are cut into: the count whose rounds of blocks over
-  // the SMs come to the fewest steps.
-  int finish(int kv_heads, int head_dim) {
-    const int64_t items = tiles * kv_heads, sms = device_sm_count(), all = steps(max_keys, max_rows);
+  // the SMs come to the fewest steps.  Of keys that are converted on the way a tile is a step,
+  // whoever multiplies it, and the fewest steps are taken however close the next: 12 requests of 160
+  // rows on 8192 keys, 8 heads, 101 us so and 133 with the rule of plain rows, one of 120 on 20000 18.8 and 20.8.
+  int finish(int kv_heads, int head_dim, bool converts) {
+    const int64_t items = tiles * kv_heads, sms = device_sm_count();
+    const int64_t all = converts ? ceil_div(max_keys, kTileKeys) : steps(max_keys, max_rows);
     int64_t best = INT64_MAX / 16;
     for (int64_t n = 1; n <= std::min<int64_t>(std::max<int64_t>(all / 2, 1), sms) && items > 0; ++n) {
       if (n > 1 && items * n > 4 * sms) break;
       // in 32nds of a step; a part of 256 rows of 128 written and read again is about one
       const int64_t cost = 32 * ceil_div(items * n, sms) * (ceil_div(all, n) + kItemSteps) +
                            (n > 1 ? 32 * kJoinSteps + items * n * head_dim / 128 : 0);
-      if (10 * cost < 9 * best) {  // for a tenth or more
+      if (converts ? cost < best : 10 * cost < 9 * best) {  // for a tenth or more
         best = cost;
         splits = (int)n;
       }
@@ -187,10 +190,10 @@ inline bool few_rows(int64_t max_rows) { return max_rows <= kSplitRows; }
 
 // Quantised rows that a tile pass brings to the element type beforehand (attend_unpack.cuh):
 // where the sequences have kUnpackTiles row tiles each or more, and the dense rows fit
-// kUnpackMost (the passes over the rows themselves need next to no memory).  5 requests of
-// 16384 keys, 32 heads of 128 on 8, beforehand and on the way: one row tile 186 and 118 us, two
-// 261 and 224, three 300 and 287, four 432 and 462, six 494 and 560, eight 679 and 824; 32
-// requests with four 1956 and 1965.
+// kUnpackMost (the passes over the rows themselves need next to no memory).  5 requests of up to
+// 16384 keys, 32 heads of 128 on 8, beforehand and on the way: one row tile 120 and 99 us, two 138 and
+// 123, three 217 and 237, four 202 and 203, six 238 and 269, eight 287 and 338; 32 requests: two
+// 801 and 667, four 1162 and 1179.
 struct UnpackBounds {
   int64_t pages = 0, stride = 0;
   int sequences = 0;
@@ -249,13 +252,13 @@ inline int window_plan(WindowPlan *w, const HeadArgs &a, bool quantised, int B, 
   // with whole sequences, 26 with parts).
   w->whole = w->few && uniform && w->split.max_tiles <= kWholeUnits &&
              (int64_t)B * a.kv_heads <= device_sm_count();
-  const int rc = w->few ? w->split.finish(a.kv_heads) : w->tile.finish(a.kv_heads, a.head_dim);
+  w->unpacks = quantised && !w->few && w->tile.tiles >= kUnpackTiles * w->unpack.sequences &&
+               w->unpack.bytes(B, a.kv_heads, a.head_dim) <= kUnpackMost;
+  const int rc = w->few ? w->split.finish(a.kv_heads) : w->tile.finish(a.kv_heads, a.head_dim, quantised && !w->unpacks);
   w->bytes = w->whole ? 0
              : w->few ? w->split.bytes(B, a.kv_heads, a.head_dim, true)
                       : w->tile.bytes(a.kv_heads, a.head_dim, true);
   w->pass_bytes = round_up(w->bytes, 256);
-  w->unpacks = quantised && !w->few && w->tile.tiles >= kUnpackTiles * w->unpack.sequences &&
-               w->unpack.bytes(B, a.kv_heads, a.head_dim) <= kUnpackMost;
   if (w->unpacks) w->bytes = w->pass_bytes + w->unpack.bytes(B, a.kv_heads, a.head_dim);
   return rc;
 }
@@ -263,11 +266,23 @@ inline int window_plan(WindowPlan *w, const HeadArgs &a, bool quantised, int B, 
 struct SharedPlan {
   SplitBounds split;  // prefixes and suffixes when rows are few
   TileBounds tile;    // and when they are many
-  bool few = true;
-  int64_t prefix_pages = 0, bytes = 0;
+  bool few = true, mixed = false;  // mixed: prefixes by the tile pass, suffixes by the split pass
+  int64_t prefix_pages = 0, bytes = 0, split_at = 0;  // split_at: of a mixed call, where the split pass's workspace begins
 };
 
-inline int shared_plan(SharedPlan *w, const HeadArgs &a, int B, int n_groups, const int32_t *h_group_sizes,
+// Quantised suffixes beside prefixes of many rows go to the split pass where they come to two key tiles
+// or more for each SM: a tile pass would convert and multiply them for 128 rows of which few are real,
+// against 2 us for another kernel.  32 heads of 128 on 8, a prefix of 16384: 32 requests with
+// suffixes of up to 1024 in 37 us, 53 in one pass; 16 with up to 64, which is below, 37.0 and 36.6; a
+// prefix of 1024 and 32 suffixes of up to 32, 28.8 and 27.1.
+inline bool mixes(SharedPlan &w, const HeadArgs &a, bool quantised, int B, int64_t max_suffix) {
+  if (!quantised || !few_rows(a.q_heads / a.kv_heads)) return false;
+  if ((int64_t)B * a.kv_heads * ceil_div(max_suffix, kTileKeys) < 2 * device_sm_count()) return false;
+  for (int b = 0; b < B; ++b) w.split.add(1, max_suffix, 0, 0);
+  return w.split.finish(a.kv_heads) == CPKV_OK;
+}
+
+inline int shared_plan(SharedPlan *w, const HeadArgs &a, bool quantised, int B, int n_groups, const int32_t *h_group_sizes,
                 const int32_t *h_prefix_lens, int page_size, int64_t max_suffix) {
   const int group = a.q_heads / a.kv_heads;
   int64_t sum = 0;
@@ -288,6 +303,11 @@ inline int shared_plan(SharedPlan *w, const HeadArgs &a, int B, int n_groups, co
     for (int b = 0; b < B; ++b) w->split.add(1, max_suffix, 0, 0);
     rc = w->split.finish(a.kv_heads);
     w->bytes = w->split.bytes(n_groups + B, a.kv_heads, a.head_dim, false);
+  } else if (mixes(*w, a, quantised, B, max_suffix)) {
+    w->mixed = true;
+    rc = w->tile.finish(a.kv_heads, a.head_dim, false);  // (fewer parts leave SMs to the split pass: 39.0 us, 43.3 counted as above)
+    w->split_at = round_up(w->tile.bytes(a.kv_heads, a.head_dim, false), 256);
+    w->bytes = w->split_at + w->split.bytes(B, a.kv_heads, a.head_dim, false);
   } else {
     w->tile.add_singles(B, max_suffix);
     rc = w->tile.finish_shared(a.kv_heads);
@@ -323,7 +343,7 @@ int for_type_and_dim(const HeadArgs &a, F f) {
 
 // A block takes a whole sequence unless the mode is kLine.
 template <typename T, int D, SplitMode kMode, typename Rows, typename S>
-int split_pass_of(SplitParams<S> *p, const SplitBounds &b, cudaStream_t stream) {
+int split_pass_of(SplitParams<S> *p, const SplitBounds &b, bool dependent, cudaStream_t stream) {
   using Pass = SplitPass<T, D, kMode, S, Rows>;
   using Shape = typename Pass::Shape;
   const int smem = Shape::kSmem + (kMode == kLine ? (p->seqs.count + 1) * 4 : 0);
@@ -336,16 +356,17 @@ int split_pass_of(SplitParams<S> *p, const SplitBounds &b, cudaStream_t stream) 
     blocks = p->space.grid = std::max(resident / heads, 1) * heads;
   }
   if (blocks > INT32_MAX) return CPKV_ERR_LIMIT;
-  return launch_kernel(kernel, dim3((unsigned)blocks), dim3(kSplitWarps * 32), smem, false, stream, *p);
+  return launch_kernel(kernel, dim3((unsigned)blocks), dim3(kSplitWarps * 32), smem, dependent, stream, *p);
 }
 
-// max_rows: of a sequence.
+// max_rows: of a sequence.  dependent: may begin while the kernel before it runs (quantised rows).
 template <typename T, int D, SplitMode kMode, bool kQuantised, typename S>
-int split_pass(SplitParams<S> *p, const SplitBounds &b, int64_t max_rows, cudaStream_t stream) {
+int split_pass(SplitParams<S> *p, const SplitBounds &b, int64_t max_rows, cudaStream_t stream, bool dependent = false) {
   if constexpr (!kQuantised) {
-    return split_pass_of<T, D, kMode, Plain>(p, b, stream);
+    return split_pass_of<T, D, kMode, Plain>(p, b, false, stream);
   } else {
-    return max_rows <= 8 ? split_pass_of<T, D, kMode, Quantised<1>>(p, b, stream) : split_pass_of<T, D, kMode, Quantised<2>>(p, b, stream);
+    return max_rows <= 8 ? split_pass_of<T, D, kMode, Quantised<1>>(p, b, dependent, stream)
+                         : split_pass_of<T, D, kMode, Quantised<2>>(p, b, dependent, stream);
   }
 }
 
@@ -482,7 +503,37 @@ int attend_window(const HeadArgs &heads, const Seqs<N> &seqs, const PagedPools &
   });
 }
 
-// Prefixes and suffixes in one pass, joined.
+// Quantised prefixes in a tile pass; suffixes in a split pass, whose blocks take the SMs as the
+// tile pass leaves them; both joined.
+template <int N>
+int attend_mixed(const HeadArgs &heads, const SharedSeqs<N> &seqs, const PagedPools &pools, const AttendIo &io,
+                 const SharedPlan &plan, char *workspace, cudaStream_t stream) {
+  const int64_t rows = (int64_t)(seqs.count - seqs.groups) * heads.q_heads;
+  TileParams<SharedSeqs<N>> t = {};
+  fill_tiles<true>(&t, seqs, seqs.groups, pools, io, plan.tile, workspace, false);
+  using One = SharedSeqs<kFewSeqs>;  // the requests alone
+  SplitParams<One> p = {};
+  p.seqs.table = seqs.table;
+  p.seqs.suffix_lens = seqs.suffix_lens;
+  p.seqs.stride = seqs.stride;
+  p.seqs.status = seqs.status;
+  p.seqs.suffix_cap = seqs.suffix_cap;
+  p.seqs.count = seqs.count - seqs.groups;
+  p.pools = pools;
+  p.io = io;
+  p.space = plan.split.space(workspace + plan.split_at, p.seqs.count, heads.kv_heads, false);
+  return for_type_and_dim(heads, [&](auto type, auto dim) {
+    using T = decltype(type);
+    constexpr int D = decltype(dim)::value;
+    int rc = tile_pass<T, D, true>(t, plan.tile, stream);
+    if (rc != CPKV_OK) return rc;
+    rc = split_pass<T, D, kLine, true>(&p, plan.split, io.group.d, stream, true);
+    if (rc != CPKV_OK) return rc;
+    return join_pass<T, D>(MixedSource<SharedSeqs<N>, One>{source_of(t), source_of(p)}, io, rows, stream);
+  });
+}
+
+// Prefixes and suffixes in one pass, joined (quantised ones beside many rows in two).
 template <bool kQuantised, int N>
 int attend_shared(const HeadArgs &heads, const SharedSeqs<N> &seqs, const PagedPools &pools, const AttendIo &io,
                   const SharedPlan &plan, char *workspace, cudaStream_t stream) {
@@ -499,6 +550,9 @@ int attend_shared(const HeadArgs &heads, const SharedSeqs<N> &seqs, const PagedP
       const int rc = split_pass<T, D, kLine, kQuantised>(&p, plan.split, plan.tile.max_rows, stream);
       return rc != CPKV_OK ? rc : join_pass<T, D>(source_of(p), io, rows, stream);
     });
+  }
+  if constexpr (kQuantised) {
+    if (plan.mixed) return attend_mixed(heads, seqs, pools, io, plan, workspace, stream);
   }
   TileParams<SharedSeqs<N>> p = {};
   fill_tiles<kQuantised>(&p, seqs, seqs.groups, pools, io, plan.tile, workspace, false);
@@ -666,6 +720,21 @@ inline int window_bytes(bool quantised, const HeadArgs &heads, int B, const int3
   return CPKV_OK;
 }
 
+// Bytes of the workspace of a shared call.
+inline int shared_bytes(bool quantised, const HeadArgs &heads, int B, int n_groups, const int32_t *h_group_sizes,
+                        const int32_t *h_prefix_lens, int64_t max_suffix_len, int64_t *h_bytes) {
+  if (B < 0 || n_groups < 0 || max_suffix_len < 0 || h_bytes == nullptr) return CPKV_ERR_ARG;
+  int rc = check_heads(heads);
+  if (rc != CPKV_OK) return rc;
+  if (B > CPKV_MAX_BATCH || n_groups > CPKV_MAX_BATCH || max_suffix_len > INT32_MAX / 2) return CPKV_ERR_LIMIT;
+  if (n_groups > 0 && (h_group_sizes == nullptr || h_prefix_lens == nullptr)) return CPKV_ERR_ARG;
+  SharedPlan plan;
+  rc = shared_plan(&plan, heads, quantised, B, n_groups, h_group_sizes, h_prefix_lens, 0, max_suffix_len);
+  if (rc != CPKV_OK) return rc;
+  *h_bytes = plan.bytes;
+  return CPKV_OK;
+}
+
 struct SharedCall {
   int B, n_groups;
   const int32_t *h_group_sizes, *h_prefix_lens;
@@ -690,7 +759,7 @@ int shared_call(const HeadArgs &heads, const RowArgs &rows, const SharedCall &c,
   if (n_groups > 0 && (c.h_group_sizes == nullptr || c.h_prefix_lens == nullptr)) return CPKV_ERR_ARG;
   if (c.table_stride < 0 || c.max_suffix_len > c.table_stride * rows.page_size) return CPKV_ERR_CAPACITY;
   SharedPlan plan;
-  rc = shared_plan(&plan, heads, B, n_groups, c.h_group_sizes, c.h_prefix_lens, rows.page_size, c.max_suffix_len);
+  rc = shared_plan(&plan, heads, kQuantised, B, n_groups, c.h_group_sizes, c.h_prefix_lens, rows.page_size, c.max_suffix_len);
   if (rc != CPKV_OK) return rc;
   if (c.num_prefix_pages < plan.prefix_pages) return CPKV_ERR_CAPACITY;
   if (B == 0) return CPKV_OK;

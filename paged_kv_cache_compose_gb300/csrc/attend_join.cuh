@@ -81,6 +81,27 @@ CPKV_DEV bool find_parts(Parts *r, const TileSource<S> &src, const AttendIo &io,
   return true;
 }
 
+// Prefixes by a tile pass, suffixes by a split pass, whose sequences are the requests alone.
+template <typename S, typename One>
+struct MixedSource : TileSource<S> {
+  SplitSource<One> suffixes;
+};
+
+template <typename S, typename One>
+CPKV_DEV Spot find_spot(const MixedSource<S, One> &src, const AttendIo &io, int s, int i, int g) {
+  const TileSource<S> &prefixes = src;
+  if (s < src.seqs.groups) return find_spot(prefixes, io, s, i, g);
+  Spot at = find_spot(src.suffixes, io, s - src.seqs.groups, i, g);
+  at.rt = -1;
+  return at;
+}
+
+template <typename S, typename One>
+CPKV_DEV bool find_parts(Parts *r, const MixedSource<S, One> &src, const AttendIo &io, const Spot &at, int h) {
+  const TileSource<S> &prefixes = src;
+  return at.rt < 0 ? find_parts(r, src.suffixes, io, at, h) : find_parts(r, prefixes, io, at, h);
+}
+
 // The places of a query row in a pass.
 struct Spots {
   Spot at[2];

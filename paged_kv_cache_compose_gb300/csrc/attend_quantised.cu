@@ -25,6 +25,13 @@ extern "C" int cpkv_attend_window_quantised(int B, int page_size, int cp_size, i
   return window_call<true>(heads, rows, call, results);
 }
 
+extern "C" int cpkv_attend_shared_quantised_workspace_bytes(int B, int n_groups, int q_heads, int kv_heads, int head_dim,
+                                                            const int32_t *h_group_sizes, const int32_t *h_prefix_lens,
+                                                            int64_t max_suffix_len, int64_t *h_bytes) {
+  return shared_bytes(true, HeadArgs{CPKV_BF16, q_heads, kv_heads, head_dim}, B, n_groups, h_group_sizes, h_prefix_lens, max_suffix_len,
+                      h_bytes);
+}
+
 extern "C" int cpkv_attend_shared_quantised(int B, int n_groups, int page_size, int cp_size, int dtype, int q_heads,
                                             const cpkv_quantised_row *h_row, const int32_t *h_group_sizes,
                                             const int32_t *h_prefix_lens, int64_t max_suffix_len,

@@ -484,6 +484,7 @@ __global__ void __launch_bounds__(kSplitWarps * 32, SplitShapeQ<D, kMode, kBlock
   }
   cp_async_wait<0>();
   if constexpr (kWhole) end_rows(true);
+  if (!kWhole && blockIdx.x == gridDim.x - 1) wait_prerequisite();  // the joining kernel waits for this one only
 }
 
 }  // namespace cpkv

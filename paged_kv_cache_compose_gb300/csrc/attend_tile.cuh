@@ -39,9 +39,8 @@
 // decode step of 256 requests on a prefix of 65536: 0.55 ms, 1.02 PFLOP/s.
 // With the products issued by one lane of a diverged warp, or operands worked out by
 // it, the same prefill took 2.65 ms, with copies by cp.async alone 4.0 ms.
-// Quantised rows: 48 requests of three prefixes of about 9000 keys in 50.3 us (42.6 over plain
-// rows, twice their bytes), 5 requests of 64 tokens on 8192 keys in 68 us (the tensor pipe is
-// busy 37% of them): the conversion's instructions and the softmax's bound it together.
+// Quantised rows: 5 requests of 64 tokens on 8192 keys in 60 us (the tensor pipe is busy 37%
+// of a cold one's 68): the conversion's instructions and the softmax's bound it together.
 #pragma once
 
 #include <cuda.h>

@@ -293,6 +293,9 @@ class PagedCache:
     def _window_size(self):
         return _window_bytes
 
+    def _shared_size(self):
+        return _shared_bytes
+
     def attend_shared(self, q, group_sizes, prefix_lens, prefix_pages, page_table, suffix_lens, *,
                       max_suffix_len: int, scale: float | None = None, out=None, lse=None, workspace=None, stream=None):
         """A decode step of requests in consecutive groups: ``q`` [requests,
@@ -304,7 +307,7 @@ class PagedCache:
         if scale is None:
             scale = self._scale
         self._attend("attend_shared", (self.table.native, self.kv_heads, q, group_sizes, prefix_lens, prefix_pages, page_table,
-                                       suffix_lens, max_suffix_len, scale, out, lse), stream, workspace, _shared_bytes)
+                                       suffix_lens, max_suffix_len, scale, out, lse), stream, workspace, self._shared_size())
         return out
 
 
@@ -337,6 +340,9 @@ class QuantisedCache(PagedCache):
     def _window_size(self):
         return _window_quantised_bytes
 
+    def _shared_size(self):
+        return _shared_quantised_bytes
+
     def read_rows(self, slots, *, k_out=None, v_out=None, stream=None):
         """Cache rows ``slots`` (as in ``append_rotary``; negative: zeros) back
         in 16 bits: ``k_out`` [slots, kv_heads, key_dim] and ``v_out`` [slots,
@@ -362,3 +368,8 @@ def _window_quantised_bytes(table, kv_heads, q, q_lens, page_table, kv_lens, max
 def _shared_bytes(table, kv_heads, q, group_sizes, prefix_lens, prefix_pages, page_table, suffix_lens, max_suffix_len, *rest) -> int:
     return cpkv.cpkv_attend_shared_workspace_bytes(suffix_lens.shape[0], q.shape[1], kv_heads, q.shape[2], group_sizes, prefix_lens,
                                                    max_suffix_len)
+
+
+def _shared_quantised_bytes(table, kv_heads, q, group_sizes, prefix_lens, prefix_pages, page_table, suffix_lens, max_suffix_len, *rest) -> int:
+    return cpkv.cpkv_attend_shared_quantised_workspace_bytes(suffix_lens.shape[0], q.shape[1], kv_heads, q.shape[2], group_sizes,
+                                                             prefix_lens, max_suffix_len)

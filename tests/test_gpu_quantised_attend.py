@@ -254,6 +254,11 @@ def test_requests_without_any_keys(q_lens, heads):
     (300, 1, 128, 32, 2, BF16, [1, 1], [96, 1024], [70, 1]),
     (8, 1, 128, 1, 3, FP16, [24], [700], [1 + 11 * i for i in range(24)]),
     (16, 1, 128, 16, 2, BF16, [1], [3008], [2000]),
+    # prefixes of many rows, whose requests' suffixes are of few
+    (16, 2, 64, 16, 2, BF16, [5, 0, 20], [96, 32, 0], [0, 1, 64, 65, 200] + [(37 * i) % 130 for i in range(20)]),
+    (32, 2, 128, 8, 3, FP16, [3] * 17, [8 * i for i in range(17)], [(7 * i) % 90 for i in range(51)]),
+    (24, 8, 64, 64, 1, BF16, [60], [4160], [1000 - 16 * i for i in range(60)]),
+    (8, 1, 128, 16, 2, BF16, [12], [64], [0] * 12),
 ], ids=name)
 def test_shared_matches_64_bits(case):
     hq, hkv, d, ps, cp, dtype, sizes, prefix, suffix = case
@@ -275,6 +280,59 @@ def test_shared_matches_64_bits(case):
     assert int(cache.d_status) == 0
     model.check(*results[0], want, dtype)
     assert torch.equal(results[0][0], results[1][0]) and torch.equal(results[0][1], results[1][1])
+
+
+def test_shared_of_two_passes_in_a_graph():
+    """Prefix and suffixes by two kernels and joined, captured: replays follow the lengths and agree with a plain call."""
+    rng = np.random.default_rng(11)
+    hq, hkv, d, ps, n = 16, 2, 64, 16, 40
+    lists, n_pages = page_tables(rng, [640] + [300] * n, ps)
+    pools = qmodel.Pools(n_pages, ps, 2, QuantisedRow.of(hkv, d), BF16).fill(rng)
+    cache = cache_of(pools, BF16)
+    q = queries(rng, n, hq, d, BF16).cuda()
+    prefix_pages, table = torch.from_numpy(lists[0, :40].astype(np.int32)).cuda(), torch.from_numpy(lists[1:]).cuda()
+    lens = torch.ones(n, dtype=torch.int32).cuda()
+
+    def attend(**more):
+        return cache.attend_shared(q, [n], [640], prefix_pages, table, lens, max_suffix_len=300, **more)
+
+    attend()
+    torch.cuda.synchronize()
+    graph, out = torch.cuda.CUDAGraph(), torch.empty_like(q)
+    with torch.cuda.graph(graph):
+        attend(out=out)
+    for _ in range(3):
+        suffix = rng.integers(0, 301, n).astype(np.int32)
+        lens.copy_(torch.from_numpy(suffix))
+        graph.replay()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, attend())
+        want = model.shared(q.cpu(), [n], [640], prefix_pages.cpu().numpy(), lists[1:], suffix.tolist(), qmodel.Dense(pools),
+                            kv_heads=hkv, dim=d, scale=d**-0.5)
+        lse = torch.empty(n, hq, device="cuda")
+        model.check(attend(lse=lse), lse, want, BF16)
+    assert int(cache.d_status) == 0
+
+
+def test_shared_takes_its_workspace_and_no_less():
+    rng = np.random.default_rng(12)
+    hq, hkv, d, ps, n = 8, 1, 128, 16, 24
+    lists, n_pages = page_tables(rng, [160] + [40] * n, ps)
+    pools = qmodel.Pools(n_pages, ps, 2, QuantisedRow.of(hkv, d), FP16).fill(rng)
+    cache = cache_of(pools, FP16)
+    q = queries(rng, n, hq, d, FP16).cuda()
+    need = cpkv.cpkv_attend_shared_quantised_workspace_bytes(n, hq, hkv, d, [n], [160], 40)
+    args = (q, [n], [160], torch.from_numpy(lists[0, :10].astype(np.int32)).cuda(), torch.from_numpy(lists[1:]).cuda(),
+            torch.arange(1, n + 1, dtype=torch.int32).cuda())
+    room = torch.full((need + 512,), 0x5A, dtype=torch.uint8, device="cuda")
+    at = -room.data_ptr() % 16
+    out = cache.attend_shared(*args, max_suffix_len=40, workspace=room[at:at + need])
+    assert torch.equal(out, cache.attend_shared(*args, max_suffix_len=40))
+    assert (room[at + need:] == 0x5A).all() and (room[:at] == 0x5A).all()
+    with pytest.raises(cpkv.CpkvError) as e:
+        cache.attend_shared(*args, max_suffix_len=40, workspace=room[at:at + need - 16])
+    assert e.value.code == cpkv.CPKV_ERR_CAPACITY
 
 
 def test_shared_reports_bad_pages():

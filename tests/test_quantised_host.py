@@ -177,3 +177,22 @@ def test_workspace_sizes(lib):
         args = dict(B=1, q_heads=4, kv_heads=2, head_dim=64, q_lens=None, max_kv_len=10)
         with pytest.raises(cpkv.CpkvError):
             size(**{**args, **bad})
+
+
+def test_shared_workspace_sizes(lib):
+    """Suffixes beside prefixes of many rows have parts of their own; few rows need what plain rows do."""
+    def size(*args, **named):
+        return cpkv.cpkv_attend_shared_quantised_workspace_bytes(*args, **named)
+
+    def plain(*args):
+        return cpkv.cpkv_attend_shared_workspace_bytes(*args)
+
+    for same in ((4, 8, 2, 128, [1, 3], [64, 0], 50), (1, 4, 2, 64, [1], [100], 10), (40, 64, 2, 64, [40], [512], 300)):
+        assert size(*same) == plain(*same)
+    assert size(64, 32, 8, 128, [64], [4096], 1024) > 64 * 8 * 16 * 129 * 4  # a part of 16 rows for each request and head
+    assert size(0, 8, 2, 128, [], [], 0) >= 0
+    for changed in (dict(head_dim=96), dict(B=1025), dict(B=3), dict(q_heads=3), dict(max_suffix_len=-1), dict(prefix_lens=[-16])):
+        args = dict(B=2, q_heads=4, kv_heads=2, head_dim=64, group_sizes=[2], prefix_lens=[16], max_suffix_len=10)
+        with pytest.raises(cpkv.CpkvError):
+            size(**{**args, **changed})
+    assert lib.cpkv_attend_shared_quantised_workspace_bytes(1, 1, 4, 2, 64, None, None, 10, ctypes.byref(ctypes.c_int64())) == cpkv.CPKV_ERR_ARG
