@@ -606,7 +606,7 @@ def cpkv_append_quantised(k, v, d_slots, d_positions, d_cos_sin, *, table: Quant
                           axis_of_freq=None, interleaved=False, stream=None):
     """``cpkv_append_rotary`` into quantised rows."""
     _check("cpkv_append_quantised", serving().append_rotary(
-        table.native, k.shape[1], k.shape[2], v.shape[2], k, v, d_slots, d_positions, d_cos_sin, d_status, q, q_out,
+        table.native, table.row.kv_heads, table.row.key_dim, table.row.value_dim, k, v, d_slots, d_positions, d_cos_sin, d_status, q, q_out,
         None if axis_of_freq is None else bytes(axis_of_freq), interleaved, _handle(stream, table)))
 
 

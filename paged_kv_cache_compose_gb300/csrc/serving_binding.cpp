@@ -233,6 +233,10 @@ PyObject *append_rotary(PyObject *, PyObject *const *a, Py_ssize_t n) {
     const Rows k = rows(a[4], "k", t), v = rows(a[5], "v", t);
     if (k.heads != whole(a[1]) || k.dim != whole(a[2])) fail("k", "[tokens, kv_heads, key_dim] of the cache");
     if (v.n != k.n || v.heads != k.heads || v.dim != whole(a[3])) fail("v", "[tokens, kv_heads, value_dim] of the cache, k's tokens");
+    if (t.row() != nullptr) {  // what the kernel reads goes by the row, whatever widths the caller names
+      if (k.heads != t.row()->kv_heads || k.dim != t.row()->key_dim) fail("k", "[tokens, kv_heads, key_dim] of the cache");
+      if (v.dim != t.row()->value_dim) fail("v", "[tokens, kv_heads, value_dim] of the cache");
+    }
     int64_t count = 0;
     const int64_t *slots = list<int64_t>(a[6], "slots", t, at::kLong, &count);
     if (count != k.n) fail("slots", "a slot per token");
