@@ -252,7 +252,7 @@ inline int window_plan(WindowPlan *w, const HeadArgs &a, bool quantised, int B, 
   // with whole sequences, 26 with parts).
   w->whole = w->few && uniform && w->split.max_tiles <= kWholeUnits &&
              (int64_t)B * a.kv_heads <= device_sm_count();
-  w->unpacks = quantised && !w->few && w->tile.tiles >= kUnpackTiles * w->unpack.sequences &&
+  w->unpacks = quantised && !w->few && w->unpack.pages > 0 && w->tile.tiles >= kUnpackTiles * w->unpack.sequences &&
                w->unpack.bytes(B, a.kv_heads, a.head_dim) <= kUnpackMost;
   const int rc = w->few ? w->split.finish(a.kv_heads) : w->tile.finish(a.kv_heads, a.head_dim, quantised && !w->unpacks);
   w->bytes = w->whole ? 0

@@ -55,3 +55,31 @@ def test_append_functions_refuse_other_heads_and_widths(call):
             cache.append_rotary(bad_k, bad_v, slots, positions, table)
     torch.cuda.synchronize()
     assert not bool(cache.table.pools[0].any()) and int(cache.d_status) == 0
+
+
+# --------------------------------------------------------------------------- attention: no keys
+
+@pytest.mark.parametrize("q_lens, heads", [([1024], 32), ([300] * 3, 16), ([0, 900], 8)], ids=str)
+def test_many_query_rows_without_any_keys(q_lens, heads):
+    """As over rows of 16 bits: zeros and a log-sum-exp of -infinity, also in a graph."""
+    hkv, d = heads // 4, 128
+    cache = cache_of(qmodel.Pools(3, 16, 1, QuantisedRow.of(hkv, d), BF16).fill(np.random.default_rng(0)), BF16)
+    q = torch.ones(sum(q_lens), heads, d, dtype=BF16, device="cuda")
+    lens = torch.zeros(len(q_lens), dtype=torch.int32, device="cuda")
+    for pages, most in ((0, 0), (1, 0), (1, 16)):
+        out, lse = torch.full_like(q, 7.0), torch.zeros(q.shape[:2], device="cuda")
+        table = torch.full((len(q_lens), pages), -7, dtype=torch.int32, device="cuda")
+
+        def attend():
+            cache.attend_window(q, q_lens, table, lens, max_kv_len=most, window=3, sinks=2, out=out, lse=lse)
+
+        attend()
+        torch.cuda.synchronize()
+        assert int(cache.d_status) == 0 and bool((out == 0).all()) and bool(torch.isneginf(lse).all())
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            attend()
+        out.fill_(7.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert int(cache.d_status) == 0 and bool((out == 0).all())
