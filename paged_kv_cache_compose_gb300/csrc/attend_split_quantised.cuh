@@ -254,11 +254,12 @@ __global__ void __launch_bounds__(kSplitWarps * 32, SplitShapeQ<D, kMode, kBlock
         sum[b][r] = 0.f;
 #pragma unroll
         for (int w = 0; w < kSplitWarps; ++w) sum[b][r] += exp2_approx(v[w].x - base) * v[w].y;
-        const float mine = exp2_approx(n[b][r] - base);  // the values' scales come back here
+        // the values' scales come back here, in two factors: 2^-126 and less (scales below some 2^-112) would be flushed to 0
+        const float to = n[b][r] - base, by = fmaxf(to, -100.f), mine = exp2_approx(by), rest = exp2_approx(to - by);
 #pragma unroll
         for (int c = 0; c < kChunks; ++c) {
-          o[b][c][r] *= mine;
-          o[b][c][2 + r] *= mine;
+          o[b][c][r] = o[b][c][r] * mine * rest;
+          o[b][c][2 + r] = o[b][c][2 + r] * mine * rest;
         }
       }
     auto each = [&](int columns, float *buf, bool put) {

@@ -4,9 +4,12 @@ import pytest
 import torch
 
 import quantised_model as qmodel
+import serving_model as model
 from paged_kv_cache_compose_gb300 import cpkv
 from paged_kv_cache_compose_gb300.cpkv import QuantisedRow
 from test_gpu_quantised import cache_of, tensor, turns
+from test_gpu_quantised_attend import KIND_NAMES, KINDS, want_window
+from test_gpu_serving import page_tables, queries, run_window
 
 pytestmark = pytest.mark.gpu
 
@@ -83,3 +86,59 @@ def test_many_query_rows_without_any_keys(q_lens, heads):
         graph.replay()
         torch.cuda.synchronize()
         assert int(cache.d_status) == 0 and bool((out == 0).all())
+
+
+# --------------------------------------------------------------------------- attention: values near the smallest numbers
+
+def window_of_sizes(nq, hq, kv, sizes, d=64, ps=16):
+    """A bf16 cache whose values have these powers of two, one drawn for each token: (case, pools, lists, q)."""
+    rng = np.random.default_rng(kv[0] + nq)
+    lists, n_pages = page_tables(rng, kv, ps)
+    pools = qmodel.Pools(n_pages, ps, 2, QuantisedRow.of(1, d), BF16)
+    for page in lists[0]:
+        for off in range(ps):
+            v = rng.standard_normal((1, d))
+            v[0, rng.integers(d)] = 1.75  # the largest of its group, which is therefore not below 2^size
+            pools.put(int(page), off, rng.standard_normal((1, d)), np.clip(v, -1.75, 1.75) * 2.0 ** rng.integers(*sizes))
+    return (hq, 1, d, ps, 2, BF16, 0, 0, [nq], kv), pools, lists, queries(rng, nq, hq, d, BF16)
+
+
+def check_scaled(out, lse, want, power):
+    """serving_model.check in units of 2^-power, in which its 2^-24 is half a step of bf16's smallest numbers (2^-134) or more."""
+    model.check(out.double() * 2.0**power, lse, (want[0] * 2.0**power, want[1], want[2] * 2.0**power), BF16)
+
+
+# Values of 2^-116 and more have scales of 2^-124, and all of e4m3's multiples of those are bf16 numbers, so each pass's bound is the usual one.
+@pytest.mark.parametrize("sizes", [(-116, -110), (-116, -60)], ids=["tiny", "spread"])
+@pytest.mark.parametrize("nq, hq, kv", KINDS + [(1, 12, [3000])], ids=KIND_NAMES + ["split-16-rows"])
+def test_tiny_values_are_not_lost(nq, hq, kv, sizes):
+    case, pools, lists, q = window_of_sizes(nq, hq, kv, sizes)
+    out, lse = run_window(cache_of(pools, BF16), case, q, lists)
+    want = want_window(case, pools, lists, q)
+    assert bool((want[0].abs() > 2.0**-124).any()) and bool(out.any())
+    check_scaled(out, lse, want, 110)
+
+
+@pytest.mark.parametrize("nq, hq, kv", [(1, 2, [3000]), (3, 2, [3000]), (1, 2, [200]), (1, 12, [3000])], ids=["split", "split-queries", "few-keys", "split-16-rows"])
+def test_values_of_the_smallest_scale(nq, hq, kv):
+    """Scales of 2^-126, the least that the append writes: beside few query rows the values are e4m3 numbers until the end."""
+    case, pools, lists, q = window_of_sizes(nq, hq, kv, (-124, -117))
+    out, lse = run_window(cache_of(pools, BF16), case, q, lists)
+    check_scaled(out, lse, want_window(case, pools, lists, q), 110)
+
+
+def test_shared_keeps_tiny_values():
+    """Of few rows: prefix and suffixes in one split pass."""
+    d, ps, sizes, prefix, suffix = 64, 16, [3], [160], [40, 0, 77]
+    rng = np.random.default_rng(5)
+    lists, n_pages = page_tables(rng, prefix + suffix, ps)
+    pools = qmodel.Pools(n_pages, ps, 2, QuantisedRow.of(1, d), BF16)
+    for page in range(1, n_pages + 1):
+        for off in range(ps):
+            pools.put(page, off, rng.standard_normal((1, d)), np.clip(rng.standard_normal((1, d)), -1.75, 1.75) * 2.0**-113)
+    q = queries(rng, 3, 4, d, BF16)
+    pages, table = lists[0, :10].astype(np.int32), lists[1:]
+    lse = torch.empty(3, 4, device="cuda")
+    out = cache_of(pools, BF16).attend_shared(q.cuda(), sizes, prefix, torch.from_numpy(pages).cuda(), torch.from_numpy(table).cuda(),
+                                              torch.tensor(suffix, dtype=torch.int32).cuda(), max_suffix_len=77, lse=lse)
+    check_scaled(out, lse, model.shared(q, sizes, prefix, pages, table, suffix, qmodel.Dense(pools), kv_heads=1, dim=d, scale=d**-0.5), 110)
