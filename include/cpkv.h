@@ -700,8 +700,9 @@ int cpkv_attend_shared_workspace_bytes(int B, int n_groups, int q_heads, int kv_
  * keep_keys the key vectors stay in 16 bits, as the rotated part of latent rows does.
  * The append writes as a group's scale the smallest power of two, at least 2^-126, with
  * |x| <= 448 scale for all finite elements x of the group, and x / scale rounded once to
- * e4m3 (to nearest, ties to even; an infinity or a NaN as e4m3's NaN).  The readers
- * take any positive scale.
+ * e4m3 (to nearest, ties to even; an infinity or a NaN as e4m3's NaN).  A rotated key element is
+ * taken as it is before any rounding, past the largest float too; past 448 * 2^127, which no
+ * scale reaches, as an infinity.  The readers take any positive scale.
  * ------------------------------------------------------------------------- */
 
 /* Where a quantised row keeps what, in bytes from its start. */
@@ -757,7 +758,7 @@ int cpkv_read_quantised(int64_t n_rows, int page_size, int cp_size, int dtype, c
  * scale, v = e4m3 * value scale.  Beside 16 query rows per key/value head or fewer the
  * products are of the e4m3 numbers themselves and the scales are applied in 32 bits; beside
  * more, keys and values are brought to the element type first (e4m3 * scale rounded once: in bf16
- * exact for the append's scales, in fp16 up to 65504, and in steps of 2^-24 below 2^-14).
+ * exact for the append's scales, down to steps of 2^-133, in fp16 up to 65504, and in steps of 2^-24 below 2^-14).
  *   h_row          quantised keys (no keep_keys), key_dim = value_dim (ARG otherwise)
  *   d_workspace    at least cpkv_attend_window_quantised_workspace_bytes: beside many query
  *                  rows, the rows that they see are read back into it first

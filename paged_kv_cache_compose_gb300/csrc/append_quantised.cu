@@ -5,10 +5,10 @@
 // group's scale.  In 32 bits y is off by less than 2^-23 of |a c| + |b s|, which falls on the
 // wrong side of a border between two e4m3 numbers for one element in about 2^18: the row
 // would depend on the order of three instructions.  So each element is rounded from below and
-// from above its error, and where the two differ (or the group's scale does) the head is
-// worked out again exactly: products as pairs (a rounded product and its exact rest),
-// their sum rounded "to odd", a 32-bit number whose last bit says that something follows,
-// which rounds to e4m3 as the exact sum does.  Bytes bound the call (5.6 TB/s
+// from above its error, and where the two differ it is worked out again in 64 bits (a whole head
+// where its scale may differ, or 32 bits' range does not hold it): exact products, their sum rounded
+// "to odd", towards zero with a last bit that says that something follows, which then rounds
+// to e4m3 as the exact sum does.  Bytes bound the call (5.6 TB/s
 // on 44600 tokens of 32 + 8 heads of 128, in 181 us) nearly as much as instructions do.
 #include "append.cuh"
 #include "quantised.cuh"
@@ -29,34 +29,30 @@ struct QuantisedParams {
   FastDiv parts;
 };
 
-// x y exactly, as a rounded product and the rest.
-struct Exact {
-  float hi, lo;
-};
-CPKV_DEV Exact product(float x, float y) {
-  const float p = __fmul_rn(x, y);
-  return Exact{p, __fmaf_rn(x, y, -p)};
-}
-CPKV_DEV Exact sum(float x, float y) {
-  const float s = __fadd_rn(x, y), z = __fsub_rn(s, x);
-  return Exact{s, __fadd_rn(__fsub_rn(x, __fsub_rn(s, z)), __fsub_rn(y, z))};
+// a c + b s "rounded to odd": to 64 bits towards zero, the last bit set unless the sum is exact.
+// The products are exact (11 and 24 bits of fraction at most, and far from the ends of the
+// range), and so is the rest of their sum.
+CPKV_DEV double turned_to_odd(float a, float c, float b, float s) {
+  const double p = (double)a * c, q = (double)b * s, sum = __dadd_rn(p, q), z = __dsub_rn(sum, p);
+  const double rest = __dadd_rn(__dsub_rn(p, __dsub_rn(sum, z)), __dsub_rn(q, z));
+  long long bits = __double_as_longlong(sum);
+  if (rest != 0 && fabs(sum) < INFINITY) bits = (bits - ((__double_as_longlong(rest) ^ bits) < 0 ? 1 : 0)) | 1;
+  return __longlong_as_double(bits);
 }
 
-// p + q rounded to odd: towards zero, the last bit set unless the sum is exact.
-CPKV_DEV float sum_to_odd(Exact p, Exact q) {
-  const Exact top = sum(p.hi, q.hi);
-  const Exact r = sum(top.hi, __fadd_rn(top.lo, __fadd_rn(p.lo, q.lo)));
-  uint32_t bits = __float_as_uint(r.hi);
-  if (r.lo != 0.f) bits = (bits - ((__float_as_uint(r.lo) ^ bits) >> 31)) | 1u;
-  return __uint_as_float(bits);
+// The same number in 32 bits, rounded to odd.
+CPKV_DEV float to_odd(double x) {
+  const float y = __double2float_rz(x);
+  return y == x ? y : __uint_as_float(__float_as_uint(y) | 1u);
 }
 
 // The largest of a group's threads, which lie side by side.
-CPKV_DEV float largest_of(float x, int threads) {
+template <typename F>
+CPKV_DEV F largest_of(F x, int threads) {
   const uint32_t first = (threadIdx.x & 31) & ~(uint32_t)(threads - 1), mask = ((1u << threads) - 1) << first;
-  x = fmaxf(x, __shfl_xor_sync(mask, x, 1));
-  x = fmaxf(x, __shfl_xor_sync(mask, x, 2));
-  if (threads == 8) x = fmaxf(x, __shfl_xor_sync(mask, x, 4));
+  x = max(x, __shfl_xor_sync(mask, x, 1));
+  x = max(x, __shfl_xor_sync(mask, x, 2));
+  if (threads == 8) x = max(x, __shfl_xor_sync(mask, x, 4));
   return x;
 }
 
@@ -102,10 +98,13 @@ CPKV_DEV bool all_of(bool ok, int threads) {
   return __all_sync(mask, ok) != 0;
 }
 
-// Quantises a thread's 16 elements, each known to the error d of its pair; false where what
-// comes out may depend on the errors, or an element is infinite or a NaN.
+// Quantises a thread's 16 elements, each known to the error d of its pair: bytes of the least and of the
+// most that it may be, and the group's scale.  False where that may depend on the errors too, an element is
+// infinite or a NaN, or the errors are not relative ones because products leave the normal numbers: in a group that
+// reaches 2^-100 an element of 2^-120 or more has an error of less than d also with what is lost below 2^-149, and a
+// smaller one is e4m3's zero; of other groups only zeros are known.
 template <bool kPairs>
-CPKV_DEV bool quantise_surely(const float *y, const float *d, int threads, GroupScale *g, uint2 *lo, uint2 *hi) {
+CPKV_DEV bool quantise_between(const float *y, const float *d, int threads, GroupScale *g, uint32_t (&below)[4], uint32_t (&above)[4]) {
   float top = 0.f, off = 0.f, marks = 0.f;
 #pragma unroll
   for (int i = 0; i < 16; ++i) {
@@ -117,7 +116,6 @@ CPKV_DEV bool quantise_surely(const float *y, const float *d, int threads, Group
   const float most = largest_of(top + off, threads), least = largest_of(top - off, threads);
   *g = group_scale(most);
   const float f = g->inverse;
-  uint32_t below[4], above[4];
 #pragma unroll
   for (int w = 0; w < 4; ++w) {
     float a[4], b[4];
@@ -131,10 +129,7 @@ CPKV_DEV bool quantise_surely(const float *y, const float *d, int threads, Group
     below[w] = pack_e4m3(a[0], a[1], a[2], a[3]);
     above[w] = pack_e4m3(b[0], b[1], b[2], b[3]);
   }
-  *lo = make_uint2(below[0], below[1]);
-  *hi = make_uint2(below[2], below[3]);
-  return marks == 0.f && group_scale(least).scale == g->scale && below[0] == above[0] && below[1] == above[1] && below[2] == above[2] &&
-         below[3] == above[3];
+  return marks == 0.f && (most >= 0x1p-100f || most == 0.f) && group_scale(least).scale == g->scale;
 }
 
 template <typename T>
@@ -144,39 +139,68 @@ CPKV_DEV void unpack8(const uint4 &v, float *y) {
 }
 
 struct ExactUnit {
-  uint2 lo, hi;
+  uint32_t bytes[4];
   float scale;
 };
 
-// A unit of a key head, exactly; all threads of the head call.  Read again and apart, so that
-// the usual way needs no registers for it.
+// A unit of a key head, the elements that are not known yet (a bit each) exactly, and the group's scale
+// where that is not (`whole`, of all its threads).  Read again, apart and an element at a time, so that
+// the usual way needs no registers for it.  64-bit operations are slow: with all of a head's elements so, the
+// traced append took 259 us.
 template <typename T, bool kPairs, bool kAxes>
-__device__ __noinline__ ExactUnit exact_unit(const QuantisedParams &p, const Work<kAxes> &w, int head, int unit) {
+__device__ __noinline__ ExactUnit exact_unit(const QuantisedParams &p, const Work<kAxes> &w, int head, int unit, bool whole, uint32_t unknown,
+                                             ExactUnit known) {
   const AppendParams &a = p.a;
   const bool turns = unit * 8 < a.half;
   const int a0 = turns && !kPairs ? unit * 16 : unit * 32, a1 = turns && !kPairs ? a0 + a.half * 2 : a0 + 16;
   const char *const src = a.k + w.n * a.k_stride + head * (a.key_dim * 2);
-  float v[16], y[16];
+  float v[16], c[8], s[8];
   unpack8<T>(ld_stream16(src + a0), v);
   unpack8<T>(ld_stream16(src + a1), v + 8);
-  float c[8], s[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) c[i] = 1.f, s[i] = 0.f;  // of elements that are not turned
   if (turns) {
     angles4<kAxes>(a, w, unit * 8, c, s);
     angles4<kAxes>(a, w, unit * 8 + 4, c + 4, s + 4);
   }
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int one = kPairs ? 2 * i : i, two = kPairs ? 2 * i + 1 : i + 8;
-    y[one] = v[one];
-    y[two] = v[two];
-    if (turns) {
-      const Exact ac = product(v[one], c[i]), bc = product(v[two], c[i]), as = product(v[one], s[i]), bs = product(v[two], s[i]);
-      y[one] = sum_to_odd(ac, Exact{-bs.hi, -bs.lo});
-      y[two] = sum_to_odd(bc, as);
+  struct Turn {
+    float a, c, b, s;
+  };
+  auto turn_of = [&](int i) {  // element i is a c + b s
+    const int k = kPairs ? i / 2 : i % 8, first = kPairs ? 2 * k : k, other = i == first ? first + (kPairs ? 1 : 8) : first;
+    return Turn{v[i], c[k], turns ? v[other] : 0.f, i == first ? -s[k] : s[k]};
+  };
+  int e = (int)(__float_as_uint(known.scale) >> 23) - 127;
+  if (whole) {
+    double top = 0;
+#pragma unroll 1
+    for (int i = 0; i < 16; ++i) {
+      const Turn t = turn_of(i);
+      const double y = fabs(turned_to_odd(t.a, t.c, t.b, t.s));
+      if (y <= kMostQuantised) top = max(top, y);
     }
+    e = group_exponent(largest_of(top, 1 << p.lane_shift));
+    known.scale = __uint_as_float((uint32_t)(127 + e) << 23);
+    unknown = 0xffffu;
   }
-  const GroupScale g = group_scale(largest_of16(y, 1 << p.lane_shift));
-  return ExactUnit{pack8(y, g.inverse), pack8(y + 8, g.inverse), g.scale};
+  const double inverse = __hiloint2double((1023 - e) << 20, 0);
+#pragma unroll 1
+  for (int i = 0; i < 16; ++i) {
+    if (!(unknown >> i & 1)) continue;
+    const Turn t = turn_of(i);
+    const double y = turned_to_odd(t.a, t.c, t.b, t.s);
+    const float z = fabs(y) <= kMostQuantised ? to_odd(y * inverse) : NAN;
+    const uint32_t byte = pack_e4m3(z, 0.f, 0.f, 0.f) & 0xffu;
+    const int at = i % 4 * 8;
+    known.bytes[i / 4] = (known.bytes[i / 4] & ~(0xffu << at)) | byte << at;
+  }
+  return known;
+}
+
+// A bit for each byte in which two words differ.
+CPKV_DEV uint32_t differing(uint32_t x, uint32_t y) {
+  const uint32_t d = x ^ y;
+  return ((d & 0xffu) != 0) | ((d & 0xff00u) != 0) << 1 | ((d & 0xff0000u) != 0) << 2 | ((d & 0xff000000u) != 0) << 3;
 }
 
 // A warp takes a token, or one of `parts` shares of it where tokens are few: its row and
@@ -226,6 +250,9 @@ CPKV_DEV void quantise_token(const QuantisedParams &p, const Work<kAxes> &w, int
     }
   }
   if (row == nullptr) return;
+  float off[8];  // what a turned element may be off, of its pair's sum of magnitudes; position 0 turns nothing, and leaves ties
+#pragma unroll
+  for (int k = 0; k < 8; ++k) off[k] = s[k] == 0.f && fabsf(c[k]) == 1.f ? 0.f : fmaxf(fabsf(c[k]), fabsf(s[k])) * 0x1p-22f;
   for (int i = part - p.k_first + (part < p.k_first ? parts : 0); i < p.k_turns; i += parts) {
     const int head = i * heads + sub;
     if (head >= a.heads - a.q_heads) continue;
@@ -251,22 +278,25 @@ CPKV_DEV void quantise_token(const QuantisedParams &p, const Work<kAxes> &w, int
         const float v1 = y[i1], v2 = y[i2];
         y[i1] = __fmaf_rn(v1, c[k], -__fmul_rn(v2, s[k]));
         y[i2] = __fmaf_rn(v2, c[k], __fmul_rn(v1, s[k]));
-        d[k] = (fabsf(v1) + fabsf(v2)) * (fmaxf(fabsf(c[k]), fabsf(s[k])) * 0x1p-22f);
+        d[k] = (fabsf(v1) + fabsf(v2)) * off[k];
       }
     }
     GroupScale g;
-    uint2 lo, hi;
-    const bool sure = quantise_surely<kPairs>(y, d, 1 << p.lane_shift, &g, &lo, &hi);
+    ExactUnit known;
+    uint32_t above[4];
+    const bool scaled = quantise_between<kPairs>(y, d, 1 << p.lane_shift, &g, known.bytes, above);
+    const bool sure = scaled && known.bytes[0] == above[0] && known.bytes[1] == above[1] && known.bytes[2] == above[2] && known.bytes[3] == above[3];
+    known.scale = g.scale;
     if (!all_of(sure, 1 << p.lane_shift)) {
-      const ExactUnit exact = exact_unit<T, kPairs, kAxes>(p, w, head, unit);
-      lo = exact.lo;
-      hi = exact.hi;
-      g.scale = exact.scale;
+      uint32_t unknown = 0;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) unknown |= differing(known.bytes[e], above[e]) << (4 * e);
+      known = exact_unit<T, kPairs, kAxes>(p, w, head, unit, !all_of(scaled, 1 << p.lane_shift), unknown, known);
     }
     char *const dst = row + a.k_off + head * a.key_dim;
-    *reinterpret_cast<uint2 *>(dst + (a0 >> 1)) = lo;
-    *reinterpret_cast<uint2 *>(dst + (a1 >> 1)) = hi;
-    if (unit == 0) *reinterpret_cast<float *>(row + p.ks_off + head * 4) = g.scale;
+    *reinterpret_cast<uint2 *>(dst + (a0 >> 1)) = make_uint2(known.bytes[0], known.bytes[1]);
+    *reinterpret_cast<uint2 *>(dst + (a1 >> 1)) = make_uint2(known.bytes[2], known.bytes[3]);
+    if (unit == 0) *reinterpret_cast<float *>(row + p.ks_off + head * 4) = known.scale;
   }
   for (int i = part - p.v_first + (part < p.v_first ? parts : 0); i < p.v_turns; i += parts) {
     const int at = i * 32 + lane;

@@ -6,7 +6,8 @@
 // e4m3(x / s), rounded once to nearest even, an infinity or a NaN as e4m3's NaN.
 // A power of two loses none of the three bits of fraction (448 is the largest e4m3
 // number: the largest element falls into (224, 448]), makes the division exact, and
-// the product s * e4m3 of a row read back exact in bf16.  Readers take any scale.
+// the product s * e4m3 of a row read back exact in bf16 within that type's range (multiples of
+// 2^-133, less than 2^128).  Readers take any scale.
 #pragma once
 
 #include "paged.cuh"
@@ -60,6 +61,13 @@ CPKV_DEV GroupScale group_scale(float largest) {
   const int e = max((int)((__float_as_uint(largest) + 0x1fffffu) >> 23) - 8, 1);
   return GroupScale{__uint_as_float((uint32_t)e << 23), __uint_as_float((uint32_t)(254 - e) << 23)};
 }
+
+// The exponent of the scale, -126 to 127, from the largest magnitude in 64 bits; and the most
+// that a scale reaches, 448 * 2^127: what is larger is kept as an infinity is.
+CPKV_DEV int group_exponent(double largest) {
+  return max((int)((__double_as_longlong(largest) + 0x3ffffffffffffll) >> 52) - 8 - 1023, -126);
+}
+constexpr double kMostQuantised = 0x1.cp135;
 
 // Four numbers rounded to e4m3, the first in the lowest byte.
 CPKV_DEV uint32_t pack_e4m3(float a, float b, float c, float d) {

@@ -1,7 +1,7 @@
 // cpkv_read_quantised: rows of quantised pools, named by slot, back into 16 bits.
 //
 // x = e4m3 * scale, in 32 bits and rounded once: exact in bf16 for the scales that
-// the append writes.  Two operations an element: bytes bound it, the rows read once
+// the append writes, but for multiples of less than 2^-133 and what reaches 2^128.  Two operations an element: bytes bound it, the rows read once
 // and the results, twice their size, written once.
 #include "quantised.cuh"
 #include "tcgen05.cuh"

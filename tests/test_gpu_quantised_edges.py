@@ -1,4 +1,7 @@
 """Quantised rows on the GPU: calls that are refused, empty caches, the ends of the number range."""
+import bisect
+from fractions import Fraction
+
 import numpy as np
 import pytest
 import torch
@@ -142,3 +145,100 @@ def test_shared_keeps_tiny_values():
     out = cache_of(pools, BF16).attend_shared(q.cuda(), sizes, prefix, torch.from_numpy(pages).cuda(), torch.from_numpy(table).cuda(),
                                               torch.tensor(suffix, dtype=torch.int32).cuda(), max_suffix_len=77, lse=lse)
     check_scaled(out, lse, model.shared(q, sizes, prefix, pages, table, suffix, qmodel.Dense(pools), kv_heads=1, dim=d, scale=d**-0.5), 110)
+
+
+# --------------------------------------------------------------------------- append: exact roundings
+
+NUMBERS = [Fraction(float(x)) for x in qmodel.VALUES[:127]]
+LIMIT = 448 * Fraction(2)**127  # what the largest scale reaches
+
+
+def exact_bytes(x):
+    """A group of rational numbers (None: infinite or no number) as (bytes, scale)."""
+    x = [None if v is None or abs(v) > LIMIT else v for v in x]
+    top = max([abs(v) for v in x if v is not None], default=Fraction(0))
+    k = -126
+    while 448 * Fraction(2)**k < top:
+        k += 1
+    out = []
+    for v in x:
+        if v is None:
+            out.append(qmodel.NAN)
+            continue
+        z = abs(v) / Fraction(2)**k
+        up = min(max(bisect.bisect_left(NUMBERS, z), 1), 126)
+        low, high = z - NUMBERS[up - 1], NUMBERS[up] - z
+        out.append((up - 1 if low < high or (low == high and up % 2 == 1) else up) | (128 if v < 0 else 0))
+    return out, 2.0**k
+
+
+def pair_of(case, rng, dtype):
+    """One pair of a key's elements, and its cosine and sine (float32)."""
+    eps = float(torch.finfo(dtype).eps)
+    number = lambda: float(rng.choice([-1, 1])) * (1 + eps * int(rng.integers(1 / eps)))  # of the type, from 1 to 2
+    angle = rng.uniform(-3.2, 3.2)
+    c, s = np.float32(np.cos(angle)), np.float32(np.sin(angle))
+    if case == "huge":  # the exact rotation passes 32 bits' range
+        return number() * 2.0**127, number() * 2.0**127, c, s
+    if case == "past":  # some of them past what any scale reaches
+        return number() * 2.0**126, number() * 2.0**126, np.float32(c * 600), np.float32(s * 600)
+    if case == "tiny":  # products' rests lie below 32 bits' range
+        return number() * 2.0 ** int(rng.integers(-133, -117)), number() * 2.0 ** int(rng.integers(-133, -117)), c, s
+    if case == "least":  # as small as the type's and the table's numbers get
+        return number() * 2.0**-126, number() * 2.0**-126, np.float32(c * 2.0**-8), np.float32(s * 2.0**-8)
+    if case == "ties":  # an odd multiple of half a step, but for a rest of 2^-47 and less of it that two products' rests leave
+        tie = float(rng.choice([17, 19, 21, 23, 25, 27, 29, 31])) / 16 * 2.0 ** int(rng.integers(0, 7))
+        a, b = abs(number()), abs(number())
+        c = np.float32(tie / a)
+        rest = Fraction(a) * Fraction(float(c)) - Fraction(tie)
+        return a, b, c, np.float32(float(rest / Fraction(b)))
+    # "cancels": both products are nearly the same
+    a, b = number(), number()
+    return a, b, c, np.float32(a * float(c) / b)
+
+
+@pytest.mark.parametrize("interleaved", [False, True], ids=["halves", "pairs"])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("case, dtype", [("huge", BF16), ("past", BF16), ("tiny", BF16), ("least", BF16), ("ties", BF16), ("ties", FP16), ("cancels", BF16),
+                                         ("cancels", FP16)], ids=lambda x: str(x).replace("torch.", ""))
+def test_append_rounds_from_the_exact_value(case, dtype, d, interleaved):
+    """Every byte and scale against rational arithmetic, where 32 bits are not enough."""
+    n, hkv, ps, half = 24, 2, 16, d // 2
+    rng = np.random.default_rng(d + interleaved)
+    k, table = np.zeros((n, hkv, d)), np.zeros((n, d), np.float32)
+    for t in range(n):
+        for i in range(half):
+            for h in range(hkv):  # heads share the angles: the last head's, whose pairs are as meant; the other's are turned by them
+                a, b, c, s = pair_of(case, rng, dtype)
+                one, two = (2 * i, 2 * i + 1) if interleaved else (i, i + half)
+                k[t, h, one], k[t, h, two], table[t, i], table[t, half + i] = a, b, c, s
+        if case in ("ties", "cancels"):  # a group of ordinary size: its largest element is 448, not turned
+            k[t, :, [0, 1 if interleaved else half]] = np.array([[448.0], [0.0]])
+            table[t, 0], table[t, half] = 1.0, 0.0
+    keys = tensor(k, dtype)
+    k = keys.double().numpy()  # (subnormal numbers have fewer bits)
+    row = QuantisedRow.of(hkv, d)
+    pools = qmodel.Pools(2, ps, 1, row, dtype)
+    cache = cache_of(pools, dtype)
+    cache.append_rotary(keys.cuda(), keys.cuda(), torch.arange(ps, ps + n).cuda(), torch.arange(n, dtype=torch.int32).cuda(), torch.from_numpy(table).cuda(),
+                        interleaved=interleaved)
+    torch.cuda.synchronize()
+    assert int(cache.d_status) == 0
+    got = cache.table.pools[0].cpu().numpy().reshape(-1, row.row_bytes)[ps:ps + n]
+    bad = []
+    for t in range(n):
+        for h in range(hkv):
+            y = [None] * d
+            for i in range(half):
+                one, two = (2 * i, 2 * i + 1) if interleaved else (i, i + half)
+                a, b, c, s = (Fraction(float(v)) for v in (k[t, h, one], k[t, h, two], table[t, i], table[t, half + i]))
+                y[one], y[two] = a * c - b * s, b * c + a * s
+            want, scale = exact_bytes(y)
+            at = row.key_offset + h * d
+            mine, at_scale = got[t, at:at + d], row.key_scale_offset + 4 * h
+            mine, want = np.where(mine == 128, 0, mine), np.where(np.array(want) == 128, 0, want)  # a zero has no sign
+            if (mine != want).any() or float(np.ascontiguousarray(got[t, at_scale:at_scale + 4]).view(np.float32)[0]) != scale:
+                bad.append((t, h, int((mine != want).sum())))
+    assert not bad, f"{len(bad)} of {n * hkv} heads differ, first (token, head, bytes) {bad[0]}"
+    if case == "past":
+        assert (got[:, :2 * d] & 127 == qmodel.NAN).any()
