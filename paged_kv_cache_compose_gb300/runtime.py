@@ -202,6 +202,7 @@ class PagedCache:
     one."""
 
     _workspaces = {}  # of all handles, by device and stream
+    _keeps = None  # bytes of the largest workspace that stays with its stream; None: any
 
     def __init__(self, pools, *, page_size: int, kv_heads: int, key_dim: int, value_dim: int | None = None,
                  key_offset: int = 0, value_offset: int | None = None, dense: bool = False):
@@ -240,8 +241,12 @@ class PagedCache:
             with torch.cuda.device(self.device):  # the size goes by its SMs
                 need = size(*args)
             if need > (0 if workspace is None else workspace.numel()):
-                workspace = self._empty((need if captured else need + need // 4,), torch.uint8, stream)
-                if not captured:
+                keep = not captured and (self._keeps is None or need <= self._keeps)
+                if keep:  # the smaller one goes first
+                    workspace = None
+                    self._workspaces.pop((self.device.index, stream), None)
+                workspace = self._empty((need + need // 4 if keep else need,), torch.uint8, stream)
+                if keep:
                     self._workspaces[self.device.index, stream] = workspace
                 rc = native(*args, workspace, self.d_status, stream)
         if rc:
@@ -321,7 +326,13 @@ class QuantisedCache(PagedCache):
     fp16) is the type of what goes in and comes out.  ``keep_keys``: the key
     vectors stay in ``dtype`` (the rotated part of latent rows); such rows are
     appended and read back, not attended to.  ``row``: another layout of the
-    row (``cpkv.QuantisedRow``)."""
+    row (``cpkv.QuantisedRow``).
+
+    Beside many query tokens ``attend_window`` reads rows back into its
+    workspace, up to 4 GiB of them.  A workspace of more than 256 MiB is the
+    call's: its memory goes back to the stream's allocator afterwards."""
+
+    _keeps = 256 << 20
 
     def __init__(self, pools, *, page_size: int, kv_heads: int, key_dim: int, value_dim: int | None = None,
                  dtype=torch.bfloat16, keep_keys: bool = False, row: cpkv.QuantisedRow | None = None, dense: bool = False):
