@@ -250,9 +250,11 @@ CPKV_DEV void quantise_token(const QuantisedParams &p, const Work<kAxes> &w, int
     }
   }
   if (row == nullptr) return;
-  float off[8];  // what a turned element may be off, of its pair's sum of magnitudes; position 0 turns nothing, and leaves ties
+  float off[8] = {};  // what a turned element may be off, of its pair's sum of magnitudes; position 0 turns nothing, and leaves ties
+  if (turns) {
 #pragma unroll
-  for (int k = 0; k < 8; ++k) off[k] = s[k] == 0.f && fabsf(c[k]) == 1.f ? 0.f : fmaxf(fabsf(c[k]), fabsf(s[k])) * 0x1p-22f;
+    for (int k = 0; k < 8; ++k) off[k] = s[k] == 0.f && fabsf(c[k]) == 1.f ? 0.f : fmaxf(fabsf(c[k]), fabsf(s[k])) * 0x1p-22f;
+  }
   for (int i = part - p.k_first + (part < p.k_first ? parts : 0); i < p.k_turns; i += parts) {
     const int head = i * heads + sub;
     if (head >= a.heads - a.q_heads) continue;
