@@ -11,7 +11,7 @@ import serving_model as model
 from paged_kv_cache_compose_gb300 import cpkv
 from paged_kv_cache_compose_gb300.cpkv import QuantisedRow
 from test_gpu_quantised import cache_of, tensor, turns
-from test_gpu_quantised_attend import KIND_NAMES, KINDS, want_window
+from test_gpu_quantised_attend import KIND_NAMES, KINDS, want_window, window_case
 from test_gpu_serving import page_tables, queries, run_window
 
 pytestmark = pytest.mark.gpu
@@ -242,3 +242,43 @@ def test_append_rounds_from_the_exact_value(case, dtype, d, interleaved):
     assert not bad, f"{len(bad)} of {n * hkv} heads differ, first (token, head, bytes) {bad[0]}"
     if case == "past":
         assert (got[:, :2 * d] & 127 == qmodel.NAN).any()
+
+
+# --------------------------------------------------------------------------- attention: many requests, many heads
+
+def test_a_token_of_very_many_heads():
+    """Rows read back without lengths of queries: one token a request, 1100 heads of it on one key head."""
+    hq, d, ps = 1100, 64, 16
+    case = (hq, 1, d, ps, 2, BF16, 70, 5, [1, 1], [300, 41])
+    rng, pools, lists, q = window_case(case)
+    args = (2, hq, 1, d, None, 300)
+    assert cpkv.cpkv_attend_window_quantised_workspace_bytes(*args, window=70, sinks=5) > cpkv.cpkv_attend_window_workspace_bytes(*args, window=70, sinks=5)
+    cache = cache_of(pools, BF16)
+    out, lse = run_window(cache, case, q, lists)
+    assert int(cache.d_status) == 0
+    some = [0, 1, 255, 256, 700, 1023, 1024, 1099]
+    want = want_window((len(some),) + case[1:], pools, lists, q[:, some])
+    model.check(out[:, some], lse[:, some], want, BF16)
+
+
+@pytest.mark.parametrize("tokens, window, dtype", [(20, 0, BF16), (20, 33, FP16), (60, 0, FP16), (60, 40, BF16)], ids=["tile", "tile-window", "unpacked", "unpacked-window"])
+def test_more_requests_than_the_small_tables_hold(tokens, window, dtype):
+    """Forty requests of different lengths, some without queries or keys, converted on the way or read back first."""
+    hq, hkv, d, ps = 32, 2, 64, 8
+    q_lens = [tokens - i % 3 if i % 13 else 0 for i in range(40)]
+    kv_lens = [0 if i % 11 == 5 else n + (17 * i) % 90 for i, n in enumerate(q_lens)]
+    case = (hq, hkv, d, ps, 3, dtype, window, 3 if window else 0, q_lens, kv_lens)
+    rng, pools, lists, q = window_case(case)
+    more = cpkv.cpkv_attend_window_quantised_workspace_bytes(40, hq, hkv, d, q_lens, max(kv_lens), window, case[7])
+    assert (more > 40 * 60 * hkv * d * 4) == (tokens == 60)
+    cache = cache_of(pools, dtype)
+    out, lse = run_window(cache, case, q, lists)
+    assert int(cache.d_status) == 0
+    first = np.cumsum([0] + q_lens)
+    for b in (1, 5, 12, 16, 17, 38):
+        at = slice(first[b], first[b + 1])
+        heads = [0, 15, 16, 31]  # of two key heads
+        want = model.window(q[at][:, heads], [q_lens[b]], lists[b:b + 1], [kv_lens[b]], qmodel.Dense(pools),
+                            kv_heads=2, dim=d, window=window, sinks=case[7], scale=d**-0.5)
+        model.check(out[at][:, heads], lse[at][:, heads], want, dtype, f"request {b}")
+

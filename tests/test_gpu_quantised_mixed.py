@@ -96,6 +96,7 @@ CASES = {  # q heads, kv heads, dim, ps, cp, dtype, group sizes, prefix lens, su
     "groups-past-16": (32, 8, 64, 8, 3, FP16, [3, 2, 5] * 7, [8 * i for i in range(21)], [(7 * i) % 90 for i in range(70)]),
     "nothing-here-and-there": (32, 8, 128, 16, 2, BF16, [0, 8, 0, 17, 24, 0], [64, 0, 0, 48, 1040, 16], (EMPTY * 7)[:49]),
     "no-prefix-at-all": (32, 8, 128, 16, 2, BF16, [25, 25], [0, 0], (EMPTY * 7)[:50]),
+    "a-thousand-requests": (8, 2, 64, 16, 2, BF16, [24, 1000], [640, 160], [(31 * i) % 70 for i in range(1024)]),
     "lengths-below-the-bound": (32, 8, 64, 16, 2, FP16, [40], [2048], [0] * 20 + [1] * 10 + [300] + [0] * 9),
 }
 
