@@ -9,7 +9,7 @@
 // where its scale may differ, or 32 bits' range does not hold it): exact products, their sum rounded
 // "to odd", towards zero with a last bit that says that something follows, which then rounds
 // to e4m3 as the exact sum does.  Bytes bound the call (5.6 TB/s
-// on 44600 tokens of 32 + 8 heads of 128, in 181 us) nearly as much as instructions do.
+// on 44600 tokens of 32 + 8 heads of 128, in 183 us) nearly as much as instructions do.
 #include "append.cuh"
 #include "quantised.cuh"
 
@@ -333,8 +333,8 @@ CPKV_DEV Work<kAxes> token_work(const AppendParams &p, int n) {
 }
 
 // kAtOnce turns of a token's queries have their loads in flight together: four where it has so
-// many, and then five blocks to an SM instead of six.  32 heads of 128 (eight turns): 197 us
-// with two and 181 with four for 44600 tokens; 16 heads of 64 (two turns): 171 and 191 us for 131072.
+// many, and then five blocks to an SM instead of six.  32 heads of 128 (eight turns): 188 us
+// with two and 183 with four for 44600 tokens; 16 heads of 64 (two turns): 163 and 191 us for 131072.
 constexpr int append_blocks(int at_once) { return at_once == 4 ? 5 : 6; }
 
 template <typename T, bool kPairs, bool kAxes, int kAtOnce>

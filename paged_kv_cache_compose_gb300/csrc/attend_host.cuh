@@ -189,11 +189,14 @@ struct TileBounds {
 inline bool few_rows(int64_t max_rows) { return max_rows <= kSplitRows; }
 
 // Quantised rows that a tile pass brings to the element type beforehand (attend_unpack.cuh):
-// where the sequences have kUnpackTiles row tiles each or more, and the dense rows fit
-// kUnpackMost (the passes over the rows themselves need next to no memory).  5 requests of up to
+// where a call's sequences come to kUnpackTiles row tiles or more on the average, and the dense rows, of
+// all of them at the bound of the lengths, fit kUnpackMost (the passes over the rows themselves need next to no
+// memory).  5 requests of up to
 // 16384 keys, 32 heads of 128 on 8, beforehand and on the way: one row tile 120 and 99 us, two 138 and
 // 123, three 217 and 237, four 202 and 203, six 238 and 269, eight 287 and 338; 32 requests: two
-// 801 and 667, four 1162 and 1179.
+// 801 and 667, four 1162 and 1179.  That is of equal requests; in a ragged call the average may read rows
+// back that few queries see: 4096 tokens beside 15 single ones, all on 16384 keys, 1092 and 1104 us (1 GiB of rows), on
+// 4096 keys 227 and 199, the 4096 on as many and the others on 32768 keys 927 and 475.
 struct UnpackBounds {
   int64_t pages = 0, stride = 0;
   int sequences = 0;

@@ -23,9 +23,9 @@
 // permutation, so a lane's outputs are elements 16 c + 2 g and + 1 (g = lane / 4) of rows 2 t and + 1.
 //
 // Measured with the joining pass: 64 requests of 8 query rows, 8 heads of 64, the last 4096 of up
-// to 65536 keys, 65.9 us (4.3 TB/s; instructions issue in 60% of the cycles), 96.7 with queries and
+// to 65536 keys, 66.7 us (4.2 TB/s; instructions issue in 60% of the cycles), 96.7 with queries and
 // weights as the first operand and 16 rows always; 12 requests of 12 query rows on 8 heads of 128,
-// up to 16384 keys in one-token pages, 67.9 us (3.8 TB/s).  A unit at a time, with half the
+// up to 16384 keys in one-token pages, 67.8 us (3.8 TB/s).  A unit at a time, with half the
 // loads in flight and a vote for each: 77 and 73 us.
 #pragma once
 

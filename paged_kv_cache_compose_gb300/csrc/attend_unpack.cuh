@@ -4,7 +4,7 @@
 // A tile pass over quantised rows converts a tile of keys for each 256 query rows that
 // go over it, and the conversion, not the products, sets its pace (2.0 us a tile, 1.4
 // over plain rows).  Reading a key's row back takes 10 kB of traffic at 8 heads of 128, once
-// for all query rows.  Only rows that a query of the sequence sees are read; page p of
+// for all query rows (which is the worse of the two for a sequence of few of them in such a call).  Only rows that a query of the sequence sees are read; page p of
 // a sequence is dense page first(s) + its place among them, as its table says.
 #pragma once
 
